@@ -10,7 +10,9 @@ The entry points mirror include/gemm_f32.h one to one (same names, same
 argument order; pointers are plain integers, streams are ``cudaStream_t``
 values as integers, 0 = the legacy default stream). ``matmul`` and ``gemm``
 are convenience wrappers over ``gemm_f32_ex`` and ``gemm_f32_general`` for
-torch CUDA tensors.
+torch CUDA tensors; ``grouped_matmul``, ``grouped_wgrad``, ``lora_matmul`` and
+``lora_backward`` those of the products over segments of rows
+(include/segment_gemm_f32.h), for float32 and bfloat16 tensors.
 
 ``checked_library()`` loads libgemm_f32_checked.so, the same library built
 with device-side index checks (see include/gemm_f32.h, "The checked build");
@@ -28,7 +30,8 @@ LIB_PATH = os.path.join(_PKG, "libgemm_f32.so")
 LIB_CHECKED_PATH = os.path.join(_PKG, "libgemm_f32_checked.so")
 INCLUDE_DIR = os.path.join(os.path.dirname(_PKG), "include")
 HEADER_PATH = os.path.join(INCLUDE_DIR, "gemm_f32.h")
-HEADERS = [HEADER_PATH, os.path.join(INCLUDE_DIR, "reduce_f32.h")]
+HEADERS = [HEADER_PATH, os.path.join(INCLUDE_DIR, "reduce_f32.h"),
+           os.path.join(INCLUDE_DIR, "segment_gemm_f32.h")]
 
 # gemm_f32_mode
 EXACT, TF32, EXACT_SIMT = 0, 1, 2
@@ -47,6 +50,9 @@ KERNELS = {"auto": KERNEL_AUTO, "simt": KERNEL_SIMT, "tc_tma": KERNEL_TC_TMA, "t
 # gemm_f32_order, gemm_f32_op
 ROW_MAJOR, COL_MAJOR = 0, 1
 OP_N, OP_T = 0, 1
+# gemm_f32_type
+TYPE_F32, TYPE_BF16 = 0, 1
+MAX_SEGMENTS = 2048
 
 
 class GemmError(RuntimeError):
@@ -83,6 +89,13 @@ def _open(path):
     lib.gemm_f32_general.restype = i32
     lib.reduce_f32_sum.argtypes = [i64, p, p, i32, p]
     lib.reduce_f32_sum.restype = i32
+    lib.gemm_f32_grouped.argtypes = [i32, i32, i64, i64, i64, i64, p, i64, p, i64, i64, p, i64, p, p]
+    lib.gemm_f32_grouped.restype = i32
+    lib.gemm_f32_grouped_wgrad.argtypes = [i32, i64, i64, i64, i64, p, i64, p, i64, p, i64, i64, p, p]
+    lib.gemm_f32_grouped_wgrad.restype = i32
+    lib.gemm_f32_lora.argtypes = ([i32, i32, i32] + [i64] * 6 + [p, i64, p, i64, p, i64, i64,
+                                  p, i64, i64, p, p, p, p, i64, p, i64, p])
+    lib.gemm_f32_lora.restype = i32
     lib.gemm_f32_status_string.argtypes = [i32]
     lib.gemm_f32_status_string.restype = ctypes.c_char_p
     lib.gemm_f32_measure_peaks.argtypes = [ctypes.POINTER(ctypes.c_double)] * 4
@@ -183,6 +196,29 @@ def gemm_f32_noalloc(M, N, K, A, lda, B, ldb, C, ldc, mode, stream=0) -> int:
 def reduce_f32_sum(n, x, out, groups=0, stream=0) -> int:
     """*out = sum of x[0, n) (device pointers; see include/reduce_f32.h)."""
     return _load().reduce_f32_sum(n, x, out, groups, stream or None)
+
+
+def gemm_f32_grouped(type, transb, groups, M, N, K, A, lda, B, ldb, strideb, C, ldc, offsets,
+                     stream=0) -> int:
+    """C_g = A_g op(B_g) for every segment g (see include/segment_gemm_f32.h)."""
+    return _load().gemm_f32_grouped(type, transb, groups, M, N, K, A, lda, B, ldb, strideb, C, ldc,
+                                    offsets, stream or None)
+
+
+def gemm_f32_grouped_wgrad(type, groups, M, N, K, A, lda, D, ldd, C, ldc, stridec, offsets,
+                           stream=0) -> int:
+    """C_g = A_g^T D_g for every segment g (see include/segment_gemm_f32.h)."""
+    return _load().gemm_f32_grouped_wgrad(type, groups, M, N, K, A, lda, D, ldd, C, ldc, stridec,
+                                          offsets, stream or None)
+
+
+def gemm_f32_lora(type, transw, transl, segments, bank, M, N, K, R, X, ldx, W, ldw, A, lda, stridea,
+                  B, ldb, strideb, offsets, index, scales, U, ldu, Y, ldy, stream=0) -> int:
+    """Y = X op(W) + s (X A_a) B_a, a the adapter of the row's segment (see
+    include/segment_gemm_f32.h)."""
+    return _load().gemm_f32_lora(type, transw, transl, segments, bank, M, N, K, R, X, ldx, W, ldw,
+                                 A, lda, stridea, B, ldb, strideb, offsets, index or None,
+                                 scales or None, U or None, ldu, Y, ldy, stream or None)
 
 
 def gemm_f32_status_string(status: int) -> str:
@@ -384,6 +420,212 @@ def vector_sum(x, groups=0, out=None, stream=None):
     if st != OK:
         raise GemmError(st, "reduce_f32_sum")
     return out
+
+
+def _segment_type(t, name):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in (torch.float32,
+                                                                          torch.bfloat16):
+        raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor")
+    return TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32
+
+
+def _check_like(t, name, like, dim):
+    """A `dim`-D tensor of like's type and device whose matrices the library
+    can address as (pointer, leading dimension, stride of the stack)."""
+    _segment_type(t, name)
+    if t.dim() != dim:
+        raise TypeError(f"{name} must have {dim} dimensions, not {t.dim()}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, the other operands {like.dtype} on "
+                         f"{like.device}")
+    _check_rows(t.shape[-2:], t.stride(-2), t.stride(-1), name)
+
+
+def _check_out(out, name, shape, like):
+    """out, or a new tensor of the shape; a stack's matrices must not overlap."""
+    import torch
+
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    _check_like(out, name, like, len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} has the wrong shape: {tuple(out.shape)}, not {tuple(shape)}")
+    if len(shape) == 3 and out.numel() and shape[0] > 1 and (
+            out.stride(0) < (shape[1] - 1) * _ld2(out) + shape[2]):
+        raise ValueError(f"{name}'s matrices overlap")
+    return out
+
+
+def _check_offsets(offsets, device):
+    import torch
+
+    if (not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int64 or offsets.dim() != 1
+            or offsets.device != device or not offsets.is_contiguous() or offsets.numel() < 1):
+        raise TypeError("offsets must be a contiguous 1-D int64 tensor of segments + 1 values on "
+                        "the operands' device")
+    segments = offsets.numel() - 1
+    if segments > MAX_SEGMENTS:
+        raise ValueError(f"{segments} segments: at most {MAX_SEGMENTS} a call")
+    return segments
+
+
+def _check_array(t, name, dtype, count, device):
+    import torch
+
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device
+            or tuple(t.shape) != (count,) or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {count} values on the "
+                        "operands' device")
+    return t.data_ptr()
+
+
+def _ld2(t) -> int:
+    """Leading dimension of the matrices of a 2-D or 3-D tensor."""
+    rows, cols = int(t.shape[-2]), int(t.shape[-1])
+    return max(int(t.stride(-2)), cols, 1) if rows > 1 else max(cols, 1)
+
+
+def _stride(t) -> int:
+    return int(t.stride(0)) if t.shape[0] > 1 else 0
+
+
+def _call(name, device, stream, *args):
+    import torch
+
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    with torch.cuda.device(device):
+        st = globals()[name](*args, stream)
+    if st != OK:
+        raise GemmError(st, name)
+
+
+def grouped_matmul(a, b, offsets, transb=False, out=None, stream=None):
+    """Products grouped by expert: out[t] = a[t] @ op(b[g]) for the rows t of
+    segment g, offsets[g] <= t < offsets[g + 1].
+
+    ``a`` is M x K, float32 or bfloat16; ``b`` G x K x N, or G x N x K with
+    ``transb`` (which also is the gradient of the inputs: ``grouped_matmul(dy,
+    b, offsets, transb=True)``); ``offsets`` G + 1 int64 values on the device,
+    never read by the host. ``out`` (M x N) is returned; rows of no segment are
+    not written. Stream ordered on ``stream`` (default: torch's current one).
+    """
+    kind = _segment_type(a, "a")
+    _check_like(a, "a", a, 2)
+    _check_like(b, "b", a, 3)
+    groups = _check_offsets(offsets, a.device)
+    m, k = a.shape
+    k2, n = (b.shape[2], b.shape[1]) if transb else (b.shape[1], b.shape[2])
+    if b.shape[0] != groups:
+        raise ValueError(f"{b.shape[0]} matrices for {groups} segments")
+    if k != k2:
+        raise ValueError(f"inner dimensions differ: a is {m} x {k}, op(b) {k2} x {n}")
+    out = _check_out(out, "out", (m, n), a)
+    _call("gemm_f32_grouped", a.device, stream, kind, OP_T if transb else OP_N, groups, m, n, k,
+          a.data_ptr(), _ld2(a), b.data_ptr(), _ld2(b), _stride(b), out.data_ptr(), _ld2(out),
+          offsets.data_ptr())
+    return out
+
+
+def grouped_wgrad(a, d, offsets, out=None, stream=None):
+    """Weight gradients of grouped_matmul: out[g] = a[rows of g]^T @ d[rows of
+    g], zero where segment g is empty. ``a`` is M x K, ``d`` M x N, ``out`` G x
+    K x N (returned)."""
+    kind = _segment_type(a, "a")
+    _check_like(a, "a", a, 2)
+    _check_like(d, "d", a, 2)
+    groups = _check_offsets(offsets, a.device)
+    m, k = a.shape
+    m2, n = d.shape
+    if m != m2:
+        raise ValueError(f"a has {m} rows, d {m2}")
+    out = _check_out(out, "out", (groups, k, n), a)
+    _call("gemm_f32_grouped_wgrad", a.device, stream, kind, groups, m, n, k, a.data_ptr(), _ld2(a),
+          d.data_ptr(), _ld2(d), out.data_ptr(), _ld2(out), _stride(out), offsets.data_ptr())
+    return out
+
+
+def lora_matmul(x, w, lora_a, lora_b, offsets, adapters=None, scales=None, transw=False,
+                transl=False, out=None, shrink_out=None, stream=None):
+    """A shared projection with a low-rank adapter for each segment of rows:
+    out = x @ op(w) + u @ op(lora_b[i]), u = scales[i] * (x @ op(lora_a[i])),
+    i = adapters[segment of the row].
+
+    ``x`` is M x K; ``w`` K x N (N x K with ``transw``); ``lora_a`` a bank of
+    K x R and ``lora_b`` of R x N matrices (R x K and N x R with ``transl``);
+    ``offsets`` segments + 1 int64 values, ``adapters`` int32, one for each
+    segment (a value outside the bank: no adapter; None: adapter g for segment
+    g), ``scales`` float32, one for each adapter (None: 1), all on the device.
+    ``shrink_out`` (M x R), if given, receives u for lora_backward. Returns
+    ``out`` (M x N).
+    """
+    import torch
+
+    kind = _segment_type(x, "x")
+    _check_like(x, "x", x, 2)
+    _check_like(w, "w", x, 2)
+    _check_like(lora_a, "lora_a", x, 3)
+    _check_like(lora_b, "lora_b", x, 3)
+    segments = _check_offsets(offsets, x.device)
+    m, k = x.shape
+    k2, n = (w.shape[1], w.shape[0]) if transw else tuple(w.shape)
+    bank, ka, r = lora_a.shape if not transl else (lora_a.shape[0], lora_a.shape[2], lora_a.shape[1])
+    bank2, rb, nb = lora_b.shape if not transl else (lora_b.shape[0], lora_b.shape[2],
+                                                     lora_b.shape[1])
+    if k != k2:
+        raise ValueError(f"inner dimensions differ: x is {m} x {k}, op(w) {k2} x {n}")
+    if (ka, rb, nb, bank2) != (k, r, n, bank):
+        raise ValueError(f"op(lora_a) is {bank} of {ka} x {r} and op(lora_b) {bank2} of {rb} x {nb} "
+                         f"beside a {k} x {n} projection")
+    if adapters is None and segments > bank:
+        raise ValueError(f"{segments} segments, {bank} adapters and no choice of adapters")
+    index = 0 if adapters is None else _check_array(adapters, "adapters", torch.int32, segments,
+                                                    x.device)
+    scale = 0 if scales is None else _check_array(scales, "scales", torch.float32, bank, x.device)
+    out = _check_out(out, "out", (m, n), x)
+    u, ldu = 0, max(r, 1)
+    if shrink_out is not None:
+        _check_out(shrink_out, "shrink_out", (m, r), x)
+        u, ldu = shrink_out.data_ptr(), _ld2(shrink_out)
+    _call("gemm_f32_lora", x.device, stream, kind, OP_T if transw else OP_N,
+          OP_T if transl else OP_N, segments, bank, m, n, k, r, x.data_ptr(), _ld2(x), w.data_ptr(),
+          _ld2(w), lora_a.data_ptr(), _ld2(lora_a), _stride(lora_a), lora_b.data_ptr(),
+          _ld2(lora_b), _stride(lora_b), offsets.data_ptr(), index, scale, u, ldu, out.data_ptr(),
+          _ld2(out))
+    return out
+
+
+def lora_backward(dy, x, shrink, w, lora_a, lora_b, offsets, scales=None, transw=False,
+                  transl=False, stream=None):
+    """Gradients of lora_matmul with one adapter for each segment (adapters
+    None; rows sorted by adapter) on a frozen ``w``: (dx, d lora_a, d lora_b).
+    ``shrink`` is the forward's shrink_out. Factors of empty segments get zero.
+    """
+    import torch
+
+    _segment_type(dy, "dy")
+    _check_like(shrink, "shrink", dy, 2)
+    _check_like(x, "x", dy, 2)
+    _check_like(lora_a, "lora_a", dy, 3)
+    _check_like(lora_b, "lora_b", dy, 3)
+    segments = _check_offsets(offsets, dy.device)
+    if lora_a.shape[0] != segments:
+        raise ValueError(f"{lora_a.shape[0]} adapters for {segments} segments: the backward pass "
+                         "wants one each")
+    if shrink.shape != (x.shape[0], lora_a.shape[1 if transl else 2]):
+        raise ValueError("shrink has the wrong shape")
+    if dy.shape[0] != x.shape[0]:
+        raise ValueError(f"dy has {dy.shape[0]} rows, x {x.shape[0]}")
+    v = torch.empty_like(shrink, memory_format=torch.contiguous_format)
+    dx = lora_matmul(dy, w, lora_b, lora_a, offsets, None, scales, not transw, not transl, None, v,
+                     stream)
+    if transl:
+        return (dx, grouped_wgrad(v, x, offsets, None, stream),
+                grouped_wgrad(dy, shrink, offsets, None, stream))
+    return (dx, grouped_wgrad(x, v, offsets, None, stream),
+            grouped_wgrad(shrink, dy, offsets, None, stream))
 
 
 def _check_host(x, name):

@@ -20,6 +20,7 @@
 #include "../../include/gemm_f32.h"
 #include "../../include/reduce_f32.h"
 #include "kernels.h"
+#include "segments.h"
 
 namespace {
 
@@ -403,7 +404,8 @@ long long take_index_faults(bool clear, gemm::IndexFault *first) {
   }
   int (*const takers[])(gemm::IndexFault *, bool) = {
       gemm::tc_index_fault_take, gemm::simt_index_fault_take, gemm::pack_index_fault_take,
-      gemm::transpose_index_fault_take, gemm::reduce_index_fault_take};
+      gemm::transpose_index_fault_take, gemm::reduce_index_fault_take,
+      gemm::seg_simt_index_fault_take};
   long long total = 0;
   bool have = false;
   for (auto take : takers) {
@@ -420,6 +422,10 @@ long long take_index_faults(bool clear, gemm::IndexFault *first) {
 }
 
 }  // namespace
+
+int gemm::current_device_info(int *dev_out, int *sm_count) {
+  return current_device(dev_out, sm_count);
+}
 
 extern "C" {
 

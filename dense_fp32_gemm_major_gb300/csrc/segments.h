@@ -1,0 +1,51 @@
+// segments.h -- host-side interface between the segmented products' C ABI
+// (seg_api.cu) and their kernels. Internal to libgemm_f32.so.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+
+namespace gemm {
+
+constexpr int kMaxSegments = 2048;
+
+// A stack of equal row-major matrices: element (z, i, j) at p[z * stride +
+// i * ld + j].
+struct SegMatrix {
+  const void *p = nullptr;
+  int64_t ld = 0, stride = 0;
+  int64_t rows = 0, cols = 0, count = 1;  // as stored
+};
+
+// One segmented product. The result's rows are tokens (wgrad = false) or a
+// matrix for each segment (wgrad = true):
+//
+//   rows:   C[t, :] = scale_z A[t, :] op(B_z)  for the rows t of segment g,
+//           z = index[g] (or g); dense: all M rows with B_0, plus U[t, :]
+//           op(L_z) for the rows of segments with an adapter (R > 0)
+//   wgrad:  C_g = A_g^T B_g, the sum over the rows of segment g
+struct SegArgs {
+  bool bf16 = false, wgrad = false, dense = false;
+  int64_t groups = 0, M = 0, N = 0, K = 0;
+  SegMatrix A, B, C;
+  int transb = 0;
+  const int64_t *offsets = nullptr;
+  const int32_t *index = nullptr;
+  const float *scales = nullptr;
+  int64_t bank = 0;  // matrices z may name; others: no product
+  int64_t R = 0;     // dense: width of U
+  SegMatrix U, L;
+  int transl = 0;
+};
+
+// Requires M, N >= 1 (rows) or groups, N, K >= 1 (wgrad).
+int seg_simt_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
+
+int seg_simt_index_fault_take(IndexFault *out, bool clear);
+
+// Capability check and SM count of the current device (api.cu).
+int current_device_info(int *dev_out, int *sm_count);
+
+}  // namespace gemm

@@ -1,0 +1,125 @@
+/*
+ * segment_gemm_f32.h -- C ABI of libgemm_f32.so, part 3: matrix products over
+ * segments of rows on an NVIDIA GB300 (sm_103a): products grouped by expert
+ * with ragged sizes, their weight gradients, and low-rank adapters of many
+ * requests beside a shared projection.
+ *
+ * Segments. The rows (tokens) of a row-major matrix lie sorted by segment:
+ * segment g is rows offsets[g] .. offsets[g + 1] - 1. `offsets` holds
+ * segments + 1 int64 values in DEVICE memory, non-decreasing, from 0 to at
+ * most M; the host never reads them, so a router's output on the same stream
+ * can be passed on without a synchronisation. Segments may be empty; rows
+ * before offsets[0] and from offsets[segments] on belong to none. Values
+ * outside [0, M] are held to it and a decreasing one makes its segment empty,
+ * so that no access leaves the matrices (rows claimed by two segments have
+ * unspecified results). At most GEMM_F32_MAX_SEGMENTS segments a call.
+ *
+ * Types. `type` is that of every matrix of the call (a gemm_f32_type). The
+ * "f32" of the names is the type of the sums: products are exact to fp32 or
+ * better and accumulated in fp32, whatever the operands' type.
+ *   GEMM_F32_TYPE_F32   fp32 operands and results, FP32 class: |C - AB| <=
+ *                       2 K 2^-24 (|A| |B|), as GEMM_F32_EXACT. Operands are
+ *                       finite (an infinite one gives NaN in its results).
+ *   GEMM_F32_TYPE_BF16  bf16 operands, fp32 sums, results rounded once to bf16
+ *                       (nearest even).
+ * A row of one segment never reaches the results of another: NaN and
+ * infinities stay in the rows (and, in gradients, in the segments) that hold
+ * them.
+ *
+ * Streams, ownership, errors and thread safety are those of gemm_f32.h.
+ * Results do not depend on timing: the same call gives the same bits.
+ */
+#ifndef SEGMENT_GEMM_F32_H
+#define SEGMENT_GEMM_F32_H
+
+#include <stdint.h>
+
+#include "gemm_f32.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum {
+    GEMM_F32_TYPE_F32 = 0,
+    GEMM_F32_TYPE_BF16 = 1
+} gemm_f32_type;
+
+#define GEMM_F32_MAX_SEGMENTS 2048
+
+/*
+ * gemm_f32_grouped -- C_g = A_g op(B_g) for every segment (expert) g: rows of A
+ * times the segment's own matrix, into the same rows of C.
+ *   groups    segments, 0 .. GEMM_F32_MAX_SEGMENTS
+ *   M, N, K   A is M x K, op(B_g) K x N, C is M x N
+ *   transb    GEMM_OP_N: B_g stored K x N (ldb >= max(1, N)); GEMM_OP_T: N x K
+ *             (ldb >= max(1, K)) -- also the gradient of the inputs of a
+ *             product with GEMM_OP_N
+ *   B         B_g starts strideb elements after B_(g-1); strideb >= 0 (0: one
+ *             matrix for all)
+ *   C         rows of no segment are not written; must not overlap A, B or
+ *             offsets (GEMM_ERR_ALIAS)
+ * Pointers are device pointers aligned to their element (offsets to 8 bytes).
+ * K == 0 sets the segments' rows to zero. Size limits as for gemm_f32.
+ */
+int gemm_f32_grouped(int type, int transb, int64_t groups, int64_t M, int64_t N, int64_t K,
+                     const void *A, int64_t lda,
+                     const void *B, int64_t ldb, int64_t strideb,
+                     void *C, int64_t ldc,
+                     const int64_t *offsets, void *stream);
+
+/*
+ * gemm_f32_grouped_wgrad -- C_g = A_g^T D_g for every segment g: the gradient
+ * of B_g in C = A B (D: the gradient of the product's result).
+ *   M, N, K   A is M x K, D is M x N, every C_g K x N
+ *   C         C_g starts stridec elements after C_(g-1); stridec >= (K - 1) ldc
+ *             + N. An empty segment's C_g is set to zero.
+ */
+int gemm_f32_grouped_wgrad(int type, int64_t groups, int64_t M, int64_t N, int64_t K,
+                           const void *A, int64_t lda,
+                           const void *D, int64_t ldd,
+                           void *C, int64_t ldc, int64_t stridec,
+                           const int64_t *offsets, void *stream);
+
+/*
+ * gemm_f32_lora -- a shared projection with a low-rank adapter for each
+ * segment (request):
+ *
+ *     U = s_a (X A_a),   Y = X op(W) + U B_a,   a = index[segment of the row]
+ *
+ *   segments  0 .. GEMM_F32_MAX_SEGMENTS
+ *   bank      adapters held in A, B and scales
+ *   M, N, K, R  X is M x K, op(W) K x N, A_a K x R, B_a R x N, U M x R, Y M x N
+ *   transw    W stored K x N (GEMM_OP_N) or N x K (GEMM_OP_T)
+ *   transl    GEMM_OP_N: A_a stored K x R and B_a R x N; GEMM_OP_T: A_a R x K
+ *             and B_a N x R. With dY for X, W and the factors exchanged and
+ *             both flags flipped the same call is the gradient of X, and U
+ *             the second operand of the gradient of A.
+ *   A, B      adapter a starts stridea (strideb) elements after a - 1
+ *   index     device int32, one adapter for each segment; NULL: adapter g for
+ *             segment g. A value outside [0, bank) means none: such rows, and
+ *             rows of no segment, get X op(W) alone.
+ *   scales    device float, s_a for each adapter; NULL: 1
+ *   U, ldu    receives U (rows of no segment are not written, those of a
+ *             segment without adapter are zero); NULL: kept in a workspace
+ *             from the library's pool. For GEMM_F32_TYPE_BF16 it is rounded to
+ *             bf16, here as there: it is an operand of the second product.
+ *   Y         all M rows are written; Y and U must not overlap anything else
+ *             (GEMM_ERR_ALIAS)
+ * R == 0 is the projection alone.
+ */
+int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t bank,
+                  int64_t M, int64_t N, int64_t K, int64_t R,
+                  const void *X, int64_t ldx,
+                  const void *W, int64_t ldw,
+                  const void *A, int64_t lda, int64_t stridea,
+                  const void *B, int64_t ldb, int64_t strideb,
+                  const int64_t *offsets, const int32_t *index, const float *scales,
+                  void *U, int64_t ldu,
+                  void *Y, int64_t ldy, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SEGMENT_GEMM_F32_H */
