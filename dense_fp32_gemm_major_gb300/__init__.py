@@ -96,6 +96,10 @@ def _open(path):
     lib.gemm_f32_lora.argtypes = ([i32, i32, i32] + [i64] * 6 + [p, i64, p, i64, p, i64, i64,
                                   p, i64, i64, p, p, p, p, i64, p, i64, p])
     lib.gemm_f32_lora.restype = i32
+    lib.gemm_f32_lora_backward.argtypes = ([i32, i32, i32] + [i64] * 5 + [p, i64] * 4
+                                           + [p, i64, i64] * 2 + [p, p, p, i64]
+                                           + [p, i64, i64] * 2 + [p])
+    lib.gemm_f32_lora_backward.restype = i32
     lib.gemm_f32_status_string.argtypes = [i32]
     lib.gemm_f32_status_string.restype = ctypes.c_char_p
     lib.gemm_f32_measure_peaks.argtypes = [ctypes.POINTER(ctypes.c_double)] * 4
@@ -219,6 +223,16 @@ def gemm_f32_lora(type, transw, transl, segments, bank, M, N, K, R, X, ldx, W, l
     return _load().gemm_f32_lora(type, transw, transl, segments, bank, M, N, K, R, X, ldx, W, ldw,
                                  A, lda, stridea, B, ldb, strideb, offsets, index or None,
                                  scales or None, U or None, ldu, Y, ldy, stream or None)
+
+
+def gemm_f32_lora_backward(type, transw, transl, segments, M, N, K, R, dY, lddy, X, ldx, U, ldu, W,
+                           ldw, A, lda, stridea, B, ldb, strideb, offsets, scales, dX, lddx, dA,
+                           ldda, strideda, dB, lddb, stridedb, stream=0) -> int:
+    """Gradients of gemm_f32_lora (see include/segment_gemm_f32.h)."""
+    return _load().gemm_f32_lora_backward(type, transw, transl, segments, M, N, K, R, dY, lddy, X,
+                                          ldx, U, ldu, W, ldw, A, lda, stridea, B, ldb, strideb,
+                                          offsets, scales or None, dX, lddx, dA, ldda, strideda, dB,
+                                          lddb, stridedb, stream or None)
 
 
 def gemm_f32_status_string(status: int) -> str:
@@ -605,27 +619,35 @@ def lora_backward(dy, x, shrink, w, lora_a, lora_b, offsets, scales=None, transw
     """
     import torch
 
-    _segment_type(dy, "dy")
+    kind = _segment_type(dy, "dy")
+    _check_like(dy, "dy", dy, 2)
     _check_like(shrink, "shrink", dy, 2)
     _check_like(x, "x", dy, 2)
+    _check_like(w, "w", dy, 2)
     _check_like(lora_a, "lora_a", dy, 3)
     _check_like(lora_b, "lora_b", dy, 3)
     segments = _check_offsets(offsets, dy.device)
-    if lora_a.shape[0] != segments:
-        raise ValueError(f"{lora_a.shape[0]} adapters for {segments} segments: the backward pass "
-                         "wants one each")
-    if shrink.shape != (x.shape[0], lora_a.shape[1 if transl else 2]):
-        raise ValueError("shrink has the wrong shape")
-    if dy.shape[0] != x.shape[0]:
-        raise ValueError(f"dy has {dy.shape[0]} rows, x {x.shape[0]}")
-    v = torch.empty_like(shrink, memory_format=torch.contiguous_format)
-    dx = lora_matmul(dy, w, lora_b, lora_a, offsets, None, scales, not transw, not transl, None, v,
-                     stream)
-    if transl:
-        return (dx, grouped_wgrad(v, x, offsets, None, stream),
-                grouped_wgrad(dy, shrink, offsets, None, stream))
-    return (dx, grouped_wgrad(x, v, offsets, None, stream),
-            grouped_wgrad(shrink, dy, offsets, None, stream))
+    (m, k), n, r = x.shape, dy.shape[1], shrink.shape[1]
+    if dy.shape[0] != m or shrink.shape[0] != m:
+        raise ValueError(f"x has {m} rows, dy {dy.shape[0]} and shrink {shrink.shape[0]}")
+    if (tuple(w.shape) != ((n, k) if transw else (k, n))
+            or tuple(lora_a.shape) != ((segments, r, k) if transl else (segments, k, r))
+            or tuple(lora_b.shape) != ((segments, n, r) if transl else (segments, r, n))):
+        raise ValueError(f"w {tuple(w.shape)}, lora_a {tuple(lora_a.shape)} and lora_b "
+                         f"{tuple(lora_b.shape)} are not those of {segments} segments, a {k} x {n} "
+                         f"projection and rank {r}")
+    scale = 0 if scales is None else _check_array(scales, "scales", torch.float32, segments,
+                                                  dy.device)
+    dx = _check_out(None, "dx", (m, k), dy)
+    da = _check_out(None, "da", tuple(lora_a.shape), dy)
+    db = _check_out(None, "db", tuple(lora_b.shape), dy)
+    _call("gemm_f32_lora_backward", dy.device, stream, kind, OP_T if transw else OP_N,
+          OP_T if transl else OP_N, segments, m, n, k, r, dy.data_ptr(), _ld2(dy), x.data_ptr(),
+          _ld2(x), shrink.data_ptr(), _ld2(shrink), w.data_ptr(), _ld2(w), lora_a.data_ptr(),
+          _ld2(lora_a), _stride(lora_a), lora_b.data_ptr(), _ld2(lora_b), _stride(lora_b),
+          offsets.data_ptr(), scale, dx.data_ptr(), _ld2(dx), da.data_ptr(), _ld2(da), _stride(da),
+          db.data_ptr(), _ld2(db), _stride(db))
+    return dx, da, db
 
 
 def _check_host(x, name):

@@ -405,7 +405,7 @@ long long take_index_faults(bool clear, gemm::IndexFault *first) {
   int (*const takers[])(gemm::IndexFault *, bool) = {
       gemm::tc_index_fault_take, gemm::simt_index_fault_take, gemm::pack_index_fault_take,
       gemm::transpose_index_fault_take, gemm::reduce_index_fault_take,
-      gemm::seg_simt_index_fault_take};
+      gemm::seg_tc_index_fault_take};
   long long total = 0;
   bool have = false;
   for (auto take : takers) {
@@ -695,7 +695,9 @@ int gemm_f32_poll_device_status(void *stream) {
   int dev = 0, sms = 0;
   const int st = current_device(&dev, &sms);
   if (st != gemm::kOk) return st;
-  const int tst = gemm::tc_poll_status(static_cast<cudaStream_t>(stream));
+  int tst = gemm::tc_poll_status(static_cast<cudaStream_t>(stream));
+  const int sst = gemm::seg_tc_poll_status(static_cast<cudaStream_t>(stream));
+  if (tst == gemm::kOk) tst = sst;
   if (tst != gemm::kOk || !GEMM_F32_INDEX_CHECKS) return tst;
   // Checked build: a recorded index violation, left for take_index_fault.
   if (take_index_faults(false, nullptr) > 0) return GEMM_ERR_INDEX;

@@ -60,7 +60,103 @@ bool common_ok(int type, int64_t groups) {
 }
 
 int launch(const SegArgs &a, int sms, cudaStream_t stream) {
-  return gemm::seg_simt_launch(a, sms, stream);
+  return gemm::seg_tc_launch(a, sms, stream);
+}
+
+// Y = X op(W) + U op(B_a), U = s_a (X op(A_a)).
+struct Lora {
+  bool bf16 = false, adapted = false;
+  int transw = 0, transl = 0;
+  int64_t segments = 0, bank = 0, M = 0, N = 0, K = 0, R = 0;
+  SegMatrix X, W, A, B, U, Y;
+  const int64_t *offsets = nullptr;
+  const int32_t *index = nullptr;
+  const float *scales = nullptr;
+};
+
+// U (in the caller's matrix or here), its second term for bf16 -- U is an
+// operand of the second product, and rounded to one bf16 would add an error
+// as large as the result's own rounding -- and U B in fp32, the addend of the
+// projection's tiles. A tile of the projection holds rows of several
+// segments, and an MMA over all of them would let one adapter's NaN or
+// infinity into the others' rows (0 * inf), so U B is a product of its own.
+struct Work {
+  void *p = nullptr;
+  SegMatrix u, u_lo, sum;
+
+  int take(const Lora &l, cudaStream_t s) {
+    u = l.U;
+    if (!l.adapted) return gemm::kOk;
+    const int elem = l.bf16 ? 2 : 4;
+    auto up = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
+    const int64_t ld = (l.R + 7) / 8 * 8, sum_ld = (l.N + 3) / 4 * 4;
+    const int64_t ub = l.U.p == nullptr ? up(l.M * ld * elem) : 0;
+    const int64_t lb = l.bf16 ? up(l.M * (l.U.p == nullptr ? ld : l.U.ld) * 2) : 0;
+    const int64_t sb = up(l.M * sum_ld * 4);
+    if (ub + lb + sb == 0) return gemm::kOk;
+    const int st = gemm::pool_alloc(&p, static_cast<size_t>(ub + lb + sb), s);
+    if (st != gemm::kOk) return st;
+    uint8_t *at = static_cast<uint8_t *>(p);
+    if (l.U.p == nullptr) u = SegMatrix{at, ld, 0, l.M, l.R, 1};
+    if (l.bf16) {
+      u_lo = u;
+      u_lo.p = at + ub;
+    }
+    sum = SegMatrix{at + ub + lb, sum_ld, 0, l.M, l.N, 1};
+    return gemm::kOk;
+  }
+
+  int give_back(int st, cudaStream_t s) {
+    if (p == nullptr) return st;
+    const int fst = gemm::pool_free(p, s);
+    return st != gemm::kOk ? st : fst;
+  }
+};
+
+int lora_run(const Lora &l, const Work &work, int sms, cudaStream_t s) {
+  SegArgs y;
+  y.bf16 = l.bf16;
+  y.groups = l.segments;
+  y.M = l.M;
+  y.bank = l.bank;
+  y.offsets = l.offsets;
+  y.index = l.index;
+  if (l.adapted) {
+    SegArgs u = y;  // U = s (X A)
+    u.N = l.R;
+    u.K = l.K;
+    u.A = l.X;
+    u.B = l.A;
+    u.transb = l.transl;
+    u.scales = l.scales;
+    u.C = work.u;
+    u.C_lo = work.u_lo;
+    int st = launch(u, sms, s);
+    if (st != gemm::kOk) return st;
+    if (l.N == 0) return st;
+    SegArgs e = y;  // U B
+    e.N = l.N;
+    e.K = l.R;
+    e.A = work.u;
+    e.A_lo = work.u_lo.p;
+    e.B = l.B;
+    e.transb = l.transl;
+    e.C = work.sum;
+    e.c_f32 = true;
+    st = launch(e, sms, s);
+    if (st != gemm::kOk) return st;
+    y.add = work.sum;
+  }
+  y.dense = true;
+  y.groups = l.adapted ? l.segments : 0;
+  y.index = nullptr;
+  y.N = l.N;
+  y.K = l.K;
+  y.A = l.X;
+  y.B = l.W;
+  y.transb = l.transw;
+  y.C = l.Y;
+  return launch(y, sms, s);
 }
 
 }  // namespace
@@ -134,68 +230,140 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
       !dim_ok(K) || !dim_ok(R) || !dim_ok(bank))
     return GEMM_ERR_INVALID_ARG;
   const int elem = type == GEMM_F32_TYPE_BF16 ? 2 : 4;
-  const bool adapted = R > 0 && bank > 0 && segments > 0 && M > 0;
-  SegArgs y;
-  y.bf16 = type == GEMM_F32_TYPE_BF16;
-  y.dense = true;
-  y.groups = adapted ? segments : 0;
-  y.bank = bank;
-  y.M = M;
-  y.N = N;
-  y.K = K;
-  y.R = adapted ? R : 0;
-  y.transb = transw;
-  y.transl = transl;
-  y.A = SegMatrix{X, ldx, 0, M, K, 1};
-  y.B = SegMatrix{W, ldw, 0, transw ? N : K, transw ? K : N, 1};
-  y.C = SegMatrix{Y, ldy, 0, M, N, 1};
-  y.L = SegMatrix{B, ldb, strideb, transl ? N : R, transl ? R : N, bank};
-  y.offsets = offsets;
-  y.index = index;
-  SegArgs u = y;  // U = s (X A)
-  u.dense = false;
-  u.N = R;
-  u.R = 0;
-  u.transb = transl;
-  u.scales = scales;
-  u.B = SegMatrix{A, lda, stridea, transl ? R : K, transl ? K : R, bank};
-  u.C = SegMatrix{U, ldu, 0, M, R, 1};
+  Lora l;
+  l.bf16 = type == GEMM_F32_TYPE_BF16;
+  l.transw = transw;
+  l.transl = transl;
+  l.adapted = R > 0 && bank > 0 && segments > 0 && M > 0;
+  l.segments = segments;
+  l.bank = bank;
+  l.M = M;
+  l.N = N;
+  l.K = K;
+  l.R = R;
+  l.X = SegMatrix{X, ldx, 0, M, K, 1};
+  l.W = SegMatrix{W, ldw, 0, transw ? N : K, transw ? K : N, 1};
+  l.A = SegMatrix{A, lda, stridea, transl ? R : K, transl ? K : R, bank};
+  l.B = SegMatrix{B, ldb, strideb, transl ? N : R, transl ? R : N, bank};
+  l.U = SegMatrix{U, ldu, 0, M, R, 1};
+  l.Y = SegMatrix{Y, ldy, 0, M, N, 1};
+  l.offsets = offsets;
+  l.index = index;
+  l.scales = scales;
   Range rx, rw, ra, rb, ro, ri, rs, ru, ry;
-  if (!stack_ok(y.A, elem, false, &rx) || !stack_ok(y.B, elem, false, &rw) ||
-      !stack_ok(y.C, elem, true, &ry))
+  if (!stack_ok(l.X, elem, false, &rx) || !stack_ok(l.W, elem, false, &rw) ||
+      !stack_ok(l.Y, elem, true, &ry))
     return GEMM_ERR_INVALID_ARG;
-  if (adapted &&
-      (!stack_ok(u.B, elem, false, &ra) || !stack_ok(y.L, elem, false, &rb) ||
+  if (l.adapted &&
+      (!stack_ok(l.A, elem, false, &ra) || !stack_ok(l.B, elem, false, &rb) ||
        !array_ok(offsets, segments + 1, 8, false, &ro) ||
        !array_ok(index, segments, 4, true, &ri) || !array_ok(scales, bank, 4, true, &rs) ||
-       (U != nullptr && !stack_ok(u.C, elem, true, &ru))))
+       (U != nullptr && !stack_ok(l.U, elem, true, &ru))))
     return GEMM_ERR_INVALID_ARG;
   const Range in[] = {rx, rw, ra, rb, ro, ri, rs};
   for (const Range &r : in)
     if (overlap(r, ry) || overlap(r, ru)) return GEMM_ERR_ALIAS;
   if (overlap(ru, ry)) return GEMM_ERR_ALIAS;
-  if (M == 0 || (N == 0 && (!adapted || U == nullptr))) return GEMM_OK;
+  if (M == 0 || (N == 0 && (!l.adapted || U == nullptr))) return GEMM_OK;
   int dev = 0, sms = 0;
   int st = gemm::current_device_info(&dev, &sms);
   if (st != gemm::kOk) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void *work = nullptr;
-  if (adapted) {
-    if (U == nullptr) {
-      u.C.ld = (R + 7) / 8 * 8;
-      st = gemm::pool_alloc(&work, static_cast<size_t>(M) * u.C.ld * elem, s);
-      if (st != gemm::kOk) return st;
-      u.C.p = work;
-    }
-    y.U = u.C;
-    st = launch(u, sms, s);
+  Work work;
+  st = work.take(l, s);
+  if (st == gemm::kOk) st = lora_run(l, work, sms, s);
+  return work.give_back(st, s);
+}
+
+int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, int64_t M,
+                           int64_t N, int64_t K, int64_t R, const void *dY, int64_t lddy,
+                           const void *X, int64_t ldx, const void *U, int64_t ldu, const void *W,
+                           int64_t ldw, const void *A, int64_t lda, int64_t stridea,
+                           const void *B, int64_t ldb, int64_t strideb, const int64_t *offsets,
+                           const float *scales, void *dX, int64_t lddx, void *dA, int64_t ldda,
+                           int64_t strideda, void *dB, int64_t lddb, int64_t stridedb,
+                           void *stream) {
+  if (!common_ok(type, segments) || !op_ok(transw) || !op_ok(transl) || !dim_ok(M) || !dim_ok(N) ||
+      !dim_ok(K) || !dim_ok(R))
+    return GEMM_ERR_INVALID_ARG;
+  const int elem = type == GEMM_F32_TYPE_BF16 ? 2 : 4;
+  // dX = dY op(W)^T + s (dY B^T) A^T: the forward with N and K, and the
+  // factors, exchanged, every matrix read the other way round.
+  Lora l;
+  l.bf16 = type == GEMM_F32_TYPE_BF16;
+  l.transw = transw ? GEMM_OP_N : GEMM_OP_T;
+  l.transl = transl ? GEMM_OP_N : GEMM_OP_T;
+  l.adapted = R > 0 && segments > 0 && M > 0;
+  l.segments = l.bank = segments;
+  l.M = M;
+  l.N = K;
+  l.K = N;
+  l.R = R;
+  l.X = SegMatrix{dY, lddy, 0, M, N, 1};
+  l.W = SegMatrix{W, ldw, 0, transw ? N : K, transw ? K : N, 1};
+  l.A = SegMatrix{B, ldb, strideb, transl ? N : R, transl ? R : N, segments};
+  l.B = SegMatrix{A, lda, stridea, transl ? R : K, transl ? K : R, segments};
+  l.U = SegMatrix{nullptr, 0, 0, M, R, 1};
+  l.Y = SegMatrix{dX, lddx, 0, M, K, 1};
+  l.offsets = offsets;
+  l.scales = scales;
+  const SegMatrix x{X, ldx, 0, M, K, 1}, u{U, ldu, 0, M, R, 1};
+  const SegMatrix da{dA, ldda, strideda, transl ? R : K, transl ? K : R, segments};
+  const SegMatrix db{dB, lddb, stridedb, transl ? N : R, transl ? R : N, segments};
+  Range rdy, rx, ru, rw, ra, rb, ro, rs, rdx, rda, rdb;
+  if (!stack_ok(l.X, elem, false, &rdy) || !stack_ok(l.W, elem, false, &rw) ||
+      !stack_ok(l.Y, elem, true, &rdx) || !stack_ok(da, elem, true, &rda) ||
+      !stack_ok(db, elem, true, &rdb))
+    return GEMM_ERR_INVALID_ARG;
+  if (segments > 0 && !array_ok(offsets, segments + 1, 8, false, &ro)) return GEMM_ERR_INVALID_ARG;
+  if (l.adapted &&
+      (!stack_ok(x, elem, false, &rx) || !stack_ok(u, elem, false, &ru) ||
+       !stack_ok(l.A, elem, false, &rb) || !stack_ok(l.B, elem, false, &ra) ||
+       !array_ok(scales, segments, 4, true, &rs)))
+    return GEMM_ERR_INVALID_ARG;
+  const Range in[] = {rdy, rx, ru, rw, ra, rb, ro, rs}, out[] = {rdx, rda, rdb};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range &r : in)
+      if (overlap(r, out[i])) return GEMM_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[j], out[i])) return GEMM_ERR_ALIAS;
   }
-  if (st == gemm::kOk && N > 0) st = launch(y, sms, s);
-  if (work != nullptr) {
-    const int fst = gemm::pool_free(work, s);
-    if (st == gemm::kOk) st = fst;
+  if ((M == 0 || (K == 0 && N == 0)) && (segments == 0 || R == 0)) return GEMM_OK;
+  int dev = 0, sms = 0;
+  int st = gemm::current_device_info(&dev, &sms);
+  if (st != gemm::kOk) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Work work;
+  st = work.take(l, s);
+  if (st == gemm::kOk && M > 0) st = lora_run(l, work, sms, s);
+  // dA = X^T V (stored R x K: V^T X) and dB = U^T dY (stored N x R: dY^T U).
+  SegArgs g;
+  g.bf16 = l.bf16;
+  g.wgrad = true;
+  g.groups = segments;
+  g.M = M;
+  g.offsets = offsets;
+  const SegMatrix v = work.u;
+  if (st == gemm::kOk && segments > 0 && R > 0 && K > 0) {
+    g.A = transl ? v : x;
+    g.B = transl ? x : v;
+    g.A_lo = transl ? work.u_lo.p : nullptr;
+    g.B_lo = transl ? nullptr : work.u_lo.p;
+    g.C = da;
+    g.K = da.rows;
+    g.N = da.cols;
+    st = launch(g, sms, s);
   }
-  return st;
+  if (st == gemm::kOk && segments > 0 && R > 0 && N > 0) {
+    g.A = transl ? l.X : u;
+    g.B = transl ? u : l.X;
+    g.A_lo = g.B_lo = nullptr;
+    g.C = db;
+    g.K = db.rows;
+    g.N = db.cols;
+    st = launch(g, sms, s);
+  }
+  return work.give_back(st, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,948 @@
+// seg_tc.cu -- segmented matrix products on the tensor cores of sm_103a.
+//
+// A tile of the result is computed transposed, D = L Q^T, on a CTA pair
+// (tcgen05 cta_group::2): 256 lanes n (columns of the result, 128 a CTA) by up
+// to 256 columns q,
+//
+//   rows:   D[n, t] = sum_k B_z[k, n] A[t, k]      q = rows t of one segment
+//   wgrad:  D[n, i] = sum_t B[t, n] A[t, i]        t = rows of the segment
+//
+// so a segment with few rows needs few columns (N of the MMA is the tile's own
+// row count, rounded up to 32): the weights then stream through at the rate of
+// memory whatever the other 240 columns would have cost. Lanes are consecutive
+// in the result's rows.
+//
+// Tiles of all segments form one list, dealt round-robin to persistent pairs;
+// every role walks it by itself from a table of the segments' first tiles,
+// which each CTA makes from the device's offsets at its start. Operands stand
+// in shared memory as lines of 64 contiguous elements (128 bytes, 128-byte
+// swizzle), K-major or MN-major as they lie in memory: no transposed copy.
+//
+// bf16 operands come by TMA, 64 k of 128 + 128 lines a stage, and go to
+// kind::f16 MMAs as they are. float32 operands, and bf16 ones that TMA cannot
+// read as given, are loaded by eight warps; a float32 value is split into
+// three bf16 terms on the way,
+//
+//   x = h + m + l,   h = bf16(x), m = bf16(x - h), l = bf16(x - h - m),
+//
+// exact for finite x (24 bits in three terms of 8; Henry, Tang and Heinecke,
+// "Leveraging the bfloat16 artificial intelligence datatype for
+// higher-precision computations", ARITH 2019). The products hh, hm, mh, mm,
+// hl, lh are summed; those left out are below 2^-24 of |x y|.
+//
+// The tensor core truncates as it adds to an accumulator: sums of K products
+// drift by about 2^-24 per MMA (measured: 4.4e-6 of the result's norm after
+// 256 bf16 MMAs of one accumulator, against 1.1e-6 of an FP32 FMA chain). For
+// float32 each accumulator therefore holds 64 k only, its small products
+// first, and the epilogue warps add it to sums in registers, rounded to
+// nearest, while the next one fills.
+//
+// Every barrier wait is bounded; on a timeout the pair lets its copies and
+// MMAs finish (bounded), frees TMEM and exits, and the host reads the status.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "ptx.cuh"
+#include "segments.h"
+
+namespace gemm {
+
+__device__ int g_seg_status;  // first error recorded by a kernel of this unit
+
+namespace {
+
+constexpr int kLanes = 256;     // result columns per tile (MMA M, of the pair)
+constexpr int kCols = 256;      // most rows per tile (MMA N)
+constexpr int kBK = 64;         // k per stage: one 128-byte line of bf16
+constexpr int kLines = 128;     // lines of one operand per CTA and stage
+constexpr int kOpBytes = kLines * 128;
+constexpr int kColStep = 32;    // granularity of the MMA's N
+constexpr int kRasterM = 8;     // row tiles per raster group
+constexpr uint32_t kTmemCols = 512;
+
+struct SegOperand {
+  const void *p[2];  // one or two terms of the operand
+  long long ld, zs, extent;
+  int vec;           // 8 elements at a multiple of 8 are one aligned load
+};
+
+struct SegTc {
+  int wgrad, dense;
+  int groups, M, N, K, bank;
+  int passes;        // terms summed of a two-term operand: 1 or 2
+  int tiles_n;
+  int q_box;         // TMA: lines per copy of Q (rows kind)
+  SegOperand L, Q;   // plain loads
+  const int64_t *offsets;
+  const int32_t *index;
+  const float *scales;
+  const float *add;  // dense: fp32 addend of the rows that the segments hold
+  long long add_ld, add_extent;
+  void *C, *C_lo;    // C_lo: the result's second term
+  int c_f32;
+  long long c_ld, c_lo_ld, c_stride, c_extent, c_lo_extent;
+  unsigned long long timeout_ns;
+};
+
+template <class T, bool TMA>
+struct Cfg {
+  static constexpr bool kSplit = std::is_same<T, float>::value;  // three-term operands
+  static constexpr int kTerms = kSplit ? 3 : 1;
+  static constexpr int kStageBytes = 2 * kTerms * kOpBytes;
+  static constexpr int kStages = kSplit ? 2 : 6;
+  static constexpr int kMmaWarp = 1;
+  static constexpr int kFixWarp = 2;
+  static constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+  static constexpr int kLoadWarp0 = 12, kLoadWarps = 8;
+  static constexpr int kThreads = 32 * (TMA ? kLoadWarp0 : kLoadWarp0 + kLoadWarps);
+  static constexpr int kFullCount = TMA ? 2 : kLoadWarps + 1;
+};
+
+template <int STAGES>
+struct Shared {
+  uint64_t full[STAGES], empty[STAGES], part[STAGES];
+  uint64_t acc_full[2], acc_empty[2], drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// One tile of the list, as every role sees it.
+struct Tile {
+  int g, z;       // segment; its matrix (-1: none)
+  int n0;         // first lane (result column)
+  int q0, qn;     // first column and how many are in the result
+  int k0, klen;   // first row of the contraction (wgrad) and its length
+  int row0;       // rows kind: row of the result of column 0 is q0 (absolute)
+};
+
+struct Table {
+  int *first;     // [groups + 1] tiles of the segments before
+  int2 *rows;     // [groups] rows of the segment
+};
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int t, Tile &o) {
+  const int groups = p.dense ? 1 : p.groups;
+  if (t >= tab.first[groups]) return false;
+  int lo = 0, hi = groups;  // the segment whose tiles hold t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.first[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int idx = t - tab.first[lo];
+  const int2 rows = tab.rows[lo];
+  const int height = p.wgrad ? p.K : rows.y - rows.x;
+  const int tm = cdiv(height, kCols);
+  // Groups of kRasterM row tiles, lane tiles in the outer loop, so that the
+  // pairs at work at one time share operand tiles in L2.
+  const int group = idx / (kRasterM * p.tiles_n);
+  const int m_first = group * kRasterM;
+  const int width = min(kRasterM, tm - m_first);
+  const int rem = idx - group * kRasterM * p.tiles_n;
+  const int mi = m_first + rem % width, ni = rem / width;
+  o.g = lo;
+  o.n0 = ni * kLanes;
+  o.qn = min(kCols, height - mi * kCols);
+  if (p.wgrad) {
+    o.z = 0;
+    o.q0 = mi * kCols;
+    o.k0 = rows.x;
+    o.klen = rows.y - rows.x;
+  } else {
+    o.z = lo;
+    if (p.dense) {
+      o.z = 0;
+    } else if (p.index != nullptr) {
+      o.z = p.index[lo];
+      if (o.z < 0 || o.z >= p.bank) o.z = -1;
+    } else if (o.z >= p.bank) {
+      o.z = -1;
+    }
+    o.q0 = rows.x + mi * kCols;
+    o.k0 = 0;
+    o.klen = o.z < 0 ? 0 : p.K;
+  }
+  return true;
+}
+
+// MMA columns of a tile: its own, in steps the operand's layout allows (an
+// MN-major Q comes in lines of 64, one per CTA at least).
+template <bool QMN>
+__device__ __forceinline__ int mma_cols(const Tile &t) {
+  constexpr int step = QMN ? 128 : kColStep;
+  return cdiv(t.qn, step) * step;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const SegTc &p,
+                                          volatile int *abort) {
+  const bool ok = mbar_wait_bounded(bar, parity, p.timeout_ns, abort, &g_seg_status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Spin (bounded, ignoring the abort flag) until the phase completes.
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint64_t timeout_ns) {
+  const uint32_t a = smem_addr(bar);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (global_timer_ns() - t0 > timeout_ns) break;
+  }
+}
+
+template <int STAGES>
+struct Ring {
+  uint32_t idx = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++idx == STAGES) {
+      idx = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// ------------------------------------------------------------ instructions --
+
+// D[tmem] (+)= A[smem] B[smem]^T, kind::f16 with bf16 operands, on the pair.
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B bf16
+// (bits 7-9 and 10-12 = 1), MN-major operands (bits 15 and 16), N >> 3 in bits
+// 17-22, M >> 4 in bits 24-28.
+__device__ __forceinline__ uint32_t idesc_bf16(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// Descriptor of the 16 k of step kk. K-major: lines are rows, 8-line atoms 1024
+// bytes apart, a step 32 bytes along the line. MN-major: lines are k, 64 lines
+// to a chunk of 64 elements (8192 bytes), a step 16 lines.
+template <bool MN>
+__device__ __forceinline__ uint64_t line_desc(uint32_t base, int kk) {
+  if (MN) return smem_desc(base + kk * 2048, 8192, 1024, 2);
+  return smem_desc(base + kk * 32, 16, 1024, 2);
+}
+
+// 3-D tiled load whose bytes complete on the barrier at the shared::cluster
+// address `bar` (which may be the pair's other CTA's).
+__device__ __forceinline__ void tma_lines(void *dst, const CUtensorMap *map, uint32_t bar, int x,
+                                          int y, int z) {
+  tma_load_3d_pair(dst, map, bar, x, y, z);
+}
+
+// Arrive on the barrier at the shared::cluster address.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// ------------------------------------------------------------- plain loads --
+
+struct Eight {
+  float v[8];
+};
+
+// Elements [x, x + 8) of the line at `row` (element offset), those at or past
+// `limit` zero.
+template <class T>
+__device__ __forceinline__ Eight load_eight(const SegOperand &o, const T *p, int site,
+                                            long long row, int x, int limit) {
+  Eight e;
+  const long long off = row + x;
+  if (o.vec && x + 8 <= limit && index_ok(site, off, 8, o.extent)) {
+    if constexpr (std::is_same<T, float>::value) {
+      const float4 a = __ldg(reinterpret_cast<const float4 *>(p + off));
+      const float4 b = __ldg(reinterpret_cast<const float4 *>(p + off) + 1);
+      e.v[0] = a.x, e.v[1] = a.y, e.v[2] = a.z, e.v[3] = a.w;
+      e.v[4] = b.x, e.v[5] = b.y, e.v[6] = b.z, e.v[7] = b.w;
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p + off));
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        e.v[2 * i] = __uint_as_float(w[i] << 16);
+        e.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      e.v[i] = x + i < limit && index_ok(site, off + i, 1, o.extent)
+                   ? static_cast<float>(p[off + i])
+                   : 0.0f;
+  }
+  return e;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Store eight elements as bf16, or as the three terms (kOpBytes apart).
+template <int TERMS>
+__device__ __forceinline__ void store_eight(uint8_t *dst, Eight e) {
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack_bf16(e.v[2 * i], e.v[2 * i + 1]);
+      if (t + 1 < TERMS) {  // what the term leaves, exactly
+        e.v[2 * i] -= low_half(w[i]);
+        e.v[2 * i + 1] -= high_half(w[i]);
+      }
+    }
+    *reinterpret_cast<uint4 *>(dst + t * kOpBytes) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <class T, bool TMA>
+__device__ __forceinline__ void set_registers(bool epilogue, bool loader) {
+  // Float32: the epilogue warps hold 128 sums each. 128 x 40 + 256 x 152 +
+  // 256 x 64 registers, within the launch's 640 x 96 (checked by the host).
+  if constexpr (Cfg<T, TMA>::kSplit) {
+    if (epilogue)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    else if (loader)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+  }
+}
+
+// ------------------------------------------------------------------ kernel --
+
+// LMN, QMN: the operand lies with its lane (column) index contiguous.
+template <class T, bool TMA, bool LMN, bool QMN>
+__global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
+    seg_tc_kernel(const __grid_constant__ CUtensorMap map_l0,
+                  const __grid_constant__ CUtensorMap map_l1,
+                  const __grid_constant__ CUtensorMap map_q0,
+                  const __grid_constant__ CUtensorMap map_q1, const SegTc p) {
+  using C = Cfg<T, TMA>;
+  constexpr int STAGES = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *stages = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Shared<STAGES> *sh = reinterpret_cast<Shared<STAGES> *>(stages + STAGES * C::kStageBytes);
+  Table tab;
+  tab.rows = reinterpret_cast<int2 *>(sh + 1);
+  const int groups = p.dense ? 1 : p.groups;
+  tab.first = reinterpret_cast<int *>(tab.rows + groups);
+  volatile int *abort = &sh->abort;
+
+  const uint32_t warp = warp_index();
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&sh->full[s], C::kFullCount);
+      mbar_init(&sh->empty[s], 1);
+      // TMA: this CTA's bytes of a stage that is masked before use; plain
+      // loads: this CTA's load warps, passed on by the odd CTA's relay.
+      mbar_init(&sh->part[s], TMA ? 1 : C::kLoadWarps);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sh->acc_full[a], 1);
+      mbar_init(&sh->acc_empty[a], 2 * C::kEpiWarps);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_barrier_init();
+  }
+  if (TMA && warp == 0 && lane == 0) {
+    tma_prefetch_map(&map_l0);
+    tma_prefetch_map(&map_q0);
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc<2>(&sh->tmem_base, kTmemCols);
+    tmem_relinquish<2>();
+  }
+  grid_dependency_wait();
+  // The table of segments: their rows, and the tiles before each.
+  for (int g = threadIdx.x; g < groups; g += C::kThreads) {
+    int2 r = make_int2(0, p.M);
+    if (!p.dense) {
+      const long long a = p.offsets[g], b = p.offsets[g + 1];
+      const long long s = a < 0 ? 0 : (a > p.M ? p.M : a);
+      r = make_int2(static_cast<int>(s), static_cast<int>(b < s ? s : (b > p.M ? p.M : b)));
+    }
+    tab.rows[g] = r;
+    tab.first[g] = cdiv(p.wgrad ? p.K : r.y - r.x, kCols) * p.tiles_n;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int sum = 0;
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+      const int g = g0 + static_cast<int>(lane);
+      const int own = g < groups ? tab.first[g] : 0;
+      int v = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, d);
+        if (static_cast<int>(lane) >= d) v += w;
+      }
+      if (g < groups) tab.first[g] = sum + v - own;
+      sum += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) tab.first[groups] = sum;
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // barriers and TMEM of both CTAs are set up
+  tc_fence_after_sync();
+  const uint32_t tmem = sh->tmem_base;
+  grid_launch_dependents();
+
+  const bool epilogue = warp >= C::kEpiWarp0 && warp < C::kEpiWarp0 + C::kEpiWarps;
+  const bool loader = !TMA && warp >= C::kLoadWarp0;
+  set_registers<T, TMA>(epilogue, loader);
+
+  Tile t;
+  if (TMA && warp == 0) {
+    // ------------------------------------------------------------- copies --
+    if (lane == 0) {
+      Ring<STAGES> r;
+      uint32_t armed_full = 0, armed_part = 0, parity_full = 0, parity_part = 0, part_phase = 0;
+      bool ok = true;
+      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+        const int half = mma_cols<QMN>(t) / 2;
+        const int ln = t.n0 + static_cast<int>(rank) * 128;
+        const int qn = t.q0 + static_cast<int>(rank) * half;
+        const int copies = QMN ? half / 64 : cdiv(half, p.q_box);
+        const uint32_t bytes =
+            kOpBytes + static_cast<uint32_t>(copies) * (QMN ? 8192u : 128u * p.q_box);
+        const int blocks = cdiv(t.klen, kBK);
+        for (int kb = 0; kb < blocks * p.passes; ++kb) {
+          if (!mbar_wait_bounded(&sh->empty[r.idx], r.phase ^ 1, p.timeout_ns, abort,
+                                 &g_seg_status)) {
+            ok = false;
+            break;
+          }
+          const int second = kb >= blocks, kk = (second ? kb - blocks : kb) * kBK;
+          const CUtensorMap *ml = second ? &map_l1 : &map_l0, *mq = second ? &map_q1 : &map_q0;
+          uint8_t *st = stages + r.idx * C::kStageBytes;
+          const int tail = t.klen - kk;
+          const bool fix = QMN && tail < kBK && tail % 16 != 0;
+          uint32_t bar;
+          if (fix) {  // this CTA's own barrier; the fix warp passes it on
+            bar = smem_addr(&sh->part[r.idx]);
+            mbar_arrive_expect_tx(&sh->part[r.idx], bytes);
+            armed_part |= 1u << r.idx;
+            parity_part = (parity_part & ~(1u << r.idx)) | (part_phase & (1u << r.idx));
+            part_phase ^= 1u << r.idx;
+          } else {
+            bar = mbar_cluster_addr(&sh->full[r.idx], 0);
+            if (rank == 0) {
+              mbar_arrive_expect_tx(&sh->full[r.idx], 2 * bytes);
+              mbar_arrive(&sh->full[r.idx]);
+            }
+            armed_full |= 1u << r.idx;
+            parity_full = (parity_full & ~(1u << r.idx)) | (r.phase << r.idx);
+          }
+          if (LMN) {
+            tma_lines(st, ml, bar, ln, t.k0 + kk, t.z);
+            tma_lines(st + 8192, ml, bar, ln + 64, t.k0 + kk, t.z);
+          } else {
+            tma_lines(st, ml, bar, kk, ln, t.z);
+          }
+          for (int c = 0; c < copies; ++c) {
+            if (QMN)
+              tma_lines(st + kOpBytes + c * 8192, mq, bar, qn + c * 64, t.k0 + kk, 0);
+            else
+              tma_lines(st + kOpBytes + c * p.q_box * 128, mq, bar, kk, qn + c * p.q_box, 0);
+          }
+          r.next();
+        }
+      }
+      // On a timeout let the copies that were started land.
+      if (!ok)
+        for (int s = 0; s < STAGES; ++s) {
+          if (rank == 0 && (armed_full >> s & 1u))
+            drain_wait(&sh->full[s], parity_full >> s & 1u, p.timeout_ns);
+          if (armed_part >> s & 1u) drain_wait(&sh->part[s], parity_part >> s & 1u, p.timeout_ns);
+        }
+    }
+    __syncwarp();
+  } else if (TMA && QMN && warp == C::kFixWarp) {
+    // -------------------------------------------------------------- masks --
+    // The last stage of a segment whose rows end inside a step of 16: zero
+    // both operands' lines from its end to the step's, which hold the next
+    // segment's rows (whatever they are: NaN times zero is NaN).
+    Ring<STAGES> r;
+    uint32_t part_phase = 0;
+    bool ok = true;
+    for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+      const int half = mma_cols<QMN>(t) / 2;
+      const int blocks = cdiv(t.klen, kBK);
+      for (int kb = 0; kb < blocks * p.passes; ++kb) {
+        const int kk = (kb >= blocks ? kb - blocks : kb) * kBK;
+        const int tail = t.klen - kk;
+        if (tail < kBK && tail % 16 != 0) {
+          if (!warp_wait(&sh->part[r.idx], part_phase >> r.idx & 1u, p, abort)) {
+            ok = false;
+            break;
+          }
+          part_phase ^= 1u << r.idx;
+          uint8_t *st = stages + r.idx * C::kStageBytes;
+          const int end = (tail + 15) / 16 * 16;
+          const int chunks = 2 + half / 64;  // of L, then of Q
+          for (int e = static_cast<int>(lane); e < chunks * (end - tail) * 8; e += 32) {
+            const int c = e / ((end - tail) * 8), w = e % ((end - tail) * 8);
+            *reinterpret_cast<uint4 *>(st + c * 8192 + (tail + w / 8) * 128 + w % 8 * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->full[r.idx], 0));
+        }
+        r.next();
+      }
+    }
+  } else if (warp == C::kMmaWarp) {
+    if (rank == 0 && lane == 0) {
+      // --------------------------------------------------- MMA (even CTA) --
+      Ring<STAGES> r;
+      Ring<2> acc;
+      bool ok = true;
+      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+        const int blocks = cdiv(t.klen, kBK);
+        const uint32_t idesc = idesc_bf16(kLanes, static_cast<uint32_t>(mma_cols<QMN>(t)), LMN, QMN);
+        for (int kb = 0; kb < blocks * p.passes; ++kb) {
+          const bool first = C::kSplit || kb == 0;
+          if (first) {
+            // Both CTAs' epilogues have drained the accumulator.
+            if (!mbar_wait_bounded<true>(&sh->acc_empty[acc.idx], acc.phase ^ 1, p.timeout_ns,
+                                         abort, &g_seg_status)) {
+              ok = false;
+              break;
+            }
+          }
+          if (!mbar_wait_bounded<true>(&sh->full[r.idx], r.phase, p.timeout_ns, abort,
+                                       &g_seg_status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const int kk0 = (kb >= blocks ? kb - blocks : kb) * kBK;
+          const int steps = min(kBK / 16, cdiv(t.klen - kk0, 16));
+          const uint32_t l = smem_addr(stages + r.idx * C::kStageBytes);
+          const uint32_t q = l + C::kTerms * kOpBytes;
+          const uint32_t d = tmem + acc.idx * kCols;
+          if constexpr (C::kSplit) {
+            // Small products first: mm, hl, lh, hm, mh, then hh.
+            constexpr int tl[6] = {1, 0, 2, 0, 1, 0}, tq[6] = {1, 2, 0, 1, 0, 0};
+            uint32_t more = 0;
+#pragma unroll
+            for (int c = 0; c < 6; ++c)
+              for (int kk = 0; kk < steps; ++kk) {
+                mma_bf16_pair(d, line_desc<LMN>(l + tl[c] * kOpBytes, kk),
+                              line_desc<QMN>(q + tq[c] * kOpBytes, kk), idesc, more);
+                more = 1;
+              }
+          } else {
+            for (int kk = 0; kk < steps; ++kk)
+              mma_bf16_pair(d, line_desc<LMN>(l, kk), line_desc<QMN>(q, kk), idesc,
+                            kb != 0 || kk != 0);
+          }
+          mma_commit_multicast<2>(&sh->empty[r.idx], 3);
+          if (C::kSplit || kb + 1 == blocks * p.passes) {
+            mma_commit_multicast<2>(&sh->acc_full[acc.idx], 3);
+            acc.next();
+          }
+          r.next();
+        }
+      }
+      // Every MMA issued completes before TMEM is released.
+      mma_commit_multicast<2>(&sh->drain, 1);
+      drain_wait(&sh->drain, 0, p.timeout_ns);
+    } else if (!TMA && rank == 1 && lane == 0) {
+      // ----------------------------------------------------- relay (odd) --
+      Ring<STAGES> r;
+      bool ok = true;
+      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+        const int n = cdiv(t.klen, kBK) * p.passes;
+        for (int kb = 0; kb < n; ++kb) {
+          if (!mbar_wait_bounded(&sh->part[r.idx], r.phase, p.timeout_ns, abort, &g_seg_status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_at(mbar_cluster_addr(&sh->full[r.idx], 0));
+          r.next();
+        }
+      }
+    }
+    __syncwarp();
+  } else if (epilogue) {
+    // ----------------------------------------------------------- epilogue --
+    const uint32_t quad = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
+    const uint32_t tlane = tmem + ((quad * 32) << 16) + part * 128;
+    Ring<2> acc;
+    bool ok = true;
+    long long add0 = 0, add1 = 0;  // rows with an addend
+    if (p.add != nullptr) {
+      add0 = p.offsets[0];
+      add1 = p.offsets[p.groups];
+    }
+    for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+      const int blocks = cdiv(t.klen, kBK) * p.passes;
+      const int n = t.n0 + static_cast<int>(rank * 128 + quad * 32 + lane);
+      const int c0 = static_cast<int>(part) * 128;
+      const float scale =
+          !p.wgrad && !p.dense && p.scales != nullptr && t.z >= 0 ? p.scales[t.z] : 1.0f;
+      const long long base = p.wgrad ? t.g * p.c_stride : 0;
+      auto store = [&](int c, float v) {  // column c of the tile
+        if (n >= p.N || c >= t.qn) return;
+        const long long row = t.q0 + c;
+        v *= scale;
+        if (row >= add0 && row < add1 && index_ok(kSitePartialRead, row * p.add_ld + n, 1, p.add_extent))
+          v += p.add[row * p.add_ld + n];
+        const long long off = base + row * p.c_ld + n;
+        if (!index_ok(kSiteCStore, off, 1, p.c_extent)) return;
+        if (p.c_f32) {
+          static_cast<float *>(p.C)[off] = v;
+        } else {
+          const __nv_bfloat16 h = __float2bfloat16_rn(v);
+          static_cast<__nv_bfloat16 *>(p.C)[off] = h;
+          const long long lo = row * p.c_lo_ld + n;
+          if (p.C_lo != nullptr && index_ok(kSitePartialWrite, lo, 1, p.c_lo_extent))
+            static_cast<__nv_bfloat16 *>(p.C_lo)[lo] = __float2bfloat16_rn(v - static_cast<float>(h));
+        }
+      };
+      if constexpr (C::kSplit) {
+        float sum[128];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) sum[c] = 0.0f;
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (!warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < 128; c += 16)
+            if (c0 + c < t.qn) {
+              uint32_t v[16];
+              tmem_load_16cols(tlane + acc.idx * kCols + c, v);
+              tmem_load_wait();
+              tmem_regs_ready(v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[c + j] += __uint_as_float(v[j]);
+            }
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[acc.idx], 0));
+          acc.next();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) store(c0 + c, sum[c]);
+      } else {
+        if (blocks > 0) {
+          if (!warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort)) break;
+          tc_fence_after_sync();
+        }
+        for (int c = 0; c < 128 && c0 + c < t.qn; c += 32) {
+          uint32_t v[32];
+          if (blocks > 0) {
+            tmem_load_32cols(tlane + acc.idx * kCols + c, v);
+            tmem_load_wait();
+            tmem_regs_ready(v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) store(c0 + c + j, __uint_as_float(v[j]));
+        }
+        if (blocks > 0) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[acc.idx], 0));
+          acc.next();
+        }
+      }
+    }
+  } else if (loader) {
+    // -------------------------------------------------------- plain loads --
+    // Eight lanes to a line of 64 elements, four lines a warp and load; both
+    // operands are masked here, by row and by column.
+    const int lw = static_cast<int>(warp) - C::kLoadWarp0;
+    const int sub = static_cast<int>(lane) >> 3, j = static_cast<int>(lane) & 7;
+    Ring<STAGES> r;
+    bool ok = true;
+    for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+      const int half = mma_cols<QMN>(t) / 2;
+      const int ln = t.n0 + static_cast<int>(rank) * 128;
+      const int qn = static_cast<int>(rank) * half;  // within the tile
+      const int blocks = cdiv(t.klen, kBK);
+      for (int kb = 0; kb < blocks * p.passes; ++kb) {
+        const int second = kb >= blocks, kk = (second ? kb - blocks : kb) * kBK;
+        uint8_t *st = stages + r.idx * C::kStageBytes;
+        bool free = false;
+#pragma unroll
+        for (int op = 0; op < 2; ++op) {
+          const SegOperand &o = op == 0 ? p.L : p.Q;
+          const bool mn = op == 0 ? LMN : QMN;
+          const T *src = static_cast<const T *>(second ? o.p[1] : o.p[0]);
+          const int site = op == 0 ? kSiteLoadB : kSiteLoadA;
+          const long long z = op == 0 ? t.z * o.zs : 0;
+          Eight e[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int line = s * 32 + lw * 4 + sub;
+            long long row;
+            int x, limit;
+            if (mn) {  // line: k; elements: lanes or columns
+              const int k = kk + (line & 63);
+              x = (op == 0 ? ln : t.q0 + qn) + (line >> 6) * 64 + j * 8;
+              limit = k < t.klen ? (op == 0 ? p.N : p.K) : 0;
+              if (op == 1 && (line >> 6) * 64 >= half) limit = 0;
+              row = z + static_cast<long long>(t.k0 + k) * o.ld;
+            } else {
+              const int m = op == 0 ? ln + line : qn + line;
+              x = kk + j * 8;
+              limit = (op == 0 ? m < p.N : line < half && m < t.qn) ? p.K : 0;
+              row = z + static_cast<long long>(op == 0 ? m : t.q0 + m) * o.ld;
+            }
+            e[s] = load_eight<T>(o, src, site, row, x, limit);
+          }
+          if (!free) {
+            if (!warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
+              ok = false;
+              break;
+            }
+            free = true;
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const int line = s * 32 + lw * 4 + sub;
+            if (op == 1 && !mn && line >= half) continue;  // no MMA column
+            store_eight<C::kTerms>(st + op * C::kTerms * kOpBytes + line * 128 +
+                                       ((j ^ (line & 7)) * 16),
+                                   e[s]);
+          }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rank == 0 ? &sh->full[r.idx] : &sh->part[r.idx]);
+        r.next();
+      }
+    }
+  }
+
+  // Neither CTA frees its TMEM or leaves while the pair's MMAs, copies or
+  // arrivals may still reach it.
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc<2>(tmem, kTmemCols);
+  }
+}
+
+// -------------------------------------------------------------------- host --
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// bf16 map over a stack of row-major matrices, zero outside each: lines of 64
+// columns, `lines` rows a copy.
+bool encode_lines(const SegMatrix &m, const void *ptr, int lines, CUtensorMap *out) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const bool stack = m.count > 1 && m.stride > 0;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
+                              static_cast<cuuint64_t>(stack ? m.count : 1)};
+  const cuuint64_t pitch = static_cast<cuuint64_t>(m.ld) * 2;
+  const cuuint64_t strides[2] = {pitch, stack ? static_cast<cuuint64_t>(m.stride) * 2 : pitch};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(lines), 1}, step[3] = {1, 1, 1};
+  return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
+            step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// TMA reads 16-byte aligned rows; a stride of zero (one matrix for all) is not
+// a stride of its maps.
+bool tma_ok(const SegMatrix &m, const void *p) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && m.ld % 8 == 0 && m.stride % 8 == 0 &&
+         (m.count <= 1 || m.stride > 0);
+}
+
+long long extent_of(const SegMatrix &m) {
+  return (m.count - 1) * m.stride + matrix_extent(m.rows, m.cols, m.ld);
+}
+
+SegOperand operand_of(const SegMatrix &m, const void *second, int elem) {
+  SegOperand o;
+  o.p[0] = m.p;
+  o.p[1] = second != nullptr ? second : m.p;
+  o.ld = m.ld;
+  o.zs = m.stride;
+  o.extent = extent_of(m);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(o.p[0]) | reinterpret_cast<uintptr_t>(o.p[1]);
+  const int per16 = 16 / elem;
+  o.vec = at % 16 == 0 && m.ld % per16 == 0 && m.stride % per16 == 0;
+  return o;
+}
+
+template <class T, bool TMA, bool LMN, bool QMN>
+int launch(const CUtensorMap (&maps)[4], const SegTc &p, int sm_count, cudaStream_t stream) {
+  using C = Cfg<T, TMA>;
+  auto *kernel = seg_tc_kernel<T, TMA, LMN, QMN>;
+  const int groups = p.dense ? 1 : p.groups;
+  const int fixed = C::kStages * C::kStageBytes + static_cast<int>(sizeof(Shared<C::kStages>)) + 1024;
+  const int smem = fixed + groups * 12 + 4;
+  static std::once_flag once;
+  static bool ready = false;
+  std::call_once(once, [&] {
+    cudaFuncAttributes at;
+    ready = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 fixed + kMaxSegments * 12 + 4) == cudaSuccess &&
+            cudaFuncGetAttributes(&at, kernel) == cudaSuccess &&
+            // the register split draws on the launch's registers
+            (!C::kSplit || at.numRegs * C::kThreads >= 128 * 40 + 256 * 152 + 256 * 64);
+  });
+  if (!ready) return kErrLaunch;
+  // Tiles at most: every segment may end in a part tile.
+  const long long height = p.wgrad ? p.K : p.M;
+  long long tiles = p.wgrad ? static_cast<long long>(groups) * ((height + kCols - 1) / kCols)
+                            : height / kCols + (p.dense ? 1 : groups);
+  tiles *= p.tiles_n;
+  if (tiles > 0x7fffffffLL) return kErrInvalidArg;
+  long long pairs = sm_count / 2;
+  if (pairs > tiles) pairs = tiles;
+  if (pairs < 1) pairs = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], p) == cudaSuccess
+             ? kOk
+             : kErrLaunch;
+}
+
+template <class T, bool TMA>
+int launch_layout(bool lmn, bool qmn, const CUtensorMap (&maps)[4], const SegTc &p, int sm_count,
+                  cudaStream_t stream) {
+  if (qmn) return launch<T, TMA, true, true>(maps, p, sm_count, stream);
+  if (lmn) return launch<T, TMA, true, false>(maps, p, sm_count, stream);
+  return launch<T, TMA, false, false>(maps, p, sm_count, stream);
+}
+
+}  // namespace
+
+GEMM_INDEX_FAULT_TAKE(seg_tc_index_fault_take)
+
+int seg_tc_poll_status(cudaStream_t stream) {
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return kErrLaunch;
+  int h = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&h, g_seg_status, sizeof(int)) != cudaSuccess) return kErrLaunch;
+  if (h != 0 && cudaMemcpyToSymbol(g_seg_status, &zero, sizeof(int)) != cudaSuccess)
+    return kErrLaunch;
+  return h;
+}
+
+int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
+  SegTc p = {};
+  p.wgrad = a.wgrad;
+  p.dense = a.dense;
+  p.groups = static_cast<int>(a.groups);
+  p.M = static_cast<int>(a.M);
+  p.N = static_cast<int>(a.N);
+  p.K = static_cast<int>(a.K);
+  p.bank = static_cast<int>(a.bank);
+  p.passes = a.A_lo != nullptr || a.B_lo != nullptr ? 2 : 1;
+  p.tiles_n = static_cast<int>((a.N + kLanes - 1) / kLanes);
+  p.offsets = a.offsets;
+  p.index = a.index;
+  p.scales = a.scales;
+  p.add = static_cast<const float *>(a.add.p);
+  p.add_ld = a.add.ld;
+  p.add_extent = extent_of(a.add);
+  p.C = const_cast<void *>(a.C.p);
+  p.c_f32 = !a.bf16 || a.c_f32;
+  p.c_ld = a.C.ld;
+  p.c_stride = a.C.stride;
+  p.c_extent = extent_of(a.C);
+  p.C_lo = const_cast<void *>(a.C_lo.p);
+  p.c_lo_ld = a.C_lo.ld;
+  p.c_lo_extent = extent_of(a.C_lo);
+  // 2 s, and 2 us for each k of the longest contraction.
+  p.timeout_ns = 2000000000ull + 2000ull * static_cast<unsigned long long>(a.wgrad ? a.M : a.K);
+  // Lines per copy of Q: about half a tile's rows, as the average segment has
+  // them, so that small segments do not read their neighbours' rows.
+  const long long average = p.dense ? a.M : a.M / (a.groups > 0 ? a.groups : 1);
+  p.q_box = average <= 64 ? 32 : (average <= 128 ? 64 : 128);
+  const bool lmn = a.wgrad || !a.transb, qmn = a.wgrad;
+  p.L = operand_of(a.B, a.B_lo, a.bf16 ? 2 : 4);
+  p.Q = operand_of(a.A, a.A_lo, a.bf16 ? 2 : 4);
+  CUtensorMap maps[4];
+  std::memset(maps, 0, sizeof(maps));
+  if (!a.bf16) return launch_layout<float, false>(lmn, qmn, maps, p, sm_count, stream);
+  const bool empty = a.K == 0 || a.M == 0;  // no operand is read
+  if (!empty && tma_ok(a.B, p.L.p[0]) && tma_ok(a.B, p.L.p[1]) && tma_ok(a.A, p.Q.p[0]) &&
+      tma_ok(a.A, p.Q.p[1])) {
+    const int l_lines = lmn ? 64 : 128, q_lines = qmn ? 64 : p.q_box;
+    if (encode_lines(a.B, p.L.p[0], l_lines, &maps[0]) &&
+        encode_lines(a.B, p.L.p[1], l_lines, &maps[1]) &&
+        encode_lines(a.A, p.Q.p[0], q_lines, &maps[2]) &&
+        encode_lines(a.A, p.Q.p[1], q_lines, &maps[3]))
+      return launch_layout<__nv_bfloat16, true>(lmn, qmn, maps, p, sm_count, stream);
+    return kErrLaunch;
+  }
+  return launch_layout<__nv_bfloat16, false>(lmn, qmn, maps, p, sm_count, stream);
+}
+
+}  // namespace gemm

@@ -23,8 +23,7 @@ struct SegMatrix {
 // matrix for each segment (wgrad = true):
 //
 //   rows:   C[t, :] = scale_z A[t, :] op(B_z)  for the rows t of segment g,
-//           z = index[g] (or g); dense: all M rows with B_0, plus U[t, :]
-//           op(L_z) for the rows of segments with an adapter (R > 0)
+//           z = index[g] (or g); dense: all M rows with B_0, plus `add`
 //   wgrad:  C_g = A_g^T B_g, the sum over the rows of segment g
 struct SegArgs {
   bool bf16 = false, wgrad = false, dense = false;
@@ -35,15 +34,21 @@ struct SegArgs {
   const int32_t *index = nullptr;
   const float *scales = nullptr;
   int64_t bank = 0;  // matrices z may name; others: no product
-  int64_t R = 0;     // dense: width of U
-  SegMatrix U, L;
-  int transl = 0;
+  // Second terms of A and B (same layout; the sum A + A_lo, or B + B_lo, is
+  // meant; at most one of them), and of the result: C + C_lo, C rounded.
+  const void *A_lo = nullptr, *B_lo = nullptr;
+  SegMatrix C_lo;
+  bool c_f32 = false;  // a float32 result of bf16 operands
+  SegMatrix add;       // dense: float32 addend of the result
 };
 
 // Requires M, N >= 1 (rows) or groups, N, K >= 1 (wgrad).
-int seg_simt_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
+int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
 
-int seg_simt_index_fault_take(IndexFault *out, bool clear);
+int seg_tc_index_fault_take(IndexFault *out, bool clear);
+
+// Synchronise `stream`, then read and clear the kernels' status word.
+int seg_tc_poll_status(cudaStream_t stream);
 
 // Capability check and SM count of the current device (api.cu).
 int current_device_info(int *dev_out, int *sm_count);

@@ -101,12 +101,13 @@ int gemm_f32_grouped_wgrad(int type, int64_t groups, int64_t M, int64_t N, int64
  *             rows of no segment, get X op(W) alone.
  *   scales    device float, s_a for each adapter; NULL: 1
  *   U, ldu    receives U (rows of no segment are not written, those of a
- *             segment without adapter are zero); NULL: kept in a workspace
- *             from the library's pool. For GEMM_F32_TYPE_BF16 it is rounded to
- *             bf16, here as there: it is an operand of the second product.
+ *             segment without adapter are zero), rounded to the type: what
+ *             gemm_f32_lora_backward takes. NULL: not returned. The second
+ *             product takes U unrounded (bf16: as the sum of two bf16 terms).
  *   Y         all M rows are written; Y and U must not overlap anything else
  *             (GEMM_ERR_ALIAS)
- * R == 0 is the projection alone.
+ * R == 0 is the projection alone. U's terms and U B (M x N fp32) stand in a
+ * workspace from the library's stream-ordered pool meanwhile.
  */
 int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t bank,
                   int64_t M, int64_t N, int64_t K, int64_t R,
@@ -117,6 +118,31 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
                   const int64_t *offsets, const int32_t *index, const float *scales,
                   void *U, int64_t ldu,
                   void *Y, int64_t ldy, void *stream);
+
+/*
+ * gemm_f32_lora_backward -- gradients of gemm_f32_lora on a frozen W, with
+ * adapter g for segment g (rows sorted by adapter):
+ *
+ *     V = s_g (dY B_g^T),   dX = dY op(W)^T + V A_g^T,
+ *     dA_g = X^T V,         dB_g = U^T dY        over the rows of segment g
+ *
+ *   U         the forward's U, M x R
+ *   dA, dB    as A and B are stored (transl), pitches ldda, lddb and strides
+ *             strideda, stridedb; empty segments' are zero
+ *   others    as for gemm_f32_lora
+ */
+int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments,
+                           int64_t M, int64_t N, int64_t K, int64_t R,
+                           const void *dY, int64_t lddy,
+                           const void *X, int64_t ldx,
+                           const void *U, int64_t ldu,
+                           const void *W, int64_t ldw,
+                           const void *A, int64_t lda, int64_t stridea,
+                           const void *B, int64_t ldb, int64_t strideb,
+                           const int64_t *offsets, const float *scales,
+                           void *dX, int64_t lddx,
+                           void *dA, int64_t ldda, int64_t strideda,
+                           void *dB, int64_t lddb, int64_t stridedb, void *stream);
 
 #ifdef __cplusplus
 }
