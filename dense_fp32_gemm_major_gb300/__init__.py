@@ -510,8 +510,12 @@ def _call(name, device, stream, *args):
 
     if stream is None:
         stream = torch.cuda.current_stream(device).cuda_stream
-    with torch.cuda.device(device):
-        st = globals()[name](*args, stream)
+    function = getattr(_lib or _load(), name)
+    if torch.cuda.current_device() == device.index:
+        st = function(*args, stream or None)
+    else:
+        with torch.cuda.device(device):
+            st = function(*args, stream or None)
     if st != OK:
         raise GemmError(st, name)
 

@@ -79,6 +79,7 @@ struct SegTc {
   int passes;        // terms summed of a two-term operand: 1 or 2
   int tiles_n;
   int q_box;         // TMA: lines per copy of Q (rows kind)
+  int l_whole, q_whole;  // TMA: an MN-major operand comes as one 4-D copy
   SegOperand L, Q;   // plain loads
   const int64_t *offsets;
   const int32_t *index;
@@ -152,11 +153,16 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int t,
   const int rem = idx - group * kRasterM * p.tiles_n;
   const int mi = m_first + rem % width, ni = rem / width;
   o.g = lo;
+  // The segment's rows in tm equal parts (in steps of kColStep), not whole
+  // tiles and a rest: the pairs end together, and no tile is all operand
+  // traffic and no work.
+  const int step = p.wgrad ? 128 : kColStep;
+  const int width_q = cdiv(cdiv(height, tm), step) * step;
   o.n0 = ni * kLanes;
-  o.qn = min(kCols, height - mi * kCols);
+  o.qn = min(width_q, height - mi * width_q);
   if (p.wgrad) {
     o.z = 0;
-    o.q0 = mi * kCols;
+    o.q0 = mi * width_q;
     o.k0 = rows.x;
     o.klen = rows.y - rows.x;
   } else {
@@ -169,7 +175,7 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int t,
     } else if (o.z >= p.bank) {
       o.z = -1;
     }
-    o.q0 = rows.x + mi * kCols;
+    o.q0 = rows.x + mi * width_q;
     o.k0 = 0;
     o.klen = o.z < 0 ? 0 : p.K;
   }
@@ -238,13 +244,6 @@ template <bool MN>
 __device__ __forceinline__ uint64_t line_desc(uint32_t base, int kk) {
   if (MN) return smem_desc(base + kk * 2048, 8192, 1024, 2);
   return smem_desc(base + kk * 32, 16, 1024, 2);
-}
-
-// 3-D tiled load whose bytes complete on the barrier at the shared::cluster
-// address `bar` (which may be the pair's other CTA's).
-__device__ __forceinline__ void tma_lines(void *dst, const CUtensorMap *map, uint32_t bar, int x,
-                                          int y, int z) {
-  tma_load_3d_pair(dst, map, bar, x, y, z);
 }
 
 // Arrive on the barrier at the shared::cluster address.
@@ -463,17 +462,23 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
             armed_full |= 1u << r.idx;
             parity_full = (parity_full & ~(1u << r.idx)) | (r.phase << r.idx);
           }
-          if (LMN) {
-            tma_lines(st, ml, bar, ln, t.k0 + kk, t.z);
-            tma_lines(st + 8192, ml, bar, ln + 64, t.k0 + kk, t.z);
+          if (!LMN) {
+            tma_load_3d_pair(st, ml, bar, kk, ln, t.z);
+          } else if (p.l_whole) {
+            tma_load_4d_pair(st, ml, bar, 0, t.k0 + kk, ln / 64, t.z);
           } else {
-            tma_lines(st, ml, bar, kk, ln, t.z);
+            tma_load_3d_pair(st, ml, bar, ln, t.k0 + kk, t.z);
+            tma_load_3d_pair(st + 8192, ml, bar, ln + 64, t.k0 + kk, t.z);
           }
-          for (int c = 0; c < copies; ++c) {
-            if (QMN)
-              tma_lines(st + kOpBytes + c * 8192, mq, bar, qn + c * 64, t.k0 + kk, 0);
-            else
-              tma_lines(st + kOpBytes + c * p.q_box * 128, mq, bar, kk, qn + c * p.q_box, 0);
+          if (QMN && p.q_whole) {
+            tma_load_4d_pair(st + kOpBytes, mq, bar, 0, t.k0 + kk, qn / 64, 0);
+          } else {
+            for (int c = 0; c < copies; ++c) {
+              if (QMN)
+                tma_load_3d_pair(st + kOpBytes + c * 8192, mq, bar, qn + c * 64, t.k0 + kk, 0);
+              else
+                tma_load_3d_pair(st + kOpBytes + c * p.q_box * 128, mq, bar, kk, qn + c * p.q_box, 0);
+            }
           }
           r.next();
         }
@@ -541,8 +546,10 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               break;
             }
           }
-          if (!mbar_wait_bounded<true>(&sh->full[r.idx], r.phase, p.timeout_ns, abort,
-                                       &g_seg_status)) {
+          // Copies alone complete a stage of the rows form; other stages have
+          // arrivals of the odd CTA's warps (acquire at cluster scope).
+          if (!mbar_wait_bounded<!TMA || QMN>(&sh->full[r.idx], r.phase, p.timeout_ns, abort,
+                                              &g_seg_status)) {
             ok = false;
             break;
           }
@@ -600,42 +607,25 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     // ----------------------------------------------------------- epilogue --
     const uint32_t quad = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
     const uint32_t tlane = tmem + ((quad * 32) << 16) + part * 128;
+    const int c0 = static_cast<int>(part) * 128;  // this warp's first column
     Ring<2> acc;
-    bool ok = true;
-    long long add0 = 0, add1 = 0;  // rows with an addend
+    int add0 = 0, add1 = 0;  // rows with an addend
     if (p.add != nullptr) {
-      add0 = p.offsets[0];
-      add1 = p.offsets[p.groups];
+      const long long a = p.offsets[0], b = p.offsets[p.groups];
+      add0 = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
+      add1 = static_cast<int>(b < 0 ? 0 : (b > p.M ? p.M : b));
     }
-    for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+    for (int i = pair; tile_at(p, tab, i, t); i += pairs) {
       const int blocks = cdiv(t.klen, kBK) * p.passes;
       const int n = t.n0 + static_cast<int>(rank * 128 + quad * 32 + lane);
-      const int c0 = static_cast<int>(part) * 128;
-      const float scale =
-          !p.wgrad && !p.dense && p.scales != nullptr && t.z >= 0 ? p.scales[t.z] : 1.0f;
-      const long long base = p.wgrad ? t.g * p.c_stride : 0;
-      auto store = [&](int c, float v) {  // column c of the tile
-        if (n >= p.N || c >= t.qn) return;
-        const long long row = t.q0 + c;
-        v *= scale;
-        if (row >= add0 && row < add1 && index_ok(kSitePartialRead, row * p.add_ld + n, 1, p.add_extent))
-          v += p.add[row * p.add_ld + n];
-        const long long off = base + row * p.c_ld + n;
-        if (!index_ok(kSiteCStore, off, 1, p.c_extent)) return;
-        if (p.c_f32) {
-          static_cast<float *>(p.C)[off] = v;
-        } else {
-          const __nv_bfloat16 h = __float2bfloat16_rn(v);
-          static_cast<__nv_bfloat16 *>(p.C)[off] = h;
-          const long long lo = row * p.c_lo_ld + n;
-          if (p.C_lo != nullptr && index_ok(kSitePartialWrite, lo, 1, p.c_lo_extent))
-            static_cast<__nv_bfloat16 *>(p.C_lo)[lo] = __float2bfloat16_rn(v - static_cast<float>(h));
-        }
-      };
       if constexpr (C::kSplit) {
+        // Sum the accumulators of 64 k each in registers; the sums go back to
+        // TMEM in the place of the last one, so that float32 and bf16 results
+        // leave through the same short loop.
         float sum[128];
 #pragma unroll
         for (int c = 0; c < 128; ++c) sum[c] = 0.0f;
+        bool ok = true;
         for (int kb = 0; kb < blocks; ++kb) {
           if (!warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort)) {
             ok = false;
@@ -650,40 +640,96 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               tmem_load_wait();
               tmem_regs_ready(v);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) sum[c + j] += __uint_as_float(v[j]);
+              for (int k = 0; k < 16; ++k) sum[c + k] += __uint_as_float(v[k]);
             }
+          if (kb + 1 == blocks) break;
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[acc.idx], 0));
           acc.next();
         }
         if (!ok) break;
+        if (blocks > 1) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c) store(c0 + c, sum[c]);
-      } else {
-        if (blocks > 0) {
-          if (!warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort)) break;
-          tc_fence_after_sync();
+          for (int c = 0; c < 128; c += 16)
+            if (c0 + c < t.qn) {
+              uint32_t v[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(sum[c + k]);
+              tmem_store_16cols(tlane + acc.idx * kCols + c, v);
+            }
+          tmem_store_wait();
         }
-        for (int c = 0; c < 128 && c0 + c < t.qn; c += 32) {
-          uint32_t v[32];
-          if (blocks > 0) {
-            tmem_load_32cols(tlane + acc.idx * kCols + c, v);
-            tmem_load_wait();
-            tmem_regs_ready(v);
-          } else {
+      } else if (blocks > 0) {
+        if (!warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort)) break;
+        tc_fence_after_sync();
+      }
+      const float scale =
+          !p.wgrad && !p.dense && p.scales != nullptr && t.z >= 0 ? p.scales[t.z] : 1.0f;
+      const long long row0 = t.q0 + c0;
+      const long long at = (p.wgrad ? t.g * p.c_stride : 0) + row0 * p.c_ld + n;
+      const int count = n < p.N ? t.qn - c0 : 0;  // this lane's columns
+#pragma unroll 1
+      for (int c = 0; c < 128 && c0 + c < t.qn; c += 16) {
+        float f[16];
+        if (blocks > 0) {
+          uint32_t v[16];
+          tmem_load_16cols(tlane + acc.idx * kCols + c, v);
+          tmem_load_wait();
+          tmem_regs_ready(v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0;
+          for (int k = 0; k < 16; ++k) f[k] = scale * __uint_as_float(v[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) f[k] = 0.0f;
+        }
+        if (p.add != nullptr) {  // sixteen loads in flight
+          const long long from = row0 * p.add_ld + n;
+          float a[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int row = t.q0 + c0 + c + k;
+            const long long off = from + (c + k) * p.add_ld;
+            a[k] = c + k < count && row >= add0 && row < add1 &&
+                           index_ok(kSitePartialRead, off, 1, p.add_extent)
+                       ? __ldg(p.add + off)
+                       : 0.0f;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) store(c0 + c + j, __uint_as_float(v[j]));
+          for (int k = 0; k < 16; ++k) f[k] += a[k];
         }
-        if (blocks > 0) {
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[acc.idx], 0));
-          acc.next();
+        if (p.c_f32) {
+          float *dst = static_cast<float *>(p.C);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const long long off = at + (c + k) * p.c_ld;
+            if (c + k < count && index_ok(kSiteCStore, off, 1, p.c_extent)) dst[off] = f[k];
+          }
+        } else {
+          __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.C);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const long long off = at + (c + k) * p.c_ld;
+            if (c + k < count && index_ok(kSiteCStore, off, 1, p.c_extent))
+              dst[off] = __float2bfloat16_rn(f[k]);
+          }
+          if (p.C_lo != nullptr) {
+            __nv_bfloat16 *lo = static_cast<__nv_bfloat16 *>(p.C_lo);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const long long off = (row0 + c + k) * p.c_lo_ld + n;
+              if (c + k < count && index_ok(kSitePartialWrite, off, 1, p.c_lo_extent))
+                lo[off] = __float2bfloat16_rn(
+                    f[k] - static_cast<float>(__float2bfloat16_rn(f[k])));
+            }
+          }
         }
+      }
+      if (blocks > 0) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[acc.idx], 0));
+        acc.next();
       }
     }
   } else if (loader) {
@@ -788,11 +834,25 @@ EncodeTiledFn encode_fn() {
 }
 
 // bf16 map over a stack of row-major matrices, zero outside each: lines of 64
-// columns, `lines` rows a copy.
-bool encode_lines(const SegMatrix &m, const void *ptr, int lines, CUtensorMap *out) {
+// columns, `lines` rows a copy; chunks = 2: the same seen as chunks of 64 columns
+// (a multiple of 64, so that no chunk leaves its row), two of them a copy.
+bool encode_lines(const SegMatrix &m, const void *ptr, int lines, int chunks, CUtensorMap *out) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const bool stack = m.count > 1 && m.stride > 0;
+  if (chunks == 2) {
+    const cuuint64_t pitch = static_cast<cuuint64_t>(m.ld) * 2;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(m.rows),
+                                static_cast<cuuint64_t>(m.cols / 64),
+                                static_cast<cuuint64_t>(stack ? m.count : 1)};
+    const cuuint64_t strides[3] = {pitch, 128,
+                                   stack ? static_cast<cuuint64_t>(m.stride) * 2 : pitch};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(lines), 2, 1}, step[4] = {1, 1, 1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box,
+              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
                               static_cast<cuuint64_t>(stack ? m.count : 1)};
   const cuuint64_t pitch = static_cast<cuuint64_t>(m.ld) * 2;
@@ -935,10 +995,17 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   if (!empty && tma_ok(a.B, p.L.p[0]) && tma_ok(a.B, p.L.p[1]) && tma_ok(a.A, p.Q.p[0]) &&
       tma_ok(a.A, p.Q.p[1])) {
     const int l_lines = lmn ? 64 : 128, q_lines = qmn ? 64 : p.q_box;
-    if (encode_lines(a.B, p.L.p[0], l_lines, &maps[0]) &&
-        encode_lines(a.B, p.L.p[1], l_lines, &maps[1]) &&
-        encode_lines(a.A, p.Q.p[0], q_lines, &maps[2]) &&
-        encode_lines(a.A, p.Q.p[1], q_lines, &maps[3]))
+    // One copy of both chunks, where every tile has both: lanes always do.
+    p.l_whole = lmn && a.N % 64 == 0;
+    p.q_whole = qmn && a.K % kCols == 0;
+    const int lc = p.l_whole ? 2 : 1, qc = p.q_whole ? 2 : 1;
+    bool ok = encode_lines(a.B, p.L.p[0], l_lines, lc, &maps[0]) &&
+              encode_lines(a.A, p.Q.p[0], q_lines, qc, &maps[2]);
+    maps[1] = maps[0];
+    maps[3] = maps[2];
+    if (ok && a.B_lo != nullptr) ok = encode_lines(a.B, a.B_lo, l_lines, lc, &maps[1]);
+    if (ok && a.A_lo != nullptr) ok = encode_lines(a.A, a.A_lo, q_lines, qc, &maps[3]);
+    if (ok)
       return launch_layout<__nv_bfloat16, true>(lmn, qmn, maps, p, sm_count, stream);
     return kErrLaunch;
   }
