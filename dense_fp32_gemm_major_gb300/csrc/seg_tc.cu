@@ -103,7 +103,7 @@ struct Cfg {
   static constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
   static constexpr int kLoadWarp0 = 12, kLoadWarps = 8;
   static constexpr int kThreads = 32 * (TMA ? kLoadWarp0 : kLoadWarp0 + kLoadWarps);
-  static constexpr int kFullCount = TMA ? 2 : kLoadWarps + 1;
+  
 };
 
 template <int STAGES>
@@ -354,11 +354,14 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   const uint32_t warp = warp_index();
   const uint32_t lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  // Arrivals that fill a stage. TMA: the even CTA's copies (both CTAs' bytes),
+  // or for weight gradients one arrival from each CTA's copies or masks.
+  constexpr int kFullCount = TMA ? (QMN ? 2 : 1) : C::kLoadWarps + 1;
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&sh->full[s], C::kFullCount);
+      mbar_init(&sh->full[s], kFullCount);
       mbar_init(&sh->empty[s], 1);
       // TMA: this CTA's bytes of a stage that is masked before use; plain
       // loads: this CTA's load warps, passed on by the odd CTA's relay.
@@ -425,8 +428,10 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     // ------------------------------------------------------------- copies --
     if (lane == 0) {
       Ring<STAGES> r;
-      uint32_t armed_full = 0, armed_part = 0, parity_full = 0, parity_part = 0, part_phase = 0;
+      uint32_t part_phase = 0, parts = 0;  // stages that went to part[], by phase and at all
+      int issued = 0;
       bool ok = true;
+      const uint32_t full0 = mbar_cluster_addr(&sh->full[0], 0);
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const int half = mma_cols<QMN>(t) / 2;
         const int ln = t.n0 + static_cast<int>(rank) * 128;
@@ -434,61 +439,61 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
         const int copies = QMN ? half / 64 : cdiv(half, p.q_box);
         const uint32_t bytes =
             kOpBytes + static_cast<uint32_t>(copies) * (QMN ? 8192u : 128u * p.q_box);
-        const int blocks = cdiv(t.klen, kBK);
-        for (int kb = 0; kb < blocks * p.passes; ++kb) {
-          if (!mbar_wait_bounded(&sh->empty[r.idx], r.phase ^ 1, p.timeout_ns, abort,
-                                 &g_seg_status)) {
-            ok = false;
-            break;
-          }
-          const int second = kb >= blocks, kk = (second ? kb - blocks : kb) * kBK;
-          const CUtensorMap *ml = second ? &map_l1 : &map_l0, *mq = second ? &map_q1 : &map_q0;
-          uint8_t *st = stages + r.idx * C::kStageBytes;
-          const int tail = t.klen - kk;
-          const bool fix = QMN && tail < kBK && tail % 16 != 0;
-          uint32_t bar;
-          if (fix) {  // this CTA's own barrier; the fix warp passes it on
-            bar = smem_addr(&sh->part[r.idx]);
-            mbar_arrive_expect_tx(&sh->part[r.idx], bytes);
-            armed_part |= 1u << r.idx;
-            parity_part = (parity_part & ~(1u << r.idx)) | (part_phase & (1u << r.idx));
-            part_phase ^= 1u << r.idx;
-          } else {
-            bar = mbar_cluster_addr(&sh->full[r.idx], 0);
-            if (rank == 0) {
+        for (int pass = 0; ok && pass < p.passes; ++pass) {
+          const CUtensorMap *ml = pass ? &map_l1 : &map_l0, *mq = pass ? &map_q1 : &map_q0;
+          for (int kk = 0; kk < t.klen; kk += kBK) {
+            if (!mbar_wait_bounded(&sh->empty[r.idx], r.phase ^ 1, p.timeout_ns, abort,
+                                   &g_seg_status)) {
+              ok = false;
+              break;
+            }
+            uint8_t *st = stages + r.idx * C::kStageBytes;
+            uint32_t bar = full0 + r.idx * 8;
+            parts &= ~(1u << r.idx);
+            if (QMN && t.klen - kk < kBK && (t.klen - kk) % 16 != 0) {
+              // This CTA's own barrier; the mask warp passes it on.
+              bar = smem_addr(&sh->part[r.idx]);
+              mbar_arrive_expect_tx(&sh->part[r.idx], bytes);
+              parts |= 1u << r.idx;
+              part_phase ^= 1u << r.idx;
+            } else if (rank == 0) {
               mbar_arrive_expect_tx(&sh->full[r.idx], 2 * bytes);
-              mbar_arrive(&sh->full[r.idx]);
+              if (QMN) mbar_arrive(&sh->full[r.idx]);
             }
-            armed_full |= 1u << r.idx;
-            parity_full = (parity_full & ~(1u << r.idx)) | (r.phase << r.idx);
-          }
-          if (!LMN) {
-            tma_load_3d_pair(st, ml, bar, kk, ln, t.z);
-          } else if (p.l_whole) {
-            tma_load_4d_pair(st, ml, bar, 0, t.k0 + kk, ln / 64, t.z);
-          } else {
-            tma_load_3d_pair(st, ml, bar, ln, t.k0 + kk, t.z);
-            tma_load_3d_pair(st + 8192, ml, bar, ln + 64, t.k0 + kk, t.z);
-          }
-          if (QMN && p.q_whole) {
-            tma_load_4d_pair(st + kOpBytes, mq, bar, 0, t.k0 + kk, qn / 64, 0);
-          } else {
-            for (int c = 0; c < copies; ++c) {
-              if (QMN)
-                tma_load_3d_pair(st + kOpBytes + c * 8192, mq, bar, qn + c * 64, t.k0 + kk, 0);
-              else
-                tma_load_3d_pair(st + kOpBytes + c * p.q_box * 128, mq, bar, kk, qn + c * p.q_box, 0);
+            if (!LMN) {
+              tma_load_3d_pair(st, ml, bar, kk, ln, t.z);
+            } else if (p.l_whole) {
+              tma_load_4d_pair(st, ml, bar, 0, t.k0 + kk, ln / 64, t.z);
+            } else {
+              tma_load_3d_pair(st, ml, bar, ln, t.k0 + kk, t.z);
+              tma_load_3d_pair(st + 8192, ml, bar, ln + 64, t.k0 + kk, t.z);
             }
+            if (QMN && p.q_whole) {
+              tma_load_4d_pair(st + kOpBytes, mq, bar, 0, t.k0 + kk, qn / 64, 0);
+            } else {
+              for (int c = 0; c < copies; ++c) {
+                if (QMN)
+                  tma_load_3d_pair(st + kOpBytes + c * 8192, mq, bar, qn + c * 64, t.k0 + kk, 0);
+                else
+                  tma_load_3d_pair(st + kOpBytes + c * p.q_box * 128, mq, bar, kk,
+                                   qn + c * p.q_box, 0);
+              }
+            }
+            ++issued;
+            r.next();
           }
-          r.next();
         }
       }
-      // On a timeout let the copies that were started land.
+      // On a timeout let the copies that were started land: those of the last
+      // stages issued, one phase back where the ring has wrapped since.
       if (!ok)
-        for (int s = 0; s < STAGES; ++s) {
-          if (rank == 0 && (armed_full >> s & 1u))
-            drain_wait(&sh->full[s], parity_full >> s & 1u, p.timeout_ns);
-          if (armed_part >> s & 1u) drain_wait(&sh->part[s], parity_part >> s & 1u, p.timeout_ns);
+        for (int s = 0; s < STAGES && s < issued; ++s) {
+          r.phase ^= r.idx == 0 ? 1u : 0u;
+          r.idx = r.idx == 0 ? STAGES - 1 : r.idx - 1;
+          if (parts >> r.idx & 1u)
+            drain_wait(&sh->part[r.idx], (part_phase >> r.idx & 1u) ^ 1u, p.timeout_ns);
+          else if (rank == 0)
+            drain_wait(&sh->full[r.idx], r.phase, p.timeout_ns);
         }
     }
     __syncwarp();
@@ -533,55 +538,66 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       Ring<STAGES> r;
       Ring<2> acc;
       bool ok = true;
+      // Descriptors of the first stage; others are a number of 16-byte units on.
+      const uint32_t base = smem_addr(stages);
+      const uint64_t l0 = line_desc<LMN>(base, 0);
+      const uint64_t q0 = line_desc<QMN>(base + C::kTerms * kOpBytes, 0);
+      constexpr uint32_t kUnit = kOpBytes >> 4, kl = LMN ? 128 : 2, kq = QMN ? 128 : 2;
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
-        const int blocks = cdiv(t.klen, kBK);
         const uint32_t idesc = idesc_bf16(kLanes, static_cast<uint32_t>(mma_cols<QMN>(t)), LMN, QMN);
-        for (int kb = 0; kb < blocks * p.passes; ++kb) {
-          const bool first = C::kSplit || kb == 0;
-          if (first) {
-            // Both CTAs' epilogues have drained the accumulator.
-            if (!mbar_wait_bounded<true>(&sh->acc_empty[acc.idx], acc.phase ^ 1, p.timeout_ns,
-                                         abort, &g_seg_status)) {
+        uint32_t more = 0;  // 0: the next MMA starts its accumulator
+        for (int pass = 0; ok && pass < p.passes; ++pass)
+          for (int kk0 = 0; kk0 < t.klen; kk0 += kBK) {
+            if (more == 0) {
+              // Both CTAs' epilogues have drained the accumulator.
+              if (!mbar_wait_bounded<true>(&sh->acc_empty[acc.idx], acc.phase ^ 1, p.timeout_ns,
+                                           abort, &g_seg_status)) {
+                ok = false;
+                break;
+              }
+            }
+            // Copies alone complete a stage of the rows form; other stages
+            // have arrivals of the odd CTA's warps (acquire at cluster scope).
+            if (!mbar_wait_bounded<!TMA || QMN>(&sh->full[r.idx], r.phase, p.timeout_ns, abort,
+                                                &g_seg_status)) {
               ok = false;
               break;
             }
-          }
-          // Copies alone complete a stage of the rows form; other stages have
-          // arrivals of the odd CTA's warps (acquire at cluster scope).
-          if (!mbar_wait_bounded<!TMA || QMN>(&sh->full[r.idx], r.phase, p.timeout_ns, abort,
-                                              &g_seg_status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const int kk0 = (kb >= blocks ? kb - blocks : kb) * kBK;
-          const int steps = min(kBK / 16, cdiv(t.klen - kk0, 16));
-          const uint32_t l = smem_addr(stages + r.idx * C::kStageBytes);
-          const uint32_t q = l + C::kTerms * kOpBytes;
-          const uint32_t d = tmem + acc.idx * kCols;
-          if constexpr (C::kSplit) {
-            // Small products first: mm, hl, lh, hm, mh, then hh.
-            constexpr int tl[6] = {1, 0, 2, 0, 1, 0}, tq[6] = {1, 2, 0, 1, 0, 0};
-            uint32_t more = 0;
+            tc_fence_after_sync();
+            const int left = t.klen - kk0;
+            const uint64_t l = l0 + r.idx * (C::kStageBytes >> 4);
+            const uint64_t q = q0 + r.idx * (C::kStageBytes >> 4);
+            const uint32_t d = tmem + acc.idx * kCols;
+            auto products = [&](auto steps) {
+              if constexpr (C::kSplit) {
+                // Small products first: mm, hl, lh, hm, mh, then hh.
+                constexpr uint32_t tl[6] = {1, 0, 2, 0, 1, 0}, tq[6] = {1, 2, 0, 1, 0, 0};
 #pragma unroll
-            for (int c = 0; c < 6; ++c)
-              for (int kk = 0; kk < steps; ++kk) {
-                mma_bf16_pair(d, line_desc<LMN>(l + tl[c] * kOpBytes, kk),
-                              line_desc<QMN>(q + tq[c] * kOpBytes, kk), idesc, more);
-                more = 1;
+                for (int c = 0; c < 6; ++c)
+#pragma unroll
+                  for (int kk = 0; kk < steps(); ++kk) {
+                    mma_bf16_pair(d, l + tl[c] * kUnit + kk * kl, q + tq[c] * kUnit + kk * kq,
+                                  idesc, c + kk > 0 ? 1u : 0u);
+                  }
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < steps(); ++kk)
+                  mma_bf16_pair(d, l + kk * kl, q + kk * kq, idesc, kk > 0 ? 1u : more);
               }
-          } else {
-            for (int kk = 0; kk < steps; ++kk)
-              mma_bf16_pair(d, line_desc<LMN>(l, kk), line_desc<QMN>(q, kk), idesc,
-                            kb != 0 || kk != 0);
+            };
+            if (left > kBK - 16)
+              products([] { return kBK / 16; });
+            else
+              products([left] { return (left + 15) / 16; });
+            mma_commit_multicast<2>(&sh->empty[r.idx], 3);
+            more = 1;
+            if (C::kSplit || (kk0 + kBK >= t.klen && pass + 1 == p.passes)) {
+              mma_commit_multicast<2>(&sh->acc_full[acc.idx], 3);
+              acc.next();
+              more = 0;
+            }
+            r.next();
           }
-          mma_commit_multicast<2>(&sh->empty[r.idx], 3);
-          if (C::kSplit || kb + 1 == blocks * p.passes) {
-            mma_commit_multicast<2>(&sh->acc_full[acc.idx], 3);
-            acc.next();
-          }
-          r.next();
-        }
       }
       // Every MMA issued completes before TMEM is released.
       mma_commit_multicast<2>(&sh->drain, 1);
