@@ -190,9 +190,54 @@ __device__ __forceinline__ int mma_cols(const Tile &t) {
   return cdiv(t.qn, step) * step;
 }
 
+// One try that suspends the thread for up to 20 us: a role that polls in a
+// tight loop (eight epilogue warps do most of the time) takes shared-memory
+// cycles from the copies and the MMAs.
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  if (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return done != 0;
+}
+
+// Wait for the phase; gives up (false) after the launch's limit, recording a
+// timeout, or when another role of the CTA has given up.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const SegTc &p,
+                                     volatile int *abort) {
+  const uint32_t a = smem_addr(bar);
+  if (try_wait_long<CLUSTER>(a, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!try_wait_long<CLUSTER>(a, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > p.timeout_ns) {
+      *abort = 1;
+      atomicCAS(&g_seg_status, 0, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const SegTc &p,
                                           volatile int *abort) {
-  const bool ok = mbar_wait_bounded(bar, parity, p.timeout_ns, abort, &g_seg_status);
+  const bool ok = wait(bar, parity, p, abort);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -442,8 +487,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
         for (int pass = 0; ok && pass < p.passes; ++pass) {
           const CUtensorMap *ml = pass ? &map_l1 : &map_l0, *mq = pass ? &map_q1 : &map_q0;
           for (int kk = 0; kk < t.klen; kk += kBK) {
-            if (!mbar_wait_bounded(&sh->empty[r.idx], r.phase ^ 1, p.timeout_ns, abort,
-                                   &g_seg_status)) {
+            if (!wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
               ok = false;
               break;
             }
@@ -550,16 +594,14 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
           for (int kk0 = 0; kk0 < t.klen; kk0 += kBK) {
             if (more == 0) {
               // Both CTAs' epilogues have drained the accumulator.
-              if (!mbar_wait_bounded<true>(&sh->acc_empty[acc.idx], acc.phase ^ 1, p.timeout_ns,
-                                           abort, &g_seg_status)) {
+              if (!wait<true>(&sh->acc_empty[acc.idx], acc.phase ^ 1, p, abort)) {
                 ok = false;
                 break;
               }
             }
             // Copies alone complete a stage of the rows form; other stages
             // have arrivals of the odd CTA's warps (acquire at cluster scope).
-            if (!mbar_wait_bounded<!TMA || QMN>(&sh->full[r.idx], r.phase, p.timeout_ns, abort,
-                                                &g_seg_status)) {
+            if (!wait<!TMA || QMN>(&sh->full[r.idx], r.phase, p, abort)) {
               ok = false;
               break;
             }
@@ -609,7 +651,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const int n = cdiv(t.klen, kBK) * p.passes;
         for (int kb = 0; kb < n; ++kb) {
-          if (!mbar_wait_bounded(&sh->part[r.idx], r.phase, p.timeout_ns, abort, &g_seg_status)) {
+          if (!wait(&sh->part[r.idx], r.phase, p, abort)) {
             ok = false;
             break;
           }
