@@ -20,8 +20,8 @@
 //
 // bf16 operands come by TMA, 64 k of 128 + 128 lines a stage, and go to
 // kind::f16 MMAs as they are. float32 operands, and bf16 ones that TMA cannot
-// read as given, are loaded by eight warps; a float32 value is split into
-// three bf16 terms on the way,
+// read as given, are loaded by eight warps; a float32 value, 32 k a stage, is
+// split into three bf16 terms on the way,
 //
 //   x = h + m + l,   h = bf16(x), m = bf16(x - h), l = bf16(x - h - m),
 //
@@ -33,7 +33,7 @@
 // The tensor core truncates as it adds to an accumulator: sums of K products
 // drift by about 2^-24 per MMA (measured: 4.4e-6 of the result's norm after
 // 256 bf16 MMAs of one accumulator, against 1.1e-6 of an FP32 FMA chain). For
-// float32 each accumulator therefore holds 64 k only, its small products
+// float32 each accumulator therefore holds 32 k only, its small products
 // first, and the epilogue warps add it to sums in registers, rounded to
 // nearest, while the next one fills.
 //
@@ -60,9 +60,7 @@ namespace {
 
 constexpr int kLanes = 256;     // result columns per tile (MMA M, of the pair)
 constexpr int kCols = 256;      // most rows per tile (MMA N)
-constexpr int kBK = 64;         // k per stage: one 128-byte line of bf16
-constexpr int kLines = 128;     // lines of one operand per CTA and stage
-constexpr int kOpBytes = kLines * 128;
+constexpr int kHalf = 128;      // lanes, and columns at most, of one CTA of the pair
 constexpr int kColStep = 32;    // granularity of the MMA's N
 constexpr int kRasterM = 8;     // row tiles per raster group
 constexpr uint32_t kTmemCols = 512;
@@ -96,19 +94,31 @@ template <class T, bool TMA>
 struct Cfg {
   static constexpr bool kSplit = std::is_same<T, float>::value;  // three-term operands
   static constexpr int kTerms = kSplit ? 3 : 1;
+  // k per stage: 128-byte lines of bf16, or 64-byte ones of each float32 term
+  // (two stages of three terms leave room for the values in flight).
+  static constexpr int kBK = kSplit ? 32 : 64;
+  static constexpr int kOpBytes = kHalf * kBK * 2;  // one term of one operand
   static constexpr int kStageBytes = 2 * kTerms * kOpBytes;
   static constexpr int kStages = kSplit ? 2 : 6;
+  // Float32 values on their way: lines of 32 (128 bytes, 128-byte swizzle),
+  // 128 of either operand a stage.
+  static constexpr int kRawOpBytes = kHalf * 128;
+  static constexpr int kRawStages = kSplit ? 3 : 1;
+  static constexpr int kRawBytes = kSplit ? kRawStages * 2 * kRawOpBytes : 0;
+  static constexpr bool kLoaders = kSplit || !TMA;  // warps that fill the stages
   static constexpr int kMmaWarp = 1;
   static constexpr int kFixWarp = 2;
   static constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
   static constexpr int kLoadWarp0 = 12, kLoadWarps = 8;
-  static constexpr int kThreads = 32 * (TMA ? kLoadWarp0 : kLoadWarp0 + kLoadWarps);
+  static constexpr int kThreads = 32 * (kLoaders ? kLoadWarp0 + kLoadWarps : kLoadWarp0);
+  static constexpr int kCopyWarps = 3;  // float32 without TMA: warps 0, 2 and 3
   
 };
 
-template <int STAGES>
+template <int STAGES, int RAW>
 struct Shared {
   uint64_t full[STAGES], empty[STAGES], part[STAGES];
+  uint64_t raw_full[RAW], raw_empty[RAW];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort;
@@ -282,13 +292,13 @@ __device__ __forceinline__ uint32_t idesc_bf16(uint32_t m, uint32_t n, bool a_mn
          ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// Descriptor of the 16 k of step kk. K-major: lines are rows, 8-line atoms 1024
-// bytes apart, a step 32 bytes along the line. MN-major: lines are k, 64 lines
-// to a chunk of 64 elements (8192 bytes), a step 16 lines.
-template <bool MN>
-__device__ __forceinline__ uint64_t line_desc(uint32_t base, int kk) {
-  if (MN) return smem_desc(base + kk * 2048, 8192, 1024, 2);
-  return smem_desc(base + kk * 32, 16, 1024, 2);
+// Descriptor of an operand's first 16 k. K-major: lines are rows of BK k, 8-line
+// atoms one after another, 16 k are 32 bytes along the line. MN-major: lines are
+// k, BK lines to a chunk of 64 elements, 16 k are 16 lines.
+template <bool MN, int BK>
+__device__ __forceinline__ uint64_t line_desc(uint32_t base) {
+  if (MN) return smem_desc(base, BK * 128, 1024, 2);
+  return smem_desc(base, 16, BK * 16, BK == 64 ? 2 : 4);
 }
 
 // Arrive on the barrier at the shared::cluster address.
@@ -299,80 +309,59 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
 
 // ------------------------------------------------------------- plain loads --
 
-struct Eight {
-  float v[8];
-};
-
-// Elements [x, x + 8) of the line at `row` (element offset), those at or past
-// `limit` zero.
-template <class T>
-__device__ __forceinline__ Eight load_eight(const SegOperand &o, const T *p, int site,
-                                            long long row, int x, int limit) {
-  Eight e;
-  const long long off = row + x;
-  if (o.vec && x + 8 <= limit && index_ok(site, off, 8, o.extent)) {
-    if constexpr (std::is_same<T, float>::value) {
-      const float4 a = __ldg(reinterpret_cast<const float4 *>(p + off));
-      const float4 b = __ldg(reinterpret_cast<const float4 *>(p + off) + 1);
-      e.v[0] = a.x, e.v[1] = a.y, e.v[2] = a.z, e.v[3] = a.w;
-      e.v[4] = b.x, e.v[5] = b.y, e.v[6] = b.z, e.v[7] = b.w;
-    } else {
-      const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p + off));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e.v[2 * i] = __uint_as_float(w[i] << 16);
-        e.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      e.v[i] = x + i < limit && index_ok(site, off + i, 1, o.extent)
-                   ? static_cast<float>(p[off + i])
-                   : 0.0f;
-  }
-  return e;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ float low_half(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_half(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Store eight elements as bf16, or as the three terms (kOpBytes apart).
-template <int TERMS>
-__device__ __forceinline__ void store_eight(uint8_t *dst, Eight e) {
+// Bf16 elements [x, x + 8) of the line at `row` (element offset), those at or
+// past `limit` zero.
+__device__ __forceinline__ uint4 load_eight(const SegOperand &o, const __nv_bfloat16 *p, int site,
+                                            long long row, int x, int limit) {
+  const long long off = row + x;
+  if (o.vec && x + 8 <= limit && index_ok(site, off, 8, o.extent))
+    return __ldg(reinterpret_cast<const uint4 *>(p + off));
+  const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+  uint32_t e[8];
 #pragma unroll
-  for (int t = 0; t < TERMS; ++t) {
+  for (int i = 0; i < 8; ++i)
+    e[i] = x + i < limit && index_ok(site, off + i, 1, o.extent) ? __ldg(h + off + i) : 0;
+  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+}
+
+// Copy a float from global to shared memory, asynchronously; `bytes` 0: zero.
+__device__ __forceinline__ void copy_float(uint32_t dst, const float *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// Eight float32 values as three bf16 terms (`term` bytes apart).
+__device__ __forceinline__ void store_terms(uint8_t *dst, int term, float (&v)[8]) {
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = pack_bf16(e.v[2 * i], e.v[2 * i + 1]);
-      if (t + 1 < TERMS) {  // what the term leaves, exactly
-        e.v[2 * i] -= low_half(w[i]);
-        e.v[2 * i + 1] -= high_half(w[i]);
+      w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      if (t < 2) {  // what the term leaves, exactly
+        v[2 * i] -= __uint_as_float(w[i] << 16);
+        v[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
       }
     }
-    *reinterpret_cast<uint4 *>(dst + t * kOpBytes) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(dst + t * term) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-template <class T, bool TMA>
-__device__ __forceinline__ void set_registers(bool epilogue, bool loader) {
-  // Float32: the epilogue warps hold 128 sums each. 128 x 40 + 256 x 152 +
-  // 256 x 64 registers, within the launch's 640 x 96 (checked by the host).
-  if constexpr (Cfg<T, TMA>::kSplit) {
-    if (epilogue)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    else if (loader)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-  }
+// Registers of a role's warps, float32: the epilogue warps hold 128 sums each.
+// 128 x 40 + 256 x 152 + 256 x 64 registers, within the launch's 640 x 96
+// (checked by the host). Stated where each role begins: the compiler then
+// allots by role.
+template <bool SPLIT, int R>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (SPLIT && R > 96)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  else if constexpr (SPLIT)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 // ------------------------------------------------------------------ kernel --
@@ -385,11 +374,13 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
                   const __grid_constant__ CUtensorMap map_q0,
                   const __grid_constant__ CUtensorMap map_q1, const SegTc p) {
   using C = Cfg<T, TMA>;
-  constexpr int STAGES = C::kStages;
+  constexpr int STAGES = C::kStages, kBK = C::kBK, kOpBytes = C::kOpBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *stages = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  Shared<STAGES> *sh = reinterpret_cast<Shared<STAGES> *>(stages + STAGES * C::kStageBytes);
+  uint8_t *raw = stages + STAGES * C::kStageBytes;
+  using Sh = Shared<STAGES, C::kRawStages>;
+  Sh *sh = reinterpret_cast<Sh *>(raw + C::kRawBytes);
   Table tab;
   tab.rows = reinterpret_cast<int2 *>(sh + 1);
   const int groups = p.dense ? 1 : p.groups;
@@ -399,18 +390,23 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   const uint32_t warp = warp_index();
   const uint32_t lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  // Arrivals that fill a stage. TMA: the even CTA's copies (both CTAs' bytes),
-  // or for weight gradients one arrival from each CTA's copies or masks.
-  constexpr int kFullCount = TMA ? (QMN ? 2 : 1) : C::kLoadWarps + 1;
+  // Arrivals that fill a stage. Copies straight to it: the even CTA's (both
+  // CTAs' bytes), or for weight gradients one arrival from each CTA's copies or
+  // masks. Else the even CTA's load warps and the odd one's relay.
+  constexpr int kFullCount = C::kLoaders ? C::kLoadWarps + 1 : (QMN ? 2 : 1);
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&sh->full[s], kFullCount);
       mbar_init(&sh->empty[s], 1);
-      // TMA: this CTA's bytes of a stage that is masked before use; plain
-      // loads: this CTA's load warps, passed on by the odd CTA's relay.
-      mbar_init(&sh->part[s], TMA ? 1 : C::kLoadWarps);
+      // This CTA's bytes of a stage that is masked before use; or its load
+      // warps, passed on by the odd CTA's relay.
+      mbar_init(&sh->part[s], C::kLoaders ? C::kLoadWarps : 1);
+    }
+    for (int s = 0; s < C::kRawStages; ++s) {
+      mbar_init(&sh->raw_full[s], TMA ? 1 : 32 * C::kCopyWarps);
+      mbar_init(&sh->raw_empty[s], C::kLoadWarps);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sh->acc_full[a], 1);
@@ -465,11 +461,10 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   grid_launch_dependents();
 
   const bool epilogue = warp >= C::kEpiWarp0 && warp < C::kEpiWarp0 + C::kEpiWarps;
-  const bool loader = !TMA && warp >= C::kLoadWarp0;
-  set_registers<T, TMA>(epilogue, loader);
+  const bool loader = C::kLoaders && warp >= C::kLoadWarp0;
 
   Tile t;
-  if (TMA && warp == 0) {
+  if (TMA && !C::kSplit && warp == 0) {
     // ------------------------------------------------------------- copies --
     if (lane == 0) {
       Ring<STAGES> r;
@@ -479,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       const uint32_t full0 = mbar_cluster_addr(&sh->full[0], 0);
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const int half = mma_cols<QMN>(t) / 2;
-        const int ln = t.n0 + static_cast<int>(rank) * 128;
+        const int ln = t.n0 + static_cast<int>(rank) * kHalf;
         const int qn = t.q0 + static_cast<int>(rank) * half;
         const int copies = QMN ? half / 64 : cdiv(half, p.q_box);
         const uint32_t bytes =
@@ -541,7 +536,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (TMA && QMN && warp == C::kFixWarp) {
+  } else if (TMA && !C::kSplit && QMN && warp == C::kFixWarp) {
     // -------------------------------------------------------------- masks --
     // The last stage of a segment whose rows end inside a step of 16: zero
     // both operands' lines from its end to the step's, which hold the next
@@ -576,7 +571,120 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
         r.next();
       }
     }
+  } else if (C::kSplit && TMA && warp == 0) {
+    // ------------------------------------------------ float32 by TMA --
+    set_registers<C::kSplit, 40>();
+    if (lane == 0) {
+      Ring<C::kRawStages> r;
+      int issued = 0;
+      bool ok = true;
+      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+        const int half = mma_cols<QMN>(t) / 2;
+        const int ln = t.n0 + static_cast<int>(rank) * kHalf;
+        const int qn = t.q0 + static_cast<int>(rank) * half;
+        const int copies = QMN ? half / 32 : cdiv(half, p.q_box);
+        const uint32_t bytes = C::kRawOpBytes +
+                               static_cast<uint32_t>(copies) * (QMN ? 4096u : 128u * p.q_box);
+        for (int kk = 0; kk < t.klen; kk += kBK) {
+          if (!wait(&sh->raw_empty[r.idx], r.phase ^ 1, p, abort)) {
+            ok = false;
+            break;
+          }
+          uint8_t *l = raw + r.idx * 2 * C::kRawOpBytes, *q = l + C::kRawOpBytes;
+          const uint32_t bar = smem_addr(&sh->raw_full[r.idx]);
+          mbar_arrive_expect_tx(&sh->raw_full[r.idx], bytes);
+          if (!LMN) {
+            tma_load_3d_pair(l, &map_l0, bar, kk, ln, t.z);
+          } else if (p.l_whole) {
+            tma_load_4d_pair(l, &map_l0, bar, 0, t.k0 + kk, ln / 32, t.z);
+          } else {
+            for (int c = 0; c < 4; ++c)
+              tma_load_3d_pair(l + c * 4096, &map_l0, bar, ln + c * 32, t.k0 + kk, t.z);
+          }
+          if (QMN && p.q_whole) {
+            tma_load_4d_pair(q, &map_q0, bar, 0, t.k0 + kk, qn / 32, 0);
+          } else {
+            for (int c = 0; c < copies; ++c) {
+              if (QMN)
+                tma_load_3d_pair(q + c * 4096, &map_q0, bar, qn + c * 32, t.k0 + kk, 0);
+              else
+                tma_load_3d_pair(q + c * p.q_box * 128, &map_q0, bar, kk, qn + c * p.q_box, 0);
+            }
+          }
+          ++issued;
+          r.next();
+        }
+      }
+      if (!ok)  // let the copies that were started land
+        for (int s = 0; s < C::kRawStages && s < issued; ++s) {
+          r.phase ^= r.idx == 0 ? 1u : 0u;
+          r.idx = r.idx == 0 ? C::kRawStages - 1 : r.idx - 1;
+          drain_wait(&sh->raw_full[r.idx], r.phase, p.timeout_ns);
+        }
+    }
+    __syncwarp();
+  } else if (C::kSplit && !TMA && warp < C::kEpiWarp0 && warp != C::kMmaWarp) {
+    // ------------------------------- float32 of any pitch and alignment --
+    set_registers<C::kSplit, 40>();
+    // A line of 32 values a warp and copy, eight lines at a time; the warps
+    // take the groups of eight in turn.
+    const int cw = warp == 0 ? 0 : static_cast<int>(warp) - 1;
+    const int ln31 = static_cast<int>(lane);
+    Ring<C::kRawStages> r;
+    bool ok = true;
+    for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+      const int half = mma_cols<QMN>(t) / 2;
+      const int ln = t.n0 + static_cast<int>(rank) * kHalf;
+      const int qn = static_cast<int>(rank) * half;
+      for (int kk = 0; kk < t.klen; kk += kBK) {
+        if (!warp_wait(&sh->raw_empty[r.idx], r.phase ^ 1, p, abort)) {
+          ok = false;
+          break;
+        }
+        const uint32_t base = smem_addr(raw) + r.idx * 2 * C::kRawOpBytes;
+        for (int g = cw; g < 32; g += C::kCopyWarps) {  // sixteen groups of L, then of Q
+          const bool is_l = g < 16, mn = is_l ? LMN : QMN;
+          const SegOperand &o = is_l ? p.L : p.Q;
+          const int line0 = (g & 15) * 8;  // K-major: the row; MN-major: chunk * 32 + k
+          long long off;
+          int first, last, x, end;  // lines [first, last) and values x < end exist
+          if (mn) {
+            const int k = kk + (line0 & 31), lane0 = (is_l ? ln : t.q0 + qn) + (line0 >> 5) * 32;
+            off = static_cast<long long>(t.k0 + k) * o.ld + lane0;
+            first = k;
+            last = is_l || (line0 >> 5) * 32 < half ? t.klen : 0;
+            x = lane0;
+            end = is_l ? p.N : p.K;
+          } else {
+            const int m = (is_l ? ln : qn) + line0;
+            off = static_cast<long long>(is_l ? m : t.q0 + m) * o.ld + kk;
+            first = m;
+            last = is_l ? p.N : (line0 < half ? t.qn : 0);
+            x = kk;
+            end = p.K;
+          }
+          if (!is_l && first >= last) continue;  // no columns here: never read
+          if (is_l) off += t.z * o.zs;
+          const float *src = static_cast<const float *>(o.p[0]);
+          const uint32_t dst = base + (g * 8) * 128 + (ln31 & 3) * 4;
+          const bool in = x + ln31 < end;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const long long at = off + e * o.ld + ln31;
+            const bool take = in && first + e < last &&
+                              index_ok(is_l ? kSiteLoadB : kSiteLoadA, at, 1, o.extent);
+            copy_float(dst + e * 128 + ((ln31 >> 2) ^ e) * 16, take ? src + at : src, take ? 4 : 0);
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_addr(&sh->raw_full[r.idx]))
+                     : "memory");
+        r.next();
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == C::kMmaWarp) {
+    set_registers<C::kSplit, 40>();
     if (rank == 0 && lane == 0) {
       // --------------------------------------------------- MMA (even CTA) --
       Ring<STAGES> r;
@@ -584,9 +692,9 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       bool ok = true;
       // Descriptors of the first stage; others are a number of 16-byte units on.
       const uint32_t base = smem_addr(stages);
-      const uint64_t l0 = line_desc<LMN>(base, 0);
-      const uint64_t q0 = line_desc<QMN>(base + C::kTerms * kOpBytes, 0);
-      constexpr uint32_t kUnit = kOpBytes >> 4, kl = LMN ? 128 : 2, kq = QMN ? 128 : 2;
+      const uint64_t l0 = line_desc<LMN, C::kBK>(base);
+      const uint64_t q0 = line_desc<QMN, C::kBK>(base + C::kTerms * C::kOpBytes);
+      constexpr uint32_t kTerm = C::kOpBytes >> 4, kl = LMN ? 128 : 2, kq = QMN ? 128 : 2;
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const uint32_t idesc = idesc_bf16(kLanes, static_cast<uint32_t>(mma_cols<QMN>(t)), LMN, QMN);
         uint32_t more = 0;  // 0: the next MMA starts its accumulator
@@ -601,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
             }
             // Copies alone complete a stage of the rows form; other stages
             // have arrivals of the odd CTA's warps (acquire at cluster scope).
-            if (!wait<!TMA || QMN>(&sh->full[r.idx], r.phase, p, abort)) {
+            if (!wait<C::kLoaders || QMN>(&sh->full[r.idx], r.phase, p, abort)) {
               ok = false;
               break;
             }
@@ -618,7 +726,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
                 for (int c = 0; c < 6; ++c)
 #pragma unroll
                   for (int kk = 0; kk < steps(); ++kk) {
-                    mma_bf16_pair(d, l + tl[c] * kUnit + kk * kl, q + tq[c] * kUnit + kk * kq,
+                    mma_bf16_pair(d, l + tl[c] * kTerm + kk * kl, q + tq[c] * kTerm + kk * kq,
                                   idesc, c + kk > 0 ? 1u : 0u);
                   }
               } else {
@@ -644,7 +752,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       // Every MMA issued completes before TMEM is released.
       mma_commit_multicast<2>(&sh->drain, 1);
       drain_wait(&sh->drain, 0, p.timeout_ns);
-    } else if (!TMA && rank == 1 && lane == 0) {
+    } else if (C::kLoaders && rank == 1 && lane == 0) {
       // ----------------------------------------------------- relay (odd) --
       Ring<STAGES> r;
       bool ok = true;
@@ -663,6 +771,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     __syncwarp();
   } else if (epilogue) {
     // ----------------------------------------------------------- epilogue --
+    set_registers<C::kSplit, 152>();
     const uint32_t quad = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
     const uint32_t tlane = tmem + ((quad * 32) << 16) + part * 128;
     const int c0 = static_cast<int>(part) * 128;  // this warp's first column
@@ -677,7 +786,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       const int blocks = cdiv(t.klen, kBK) * p.passes;
       const int n = t.n0 + static_cast<int>(rank * 128 + quad * 32 + lane);
       if constexpr (C::kSplit) {
-        // Sum the accumulators of 64 k each in registers; the sums go back to
+        // Sum the accumulators of 32 k each in registers; the sums go back to
         // TMEM in the place of the last one, so that float32 and bf16 results
         // leave through the same short loop.
         float sum[128];
@@ -792,71 +901,122 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     }
   } else if (loader) {
     // -------------------------------------------------------- plain loads --
-    // Eight lanes to a line of 64 elements, four lines a warp and load; both
-    // operands are masked here, by row and by column.
+    set_registers<C::kSplit, 64>();
+    // Both operands are masked here, by row and by column.
     const int lw = static_cast<int>(warp) - C::kLoadWarp0;
-    const int sub = static_cast<int>(lane) >> 3, j = static_cast<int>(lane) & 7;
     Ring<STAGES> r;
     bool ok = true;
-    for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
-      const int half = mma_cols<QMN>(t) / 2;
-      const int ln = t.n0 + static_cast<int>(rank) * 128;
-      const int qn = static_cast<int>(rank) * half;  // within the tile
-      const int blocks = cdiv(t.klen, kBK);
-      for (int kb = 0; kb < blocks * p.passes; ++kb) {
-        const int second = kb >= blocks, kk = (second ? kb - blocks : kb) * kBK;
-        uint8_t *st = stages + r.idx * C::kStageBytes;
-        bool free = false;
-#pragma unroll
-        for (int op = 0; op < 2; ++op) {
-          const SegOperand &o = op == 0 ? p.L : p.Q;
-          const bool mn = op == 0 ? LMN : QMN;
-          const T *src = static_cast<const T *>(second ? o.p[1] : o.p[0]);
-          const int site = op == 0 ? kSiteLoadB : kSiteLoadA;
-          const long long z = op == 0 ? t.z * o.zs : 0;
-          Eight e[4];
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const int line = s * 32 + lw * 4 + sub;
-            long long row;
-            int x, limit;
-            if (mn) {  // line: k; elements: lanes or columns
-              const int k = kk + (line & 63);
-              x = (op == 0 ? ln : t.q0 + qn) + (line >> 6) * 64 + j * 8;
-              limit = k < t.klen ? (op == 0 ? p.N : p.K) : 0;
-              if (op == 1 && (line >> 6) * 64 >= half) limit = 0;
-              row = z + static_cast<long long>(t.k0 + k) * o.ld;
-            } else {
-              const int m = op == 0 ? ln + line : qn + line;
-              x = kk + j * 8;
-              limit = (op == 0 ? m < p.N : line < half && m < t.qn) ? p.K : 0;
-              row = z + static_cast<long long>(op == 0 ? m : t.q0 + m) * o.ld;
-            }
-            e[s] = load_eight<T>(o, src, site, row, x, limit);
+    if constexpr (C::kSplit) {
+      // Split the values that have arrived: eight a lane, four lanes to a line
+      // of 32. Lanes 4 to 7 of each eight take the line 5 away (k ^ 5), whose
+      // swizzled pieces lie in the other banks, as read and as written.
+      const int g = static_cast<int>(lane) >> 2, j = static_cast<int>(lane) & 3;
+      const int k8 = (g >> 1) ^ ((g & 1) * 5);  // line within eight
+      Ring<C::kRawStages> a;
+      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+        const int half = mma_cols<QMN>(t) / 2;
+        for (int kk = 0; kk < t.klen; kk += kBK) {
+          if (!warp_wait(&sh->raw_full[a.idx], a.phase, p, abort) ||
+              !warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
+            ok = false;
+            break;
           }
-          if (!free) {
-            if (!warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
+          const uint8_t *from = raw + a.idx * 2 * C::kRawOpBytes;
+          uint8_t *to = stages + r.idx * C::kStageBytes;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool mn = u < 2 ? LMN : QMN;
+            const int line = ((u & 1) * 8 + lw) * 8 + k8;  // MN-major: chunk * 32 + k
+            // K-major Q: rows; MN-major: chunks of 32 columns.
+            if (u >= 2 && (QMN ? line : line & ~7) >= half) continue;
+            const uint8_t *src = from + (u < 2 ? 0 : C::kRawOpBytes) + line * 128;
+            float v[8];
+            *reinterpret_cast<float4 *>(v) =
+                *reinterpret_cast<const float4 *>(src + ((2 * j) ^ k8) * 16);
+            *reinterpret_cast<float4 *>(v + 4) =
+                *reinterpret_cast<const float4 *>(src + ((2 * j + 1) ^ k8) * 16);
+            if (QMN && kk + (line & 31) >= t.klen) {  // the next segment's row
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            }
+            uint8_t *dst = to + (u < 2 ? 0 : C::kTerms * kOpBytes);
+            if (mn)  // line k of a chunk of 64, in its first or second half
+              dst += (line >> 6) * (kBK * 128) + (line & 31) * 128 +
+                     ((((line >> 5 & 1) * 4 + j) ^ k8) * 16);
+            else
+              dst += line * 64 + ((j ^ (k8 >> 1 & 3)) * 16);
+            store_terms(dst, kOpBytes, v);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh->raw_empty[a.idx]);
+            mbar_arrive(rank == 0 ? &sh->full[r.idx] : &sh->part[r.idx]);
+          }
+          a.next();
+          r.next();
+        }
+      }
+    } else if constexpr (!TMA) {
+      // Eight lanes to a line of 64 elements, four lines a warp and load.
+      const int sub = static_cast<int>(lane) >> 3, j = static_cast<int>(lane) & 7;
+      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
+        const int half = mma_cols<QMN>(t) / 2;
+        const int ln = t.n0 + static_cast<int>(rank) * kHalf;
+        const int qn = static_cast<int>(rank) * half;  // within the tile
+        const int blocks = cdiv(t.klen, kBK);
+        for (int kb = 0; kb < blocks * p.passes; ++kb) {
+          const int second = kb >= blocks, kk = (second ? kb - blocks : kb) * kBK;
+          uint8_t *st = stages + r.idx * C::kStageBytes;
+#pragma unroll
+          for (int op = 0; op < 2; ++op) {
+            const SegOperand &o = op == 0 ? p.L : p.Q;
+            const bool mn = op == 0 ? LMN : QMN;
+            const T *src = static_cast<const T *>(second ? o.p[1] : o.p[0]);
+            const int site = op == 0 ? kSiteLoadB : kSiteLoadA;
+            const long long z = op == 0 ? t.z * o.zs : 0;
+            uint4 e[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const int line = s * 32 + lw * 4 + sub;
+              long long row;
+              int x, limit;
+              if (mn) {  // line: k; elements: lanes or columns
+                const int k = kk + (line & 63);
+                x = (op == 0 ? ln : t.q0 + qn) + (line >> 6) * 64 + j * 8;
+                limit = k < t.klen ? (op == 0 ? p.N : p.K) : 0;
+                if (op == 1 && (line >> 6) * 64 >= half) limit = 0;
+                row = z + static_cast<long long>(t.k0 + k) * o.ld;
+              } else {
+                const int m = op == 0 ? ln + line : qn + line;
+                x = kk + j * 8;
+                limit = (op == 0 ? m < p.N : line < half && m < t.qn) ? p.K : 0;
+                row = z + static_cast<long long>(op == 0 ? m : t.q0 + m) * o.ld;
+              }
+              e[s] = load_eight(o, src, site, row, x, limit);
+            }
+            if (op == 0 && !warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
               ok = false;
               break;
             }
-            free = true;
-          }
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const int line = s * 32 + lw * 4 + sub;
-            if (op == 1 && !mn && line >= half) continue;  // no MMA column
-            store_eight<C::kTerms>(st + op * C::kTerms * kOpBytes + line * 128 +
-                                       ((j ^ (line & 7)) * 16),
-                                   e[s]);
+            for (int s = 0; s < 4; ++s) {
+              const int line = s * 32 + lw * 4 + sub;
+              if (op == 1 && !mn && line >= half) continue;  // no MMA column
+              *reinterpret_cast<uint4 *>(st + op * kOpBytes + line * 128 + (j ^ (line & 7)) * 16) =
+                  e[s];
+            }
           }
+          if (!ok) break;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(rank == 0 ? &sh->full[r.idx] : &sh->part[r.idx]);
+          r.next();
         }
-        if (!ok) break;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(rank == 0 ? &sh->full[r.idx] : &sh->part[r.idx]);
-        r.next();
       }
     }
+  } else {
+    set_registers<C::kSplit, 40>();
   }
 
   // Neither CTA frees its TMEM or leaves while the pair's MMAs, copies or
@@ -891,40 +1051,44 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 map over a stack of row-major matrices, zero outside each: lines of 64
-// columns, `lines` rows a copy; chunks = 2: the same seen as chunks of 64 columns
-// (a multiple of 64, so that no chunk leaves its row), two of them a copy.
-bool encode_lines(const SegMatrix &m, const void *ptr, int lines, int chunks, CUtensorMap *out) {
+// Map over a stack of row-major matrices, zero outside each: lines of 128 bytes
+// (64 bf16 or 32 float32 columns), `lines` rows a copy; chunks > 1: the same
+// seen as chunks of one line's columns (a multiple of them, so that no chunk
+// leaves its row), that many a copy.
+bool encode_lines(const SegMatrix &m, const void *ptr, bool bf16, int lines, int chunks,
+                  CUtensorMap *out) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
+  const cuuint64_t elem = bf16 ? 2 : 4;
+  const cuuint32_t line = bf16 ? 64 : 32;
   const bool stack = m.count > 1 && m.stride > 0;
-  if (chunks == 2) {
-    const cuuint64_t pitch = static_cast<cuuint64_t>(m.ld) * 2;
-    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(m.rows),
-                                static_cast<cuuint64_t>(m.cols / 64),
-                                static_cast<cuuint64_t>(stack ? m.count : 1)};
-    const cuuint64_t strides[3] = {pitch, 128,
-                                   stack ? static_cast<cuuint64_t>(m.stride) * 2 : pitch};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(lines), 2, 1}, step[4] = {1, 1, 1, 1};
-    return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box,
-              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t pitch = static_cast<cuuint64_t>(m.ld) * elem;
+  const cuuint64_t next = stack ? static_cast<cuuint64_t>(m.stride) * elem : pitch;
+  const cuuint64_t count = static_cast<cuuint64_t>(stack ? m.count : 1);
+  const cuuint64_t rows = static_cast<cuuint64_t>(m.rows), cols = static_cast<cuuint64_t>(m.cols);
+  const cuuint32_t height = static_cast<cuuint32_t>(lines);
+  cuuint64_t dims[4] = {cols, rows, count, 1}, strides[3] = {pitch, next, 0};
+  cuuint32_t box[4] = {line, height, 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  if (chunks > 1) {
+    dims[0] = line;
+    dims[2] = cols / line;
+    dims[3] = count;
+    strides[1] = 128;
+    strides[2] = next;
+    box[2] = static_cast<cuuint32_t>(chunks);
   }
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
-                              static_cast<cuuint64_t>(stack ? m.count : 1)};
-  const cuuint64_t pitch = static_cast<cuuint64_t>(m.ld) * 2;
-  const cuuint64_t strides[2] = {pitch, stack ? static_cast<cuuint64_t>(m.stride) * 2 : pitch};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(lines), 1}, step[3] = {1, 1, 1};
-  return fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
-            step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+            chunks > 1 ? 4 : 3, const_cast<void *>(ptr), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // TMA reads 16-byte aligned rows; a stride of zero (one matrix for all) is not
 // a stride of its maps.
-bool tma_ok(const SegMatrix &m, const void *p) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && m.ld % 8 == 0 && m.stride % 8 == 0 &&
+bool tma_ok(const SegMatrix &m, const void *p, int elem) {
+  const int per16 = 16 / elem;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && m.ld % per16 == 0 && m.stride % per16 == 0 &&
          (m.count <= 1 || m.stride > 0);
 }
 
@@ -950,7 +1114,8 @@ int launch(const CUtensorMap (&maps)[4], const SegTc &p, int sm_count, cudaStrea
   using C = Cfg<T, TMA>;
   auto *kernel = seg_tc_kernel<T, TMA, LMN, QMN>;
   const int groups = p.dense ? 1 : p.groups;
-  const int fixed = C::kStages * C::kStageBytes + static_cast<int>(sizeof(Shared<C::kStages>)) + 1024;
+  const int fixed = C::kStages * C::kStageBytes + C::kRawBytes +
+                    static_cast<int>(sizeof(Shared<C::kStages, C::kRawStages>)) + 1024;
   const int smem = fixed + groups * 12 + 4;
   static std::once_flag once;
   static bool ready = false;
@@ -1044,30 +1209,35 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   const long long average = p.dense ? a.M : a.M / (a.groups > 0 ? a.groups : 1);
   p.q_box = average <= 64 ? 32 : (average <= 128 ? 64 : 128);
   const bool lmn = a.wgrad || !a.transb, qmn = a.wgrad;
-  p.L = operand_of(a.B, a.B_lo, a.bf16 ? 2 : 4);
-  p.Q = operand_of(a.A, a.A_lo, a.bf16 ? 2 : 4);
+  const int elem = a.bf16 ? 2 : 4;
+  p.L = operand_of(a.B, a.B_lo, elem);
+  p.Q = operand_of(a.A, a.A_lo, elem);
   CUtensorMap maps[4];
   std::memset(maps, 0, sizeof(maps));
-  if (!a.bf16) return launch_layout<float, false>(lmn, qmn, maps, p, sm_count, stream);
   const bool empty = a.K == 0 || a.M == 0;  // no operand is read
-  if (!empty && tma_ok(a.B, p.L.p[0]) && tma_ok(a.B, p.L.p[1]) && tma_ok(a.A, p.Q.p[0]) &&
-      tma_ok(a.A, p.Q.p[1])) {
-    const int l_lines = lmn ? 64 : 128, q_lines = qmn ? 64 : p.q_box;
-    // One copy of both chunks, where every tile has both: lanes always do.
-    p.l_whole = lmn && a.N % 64 == 0;
+  const bool tma = !empty && tma_ok(a.B, p.L.p[0], elem) && tma_ok(a.B, p.L.p[1], elem) &&
+                   tma_ok(a.A, p.Q.p[0], elem) && tma_ok(a.A, p.Q.p[1], elem);
+  if (tma) {
+    const int line = 128 / elem, bk = a.bf16 ? 64 : 32;
+    const int l_lines = lmn ? bk : kHalf, q_lines = qmn ? bk : p.q_box;
+    // One copy of all chunks, where every tile has them all: lanes always do.
+    p.l_whole = lmn && a.N % line == 0;
     p.q_whole = qmn && a.K % kCols == 0;
-    const int lc = p.l_whole ? 2 : 1, qc = p.q_whole ? 2 : 1;
-    bool ok = encode_lines(a.B, p.L.p[0], l_lines, lc, &maps[0]) &&
-              encode_lines(a.A, p.Q.p[0], q_lines, qc, &maps[2]);
+    const int lc = p.l_whole ? kHalf / line : 1, qc = p.q_whole ? kHalf / line : 1;
+    if (!encode_lines(a.B, p.L.p[0], a.bf16, l_lines, lc, &maps[0]) ||
+        !encode_lines(a.A, p.Q.p[0], a.bf16, q_lines, qc, &maps[2]))
+      return kErrLaunch;
     maps[1] = maps[0];
     maps[3] = maps[2];
-    if (ok && a.B_lo != nullptr) ok = encode_lines(a.B, a.B_lo, l_lines, lc, &maps[1]);
-    if (ok && a.A_lo != nullptr) ok = encode_lines(a.A, a.A_lo, q_lines, qc, &maps[3]);
-    if (ok)
-      return launch_layout<__nv_bfloat16, true>(lmn, qmn, maps, p, sm_count, stream);
-    return kErrLaunch;
+    if ((a.B_lo != nullptr && !encode_lines(a.B, a.B_lo, a.bf16, l_lines, lc, &maps[1])) ||
+        (a.A_lo != nullptr && !encode_lines(a.A, a.A_lo, a.bf16, q_lines, qc, &maps[3])))
+      return kErrLaunch;
   }
-  return launch_layout<__nv_bfloat16, false>(lmn, qmn, maps, p, sm_count, stream);
+  if (a.bf16)
+    return tma ? launch_layout<__nv_bfloat16, true>(lmn, qmn, maps, p, sm_count, stream)
+               : launch_layout<__nv_bfloat16, false>(lmn, qmn, maps, p, sm_count, stream);
+  return tma ? launch_layout<float, true>(lmn, qmn, maps, p, sm_count, stream)
+             : launch_layout<float, false>(lmn, qmn, maps, p, sm_count, stream);
 }
 
 }  // namespace gemm
