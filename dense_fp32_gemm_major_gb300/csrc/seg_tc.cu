@@ -33,7 +33,7 @@
 // The tensor core truncates as it adds to an accumulator: sums of K products
 // drift by about 2^-24 per MMA (measured: 4.4e-6 of the result's norm after
 // 256 bf16 MMAs of one accumulator, against 1.1e-6 of an FP32 FMA chain). For
-// float32 each accumulator therefore holds 32 k only, its small products
+// float32 each accumulator therefore holds 64 k only, a stage's small products
 // first, and the epilogue warps add it to sums in registers, rounded to
 // nearest, while the next one fills.
 //
@@ -97,6 +97,8 @@ struct Cfg {
   // k per stage: 128-byte lines of bf16, or 64-byte ones of each float32 term
   // (two stages of three terms leave room for the values in flight).
   static constexpr int kBK = kSplit ? 32 : 64;
+  // k of one accumulator, float32 (two stages).
+  static constexpr int kChunk = kSplit ? 64 : kBK;
   static constexpr int kOpBytes = kHalf * kBK * 2;  // one term of one operand
   static constexpr int kStageBytes = 2 * kTerms * kOpBytes;
   static constexpr int kStages = kSplit ? 2 : 6;
@@ -392,17 +394,15 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   // Arrivals that fill a stage. Copies straight to it: the even CTA's (both
   // CTAs' bytes), or for weight gradients one arrival from each CTA's copies or
-  // masks. Else the even CTA's load warps and the odd one's relay.
-  constexpr int kFullCount = C::kLoaders ? C::kLoadWarps + 1 : (QMN ? 2 : 1);
+  // masks. Else one from each CTA's load warps.
+  constexpr int kFullCount = C::kLoaders || QMN ? 2 : 1;
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&sh->full[s], kFullCount);
       mbar_init(&sh->empty[s], 1);
-      // This CTA's bytes of a stage that is masked before use; or its load
-      // warps, passed on by the odd CTA's relay.
-      mbar_init(&sh->part[s], C::kLoaders ? C::kLoadWarps : 1);
+      mbar_init(&sh->part[s], 1);  // this CTA's bytes of a stage that is masked before use
     }
     for (int s = 0; s < C::kRawStages; ++s) {
       mbar_init(&sh->raw_full[s], TMA ? 1 : 32 * C::kCopyWarps);
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sh->acc_full[a], 1);
-      mbar_init(&sh->acc_empty[a], 2 * C::kEpiWarps);
+      mbar_init(&sh->acc_empty[a], 2);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
 #pragma unroll
                   for (int kk = 0; kk < steps(); ++kk) {
                     mma_bf16_pair(d, l + tl[c] * kTerm + kk * kl, q + tq[c] * kTerm + kk * kq,
-                                  idesc, c + kk > 0 ? 1u : 0u);
+                                  idesc, c + kk > 0 ? 1u : more);
                   }
               } else {
 #pragma unroll
@@ -741,7 +741,8 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               products([left] { return (left + 15) / 16; });
             mma_commit_multicast<2>(&sh->empty[r.idx], 3);
             more = 1;
-            if (C::kSplit || (kk0 + kBK >= t.klen && pass + 1 == p.passes)) {
+            if ((C::kSplit && (kk0 + kBK) % C::kChunk == 0) ||
+                (kk0 + kBK >= t.klen && pass + 1 == p.passes)) {
               mma_commit_multicast<2>(&sh->acc_full[acc.idx], 3);
               acc.next();
               more = 0;
@@ -752,21 +753,6 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       // Every MMA issued completes before TMEM is released.
       mma_commit_multicast<2>(&sh->drain, 1);
       drain_wait(&sh->drain, 0, p.timeout_ns);
-    } else if (C::kLoaders && rank == 1 && lane == 0) {
-      // ----------------------------------------------------- relay (odd) --
-      Ring<STAGES> r;
-      bool ok = true;
-      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
-        const int n = cdiv(t.klen, kBK) * p.passes;
-        for (int kb = 0; kb < n; ++kb) {
-          if (!wait(&sh->part[r.idx], r.phase, p, abort)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_at(mbar_cluster_addr(&sh->full[r.idx], 0));
-          r.next();
-        }
-      }
     }
     __syncwarp();
   } else if (epilogue) {
@@ -782,26 +768,35 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       add0 = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
       add1 = static_cast<int>(b < 0 ? 0 : (b > p.M ? p.M : b));
     }
+    // The accumulator can be refilled: one arrival for all the CTA's epilogue
+    // warps (a release at cluster scope from each costs more than the barrier
+    // that gathers them). False if one of them gave up on its wait; every warp
+    // comes here once for each accumulator.
+    auto drained = [&](uint32_t a, bool ok) {
+      tc_fence_before_sync();
+      ok = named_barrier_and(1, 32 * C::kEpiWarps, ok);
+      if (ok && threadIdx.x == 32 * C::kEpiWarp0)
+        mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[a], 0));
+      return ok;
+    };
     for (int i = pair; tile_at(p, tab, i, t); i += pairs) {
-      const int blocks = cdiv(t.klen, kBK) * p.passes;
+      const int blocks = cdiv(t.klen, C::kChunk) * p.passes;
       const int n = t.n0 + static_cast<int>(rank * 128 + quad * 32 + lane);
+      bool ok = true;
+      bool joined = false;  // left the last barrier on a failure
       if constexpr (C::kSplit) {
-        // Sum the accumulators of 32 k each in registers; the sums go back to
+        // Sum the accumulators of 64 k each in registers; the sums go back to
         // TMEM in the place of the last one, so that float32 and bf16 results
         // leave through the same short loop.
         float sum[128];
 #pragma unroll
         for (int c = 0; c < 128; ++c) sum[c] = 0.0f;
-        bool ok = true;
         for (int kb = 0; kb < blocks; ++kb) {
-          if (!warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort)) {
-            ok = false;
-            break;
-          }
+          ok = warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort);
           tc_fence_after_sync();
 #pragma unroll
           for (int c = 0; c < 128; c += 16)
-            if (c0 + c < t.qn) {
+            if (ok && c0 + c < t.qn) {
               uint32_t v[16];
               tmem_load_16cols(tlane + acc.idx * kCols + c, v);
               tmem_load_wait();
@@ -810,13 +805,14 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               for (int k = 0; k < 16; ++k) sum[c + k] += __uint_as_float(v[k]);
             }
           if (kb + 1 == blocks) break;
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[acc.idx], 0));
+          ok = drained(acc.idx, ok);
+          if (!ok) {
+            joined = true;
+            break;
+          }
           acc.next();
         }
-        if (!ok) break;
-        if (blocks > 1) {
+        if (blocks > 1 && ok) {
 #pragma unroll
           for (int c = 0; c < 128; c += 16)
             if (c0 + c < t.qn) {
@@ -828,7 +824,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
           tmem_store_wait();
         }
       } else if (blocks > 0) {
-        if (!warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort)) break;
+        ok = warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort);
         tc_fence_after_sync();
       }
       const float scale =
@@ -837,7 +833,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       const long long at = (p.wgrad ? t.g * p.c_stride : 0) + row0 * p.c_ld + n;
       const int count = n < p.N ? t.qn - c0 : 0;  // this lane's columns
 #pragma unroll 1
-      for (int c = 0; c < 128 && c0 + c < t.qn; c += 16) {
+      for (int c = 0; ok && c < 128 && c0 + c < t.qn; c += 16) {
         float f[16];
         if (blocks > 0) {
           uint32_t v[16];
@@ -893,9 +889,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
         }
       }
       if (blocks > 0) {
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[acc.idx], 0));
+        if (joined || !drained(acc.idx, ok)) break;
         acc.next();
       }
     }
@@ -906,6 +900,17 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     const int lw = static_cast<int>(warp) - C::kLoadWarp0;
     Ring<STAGES> r;
     bool ok = true;
+    // The CTA's part of a stage is written: one release at cluster scope for
+    // all its load warps (a thread of the odd CTA that waited for their
+    // arrivals and passed them on was 375 ns of every stage's way).
+    const uint32_t full0 = mbar_cluster_addr(&sh->full[0], 0);
+    // False if a warp gave up on a wait; each comes here once a stage.
+    auto filled = [&](uint32_t s, bool ok) {
+      fence_proxy_async_smem();
+      ok = named_barrier_and(2, 32 * C::kLoadWarps, ok);
+      if (ok && threadIdx.x == 32 * C::kLoadWarp0) mbar_arrive_at(full0 + s * 8);
+      return ok;
+    };
     if constexpr (C::kSplit) {
       // Split the values that have arrived: eight a lane, four lanes to a line
       // of 32. Lanes 4 to 7 of each eight take the line 5 away (k ^ 5), whose
@@ -916,11 +921,8 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const int half = mma_cols<QMN>(t) / 2;
         for (int kk = 0; kk < t.klen; kk += kBK) {
-          if (!warp_wait(&sh->raw_full[a.idx], a.phase, p, abort) ||
-              !warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
-            ok = false;
-            break;
-          }
+          ok = warp_wait(&sh->raw_full[a.idx], a.phase, p, abort) &&
+               warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort);
           const uint8_t *from = raw + a.idx * 2 * C::kRawOpBytes;
           uint8_t *to = stages + r.idx * C::kStageBytes;
 #pragma unroll
@@ -928,7 +930,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
             const bool mn = u < 2 ? LMN : QMN;
             const int line = ((u & 1) * 8 + lw) * 8 + k8;  // MN-major: chunk * 32 + k
             // K-major Q: rows; MN-major: chunks of 32 columns.
-            if (u >= 2 && (QMN ? line : line & ~7) >= half) continue;
+            if (!ok || (u >= 2 && (QMN ? line : line & ~7) >= half)) continue;
             const uint8_t *src = from + (u < 2 ? 0 : C::kRawOpBytes) + line * 128;
             float v[8];
             *reinterpret_cast<float4 *>(v) =
@@ -947,12 +949,9 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               dst += line * 64 + ((j ^ (k8 >> 1 & 3)) * 16);
             store_terms(dst, kOpBytes, v);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh->raw_empty[a.idx]);
-            mbar_arrive(rank == 0 ? &sh->full[r.idx] : &sh->part[r.idx]);
-          }
+          ok = filled(r.idx, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&sh->raw_empty[a.idx]);
           a.next();
           r.next();
         }
@@ -995,22 +994,17 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               }
               e[s] = load_eight(o, src, site, row, x, limit);
             }
-            if (op == 0 && !warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
-              ok = false;
-              break;
-            }
+            if (op == 0) ok = warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
+            for (int s = 0; ok && s < 4; ++s) {
               const int line = s * 32 + lw * 4 + sub;
               if (op == 1 && !mn && line >= half) continue;  // no MMA column
               *reinterpret_cast<uint4 *>(st + op * kOpBytes + line * 128 + (j ^ (line & 7)) * 16) =
                   e[s];
             }
           }
+          ok = filled(r.idx, ok);
           if (!ok) break;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(rank == 0 ? &sh->full[r.idx] : &sh->part[r.idx]);
           r.next();
         }
       }
