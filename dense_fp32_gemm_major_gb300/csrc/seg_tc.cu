@@ -86,6 +86,7 @@ struct SegTc {
   long long add_ld, add_extent;
   void *C, *C_lo;    // C_lo: the result's second term
   int c_f32;
+  int c_rows;        // rows of the result can leave as 16-byte pieces
   long long c_ld, c_lo_ld, c_stride, c_extent, c_lo_extent;
   unsigned long long timeout_ns;
 };
@@ -107,6 +108,9 @@ struct Cfg {
   static constexpr int kRawOpBytes = kHalf * 128;
   static constexpr int kRawStages = kSplit ? 3 : 1;
   static constexpr int kRawBytes = kSplit ? kRawStages * 2 * kRawOpBytes : 0;
+  // Results on their way out, per 128 columns of the tile: two pieces of 16
+  // rows of 128 bf16, or one of float32.
+  static constexpr int kOutBytes = 8192;
   static constexpr bool kLoaders = kSplit || !TMA;  // warps that fill the stages
   static constexpr int kMmaWarp = 1;
   static constexpr int kFixWarp = 2;
@@ -137,7 +141,7 @@ struct Tile {
 
 struct Table {
   int *first;     // [groups + 1] tiles of the segments before
-  int2 *rows;     // [groups] rows of the segment
+  int *row;       // [groups + 1] offsets, held to the rows there are
 };
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -154,7 +158,7 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int t,
       hi = mid;
   }
   const int idx = t - tab.first[lo];
-  const int2 rows = tab.rows[lo];
+  const int2 rows = make_int2(tab.row[lo], max(tab.row[lo], tab.row[lo + 1]));
   const int height = p.wgrad ? p.K : rows.y - rows.x;
   const int tm = cdiv(height, kCols);
   // Groups of kRasterM row tiles, lane tiles in the outer loop, so that the
@@ -303,9 +307,29 @@ __device__ __forceinline__ uint64_t line_desc(uint32_t base) {
   return smem_desc(base, 16, BK * 16, BK == 64 ? 2 : 4);
 }
 
-// Arrive on the barrier at the shared::cluster address.
+// Arrive on the barrier at the shared::cluster address (the even CTA's). What
+// it announces never crosses the pair: lines that the odd CTA's threads wrote to
+// its own shared memory, fenced for its own tensor core, or its own TMEM read
+// out. A release at CTA scope is therefore enough; one at cluster scope cost
+// 280 ns of every float32 stage (4096 x 4864 x 4096: 672 against 530 us).
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Store the box at (x, y, z) of the map from shared memory, asynchronously.
+__device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src, int x, int y,
+                                          int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Copy `bytes` (a multiple of 16) from shared to global memory, asynchronously.
+__device__ __forceinline__ void store_bulk(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+               "r"(bytes)
                : "memory");
 }
 
@@ -374,7 +398,8 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     seg_tc_kernel(const __grid_constant__ CUtensorMap map_l0,
                   const __grid_constant__ CUtensorMap map_l1,
                   const __grid_constant__ CUtensorMap map_q0,
-                  const __grid_constant__ CUtensorMap map_q1, const SegTc p) {
+                  const __grid_constant__ CUtensorMap map_q1,
+                  const __grid_constant__ CUtensorMap map_c, const SegTc p) {
   using C = Cfg<T, TMA>;
   constexpr int STAGES = C::kStages, kBK = C::kBK, kOpBytes = C::kOpBytes;
   extern __shared__ uint8_t smem_raw[];
@@ -382,11 +407,12 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *raw = stages + STAGES * C::kStageBytes;
   using Sh = Shared<STAGES, C::kRawStages>;
-  Sh *sh = reinterpret_cast<Sh *>(raw + C::kRawBytes);
+  uint8_t *out = raw + C::kRawBytes;
+  Sh *sh = reinterpret_cast<Sh *>(out + 2 * C::kOutBytes);
   Table tab;
-  tab.rows = reinterpret_cast<int2 *>(sh + 1);
   const int groups = p.dense ? 1 : p.groups;
-  tab.first = reinterpret_cast<int *>(tab.rows + groups);
+  tab.row = reinterpret_cast<int *>(sh + 1);
+  tab.first = tab.row + groups + 1;
   volatile int *abort = &sh->abort;
 
   const uint32_t warp = warp_index();
@@ -426,16 +452,14 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   }
   grid_dependency_wait();
   // The table of segments: their rows, and the tiles before each.
-  for (int g = threadIdx.x; g < groups; g += C::kThreads) {
-    int2 r = make_int2(0, p.M);
-    if (!p.dense) {
-      const long long a = p.offsets[g], b = p.offsets[g + 1];
-      const long long s = a < 0 ? 0 : (a > p.M ? p.M : a);
-      r = make_int2(static_cast<int>(s), static_cast<int>(b < s ? s : (b > p.M ? p.M : b)));
-    }
-    tab.rows[g] = r;
-    tab.first[g] = cdiv(p.wgrad ? p.K : r.y - r.x, kCols) * p.tiles_n;
+  for (int g = threadIdx.x; g <= groups; g += C::kThreads) {
+    const long long a = p.dense ? (g ? p.M : 0) : p.offsets[g];
+    tab.row[g] = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
   }
+  __syncthreads();
+  for (int g = threadIdx.x; g < groups; g += C::kThreads)
+    tab.first[g] =
+        cdiv(p.wgrad ? p.K : max(tab.row[g + 1] - tab.row[g], 0), kCols) * p.tiles_n;
   __syncthreads();
   if (warp == 0) {
     int sum = 0;
@@ -783,7 +807,6 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       const int blocks = cdiv(t.klen, C::kChunk) * p.passes;
       const int n = t.n0 + static_cast<int>(rank * 128 + quad * 32 + lane);
       bool ok = true;
-      bool joined = false;  // left the last barrier on a failure
       if constexpr (C::kSplit) {
         // Sum the accumulators of 64 k each in registers; the sums go back to
         // TMEM in the place of the last one, so that float32 and bf16 results
@@ -806,10 +829,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
             }
           if (kb + 1 == blocks) break;
           ok = drained(acc.idx, ok);
-          if (!ok) {
-            joined = true;
-            break;
-          }
+          if (!ok) break;
           acc.next();
         }
         if (blocks > 1 && ok) {
@@ -827,13 +847,15 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
         ok = warp_wait(&sh->acc_full[acc.idx], acc.phase, p, abort);
         tc_fence_after_sync();
       }
+      // All warps go on together from here, or none does.
+      if (!named_barrier_and(1, 32 * C::kEpiWarps, ok)) break;
       const float scale =
           !p.wgrad && !p.dense && p.scales != nullptr && t.z >= 0 ? p.scales[t.z] : 1.0f;
       const long long row0 = t.q0 + c0;
       const long long at = (p.wgrad ? t.g * p.c_stride : 0) + row0 * p.c_ld + n;
       const int count = n < p.N ? t.qn - c0 : 0;  // this lane's columns
 #pragma unroll 1
-      for (int c = 0; ok && c < 128 && c0 + c < t.qn; c += 16) {
+      for (int c = 0; c < 128 && c0 + c < t.qn; c += 16) {
         float f[16];
         if (blocks > 0) {
           uint32_t v[16];
@@ -861,7 +883,53 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) f[k] += a[k];
         }
-        if (p.c_f32) {
+        if (p.c_rows) {
+          // Sixteen rows of this CTA's 128 lanes meet in shared memory and
+          // leave as whole pieces of their rows.
+          const int elem = p.c_f32 ? 4 : 2, row_bytes = kHalf * elem;
+          const uint32_t to = smem_addr(out) + part * C::kOutBytes +
+                              (p.c_f32 ? 0 : (c >> 4 & 1) * (C::kOutBytes / 2));
+          const uint32_t at_lane = to + (quad * 32 + lane) * elem;
+          if (quad == 0) {  // the copies that last read this piece are done with it
+            if (p.c_f32)
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            else
+              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          }
+          named_barrier_sync(3 + part, 128);
+          if (p.c_f32) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(at_lane + k * row_bytes), "f"(f[k])
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at_lane + k * row_bytes),
+                           "h"(__bfloat16_as_ushort(__float2bfloat16_rn(f[k])))
+                           : "memory");
+          }
+          fence_proxy_async_smem();
+          named_barrier_sync(3 + part, 128);
+          if (quad == 0) {
+            const int n_cta = t.n0 + static_cast<int>(rank) * kHalf;
+            const int width = min(kHalf, p.N - n_cta);
+            if (c0 + c + 16 <= t.qn) {
+              // One box of sixteen rows (as a copy for each row, 256 bytes at
+              // a time, results left at 2 TB/s).
+              if (lane == 0 && width > 0)
+                store_box(&map_c, to, n_cta, t.q0 + c0 + c, p.wgrad ? t.g : 0);
+            } else {  // the segment ends here
+              const int row = c + static_cast<int>(lane);
+              const long long off = at - n + n_cta + row * p.c_ld;
+              if (lane < 16 && c0 + row < t.qn && width > 0 &&
+                  index_ok(kSiteCStore, off, width, p.c_extent))
+                store_bulk(static_cast<uint8_t *>(p.C) + off * elem, to + lane * row_bytes,
+                           static_cast<uint32_t>(width * elem));
+            }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else if (p.c_f32) {
           float *dst = static_cast<float *>(p.C);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -889,10 +957,11 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
         }
       }
       if (blocks > 0) {
-        if (joined || !drained(acc.idx, ok)) break;
+        drained(acc.idx, true);
         acc.next();
       }
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (loader) {
     // -------------------------------------------------------- plain loads --
     set_registers<C::kSplit, 64>();
@@ -1078,6 +1147,22 @@ bool encode_lines(const SegMatrix &m, const void *ptr, bool bf16, int lines, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of the results: boxes of 128 columns by 16 rows, not swizzled.
+bool encode_result(const SegMatrix &m, bool f32, CUtensorMap *out) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t elem = f32 ? 4 : 2, pitch = static_cast<cuuint64_t>(m.ld) * elem;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
+                              static_cast<cuuint64_t>(m.count)};
+  const cuuint64_t strides[2] = {
+      pitch, m.count > 1 ? static_cast<cuuint64_t>(m.stride) * elem : pitch};
+  const cuuint32_t box[3] = {kHalf, 16, 1}, step[3] = {1, 1, 1};
+  return fn(out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void *>(m.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // TMA reads 16-byte aligned rows; a stride of zero (one matrix for all) is not
 // a stride of its maps.
 bool tma_ok(const SegMatrix &m, const void *p, int elem) {
@@ -1104,19 +1189,19 @@ SegOperand operand_of(const SegMatrix &m, const void *second, int elem) {
 }
 
 template <class T, bool TMA, bool LMN, bool QMN>
-int launch(const CUtensorMap (&maps)[4], const SegTc &p, int sm_count, cudaStream_t stream) {
+int launch(const CUtensorMap (&maps)[5], const SegTc &p, int sm_count, cudaStream_t stream) {
   using C = Cfg<T, TMA>;
   auto *kernel = seg_tc_kernel<T, TMA, LMN, QMN>;
   const int groups = p.dense ? 1 : p.groups;
-  const int fixed = C::kStages * C::kStageBytes + C::kRawBytes +
+  const int fixed = C::kStages * C::kStageBytes + C::kRawBytes + 2 * C::kOutBytes +
                     static_cast<int>(sizeof(Shared<C::kStages, C::kRawStages>)) + 1024;
-  const int smem = fixed + groups * 12 + 4;
+  const int smem = fixed + groups * 8 + 8;
   static std::once_flag once;
   static bool ready = false;
   std::call_once(once, [&] {
     cudaFuncAttributes at;
     ready = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 fixed + kMaxSegments * 12 + 4) == cudaSuccess &&
+                                 fixed + kMaxSegments * 8 + 8) == cudaSuccess &&
             cudaFuncGetAttributes(&at, kernel) == cudaSuccess &&
             // the register split draws on the launch's registers
             (!C::kSplit || at.numRegs * C::kThreads >= 128 * 40 + 256 * 152 + 256 * 64);
@@ -1145,13 +1230,13 @@ int launch(const CUtensorMap (&maps)[4], const SegTc &p, int sm_count, cudaStrea
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], p) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p) == cudaSuccess
              ? kOk
              : kErrLaunch;
 }
 
 template <class T, bool TMA>
-int launch_layout(bool lmn, bool qmn, const CUtensorMap (&maps)[4], const SegTc &p, int sm_count,
+int launch_layout(bool lmn, bool qmn, const CUtensorMap (&maps)[5], const SegTc &p, int sm_count,
                   cudaStream_t stream) {
   if (qmn) return launch<T, TMA, true, true>(maps, p, sm_count, stream);
   if (lmn) return launch<T, TMA, true, false>(maps, p, sm_count, stream);
@@ -1190,6 +1275,9 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   p.add_extent = extent_of(a.add);
   p.C = const_cast<void *>(a.C.p);
   p.c_f32 = !a.bf16 || a.c_f32;
+  const int64_t c_elem = p.c_f32 ? 4 : 2;
+  p.c_rows = a.C_lo.p == nullptr && reinterpret_cast<uintptr_t>(a.C.p) % 16 == 0 &&
+             a.C.ld * c_elem % 16 == 0 && a.C.stride * c_elem % 16 == 0 && a.N * c_elem % 16 == 0;
   p.c_ld = a.C.ld;
   p.c_stride = a.C.stride;
   p.c_extent = extent_of(a.C);
@@ -1206,7 +1294,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   const int elem = a.bf16 ? 2 : 4;
   p.L = operand_of(a.B, a.B_lo, elem);
   p.Q = operand_of(a.A, a.A_lo, elem);
-  CUtensorMap maps[4];
+  CUtensorMap maps[5];
   std::memset(maps, 0, sizeof(maps));
   const bool empty = a.K == 0 || a.M == 0;  // no operand is read
   const bool tma = !empty && tma_ok(a.B, p.L.p[0], elem) && tma_ok(a.B, p.L.p[1], elem) &&
@@ -1227,6 +1315,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
         (a.A_lo != nullptr && !encode_lines(a.A, a.A_lo, a.bf16, q_lines, qc, &maps[3])))
       return kErrLaunch;
   }
+  if (p.c_rows && !encode_result(a.C, p.c_f32, &maps[4])) return kErrLaunch;
   if (a.bf16)
     return tma ? launch_layout<__nv_bfloat16, true>(lmn, qmn, maps, p, sm_count, stream)
                : launch_layout<__nv_bfloat16, false>(lmn, qmn, maps, p, sm_count, stream);
