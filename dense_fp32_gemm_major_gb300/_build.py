@@ -28,7 +28,8 @@ OBJ_DIR_CHECKED = os.path.join(OBJ_DIR, "checked")
 LIB_CHECKED = os.path.join(PKG, "libgemm_f32_checked.so")
 CHECKED_FLAGS = ["-DGEMM_F32_INDEX_CHECKS=1"]
 SOURCES = ["api.cu", "simt_gemm.cu", "tc_gemm.cu", "transpose.cu", "pack.cu", "reduce.cu",
-           "probe.cu", "seg_api.cu", "seg_tc.cu"]
+           "probe.cu", "seg_api.cu", "seg_tc.cu",
+           "seg_pack.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

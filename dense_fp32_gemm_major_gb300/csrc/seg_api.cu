@@ -59,104 +59,190 @@ bool common_ok(int type, int64_t groups) {
          groups <= GEMM_F32_MAX_SEGMENTS;
 }
 
-int launch(const SegArgs &a, int sms, cudaStream_t stream) {
-  return gemm::seg_tc_launch(a, sms, stream);
-}
+// The workspace of a call, from the library's pool: copies of operands that the
+// kernels cannot read as they lie, and what its products hand to one another.
+class Workspace {
+ public:
+  Workspace(bool bf16, const int64_t *offsets, int64_t groups, int64_t M)
+      : bf16_(bf16), offsets_(offsets), groups_(groups), rows_(M) {}
+
+  // Have m copied, unless it is readable or empty. by_segment: matrix g is
+  // used only where segment g has rows.
+  void readable(SegMatrix &m, bool by_segment = false) {
+    if (m.rows == 0 || m.cols == 0 || m.count == 0 || gemm::seg_tc_readable(m, bf16_)) return;
+    gemm::SegCopy &c = copies_[copy_count_];
+    c.src = m;
+    if (m.stride == 0) c.src.count = 1;
+    if (by_segment && m.stride != 0) {
+      c.offsets = offsets_;
+      c.groups = groups_;
+      c.M = rows_;
+      c.by_matrix = true;
+    }
+    target_[copy_count_++] = &m;
+    matrix(m, m.rows, m.cols, bf16_ ? 2 : 4, m.stride == 0 ? 1 : m.count);
+  }
+
+  // A new stack of matrices with readable rows.
+  void matrix(SegMatrix &m, int64_t rows, int64_t cols, int elem, int64_t count = 1) {
+    const int64_t per16 = 16 / elem;
+    m.rows = rows;
+    m.cols = cols;
+    m.ld = (cols + per16 - 1) / per16 * per16;
+    if (count > 1) m.stride = rows * m.ld;
+    placed_[placed_count_] = &m;
+    at_[placed_count_++] = bytes_;
+    bytes_ += static_cast<size_t>((count * rows * m.ld * elem + 255) / 256 * 256);
+  }
+
+  // Allocate, place, and copy.
+  int take(int sms, cudaStream_t s) {
+    if (bytes_ == 0) return gemm::kOk;
+    const int st = gemm::pool_alloc(&p_, bytes_, s);
+    if (st != gemm::kOk) return st;
+    for (int i = 0; i < placed_count_; ++i) placed_[i]->p = static_cast<uint8_t *>(p_) + at_[i];
+    for (int i = 0; i < copy_count_; ++i) {
+      copies_[i].dst = *target_[i];
+      const int cst = gemm::seg_pack_launch(copies_[i], bf16_, sms, s);
+      if (cst != gemm::kOk) return cst;
+    }
+    return gemm::kOk;
+  }
+
+  // Rows of the segments, from here to the caller's matrix.
+  int hand_back(const SegMatrix &from, const SegMatrix &to, int sms, cudaStream_t s) {
+    gemm::SegCopy c;
+    c.src = from;
+    c.dst = to;
+    c.offsets = offsets_;
+    c.groups = groups_;
+    c.M = rows_;
+    return gemm::seg_pack_launch(c, bf16_, sms, s);
+  }
+
+  int give_back(int st, cudaStream_t s) {
+    if (p_ == nullptr) return st;
+    const int fst = gemm::pool_free(p_, s);
+    return st != gemm::kOk ? st : fst;
+  }
+
+ private:
+  static constexpr int kMost = 12;
+  bool bf16_;
+  const int64_t *offsets_;
+  int64_t groups_, rows_;
+  void *p_ = nullptr;
+  size_t bytes_ = 0;
+  gemm::SegCopy copies_[kMost];
+  SegMatrix *target_[kMost], *placed_[kMost];
+  size_t at_[kMost];
+  int copy_count_ = 0, placed_count_ = 0;
+};
 
 // Y = X op(W) + U op(B_a), U = s_a (X op(A_a)).
 struct Lora {
   bool bf16 = false, adapted = false;
   int transw = 0, transl = 0;
   int64_t segments = 0, bank = 0, M = 0, N = 0, K = 0, R = 0;
-  SegMatrix X, W, A, B, U, Y;
+  SegMatrix X, W, A, B, Y;
+  SegMatrix user_u;          // the caller's, or none
+  SegMatrix u, u_lo, sum;    // U, its second term (bf16), and U B in fp32
   const int64_t *offsets = nullptr;
   const int32_t *index = nullptr;
   const float *scales = nullptr;
-};
+  bool fused = false;
 
-// U (in the caller's matrix or here), its second term for bf16 -- U is an
-// operand of the second product, and rounded to one bf16 would add an error
-// as large as the result's own rounding -- and U B in fp32, the addend of the
-// projection's tiles. A tile of the projection holds rows of several
-// segments, and an MMA over all of them would let one adapter's NaN or
-// infinity into the others' rows (0 * inf), so U B is a product of its own.
-struct Work {
-  void *p = nullptr;
-  SegMatrix u, u_lo, sum;
+  // U B in the projection's own accumulators, or a product of its own that the
+  // projection's tiles add? An MMA over rows of several segments would let one
+  // adapter's NaN or infinity into the others' rows (0 * inf), so the fused
+  // form's tiles are the segments' own: each segment reads W again, from L2.
+  // With 128 rows a segment and more that costs nothing next to U B's way
+  // through memory (8192 rows, nine segments, 4096 x 4096, rank 64 bf16: 259 ->
+  // 215 us); 32 rows in 32 segments would read W 32 times.
+  void prepare(Workspace &w) {
+    fused = adapted && K > 0 && M >= 128 * segments && transw == transl;
+    w.readable(X);
+    w.readable(W);
+    if (!adapted) return;
+    w.readable(A);
+    w.readable(B);
+    // bf16: U is an operand of the second product, and rounded to one bf16 it
+    // would add an error as large as the result's own rounding: two terms.
+    const int elem = bf16 ? 2 : 4;
+    if (user_u.p != nullptr && gemm::seg_tc_readable(user_u, bf16))
+      u = user_u;
+    else
+      w.matrix(u, M, R, elem);
+    if (bf16) w.matrix(u_lo, M, R, elem);
+    if (!fused) w.matrix(sum, M, N, 4);
+  }
 
-  int take(const Lora &l, cudaStream_t s) {
-    u = l.U;
-    if (!l.adapted) return gemm::kOk;
-    const int elem = l.bf16 ? 2 : 4;
-    auto up = [](int64_t bytes) { return (bytes + 255) / 256 * 256; };
-    const int64_t ld = (l.R + 7) / 8 * 8, sum_ld = (l.N + 3) / 4 * 4;
-    const int64_t ub = l.U.p == nullptr ? up(l.M * ld * elem) : 0;
-    const int64_t lb = l.bf16 ? up(l.M * (l.U.p == nullptr ? ld : l.U.ld) * 2) : 0;
-    const int64_t sb = up(l.M * sum_ld * 4);
-    if (ub + lb + sb == 0) return gemm::kOk;
-    const int st = gemm::pool_alloc(&p, static_cast<size_t>(ub + lb + sb), s);
-    if (st != gemm::kOk) return st;
-    uint8_t *at = static_cast<uint8_t *>(p);
-    if (l.U.p == nullptr) u = SegMatrix{at, ld, 0, l.M, l.R, 1};
-    if (l.bf16) {
-      u_lo = u;
-      u_lo.p = at + ub;
+  int run(Workspace &w, int sms, cudaStream_t s) {
+    SegArgs y;
+    y.bf16 = bf16;
+    y.M = M;
+    y.bank = bank;
+    y.offsets = offsets;
+    y.groups = adapted ? segments : 0;
+    if (adapted) {
+      SegArgs p = y;  // U = s (X A)
+      p.index = index;
+      p.N = R;
+      p.K = K;
+      p.A = X;
+      p.B = A;
+      p.transb = transl;
+      p.scales = scales;
+      p.C = u;
+      p.C_lo = u_lo;
+      int st = gemm::seg_tc_launch(p, sms, s);
+      if (st == gemm::kOk && user_u.p != nullptr && u.p != user_u.p)
+        st = w.hand_back(u, user_u, sms, s);
+      if (st != gemm::kOk || N == 0) return st;
     }
-    sum = SegMatrix{at + ub + lb, sum_ld, 0, l.M, l.N, 1};
-    return gemm::kOk;
-  }
-
-  int give_back(int st, cudaStream_t s) {
-    if (p == nullptr) return st;
-    const int fst = gemm::pool_free(p, s);
-    return st != gemm::kOk ? st : fst;
+    y.dense = true;
+    y.N = N;
+    y.K = K;
+    y.A = X;
+    y.B = W;
+    y.transb = transw;
+    y.C = Y;
+    if (!adapted) return gemm::seg_tc_launch(y, sms, s);
+    if (fused) {
+      y.index = index;
+      y.R = R;
+      y.U = u;
+      y.U_lo = u_lo;
+      y.L = B;
+      return gemm::seg_tc_launch(y, sms, s);
+    }
+    SegArgs e = y;  // U B
+    e.dense = false;
+    e.index = index;
+    e.K = R;
+    e.A = u;
+    e.A_lo = u_lo;
+    e.B = B;
+    e.transb = transl;
+    e.C = sum;
+    e.c_f32 = true;
+    int st = gemm::seg_tc_launch(e, sms, s);
+    if (st != gemm::kOk) return st;
+    y.add = sum;
+    return gemm::seg_tc_launch(y, sms, s);
   }
 };
 
-int lora_run(const Lora &l, const Work &work, int sms, cudaStream_t s) {
-  SegArgs y;
-  y.bf16 = l.bf16;
-  y.groups = l.segments;
-  y.M = l.M;
-  y.bank = l.bank;
-  y.offsets = l.offsets;
-  y.index = l.index;
-  if (l.adapted) {
-    SegArgs u = y;  // U = s (X A)
-    u.N = l.R;
-    u.K = l.K;
-    u.A = l.X;
-    u.B = l.A;
-    u.transb = l.transl;
-    u.scales = l.scales;
-    u.C = work.u;
-    u.C_lo = work.u_lo;
-    int st = launch(u, sms, s);
-    if (st != gemm::kOk) return st;
-    if (l.N == 0) return st;
-    SegArgs e = y;  // U B
-    e.N = l.N;
-    e.K = l.R;
-    e.A = work.u;
-    e.A_lo = work.u_lo.p;
-    e.B = l.B;
-    e.transb = l.transl;
-    e.C = work.sum;
-    e.c_f32 = true;
-    st = launch(e, sms, s);
-    if (st != gemm::kOk) return st;
-    y.add = work.sum;
+// One product, its operands copied where they have to be.
+int launch(SegArgs &a, int sms, cudaStream_t s) {
+  Workspace w(a.bf16, a.offsets, a.groups, a.M);
+  if (a.M > 0 && (a.wgrad || a.K > 0)) {
+    w.readable(a.A);
+    w.readable(a.B, !a.wgrad);
   }
-  y.dense = true;
-  y.groups = l.adapted ? l.segments : 0;
-  y.index = nullptr;
-  y.N = l.N;
-  y.K = l.K;
-  y.A = l.X;
-  y.B = l.W;
-  y.transb = l.transw;
-  y.C = l.Y;
-  return launch(y, sms, s);
+  int st = w.take(sms, s);
+  if (st == gemm::kOk) st = gemm::seg_tc_launch(a, sms, s);
+  return w.give_back(st, s);
 }
 
 }  // namespace
@@ -245,7 +331,7 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
   l.W = SegMatrix{W, ldw, 0, transw ? N : K, transw ? K : N, 1};
   l.A = SegMatrix{A, lda, stridea, transl ? R : K, transl ? K : R, bank};
   l.B = SegMatrix{B, ldb, strideb, transl ? N : R, transl ? R : N, bank};
-  l.U = SegMatrix{U, ldu, 0, M, R, 1};
+  l.user_u = SegMatrix{U, ldu, 0, M, R, 1};
   l.Y = SegMatrix{Y, ldy, 0, M, N, 1};
   l.offsets = offsets;
   l.index = index;
@@ -258,7 +344,7 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
       (!stack_ok(l.A, elem, false, &ra) || !stack_ok(l.B, elem, false, &rb) ||
        !array_ok(offsets, segments + 1, 8, false, &ro) ||
        !array_ok(index, segments, 4, true, &ri) || !array_ok(scales, bank, 4, true, &rs) ||
-       (U != nullptr && !stack_ok(l.U, elem, true, &ru))))
+       (U != nullptr && !stack_ok(l.user_u, elem, true, &ru))))
     return GEMM_ERR_INVALID_ARG;
   const Range in[] = {rx, rw, ra, rb, ro, ri, rs};
   for (const Range &r : in)
@@ -269,9 +355,10 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
   int st = gemm::current_device_info(&dev, &sms);
   if (st != gemm::kOk) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Work work;
-  st = work.take(l, s);
-  if (st == gemm::kOk) st = lora_run(l, work, sms, s);
+  Workspace work(l.bf16, offsets, segments, M);
+  l.prepare(work);
+  st = work.take(sms, s);
+  if (st == gemm::kOk) st = l.run(work, sms, s);
   return work.give_back(st, s);
 }
 
@@ -303,11 +390,10 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
   l.W = SegMatrix{W, ldw, 0, transw ? N : K, transw ? K : N, 1};
   l.A = SegMatrix{B, ldb, strideb, transl ? N : R, transl ? R : N, segments};
   l.B = SegMatrix{A, lda, stridea, transl ? R : K, transl ? K : R, segments};
-  l.U = SegMatrix{nullptr, 0, 0, M, R, 1};
   l.Y = SegMatrix{dX, lddx, 0, M, K, 1};
   l.offsets = offsets;
   l.scales = scales;
-  const SegMatrix x{X, ldx, 0, M, K, 1}, u{U, ldu, 0, M, R, 1};
+  SegMatrix x{X, ldx, 0, M, K, 1}, u{U, ldu, 0, M, R, 1};
   const SegMatrix da{dA, ldda, strideda, transl ? R : K, transl ? K : R, segments};
   const SegMatrix db{dB, lddb, stridedb, transl ? N : R, transl ? R : N, segments};
   Range rdy, rx, ru, rw, ra, rb, ro, rs, rdx, rda, rdb;
@@ -333,9 +419,16 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
   int st = gemm::current_device_info(&dev, &sms);
   if (st != gemm::kOk) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Work work;
-  st = work.take(l, s);
-  if (st == gemm::kOk && M > 0) st = lora_run(l, work, sms, s);
+  Workspace work(l.bf16, offsets, segments, M);
+  if (M > 0) {
+    l.prepare(work);
+    if (l.adapted) {
+      work.readable(x);
+      work.readable(u);
+    }
+  }
+  st = work.take(sms, s);
+  if (st == gemm::kOk && M > 0) st = l.run(work, sms, s);
   // dA = X^T V (stored R x K: V^T X) and dB = U^T dY (stored N x R: dY^T U).
   SegArgs g;
   g.bf16 = l.bf16;
@@ -343,25 +436,25 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
   g.groups = segments;
   g.M = M;
   g.offsets = offsets;
-  const SegMatrix v = work.u;
+  const SegMatrix &v = l.u;
   if (st == gemm::kOk && segments > 0 && R > 0 && K > 0) {
     g.A = transl ? v : x;
     g.B = transl ? x : v;
-    g.A_lo = transl ? work.u_lo.p : nullptr;
-    g.B_lo = transl ? nullptr : work.u_lo.p;
+    g.A_lo = transl ? l.u_lo : SegMatrix{};
+    g.B_lo = transl ? SegMatrix{} : l.u_lo;
     g.C = da;
     g.K = da.rows;
     g.N = da.cols;
-    st = launch(g, sms, s);
+    st = gemm::seg_tc_launch(g, sms, s);
   }
   if (st == gemm::kOk && segments > 0 && R > 0 && N > 0) {
     g.A = transl ? l.X : u;
     g.B = transl ? u : l.X;
-    g.A_lo = g.B_lo = nullptr;
+    g.A_lo = g.B_lo = SegMatrix{};
     g.C = db;
     g.K = db.rows;
     g.N = db.cols;
-    st = launch(g, sms, s);
+    st = gemm::seg_tc_launch(g, sms, s);
   }
   return work.give_back(st, s);
 }

@@ -4,8 +4,9 @@
 // (tcgen05 cta_group::2): 256 lanes n (columns of the result, 128 a CTA) by up
 // to 256 columns q,
 //
-//   rows:   D[n, t] = sum_k B_z[k, n] A[t, k]      q = rows t of one segment
-//   wgrad:  D[n, i] = sum_t B[t, n] A[t, i]        t = rows of the segment
+//   rows:    D[n, t] = sum_k B_z[k, n] A[t, k]     q = rows t of one segment
+//   adapted: D[n, t] = sum_k B[k, n] A[t, k] + sum_r L_a[r, n] U[t, r]
+//   wgrad:   D[n, i] = sum_t B[t, n] A[t, i]       t = rows of the segment
 //
 // so a segment with few rows needs few columns (N of the MMA is the tile's own
 // row count, rounded up to 32): the weights then stream through at the rate of
@@ -18,10 +19,9 @@
 // in shared memory as lines of 64 contiguous elements (128 bytes, 128-byte
 // swizzle), K-major or MN-major as they lie in memory: no transposed copy.
 //
-// bf16 operands come by TMA, 64 k of 128 + 128 lines a stage, and go to
-// kind::f16 MMAs as they are. float32 operands, and bf16 ones that TMA cannot
-// read as given, are loaded by eight warps; a float32 value, 32 k a stage, is
-// split into three bf16 terms on the way,
+// Both types come by TMA. bf16 operands, 64 k of 128 + 128 lines a stage, go to
+// kind::f16 MMAs as they are. float32 values, 32 k a stage, are split by eight
+// warps into three bf16 terms on the way,
 //
 //   x = h + m + l,   h = bf16(x), m = bf16(x - h), l = bf16(x - h - m),
 //
@@ -35,7 +35,7 @@
 // 256 bf16 MMAs of one accumulator, against 1.1e-6 of an FP32 FMA chain). For
 // float32 each accumulator therefore holds 64 k only, a stage's small products
 // first, and the epilogue warps add it to sums in registers, rounded to
-// nearest, while the next one fills.
+// nearest, while the next one fills (3.3e-7 whatever K; with 128 k 7.5e-7).
 //
 // Every barrier wait is bounded; on a timeout the pair lets its copies and
 // MMAs finish (bounded), frees TMEM and exits, and the host reads the status.
@@ -63,22 +63,24 @@ constexpr int kCols = 256;      // most rows per tile (MMA N)
 constexpr int kHalf = 128;      // lanes, and columns at most, of one CTA of the pair
 constexpr int kColStep = 32;    // granularity of the MMA's N
 constexpr int kRasterM = 8;     // row tiles per raster group
+constexpr int kBlock = 64;      // k of a block: a bf16 stage, or a float32 accumulator
+constexpr int kMaxSplits = 16;
 constexpr uint32_t kTmemCols = 512;
 
-struct SegOperand {
-  const void *p[2];  // one or two terms of the operand
-  long long ld, zs, extent;
-  int vec;           // 8 elements at a multiple of 8 are one aligned load
-};
+enum Form : int { kRows = 0, kDense = 1, kAdapted = 2, kWgrad = 3 };
 
 struct SegTc {
-  int wgrad, dense;
-  int groups, M, N, K, bank;
-  int passes;        // terms summed of a two-term operand: 1 or 2
+  int form;
+  int groups;        // segments
+  int entries;       // of the table: groups; dense 1; adapted groups + 2
+  int M, N, K, R, bank;
+  int z_step;        // 0: one matrix for every segment
+  // Passes over the operands of a tile: one, or two with a two-term operand;
+  // adapted: A and B, then U (its terms) and the adapter's L.
+  int passes;
   int tiles_n;
-  int q_box;         // TMA: lines per copy of Q (rows kind)
-  int l_whole, q_whole;  // TMA: an MN-major operand comes as one 4-D copy
-  SegOperand L, Q;   // plain loads
+  int q_box;         // lines per copy of a K-major Q
+  int l_whole, l_whole1;  // the MN-major L of pass 0, of the others, comes as one 4-D copy
   const int64_t *offsets;
   const int32_t *index;
   const float *scales;
@@ -86,20 +88,23 @@ struct SegTc {
   long long add_ld, add_extent;
   void *C, *C_lo;    // C_lo: the result's second term
   int c_f32;
-  int c_rows;        // rows of the result can leave as 16-byte pieces
+  int c_rows;        // rows of the result can leave by TMA
   long long c_ld, c_lo_ld, c_stride, c_extent, c_lo_extent;
+  // Few tiles: the blocks of each go to several pairs, which leave their sums
+  // in slots (one a work item, 2 x 256 x 128 floats); the last one adds them.
+  float *slots;
+  unsigned *arrived;  // [2 tile + rank], zero
+  long long slot_extent;
   unsigned long long timeout_ns;
 };
 
-template <class T, bool TMA>
+template <class T>
 struct Cfg {
   static constexpr bool kSplit = std::is_same<T, float>::value;  // three-term operands
   static constexpr int kTerms = kSplit ? 3 : 1;
   // k per stage: 128-byte lines of bf16, or 64-byte ones of each float32 term
   // (two stages of three terms leave room for the values in flight).
   static constexpr int kBK = kSplit ? 32 : 64;
-  // k of one accumulator, float32 (two stages).
-  static constexpr int kChunk = kSplit ? 64 : kBK;
   static constexpr int kOpBytes = kHalf * kBK * 2;  // one term of one operand
   static constexpr int kStageBytes = 2 * kTerms * kOpBytes;
   static constexpr int kStages = kSplit ? 2 : 6;
@@ -111,14 +116,11 @@ struct Cfg {
   // Results on their way out, per 128 columns of the tile: two pieces of 16
   // rows of 128 bf16, or one of float32.
   static constexpr int kOutBytes = 8192;
-  static constexpr bool kLoaders = kSplit || !TMA;  // warps that fill the stages
   static constexpr int kMmaWarp = 1;
   static constexpr int kFixWarp = 2;
   static constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
   static constexpr int kLoadWarp0 = 12, kLoadWarps = 8;
-  static constexpr int kThreads = 32 * (kLoaders ? kLoadWarp0 + kLoadWarps : kLoadWarp0);
-  static constexpr int kCopyWarps = 3;  // float32 without TMA: warps 0, 2 and 3
-  
+  static constexpr int kThreads = 32 * (kSplit ? kLoadWarp0 + kLoadWarps : kLoadWarp0);
 };
 
 template <int STAGES, int RAW>
@@ -128,28 +130,60 @@ struct Shared {
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem_base;
   int abort;
+  int tiles[3];  // of width 256, 128, 64
+  int longest;   // rows of the longest segment
+  int last;      // this CTA's sums complete a split tile
 };
 
-// One tile of the list, as every role sees it.
+// One work item -- a tile of the list, or a part of its blocks -- as every role
+// sees it.
 struct Tile {
-  int g, z;       // segment; its matrix (-1: none)
-  int n0;         // first lane (result column)
-  int q0, qn;     // first column and how many are in the result
-  int k0, klen;   // first row of the contraction (wgrad) and its length
-  int row0;       // rows kind: row of the result of column 0 is q0 (absolute)
+  int item, index;  // of the list; tile
+  int g, z;         // segment; its matrix
+  int a;            // adapted: the segment's adapter
+  int n0;           // first lane (result column)
+  int q0, qn;       // first column (rows form: row of the result), and how many
+  int k0;           // wgrad: first row of the contraction
+  int klen, xlen;   // k of the first pass, of each of the others
+  int b0, b1;       // blocks to sum, counted through the passes
+};
+
+struct SegMaps {
+  CUtensorMap l[3], q[3], c;  // by pass; of the results
 };
 
 struct Table {
-  int *first;     // [groups + 1] tiles of the segments before
-  int *row;       // [groups + 1] offsets, held to the rows there are
+  int *first;     // [entries + 1] tiles of the entries before
+  int *row;       // [entries + 1] offsets, held to the rows there are
+  int width;      // most columns of a tile
+  int splits;     // work items per tile
 };
 
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int t, Tile &o) {
-  const int groups = p.dense ? 1 : p.groups;
-  if (t >= tab.first[groups]) return false;
-  int lo = 0, hi = groups;  // the segment whose tiles hold t
+__device__ __forceinline__ int matrix_of(const SegTc &p, int g) {
+  const int z = p.index != nullptr ? p.index[g] : g;
+  return z >= 0 && z < p.bank ? z : -1;
+}
+
+// Passes of a tile in blocks: f(pass, length, first k, last k) for each pass
+// that has some of the item's blocks; false stops.
+template <class F>
+__device__ __forceinline__ bool for_passes(const SegTc &p, const Tile &t, const F &f) {
+  int base = 0;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int len = pass == 0 ? t.klen : t.xlen, n = cdiv(len, kBlock);
+    const int lo = max(t.b0 - base, 0), hi = min(t.b1 - base, n);
+    if (lo < hi && !f(pass, len, lo * kBlock, min(hi * kBlock, len))) return false;
+    base += n;
+  }
+  return true;
+}
+
+__device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int item, Tile &o) {
+  const int t = tab.splits > 1 ? item / tab.splits : item;
+  if (t >= tab.first[p.entries]) return false;
+  int lo = 0, hi = p.entries;  // the entry whose tiles hold t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (tab.first[mid] <= t)
@@ -158,44 +192,82 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int t,
       hi = mid;
   }
   const int idx = t - tab.first[lo];
-  const int2 rows = make_int2(tab.row[lo], max(tab.row[lo], tab.row[lo + 1]));
-  const int height = p.wgrad ? p.K : rows.y - rows.x;
-  const int tm = cdiv(height, kCols);
+  const int r0 = tab.row[lo], rows = max(tab.row[lo + 1] - r0, 0);
+  const int height = p.form == kWgrad ? p.K : rows;
+  const int tm = cdiv(height, tab.width);
   // Groups of kRasterM row tiles, lane tiles in the outer loop, so that the
   // pairs at work at one time share operand tiles in L2.
   const int group = idx / (kRasterM * p.tiles_n);
   const int m_first = group * kRasterM;
-  const int width = min(kRasterM, tm - m_first);
+  const int across = min(kRasterM, tm - m_first);
   const int rem = idx - group * kRasterM * p.tiles_n;
-  const int mi = m_first + rem % width, ni = rem / width;
-  o.g = lo;
-  // The segment's rows in tm equal parts (in steps of kColStep), not whole
+  const int mi = m_first + rem % across, ni = rem / across;
+  // The segment's rows in tm equal parts (in steps the MMA allows), not whole
   // tiles and a rest: the pairs end together, and no tile is all operand
   // traffic and no work.
-  const int step = p.wgrad ? 128 : kColStep;
-  const int width_q = cdiv(cdiv(height, tm), step) * step;
+  const int step = p.form == kWgrad ? 128 : kColStep;
+  const int part = cdiv(cdiv(height, tm), step) * step;
+  o.item = item;
+  o.index = t;
+  o.g = lo;
   o.n0 = ni * kLanes;
-  o.qn = min(width_q, height - mi * width_q);
-  if (p.wgrad) {
-    o.z = 0;
-    o.q0 = mi * width_q;
-    o.k0 = rows.x;
-    o.klen = rows.y - rows.x;
+  o.qn = min(part, height - mi * part);
+  o.q0 = mi * part;
+  o.k0 = 0;
+  o.z = 0;
+  o.a = -1;
+  o.klen = o.xlen = p.K;
+  if (p.form == kWgrad) {
+    o.k0 = r0;
+    o.klen = o.xlen = rows;
   } else {
-    o.z = lo;
-    if (p.dense) {
-      o.z = 0;
-    } else if (p.index != nullptr) {
-      o.z = p.index[lo];
-      if (o.z < 0 || o.z >= p.bank) o.z = -1;
-    } else if (o.z >= p.bank) {
-      o.z = -1;
+    o.q0 += r0;
+    if (p.form == kRows) {
+      o.z = matrix_of(p, lo);
+      if (o.z < 0) o.klen = o.xlen = 0;
+    } else if (p.form == kAdapted) {
+      o.a = lo > 0 && lo <= p.groups ? matrix_of(p, lo - 1) : -1;
+      o.xlen = o.a >= 0 ? p.R : 0;
     }
-    o.q0 = rows.x + mi * width_q;
-    o.k0 = 0;
-    o.klen = o.z < 0 ? 0 : p.K;
+  }
+  const int blocks = cdiv(o.klen, kBlock) + (p.passes - 1) * cdiv(o.xlen, kBlock);
+  if (tab.splits > 1) {
+    const int s = item - t * tab.splits;
+    o.b0 = static_cast<int>(static_cast<long long>(blocks) * s / tab.splits);
+    o.b1 = static_cast<int>(static_cast<long long>(blocks) * (s + 1) / tab.splits);
+  } else {
+    o.b0 = 0;
+    o.b1 = blocks;
   }
   return true;
+}
+
+// How the list is cut, from its tiles at each width (every CTA finds the same).
+// Fewer tiles than pairs leave pairs idle, and a list a little longer than a
+// multiple of them leaves most idle in the last round, so a narrower tile is
+// taken where the rounds it makes are shorter: a round costs its columns and
+// about 96 more (copies of the lanes' operand and hand-overs; a round of 256
+// columns takes 2.2 times one of 64). Tiles that still leave half the pairs
+// idle are split along k, into at least four blocks an item.
+__device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int longest, int pairs,
+                                           Table &tab) {
+  int best = 0, cost = 0x7fffffff;
+  for (int i = 0; i < (p.form == kWgrad ? 2 : 3); ++i) {
+    if (i > 0 && tiles[i] == tiles[i - 1]) continue;
+    const int c = min(cdiv(tiles[i], pairs), 1 << 20) * ((kCols >> i) + 96);
+    if (c < cost) {
+      cost = c;
+      best = i;
+    }
+  }
+  tab.width = kCols >> best;
+  tab.splits = 1;
+  const int n = tiles[best];
+  if (p.slots != nullptr && n > 0 && n * 2 <= pairs) {
+    const int k = p.form == kWgrad ? longest : p.K;
+    const int blocks = p.passes * cdiv(k, kBlock);
+    tab.splits = max(min(min(pairs / n, blocks / 4), kMaxSplits), 1);
+  }
 }
 
 // MMA columns of a tile: its own, in steps the operand's layout allows (an
@@ -333,32 +405,11 @@ __device__ __forceinline__ void store_bulk(void *dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
-// ------------------------------------------------------------- plain loads --
+// ----------------------------------------------------------- float32 terms --
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Bf16 elements [x, x + 8) of the line at `row` (element offset), those at or
-// past `limit` zero.
-__device__ __forceinline__ uint4 load_eight(const SegOperand &o, const __nv_bfloat16 *p, int site,
-                                            long long row, int x, int limit) {
-  const long long off = row + x;
-  if (o.vec && x + 8 <= limit && index_ok(site, off, 8, o.extent))
-    return __ldg(reinterpret_cast<const uint4 *>(p + off));
-  const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-  uint32_t e[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    e[i] = x + i < limit && index_ok(site, off + i, 1, o.extent) ? __ldg(h + off + i) : 0;
-  return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-}
-
-// Copy a float from global to shared memory, asynchronously; `bytes` 0: zero.
-__device__ __forceinline__ void copy_float(uint32_t dst, const float *src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
 }
 
 // Eight float32 values as three bf16 terms (`term` bytes apart).
@@ -393,26 +444,21 @@ __device__ __forceinline__ void set_registers() {
 // ------------------------------------------------------------------ kernel --
 
 // LMN, QMN: the operand lies with its lane (column) index contiguous.
-template <class T, bool TMA, bool LMN, bool QMN>
-__global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
-    seg_tc_kernel(const __grid_constant__ CUtensorMap map_l0,
-                  const __grid_constant__ CUtensorMap map_l1,
-                  const __grid_constant__ CUtensorMap map_q0,
-                  const __grid_constant__ CUtensorMap map_q1,
-                  const __grid_constant__ CUtensorMap map_c, const SegTc p) {
-  using C = Cfg<T, TMA>;
+template <class T, bool LMN, bool QMN>
+__global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
+    seg_tc_kernel(const __grid_constant__ SegMaps maps, const SegTc p) {
+  using C = Cfg<T>;
   constexpr int STAGES = C::kStages, kBK = C::kBK, kOpBytes = C::kOpBytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *stages = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *raw = stages + STAGES * C::kStageBytes;
-  using Sh = Shared<STAGES, C::kRawStages>;
   uint8_t *out = raw + C::kRawBytes;
+  using Sh = Shared<STAGES, C::kRawStages>;
   Sh *sh = reinterpret_cast<Sh *>(out + 2 * C::kOutBytes);
   Table tab;
-  const int groups = p.dense ? 1 : p.groups;
   tab.row = reinterpret_cast<int *>(sh + 1);
-  tab.first = tab.row + groups + 1;
+  tab.first = tab.row + p.entries + 1;
   volatile int *abort = &sh->abort;
 
   const uint32_t warp = warp_index();
@@ -420,8 +466,8 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   // Arrivals that fill a stage. Copies straight to it: the even CTA's (both
   // CTAs' bytes), or for weight gradients one arrival from each CTA's copies or
-  // masks. Else one from each CTA's load warps.
-  constexpr int kFullCount = C::kLoaders || QMN ? 2 : 1;
+  // masks. float32: one from each CTA's load warps.
+  constexpr int kFullCount = C::kSplit || QMN ? 2 : 1;
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
@@ -431,7 +477,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       mbar_init(&sh->part[s], 1);  // this CTA's bytes of a stage that is masked before use
     }
     for (int s = 0; s < C::kRawStages; ++s) {
-      mbar_init(&sh->raw_full[s], TMA ? 1 : 32 * C::kCopyWarps);
+      mbar_init(&sh->raw_full[s], 1);
       mbar_init(&sh->raw_empty[s], C::kLoadWarps);
     }
     for (int a = 0; a < 2; ++a) {
@@ -440,11 +486,12 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
+    sh->tiles[0] = sh->tiles[1] = sh->tiles[2] = sh->longest = 0;
     fence_barrier_init();
   }
-  if (TMA && warp == 0 && lane == 0) {
-    tma_prefetch_map(&map_l0);
-    tma_prefetch_map(&map_q0);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&maps.l[0]);
+    tma_prefetch_map(&maps.q[0]);
   }
   if (warp == C::kMmaWarp) {
     tmem_alloc<2>(&sh->tmem_base, kTmemCols);
@@ -452,30 +499,45 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   }
   grid_dependency_wait();
   // The table of segments: their rows, and the tiles before each.
-  for (int g = threadIdx.x; g <= groups; g += C::kThreads) {
-    const long long a = p.dense ? (g ? p.M : 0) : p.offsets[g];
+  for (int g = threadIdx.x; g <= p.entries; g += C::kThreads) {
+    long long a;
+    if (p.form == kDense)
+      a = g ? p.M : 0;
+    else if (p.form == kAdapted)  // rows before and behind the segments, too
+      a = g == 0 ? 0 : (g == p.entries ? p.M : p.offsets[g - 1]);
+    else
+      a = p.offsets[g];
     tab.row[g] = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < groups; g += C::kThreads)
-    tab.first[g] =
-        cdiv(p.wgrad ? p.K : max(tab.row[g + 1] - tab.row[g], 0), kCols) * p.tiles_n;
+  for (int g = threadIdx.x; g < p.entries; g += C::kThreads) {
+    const int rows = max(tab.row[g + 1] - tab.row[g], 0);
+    const int height = p.form == kWgrad ? p.K : rows;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (height > 0) atomicAdd(&sh->tiles[i], cdiv(height, kCols >> i) * p.tiles_n);
+    atomicMax(&sh->longest, rows);
+  }
   __syncthreads();
+  choose_cut(p, sh->tiles, sh->longest, pairs, tab);
   if (warp == 0) {
     int sum = 0;
-    for (int g0 = 0; g0 < groups; g0 += 32) {
+    for (int g0 = 0; g0 < p.entries; g0 += 32) {
       const int g = g0 + static_cast<int>(lane);
-      const int own = g < groups ? tab.first[g] : 0;
+      int own = 0;
+      if (g < p.entries)
+        own = cdiv(p.form == kWgrad ? p.K : max(tab.row[g + 1] - tab.row[g], 0), tab.width) *
+              p.tiles_n;
       int v = own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int w = __shfl_up_sync(0xffffffffu, v, d);
         if (static_cast<int>(lane) >= d) v += w;
       }
-      if (g < groups) tab.first[g] = sum + v - own;
+      if (g < p.entries) tab.first[g] = sum + v - own;
       sum += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (lane == 0) tab.first[groups] = sum;
+    if (lane == 0) tab.first[p.entries] = sum;
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -485,82 +547,89 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
   grid_launch_dependents();
 
   const bool epilogue = warp >= C::kEpiWarp0 && warp < C::kEpiWarp0 + C::kEpiWarps;
-  const bool loader = C::kLoaders && warp >= C::kLoadWarp0;
-
   Tile t;
-  if (TMA && !C::kSplit && warp == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------------- copies --
+    // bf16: into the stages, both CTAs' bytes on the even CTA's barrier.
+    // float32: into this CTA's ring of raw values.
+    set_registers<C::kSplit, 40>();
+    constexpr int kLine = C::kSplit ? 32 : 64;          // elements of a line
+    constexpr int kChunk = kBK * 128;                   // bytes of an MN-major chunk
+    constexpr int RING = C::kSplit ? C::kRawStages : STAGES;
+    constexpr int kSlot = C::kSplit ? 2 * C::kRawOpBytes : C::kStageBytes;
+    uint8_t *const ring = C::kSplit ? raw : stages;
     if (lane == 0) {
-      Ring<STAGES> r;
+      uint64_t *const ring_empty = C::kSplit ? sh->raw_empty : sh->empty;
+      uint64_t *const ring_full = C::kSplit ? sh->raw_full : sh->full;
+      Ring<RING> r;
       uint32_t part_phase = 0, parts = 0;  // stages that went to part[], by phase and at all
       int issued = 0;
       bool ok = true;
-      const uint32_t full0 = mbar_cluster_addr(&sh->full[0], 0);
+      const uint32_t full0 = C::kSplit ? smem_addr(sh->raw_full) : mbar_cluster_addr(sh->full, 0);
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const int half = mma_cols<QMN>(t) / 2;
         const int ln = t.n0 + static_cast<int>(rank) * kHalf;
         const int qn = t.q0 + static_cast<int>(rank) * half;
-        const int copies = QMN ? half / 64 : cdiv(half, p.q_box);
+        const int copies = QMN ? half / kLine : cdiv(half, p.q_box);
         const uint32_t bytes =
-            kOpBytes + static_cast<uint32_t>(copies) * (QMN ? 8192u : 128u * p.q_box);
-        for (int pass = 0; ok && pass < p.passes; ++pass) {
-          const CUtensorMap *ml = pass ? &map_l1 : &map_l0, *mq = pass ? &map_q1 : &map_q0;
-          for (int kk = 0; kk < t.klen; kk += kBK) {
-            if (!wait(&sh->empty[r.idx], r.phase ^ 1, p, abort)) {
-              ok = false;
-              break;
-            }
-            uint8_t *st = stages + r.idx * C::kStageBytes;
+            static_cast<uint32_t>(kHalf * 128 + copies * (QMN ? kChunk : 128 * p.q_box));
+        ok = for_passes(p, t, [&](int pass, int len, int k_lo, int k_hi) {
+          const CUtensorMap *ml = &maps.l[pass], *mq = &maps.q[pass];
+          const int lz = p.form == kAdapted && pass > 0 ? t.a : t.z * p.z_step;
+          const bool whole = pass > 0 && p.form == kAdapted ? p.l_whole1 : p.l_whole;
+          for (int kk = k_lo; kk < k_hi; kk += kBK) {
+            if (!wait(&ring_empty[r.idx], r.phase ^ 1, p, abort)) return false;
+            uint8_t *l = ring + r.idx * kSlot;
+            uint8_t *q = l + kHalf * 128;
             uint32_t bar = full0 + r.idx * 8;
             parts &= ~(1u << r.idx);
-            if (QMN && t.klen - kk < kBK && (t.klen - kk) % 16 != 0) {
+            if (C::kSplit) {
+              mbar_arrive_expect_tx(&ring_full[r.idx], bytes);
+            } else if (QMN && len - kk < kBK && (len - kk) % 16 != 0) {
               // This CTA's own barrier; the mask warp passes it on.
               bar = smem_addr(&sh->part[r.idx]);
               mbar_arrive_expect_tx(&sh->part[r.idx], bytes);
               parts |= 1u << r.idx;
               part_phase ^= 1u << r.idx;
             } else if (rank == 0) {
-              mbar_arrive_expect_tx(&sh->full[r.idx], 2 * bytes);
-              if (QMN) mbar_arrive(&sh->full[r.idx]);
+              mbar_arrive_expect_tx(&ring_full[r.idx], 2 * bytes);
+              if (QMN) mbar_arrive(&ring_full[r.idx]);
             }
             if (!LMN) {
-              tma_load_3d_pair(st, ml, bar, kk, ln, t.z);
-            } else if (p.l_whole) {
-              tma_load_4d_pair(st, ml, bar, 0, t.k0 + kk, ln / 64, t.z);
+              tma_load_3d_pair(l, ml, bar, kk, ln, lz);
+            } else if (whole) {
+              tma_load_4d_pair(l, ml, bar, 0, t.k0 + kk, ln / kLine, lz);
             } else {
-              tma_load_3d_pair(st, ml, bar, ln, t.k0 + kk, t.z);
-              tma_load_3d_pair(st + 8192, ml, bar, ln + 64, t.k0 + kk, t.z);
+#pragma unroll
+              for (int c = 0; c < kHalf / kLine; ++c)
+                tma_load_3d_pair(l + c * kChunk, ml, bar, ln + c * kLine, t.k0 + kk, lz);
             }
-            if (QMN && p.q_whole) {
-              tma_load_4d_pair(st + kOpBytes, mq, bar, 0, t.k0 + kk, qn / 64, 0);
-            } else {
-              for (int c = 0; c < copies; ++c) {
-                if (QMN)
-                  tma_load_3d_pair(st + kOpBytes + c * 8192, mq, bar, qn + c * 64, t.k0 + kk, 0);
-                else
-                  tma_load_3d_pair(st + kOpBytes + c * p.q_box * 128, mq, bar, kk,
-                                   qn + c * p.q_box, 0);
-              }
+            for (int c = 0; c < copies; ++c) {
+              if (QMN)
+                tma_load_3d_pair(q + c * kChunk, mq, bar, qn + c * kLine, t.k0 + kk, 0);
+              else
+                tma_load_3d_pair(q + c * p.q_box * 128, mq, bar, kk, qn + c * p.q_box, 0);
             }
             ++issued;
             r.next();
           }
-        }
+          return true;
+        });
       }
       // On a timeout let the copies that were started land: those of the last
       // stages issued, one phase back where the ring has wrapped since.
       if (!ok)
-        for (int s = 0; s < STAGES && s < issued; ++s) {
+        for (int s = 0; s < RING && s < issued; ++s) {
           r.phase ^= r.idx == 0 ? 1u : 0u;
-          r.idx = r.idx == 0 ? STAGES - 1 : r.idx - 1;
+          r.idx = r.idx == 0 ? RING - 1 : r.idx - 1;
           if (parts >> r.idx & 1u)
             drain_wait(&sh->part[r.idx], (part_phase >> r.idx & 1u) ^ 1u, p.timeout_ns);
-          else if (rank == 0)
-            drain_wait(&sh->full[r.idx], r.phase, p.timeout_ns);
+          else if (C::kSplit || rank == 0)
+            drain_wait(&ring_full[r.idx], r.phase, p.timeout_ns);
         }
     }
     __syncwarp();
-  } else if (TMA && !C::kSplit && QMN && warp == C::kFixWarp) {
+  } else if (!C::kSplit && QMN && warp == C::kFixWarp) {
     // -------------------------------------------------------------- masks --
     // The last stage of a segment whose rows end inside a step of 16: zero
     // both operands' lines from its end to the step's, which hold the next
@@ -570,143 +639,29 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
     bool ok = true;
     for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
       const int half = mma_cols<QMN>(t) / 2;
-      const int blocks = cdiv(t.klen, kBK);
-      for (int kb = 0; kb < blocks * p.passes; ++kb) {
-        const int kk = (kb >= blocks ? kb - blocks : kb) * kBK;
-        const int tail = t.klen - kk;
-        if (tail < kBK && tail % 16 != 0) {
-          if (!warp_wait(&sh->part[r.idx], part_phase >> r.idx & 1u, p, abort)) {
-            ok = false;
-            break;
-          }
-          part_phase ^= 1u << r.idx;
-          uint8_t *st = stages + r.idx * C::kStageBytes;
-          const int end = (tail + 15) / 16 * 16;
-          const int chunks = 2 + half / 64;  // of L, then of Q
-          for (int e = static_cast<int>(lane); e < chunks * (end - tail) * 8; e += 32) {
-            const int c = e / ((end - tail) * 8), w = e % ((end - tail) * 8);
-            *reinterpret_cast<uint4 *>(st + c * 8192 + (tail + w / 8) * 128 + w % 8 * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->full[r.idx], 0));
-        }
-        r.next();
-      }
-    }
-  } else if (C::kSplit && TMA && warp == 0) {
-    // ------------------------------------------------ float32 by TMA --
-    set_registers<C::kSplit, 40>();
-    if (lane == 0) {
-      Ring<C::kRawStages> r;
-      int issued = 0;
-      bool ok = true;
-      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
-        const int half = mma_cols<QMN>(t) / 2;
-        const int ln = t.n0 + static_cast<int>(rank) * kHalf;
-        const int qn = t.q0 + static_cast<int>(rank) * half;
-        const int copies = QMN ? half / 32 : cdiv(half, p.q_box);
-        const uint32_t bytes = C::kRawOpBytes +
-                               static_cast<uint32_t>(copies) * (QMN ? 4096u : 128u * p.q_box);
-        for (int kk = 0; kk < t.klen; kk += kBK) {
-          if (!wait(&sh->raw_empty[r.idx], r.phase ^ 1, p, abort)) {
-            ok = false;
-            break;
-          }
-          uint8_t *l = raw + r.idx * 2 * C::kRawOpBytes, *q = l + C::kRawOpBytes;
-          const uint32_t bar = smem_addr(&sh->raw_full[r.idx]);
-          mbar_arrive_expect_tx(&sh->raw_full[r.idx], bytes);
-          if (!LMN) {
-            tma_load_3d_pair(l, &map_l0, bar, kk, ln, t.z);
-          } else if (p.l_whole) {
-            tma_load_4d_pair(l, &map_l0, bar, 0, t.k0 + kk, ln / 32, t.z);
-          } else {
-            for (int c = 0; c < 4; ++c)
-              tma_load_3d_pair(l + c * 4096, &map_l0, bar, ln + c * 32, t.k0 + kk, t.z);
-          }
-          if (QMN && p.q_whole) {
-            tma_load_4d_pair(q, &map_q0, bar, 0, t.k0 + kk, qn / 32, 0);
-          } else {
-            for (int c = 0; c < copies; ++c) {
-              if (QMN)
-                tma_load_3d_pair(q + c * 4096, &map_q0, bar, qn + c * 32, t.k0 + kk, 0);
-              else
-                tma_load_3d_pair(q + c * p.q_box * 128, &map_q0, bar, kk, qn + c * p.q_box, 0);
+      ok = for_passes(p, t, [&](int, int len, int k_lo, int k_hi) {
+        for (int kk = k_lo; kk < k_hi; kk += kBK) {
+          const int tail = len - kk;
+          if (tail < kBK && tail % 16 != 0) {
+            if (!warp_wait(&sh->part[r.idx], part_phase >> r.idx & 1u, p, abort)) return false;
+            part_phase ^= 1u << r.idx;
+            uint8_t *st = stages + r.idx * C::kStageBytes;
+            const int end = (tail + 15) / 16 * 16;
+            const int chunks = 2 + half / 64;  // of L, then of Q
+            for (int e = static_cast<int>(lane); e < chunks * (end - tail) * 8; e += 32) {
+              const int c = e / ((end - tail) * 8), w = e % ((end - tail) * 8);
+              *reinterpret_cast<uint4 *>(st + c * 8192 + (tail + w / 8) * 128 + w % 8 * 16) =
+                  make_uint4(0, 0, 0, 0);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->full[r.idx], 0));
           }
-          ++issued;
           r.next();
         }
-      }
-      if (!ok)  // let the copies that were started land
-        for (int s = 0; s < C::kRawStages && s < issued; ++s) {
-          r.phase ^= r.idx == 0 ? 1u : 0u;
-          r.idx = r.idx == 0 ? C::kRawStages - 1 : r.idx - 1;
-          drain_wait(&sh->raw_full[r.idx], r.phase, p.timeout_ns);
-        }
+        return true;
+      });
     }
-    __syncwarp();
-  } else if (C::kSplit && !TMA && warp < C::kEpiWarp0 && warp != C::kMmaWarp) {
-    // ------------------------------- float32 of any pitch and alignment --
-    set_registers<C::kSplit, 40>();
-    // A line of 32 values a warp and copy, eight lines at a time; the warps
-    // take the groups of eight in turn.
-    const int cw = warp == 0 ? 0 : static_cast<int>(warp) - 1;
-    const int ln31 = static_cast<int>(lane);
-    Ring<C::kRawStages> r;
-    bool ok = true;
-    for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
-      const int half = mma_cols<QMN>(t) / 2;
-      const int ln = t.n0 + static_cast<int>(rank) * kHalf;
-      const int qn = static_cast<int>(rank) * half;
-      for (int kk = 0; kk < t.klen; kk += kBK) {
-        if (!warp_wait(&sh->raw_empty[r.idx], r.phase ^ 1, p, abort)) {
-          ok = false;
-          break;
-        }
-        const uint32_t base = smem_addr(raw) + r.idx * 2 * C::kRawOpBytes;
-        for (int g = cw; g < 32; g += C::kCopyWarps) {  // sixteen groups of L, then of Q
-          const bool is_l = g < 16, mn = is_l ? LMN : QMN;
-          const SegOperand &o = is_l ? p.L : p.Q;
-          const int line0 = (g & 15) * 8;  // K-major: the row; MN-major: chunk * 32 + k
-          long long off;
-          int first, last, x, end;  // lines [first, last) and values x < end exist
-          if (mn) {
-            const int k = kk + (line0 & 31), lane0 = (is_l ? ln : t.q0 + qn) + (line0 >> 5) * 32;
-            off = static_cast<long long>(t.k0 + k) * o.ld + lane0;
-            first = k;
-            last = is_l || (line0 >> 5) * 32 < half ? t.klen : 0;
-            x = lane0;
-            end = is_l ? p.N : p.K;
-          } else {
-            const int m = (is_l ? ln : qn) + line0;
-            off = static_cast<long long>(is_l ? m : t.q0 + m) * o.ld + kk;
-            first = m;
-            last = is_l ? p.N : (line0 < half ? t.qn : 0);
-            x = kk;
-            end = p.K;
-          }
-          if (!is_l && first >= last) continue;  // no columns here: never read
-          if (is_l) off += t.z * o.zs;
-          const float *src = static_cast<const float *>(o.p[0]);
-          const uint32_t dst = base + (g * 8) * 128 + (ln31 & 3) * 4;
-          const bool in = x + ln31 < end;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const long long at = off + e * o.ld + ln31;
-            const bool take = in && first + e < last &&
-                              index_ok(is_l ? kSiteLoadB : kSiteLoadA, at, 1, o.extent);
-            copy_float(dst + e * 128 + ((ln31 >> 2) ^ e) * 16, take ? src + at : src, take ? 4 : 0);
-          }
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_addr(&sh->raw_full[r.idx]))
-                     : "memory");
-        r.next();
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == C::kMmaWarp) {
     set_registers<C::kSplit, 40>();
     if (rank == 0 && lane == 0) {
@@ -716,29 +671,22 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       bool ok = true;
       // Descriptors of the first stage; others are a number of 16-byte units on.
       const uint32_t base = smem_addr(stages);
-      const uint64_t l0 = line_desc<LMN, C::kBK>(base);
-      const uint64_t q0 = line_desc<QMN, C::kBK>(base + C::kTerms * C::kOpBytes);
-      constexpr uint32_t kTerm = C::kOpBytes >> 4, kl = LMN ? 128 : 2, kq = QMN ? 128 : 2;
+      const uint64_t l0 = line_desc<LMN, kBK>(base);
+      const uint64_t q0 = line_desc<QMN, kBK>(base + C::kTerms * kOpBytes);
+      constexpr uint32_t kTerm = kOpBytes >> 4, kl = LMN ? 128 : 2, kq = QMN ? 128 : 2;
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const uint32_t idesc = idesc_bf16(kLanes, static_cast<uint32_t>(mma_cols<QMN>(t)), LMN, QMN);
         uint32_t more = 0;  // 0: the next MMA starts its accumulator
-        for (int pass = 0; ok && pass < p.passes; ++pass)
-          for (int kk0 = 0; kk0 < t.klen; kk0 += kBK) {
-            if (more == 0) {
-              // Both CTAs' epilogues have drained the accumulator.
-              if (!wait<true>(&sh->acc_empty[acc.idx], acc.phase ^ 1, p, abort)) {
-                ok = false;
-                break;
-              }
-            }
-            // Copies alone complete a stage of the rows form; other stages
-            // have arrivals of the odd CTA's warps (acquire at cluster scope).
-            if (!wait<C::kLoaders || QMN>(&sh->full[r.idx], r.phase, p, abort)) {
-              ok = false;
-              break;
-            }
+        ok = for_passes(p, t, [&](int, int len, int k_lo, int k_hi) {
+          for (int kk0 = k_lo; kk0 < k_hi; kk0 += kBK) {
+            // Both CTAs' epilogues have drained the accumulator.
+            if (more == 0 && !wait<true>(&sh->acc_empty[acc.idx], acc.phase ^ 1, p, abort))
+              return false;
+            // Copies alone complete a bf16 stage of the rows form; others have
+            // arrivals of the odd CTA's warps (acquire at cluster scope).
+            if (!wait<C::kSplit || QMN>(&sh->full[r.idx], r.phase, p, abort)) return false;
             tc_fence_after_sync();
-            const int left = t.klen - kk0;
+            const int left = len - kk0;
             const uint64_t l = l0 + r.idx * (C::kStageBytes >> 4);
             const uint64_t q = q0 + r.idx * (C::kStageBytes >> 4);
             const uint32_t d = tmem + acc.idx * kCols;
@@ -749,10 +697,9 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 6; ++c)
 #pragma unroll
-                  for (int kk = 0; kk < steps(); ++kk) {
+                  for (int kk = 0; kk < steps(); ++kk)
                     mma_bf16_pair(d, l + tl[c] * kTerm + kk * kl, q + tq[c] * kTerm + kk * kq,
                                   idesc, c + kk > 0 ? 1u : more);
-                  }
               } else {
 #pragma unroll
                 for (int kk = 0; kk < steps(); ++kk)
@@ -765,14 +712,19 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               products([left] { return (left + 15) / 16; });
             mma_commit_multicast<2>(&sh->empty[r.idx], 3);
             more = 1;
-            if ((C::kSplit && (kk0 + kBK) % C::kChunk == 0) ||
-                (kk0 + kBK >= t.klen && pass + 1 == p.passes)) {
+            if (C::kSplit && ((kk0 + kBK) % kBlock == 0 || kk0 + kBK >= k_hi)) {
               mma_commit_multicast<2>(&sh->acc_full[acc.idx], 3);
               acc.next();
               more = 0;
             }
             r.next();
           }
+          return true;
+        });
+        if (!C::kSplit && ok && more) {
+          mma_commit_multicast<2>(&sh->acc_full[acc.idx], 3);
+          acc.next();
+        }
       }
       // Every MMA issued completes before TMEM is released.
       mma_commit_multicast<2>(&sh->drain, 1);
@@ -793,9 +745,8 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       add1 = static_cast<int>(b < 0 ? 0 : (b > p.M ? p.M : b));
     }
     // The accumulator can be refilled: one arrival for all the CTA's epilogue
-    // warps (a release at cluster scope from each costs more than the barrier
-    // that gathers them). False if one of them gave up on its wait; every warp
-    // comes here once for each accumulator.
+    // warps. False if one of them gave up on its wait; every warp comes here
+    // once for each accumulator.
     auto drained = [&](uint32_t a, bool ok) {
       tc_fence_before_sync();
       ok = named_barrier_and(1, 32 * C::kEpiWarps, ok);
@@ -804,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       return ok;
     };
     for (int i = pair; tile_at(p, tab, i, t); i += pairs) {
-      const int blocks = cdiv(t.klen, C::kChunk) * p.passes;
+      const int blocks = t.b1 - t.b0;
       const int n = t.n0 + static_cast<int>(rank * 128 + quad * 32 + lane);
       bool ok = true;
       if constexpr (C::kSplit) {
@@ -849,25 +800,29 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       }
       // All warps go on together from here, or none does.
       if (!named_barrier_and(1, 32 * C::kEpiWarps, ok)) break;
-      const float scale =
-          !p.wgrad && !p.dense && p.scales != nullptr && t.z >= 0 ? p.scales[t.z] : 1.0f;
+      const float scale = p.form == kRows && p.scales != nullptr && t.z >= 0 ? p.scales[t.z] : 1.0f;
       const long long row0 = t.q0 + c0;
-      const long long at = (p.wgrad ? t.g * p.c_stride : 0) + row0 * p.c_ld + n;
+      const long long at = (p.form == kWgrad ? t.g * p.c_stride : 0) + row0 * p.c_ld + n;
       const int count = n < p.N ? t.qn - c0 : 0;  // this lane's columns
-#pragma unroll 1
-      for (int c = 0; c < 128 && c0 + c < t.qn; c += 16) {
-        float f[16];
+
+      // Sixteen columns from TMEM.
+      auto load = [&](int c, float (&f)[16]) {
         if (blocks > 0) {
           uint32_t v[16];
           tmem_load_16cols(tlane + acc.idx * kCols + c, v);
           tmem_load_wait();
           tmem_regs_ready(v);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = scale * __uint_as_float(v[k]);
+          for (int k = 0; k < 16; ++k) f[k] = __uint_as_float(v[k]);
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) f[k] = 0.0f;
         }
+      };
+      // Sixteen columns of the result, from c of this warp's on.
+      auto finish = [&](int c, float (&f)[16]) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) f[k] *= scale;
         if (p.add != nullptr) {  // sixteen loads in flight
           const long long from = row0 * p.add_ld + n;
           float a[16];
@@ -918,7 +873,7 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
               // One box of sixteen rows (as a copy for each row, 256 bytes at
               // a time, results left at 2 TB/s).
               if (lane == 0 && width > 0)
-                store_box(&map_c, to, n_cta, t.q0 + c0 + c, p.wgrad ? t.g : 0);
+                store_box(&maps.c, to, n_cta, t.q0 + c0 + c, p.form == kWgrad ? t.g : 0);
             } else {  // the segment ends here
               const int row = c + static_cast<int>(lane);
               const long long off = at - n + n_cta + row * p.c_ld;
@@ -955,6 +910,61 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
             }
           }
         }
+      };
+
+      const int c_end = min(128, t.qn - c0);
+      bool write = true;
+      if (tab.splits > 1) {
+        // This item's sums to its slot; the item that completes the tile adds
+        // them all, always in the same order.
+        constexpr long long kSlotCta = static_cast<long long>(kCols) * kHalf;
+        const long long mine = static_cast<long long>(rank) * kSlotCta +
+                               static_cast<long long>(c0) * kHalf + quad * 32 + lane;
+        auto slot = [&](int s, int c) {
+          return (static_cast<long long>(t.index) * tab.splits + s) * 2 * kSlotCta + mine +
+                 static_cast<long long>(c) * kHalf;
+        };
+        const int own = t.item - t.index * tab.splits;
+#pragma unroll 1
+        for (int c = 0; c < c_end; c += 16) {
+          float f[16];
+          load(c, f);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (index_ok(kSitePartialWrite, slot(own, c + k), 1, p.slot_extent))
+              p.slots[slot(own, c + k)] = f[k];
+        }
+        __threadfence();
+        named_barrier_sync(1, 32 * C::kEpiWarps);
+        if (threadIdx.x == 32 * C::kEpiWarp0) {
+          const unsigned before = atomicAdd(&p.arrived[t.index * 2 + static_cast<int>(rank)], 1u);
+          sh->last = before + 1 == static_cast<unsigned>(tab.splits);
+        }
+        named_barrier_sync(1, 32 * C::kEpiWarps);
+        write = sh->last != 0;
+        if (write) {
+          __threadfence();
+#pragma unroll 1
+          for (int c = 0; c < c_end; c += 16) {
+            float f[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[k] = 0.0f;
+#pragma unroll 2
+            for (int s = 0; s < tab.splits; ++s)
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (index_ok(kSitePartialRead, slot(s, c + k), 1, p.slot_extent))
+                  f[k] += __ldcg(p.slots + slot(s, c + k));
+            finish(c, f);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < c_end; c += 16) {
+          float f[16];
+          load(c, f);
+          finish(c, f);
+        }
       }
       if (blocks > 0) {
         drained(acc.idx, true);
@@ -962,120 +972,65 @@ __global__ void __launch_bounds__(Cfg<T, TMA>::kThreads, 1)
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  } else if (loader) {
-    // -------------------------------------------------------- plain loads --
+  } else if (C::kSplit && warp >= C::kLoadWarp0) {
+    // -------------------------------------------------- float32 to terms --
+    // Split the values that have arrived: eight a lane, four lanes to a line
+    // of 32. Lanes 4 to 7 of each eight take the line 5 away (k ^ 5), whose
+    // swizzled pieces lie in the other banks, as read and as written.
     set_registers<C::kSplit, 64>();
-    // Both operands are masked here, by row and by column.
-    const int lw = static_cast<int>(warp) - C::kLoadWarp0;
-    Ring<STAGES> r;
-    bool ok = true;
-    // The CTA's part of a stage is written: one release at cluster scope for
-    // all its load warps (a thread of the odd CTA that waited for their
-    // arrivals and passed them on was 375 ns of every stage's way).
-    const uint32_t full0 = mbar_cluster_addr(&sh->full[0], 0);
-    // False if a warp gave up on a wait; each comes here once a stage.
-    auto filled = [&](uint32_t s, bool ok) {
-      fence_proxy_async_smem();
-      ok = named_barrier_and(2, 32 * C::kLoadWarps, ok);
-      if (ok && threadIdx.x == 32 * C::kLoadWarp0) mbar_arrive_at(full0 + s * 8);
-      return ok;
-    };
     if constexpr (C::kSplit) {
-      // Split the values that have arrived: eight a lane, four lanes to a line
-      // of 32. Lanes 4 to 7 of each eight take the line 5 away (k ^ 5), whose
-      // swizzled pieces lie in the other banks, as read and as written.
+      const int lw = static_cast<int>(warp) - C::kLoadWarp0;
       const int g = static_cast<int>(lane) >> 2, j = static_cast<int>(lane) & 3;
       const int k8 = (g >> 1) ^ ((g & 1) * 5);  // line within eight
+      Ring<STAGES> r;
       Ring<C::kRawStages> a;
+      const uint32_t full0 = mbar_cluster_addr(&sh->full[0], 0);
+      bool ok = true;
       for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
         const int half = mma_cols<QMN>(t) / 2;
-        for (int kk = 0; kk < t.klen; kk += kBK) {
-          ok = warp_wait(&sh->raw_full[a.idx], a.phase, p, abort) &&
-               warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort);
-          const uint8_t *from = raw + a.idx * 2 * C::kRawOpBytes;
-          uint8_t *to = stages + r.idx * C::kStageBytes;
+        ok = for_passes(p, t, [&](int, int len, int k_lo, int k_hi) {
+          for (int kk = k_lo; kk < k_hi; kk += kBK) {
+            bool ready = warp_wait(&sh->raw_full[a.idx], a.phase, p, abort) &&
+                         warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort);
+            const uint8_t *from = raw + a.idx * 2 * C::kRawOpBytes;
+            uint8_t *to = stages + r.idx * C::kStageBytes;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const bool mn = u < 2 ? LMN : QMN;
-            const int line = ((u & 1) * 8 + lw) * 8 + k8;  // MN-major: chunk * 32 + k
-            // K-major Q: rows; MN-major: chunks of 32 columns.
-            if (!ok || (u >= 2 && (QMN ? line : line & ~7) >= half)) continue;
-            const uint8_t *src = from + (u < 2 ? 0 : C::kRawOpBytes) + line * 128;
-            float v[8];
-            *reinterpret_cast<float4 *>(v) =
-                *reinterpret_cast<const float4 *>(src + ((2 * j) ^ k8) * 16);
-            *reinterpret_cast<float4 *>(v + 4) =
-                *reinterpret_cast<const float4 *>(src + ((2 * j + 1) ^ k8) * 16);
-            if (QMN && kk + (line & 31) >= t.klen) {  // the next segment's row
+            for (int u = 0; u < 4; ++u) {
+              const bool mn = u < 2 ? LMN : QMN;
+              const int line = ((u & 1) * 8 + lw) * 8 + k8;  // MN-major: chunk * 32 + k
+              // K-major Q: rows; MN-major: chunks of 32 columns.
+              if (!ready || (u >= 2 && (QMN ? line : line & ~7) >= half)) continue;
+              const uint8_t *src = from + (u < 2 ? 0 : C::kRawOpBytes) + line * 128;
+              float v[8];
+              *reinterpret_cast<float4 *>(v) =
+                  *reinterpret_cast<const float4 *>(src + ((2 * j) ^ k8) * 16);
+              *reinterpret_cast<float4 *>(v + 4) =
+                  *reinterpret_cast<const float4 *>(src + ((2 * j + 1) ^ k8) * 16);
+              if (QMN && kk + (line & 31) >= len) {  // the next segment's row
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-            }
-            uint8_t *dst = to + (u < 2 ? 0 : C::kTerms * kOpBytes);
-            if (mn)  // line k of a chunk of 64, in its first or second half
-              dst += (line >> 6) * (kBK * 128) + (line & 31) * 128 +
-                     ((((line >> 5 & 1) * 4 + j) ^ k8) * 16);
-            else
-              dst += line * 64 + ((j ^ (k8 >> 1 & 3)) * 16);
-            store_terms(dst, kOpBytes, v);
-          }
-          ok = filled(r.idx, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(&sh->raw_empty[a.idx]);
-          a.next();
-          r.next();
-        }
-      }
-    } else if constexpr (!TMA) {
-      // Eight lanes to a line of 64 elements, four lines a warp and load.
-      const int sub = static_cast<int>(lane) >> 3, j = static_cast<int>(lane) & 7;
-      for (int i = pair; ok && tile_at(p, tab, i, t); i += pairs) {
-        const int half = mma_cols<QMN>(t) / 2;
-        const int ln = t.n0 + static_cast<int>(rank) * kHalf;
-        const int qn = static_cast<int>(rank) * half;  // within the tile
-        const int blocks = cdiv(t.klen, kBK);
-        for (int kb = 0; kb < blocks * p.passes; ++kb) {
-          const int second = kb >= blocks, kk = (second ? kb - blocks : kb) * kBK;
-          uint8_t *st = stages + r.idx * C::kStageBytes;
-#pragma unroll
-          for (int op = 0; op < 2; ++op) {
-            const SegOperand &o = op == 0 ? p.L : p.Q;
-            const bool mn = op == 0 ? LMN : QMN;
-            const T *src = static_cast<const T *>(second ? o.p[1] : o.p[0]);
-            const int site = op == 0 ? kSiteLoadB : kSiteLoadA;
-            const long long z = op == 0 ? t.z * o.zs : 0;
-            uint4 e[4];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const int line = s * 32 + lw * 4 + sub;
-              long long row;
-              int x, limit;
-              if (mn) {  // line: k; elements: lanes or columns
-                const int k = kk + (line & 63);
-                x = (op == 0 ? ln : t.q0 + qn) + (line >> 6) * 64 + j * 8;
-                limit = k < t.klen ? (op == 0 ? p.N : p.K) : 0;
-                if (op == 1 && (line >> 6) * 64 >= half) limit = 0;
-                row = z + static_cast<long long>(t.k0 + k) * o.ld;
-              } else {
-                const int m = op == 0 ? ln + line : qn + line;
-                x = kk + j * 8;
-                limit = (op == 0 ? m < p.N : line < half && m < t.qn) ? p.K : 0;
-                row = z + static_cast<long long>(op == 0 ? m : t.q0 + m) * o.ld;
+                for (int e = 0; e < 8; ++e) v[e] = 0.0f;
               }
-              e[s] = load_eight(o, src, site, row, x, limit);
+              uint8_t *dst = to + (u < 2 ? 0 : C::kTerms * kOpBytes);
+              if (mn)  // line k of a chunk of 64, in its first or second half
+                dst += (line >> 6) * (kBK * 128) + (line & 31) * 128 +
+                       ((((line >> 5 & 1) * 4 + j) ^ k8) * 16);
+              else
+                dst += line * 64 + ((j ^ (k8 >> 1 & 3)) * 16);
+              store_terms(dst, kOpBytes, v);
             }
-            if (op == 0) ok = warp_wait(&sh->empty[r.idx], r.phase ^ 1, p, abort);
-#pragma unroll
-            for (int s = 0; ok && s < 4; ++s) {
-              const int line = s * 32 + lw * 4 + sub;
-              if (op == 1 && !mn && line >= half) continue;  // no MMA column
-              *reinterpret_cast<uint4 *>(st + op * kOpBytes + line * 128 + (j ^ (line & 7)) * 16) =
-                  e[s];
-            }
+            // The CTA's part of the stage is written: one release for all its
+            // load warps (a thread of the odd CTA that waited for their
+            // arrivals and passed them on was 375 ns of every stage's way).
+            // Each warp comes here once a stage; false if one gave up.
+            fence_proxy_async_smem();
+            if (!named_barrier_and(2, 32 * C::kLoadWarps, ready)) return false;
+            if (threadIdx.x == 32 * C::kLoadWarp0) mbar_arrive_at(full0 + r.idx * 8);
+            if (lane == 0) mbar_arrive(&sh->raw_empty[a.idx]);
+            a.next();
+            r.next();
           }
-          ok = filled(r.idx, ok);
-          if (!ok) break;
-          r.next();
-        }
+          return true;
+        });
       }
     }
   } else {
@@ -1114,112 +1069,64 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Map over a stack of row-major matrices, zero outside each: lines of 128 bytes
-// (64 bf16 or 32 float32 columns), `lines` rows a copy; chunks > 1: the same
-// seen as chunks of one line's columns (a multiple of them, so that no chunk
-// leaves its row), that many a copy.
-bool encode_lines(const SegMatrix &m, const void *ptr, bool bf16, int lines, int chunks,
-                  CUtensorMap *out) {
+// Map over a stack of row-major matrices (one, where its matrices are the same),
+// zero outside each: boxes of `box0` columns by `box1` rows; chunks > 1: the
+// same seen as chunks of box0 columns (a multiple of them, so that no chunk
+// leaves its row), that many a box.
+bool encode(const SegMatrix &m, bool bf16, int box0, int box1, int chunks,
+            bool swizzle, CUtensorMap *out) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t elem = bf16 ? 2 : 4;
-  const cuuint32_t line = bf16 ? 64 : 32;
   const bool stack = m.count > 1 && m.stride > 0;
   const cuuint64_t pitch = static_cast<cuuint64_t>(m.ld) * elem;
   const cuuint64_t next = stack ? static_cast<cuuint64_t>(m.stride) * elem : pitch;
   const cuuint64_t count = static_cast<cuuint64_t>(stack ? m.count : 1);
   const cuuint64_t rows = static_cast<cuuint64_t>(m.rows), cols = static_cast<cuuint64_t>(m.cols);
-  const cuuint32_t height = static_cast<cuuint32_t>(lines);
   cuuint64_t dims[4] = {cols, rows, count, 1}, strides[3] = {pitch, next, 0};
-  cuuint32_t box[4] = {line, height, 1, 1};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1, 1};
   const cuuint32_t step[4] = {1, 1, 1, 1};
   if (chunks > 1) {
-    dims[0] = line;
-    dims[2] = cols / line;
+    dims[0] = box[0];
+    dims[2] = cols / box[0];
     dims[3] = count;
     strides[1] = 128;
     strides[2] = next;
     box[2] = static_cast<cuuint32_t>(chunks);
   }
   return fn(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-            chunks > 1 ? 4 : 3, const_cast<void *>(ptr), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            chunks > 1 ? 4 : 3, const_cast<void *>(m.p), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Map of the results: boxes of 128 columns by 16 rows, not swizzled.
-bool encode_result(const SegMatrix &m, bool f32, CUtensorMap *out) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t elem = f32 ? 4 : 2, pitch = static_cast<cuuint64_t>(m.ld) * elem;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(m.cols), static_cast<cuuint64_t>(m.rows),
-                              static_cast<cuuint64_t>(m.count)};
-  const cuuint64_t strides[2] = {
-      pitch, m.count > 1 ? static_cast<cuuint64_t>(m.stride) * elem : pitch};
-  const cuuint32_t box[3] = {kHalf, 16, 1}, step[3] = {1, 1, 1};
-  return fn(out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-            const_cast<void *>(m.p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// TMA reads 16-byte aligned rows; a stride of zero (one matrix for all) is not
-// a stride of its maps.
-bool tma_ok(const SegMatrix &m, const void *p, int elem) {
-  const int per16 = 16 / elem;
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && m.ld % per16 == 0 && m.stride % per16 == 0 &&
-         (m.count <= 1 || m.stride > 0);
 }
 
 long long extent_of(const SegMatrix &m) {
   return (m.count - 1) * m.stride + matrix_extent(m.rows, m.cols, m.ld);
 }
 
-SegOperand operand_of(const SegMatrix &m, const void *second, int elem) {
-  SegOperand o;
-  o.p[0] = m.p;
-  o.p[1] = second != nullptr ? second : m.p;
-  o.ld = m.ld;
-  o.zs = m.stride;
-  o.extent = extent_of(m);
-  const uintptr_t at = reinterpret_cast<uintptr_t>(o.p[0]) | reinterpret_cast<uintptr_t>(o.p[1]);
-  const int per16 = 16 / elem;
-  o.vec = at % 16 == 0 && m.ld % per16 == 0 && m.stride % per16 == 0;
-  return o;
-}
-
-template <class T, bool TMA, bool LMN, bool QMN>
-int launch(const CUtensorMap (&maps)[5], const SegTc &p, int sm_count, cudaStream_t stream) {
-  using C = Cfg<T, TMA>;
-  auto *kernel = seg_tc_kernel<T, TMA, LMN, QMN>;
-  const int groups = p.dense ? 1 : p.groups;
+template <class T, bool LMN, bool QMN>
+int launch(const SegMaps &maps, const SegTc &p, int pairs, cudaStream_t stream) {
+  using C = Cfg<T>;
+  auto *kernel = seg_tc_kernel<T, LMN, QMN>;
   const int fixed = C::kStages * C::kStageBytes + C::kRawBytes + 2 * C::kOutBytes +
                     static_cast<int>(sizeof(Shared<C::kStages, C::kRawStages>)) + 1024;
-  const int smem = fixed + groups * 8 + 8;
+  auto smem = [fixed](int entries) { return fixed + 8 * entries + 8; };
   static std::once_flag once;
   static bool ready = false;
   std::call_once(once, [&] {
     cudaFuncAttributes at;
     ready = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 fixed + kMaxSegments * 8 + 8) == cudaSuccess &&
+                                 smem(kMaxSegments + 2)) == cudaSuccess &&
             cudaFuncGetAttributes(&at, kernel) == cudaSuccess &&
             // the register split draws on the launch's registers
             (!C::kSplit || at.numRegs * C::kThreads >= 128 * 40 + 256 * 152 + 256 * 64);
   });
   if (!ready) return kErrLaunch;
-  // Tiles at most: every segment may end in a part tile.
-  const long long height = p.wgrad ? p.K : p.M;
-  long long tiles = p.wgrad ? static_cast<long long>(groups) * ((height + kCols - 1) / kCols)
-                            : height / kCols + (p.dense ? 1 : groups);
-  tiles *= p.tiles_n;
-  if (tiles > 0x7fffffffLL) return kErrInvalidArg;
-  long long pairs = sm_count / 2;
-  if (pairs > tiles) pairs = tiles;
-  if (pairs < 1) pairs = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem(p.entries));
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1230,17 +1137,15 @@ int launch(const CUtensorMap (&maps)[5], const SegTc &p, int sm_count, cudaStrea
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p) == cudaSuccess
-             ? kOk
-             : kErrLaunch;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p) == cudaSuccess ? kOk : kErrLaunch;
 }
 
-template <class T, bool TMA>
-int launch_layout(bool lmn, bool qmn, const CUtensorMap (&maps)[5], const SegTc &p, int sm_count,
+template <class T>
+int launch_layout(bool lmn, bool qmn, const SegMaps &maps, const SegTc &p, int pairs,
                   cudaStream_t stream) {
-  if (qmn) return launch<T, TMA, true, true>(maps, p, sm_count, stream);
-  if (lmn) return launch<T, TMA, true, false>(maps, p, sm_count, stream);
-  return launch<T, TMA, false, false>(maps, p, sm_count, stream);
+  if (qmn) return launch<T, true, true>(maps, p, pairs, stream);
+  if (lmn) return launch<T, true, false>(maps, p, pairs, stream);
+  return launch<T, false, false>(maps, p, pairs, stream);
 }
 
 }  // namespace
@@ -1256,16 +1161,26 @@ int seg_tc_poll_status(cudaStream_t stream) {
   return h;
 }
 
+bool seg_tc_readable(const SegMatrix &m, bool bf16) {
+  const int per16 = bf16 ? 8 : 4;
+  return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % per16 == 0 &&
+         (m.count <= 1 || m.stride % per16 == 0);
+}
+
 int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   SegTc p = {};
-  p.wgrad = a.wgrad;
-  p.dense = a.dense;
+  const bool adapted = a.R > 0;
+  p.form = a.wgrad ? kWgrad : (adapted ? kAdapted : (a.dense ? kDense : kRows));
   p.groups = static_cast<int>(a.groups);
+  p.entries = p.form == kDense ? 1 : p.groups + (adapted ? 2 : 0);
   p.M = static_cast<int>(a.M);
   p.N = static_cast<int>(a.N);
   p.K = static_cast<int>(a.K);
+  p.R = static_cast<int>(a.R);
   p.bank = static_cast<int>(a.bank);
-  p.passes = a.A_lo != nullptr || a.B_lo != nullptr ? 2 : 1;
+  p.z_step = a.B.count > 1 && a.B.stride == 0 ? 0 : 1;
+  const bool two_terms = a.A_lo.p != nullptr || a.B_lo.p != nullptr;
+  p.passes = adapted ? (a.U_lo.p != nullptr ? 3 : 2) : (two_terms ? 2 : 1);
   p.tiles_n = static_cast<int>((a.N + kLanes - 1) / kLanes);
   p.offsets = a.offsets;
   p.index = a.index;
@@ -1286,41 +1201,74 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   p.c_lo_extent = extent_of(a.C_lo);
   // 2 s, and 2 us for each k of the longest contraction.
   p.timeout_ns = 2000000000ull + 2000ull * static_cast<unsigned long long>(a.wgrad ? a.M : a.K);
-  // Lines per copy of Q: about half a tile's rows, as the average segment has
-  // them, so that small segments do not read their neighbours' rows.
-  const long long average = p.dense ? a.M : a.M / (a.groups > 0 ? a.groups : 1);
-  p.q_box = average <= 64 ? 32 : (average <= 128 ? 64 : 128);
+
+  // The tiles there are at most (every segment may end in a part tile, and the
+  // narrowest is 64 columns), and at least, if the segments hold all rows.
+  const long long height = a.wgrad ? a.K : a.M;
+  const long long most = ((a.wgrad ? p.entries * ((height + 127) / 128) : height / 64 + p.entries)) *
+                         p.tiles_n;
+  const long long least =
+      (a.wgrad ? p.entries : 1) * ((height + kCols - 1) / kCols) * p.tiles_n;
+  if (most > 0x7fffffffLL) return kErrInvalidArg;
+  int pairs = sm_count / 2;
+  if (pairs < 1) pairs = 1;
+  // Lines per copy of a K-major Q: about half a tile's rows, so that small
+  // segments and narrow tiles do not read their neighbours' rows.
+  const long long average = p.form == kRows ? a.M / (a.groups > 0 ? a.groups : 1) : a.M;
+  p.q_box = average <= 64 ? 32 : (average <= 128 || least < pairs ? 64 : 128);
+
   const bool lmn = a.wgrad || !a.transb, qmn = a.wgrad;
-  const int elem = a.bf16 ? 2 : 4;
-  p.L = operand_of(a.B, a.B_lo, elem);
-  p.Q = operand_of(a.A, a.A_lo, elem);
-  CUtensorMap maps[5];
-  std::memset(maps, 0, sizeof(maps));
-  const bool empty = a.K == 0 || a.M == 0;  // no operand is read
-  const bool tma = !empty && tma_ok(a.B, p.L.p[0], elem) && tma_ok(a.B, p.L.p[1], elem) &&
-                   tma_ok(a.A, p.Q.p[0], elem) && tma_ok(a.A, p.Q.p[1], elem);
-  if (tma) {
-    const int line = 128 / elem, bk = a.bf16 ? 64 : 32;
-    const int l_lines = lmn ? bk : kHalf, q_lines = qmn ? bk : p.q_box;
-    // One copy of all chunks, where every tile has them all: lanes always do.
-    p.l_whole = lmn && a.N % line == 0;
-    p.q_whole = qmn && a.K % kCols == 0;
-    const int lc = p.l_whole ? kHalf / line : 1, qc = p.q_whole ? kHalf / line : 1;
-    if (!encode_lines(a.B, p.L.p[0], a.bf16, l_lines, lc, &maps[0]) ||
-        !encode_lines(a.A, p.Q.p[0], a.bf16, q_lines, qc, &maps[2]))
-      return kErrLaunch;
-    maps[1] = maps[0];
-    maps[3] = maps[2];
-    if ((a.B_lo != nullptr && !encode_lines(a.B, a.B_lo, a.bf16, l_lines, lc, &maps[1])) ||
-        (a.A_lo != nullptr && !encode_lines(a.A, a.A_lo, a.bf16, q_lines, qc, &maps[3])))
-      return kErrLaunch;
+  const int line = a.bf16 ? 64 : 32, bk = a.bf16 ? 64 : 32;
+  SegMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  auto encode_l = [&](const SegMatrix &m, int *whole, CUtensorMap *out) {
+    // One copy of all chunks of the lanes' operand where no chunk leaves its row.
+    *whole = lmn && m.cols % line == 0;
+    return encode(m, a.bf16, line, lmn ? bk : kHalf, *whole ? kHalf / line : 1, true, out);
+  };
+  auto encode_q = [&](const SegMatrix &m, CUtensorMap *out) {
+    return encode(m, a.bf16, line, qmn ? bk : p.q_box, 1, true, out);
+  };
+  if (a.K > 0 && a.M > 0) {  // else no operand is read
+    if (!seg_tc_readable(a.A, a.bf16) || !seg_tc_readable(a.B, a.bf16)) return kErrInvalidArg;
+    bool ok = encode_l(a.B, &p.l_whole, &maps.l[0]) && encode_q(a.A, &maps.q[0]);
+    if (adapted) {
+      ok = ok && encode_l(a.L, &p.l_whole1, &maps.l[1]) &&
+           encode_q(a.U, &maps.q[1]);
+      maps.l[2] = maps.l[1];
+      if (ok && a.U_lo.p != nullptr) ok = encode_q(a.U_lo, &maps.q[2]);
+    } else if (two_terms) {
+      maps.l[1] = maps.l[0];
+      maps.q[1] = maps.q[0];
+      if (ok && a.B_lo.p != nullptr) ok = encode_l(a.B_lo, &p.l_whole1, &maps.l[1]);
+      if (ok && a.A_lo.p != nullptr) ok = encode_q(a.A_lo, &maps.q[1]);
+    }
+    if (!ok) return kErrLaunch;
   }
-  if (p.c_rows && !encode_result(a.C, p.c_f32, &maps[4])) return kErrLaunch;
-  if (a.bf16)
-    return tma ? launch_layout<__nv_bfloat16, true>(lmn, qmn, maps, p, sm_count, stream)
-               : launch_layout<__nv_bfloat16, false>(lmn, qmn, maps, p, sm_count, stream);
-  return tma ? launch_layout<float, true>(lmn, qmn, maps, p, sm_count, stream)
-             : launch_layout<float, false>(lmn, qmn, maps, p, sm_count, stream);
+  if (p.c_rows && !encode(a.C, !p.c_f32, kHalf, 16, 1, false, &maps.c)) return kErrLaunch;
+
+  // Slots for splitting, where there can be few enough tiles and enough k.
+  void *work = nullptr;
+  if (least * 2 <= pairs && (a.wgrad ? a.M : a.K) * p.passes >= 8 * kBlock) {
+    const size_t counters = (static_cast<size_t>(2 * pairs) * sizeof(unsigned) + 255) / 256 * 256;
+    const size_t slots = static_cast<size_t>(pairs) * 2 * kCols * kHalf;
+    const int st = pool_alloc(&work, counters + slots * sizeof(float), stream);
+    if (st != kOk) return st;
+    p.arrived = static_cast<unsigned *>(work);
+    p.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(work) + counters);
+    p.slot_extent = static_cast<long long>(slots);
+    if (cudaMemsetAsync(work, 0, counters, stream) != cudaSuccess) {
+      pool_free(work, stream);
+      return kErrLaunch;
+    }
+  } else if (pairs > most) {
+    pairs = most > 0 ? static_cast<int>(most) : 1;
+  }
+  const int st = a.bf16 ? launch_layout<__nv_bfloat16>(lmn, qmn, maps, p, pairs, stream)
+                        : launch_layout<float>(lmn, qmn, maps, p, pairs, stream);
+  if (work == nullptr) return st;
+  const int fst = pool_free(work, stream);
+  return st != kOk ? st : fst;
 }
 
 }  // namespace gemm

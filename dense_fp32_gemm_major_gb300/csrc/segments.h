@@ -22,29 +22,49 @@ struct SegMatrix {
 // One segmented product. The result's rows are tokens (wgrad = false) or a
 // matrix for each segment (wgrad = true):
 //
-//   rows:   C[t, :] = scale_z A[t, :] op(B_z)  for the rows t of segment g,
-//           z = index[g] (or g); dense: all M rows with B_0, plus `add`
-//   wgrad:  C_g = A_g^T B_g, the sum over the rows of segment g
+//   rows:     C[t, :] = scale_z A[t, :] op(B_z)  for the rows t of segment g,
+//             z = index[g] (or g)
+//   dense:    all M rows with B_0, plus `add` in the segments' rows
+//   adapted:  (R > 0) all M rows with B_0, plus U[t, :] op(L_a) for the rows t
+//             of segment g, a = index[g] (or g)
+//   wgrad:    C_g = A_g^T B_g, the sum over the rows of segment g
 struct SegArgs {
   bool bf16 = false, wgrad = false, dense = false;
   int64_t groups = 0, M = 0, N = 0, K = 0;
   SegMatrix A, B, C;
-  int transb = 0;
+  int transb = 0;  // of B, and of L
   const int64_t *offsets = nullptr;
   const int32_t *index = nullptr;
   const float *scales = nullptr;
-  int64_t bank = 0;  // matrices z may name; others: no product
-  // Second terms of A and B (same layout; the sum A + A_lo, or B + B_lo, is
-  // meant; at most one of them), and of the result: C + C_lo, C rounded.
-  const void *A_lo = nullptr, *B_lo = nullptr;
-  SegMatrix C_lo;
+  int64_t bank = 0;  // matrices the index may name; others: no product
+  // Second terms of A and B (the sum A + A_lo, or B + B_lo, is meant; at most
+  // one of them), and of the result: C + C_lo, C rounded.
+  SegMatrix A_lo, B_lo, C_lo;
   bool c_f32 = false;  // a float32 result of bf16 operands
   SegMatrix add;       // dense: float32 addend of the result
+  int64_t R = 0;       // adapted: width of U
+  SegMatrix U, U_lo, L;
 };
 
-// Requires M, N >= 1 (rows) or groups, N, K >= 1 (wgrad).
+// Whether the kernels can read a matrix as it lies (by TMA: 16-byte aligned
+// rows). Others are copied first (seg_pack_launch).
+bool seg_tc_readable(const SegMatrix &m, bool bf16);
+
+// Operands readable; M, N >= 1 (rows) or groups, N, K >= 1 (wgrad).
 int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
 
+// Copies a stack of matrices, of equal shape, to another pitch and stride.
+// offsets: only rows that the segments hold (by_matrix: only the matrices of
+// segments that have rows).
+struct SegCopy {
+  SegMatrix src, dst;
+  const int64_t *offsets = nullptr;
+  int64_t groups = 0, M = 0;
+  bool by_matrix = false;
+};
+int seg_pack_launch(const SegCopy &c, bool bf16, int sm_count, cudaStream_t stream);
+
+int seg_pack_index_fault_take(IndexFault *out, bool clear);
 int seg_tc_index_fault_take(IndexFault *out, bool clear);
 
 // Synchronise `stream`, then read and clear the kernels' status word.
