@@ -80,6 +80,7 @@ struct SegTc {
   int passes;
   int tiles_n;
   int q_box;         // lines per copy of a K-major Q
+  int q_whole;       // wgrad, one pass: maps.q[2] brings all chunks of Q in one copy
   int l_whole, l_whole1;  // the MN-major L of pass 0, of the others, comes as one 4-D copy
   const int64_t *offsets;
   const int32_t *index;
@@ -91,9 +92,9 @@ struct SegTc {
   int c_rows;        // rows of the result can leave by TMA
   long long c_ld, c_lo_ld, c_stride, c_extent, c_lo_extent;
   // Few tiles: the blocks of each go to several pairs, which leave their sums
-  // in slots (one a work item, 2 x 256 x 128 floats); the last one adds them.
+  // in slots (one a work item, at most as many as pairs, 2 x 256 x 128 floats); the last one adds them.
   float *slots;
-  unsigned *arrived;  // [2 tile + rank], zero
+  unsigned *arrived;  // [2 tile + rank] of the split tiles, zero
   long long slot_extent;
   unsigned long long timeout_ns;
 };
@@ -138,7 +139,7 @@ struct Shared {
 // One work item -- a tile of the list, or a part of its blocks -- as every role
 // sees it.
 struct Tile {
-  int item, index;  // of the list; tile
+  int over, tile;   // split tiles: item and tile past the whole ones
   int g, z;         // segment; its matrix
   int a;            // adapted: the segment's adapter
   int n0;           // first lane (result column)
@@ -146,6 +147,7 @@ struct Tile {
   int k0;           // wgrad: first row of the contraction
   int klen, xlen;   // k of the first pass, of each of the others
   int b0, b1;       // blocks to sum, counted through the passes
+  bool split;       // others sum other blocks of the tile
 };
 
 struct SegMaps {
@@ -156,7 +158,8 @@ struct Table {
   int *first;     // [entries + 1] tiles of the entries before
   int *row;       // [entries + 1] offsets, held to the rows there are
   int width;      // most columns of a tile
-  int splits;     // work items per tile
+  int whole;      // tiles that are one work item each; the others are
+  int splits;     // this many
 };
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -181,7 +184,8 @@ __device__ __forceinline__ bool for_passes(const SegTc &p, const Tile &t, const 
 }
 
 __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int item, Tile &o) {
-  const int t = tab.splits > 1 ? item / tab.splits : item;
+  const int over = item - tab.whole;
+  const int t = over < 0 ? item : tab.whole + over / tab.splits;
   if (t >= tab.first[p.entries]) return false;
   int lo = 0, hi = p.entries;  // the entry whose tiles hold t
   while (hi - lo > 1) {
@@ -207,8 +211,8 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
   // traffic and no work.
   const int step = p.form == kWgrad ? 128 : kColStep;
   const int part = cdiv(cdiv(height, tm), step) * step;
-  o.item = item;
-  o.index = t;
+  o.over = over;
+  o.tile = t - tab.whole;
   o.g = lo;
   o.n0 = ni * kLanes;
   o.qn = min(part, height - mi * part);
@@ -231,8 +235,9 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
     }
   }
   const int blocks = cdiv(o.klen, kBlock) + (p.passes - 1) * cdiv(o.xlen, kBlock);
-  if (tab.splits > 1) {
-    const int s = item - t * tab.splits;
+  o.split = over >= 0 && tab.splits > 1;
+  if (o.split) {
+    const int s = over - (t - tab.whole) * tab.splits;
     o.b0 = static_cast<int>(static_cast<long long>(blocks) * s / tab.splits);
     o.b1 = static_cast<int>(static_cast<long long>(blocks) * (s + 1) / tab.splits);
   } else {
@@ -243,30 +248,37 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
 }
 
 // How the list is cut, from its tiles at each width (every CTA finds the same).
-// Fewer tiles than pairs leave pairs idle, and a list a little longer than a
-// multiple of them leaves most idle in the last round, so a narrower tile is
-// taken where the rounds it makes are shorter: a round costs its columns and
-// about 96 more (copies of the lanes' operand and hand-overs; a round of 256
-// columns takes 2.2 times one of 64). Tiles that still leave half the pairs
-// idle are split along k, into at least four blocks an item.
+// A round of tiles takes nearly the same time at every width (a block of 64 k
+// and 256, 128, 64 columns: bf16 302, 282, 275 ns, float32 1.99, 1.72, 1.55 us),
+// so narrower tiles pay only where they fill pairs that would be idle. Tiles
+// past the last full round that leave half the pairs idle are split along k, at
+// least four blocks an item.
+template <bool SPLIT>
 __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int longest, int pairs,
                                            Table &tab) {
-  int best = 0, cost = 0x7fffffff;
+  constexpr long long kFixed = SPLIT ? 640 : 1800;  // of a round, in columns
+  int best = 0;
+  long long cost = 0;
   for (int i = 0; i < (p.form == kWgrad ? 2 : 3); ++i) {
-    if (i > 0 && tiles[i] == tiles[i - 1]) continue;
-    const int c = min(cdiv(tiles[i], pairs), 1 << 20) * ((kCols >> i) + 96);
-    if (c < cost) {
+    const long long c = cdiv(tiles[i], pairs) * ((kCols >> i) + kFixed);
+    if (i == 0 || (c < cost && tiles[i] != tiles[best])) {
       cost = c;
       best = i;
     }
   }
   tab.width = kCols >> best;
-  tab.splits = 1;
   const int n = tiles[best];
-  if (p.slots != nullptr && n > 0 && n * 2 <= pairs) {
+  tab.whole = n;
+  tab.splits = 1;
+  if (p.slots != nullptr) {
+    const int rest = n % pairs;
     const int k = p.form == kWgrad ? longest : p.K;
-    const int blocks = p.passes * cdiv(k, kBlock);
-    tab.splits = max(min(min(pairs / n, blocks / 4), kMaxSplits), 1);
+    const int splits =
+        rest > 0 ? min(min(pairs / rest, p.passes * cdiv(k, kBlock) / 4), kMaxSplits) : 1;
+    if (splits > 1) {
+      tab.whole = n - rest;
+      tab.splits = splits;
+    }
   }
 }
 
@@ -519,7 +531,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     atomicMax(&sh->longest, rows);
   }
   __syncthreads();
-  choose_cut(p, sh->tiles, sh->longest, pairs, tab);
+  choose_cut<C::kSplit>(p, sh->tiles, sh->longest, pairs, tab);
   if (warp == 0) {
     int sum = 0;
     for (int g0 = 0; g0 < p.entries; g0 += 32) {
@@ -603,6 +615,12 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
 #pragma unroll
               for (int c = 0; c < kHalf / kLine; ++c)
                 tma_load_3d_pair(l + c * kChunk, ml, bar, ln + c * kLine, t.k0 + kk, lz);
+            }
+            if (QMN && p.q_whole && half == kHalf) {
+              tma_load_4d_pair(q, &maps.q[2], bar, 0, t.k0 + kk, qn / kLine, 0);
+              ++issued;
+              r.next();
+              continue;
             }
             for (int c = 0; c < copies; ++c) {
               if (QMN)
@@ -914,17 +932,17 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
 
       const int c_end = min(128, t.qn - c0);
       bool write = true;
-      if (tab.splits > 1) {
+      if (t.split) {
         // This item's sums to its slot; the item that completes the tile adds
         // them all, always in the same order.
         constexpr long long kSlotCta = static_cast<long long>(kCols) * kHalf;
         const long long mine = static_cast<long long>(rank) * kSlotCta +
                                static_cast<long long>(c0) * kHalf + quad * 32 + lane;
         auto slot = [&](int s, int c) {
-          return (static_cast<long long>(t.index) * tab.splits + s) * 2 * kSlotCta + mine +
+          return (static_cast<long long>(t.tile) * tab.splits + s) * 2 * kSlotCta + mine +
                  static_cast<long long>(c) * kHalf;
         };
-        const int own = t.item - t.index * tab.splits;
+        const int own = t.over - t.tile * tab.splits;
 #pragma unroll 1
         for (int c = 0; c < c_end; c += 16) {
           float f[16];
@@ -937,7 +955,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
         __threadfence();
         named_barrier_sync(1, 32 * C::kEpiWarps);
         if (threadIdx.x == 32 * C::kEpiWarp0) {
-          const unsigned before = atomicAdd(&p.arrived[t.index * 2 + static_cast<int>(rank)], 1u);
+          const unsigned before = atomicAdd(&p.arrived[t.tile * 2 + static_cast<int>(rank)], 1u);
           sh->last = before + 1 == static_cast<unsigned>(tab.splits);
         }
         named_barrier_sync(1, 32 * C::kEpiWarps);
@@ -1243,13 +1261,17 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
       if (ok && a.B_lo.p != nullptr) ok = encode_l(a.B_lo, &p.l_whole1, &maps.l[1]);
       if (ok && a.A_lo.p != nullptr) ok = encode_q(a.A_lo, &maps.q[1]);
     }
+    if (ok && qmn && !two_terms && a.A.cols % line == 0) {
+      p.q_whole = 1;
+      ok = encode(a.A, a.bf16, line, bk, kHalf / line, true, &maps.q[2]);
+    }
     if (!ok) return kErrLaunch;
   }
   if (p.c_rows && !encode(a.C, !p.c_f32, kHalf, 16, 1, false, &maps.c)) return kErrLaunch;
 
-  // Slots for splitting, where there can be few enough tiles and enough k.
+  // Slots for splitting, where there is enough k.
   void *work = nullptr;
-  if (least * 2 <= pairs && (a.wgrad ? a.M : a.K) * p.passes >= 8 * kBlock) {
+  if ((a.wgrad ? a.M : a.K) * p.passes >= 8 * kBlock) {
     const size_t counters = (static_cast<size_t>(2 * pairs) * sizeof(unsigned) + 255) / 256 * 256;
     const size_t slots = static_cast<size_t>(pairs) * 2 * kCols * kHalf;
     const int st = pool_alloc(&work, counters + slots * sizeof(float), stream);
