@@ -436,82 +436,90 @@ def vector_sum(x, groups=0, out=None, stream=None):
     return out
 
 
+# Operands of the segmented products. The checks run on every call, before
+# microseconds of work, so each tensor's attributes are read once.
+
 def _segment_type(t, name):
+    """The library's type code of a float32 or bfloat16 CUDA tensor."""
     import torch
 
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in (torch.float32,
-                                                                          torch.bfloat16):
-        raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor")
-    return TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        if t.dtype is torch.bfloat16:
+            return TYPE_BF16
+        if t.dtype is torch.float32:
+            return TYPE_F32
+    raise TypeError(f"{name} must be a float32 or bfloat16 CUDA tensor")
 
 
-def _check_like(t, name, like, dim):
-    """A `dim`-D tensor of like's type and device whose matrices the library
-    can address as (pointer, leading dimension, stride of the stack)."""
-    _segment_type(t, name)
-    if t.dim() != dim:
-        raise TypeError(f"{name} must have {dim} dimensions, not {t.dim()}")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, the other operands {like.dtype} on "
-                         f"{like.device}")
-    _check_rows(t.shape[-2:], t.stride(-2), t.stride(-1), name)
+def _addressing(shape, strides, name):
+    """(leading dimension, stride of the stack) of a matrix or a stack of them
+    that the library can address; the rules are those of _check_rows."""
+    rows, cols = shape[-2], shape[-1]
+    ld, unit = strides[-2], strides[-1]
+    if (unit != 1 and cols > 1) or (rows > 1 and ld < cols):
+        _check_rows((rows, cols), ld, unit, name)
+    return (ld if rows > 1 and cols else cols) or 1, (
+        strides[0] if len(shape) == 3 and shape[0] > 1 else 0)
 
 
-def _check_out(out, name, shape, like):
-    """out, or a new tensor of the shape; a stack's matrices must not overlap."""
-    import torch
+def _matrices(t, name, dim, kind, device):
+    """(shape, pointer, leading dimension, stride of the stack) of a `dim`-D
+    tensor of the type and device."""
+    if _segment_type(t, name) != kind or t.get_device() != device:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, unlike the first operand")
+    shape = t.shape
+    if len(shape) != dim:
+        raise TypeError(f"{name} must have {dim} dimensions, not {len(shape)}")
+    ld, stride = _addressing(shape, t.stride(), name)
+    return shape, t.data_ptr(), ld, stride
 
+
+def _result(out, name, shape, like, kind, device):
+    """out, or a new tensor of the shape, and its (pointer, ld, stride)."""
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    _check_like(out, name, like, len(shape))
-    if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} has the wrong shape: {tuple(out.shape)}, not {tuple(shape)}")
-    if len(shape) == 3 and out.numel() and shape[0] > 1 and (
-            out.stride(0) < (shape[1] - 1) * _ld2(out) + shape[2]):
+        out = like.new_empty(shape)
+        return out, out.data_ptr(), shape[-1] or 1, (shape[1] * shape[2] if len(shape) == 3 else 0)
+    got, ptr, ld, stride = _matrices(out, name, len(shape), kind, device)
+    if tuple(got) != shape:
+        raise ValueError(f"{name} has the wrong shape: {tuple(got)}, not {shape}")
+    if len(shape) == 3 and shape[0] > 1 and out.numel() and stride < (shape[1] - 1) * ld + shape[2]:
         raise ValueError(f"{name}'s matrices overlap")
-    return out
+    return out, ptr, ld, stride
 
 
-def _check_offsets(offsets, device):
+def _offsets(offsets, device):
+    """(segments, pointer)"""
     import torch
 
-    if (not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int64 or offsets.dim() != 1
-            or offsets.device != device or not offsets.is_contiguous() or offsets.numel() < 1):
+    if (not isinstance(offsets, torch.Tensor) or offsets.dtype is not torch.int64
+            or offsets.dim() != 1 or not offsets.is_cuda or offsets.get_device() != device
+            or not offsets.is_contiguous() or offsets.shape[0] < 1):
         raise TypeError("offsets must be a contiguous 1-D int64 tensor of segments + 1 values on "
                         "the operands' device")
-    segments = offsets.numel() - 1
+    segments = offsets.shape[0] - 1
     if segments > MAX_SEGMENTS:
         raise ValueError(f"{segments} segments: at most {MAX_SEGMENTS} a call")
-    return segments
+    return segments, offsets.data_ptr()
 
 
-def _check_array(t, name, dtype, count, device):
+def _array(t, name, dtype, count, device):
     import torch
 
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device
-            or tuple(t.shape) != (count,) or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda
+            or t.get_device() != device or t.dim() != 1 or t.shape[0] != count
+            or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of {count} values on the "
                         "operands' device")
     return t.data_ptr()
-
-
-def _ld2(t) -> int:
-    """Leading dimension of the matrices of a 2-D or 3-D tensor."""
-    rows, cols = int(t.shape[-2]), int(t.shape[-1])
-    return max(int(t.stride(-2)), cols, 1) if rows > 1 else max(cols, 1)
-
-
-def _stride(t) -> int:
-    return int(t.stride(0)) if t.shape[0] > 1 else 0
 
 
 def _call(name, device, stream, *args):
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(device)
     function = getattr(_lib or _load(), name)
-    if torch.cuda.current_device() == device.index:
+    if torch.cuda.current_device() == device:
         st = function(*args, stream or None)
     else:
         with torch.cuda.device(device):
@@ -531,19 +539,19 @@ def grouped_matmul(a, b, offsets, transb=False, out=None, stream=None):
     not written. Stream ordered on ``stream`` (default: torch's current one).
     """
     kind = _segment_type(a, "a")
-    _check_like(a, "a", a, 2)
-    _check_like(b, "b", a, 3)
-    groups = _check_offsets(offsets, a.device)
-    m, k = a.shape
-    k2, n = (b.shape[2], b.shape[1]) if transb else (b.shape[1], b.shape[2])
-    if b.shape[0] != groups:
-        raise ValueError(f"{b.shape[0]} matrices for {groups} segments")
+    dev = a.get_device()
+    (m, k), pa, lda, _ = _matrices(a, "a", 2, kind, dev)
+    (count, k2, n), pb, ldb, strideb = _matrices(b, "b", 3, kind, dev)
+    groups, po = _offsets(offsets, dev)
+    if transb:
+        k2, n = n, k2
+    if count != groups:
+        raise ValueError(f"{count} matrices for {groups} segments")
     if k != k2:
         raise ValueError(f"inner dimensions differ: a is {m} x {k}, op(b) {k2} x {n}")
-    out = _check_out(out, "out", (m, n), a)
-    _call("gemm_f32_grouped", a.device, stream, kind, OP_T if transb else OP_N, groups, m, n, k,
-          a.data_ptr(), _ld2(a), b.data_ptr(), _ld2(b), _stride(b), out.data_ptr(), _ld2(out),
-          offsets.data_ptr())
+    out, pc, ldc, _ = _result(out, "out", (m, n), a, kind, dev)
+    _call("gemm_f32_grouped", dev, stream, kind, OP_T if transb else OP_N, groups, m, n, k, pa, lda,
+          pb, ldb, strideb, pc, ldc, po)
     return out
 
 
@@ -552,16 +560,15 @@ def grouped_wgrad(a, d, offsets, out=None, stream=None):
     g], zero where segment g is empty. ``a`` is M x K, ``d`` M x N, ``out`` G x
     K x N (returned)."""
     kind = _segment_type(a, "a")
-    _check_like(a, "a", a, 2)
-    _check_like(d, "d", a, 2)
-    groups = _check_offsets(offsets, a.device)
-    m, k = a.shape
-    m2, n = d.shape
+    dev = a.get_device()
+    (m, k), pa, lda, _ = _matrices(a, "a", 2, kind, dev)
+    (m2, n), pd, ldd, _ = _matrices(d, "d", 2, kind, dev)
+    groups, po = _offsets(offsets, dev)
     if m != m2:
         raise ValueError(f"a has {m} rows, d {m2}")
-    out = _check_out(out, "out", (groups, k, n), a)
-    _call("gemm_f32_grouped_wgrad", a.device, stream, kind, groups, m, n, k, a.data_ptr(), _ld2(a),
-          d.data_ptr(), _ld2(d), out.data_ptr(), _ld2(out), _stride(out), offsets.data_ptr())
+    out, pc, ldc, stridec = _result(out, "out", (groups, k, n), a, kind, dev)
+    _call("gemm_f32_grouped_wgrad", dev, stream, kind, groups, m, n, k, pa, lda, pd, ldd, pc, ldc,
+          stridec, po)
     return out
 
 
@@ -582,36 +589,32 @@ def lora_matmul(x, w, lora_a, lora_b, offsets, adapters=None, scales=None, trans
     import torch
 
     kind = _segment_type(x, "x")
-    _check_like(x, "x", x, 2)
-    _check_like(w, "w", x, 2)
-    _check_like(lora_a, "lora_a", x, 3)
-    _check_like(lora_b, "lora_b", x, 3)
-    segments = _check_offsets(offsets, x.device)
-    m, k = x.shape
-    k2, n = (w.shape[1], w.shape[0]) if transw else tuple(w.shape)
-    bank, ka, r = lora_a.shape if not transl else (lora_a.shape[0], lora_a.shape[2], lora_a.shape[1])
-    bank2, rb, nb = lora_b.shape if not transl else (lora_b.shape[0], lora_b.shape[2],
-                                                     lora_b.shape[1])
+    dev = x.get_device()
+    (m, k), px, ldx, _ = _matrices(x, "x", 2, kind, dev)
+    (k2, n), pw, ldw, _ = _matrices(w, "w", 2, kind, dev)
+    (bank, ka, r), pa, lda, stridea = _matrices(lora_a, "lora_a", 3, kind, dev)
+    (bank2, rb, nb), pb, ldb, strideb = _matrices(lora_b, "lora_b", 3, kind, dev)
+    segments, po = _offsets(offsets, dev)
+    if transw:
+        k2, n = n, k2
+    if transl:
+        ka, r, rb, nb = r, ka, nb, rb
     if k != k2:
         raise ValueError(f"inner dimensions differ: x is {m} x {k}, op(w) {k2} x {n}")
-    if (ka, rb, nb, bank2) != (k, r, n, bank):
+    if ka != k or rb != r or nb != n or bank2 != bank:
         raise ValueError(f"op(lora_a) is {bank} of {ka} x {r} and op(lora_b) {bank2} of {rb} x {nb} "
                          f"beside a {k} x {n} projection")
     if adapters is None and segments > bank:
         raise ValueError(f"{segments} segments, {bank} adapters and no choice of adapters")
-    index = 0 if adapters is None else _check_array(adapters, "adapters", torch.int32, segments,
-                                                    x.device)
-    scale = 0 if scales is None else _check_array(scales, "scales", torch.float32, bank, x.device)
-    out = _check_out(out, "out", (m, n), x)
-    u, ldu = 0, max(r, 1)
+    pi = None if adapters is None else _array(adapters, "adapters", torch.int32, segments, dev)
+    ps = None if scales is None else _array(scales, "scales", torch.float32, bank, dev)
+    out, py, ldy, _ = _result(out, "out", (m, n), x, kind, dev)
+    pu, ldu = None, r or 1
     if shrink_out is not None:
-        _check_out(shrink_out, "shrink_out", (m, r), x)
-        u, ldu = shrink_out.data_ptr(), _ld2(shrink_out)
-    _call("gemm_f32_lora", x.device, stream, kind, OP_T if transw else OP_N,
-          OP_T if transl else OP_N, segments, bank, m, n, k, r, x.data_ptr(), _ld2(x), w.data_ptr(),
-          _ld2(w), lora_a.data_ptr(), _ld2(lora_a), _stride(lora_a), lora_b.data_ptr(),
-          _ld2(lora_b), _stride(lora_b), offsets.data_ptr(), index, scale, u, ldu, out.data_ptr(),
-          _ld2(out))
+        _, pu, ldu, _ = _result(shrink_out, "shrink_out", (m, r), x, kind, dev)
+    _call("gemm_f32_lora", dev, stream, kind, OP_T if transw else OP_N, OP_T if transl else OP_N,
+          segments, bank, m, n, k, r, px, ldx, pw, ldw, pa, lda, stridea, pb, ldb, strideb, po, pi,
+          ps, pu, ldu, py, ldy)
     return out
 
 
@@ -624,33 +627,29 @@ def lora_backward(dy, x, shrink, w, lora_a, lora_b, offsets, scales=None, transw
     import torch
 
     kind = _segment_type(dy, "dy")
-    _check_like(dy, "dy", dy, 2)
-    _check_like(shrink, "shrink", dy, 2)
-    _check_like(x, "x", dy, 2)
-    _check_like(w, "w", dy, 2)
-    _check_like(lora_a, "lora_a", dy, 3)
-    _check_like(lora_b, "lora_b", dy, 3)
-    segments = _check_offsets(offsets, dy.device)
-    (m, k), n, r = x.shape, dy.shape[1], shrink.shape[1]
-    if dy.shape[0] != m or shrink.shape[0] != m:
-        raise ValueError(f"x has {m} rows, dy {dy.shape[0]} and shrink {shrink.shape[0]}")
-    if (tuple(w.shape) != ((n, k) if transw else (k, n))
-            or tuple(lora_a.shape) != ((segments, r, k) if transl else (segments, k, r))
-            or tuple(lora_b.shape) != ((segments, n, r) if transl else (segments, r, n))):
-        raise ValueError(f"w {tuple(w.shape)}, lora_a {tuple(lora_a.shape)} and lora_b "
-                         f"{tuple(lora_b.shape)} are not those of {segments} segments, a {k} x {n} "
-                         f"projection and rank {r}")
-    scale = 0 if scales is None else _check_array(scales, "scales", torch.float32, segments,
-                                                  dy.device)
-    dx = _check_out(None, "dx", (m, k), dy)
-    da = _check_out(None, "da", tuple(lora_a.shape), dy)
-    db = _check_out(None, "db", tuple(lora_b.shape), dy)
-    _call("gemm_f32_lora_backward", dy.device, stream, kind, OP_T if transw else OP_N,
-          OP_T if transl else OP_N, segments, m, n, k, r, dy.data_ptr(), _ld2(dy), x.data_ptr(),
-          _ld2(x), shrink.data_ptr(), _ld2(shrink), w.data_ptr(), _ld2(w), lora_a.data_ptr(),
-          _ld2(lora_a), _stride(lora_a), lora_b.data_ptr(), _ld2(lora_b), _stride(lora_b),
-          offsets.data_ptr(), scale, dx.data_ptr(), _ld2(dx), da.data_ptr(), _ld2(da), _stride(da),
-          db.data_ptr(), _ld2(db), _stride(db))
+    dev = dy.get_device()
+    (m, n), pdy, lddy, _ = _matrices(dy, "dy", 2, kind, dev)
+    (m2, k), px, ldx, _ = _matrices(x, "x", 2, kind, dev)
+    (m3, r), pu, ldu, _ = _matrices(shrink, "shrink", 2, kind, dev)
+    wshape, pw, ldw, _ = _matrices(w, "w", 2, kind, dev)
+    ashape, pa, lda, stridea = _matrices(lora_a, "lora_a", 3, kind, dev)
+    bshape, pb, ldb, strideb = _matrices(lora_b, "lora_b", 3, kind, dev)
+    segments, po = _offsets(offsets, dev)
+    if m2 != m or m3 != m:
+        raise ValueError(f"dy has {m} rows, x {m2} and shrink {m3}")
+    if (tuple(wshape) != ((n, k) if transw else (k, n))
+            or tuple(ashape) != ((segments, r, k) if transl else (segments, k, r))
+            or tuple(bshape) != ((segments, n, r) if transl else (segments, r, n))):
+        raise ValueError(f"w {tuple(wshape)}, lora_a {tuple(ashape)} and lora_b {tuple(bshape)} are "
+                         f"not those of {segments} segments, a {k} x {n} projection and rank {r}")
+    ps = None if scales is None else _array(scales, "scales", torch.float32, segments, dev)
+    dx, pdx, lddx, _ = _result(None, "dx", (m, k), dy, kind, dev)
+    da, pda, ldda, strideda = _result(None, "da", tuple(ashape), dy, kind, dev)
+    db, pdb, lddb, stridedb = _result(None, "db", tuple(bshape), dy, kind, dev)
+    _call("gemm_f32_lora_backward", dev, stream, kind, OP_T if transw else OP_N,
+          OP_T if transl else OP_N, segments, m, n, k, r, pdy, lddy, px, ldx, pu, ldu, pw, ldw, pa,
+          lda, stridea, pb, ldb, strideb, po, ps, pdx, lddx, pda, ldda, strideda, pdb, lddb,
+          stridedb)
     return dx, da, db
 
 

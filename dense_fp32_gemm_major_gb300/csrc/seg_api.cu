@@ -95,11 +95,24 @@ class Workspace {
     bytes_ += static_cast<size_t>((count * rows * m.ld * elem + 255) / 256 * 256);
   }
 
-  // Allocate, place, and copy.
+  // Room for splitting the tiles of a product of this shape.
+  void splits(const SegArgs &a) {
+    if (gemm::seg_tc_splits(a)) split_ = true;
+  }
+
+  // Allocate, place, zero the split tiles' counters, and copy.
   int take(int sms, cudaStream_t s) {
-    if (bytes_ == 0) return gemm::kOk;
-    const int st = gemm::pool_alloc(&p_, bytes_, s);
+    sms_ = sms;
+    const size_t counters = static_cast<size_t>(kProducts) * sms * sizeof(unsigned);
+    const size_t slots = split_ ? static_cast<size_t>(gemm::seg_tc_slots(sms)) * sizeof(float) : 0;
+    if (bytes_ + slots == 0) return gemm::kOk;
+    const int st = gemm::pool_alloc(&p_, bytes_ + slots + (split_ ? counters : 0), s);
     if (st != gemm::kOk) return st;
+    if (split_) {
+      slots_ = reinterpret_cast<float *>(static_cast<uint8_t *>(p_) + bytes_);
+      arrived_ = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(p_) + bytes_ + slots);
+      if (cudaMemsetAsync(arrived_, 0, counters, s) != cudaSuccess) return gemm::kErrLaunch;
+    }
     for (int i = 0; i < placed_count_; ++i) placed_[i]->p = static_cast<uint8_t *>(p_) + at_[i];
     for (int i = 0; i < copy_count_; ++i) {
       copies_[i].dst = *target_[i];
@@ -109,15 +122,24 @@ class Workspace {
     return gemm::kOk;
   }
 
+  // One product, with the scratch it may want.
+  int launch(SegArgs &a, cudaStream_t s) {
+    if (split_) {
+      a.slots = slots_;
+      a.arrived = arrived_ + static_cast<size_t>(products_++ % kProducts) * sms_;
+    }
+    return gemm::seg_tc_launch(a, sms_, s);
+  }
+
   // Rows of the segments, from here to the caller's matrix.
-  int hand_back(const SegMatrix &from, const SegMatrix &to, int sms, cudaStream_t s) {
+  int hand_back(const SegMatrix &from, const SegMatrix &to, cudaStream_t s) {
     gemm::SegCopy c;
     c.src = from;
     c.dst = to;
     c.offsets = offsets_;
     c.groups = groups_;
     c.M = rows_;
-    return gemm::seg_pack_launch(c, bf16_, sms, s);
+    return gemm::seg_pack_launch(c, bf16_, sms_, s);
   }
 
   int give_back(int st, cudaStream_t s) {
@@ -127,7 +149,7 @@ class Workspace {
   }
 
  private:
-  static constexpr int kMost = 12;
+  static constexpr int kMost = 12, kProducts = 5;
   bool bf16_;
   const int64_t *offsets_;
   int64_t groups_, rows_;
@@ -137,6 +159,10 @@ class Workspace {
   SegMatrix *target_[kMost], *placed_[kMost];
   size_t at_[kMost];
   int copy_count_ = 0, placed_count_ = 0;
+  bool split_ = false;
+  float *slots_ = nullptr;
+  unsigned *arrived_ = nullptr;
+  int sms_ = 0, products_ = 0;
 };
 
 // Y = X op(W) + U op(B_a), U = s_a (X op(A_a)).
@@ -166,6 +192,10 @@ struct Lora {
     fused = adapted && K > 0 && transw == transl && M >= 128 * segments && tiles >= sms;
     w.readable(X);
     w.readable(W);
+    SegArgs shape;
+    shape.bf16 = bf16;
+    shape.K = K;
+    w.splits(shape);
     if (!adapted) return;
     w.readable(A);
     w.readable(B);
@@ -180,7 +210,7 @@ struct Lora {
     if (!fused) w.matrix(sum, M, N, 4);
   }
 
-  int run(Workspace &w, int sms, cudaStream_t s) {
+  int run(Workspace &w, cudaStream_t s) {
     SegArgs y;
     y.bf16 = bf16;
     y.M = M;
@@ -198,9 +228,9 @@ struct Lora {
       p.scales = scales;
       p.C = u;
       p.C_lo = u_lo;
-      int st = gemm::seg_tc_launch(p, sms, s);
+      int st = w.launch(p, s);
       if (st == gemm::kOk && user_u.p != nullptr && u.p != user_u.p)
-        st = w.hand_back(u, user_u, sms, s);
+        st = w.hand_back(u, user_u, s);
       if (st != gemm::kOk || N == 0) return st;
     }
     y.dense = true;
@@ -210,14 +240,14 @@ struct Lora {
     y.B = W;
     y.transb = transw;
     y.C = Y;
-    if (!adapted) return gemm::seg_tc_launch(y, sms, s);
+    if (!adapted) return w.launch(y, s);
     if (fused) {
       y.index = index;
       y.R = R;
       y.U = u;
       y.U_lo = u_lo;
       y.L = B;
-      return gemm::seg_tc_launch(y, sms, s);
+      return w.launch(y, s);
     }
     SegArgs e = y;  // U B
     e.dense = false;
@@ -229,10 +259,10 @@ struct Lora {
     e.transb = transl;
     e.C = sum;
     e.c_f32 = true;
-    int st = gemm::seg_tc_launch(e, sms, s);
+    int st = w.launch(e, s);
     if (st != gemm::kOk) return st;
     y.add = sum;
-    return gemm::seg_tc_launch(y, sms, s);
+    return w.launch(y, s);
   }
 };
 
@@ -242,9 +272,10 @@ int launch(SegArgs &a, int sms, cudaStream_t s) {
   if (a.M > 0 && (a.wgrad || a.K > 0)) {
     w.readable(a.A);
     w.readable(a.B, !a.wgrad);
+    w.splits(a);
   }
   int st = w.take(sms, s);
-  if (st == gemm::kOk) st = gemm::seg_tc_launch(a, sms, s);
+  if (st == gemm::kOk) st = w.launch(a, s);
   return w.give_back(st, s);
 }
 
@@ -361,7 +392,7 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
   Workspace work(l.bf16, offsets, segments, M);
   l.prepare(work, sms);
   st = work.take(sms, s);
-  if (st == gemm::kOk) st = l.run(work, sms, s);
+  if (st == gemm::kOk) st = l.run(work, s);
   return work.give_back(st, s);
 }
 
@@ -424,6 +455,11 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Workspace work(l.bf16, offsets, segments, M);
   if (M > 0) {
+    SegArgs shape;  // of the gradients
+    shape.bf16 = l.bf16;
+    shape.wgrad = true;
+    shape.M = M;
+    work.splits(shape);
     l.prepare(work, sms);
     if (l.adapted) {
       work.readable(x);
@@ -431,7 +467,7 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
     }
   }
   st = work.take(sms, s);
-  if (st == gemm::kOk && M > 0) st = l.run(work, sms, s);
+  if (st == gemm::kOk && M > 0) st = l.run(work, s);
   // dA = X^T V (stored R x K: V^T X) and dB = U^T dY (stored N x R: dY^T U).
   SegArgs g;
   g.bf16 = l.bf16;
@@ -448,7 +484,7 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
     g.C = da;
     g.K = da.rows;
     g.N = da.cols;
-    st = gemm::seg_tc_launch(g, sms, s);
+    st = work.launch(g, s);
   }
   if (st == gemm::kOk && segments > 0 && R > 0 && N > 0) {
     g.A = transl ? l.X : u;
@@ -457,7 +493,7 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
     g.C = db;
     g.K = db.rows;
     g.N = db.cols;
-    st = gemm::seg_tc_launch(g, sms, s);
+    st = work.launch(g, s);
   }
   return work.give_back(st, s);
 }

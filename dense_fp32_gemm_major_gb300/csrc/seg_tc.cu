@@ -65,6 +65,10 @@ constexpr int kColStep = 32;    // granularity of the MMA's N
 constexpr int kRasterM = 8;     // row tiles per raster group
 constexpr int kBlock = 64;      // k of a block: a bf16 stage, or a float32 accumulator
 constexpr int kMaxSplits = 16;
+// Splitting a tile along k costs about 4 us (the sums' way through memory, and
+// the counters' zeros before the launch); blocks take 0.3 us (bf16) and up to 2
+// us (float32). Fewest blocks of an item, and of a contraction worth splitting.
+constexpr int kItemBlocksBf16 = 8, kItemBlocksF32 = 4, kSplitBlocksBf16 = 32, kSplitBlocksF32 = 8;
 constexpr uint32_t kTmemCols = 512;
 
 enum Form : int { kRows = 0, kDense = 1, kAdapted = 2, kWgrad = 3 };
@@ -251,8 +255,7 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
 // A round of tiles takes nearly the same time at every width (a block of 64 k
 // and 256, 128, 64 columns: bf16 302, 282, 275 ns, float32 1.99, 1.72, 1.55 us),
 // so narrower tiles pay only where they fill pairs that would be idle. Tiles
-// past the last full round that leave half the pairs idle are split along k, at
-// least four blocks an item.
+// past the last full round that leave half the pairs idle are split along k.
 template <bool SPLIT>
 __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int longest, int pairs,
                                            Table &tab) {
@@ -274,7 +277,10 @@ __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int
     const int rest = n % pairs;
     const int k = p.form == kWgrad ? longest : p.K;
     const int splits =
-        rest > 0 ? min(min(pairs / rest, p.passes * cdiv(k, kBlock) / 4), kMaxSplits) : 1;
+        rest > 0 ? min(min(pairs / rest, p.passes * cdiv(k, kBlock) /
+                                              (SPLIT ? kItemBlocksF32 : kItemBlocksBf16)),
+                       kMaxSplits)
+                 : 1;
     if (splits > 1) {
       tab.whole = n - rest;
       tab.splits = splits;
@@ -1185,6 +1191,16 @@ bool seg_tc_readable(const SegMatrix &m, bool bf16) {
          (m.count <= 1 || m.stride % per16 == 0);
 }
 
+bool seg_tc_splits(const SegArgs &a) {
+  const int64_t blocks = ((a.wgrad ? a.M : a.K) + kBlock - 1) / kBlock *
+                         (a.A_lo.p != nullptr || a.B_lo.p != nullptr ? 2 : 1);
+  return blocks >= (a.bf16 ? kSplitBlocksBf16 : kSplitBlocksF32);
+}
+
+int64_t seg_tc_slots(int sm_count) {
+  return static_cast<int64_t>(sm_count > 1 ? sm_count / 2 : 1) * 2 * kCols * kHalf;
+}
+
 int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   SegTc p = {};
   const bool adapted = a.R > 0;
@@ -1269,28 +1285,15 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   }
   if (p.c_rows && !encode(a.C, !p.c_f32, kHalf, 16, 1, false, &maps.c)) return kErrLaunch;
 
-  // Slots for splitting, where there is enough k.
-  void *work = nullptr;
-  if ((a.wgrad ? a.M : a.K) * p.passes >= 8 * kBlock) {
-    const size_t counters = (static_cast<size_t>(2 * pairs) * sizeof(unsigned) + 255) / 256 * 256;
-    const size_t slots = static_cast<size_t>(pairs) * 2 * kCols * kHalf;
-    const int st = pool_alloc(&work, counters + slots * sizeof(float), stream);
-    if (st != kOk) return st;
-    p.arrived = static_cast<unsigned *>(work);
-    p.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(work) + counters);
-    p.slot_extent = static_cast<long long>(slots);
-    if (cudaMemsetAsync(work, 0, counters, stream) != cudaSuccess) {
-      pool_free(work, stream);
-      return kErrLaunch;
-    }
+  if (a.slots != nullptr && seg_tc_splits(a)) {
+    p.slots = a.slots;
+    p.arrived = a.arrived;
+    p.slot_extent = static_cast<long long>(seg_tc_slots(sm_count));
   } else if (pairs > most) {
     pairs = most > 0 ? static_cast<int>(most) : 1;
   }
-  const int st = a.bf16 ? launch_layout<__nv_bfloat16>(lmn, qmn, maps, p, pairs, stream)
-                        : launch_layout<float>(lmn, qmn, maps, p, pairs, stream);
-  if (work == nullptr) return st;
-  const int fst = pool_free(work, stream);
-  return st != kOk ? st : fst;
+  return a.bf16 ? launch_layout<__nv_bfloat16>(lmn, qmn, maps, p, pairs, stream)
+                : launch_layout<float>(lmn, qmn, maps, p, pairs, stream);
 }
 
 }  // namespace gemm

@@ -44,7 +44,16 @@ struct SegArgs {
   SegMatrix add;       // dense: float32 addend of the result
   int64_t R = 0;       // adapted: width of U
   SegMatrix U, U_lo, L;
+  // Scratch for tiles split along k: seg_tc_slots() floats, and 2 counters a
+  // pair, zero before the launch. null: no splits.
+  float *slots = nullptr;
+  unsigned *arrived = nullptr;
 };
+
+// Whether a product's contraction is long enough to be worth splitting, and
+// the floats that its slots take.
+bool seg_tc_splits(const SegArgs &a);
+int64_t seg_tc_slots(int sm_count);
 
 // Whether the kernels can read a matrix as it lies (by TMA: 16-byte aligned
 // rows). Others are copied first (seg_pack_launch).

@@ -109,9 +109,14 @@ def test_wrappers_refuse_what_is_not_on_a_gpu():
 
 
 def test_stack_addressing():
+    at = lambda t: g._addressing(t.shape, t.stride(), "t")
     t = torch.zeros(3, 5, 8)
-    assert (g._ld2(t), g._stride(t)) == (8, 40)
-    assert (g._ld2(t[:, :, :3]), g._stride(t[:, :, :3])) == (8, 40)
-    assert (g._ld2(t[:, :1]), g._stride(t[:1])) == (8, 0)
-    one = torch.zeros(5, 8).expand(3, 5, 8)
-    assert (g._ld2(one), g._stride(one)) == (8, 0)
+    assert at(t) == (8, 40) and at(t[0]) == (8, 0)
+    assert at(t[:, :, :3]) == (8, 40)
+    assert at(t[:, :1]) == (8, 40) and at(t[:1]) == (8, 0) and at(t[1:, :1, :3]) == (3, 40)
+    assert at(torch.zeros(5, 8).expand(3, 5, 8)) == (8, 0)
+    assert at(torch.zeros(0, 8)) == (8, 0) and at(torch.zeros(4, 0)) == (1, 0)
+    for bad in (torch.zeros(5, 8).t(), torch.zeros(1, 8).expand(5, 8),
+                torch.zeros(64).as_strided((2, 5, 8), (0, 4, 1))):
+        with pytest.raises(ValueError):
+            at(bad)

@@ -419,7 +419,9 @@ def test_every_access_is_inside_the_declared_extents(g, checked_lib, dt):
         b, w = normal((4, k, n), 83, dt, pad, lead), normal((k, n), 84, dt, pad, lead)
         la, lb = normal((4, k, r), 85, dt, pad, lead), normal((4, r, n), 86, dt, pad, lead)
         y, u = normal((m, n), 87, dt, pad, lead), normal((m, r), 88, dt, pad, lead)
-        ptr, ld, st = (lambda t: t.data_ptr()), g._ld2, g._stride
+        ptr = lambda t: t.data_ptr()
+        ld = lambda t: g._addressing(t.shape, t.stride(), "t")[0]
+        st = lambda t: g._addressing(t.shape, t.stride(), "t")[1]
         assert lib.gemm_f32_grouped(kind, 0, 4, m, n, k, ptr(x), ld(x), ptr(b), ld(b), st(b), ptr(y),
                                     ld(y), ptr(off), s) == g.OK
         assert lib.gemm_f32_grouped_wgrad(kind, 4, m, n, k, ptr(x), ld(x), ptr(d), ld(d), ptr(b),
