@@ -118,14 +118,18 @@ struct Cfg {
   static constexpr int kRawOpBytes = kHalf * 128;
   static constexpr int kRawStages = kSplit ? 3 : 1;
   static constexpr int kRawBytes = kSplit ? kRawStages * 2 * kRawOpBytes : 0;
-  // Results on their way out, per 128 columns of the tile: two pieces of 16
-  // rows of 128 bf16, or one of float32.
-  static constexpr int kOutBytes = 8192;
+  // Results on their way out, for each four epilogue warps: 16 rows of 128 (8
+  // float32 rows of a bf16 product).
+  static constexpr int kOutBytes = kSplit ? 8192 : 4096;
   static constexpr int kMmaWarp = 1;
   static constexpr int kFixWarp = 2;
-  static constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+  // Epilogue warps, and the columns of each: the longest way of a short tile
+  // (bf16, 16 blocks a tile: 118 us with eight of them, 99 with sixteen);
+  // float32 has registers for eight.
+  static constexpr int kEpiWarp0 = 4, kEpiWarps = kSplit ? 8 : 16;
+  static constexpr int kEpiCols = kCols / (kEpiWarps / 4);
   static constexpr int kLoadWarp0 = 12, kLoadWarps = 8;
-  static constexpr int kThreads = 32 * (kSplit ? kLoadWarp0 + kLoadWarps : kLoadWarp0);
+  static constexpr int kThreads = 32 * (kSplit ? kLoadWarp0 + kLoadWarps : kEpiWarp0 + kEpiWarps);
 };
 
 template <int STAGES, int RAW>
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
   uint8_t *raw = stages + STAGES * C::kStageBytes;
   uint8_t *out = raw + C::kRawBytes;
   using Sh = Shared<STAGES, C::kRawStages>;
-  Sh *sh = reinterpret_cast<Sh *>(out + 2 * C::kOutBytes);
+  Sh *sh = reinterpret_cast<Sh *>(out + C::kEpiWarps / 4 * C::kOutBytes);
   Table tab;
   tab.row = reinterpret_cast<int *>(sh + 1);
   tab.first = tab.row + p.entries + 1;
@@ -759,8 +763,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     // ----------------------------------------------------------- epilogue --
     set_registers<C::kSplit, 152>();
     const uint32_t quad = warp & 3, part = (warp - C::kEpiWarp0) >> 2;
-    const uint32_t tlane = tmem + ((quad * 32) << 16) + part * 128;
-    const int c0 = static_cast<int>(part) * 128;  // this warp's first column
+    const uint32_t tlane = tmem + ((quad * 32) << 16) + part * C::kEpiCols;
+    const int c0 = static_cast<int>(part) * C::kEpiCols;  // this warp's first column
     Ring<2> acc;
     int add0 = 0, add1 = 0;  // rows with an addend
     if (p.add != nullptr) {
@@ -863,50 +867,52 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
           for (int k = 0; k < 16; ++k) f[k] += a[k];
         }
         if (p.c_rows) {
-          // Sixteen rows of this CTA's 128 lanes meet in shared memory and
-          // leave as whole pieces of their rows.
+          // Rows of this CTA's 128 lanes meet in shared memory and leave as
+          // whole pieces of their rows.
           const int elem = p.c_f32 ? 4 : 2, row_bytes = kHalf * elem;
-          const uint32_t to = smem_addr(out) + part * C::kOutBytes +
-                              (p.c_f32 ? 0 : (c >> 4 & 1) * (C::kOutBytes / 2));
+          const int rows = C::kOutBytes / row_bytes;  // 16, or 8
+          const uint32_t to = smem_addr(out) + part * C::kOutBytes;
           const uint32_t at_lane = to + (quad * 32 + lane) * elem;
-          if (quad == 0) {  // the copies that last read this piece are done with it
-            if (p.c_f32)
-              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            else
-              asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          }
-          named_barrier_sync(3 + part, 128);
-          if (p.c_f32) {
+          const int n_cta = t.n0 + static_cast<int>(rank) * kHalf;
+          const int width = min(kHalf, p.N - n_cta);
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(at_lane + k * row_bytes), "f"(f[k])
-                           : "memory");
-          } else {
+          for (int h = 0; h < 16; h += 8) {
+            if (h == 8 && rows == 16) break;
+            // The copies that last read the piece are done with it.
+            if (quad == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            named_barrier_sync(3 + part, 128);
+            if (p.c_f32) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at_lane + k * row_bytes),
-                           "h"(__bfloat16_as_ushort(__float2bfloat16_rn(f[k])))
-                           : "memory");
-          }
-          fence_proxy_async_smem();
-          named_barrier_sync(3 + part, 128);
-          if (quad == 0) {
-            const int n_cta = t.n0 + static_cast<int>(rank) * kHalf;
-            const int width = min(kHalf, p.N - n_cta);
-            if (c0 + c + 16 <= t.qn) {
-              // One box of sixteen rows (as a copy for each row, 256 bytes at
-              // a time, results left at 2 TB/s).
-              if (lane == 0 && width > 0)
-                store_box(&maps.c, to, n_cta, t.q0 + c0 + c, p.form == kWgrad ? t.g : 0);
-            } else {  // the segment ends here
-              const int row = c + static_cast<int>(lane);
-              const long long off = at - n + n_cta + row * p.c_ld;
-              if (lane < 16 && c0 + row < t.qn && width > 0 &&
-                  index_ok(kSiteCStore, off, width, p.c_extent))
-                store_bulk(static_cast<uint8_t *>(p.C) + off * elem, to + lane * row_bytes,
-                           static_cast<uint32_t>(width * elem));
+              for (int k = 0; k < 16; ++k)
+                if (k >= h && k < h + rows)
+                  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at_lane + (k - h) * row_bytes),
+                               "f"(f[k])
+                               : "memory");
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at_lane + k * row_bytes),
+                             "h"(__bfloat16_as_ushort(__float2bfloat16_rn(f[k])))
+                             : "memory");
             }
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            fence_proxy_async_smem();
+            named_barrier_sync(3 + part, 128);
+            if (quad == 0) {
+              if (c0 + c + h + rows <= t.qn) {
+                // One box (as a copy for each row, 256 bytes at a time, results
+                // left at 2 TB/s).
+                if (lane == 0 && width > 0)
+                  store_box(&maps.c, to, n_cta, t.q0 + c0 + c + h, p.form == kWgrad ? t.g : 0);
+              } else {  // the segment ends here
+                const int row = c + h + static_cast<int>(lane);
+                const long long off = at - n + n_cta + row * p.c_ld;
+                if (static_cast<int>(lane) < rows && c0 + row < t.qn && width > 0 &&
+                    index_ok(kSiteCStore, off, width, p.c_extent))
+                  store_bulk(static_cast<uint8_t *>(p.C) + off * elem, to + lane * row_bytes,
+                             static_cast<uint32_t>(width * elem));
+              }
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
           }
         } else if (p.c_f32) {
           float *dst = static_cast<float *>(p.C);
@@ -936,7 +942,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
         }
       };
 
-      const int c_end = min(128, t.qn - c0);
+      const int c_end = min(C::kEpiCols, t.qn - c0);
       bool write = true;
       if (t.split) {
         // This item's sums to its slot; the item that completes the tile adds
@@ -1133,7 +1139,7 @@ template <class T, bool LMN, bool QMN>
 int launch(const SegMaps &maps, const SegTc &p, int pairs, cudaStream_t stream) {
   using C = Cfg<T>;
   auto *kernel = seg_tc_kernel<T, LMN, QMN>;
-  const int fixed = C::kStages * C::kStageBytes + C::kRawBytes + 2 * C::kOutBytes +
+  const int fixed = C::kStages * C::kStageBytes + C::kRawBytes + C::kEpiWarps / 4 * C::kOutBytes +
                     static_cast<int>(sizeof(Shared<C::kStages, C::kRawStages>)) + 1024;
   auto smem = [fixed](int entries) { return fixed + 8 * entries + 8; };
   static std::once_flag once;
@@ -1283,7 +1289,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
     }
     if (!ok) return kErrLaunch;
   }
-  if (p.c_rows && !encode(a.C, !p.c_f32, kHalf, 16, 1, false, &maps.c)) return kErrLaunch;
+  if (p.c_rows && !encode(a.C, !p.c_f32, kHalf, a.bf16 && p.c_f32 ? 8 : 16, 1, false, &maps.c)) return kErrLaunch;
 
   if (a.slots != nullptr && seg_tc_splits(a)) {
     p.slots = a.slots;
