@@ -165,12 +165,20 @@ struct SegMaps {
 struct Table {
   int *first;     // [entries + 1] tiles of the entries before
   int *row;       // [entries + 1] offsets, held to the rows there are
-  int width;      // most columns of a tile
+  int shift;      // most columns of a tile: 1 << shift
   int whole;      // tiles that are one work item each; the others are
   int splits;     // this many
 };
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// a / b for a >= 0, b > 0: the integer divisions of a tile's place in the list
+// would be half a microsecond in every role's way.
+__device__ __forceinline__ int quotient(int a, int b) {
+  if (a >= 1 << 22) return a / b;
+  const int q = static_cast<int>(__fdividef(static_cast<float>(a) + 0.5f, static_cast<float>(b)));
+  return q - (q * b > a) + ((q + 1) * b <= a);
+}
 
 __device__ __forceinline__ int matrix_of(const SegTc &p, int g) {
   const int z = p.index != nullptr ? p.index[g] : g;
@@ -193,7 +201,7 @@ __device__ __forceinline__ bool for_passes(const SegTc &p, const Tile &t, const 
 
 __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int item, Tile &o) {
   const int over = item - tab.whole;
-  const int t = over < 0 ? item : tab.whole + over / tab.splits;
+  const int t = over < 0 ? item : tab.whole + quotient(over, tab.splits);
   if (t >= tab.first[p.entries]) return false;
   int lo = 0, hi = p.entries;  // the entry whose tiles hold t
   while (hi - lo > 1) {
@@ -206,19 +214,19 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
   const int idx = t - tab.first[lo];
   const int r0 = tab.row[lo], rows = max(tab.row[lo + 1] - r0, 0);
   const int height = p.form == kWgrad ? p.K : rows;
-  const int tm = cdiv(height, tab.width);
+  const int tm = (height + (1 << tab.shift) - 1) >> tab.shift;
   // Groups of kRasterM row tiles, lane tiles in the outer loop, so that the
   // pairs at work at one time share operand tiles in L2.
-  const int group = idx / (kRasterM * p.tiles_n);
+  const int group = quotient(idx, kRasterM * p.tiles_n);
   const int m_first = group * kRasterM;
   const int across = min(kRasterM, tm - m_first);
   const int rem = idx - group * kRasterM * p.tiles_n;
-  const int mi = m_first + rem % across, ni = rem / across;
+  const int ni = quotient(rem, across), mi = m_first + rem - ni * across;
   // The segment's rows in tm equal parts (in steps the MMA allows), not whole
   // tiles and a rest: the pairs end together, and no tile is all operand
   // traffic and no work.
-  const int step = p.form == kWgrad ? 128 : kColStep;
-  const int part = cdiv(cdiv(height, tm), step) * step;
+  const int step = p.form == kWgrad ? 128 : kColStep;  // a power of two
+  const int part = (quotient(height + tm - 1, tm) + step - 1) & ~(step - 1);
   o.over = over;
   o.tile = t - tab.whole;
   o.g = lo;
@@ -246,8 +254,8 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
   o.split = over >= 0 && tab.splits > 1;
   if (o.split) {
     const int s = over - (t - tab.whole) * tab.splits;
-    o.b0 = static_cast<int>(static_cast<long long>(blocks) * s / tab.splits);
-    o.b1 = static_cast<int>(static_cast<long long>(blocks) * (s + 1) / tab.splits);
+    o.b0 = quotient(blocks * s, tab.splits);
+    o.b1 = quotient(blocks * (s + 1), tab.splits);
   } else {
     o.b0 = 0;
     o.b1 = blocks;
@@ -273,7 +281,7 @@ __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int
       best = i;
     }
   }
-  tab.width = kCols >> best;
+  tab.shift = 8 - best;
   const int n = tiles[best];
   tab.whole = n;
   tab.splits = 1;
@@ -548,7 +556,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
       const int g = g0 + static_cast<int>(lane);
       int own = 0;
       if (g < p.entries)
-        own = cdiv(p.form == kWgrad ? p.K : max(tab.row[g + 1] - tab.row[g], 0), tab.width) *
+        own = cdiv(p.form == kWgrad ? p.K : max(tab.row[g + 1] - tab.row[g], 0),
+                   1 << tab.shift) *
               p.tiles_n;
       int v = own;
 #pragma unroll
