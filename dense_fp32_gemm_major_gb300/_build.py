@@ -29,7 +29,7 @@ LIB_CHECKED = os.path.join(PKG, "libgemm_f32_checked.so")
 CHECKED_FLAGS = ["-DGEMM_F32_INDEX_CHECKS=1"]
 SOURCES = ["api.cu", "simt_gemm.cu", "tc_gemm.cu", "transpose.cu", "pack.cu", "reduce.cu",
            "probe.cu", "seg_api.cu", "seg_tc.cu",
-           "seg_pack.cu"]
+           "seg_pack.cu", "seg_rows.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

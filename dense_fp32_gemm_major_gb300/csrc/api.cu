@@ -405,7 +405,8 @@ long long take_index_faults(bool clear, gemm::IndexFault *first) {
   int (*const takers[])(gemm::IndexFault *, bool) = {
       gemm::tc_index_fault_take, gemm::simt_index_fault_take, gemm::pack_index_fault_take,
       gemm::transpose_index_fault_take, gemm::reduce_index_fault_take,
-      gemm::seg_tc_index_fault_take, gemm::seg_pack_index_fault_take};
+      gemm::seg_tc_index_fault_take, gemm::seg_pack_index_fault_take,
+      gemm::seg_rows_index_fault_take};
   long long total = 0;
   bool have = false;
   for (auto take : takers) {

@@ -97,7 +97,7 @@ class Workspace {
 
   // Room for splitting the tiles of a product of this shape.
   void splits(const SegArgs &a) {
-    if (gemm::seg_tc_splits(a)) split_ = true;
+    if (gemm::seg_tc_splits(a) && !gemm::seg_rows_fits(a)) split_ = true;
   }
 
   // Allocate, place, zero the split tiles' counters, and copy.
@@ -124,6 +124,7 @@ class Workspace {
 
   // One product, with the scratch it may want.
   int launch(SegArgs &a, cudaStream_t s) {
+    if (gemm::seg_rows_fits(a)) return gemm::seg_rows_launch(a, s);
     if (split_) {
       a.slots = slots_;
       a.arrived = arrived_ + static_cast<size_t>(products_++ % kProducts) * sms_;
@@ -194,9 +195,14 @@ struct Lora {
     w.readable(W);
     SegArgs shape;
     shape.bf16 = bf16;
+    shape.dense = true;
+    shape.M = M;
     shape.K = K;
     w.splits(shape);
     if (!adapted) return;
+    shape.dense = false;
+    shape.groups = segments;
+    w.splits(shape);
     w.readable(A);
     w.readable(B);
     // bf16: U is an operand of the second product, and rounded to one bf16 it

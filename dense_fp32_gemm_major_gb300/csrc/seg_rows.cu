@@ -1,0 +1,318 @@
+// seg_rows.cu -- segmented products of very few rows: single tokens.
+//
+//   rows, dense:  C[t, n] = s_z sum_k A[t, k] op(B_z)[k, n] (+ add[t, n])
+//
+// With one or two rows a segment the product is a reading of B: its bytes at
+// the rate of memory, or, where they are few, the latency of one way to memory
+// and back. The tensor-core kernels' set-up, TMEM and hand-overs take longer
+// than that, so up to four rows of a segment go to one CTA of plain FMAs that
+// has nothing to set up:
+//
+//   B stored K x N: a thread holds 16 bytes of n; TX threads span the CTA's
+//     columns, the others share k, eight rows of B each at a time (eight
+//     loads in flight), and their sums meet in shared memory in a fixed order.
+//   B stored N x K: a warp holds four n, its lanes share k (four loads in
+//     flight) and add by shuffles.
+//
+// Few columns a CTA (16, 64 or 256 of bf16) make many CTAs of short loops:
+// 1 x 512 x 512 float32 is sixteen CTAs of two rounds of loads.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "segments.h"
+
+namespace gemm {
+namespace {
+
+constexpr int kThreads = 256, kRows = 4, kDeep = 8, kWarpN = 4;
+
+struct P {
+  const void *A, *A_lo, *B;
+  void *C, *C_lo;
+  const float *add, *scales;
+  const int64_t *offsets;
+  const int32_t *index;
+  long long a_ld, a_lo_ld, b_ld, b_stride, c_ld, c_lo_ld, add_ld;
+  long long a_extent, b_extent, c_extent, c_lo_extent, add_extent, a_lo_extent;
+  int M, N, K, groups, bank, dense, c_f32;
+};
+
+template <class T>
+struct Vec {
+  static constexpr int n = 16 / sizeof(T);
+};
+
+// 16 bytes from p + off as floats, those at or past `left` zero.
+template <class T>
+__device__ __forceinline__ void load16(const T *p, long long off, int left, int site,
+                                       long long extent, float (&v)[Vec<T>::n]) {
+  constexpr int n = Vec<T>::n;
+  if (left >= n && index_ok(site, off, n, extent)) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p + off));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (n == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      v[i] = i < left && index_ok(site, off + i, 1, extent) ? static_cast<float>(p[off + i]) : 0.0f;
+  }
+}
+
+// One value of A: the sum of its terms.
+template <class T>
+__device__ __forceinline__ float load_a(const P &p, long long row, int k) {
+  float v = 0.0f;
+  const long long at = row * p.a_ld + k;
+  if (index_ok(kSiteLoadA, at, 1, p.a_extent)) v = static_cast<float>(static_cast<const T *>(p.A)[at]);
+  if (p.A_lo != nullptr) {
+    const long long lo = row * p.a_lo_ld + k;
+    if (index_ok(kSiteLoadA, lo, 1, p.a_lo_extent))
+      v += static_cast<float>(static_cast<const T *>(p.A_lo)[lo]);
+  }
+  return v;
+}
+
+// Rows [t, t + count) that this CTA computes, and their matrix (-1: none):
+// blockIdx.y is a row; every fourth of a segment takes those behind it.
+__device__ __forceinline__ bool rows_of(const P &p, int *count, int *z, bool *added) {
+  const int t = blockIdx.y;
+  int first = 0, last = p.M;
+  *z = 0;
+  *added = true;
+  if (p.offsets != nullptr) {
+    __shared__ int below;
+    if (threadIdx.x == 0) below = 0;
+    __syncthreads();
+    int c = 0;
+    for (int i = threadIdx.x; i <= p.groups; i += kThreads) c += p.offsets[i] <= t;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if ((threadIdx.x & 31) == 0 && c > 0) atomicAdd(&below, c);
+    __syncthreads();
+    const int g = below - 1;
+    const bool inside = g >= 0 && g < p.groups;
+    if (p.dense) {
+      *added = inside;  // all rows, but an addend for the segments'
+    } else {
+      if (!inside) return false;
+      const long long a = p.offsets[g], b = p.offsets[g + 1];
+      first = static_cast<int>(a < 0 ? 0 : a);
+      last = static_cast<int>(b > p.M ? p.M : b);
+      if (t < first || t >= last) return false;
+      *z = p.index != nullptr ? p.index[g] : g;
+      if (*z < 0 || *z >= p.bank) *z = -1;
+    }
+  }
+  // A dense product's rows may differ in having an addend: one row each then.
+  const int step = p.dense && p.add != nullptr ? 1 : kRows;
+  if ((t - first) % step != 0) return false;
+  *count = min(step, last - t);
+  return true;
+}
+
+template <class T>
+__device__ __forceinline__ void store(const P &p, int row, int n, float v, int z, bool added) {
+  if (!p.dense && p.scales != nullptr && z >= 0) v *= p.scales[z];
+  if (p.add != nullptr && added) {
+    const long long at = row * p.add_ld + n;
+    if (index_ok(kSitePartialRead, at, 1, p.add_extent)) v += p.add[at];
+  }
+  const long long at = row * p.c_ld + n;
+  if (!index_ok(kSiteCStore, at, 1, p.c_extent)) return;
+  if (p.c_f32) {
+    static_cast<float *>(p.C)[at] = v;
+    return;
+  }
+  const __nv_bfloat16 h = __float2bfloat16_rn(v);
+  static_cast<__nv_bfloat16 *>(p.C)[at] = h;
+  if (p.C_lo != nullptr) {
+    const long long lo = row * p.c_lo_ld + n;
+    if (index_ok(kSitePartialWrite, lo, 1, p.c_lo_extent))
+      static_cast<__nv_bfloat16 *>(p.C_lo)[lo] = __float2bfloat16_rn(v - static_cast<float>(h));
+  }
+}
+
+// B stored K x N. TX threads of 16 bytes across the CTA's columns.
+template <class T, int TX>
+__global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
+  constexpr int V = Vec<T>::n, TY = kThreads / TX, NT = TX * V;
+  __shared__ float sums[TY * NT];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int count, z;
+  bool added;
+  if (!rows_of(p, &count, &z, &added)) return;
+  const int t = blockIdx.y, n0 = blockIdx.x * NT;
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, n = n0 + tx * V;
+  float acc[kRows][V] = {};
+  if (z >= 0 && n < p.N) {
+    const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
+    const long long extent = p.b_extent - z * p.b_stride;
+    for (int k0 = ty * kDeep; k0 < p.K; k0 += TY * kDeep) {
+      float b[kDeep][V];
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j)
+        load16<T>(B, (k0 + j) * p.b_ld + n, k0 + j < p.K ? p.N - n : 0, kSiteLoadB, extent, b[j]);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (r < count) {
+#pragma unroll
+          for (int j = 0; j < kDeep; ++j) {
+            const float a = k0 + j < p.K ? load_a<T>(p, t + r, k0 + j) : 0.0f;
+            // (rows of B past K read as zero: a zero as well)
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[r][v] = fmaf(a, b[j][v], acc[r][v]);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (r >= count) break;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[ty * NT + tx * V + v] = acc[r][v];
+    __syncthreads();
+    for (int c = threadIdx.x; c < NT; c += kThreads) {
+      float s = 0.0f;
+#pragma unroll 8
+      for (int y = 0; y < TY; ++y) s += sums[y * NT + c];
+      if (n0 + c < p.N) store<T>(p, t + r, n0 + c, s, z, added);
+    }
+    __syncthreads();
+  }
+}
+
+// B stored N x K. A warp takes kWarpN columns.
+template <class T>
+__global__ void __launch_bounds__(kThreads) seg_rows_nk_kernel(const P p) {
+  constexpr int V = Vec<T>::n;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int count, z;
+  bool added;
+  if (!rows_of(p, &count, &z, &added)) return;
+  const int t = blockIdx.y, lane = threadIdx.x & 31;
+  const int n0 = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpN;
+  if (n0 >= p.N) return;
+  float acc[kRows][kWarpN] = {};
+  if (z >= 0) {
+    const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
+    const long long extent = p.b_extent - z * p.b_stride;
+    for (int k0 = lane * V; k0 < p.K; k0 += 32 * V) {
+      float b[kWarpN][V];
+#pragma unroll
+      for (int j = 0; j < kWarpN; ++j)
+        load16<T>(B, static_cast<long long>(n0 + j) * p.b_ld + k0, n0 + j < p.N ? p.K - k0 : 0,
+                  kSiteLoadB, extent, b[j]);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (r < count) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float a = k0 + v < p.K ? load_a<T>(p, t + r, k0 + v) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kWarpN; ++j) acc[r][j] = fmaf(a, b[j][v], acc[r][j]);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    if (r < count) {
+#pragma unroll
+      for (int j = 0; j < kWarpN; ++j) {
+        float s = acc[r][j];
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        if (lane == 0 && n0 + j < p.N) store<T>(p, t + r, n0 + j, s, z, added);
+      }
+    }
+}
+
+long long extent_of(const SegMatrix &m) {
+  return (m.count - 1) * m.stride + matrix_extent(m.rows, m.cols, m.ld);
+}
+
+template <class K>
+int launch(K kernel, const P &p, int columns, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.N + columns - 1) / columns),
+                     static_cast<unsigned>(p.M), 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? kOk : kErrLaunch;
+}
+
+template <class T>
+int launch_type(const P &p, int transb, cudaStream_t stream) {
+  constexpr int V = Vec<T>::n;
+  if (transb) return launch(seg_rows_nk_kernel<T>, p, kThreads / 32 * kWarpN, stream);
+  // A short contraction has no work for many threads along k; a narrow result
+  // none for many along n.
+  if (p.K <= 64) return launch(seg_rows_kn_kernel<T, 32>, p, 32 * V, stream);
+  if (p.N <= 2 * V) return launch(seg_rows_kn_kernel<T, 2>, p, 2 * V, stream);
+  return launch(seg_rows_kn_kernel<T, 8>, p, 8 * V, stream);
+}
+
+}  // namespace
+
+GEMM_INDEX_FAULT_TAKE(seg_rows_index_fault_take)
+
+bool seg_rows_fits(const SegArgs &a) {
+  // All rows together few, or the segments' (about two each, at most).
+  return !a.wgrad && a.R == 0 && a.K > 0 &&
+         (a.M <= 2 * kRows || (!a.dense && a.M <= 2 * a.groups && a.M <= 512));
+}
+
+int seg_rows_launch(const SegArgs &a, cudaStream_t stream) {
+  P p = {};
+  p.A = a.A.p;
+  p.A_lo = a.A_lo.p;
+  p.B = a.B.p;
+  p.C = const_cast<void *>(a.C.p);
+  p.C_lo = const_cast<void *>(a.C_lo.p);
+  p.add = static_cast<const float *>(a.add.p);
+  p.scales = a.scales;
+  p.offsets = !a.dense || a.add.p != nullptr ? a.offsets : nullptr;
+  p.index = a.index;
+  p.a_ld = a.A.ld;
+  p.a_lo_ld = a.A_lo.ld;
+  p.b_ld = a.B.ld;
+  p.b_stride = a.B.stride;
+  p.c_ld = a.C.ld;
+  p.c_lo_ld = a.C_lo.ld;
+  p.add_ld = a.add.ld;
+  p.a_extent = extent_of(a.A);
+  p.a_lo_extent = extent_of(a.A_lo);
+  p.b_extent = extent_of(a.B);
+  p.c_extent = extent_of(a.C);
+  p.c_lo_extent = extent_of(a.C_lo);
+  p.add_extent = extent_of(a.add);
+  p.M = static_cast<int>(a.M);
+  p.N = static_cast<int>(a.N);
+  p.K = static_cast<int>(a.K);
+  p.groups = static_cast<int>(a.groups);
+  p.bank = static_cast<int>(a.bank);
+  p.dense = a.dense;
+  p.c_f32 = !a.bf16 || a.c_f32;
+  return a.bf16 ? launch_type<__nv_bfloat16>(p, a.transb, stream)
+                : launch_type<float>(p, a.transb, stream);
+}
+
+}  // namespace gemm

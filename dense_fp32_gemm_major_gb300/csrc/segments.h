@@ -62,6 +62,13 @@ bool seg_tc_readable(const SegMatrix &m, bool bf16);
 // Operands readable; M, N >= 1 (rows) or groups, N, K >= 1 (wgrad).
 int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
 
+// Products of very few rows (rows and dense forms): whether these arguments are
+// such a product, and its launch. Operands readable.
+bool seg_rows_fits(const SegArgs &a);
+int seg_rows_launch(const SegArgs &a, cudaStream_t stream);
+
+int seg_rows_index_fault_take(IndexFault *out, bool clear);
+
 // Copies a stack of matrices, of equal shape, to another pitch and stride.
 // offsets: only rows that the segments hold (by_matrix: only the matrices of
 // segments that have rows).
