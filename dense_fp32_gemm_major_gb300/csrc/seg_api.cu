@@ -183,14 +183,11 @@ struct Lora {
   // projection's tiles add? An MMA over rows of several segments would let one
   // adapter's NaN or infinity into the others' rows (0 * inf), so the fused
   // form's tiles are the segments' own: each segment reads W again, from L2.
-  // With 128 rows a segment and more, and enough tiles (two rounds at least)
-  // that the segments' part tiles do not make a round more, that costs less
-  // than U B's way through memory: 8192 rows, nine segments, 4096 x 4096, rank
-  // 64 bf16 259 -> 219 us, but 2048 rows, four segments, 2048 x 2048 float32 105
-  // -> 130 us; 32 rows in 32 segments would read W 32 times.
-  void prepare(Workspace &w, int sms) {
-    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
-    fused = adapted && K > 0 && transw == transl && M >= 128 * segments && tiles >= sms;
+  // With 128 rows a segment and more that costs less than U B's way through
+  // memory (8192 rows, nine segments, 4096 x 4096, rank 64 bf16: 259 -> 219 us);
+  // 32 rows in 32 segments would read W 32 times.
+  void prepare(Workspace &w) {
+    fused = adapted && K > 0 && transw == transl && M >= 128 * segments;
     w.readable(X);
     w.readable(W);
     SegArgs shape;
@@ -396,7 +393,7 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
   if (st != gemm::kOk) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Workspace work(l.bf16, offsets, segments, M);
-  l.prepare(work, sms);
+  l.prepare(work);
   st = work.take(sms, s);
   if (st == gemm::kOk) st = l.run(work, s);
   return work.give_back(st, s);
@@ -466,7 +463,7 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
     shape.wgrad = true;
     shape.M = M;
     work.splits(shape);
-    l.prepare(work, sms);
+    l.prepare(work);
     if (l.adapted) {
       work.readable(x);
       work.readable(u);

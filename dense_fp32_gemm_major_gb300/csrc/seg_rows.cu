@@ -28,6 +28,7 @@ namespace gemm {
 namespace {
 
 constexpr int kThreads = 256, kRows = 4, kDeep = 8, kWarpN = 4;
+constexpr int kStaged = 8192;  // values of A that stand in shared memory at a time
 
 struct P {
   const void *A, *A_lo, *B;
@@ -84,47 +85,72 @@ __device__ __forceinline__ float load_a(const P &p, long long row, int k) {
   return v;
 }
 
-// Rows [t, t + count) that this CTA computes, and their matrix (-1: none):
-// blockIdx.y is a row; every fourth of a segment takes those behind it.
-__device__ __forceinline__ bool rows_of(const P &p, int *count, int *z, bool *added) {
+// k of A that stand in shared memory at a time, for `count` rows.
+__device__ __forceinline__ int chunk_of(int count) {
+  return count == 1 ? kStaged : (count == 2 ? kStaged / 2 : kStaged / 4);
+}
+
+// Rows [t, t + count) of A, k [k0, k0 + chunk), as floats.
+template <class T>
+__device__ __forceinline__ void stage_a(const P &p, float *as, int t, int count, int k0, int chunk) {
+  const int n = min(chunk, p.K - k0), end = (n + kDeep - 1) / kDeep * kDeep;
+  for (int r = 0; r < count; ++r)
+    for (int k = threadIdx.x; k < end; k += kThreads)
+      as[r * chunk + k] = k < n ? load_a<T>(p, t + r, k0 + k) : 0.0f;
+}
+
+// Rows [t, t + count) that this CTA computes, their matrix (-1: none), its
+// scale, and whether they have an addend: blockIdx.y is a row; every fourth of
+// a segment takes those behind it.
+struct Rows {
+  int count, z;
+  float scale;
+  bool added;
+};
+
+__device__ __forceinline__ bool rows_of(const P &p, Rows *o) {
   const int t = blockIdx.y;
   int first = 0, last = p.M;
-  *z = 0;
-  *added = true;
+  o->z = 0;
+  o->scale = 1.0f;
+  o->added = true;
   if (p.offsets != nullptr) {
-    __shared__ int below;
-    if (threadIdx.x == 0) below = 0;
+    // Each thread looks at its segments; all loads are on their way at once.
+    __shared__ int found[3];
+    if (threadIdx.x == 0) found[0] = -1;
     __syncthreads();
-    int c = 0;
-    for (int i = threadIdx.x; i <= p.groups; i += kThreads) c += p.offsets[i] <= t;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if ((threadIdx.x & 31) == 0 && c > 0) atomicAdd(&below, c);
+    for (int g = threadIdx.x; g < p.groups; g += kThreads) {
+      const long long a = p.offsets[g], b = p.offsets[g + 1];
+      const int z = p.index != nullptr ? p.index[g] : g;
+      if (a <= t && t < b) {
+        found[1] = static_cast<int>(a < 0 ? 0 : a);
+        found[2] = static_cast<int>(b > p.M ? p.M : b);
+        found[0] = z >= 0 && z < p.bank ? z : p.bank;  // bank: none
+      }
+    }
     __syncthreads();
-    const int g = below - 1;
-    const bool inside = g >= 0 && g < p.groups;
+    const bool inside = found[0] >= 0;
     if (p.dense) {
-      *added = inside;  // all rows, but an addend for the segments'
+      o->added = inside;  // all rows, but an addend for the segments'
     } else {
       if (!inside) return false;
-      const long long a = p.offsets[g], b = p.offsets[g + 1];
-      first = static_cast<int>(a < 0 ? 0 : a);
-      last = static_cast<int>(b > p.M ? p.M : b);
-      if (t < first || t >= last) return false;
-      *z = p.index != nullptr ? p.index[g] : g;
-      if (*z < 0 || *z >= p.bank) *z = -1;
+      first = found[1];
+      last = found[2];
+      o->z = found[0] < p.bank ? found[0] : -1;
+      if (p.scales != nullptr && o->z >= 0) o->scale = p.scales[o->z];
     }
   }
   // A dense product's rows may differ in having an addend: one row each then.
   const int step = p.dense && p.add != nullptr ? 1 : kRows;
   if ((t - first) % step != 0) return false;
-  *count = min(step, last - t);
+  o->count = min(step, last - t);
   return true;
 }
 
 template <class T>
-__device__ __forceinline__ void store(const P &p, int row, int n, float v, int z, bool added) {
-  if (!p.dense && p.scales != nullptr && z >= 0) v *= p.scales[z];
-  if (p.add != nullptr && added) {
+__device__ __forceinline__ void store(const P &p, int row, int n, float v, const Rows &o) {
+  v *= o.scale;
+  if (p.add != nullptr && o.added) {
     const long long at = row * p.add_ld + n;
     if (index_ok(kSitePartialRead, at, 1, p.add_extent)) v += p.add[at];
   }
@@ -148,33 +174,40 @@ template <class T, int TX>
 __global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
   constexpr int V = Vec<T>::n, TY = kThreads / TX, NT = TX * V;
   __shared__ float sums[TY * NT];
+  __shared__ float as[kStaged];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int count, z;
-  bool added;
-  if (!rows_of(p, &count, &z, &added)) return;
+  Rows o;
+  if (!rows_of(p, &o)) return;
+  const int count = o.count, z = o.z;
   const int t = blockIdx.y, n0 = blockIdx.x * NT;
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, n = n0 + tx * V;
   float acc[kRows][V] = {};
-  if (z >= 0 && n < p.N) {
+  if (z >= 0) {
     const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
     const long long extent = p.b_extent - z * p.b_stride;
-    for (int k0 = ty * kDeep; k0 < p.K; k0 += TY * kDeep) {
-      float b[kDeep][V];
+    const int chunk = chunk_of(count);
+    for (int c0 = 0; c0 < p.K; c0 += chunk) {
+      const int c1 = min(chunk, p.K - c0);
+      if (c0 > 0) __syncthreads();
+      stage_a<T>(p, as, t, count, c0, chunk);
+      __syncthreads();
+#pragma unroll 2
+      for (int k = ty * kDeep; k < c1; k += TY * kDeep) {
+        float b[kDeep][V];
 #pragma unroll
-      for (int j = 0; j < kDeep; ++j)
-        load16<T>(B, (k0 + j) * p.b_ld + n, k0 + j < p.K ? p.N - n : 0, kSiteLoadB, extent, b[j]);
+        for (int j = 0; j < kDeep; ++j)
+          load16<T>(B, static_cast<long long>(c0 + k + j) * p.b_ld + n, k + j < c1 ? p.N - n : 0,
+                    kSiteLoadB, extent, b[j]);
 #pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if (r < count) {
+        for (int r = 0; r < kRows; ++r)
+          if (r < count) {
 #pragma unroll
-          for (int j = 0; j < kDeep; ++j) {
-            const float a = k0 + j < p.K ? load_a<T>(p, t + r, k0 + j) : 0.0f;
-            // (rows of B past K read as zero: a zero as well)
+            for (int j = 0; j < kDeep; ++j)
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[r][v] = fmaf(a, b[j][v], acc[r][v]);
+              for (int v = 0; v < V; ++v) acc[r][v] = fmaf(as[r * chunk + k + j], b[j][v], acc[r][v]);
           }
-        }
+      }
     }
   }
 #pragma unroll
@@ -187,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
       float s = 0.0f;
 #pragma unroll 8
       for (int y = 0; y < TY; ++y) s += sums[y * NT + c];
-      if (n0 + c < p.N) store<T>(p, t + r, n0 + c, s, z, added);
+      if (n0 + c < p.N) store<T>(p, t + r, n0 + c, s, o);
     }
     __syncthreads();
   }
@@ -199,32 +232,38 @@ __global__ void __launch_bounds__(kThreads) seg_rows_nk_kernel(const P p) {
   constexpr int V = Vec<T>::n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int count, z;
-  bool added;
-  if (!rows_of(p, &count, &z, &added)) return;
+  Rows o;
+  if (!rows_of(p, &o)) return;
+  const int count = o.count, z = o.z;
   const int t = blockIdx.y, lane = threadIdx.x & 31;
   const int n0 = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpN;
-  if (n0 >= p.N) return;
+  __shared__ float as[kStaged];
   float acc[kRows][kWarpN] = {};
   if (z >= 0) {
     const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
     const long long extent = p.b_extent - z * p.b_stride;
-    for (int k0 = lane * V; k0 < p.K; k0 += 32 * V) {
-      float b[kWarpN][V];
+    const int chunk = chunk_of(count);
+    for (int c0 = 0; c0 < p.K; c0 += chunk) {
+      const int c1 = min(chunk, p.K - c0);
+      if (c0 > 0) __syncthreads();
+      stage_a<T>(p, as, t, count, c0, chunk);
+      __syncthreads();
+#pragma unroll 2
+      for (int k = lane * V; k < c1; k += 32 * V) {
+        float b[kWarpN][V];
 #pragma unroll
-      for (int j = 0; j < kWarpN; ++j)
-        load16<T>(B, static_cast<long long>(n0 + j) * p.b_ld + k0, n0 + j < p.N ? p.K - k0 : 0,
-                  kSiteLoadB, extent, b[j]);
+        for (int j = 0; j < kWarpN; ++j)
+          load16<T>(B, static_cast<long long>(n0 + j) * p.b_ld + c0 + k,
+                    n0 + j < p.N ? c1 - k : 0, kSiteLoadB, extent, b[j]);
 #pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if (r < count) {
+        for (int r = 0; r < kRows; ++r)
+          if (r < count) {
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float a = k0 + v < p.K ? load_a<T>(p, t + r, k0 + v) : 0.0f;
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int j = 0; j < kWarpN; ++j) acc[r][j] = fmaf(a, b[j][v], acc[r][j]);
+              for (int j = 0; j < kWarpN; ++j) acc[r][j] = fmaf(as[r * chunk + k + v], b[j][v], acc[r][j]);
           }
-        }
+      }
     }
   }
 #pragma unroll
@@ -235,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) seg_rows_nk_kernel(const P p) {
         float s = acc[r][j];
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        if (lane == 0 && n0 + j < p.N) store<T>(p, t + r, n0 + j, s, z, added);
+        if (lane == 0 && n0 + j < p.N) store<T>(p, t + r, n0 + j, s, o);
       }
     }
 }

@@ -68,7 +68,7 @@ constexpr int kMaxSplits = 16;
 // Splitting a tile along k costs about 4 us (the sums' way through memory, and
 // the counters' zeros before the launch); blocks take 0.3 us (bf16) and up to 2
 // us (float32). Fewest blocks of an item, and of a contraction worth splitting.
-constexpr int kItemBlocksBf16 = 8, kItemBlocksF32 = 4, kSplitBlocksBf16 = 32, kSplitBlocksF32 = 8;
+constexpr int kItemBlocksBf16 = 8, kItemBlocksF32 = 3, kSplitBlocksBf16 = 32, kSplitBlocksF32 = 8;
 constexpr uint32_t kTmemCols = 512;
 
 enum Form : int { kRows = 0, kDense = 1, kAdapted = 2, kWgrad = 3 };
@@ -263,38 +263,40 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
   return true;
 }
 
-// How the list is cut, from its tiles at each width (every CTA finds the same).
-// A round of tiles takes nearly the same time at every width (a block of 64 k
-// and 256, 128, 64 columns: bf16 302, 282, 275 ns, float32 1.99, 1.72, 1.55 us),
-// so narrower tiles pay only where they fill pairs that would be idle. Tiles
-// past the last full round that leave half the pairs idle are split along k.
+// How the list is cut, from its tiles at each width (every CTA finds the same):
+// by the time it should take, in microseconds.
+//
+// A block of 64 k takes nearly the same at every width (256, 128, 64 columns:
+// bf16 0.302, 0.282, 0.275, float32 1.99, 1.72, 1.55), so narrower tiles pay
+// only where they fill pairs that would be idle. Tiles past the last full round
+// can be split along k where that leaves every pair at most one item; the item
+// that completes a tile reads the others' sums at the rate of one SM (256
+// columns: 128 KB a CTA, about 1.05 us, an item), so the best number of items
+// is the root of the tile's time over that, and few columns allow many.
 template <bool SPLIT>
 __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int longest, int pairs,
                                            Table &tab) {
-  constexpr long long kFixed = SPLIT ? 640 : 1800;  // of a round, in columns
-  int best = 0;
-  long long cost = 0;
+  constexpr float kBlockUs = SPLIT ? 2.0f : 0.3f, kFixedCols = SPLIT ? 640.0f : 1800.0f;
+  const int blocks = p.passes * cdiv(p.form == kWgrad ? longest : p.K, kBlock);
+  const int rows = p.form == kWgrad ? p.K : longest;
+  float best = 0.0f;
   for (int i = 0; i < (p.form == kWgrad ? 2 : 3); ++i) {
-    const long long c = cdiv(tiles[i], pairs) * ((kCols >> i) + kFixed);
-    if (i == 0 || (c < cost && tiles[i] != tiles[best])) {
-      cost = c;
-      best = i;
+    const int n = tiles[i], rest = n % pairs, width = kCols >> i;
+    if (i > 0 && n == tiles[i - 1]) continue;
+    const float tile = blocks * kBlockUs * (width + kFixedCols) / (kCols + kFixedCols);
+    const float item = 1.05f * static_cast<float>(min(width, rows)) / kCols;  // its sums' reading
+    int splits = 1;
+    if (rest > 0 && p.slots != nullptr) {
+      splits = min(static_cast<int>(sqrtf(tile / item)), pairs / rest);
+      splits = min(min(splits, kMaxSplits), blocks / (SPLIT ? kItemBlocksF32 : kItemBlocksBf16));
+      splits = max(splits, 1);
     }
-  }
-  tab.shift = 8 - best;
-  const int n = tiles[best];
-  tab.whole = n;
-  tab.splits = 1;
-  if (p.slots != nullptr) {
-    const int rest = n % pairs;
-    const int k = p.form == kWgrad ? longest : p.K;
-    const int splits =
-        rest > 0 ? min(min(pairs / rest, p.passes * cdiv(k, kBlock) /
-                                              (SPLIT ? kItemBlocksF32 : kItemBlocksBf16)),
-                       kMaxSplits)
-                 : 1;
-    if (splits > 1) {
-      tab.whole = n - rest;
+    const float last = rest == 0 ? 0.0f : (splits > 1 ? tile / splits + splits * item + 3.0f : tile);
+    const float time = static_cast<float>(n / pairs) * tile + last;
+    if (i == 0 || time < best) {
+      best = time;
+      tab.shift = 8 - i;
+      tab.whole = splits > 1 ? n - rest : n;
       tab.splits = splits;
     }
   }
@@ -954,8 +956,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
       const int c_end = min(C::kEpiCols, t.qn - c0);
       bool write = true;
       if (t.split) {
-        // This item's sums to its slot; the item that completes the tile adds
-        // them all, always in the same order.
+        // This item's sums to its slot (lanes of a column side by side); the
+        // item that completes the tile adds them all, always in the same order.
         constexpr long long kSlotCta = static_cast<long long>(kCols) * kHalf;
         const long long mine = static_cast<long long>(rank) * kSlotCta +
                                static_cast<long long>(c0) * kHalf + quad * 32 + lane;
