@@ -184,10 +184,16 @@ struct Lora {
   // adapter's NaN or infinity into the others' rows (0 * inf), so the fused
   // form's tiles are the segments' own: each segment reads W again, from L2.
   // With 128 rows a segment and more that costs less than U B's way through
-  // memory (8192 rows, nine segments, 4096 x 4096, rank 64 bf16: 259 -> 219 us);
-  // 32 rows in 32 segments would read W 32 times.
-  void prepare(Workspace &w) {
-    fused = adapted && K > 0 && transw == transl && M >= 128 * segments;
+  // memory (8192 rows, nine segments, 4096 x 4096, rank 64 bf16: 259 -> 219 us;
+  // 1531 rows, seven segments, 1000 x 2048, rank 24: 131 -> 107 us with its
+  // backward pass) -- but a round of float32 tiles more, which the segments'
+  // part tiles can make, costs more where there are few (2048 rows, four
+  // segments, 2048 x 2048: 105 -> 130 us); 32 rows in 32 segments would read W
+  // 32 times.
+  void prepare(Workspace &w, int sms) {
+    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
+    fused = adapted && K > 0 && transw == transl && M >= 128 * segments &&
+            (bf16 || tiles >= sms);
     w.readable(X);
     w.readable(W);
     SegArgs shape;
@@ -393,7 +399,7 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
   if (st != gemm::kOk) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Workspace work(l.bf16, offsets, segments, M);
-  l.prepare(work);
+  l.prepare(work, sms);
   st = work.take(sms, s);
   if (st == gemm::kOk) st = l.run(work, s);
   return work.give_back(st, s);
@@ -463,7 +469,7 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
     shape.wgrad = true;
     shape.M = M;
     work.splits(shape);
-    l.prepare(work);
+    l.prepare(work, sms);
     if (l.adapted) {
       work.readable(x);
       work.readable(u);

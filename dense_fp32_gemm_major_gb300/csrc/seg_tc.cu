@@ -277,6 +277,7 @@ template <bool SPLIT>
 __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int longest, int pairs,
                                            Table &tab) {
   constexpr float kBlockUs = SPLIT ? 2.0f : 0.3f, kFixedCols = SPLIT ? 640.0f : 1800.0f;
+  constexpr float kItemUs = SPLIT ? 14.0f : 6.0f;  // an item's start and end
   const int blocks = p.passes * cdiv(p.form == kWgrad ? longest : p.K, kBlock);
   const int rows = p.form == kWgrad ? p.K : longest;
   float best = 0.0f;
@@ -291,7 +292,7 @@ __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int
       splits = min(min(splits, kMaxSplits), blocks / (SPLIT ? kItemBlocksF32 : kItemBlocksBf16));
       splits = max(splits, 1);
     }
-    const float last = rest == 0 ? 0.0f : (splits > 1 ? tile / splits + splits * item + 3.0f : tile);
+    const float last = rest == 0 ? 0.0f : (splits > 1 ? tile / splits + splits * item + kItemUs : tile);
     const float time = static_cast<float>(n / pairs) * tile + last;
     if (i == 0 || time < best) {
       best = time;
