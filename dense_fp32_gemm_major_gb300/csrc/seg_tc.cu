@@ -123,9 +123,8 @@ struct Cfg {
   static constexpr int kOutBytes = kSplit ? 8192 : 4096;
   static constexpr int kMmaWarp = 1;
   static constexpr int kFixWarp = 2;
-  // Epilogue warps, and the columns of each: the longest way of a short tile
-  // (bf16, 16 blocks a tile: 118 us with eight of them, 99 with sixteen);
-  // float32 has registers for eight.
+  // Epilogue warps, and the columns of each. bf16: 8192 x 11008 x 4096 takes 444
+  // us with eight, 415 with sixteen; float32 has registers for eight.
   static constexpr int kEpiWarp0 = 4, kEpiWarps = kSplit ? 8 : 16;
   static constexpr int kEpiCols = kCols / (kEpiWarps / 4);
   static constexpr int kLoadWarp0 = 12, kLoadWarps = 8;

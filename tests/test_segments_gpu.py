@@ -171,6 +171,39 @@ def test_grouped_without_a_contraction_is_zero(g, dt):
     assert g.grouped_matmul(a[:0], b, offsets_of([0, 0])[0]).shape == (0, 9)
 
 
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+@pytest.mark.parametrize("transb", [False, True])
+@pytest.mark.parametrize("sizes, k, n", [([1], 9000, 24), ([2, 0, 1], 8200, 70), ([4, 1], 4200, 512),
+                                         ([0, 7], 2100, 33), ([1, 1, 0, 1], 6, 700)],
+                         ids=lambda v: str(v))
+def test_grouped_few_rows(g, sizes, k, n, transb, dt):
+    # single tokens and a few more, contractions longer than what is staged
+    off, o = offsets_of(sizes)
+    a = normal((o[-1], k), 73, dt)
+    b = normal((len(sizes),) + ((n, k) if transb else (k, n)), 74, dt)
+    c = g.grouped_matmul(a, b, off, transb)
+    check_grouped(c, a, b, o, transb, dt)
+    assert torch.equal(c, g.grouped_matmul(a, b, off, transb))
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_as_many_segments_as_a_call_takes(g, dt):
+    sizes = [i % 4 + (i % 97 == 0) * 30 for i in range(g.MAX_SEGMENTS)]
+    off, o = offsets_of(sizes)
+    a, b = normal((o[-1], 72), 75, dt), normal((g.MAX_SEGMENTS, 72, 24), 76, dt)
+    c = g.grouped_matmul(a, b, off)
+    rows = torch.repeat_interleave(torch.arange(g.MAX_SEGMENTS), torch.tensor(sizes)).cuda()
+    c64 = torch.einsum("tk,tkn->tn", a.double(), b.double()[rows])
+    s64 = torch.einsum("tk,tkn->tn", a.double().abs(), b.double().abs()[rows])
+    check(c, c64, rounding(c64, s64, 72, dt))
+    d = normal((o[-1], 24), 77, dt)
+    w = g.grouped_wgrad(a, d, off)
+    for i in (0, 1, 97, 1000, 2046, 2047):
+        c64, s64 = product(a[o[i]:o[i + 1]].t(), d[o[i]:o[i + 1]])
+        check(w[i], c64, rounding(c64, s64, sizes[i], dt))
+    assert (w[4] == 0).all() and (w[2044] == 0).all()  # empty segments
+
+
 @pytest.mark.parametrize("k", [256, 4096, 16384])
 def test_long_sums_are_as_exact_as_fp32(g, k):
     # Each of K adds rounded to nearest is off by at most 2^-24 of the running
@@ -215,6 +248,20 @@ def test_wgrad(g, sizes, k, n, dt):
     a, d = normal((m, k), 21, dt), normal((m, n), 22, dt)
     c = g.grouped_wgrad(a, d, off)
     assert c.shape == (len(sizes), k, n)
+    for i, s in enumerate(sizes):
+        c64, s64 = product(a[o[i]:o[i + 1]].t(), d[o[i]:o[i + 1]])
+        check(c[i], c64, rounding(c64, s64, s, dt), f"segment {i}")
+    assert torch.equal(c, g.grouped_wgrad(a, d, off))
+
+
+@pytest.mark.parametrize("sizes, k, n", [([3001, 50], 64, 96), ([2500, 2100], 300, 520),
+                                         ([5000], 24, 17)], ids=lambda v: str(v))
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_wgrad_long_segments(g, sizes, k, n, dt):
+    # few tiles and long sums: several work items a tile
+    off, o = offsets_of(sizes)
+    a, d = normal((o[-1], k), 26, dt), normal((o[-1], n), 27, dt)
+    c = g.grouped_wgrad(a, d, off)
     for i, s in enumerate(sizes):
         c64, s64 = product(a[o[i]:o[i + 1]].t(), d[o[i]:o[i + 1]])
         check(c[i], c64, rounding(c64, s64, s, dt), f"segment {i}")
@@ -269,6 +316,7 @@ LORA = [  # sizes, adapters (None: one each), bank, K, N, R
     ([100, 0, 157, 300], [3, 1, -1, 3], 4, 136, 520, 64), ([40, 30], None, 2, 77, 131, 3),
     ([64, 64, 128, 256, 1], [0, 1, 2, 1, 9], 3, 128, 256, 200), ([129], [0], 1, 1000, 301, 1),
     ([7] * 60, [i % 9 for i in range(60)], 9, 96, 72, 24),
+    ([1500, 700, 0, 1900], [1, -1, 0, 2], 3, 200, 2560, 40), ([900, 1100], None, 2, 1000, 264, 130),
 ]
 
 
@@ -394,6 +442,41 @@ def test_gradients_against_differences(g):
     assert abs((up.sum() - down.sum()) / 2 - got) <= 1e-4 * (up.abs().sum() + down.abs().sum())
 
 
+def test_graph_capture_and_replay(g):
+    # the workspace and its zeros are part of the capture
+    off, o = offsets_of([40, 0, 25])
+    x, w = normal((65, 2048), 71, torch.bfloat16), normal((2048, 96), 72, torch.bfloat16)
+    a, b = normal((3, 2048, 16), 73, torch.bfloat16), normal((3, 16, 96), 74, torch.bfloat16)
+    ref = g.lora_matmul(x, w, a, b, off)
+    out = torch.empty_like(ref)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.lora_matmul(x, w, a, b, off, out=out)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(out, ref)
+    x.mul_(2)  # exact in every rounding
+    graph.replay()
+    assert torch.equal(out, 2 * ref)
+
+
+def test_concurrent_streams(g):
+    off, o = offsets_of([64, 64])
+    jobs = [(normal((128, 4096), 80 + i, torch.float32), normal((2, 4096, 192), 90 + i, torch.float32))
+            for i in range(4)]
+    refs = [g.grouped_matmul(a, b, off) for a, b in jobs]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in jobs], []
+    for _ in range(5):
+        for s, (a, b) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                outs.append(g.grouped_matmul(a, b, off))
+    torch.cuda.synchronize()
+    for i, c in enumerate(outs):
+        assert torch.equal(c, refs[i % 4])
+
+
 def test_streams(g):
     # offsets made on the same side stream, right before the call
     a, b = normal((400, 256), 71, torch.bfloat16), normal((4, 256, 512), 72, torch.bfloat16)
@@ -461,3 +544,17 @@ def test_wrappers_refuse(g):
             call()
     with pytest.raises(g.GemmError):  # the result on its own operand
         g.grouped_matmul(x, b[:, :, :16], off, out=x)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_example_learns(g, dt):
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "expert_adapters.py")
+    spec = importlib.util.spec_from_file_location("expert_adapters", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses = example.train(dt, steps=12, tokens=700, width=128, hidden=256)
+    assert all(a == a for a in losses) and losses[-1] < 0.9 * losses[0]
