@@ -269,14 +269,14 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
 // bf16 0.302, 0.282, 0.275, float32 1.99, 1.72, 1.55), so narrower tiles pay
 // only where they fill pairs that would be idle. Tiles past the last full round
 // can be split along k where that leaves every pair at most one item; the item
-// that completes a tile reads the others' sums at the rate of one SM (256
-// columns: 128 KB a CTA, about 1.05 us, an item), so the best number of items
+// that completes a tile reads the others' sums, bound by their way through L2
+// (256 columns, 128 KB a CTA: about 2.1 us an item), so the best number of items
 // is the root of the tile's time over that, and few columns allow many.
 template <bool SPLIT>
 __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int longest, int pairs,
                                            Table &tab) {
   constexpr float kBlockUs = SPLIT ? 2.0f : 0.3f, kFixedCols = SPLIT ? 640.0f : 1800.0f;
-  constexpr float kItemUs = SPLIT ? 14.0f : 6.0f;  // an item's start and end
+  constexpr float kItemUs = SPLIT ? 9.0f : 5.0f;  // an item's start and end
   const int blocks = p.passes * cdiv(p.form == kWgrad ? longest : p.K, kBlock);
   const int rows = p.form == kWgrad ? p.K : longest;
   float best = 0.0f;
@@ -284,7 +284,7 @@ __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int
     const int n = tiles[i], rest = n % pairs, width = kCols >> i;
     if (i > 0 && n == tiles[i - 1]) continue;
     const float tile = blocks * kBlockUs * (width + kFixedCols) / (kCols + kFixedCols);
-    const float item = 1.05f * static_cast<float>(min(width, rows)) / kCols;  // its sums' reading
+    const float item = 2.1f * static_cast<float>(min(width, rows)) / kCols;  // its sums' reading
     int splits = 1;
     if (rest > 0 && p.slots != nullptr) {
       splits = min(static_cast<int>(sqrtf(tile / item)), pairs / rest);
@@ -956,24 +956,28 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
       const int c_end = min(C::kEpiCols, t.qn - c0);
       bool write = true;
       if (t.split) {
-        // This item's sums to its slot (lanes of a column side by side); the
-        // item that completes the tile adds them all, always in the same order.
+        // This item's sums to its slot: four columns of a lane together, lanes
+        // side by side. The item that completes the tile adds them all, always
+        // in the same order. Warps past the result's last column have none.
         constexpr long long kSlotCta = static_cast<long long>(kCols) * kHalf;
-        const long long mine = static_cast<long long>(rank) * kSlotCta +
-                               static_cast<long long>(c0) * kHalf + quad * 32 + lane;
+        const bool lanes = n - static_cast<int>(lane) < p.N;
+        const long long mine =
+            static_cast<long long>(rank) * kSlotCta +
+            (static_cast<long long>(c0 / 4) * kHalf + quad * 32 + lane) * 4;
         auto slot = [&](int s, int c) {
           return (static_cast<long long>(t.tile) * tab.splits + s) * 2 * kSlotCta + mine +
                  static_cast<long long>(c) * kHalf;
         };
         const int own = t.over - t.tile * tab.splits;
 #pragma unroll 1
-        for (int c = 0; c < c_end; c += 16) {
+        for (int c = 0; lanes && c < c_end; c += 16) {
           float f[16];
           load(c, f);
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (index_ok(kSitePartialWrite, slot(own, c + k), 1, p.slot_extent))
-              p.slots[slot(own, c + k)] = f[k];
+          for (int k = 0; k < 16; k += 4)
+            if (index_ok(kSitePartialWrite, slot(own, c + k), 4, p.slot_extent))
+              *reinterpret_cast<float4 *>(p.slots + slot(own, c + k)) =
+                  make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
         }
         __threadfence();
         named_barrier_sync(1, 32 * C::kEpiWarps);
@@ -990,12 +994,18 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             float f[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) f[k] = 0.0f;
-#pragma unroll 2
-            for (int s = 0; s < tab.splits; ++s)
+#pragma unroll 4
+            for (int s = 0; s < (lanes ? tab.splits : 0); ++s)
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (index_ok(kSitePartialRead, slot(s, c + k), 1, p.slot_extent))
-                  f[k] += __ldcg(p.slots + slot(s, c + k));
+              for (int k = 0; k < 16; k += 4)
+                if (index_ok(kSitePartialRead, slot(s, c + k), 4, p.slot_extent)) {
+                  const float4 v =
+                      __ldcg(reinterpret_cast<const float4 *>(p.slots + slot(s, c + k)));
+                  f[k] += v.x;
+                  f[k + 1] += v.y;
+                  f[k + 2] += v.z;
+                  f[k + 3] += v.w;
+                }
             finish(c, f);
           }
         }
