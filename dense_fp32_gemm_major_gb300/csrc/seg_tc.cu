@@ -83,7 +83,7 @@ struct SegTc {
   // adapted: A and B, then U (its terms) and the adapter's L.
   int passes;
   int tiles_n;
-  int q_box;         // lines per copy of a K-major Q
+  int q_box, q_shift;  // lines per copy of a K-major Q: 1 << q_shift
   int q_whole;       // wgrad, one pass: maps.q[2] brings all chunks of Q in one copy
   int l_whole, l_whole1;  // the MN-major L of pass 0, of the others, comes as one 4-D copy
   const int64_t *offsets;
@@ -140,6 +140,7 @@ struct Shared {
   int abort;
   int tiles[3];  // of width 256, 128, 64
   int longest;   // rows of the longest segment
+  int cut[3];    // Table::shift, whole, splits
   int last;      // this CTA's sums complete a split tile
 };
 
@@ -272,34 +273,40 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
 // that completes a tile reads the others' sums, bound by their way through L2
 // (256 columns, 128 KB a CTA: about 2.1 us an item), so the best number of items
 // is the root of the tile's time over that, and few columns allow many.
+// A whole warp: lane i looks at width 256 >> i.
 template <bool SPLIT>
 __device__ __forceinline__ void choose_cut(const SegTc &p, const int *tiles, int longest, int pairs,
-                                           Table &tab) {
+                                           int lane, Table &tab) {
   constexpr float kBlockUs = SPLIT ? 2.0f : 0.3f, kFixedCols = SPLIT ? 640.0f : 1800.0f;
   constexpr float kItemUs = SPLIT ? 9.0f : 5.0f;  // an item's start and end
+  constexpr float kPerCol = kBlockUs / (kCols + kFixedCols);
   const int blocks = p.passes * cdiv(p.form == kWgrad ? longest : p.K, kBlock);
   const int rows = p.form == kWgrad ? p.K : longest;
-  float best = 0.0f;
-  for (int i = 0; i < (p.form == kWgrad ? 2 : 3); ++i) {
-    const int n = tiles[i], rest = n % pairs, width = kCols >> i;
-    if (i > 0 && n == tiles[i - 1]) continue;
-    const float tile = blocks * kBlockUs * (width + kFixedCols) / (kCols + kFixedCols);
-    const float item = 2.1f * static_cast<float>(min(width, rows)) / kCols;  // its sums' reading
-    int splits = 1;
-    if (rest > 0 && p.slots != nullptr) {
-      splits = min(static_cast<int>(sqrtf(tile / item)), pairs / rest);
-      splits = min(min(splits, kMaxSplits), blocks / (SPLIT ? kItemBlocksF32 : kItemBlocksBf16));
-      splits = max(splits, 1);
-    }
-    const float last = rest == 0 ? 0.0f : (splits > 1 ? tile / splits + splits * item + kItemUs : tile);
-    const float time = static_cast<float>(n / pairs) * tile + last;
-    if (i == 0 || time < best) {
-      best = time;
-      tab.shift = 8 - i;
-      tab.whole = splits > 1 ? n - rest : n;
-      tab.splits = splits;
-    }
+  const int i = lane < (p.form == kWgrad ? 2 : 3) ? lane : 0;
+  const int n = tiles[i], width = kCols >> i;
+  const int rounds = quotient(n, pairs), rest = n - rounds * pairs;
+  const float tile = blocks * (width + kFixedCols) * kPerCol;
+  const float item = 2.1f / kCols * static_cast<float>(min(width, rows));  // its sums' reading
+  int splits = 1;
+  if (rest > 0 && p.slots != nullptr) {
+    splits = min(static_cast<int>(sqrtf(__fdividef(tile, item))), quotient(pairs, rest));
+    splits = min(min(splits, kMaxSplits), blocks / (SPLIT ? kItemBlocksF32 : kItemBlocksBf16));
+    splits = max(splits, 1);
   }
+  const float last =
+      rest == 0 ? 0.0f
+                : (splits > 1 ? __fdividef(tile, static_cast<float>(splits)) + splits * item + kItemUs
+                              : tile);
+  float time = static_cast<float>(rounds) * tile + last;
+  int best = 0;
+#pragma unroll
+  for (int q = 1; q < 3; ++q) {  // wider ones first: a tie is theirs
+    const float other = __shfl_sync(0xffffffffu, time, q), mine = __shfl_sync(0xffffffffu, time, best);
+    if (other < mine) best = q;
+  }
+  tab.shift = 8 - best;
+  tab.splits = __shfl_sync(0xffffffffu, splits, best);
+  tab.whole = __shfl_sync(0xffffffffu, splits > 1 ? n - rest : n, best);
 }
 
 // MMA columns of a tile: its own, in steps the operand's layout allows (an
@@ -478,7 +485,7 @@ __device__ __forceinline__ void set_registers() {
 // LMN, QMN: the operand lies with its lane (column) index contiguous.
 template <class T, bool LMN, bool QMN>
 __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
-    seg_tc_kernel(const __grid_constant__ SegMaps maps, const SegTc p) {
+    seg_tc_kernel(const __grid_constant__ SegMaps maps, const __grid_constant__ SegTc p) {
   using C = Cfg<T>;
   constexpr int STAGES = C::kStages, kBK = C::kBK, kOpBytes = C::kOpBytes;
   extern __shared__ uint8_t smem_raw[];
@@ -529,6 +536,12 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     tmem_alloc<2>(&sh->tmem_base, kTmemCols);
     tmem_relinquish<2>();
   }
+  // The arguments into the constant cache while the previous grid ends: the
+  // roles' first looks at them would each wait for memory.
+  for (uint32_t i = threadIdx.x; i < sizeof(SegTc) / 4; i += C::kThreads) {
+    const int touched = reinterpret_cast<const int *>(&p)[i];
+    asm volatile("" ::"r"(touched));
+  }
   grid_dependency_wait();
   // The table of segments: their rows, and the tiles before each.
   for (int g = threadIdx.x; g <= p.entries; g += C::kThreads) {
@@ -551,8 +564,13 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     atomicMax(&sh->longest, rows);
   }
   __syncthreads();
-  choose_cut<C::kSplit>(p, sh->tiles, sh->longest, pairs, tab);
   if (warp == 0) {
+    choose_cut<C::kSplit>(p, sh->tiles, sh->longest, pairs, static_cast<int>(lane), tab);
+    if (lane == 0) {
+      sh->cut[0] = tab.shift;
+      sh->cut[1] = tab.whole;
+      sh->cut[2] = tab.splits;
+    }
     int sum = 0;
     for (int g0 = 0; g0 < p.entries; g0 += 32) {
       const int g = g0 + static_cast<int>(lane);
@@ -577,6 +595,9 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
   cluster_sync();  // barriers and TMEM of both CTAs are set up
   tc_fence_after_sync();
   const uint32_t tmem = sh->tmem_base;
+  tab.shift = sh->cut[0];
+  tab.whole = sh->cut[1];
+  tab.splits = sh->cut[2];
   grid_launch_dependents();
 
   const bool epilogue = warp >= C::kEpiWarp0 && warp < C::kEpiWarp0 + C::kEpiWarps;
@@ -603,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
         const int half = mma_cols<QMN>(t) / 2;
         const int ln = t.n0 + static_cast<int>(rank) * kHalf;
         const int qn = t.q0 + static_cast<int>(rank) * half;
-        const int copies = QMN ? half / kLine : cdiv(half, p.q_box);
+        const int copies = QMN ? half / kLine : (half + p.q_box - 1) >> p.q_shift;
         const uint32_t bytes =
             static_cast<uint32_t>(kHalf * 128 + copies * (QMN ? kChunk : 128 * p.q_box));
         ok = for_passes(p, t, [&](int pass, int len, int k_lo, int k_hi) {
@@ -1276,7 +1297,8 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   // Lines per copy of a K-major Q: about half a tile's rows, so that small
   // segments and narrow tiles do not read their neighbours' rows.
   const long long average = p.form == kRows ? a.M / (a.groups > 0 ? a.groups : 1) : a.M;
-  p.q_box = average <= 64 ? 32 : (average <= 128 || least < pairs ? 64 : 128);
+  p.q_shift = average <= 64 ? 5 : (average <= 128 || least < pairs ? 6 : 7);
+  p.q_box = 1 << p.q_shift;
 
   const bool lmn = a.wgrad || !a.transb, qmn = a.wgrad;
   const int line = a.bf16 ? 64 : 32, bk = a.bf16 ? 64 : 32;
