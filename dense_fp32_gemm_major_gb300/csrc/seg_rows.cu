@@ -9,25 +9,30 @@
 // has nothing to set up:
 //
 //   B stored K x N: a thread holds 16 bytes of n; TX threads span the CTA's
-//     columns, the others share k, eight rows of B each at a time (eight
-//     loads in flight), and their sums meet in shared memory in a fixed order.
+//     columns, the others share k, DEEP rows of B each at a time (as many loads
+//     in flight), and their sums meet in shared memory in a fixed order.
 //   B stored N x K: a warp holds four n, its lanes share k (four loads in
 //     flight) and add by shuffles.
 //
-// Few columns a CTA (16, 64 or 256 of bf16) make many CTAs of short loops:
-// 1 x 512 x 512 float32 is sixteen CTAs of two rounds of loads.
+// Few columns a CTA (16 to 1024 of bf16) make many CTAs of short loops: 1 x 512
+// x 512 float32 is sixteen CTAs of two rounds of loads. A long contraction goes
+// to the four CTAs of a cluster, whose first adds the others' sums from their
+// shared memory (32 rows of their own adapters, 4096 x 16: one SM reads its 128
+// KB in 8 us).
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "segments.h"
 
 namespace gemm {
 namespace {
 
-constexpr int kThreads = 256, kRows = 4, kDeep = 8, kWarpN = 4;
+constexpr int kThreads = 256, kRows = 4, kWarpN = 4;
+constexpr int kSlices = 4, kSliceK = 1024;  // CTAs of a contraction, from this k on
 constexpr int kStaged = 8192;  // values of A that stand in shared memory at a time
 
 struct P {
@@ -38,7 +43,7 @@ struct P {
   const int32_t *index;
   long long a_ld, a_lo_ld, b_ld, b_stride, c_ld, c_lo_ld, add_ld;
   long long a_extent, b_extent, c_extent, c_lo_extent, add_extent, a_lo_extent;
-  int M, N, K, groups, bank, dense, c_f32;
+  int M, N, K, groups, bank, dense, c_f32, slices;
 };
 
 template <class T>
@@ -92,8 +97,9 @@ __device__ __forceinline__ int chunk_of(int count) {
 
 // Rows [t, t + count) of A, k [k0, k0 + chunk), as floats.
 template <class T>
-__device__ __forceinline__ void stage_a(const P &p, float *as, int t, int count, int k0, int chunk) {
-  const int n = min(chunk, p.K - k0), end = (n + kDeep - 1) / kDeep * kDeep;
+__device__ __forceinline__ void stage_a(const P &p, float *as, int t, int count, int k0, int k_end,
+                                        int chunk) {
+  const int n = min(chunk, k_end - k0), end = (n + 15) / 16 * 16;
   for (int r = 0; r < count; ++r)
     for (int k = threadIdx.x; k < end; k += kThreads)
       as[r * chunk + k] = k < n ? load_a<T>(p, t + r, k0 + k) : 0.0f;
@@ -169,12 +175,14 @@ __device__ __forceinline__ void store(const P &p, int row, int n, float v, const
   }
 }
 
-// B stored K x N. TX threads of 16 bytes across the CTA's columns.
-template <class T, int TX>
+// B stored K x N. TX threads of 16 bytes across the CTA's columns, DEEP rows of
+// B in flight a thread.
+template <class T, int TX, int kDeep>
 __global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
   constexpr int V = Vec<T>::n, TY = kThreads / TX, NT = TX * V;
-  __shared__ float sums[TY * NT];
-  __shared__ float as[kStaged];
+  __shared__ float sums[TY * NT], as[kStaged];
+  float *const total = as;  // in the end: [count][NT]
+  static_assert(kRows * NT <= kStaged, "totals in A's place");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Rows o;
@@ -182,15 +190,19 @@ __global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
   const int count = o.count, z = o.z;
   const int t = blockIdx.y, n0 = blockIdx.x * NT;
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, n = n0 + tx * V;
+  // This CTA's k, a multiple of 16 but for the last one's end.
+  const int slice = (p.K / 16 + p.slices - 1) / p.slices * 16;
+  const int k_lo = min(static_cast<int>(blockIdx.z) * slice, p.K);
+  const int k_hi = static_cast<int>(blockIdx.z) + 1 == p.slices ? p.K : min(k_lo + slice, p.K);
   float acc[kRows][V] = {};
   if (z >= 0) {
     const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
     const long long extent = p.b_extent - z * p.b_stride;
     const int chunk = chunk_of(count);
-    for (int c0 = 0; c0 < p.K; c0 += chunk) {
-      const int c1 = min(chunk, p.K - c0);
-      if (c0 > 0) __syncthreads();
-      stage_a<T>(p, as, t, count, c0, chunk);
+    for (int c0 = k_lo; c0 < k_hi; c0 += chunk) {
+      const int c1 = min(chunk, k_hi - c0);
+      if (c0 > k_lo) __syncthreads();
+      stage_a<T>(p, as, t, count, c0, k_hi, chunk);
       __syncthreads();
 #pragma unroll 2
       for (int k = ty * kDeep; k < c1; k += TY * kDeep) {
@@ -210,20 +222,57 @@ __global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
       }
     }
   }
+  // Two steps: groups of threads add TY / G of a column's sums, then one the
+  // groups'.
+  constexpr int G = NT < kThreads ? kThreads / NT : 1, PER = TY / G > 0 ? TY / G : 1;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     if (r >= count) break;
 #pragma unroll
     for (int v = 0; v < V; ++v) sums[ty * NT + tx * V + v] = acc[r][v];
     __syncthreads();
-    for (int c = threadIdx.x; c < NT; c += kThreads) {
+    if constexpr (G > 1 && TY % G == 0) {
+      const int c = threadIdx.x % NT, group = threadIdx.x / NT;
       float s = 0.0f;
-#pragma unroll 8
-      for (int y = 0; y < TY; ++y) s += sums[y * NT + c];
-      if (n0 + c < p.N) store<T>(p, t + r, n0 + c, s, o);
+#pragma unroll
+      for (int y = 0; y < PER; ++y) s += sums[(group * PER + y) * NT + c];
+      __syncthreads();
+      sums[group * NT + c] = s;
+      __syncthreads();
+      if (group == 0) {
+        s = 0.0f;
+#pragma unroll
+        for (int y = 0; y < G; ++y) s += sums[y * NT + c];
+        total[r * NT + c] = s;
+      }
+    } else {
+      for (int c = threadIdx.x; c < NT; c += kThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int y = 0; y < TY; ++y) s += sums[y * NT + c];
+        total[r * NT + c] = s;
+      }
     }
     __syncthreads();
   }
+  if (p.slices > 1) cluster_sync();  // every CTA's totals are there
+  if (blockIdx.z == 0) {
+    for (int i = threadIdx.x; i < count * NT; i += kThreads) {
+      const int r = i / NT, c = i % NT;
+      float s = total[i];
+      for (int q = 1; q < p.slices; ++q) {
+        uint32_t at;
+        float v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(smem_addr(total + i)), "r"(q));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+        s += v;
+      }
+      if (n0 + c < p.N) store<T>(p, t + r, n0 + c, s, o);
+    }
+  }
+  if (p.slices > 1) cluster_sync();  // and stay until they are read
 }
 
 // B stored N x K. A warp takes kWarpN columns.
@@ -246,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) seg_rows_nk_kernel(const P p) {
     for (int c0 = 0; c0 < p.K; c0 += chunk) {
       const int c1 = min(chunk, p.K - c0);
       if (c0 > 0) __syncthreads();
-      stage_a<T>(p, as, t, count, c0, chunk);
+      stage_a<T>(p, as, t, count, c0, p.K, chunk);
       __syncthreads();
 #pragma unroll 2
       for (int k = lane * V; k < c1; k += 32 * V) {
@@ -287,26 +336,32 @@ template <class K>
 int launch(K kernel, const P &p, int columns, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.N + columns - 1) / columns),
-                     static_cast<unsigned>(p.M), 1);
+                     static_cast<unsigned>(p.M), static_cast<unsigned>(p.slices));
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = static_cast<unsigned>(p.slices);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.slices > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? kOk : kErrLaunch;
 }
 
 template <class T>
-int launch_type(const P &p, int transb, cudaStream_t stream) {
+int launch_type(P p, int transb, cudaStream_t stream) {
   constexpr int V = Vec<T>::n;
+  p.slices = !transb && p.K >= kSliceK ? kSlices : 1;
   if (transb) return launch(seg_rows_nk_kernel<T>, p, kThreads / 32 * kWarpN, stream);
   // A short contraction has no work for many threads along k; a narrow result
   // none for many along n.
-  if (p.K <= 64) return launch(seg_rows_kn_kernel<T, 32>, p, 32 * V, stream);
-  if (p.N <= 2 * V) return launch(seg_rows_kn_kernel<T, 2>, p, 2 * V, stream);
-  return launch(seg_rows_kn_kernel<T, 8>, p, 8 * V, stream);
+  if (p.K <= 16 && p.N >= 512 * V) return launch(seg_rows_kn_kernel<T, 128, 8>, p, 128 * V, stream);
+  if (p.K <= 64) return launch(seg_rows_kn_kernel<T, 32, 8>, p, 32 * V, stream);
+  if (p.N <= 2 * V) return launch(seg_rows_kn_kernel<T, 2, 8>, p, 2 * V, stream);
+  return launch(seg_rows_kn_kernel<T, 8, 8>, p, 8 * V, stream);
 }
 
 }  // namespace
