@@ -100,6 +100,7 @@ struct SegTc {
   float *slots;
   unsigned *arrived;  // [2 tile + rank] of the split tiles, zero
   long long slot_extent;
+  int ahead;          // starts before the launch before it has ended (SegArgs::ahead)
   unsigned long long timeout_ns;
 };
 
@@ -393,6 +394,14 @@ struct Ring {
 
 // ------------------------------------------------------------ instructions --
 
+// From L2, and behind grid_dependency_wait(): the grid before may have written
+// it while this one ran, so it is no constant of this grid's.
+__device__ __forceinline__ float load_added(const float *p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // D[tmem] (+)= A[smem] B[smem]^T, kind::f16 with bf16 operands, on the pair.
 __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
@@ -545,7 +554,9 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     const int touched = reinterpret_cast<const int *>(&p)[i];
     asm volatile("" ::"r"(touched));
   }
-  grid_dependency_wait();
+  // ahead: what is read from here on was there before the previous grid began;
+  // the copies wait for it before they read U, the epilogue before it writes.
+  if (!p.ahead) grid_dependency_wait();
   // The table of segments: their rows, and the tiles before each.
   for (int g = threadIdx.x; g <= p.entries; g += C::kThreads) {
     long long a;
@@ -601,7 +612,9 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
   tab.shift = sh->cut[0];
   tab.whole = sh->cut[1];
   tab.splits = sh->cut[2];
-  grid_launch_dependents();
+  // Only behind the wait: when a grid starts, all but the last one before it
+  // are then complete, which is what an `ahead` grid builds on.
+  if (!p.ahead) grid_launch_dependents();
 
   const bool epilogue = warp >= C::kEpiWarp0 && warp < C::kEpiWarp0 + C::kEpiWarps;
   Tile t;
@@ -634,6 +647,10 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
           const CUtensorMap *ml = &maps.l[pass], *mq = &maps.q[pass];
           const int lz = p.form == kAdapted && pass > 0 ? t.a : t.z * p.z_step;
           const bool whole = pass > 0 && p.form == kAdapted ? p.l_whole1 : p.l_whole;
+          if (p.ahead && pass > 0 && p.form == kAdapted) {  // U is the previous grid's
+            grid_dependency_wait();
+            asm volatile("fence.proxy.async;" ::: "memory");
+          }
           for (int kk = k_lo; kk < k_hi; kk += kBK) {
             if (!wait(&ring_empty[r.idx], r.phase ^ 1, p, abort)) return false;
             uint8_t *l = ring + r.idx * kSlot;
@@ -817,6 +834,15 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
         mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[a], 0));
       return ok;
     };
+    // Nothing is written, nor `add` read, before the previous grid has ended.
+    bool held = p.ahead;
+    auto let_go = [&] {
+      if (held) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+      }
+      held = false;
+    };
     for (int i = pair; tile_at(p, tab, i, t); i += pairs) {
       const int blocks = t.b1 - t.b0;
       const int n = t.n0 + static_cast<int>(rank * 128 + quad * 32 + lane);
@@ -863,6 +889,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
       }
       // All warps go on together from here, or none does.
       if (!named_barrier_and(1, 32 * C::kEpiWarps, ok)) break;
+      let_go();
       const float scale = p.form == kRows && p.scales != nullptr && t.z >= 0 ? p.scales[t.z] : 1.0f;
       const long long row0 = t.q0 + c0;
       const long long at = (p.form == kWgrad ? t.g * p.c_stride : 0) + row0 * p.c_ld + n;
@@ -895,7 +922,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             const long long off = from + (c + k) * p.add_ld;
             a[k] = c + k < count && row >= add0 && row < add1 &&
                            index_ok(kSitePartialRead, off, 1, p.add_extent)
-                       ? __ldg(p.add + off)
+                       ? load_added(p.add + off)
                        : 0.0f;
           }
 #pragma unroll
@@ -1046,6 +1073,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
         acc.next();
       }
     }
+    let_go();
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (C::kSplit && warp >= C::kLoadWarp0) {
     // -------------------------------------------------- float32 to terms --
@@ -1278,6 +1306,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   const int64_t c_elem = p.c_f32 ? 4 : 2;
   p.c_rows = a.C_lo.p == nullptr && reinterpret_cast<uintptr_t>(a.C.p) % 16 == 0 &&
              a.C.ld * c_elem % 16 == 0 && a.C.stride * c_elem % 16 == 0 && a.N * c_elem % 16 == 0;
+  p.ahead = a.ahead;
   p.c_ld = a.C.ld;
   p.c_stride = a.C.stride;
   p.c_extent = extent_of(a.C);

@@ -44,6 +44,10 @@ struct SegArgs {
   SegMatrix add;       // dense: float32 addend of the result
   int64_t R = 0;       // adapted: width of U
   SegMatrix U, U_lo, L;
+  // The launch before, of the same call, writes nothing that this product reads
+  // but `add` and U: it may start while that one ends. (What earlier launches
+  // wrote is complete: see seg_tc_kernel.)
+  bool ahead = false;
   // Scratch for tiles split along k: seg_tc_slots() floats, and 2 counters a
   // pair, zero before the launch. null: no splits.
   float *slots = nullptr;

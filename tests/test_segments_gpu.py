@@ -461,6 +461,44 @@ def test_graph_capture_and_replay(g):
     assert torch.equal(out, 2 * ref)
 
 
+CHAINS = [([400, 0, 300, 324], 1024, 520, 16), ([200, 311, 190], 1000, 2048, 24),
+          ([1] * 32, 2048, 1024, 16), ([2, 1, 0, 1], 512, 512, 8), ([900, 1100], 2048, 2048, 64)]
+
+
+@pytest.mark.parametrize("sizes, k, n, r", CHAINS, ids=lambda v: str(v)[:24])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_launches_of_a_step_keep_their_order(g, sizes, k, n, r, dt):
+    """Launches of a call may overlap; what one makes and the next reads, and
+    the inputs that are overwritten right behind the call, keep their order: the
+    same bits as one step at a time."""
+    m, s = sum(sizes), len(sizes)
+    off, _ = offsets_of(sizes)
+    w = normal((k, n), 1, dt)
+    jobs = [(normal((m, k), 10 + i, dt), normal((m, n), 20 + i, dt), normal((s, k, r), 30 + i, dt),
+             normal((s, r, n), 40 + i, dt)) for i in range(4)]
+    held = [t.clone() for t in jobs[0]]
+    u = torch.empty((m, r), dtype=dt, device="cuda")
+
+    def step(i, wait):
+        for to, t in zip(held, jobs[i]):
+            to.copy_(t)
+        wait()
+        x, dy, a, b = held
+        y = g.lora_matmul(x, w, a, b, off, shrink_out=u)
+        wait()
+        out = (y,) + tuple(g.lora_backward(dy, x, u, w, a, b, off))
+        wait()
+        for t in held + [u]:
+            t.fill_(float("nan"))
+        return out
+
+    refs = [step(i, torch.cuda.synchronize) for i in range(len(jobs))]
+    outs = [(i, step(i, lambda: None)) for _ in range(8) for i in range(len(jobs))]
+    for i, out in outs:
+        for c, ref in zip(out, refs[i]):
+            assert torch.equal(c, ref)
+
+
 def test_concurrent_streams(g):
     off, o = offsets_of([64, 64])
     jobs = [(normal((128, 4096), 80 + i, torch.float32), normal((2, 4096, 192), 90 + i, torch.float32))
