@@ -33,6 +33,8 @@ namespace {
 
 constexpr int kThreads = 256, kRows = 4, kWarpN = 4;
 constexpr int kSlices = 4, kSliceK = 1024;  // CTAs of a contraction, from this k on
+// bf16 operands longer than kShortK: most of N (M + 2 CTAs' rows), seg_rows_fits.
+constexpr int64_t kShortK = 128, kMostBf16 = 36 * 1024;
 constexpr int kStaged = 8192;  // values of A that stand in shared memory at a time
 
 struct P {
@@ -51,28 +53,37 @@ struct Vec {
   static constexpr int n = 16 / sizeof(T);
 };
 
-// 16 bytes from p + off as floats, those at or past `left` zero.
+// 16 bytes from p + off, the values at or past `left` zero.
 template <class T>
-__device__ __forceinline__ void load16(const T *p, long long off, int left, int site,
-                                       long long extent, float (&v)[Vec<T>::n]) {
+__device__ __forceinline__ uint4 load16(const T *p, long long off, int left, int site,
+                                        long long extent) {
   constexpr int n = Vec<T>::n;
-  if (left >= n && index_ok(site, off, n, extent)) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p + off));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    if constexpr (n == 4) {
+  if (left >= n && index_ok(site, off, n, extent))
+    return __ldg(reinterpret_cast<const uint4 *>(p + off));
+  uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(u[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      }
+  for (int i = 0; i < n; ++i)
+    if (i < left && index_ok(site, off + i, 1, extent)) {
+      if constexpr (n == 4)
+        u[i] = __float_as_uint(p[off + i]);
+      else
+        u[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(p[off + i])) << (i % 2 * 16);
     }
-  } else {
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// A load16 as floats.
+template <class T>
+__device__ __forceinline__ void unpack(const uint4 &w, float (&v)[Vec<T>::n]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-      v[i] = i < left && index_ok(site, off + i, 1, extent) ? static_cast<float>(p[off + i]) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (Vec<T>::n == 4) {
+      v[i] = __uint_as_float(u[i]);
+    } else {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
   }
 }
 
@@ -106,12 +117,11 @@ __device__ __forceinline__ void stage_a(const P &p, float *as, int t, int count,
 }
 
 // Rows [t, t + count) that this CTA computes, their matrix (-1: none), its
-// scale, and whether they have an addend: blockIdx.y is a row; every fourth of
+// scale, and the rows that have an addend: blockIdx.y is a row; every fourth of
 // a segment takes those behind it.
 struct Rows {
-  int count, z;
+  int count, z, add0, add1;
   float scale;
-  bool added;
 };
 
 __device__ __forceinline__ bool rows_of(const P &p, Rows *o) {
@@ -119,8 +129,14 @@ __device__ __forceinline__ bool rows_of(const P &p, Rows *o) {
   int first = 0, last = p.M;
   o->z = 0;
   o->scale = 1.0f;
-  o->added = true;
-  if (p.offsets != nullptr) {
+  o->add0 = o->add1 = 0;
+  if (p.dense) {
+    if (p.add != nullptr) {
+      const long long a = p.offsets[0], b = p.offsets[p.groups];
+      o->add0 = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
+      o->add1 = static_cast<int>(b < 0 ? 0 : (b > p.M ? p.M : b));
+    }
+  } else {
     // Each thread looks at its segments; all loads are on their way at once.
     __shared__ int found[3];
     if (threadIdx.x == 0) found[0] = -1;
@@ -135,28 +151,21 @@ __device__ __forceinline__ bool rows_of(const P &p, Rows *o) {
       }
     }
     __syncthreads();
-    const bool inside = found[0] >= 0;
-    if (p.dense) {
-      o->added = inside;  // all rows, but an addend for the segments'
-    } else {
-      if (!inside) return false;
-      first = found[1];
-      last = found[2];
-      o->z = found[0] < p.bank ? found[0] : -1;
-      if (p.scales != nullptr && o->z >= 0) o->scale = p.scales[o->z];
-    }
+    if (found[0] < 0) return false;
+    first = found[1];
+    last = found[2];
+    o->z = found[0] < p.bank ? found[0] : -1;
+    if (p.scales != nullptr && o->z >= 0) o->scale = p.scales[o->z];
   }
-  // A dense product's rows may differ in having an addend: one row each then.
-  const int step = p.dense && p.add != nullptr ? 1 : kRows;
-  if ((t - first) % step != 0) return false;
-  o->count = min(step, last - t);
+  if ((t - first) % kRows != 0) return false;
+  o->count = min(kRows, last - t);
   return true;
 }
 
 template <class T>
 __device__ __forceinline__ void store(const P &p, int row, int n, float v, const Rows &o) {
   v *= o.scale;
-  if (p.add != nullptr && o.added) {
+  if (p.add != nullptr && row >= o.add0 && row < o.add1) {
     const long long at = row * p.add_ld + n;
     if (index_ok(kSitePartialRead, at, 1, p.add_extent)) v += p.add[at];
   }
@@ -175,10 +184,17 @@ __device__ __forceinline__ void store(const P &p, int row, int n, float v, const
   }
 }
 
+// CTAs an SM that the compiler plans registers for. bf16: with two (three for B
+// stored N x K) it holds the loads of two rounds (one row of 4096 x 4096 12 -> 8
+// us, 20 -> 11). float32 is left to it (0): four CTAs of one round are faster
+// than two of two (9 against 12 us).
+template <class T, int BF16>
+constexpr int kCtas = Vec<T>::n == 4 ? 0 : BF16;
+
 // B stored K x N. TX threads of 16 bytes across the CTA's columns, DEEP rows of
 // B in flight a thread.
 template <class T, int TX, int kDeep>
-__global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
+__global__ void __launch_bounds__(kThreads, kCtas<T, 2>) seg_rows_kn_kernel(const P p) {
   constexpr int V = Vec<T>::n, TY = kThreads / TX, NT = TX * V;
   __shared__ float sums[TY * NT], as[kStaged];
   float *const total = as;  // in the end: [count][NT]
@@ -206,18 +222,22 @@ __global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
       __syncthreads();
 #pragma unroll 2
       for (int k = ty * kDeep; k < c1; k += TY * kDeep) {
-        float b[kDeep][V];
+        uint4 w[kDeep];
 #pragma unroll
         for (int j = 0; j < kDeep; ++j)
-          load16<T>(B, static_cast<long long>(c0 + k + j) * p.b_ld + n, k + j < c1 ? p.N - n : 0,
-                    kSiteLoadB, extent, b[j]);
+          w[j] = load16<T>(B, static_cast<long long>(c0 + k + j) * p.b_ld + n,
+                           k + j < c1 ? p.N - n : 0, kSiteLoadB, extent);
+        float b[kDeep][V];
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) unpack<T>(w[j], b[j]);
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
           if (r < count) {
 #pragma unroll
             for (int j = 0; j < kDeep; ++j)
 #pragma unroll
-              for (int v = 0; v < V; ++v) acc[r][v] = fmaf(as[r * chunk + k + j], b[j][v], acc[r][v]);
+              for (int v = 0; v < V; ++v)
+                acc[r][v] = fmaf(as[r * chunk + k + j], b[j][v], acc[r][v]);
           }
       }
     }
@@ -277,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) seg_rows_kn_kernel(const P p) {
 
 // B stored N x K. A warp takes kWarpN columns.
 template <class T>
-__global__ void __launch_bounds__(kThreads) seg_rows_nk_kernel(const P p) {
+__global__ void __launch_bounds__(kThreads, kCtas<T, 3>) seg_rows_nk_kernel(const P p) {
   constexpr int V = Vec<T>::n;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -286,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) seg_rows_nk_kernel(const P p) {
   const int count = o.count, z = o.z;
   const int t = blockIdx.y, lane = threadIdx.x & 31;
   const int n0 = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpN;
-  __shared__ float as[kStaged];
+  __shared__ __align__(16) float as[kStaged];
   float acc[kRows][kWarpN] = {};
   if (z >= 0) {
     const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
@@ -299,18 +319,28 @@ __global__ void __launch_bounds__(kThreads) seg_rows_nk_kernel(const P p) {
       __syncthreads();
 #pragma unroll 2
       for (int k = lane * V; k < c1; k += 32 * V) {
-        float b[kWarpN][V];
+        uint4 w[kWarpN];
 #pragma unroll
         for (int j = 0; j < kWarpN; ++j)
-          load16<T>(B, static_cast<long long>(n0 + j) * p.b_ld + c0 + k,
-                    n0 + j < p.N ? c1 - k : 0, kSiteLoadB, extent, b[j]);
+          w[j] = load16<T>(B, static_cast<long long>(n0 + j) * p.b_ld + c0 + k,
+                           n0 + j < p.N ? c1 - k : 0, kSiteLoadB, extent);
+        float b[kWarpN][V];
+#pragma unroll
+        for (int j = 0; j < kWarpN; ++j) unpack<T>(w[j], b[j]);
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
           if (r < count) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; v += 4) {
+              const float4 x = *reinterpret_cast<const float4 *>(as + r * chunk + k + v);
 #pragma unroll
-              for (int j = 0; j < kWarpN; ++j) acc[r][j] = fmaf(as[r * chunk + k + v], b[j][v], acc[r][j]);
+              for (int j = 0; j < kWarpN; ++j) {
+                acc[r][j] = fmaf(x.x, b[j][v], acc[r][j]);
+                acc[r][j] = fmaf(x.y, b[j][v + 1], acc[r][j]);
+                acc[r][j] = fmaf(x.z, b[j][v + 2], acc[r][j]);
+                acc[r][j] = fmaf(x.w, b[j][v + 3], acc[r][j]);
+              }
+            }
           }
       }
     }
@@ -370,8 +400,17 @@ GEMM_INDEX_FAULT_TAKE(seg_rows_index_fault_take)
 
 bool seg_rows_fits(const SegArgs &a) {
   // All rows together few, or the segments' (about two each, at most).
-  return !a.wgrad && a.R == 0 && a.K > 0 &&
-         (a.M <= 2 * kRows || (!a.dense && a.M <= 2 * a.groups && a.M <= 512));
+  if (a.wgrad || a.R > 0 || a.K <= 0) return false;
+  const int64_t fours = (a.M + kRows - 1) / kRows;
+  if (a.M > 2 * kRows && (a.dense || a.M > 2 * a.groups || a.M > 512)) return false;
+  // float32: 8 rows of 4096 x 11008 take 87 us here, 114 on the tensor cores.
+  if (!a.bf16 || a.K <= kShortK) return true;
+  // bf16: what grows with the CTAs (of four rows of a segment, at most) and
+  // with the rows is limited: 4 rows of 4096 x 4096 take 13 us here and 19 on
+  // the tensor cores, 8 rows 25 and 19; a row of each of four segments 39 and
+  // 33, of two 15 and 23; one row of 4096 x 11008 24 and 29, four 38 and 29.
+  const int64_t ctas = a.dense ? fours : (a.M < a.groups - 1 + fours ? a.M : a.groups - 1 + fours);
+  return a.N * (a.M + 2 * ctas) <= kMostBf16;
 }
 
 int seg_rows_launch(const SegArgs &a, cudaStream_t stream) {
