@@ -124,7 +124,7 @@ class Workspace {
 
   // One product, with the scratch it may want.
   int launch(SegArgs &a, cudaStream_t s) {
-    if (gemm::seg_rows_fits(a)) return gemm::seg_rows_launch(a, s);
+    if (gemm::seg_rows_fits(a)) return gemm::seg_rows_launch(a, sms_, s);
     if (split_) {
       a.slots = slots_;
       a.arrived = arrived_ + static_cast<size_t>(products_++ % kProducts) * sms_;

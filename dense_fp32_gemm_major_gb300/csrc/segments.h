@@ -69,7 +69,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
 // Products of very few rows (rows and dense forms): whether these arguments are
 // such a product, and its launch. Operands readable.
 bool seg_rows_fits(const SegArgs &a);
-int seg_rows_launch(const SegArgs &a, cudaStream_t stream);
+int seg_rows_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
 
 int seg_rows_index_fault_take(IndexFault *out, bool clear);
 
