@@ -344,6 +344,25 @@ def test_lora(g, sizes, which, bank, k, n, r, trans, dt):
     assert torch.equal(y, g.lora_matmul(x, w, a, b, off, index, scales, transw, transl))
 
 
+@pytest.mark.parametrize("sizes, first, m, k, n, r", [
+    ([1, 3], 2, 8, 1024, 2048, 16), ([3, 0, 4], 0, 8, 640, 4400, 8), ([1] * 6, 1, 8, 4096, 1000, 24),
+    ([5], 1, 8, 200, 11008, 3), ([1, 0, 1], 1, 3, 1500, 1531, 40), ([2], 0, 2, 130, 9000, 16)],
+    ids=lambda v: str(v)[:24])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_lora_few_rows(g, sizes, first, m, k, n, r, trans, dt):
+    # rows before and behind the segments share CTAs with rows in them
+    off, o = offsets_of(sizes, first)
+    x, w = normal((m, k), 91, dt), normal((n, k) if trans else (k, n), 92, dt)
+    a = normal((len(sizes), r, k) if trans else (len(sizes), k, r), 93, dt)
+    b = normal((len(sizes), n, r) if trans else (len(sizes), r, n), 94, dt)
+    one = torch.ones(len(sizes), device="cuda")
+    y = g.lora_matmul(x, w, a, b, off, transw=trans, transl=trans)
+    y64, ty, _, _ = lora_64(x, w.t() if trans else w, [t.t() if trans else t for t in a],
+                            [t.t() if trans else t for t in b], o, list(range(len(sizes))), one)
+    check(y, y64, ty, "y")
+
+
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
 def test_lora_without_adapters_is_the_projection(g, dt):
     x, w = normal((50, 64), 35, dt), normal((64, 72), 36, dt)
