@@ -78,7 +78,7 @@ struct SegTc {
   int groups;        // segments
   int entries;       // of the table: groups; dense 1; adapted groups + 2
   int M, N, K, R, bank;
-  int z_step;        // 0: one matrix for every segment
+  int z_step, a_step;  // 0: one matrix for every segment, one L for every adapter
   // Passes over the operands of a tile: one, or two with a two-term operand;
   // adapted: A and B, then U (its terms) and the adapter's L.
   int passes;
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             static_cast<uint32_t>(kHalf * 128 + copies * (QMN ? kChunk : 128 * p.q_box));
         ok = for_passes(p, t, [&](int pass, int len, int k_lo, int k_hi) {
           const CUtensorMap *ml = &maps.l[pass], *mq = &maps.q[pass];
-          const int lz = p.form == kAdapted && pass > 0 ? t.a : t.z * p.z_step;
+          const int lz = p.form == kAdapted && pass > 0 ? t.a * p.a_step : t.z * p.z_step;
           const bool whole = pass > 0 && p.form == kAdapted ? p.l_whole1 : p.l_whole;
           if (p.ahead && pass > 0 && p.form == kAdapted) {  // U is the previous grid's
             grid_dependency_wait();
@@ -1292,6 +1292,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   p.R = static_cast<int>(a.R);
   p.bank = static_cast<int>(a.bank);
   p.z_step = a.B.count > 1 && a.B.stride == 0 ? 0 : 1;
+  p.a_step = a.L.count > 1 && a.L.stride == 0 ? 0 : 1;
   const bool two_terms = a.A_lo.p != nullptr || a.B_lo.p != nullptr;
   p.passes = adapted ? (a.U_lo.p != nullptr ? 3 : 2) : (two_terms ? 2 : 1);
   p.tiles_n = static_cast<int>((a.N + kLanes - 1) / kLanes);

@@ -95,7 +95,8 @@ int gemm_f32_grouped_wgrad(int type, int64_t groups, int64_t M, int64_t N, int64
  *             and B_a N x R. With dY for X, W and the factors exchanged and
  *             both flags flipped the same call is the gradient of X, and U
  *             the second operand of the gradient of A.
- *   A, B      adapter a starts stridea (strideb) elements after a - 1
+ *   A, B      adapter a starts stridea (strideb) elements after a - 1 (0: one
+ *             factor shared by all)
  *   index     device int32, one adapter for each segment; NULL: adapter g for
  *             segment g. A value outside [0, bank) means none: such rows, and
  *             rows of no segment, get X op(W) alone.
