@@ -1215,17 +1215,24 @@ int launch(const SegMaps &maps, const SegTc &p, int pairs, cudaStream_t stream) 
   const int fixed = C::kStages * C::kStageBytes + C::kRawBytes + C::kEpiWarps / 4 * C::kOutBytes +
                     static_cast<int>(sizeof(Shared<C::kStages, C::kRawStages>)) + 1024;
   auto smem = [fixed](int entries) { return fixed + 8 * entries + 8; };
-  static std::once_flag once;
-  static bool ready = false;
-  std::call_once(once, [&] {
-    cudaFuncAttributes at;
-    ready = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 smem(kMaxSegments + 2)) == cudaSuccess &&
-            cudaFuncGetAttributes(&at, kernel) == cudaSuccess &&
-            // the register split draws on the launch's registers
-            (!C::kSplit || at.numRegs * C::kThreads >= 128 * 40 + 256 * 152 + 256 * 64);
-  });
-  if (!ready) return kErrLaunch;
+  // Shared memory above the 48 KiB default is enabled once per device.
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return kErrLaunch;
+  static bool attr_set[64] = {};
+  static std::mutex attr_mu;
+  {
+    std::lock_guard<std::mutex> g(attr_mu);
+    if (!attr_set[dev]) {
+      cudaFuncAttributes at;
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               smem(kMaxSegments + 2)) != cudaSuccess ||
+          cudaFuncGetAttributes(&at, kernel) != cudaSuccess ||
+          // the register split draws on the launch's registers
+          (C::kSplit && at.numRegs * C::kThreads < 128 * 40 + 256 * 152 + 256 * 64))
+        return kErrLaunch;
+      attr_set[dev] = true;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);

@@ -50,3 +50,17 @@ def test_lora_with_a_factor_shared_by_all_adapters(g, sizes, k, n, r, shared, tr
     x64, tx, _, _ = lora_64(dy, w if trans else w.t(), [t.t() for t in bt], [t.t() for t in at], o,
                             range(bank), scales)
     check(dx, x64, tx, "dx")
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_every_device_of_a_process(g, dt):
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one GPU")
+    for d in range(2):
+        with torch.cuda.device(d):
+            off, o = offsets_of([40, 50])
+            a, b = normal((90, 64), 31, dt), normal((2, 64, 80), 32, dt)
+            c64, s64 = product(a[:40], b[0])
+            c = g.grouped_matmul(a, b, off)
+            check(c[:40], c64, rounding(c64, s64, 64, dt))
+            g.grouped_wgrad(a, c, off)

@@ -1,0 +1,42 @@
+"""Rules of the segmented products' sources that a run on one GPU cannot show,
+checked on the CPU by reading them."""
+
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "dense_fp32_gemm_major_gb300", "csrc")
+
+
+def sources():
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh", ".h")):
+            with open(os.path.join(CSRC, name)) as f:
+                text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+            yield name, re.sub(r"//[^\n]*", "", text)
+
+
+def once_bodies(text):
+    """The bodies of the lambdas given to call_once."""
+    for m in re.finditer(r"\bcall_once\s*\([^{]*\{", text):
+        depth, i = 1, m.end()
+        while depth and i < len(text):
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+        yield text[m.end():i]
+
+
+# What the runtime keeps for each device: done once a process, it is missing on
+# every GPU but the first one used.
+PER_DEVICE = re.compile(r"cudaFuncSetAttribute|cudaFuncGetAttributes|cudaMemPool\w*|cudaMemcpyToSymbol")
+
+
+def test_what_a_device_keeps_is_not_set_once_a_process():
+    seen = 0
+    for name, text in sources():
+        for body in once_bodies(text):
+            seen += 1
+            assert not PER_DEVICE.search(body), f"{name}: {PER_DEVICE.search(body).group(0)}"
+    assert seen >= 2  # the driver's entry points
+    assert list(once_bodies("std::call_once(o, [&] { if (a) { b(); } c(); }); d();")) \
+        == [" if (a) { b(); } c(); }"]
