@@ -25,10 +25,14 @@
 //
 //   x = h + m + l,   h = bf16(x), m = bf16(x - h), l = bf16(x - h - m),
 //
-// exact for finite x (24 bits in three terms of 8; Henry, Tang and Heinecke,
-// "Leveraging the bfloat16 artificial intelligence datatype for
-// higher-precision computations", ARITH 2019). The products hh, hm, mh, mm,
-// hl, lh are summed; those left out are below 2^-24 of |x y|.
+// exact for |x| from 2^-110 to the largest finite value (24 bits in three terms
+// of 8; Henry, Tang and Heinecke, "Leveraging the bfloat16 artificial
+// intelligence datatype for higher-precision computations", ARITH 2019). h is
+// rounded to the largest finite bf16, not to infinity (|x| >= 3.3962e38); m is
+// then 2^-8 of x as elsewhere. Below 2^-110 the last bits fall under bf16's
+// smallest value: x is held to 2^-134. Of an infinite x the terms are finite,
+// infinite and NaN. The products hh, hm, mh, mm, hl, lh are summed; those left
+// out are below 2^-24 of |x y|.
 //
 // The tensor core truncates as it adds to an accumulator: sums of K products
 // drift by about 2^-24 per MMA (measured: 4.4e-6 of the result's norm after
@@ -458,9 +462,15 @@ __device__ __forceinline__ void store_bulk(void *dst, uint32_t src, uint32_t byt
 
 // ----------------------------------------------------------- float32 terms --
 
+// Two values rounded to nearest; FINITE: past the largest value, to it.
+template <bool FINITE>
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
+  uint32_t w;
+  if constexpr (FINITE)
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
 }
 
 // Eight float32 values as three bf16 terms (`term` bytes apart).
@@ -470,7 +480,7 @@ __device__ __forceinline__ void store_terms(uint8_t *dst, int term, float (&v)[8
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      w[i] = t == 0 ? pack_bf16<true>(v[2 * i], v[2 * i + 1]) : pack_bf16<false>(v[2 * i], v[2 * i + 1]);
       if (t < 2) {  // what the term leaves, exactly
         v[2 * i] -= __uint_as_float(w[i] << 16);
         v[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);

@@ -18,8 +18,13 @@
  * "f32" of the names is the type of the sums: products are exact to fp32 or
  * better and accumulated in fp32, whatever the operands' type.
  *   GEMM_F32_TYPE_F32   fp32 operands and results, FP32 class: |C - AB| <=
- *                       2 K 2^-24 (|A| |B|), as GEMM_F32_EXACT. Operands are
- *                       finite (an infinite one gives NaN in its results).
+ *                       2 K 2^-24 (|A| |B|), as GEMM_F32_EXACT, for operands
+ *                       that are zero or from 2^-110 in magnitude to the
+ *                       largest finite value, and results of 2^-126 and more
+ *                       that pass no infinity on the way. Smaller operands are
+ *                       held to 2^-134 each. Results of an infinite or NaN
+ *                       operand are not finite (NaN where fp32 arithmetic may
+ *                       have infinity; which one depends on the sizes).
  *   GEMM_F32_TYPE_BF16  bf16 operands, fp32 sums, results rounded once to bf16
  *                       (nearest even).
  * A row of one segment never reaches the results of another: NaN and

@@ -64,3 +64,47 @@ def test_every_device_of_a_process(g, dt):
             c = g.grouped_matmul(a, b, off)
             check(c[:40], c64, rounding(c64, s64, 64, dt))
             g.grouped_wgrad(a, c, off)
+
+
+@pytest.mark.parametrize("rows", [4, 8, 9, 70])
+@pytest.mark.parametrize("transb", [False, True])
+def test_fp32_up_to_the_largest_finite_value(g, rows, transb):
+    # float32 operands within 0.2 % of the largest finite value round to
+    # infinity in bfloat16; results are held to the FP32 class all the same
+    top = torch.finfo(torch.float32).max
+    off, o = offsets_of([rows])
+    a, b = normal((rows, 64), 6, torch.float32), normal((1, 64, 96), 7, torch.float32)
+    near = top * (1 - torch.arange(64, device="cuda") * 2.0 ** -13).float()
+    signs = a.sign()
+    for big, small in ((near * signs, b * 2.0 ** -10), (torch.full_like(a, -top), b * 2.0 ** -10),
+                       (signs * top * (b[0, :, :1].t() > 0), b * 2.0 ** -10)):
+        s64 = big.double().abs() @ small[0].double().abs()
+        c64 = big.double() @ small[0].double()
+        c = g.grouped_matmul(big, small.transpose(1, 2).contiguous() if transb else small, off, transb)
+        check(c, c64, rounding(c64, s64, 64, torch.float32))
+    # the other operand at the top
+    w = (near[:, None] * b[0].sign())[None]
+    x = a * 2.0 ** -10
+    c64, s64 = product(x, w[0])
+    c = g.grouped_matmul(x, w.transpose(1, 2).contiguous() if transb else w, off, transb)
+    check(c, c64, rounding(c64, s64, 64, torch.float32))
+    # and in a weight gradient
+    d = normal((rows, 40), 8, torch.float32) * 2.0 ** -10
+    c64, s64 = product((near * signs).t(), d)
+    check(g.grouped_wgrad(near * signs, d, off)[0], c64, rounding(c64, s64, rows, torch.float32))
+
+
+@pytest.mark.parametrize("rows", [4, 8, 9, 70])
+def test_fp32_down_to_the_smallest_value(g, rows):
+    # Values below 2^-110 are held to 2^-134 each (their last bits lie below
+    # bfloat16's smallest value): that much of the other operand's sum beside
+    # the FP32 class. From 2^-110 on nothing is lost.
+    off, o = offsets_of([rows])
+    b = normal((1, 64, 96), 9, torch.float32) * 2.0 ** 100
+    for low, high, lost in ((-110, -90, 0.0), (-149, -100, 2.0 ** -134)):
+        power = torch.linspace(low, high, 64, device="cuda").round().double()
+        a = ((1 + torch.rand(rows, 64, generator=torch.Generator().manual_seed(10)).cuda().double())
+             * 2.0 ** power).float()
+        c64, s64 = product(a, b[0])
+        tol = rounding(c64, s64, 64, torch.float32) + lost * b[0].double().abs().sum(0)
+        check(g.grouped_matmul(a, b, off), c64, tol)
