@@ -169,6 +169,7 @@ class Workspace {
 // Y = X op(W) + U op(B_a), U = s_a (X op(A_a)).
 struct Lora {
   bool bf16 = false, adapted = false;
+  bool zero_u = false;       // no adapters at all: U's rows are zero
   int transw = 0, transl = 0;
   int64_t segments = 0, bank = 0, M = 0, N = 0, K = 0, R = 0;
   SegMatrix X, W, A, B, Y;
@@ -234,6 +235,14 @@ struct Lora {
     y.bank = bank;
     y.offsets = offsets;
     y.groups = adapted ? segments : 0;
+    if (zero_u) {
+      SegArgs z = y;  // a product without a contraction
+      z.groups = segments;
+      z.N = R;
+      z.C = user_u;
+      const int st = w.launch(z, s);
+      if (st != gemm::kOk || N == 0) return st;
+    }
     if (adapted) {
       SegArgs p = y;  // U = s (X A)
       p.index = index;
@@ -373,7 +382,9 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
   l.bf16 = type == GEMM_F32_TYPE_BF16;
   l.transw = transw;
   l.transl = transl;
-  l.adapted = R > 0 && bank > 0 && segments > 0 && M > 0;
+  const bool rows = R > 0 && segments > 0 && M > 0;  // that an adapter may have
+  l.adapted = rows && bank > 0;
+  l.zero_u = rows && bank == 0 && U != nullptr;
   l.segments = segments;
   l.bank = bank;
   l.M = M;
@@ -395,15 +406,16 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
     return GEMM_ERR_INVALID_ARG;
   if (l.adapted &&
       (!stack_ok(l.A, elem, false, &ra) || !stack_ok(l.B, elem, false, &rb) ||
-       !array_ok(offsets, segments + 1, 8, false, &ro) ||
-       !array_ok(index, segments, 4, true, &ri) || !array_ok(scales, bank, 4, true, &rs) ||
-       (U != nullptr && !stack_ok(l.user_u, elem, true, &ru))))
+       !array_ok(index, segments, 4, true, &ri) || !array_ok(scales, bank, 4, true, &rs)))
+    return GEMM_ERR_INVALID_ARG;
+  if ((l.adapted || l.zero_u) && (!array_ok(offsets, segments + 1, 8, false, &ro) ||
+                                  (U != nullptr && !stack_ok(l.user_u, elem, true, &ru))))
     return GEMM_ERR_INVALID_ARG;
   const Range in[] = {rx, rw, ra, rb, ro, ri, rs};
   for (const Range &r : in)
     if (overlap(r, ry) || overlap(r, ru)) return GEMM_ERR_ALIAS;
   if (overlap(ru, ry)) return GEMM_ERR_ALIAS;
-  if (M == 0 || (N == 0 && (!l.adapted || U == nullptr))) return GEMM_OK;
+  if (M == 0 || (N == 0 && ((!l.adapted && !l.zero_u) || U == nullptr))) return GEMM_OK;
   int dev = 0, sms = 0;
   int st = gemm::current_device_info(&dev, &sms);
   if (st != gemm::kOk) return st;

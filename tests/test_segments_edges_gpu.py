@@ -108,3 +108,18 @@ def test_fp32_down_to_the_smallest_value(g, rows):
         c64, s64 = product(a, b[0])
         tol = rounding(c64, s64, 64, torch.float32) + lost * b[0].double().abs().sum(0)
         check(g.grouped_matmul(a, b, off), c64, tol)
+
+
+@pytest.mark.parametrize("rows", [3, 40, 300])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_shrink_of_a_bank_without_adapters_is_zero(g, rows, dt):
+    off, o = offsets_of([rows, 0, 2], first=1)
+    x, w = normal((rows + 5, 64), 11, dt), normal((64, 72), 12, dt)
+    none = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    a, b = torch.empty(0, 64, 8, dtype=dt, device="cuda"), torch.empty(0, 8, 72, dtype=dt, device="cuda")
+    for u in (torch.full((rows + 5, 8), 7.0, dtype=dt, device="cuda"),
+              torch.full((rows + 5, 11), 7.0, dtype=dt, device="cuda")[:, 1:9]):  # an odd pitch
+        y = g.lora_matmul(x, w, a, b, off, none, shrink_out=u)
+        y64, s64 = product(x, w)
+        check(y, y64, rounding(y64, s64, 64, dt))
+        assert (u[1:rows + 3] == 0).all() and (u[:1] == 7).all() and (u[rows + 3:] == 7).all()
