@@ -241,7 +241,7 @@ struct Lora {
       z.N = R;
       z.C = user_u;
       const int st = w.launch(z, s);
-      if (st != gemm::kOk || N == 0) return st;
+      if (st != gemm::kOk) return st;
     }
     if (adapted) {
       SegArgs p = y;  // U = s (X A)
@@ -257,7 +257,7 @@ struct Lora {
       int st = w.launch(p, s);
       if (st == gemm::kOk && user_u.p != nullptr && u.p != user_u.p)
         st = w.hand_back(u, user_u, s);
-      if (st != gemm::kOk || N == 0) return st;
+      if (st != gemm::kOk) return st;
     }
     y.dense = true;
     y.N = N;
@@ -266,6 +266,7 @@ struct Lora {
     y.B = W;
     y.transb = transw;
     y.C = Y;
+    if (N == 0) return gemm::kOk;  // no Y
     if (!adapted) return w.launch(y, s);
     y.ahead = ahead;
     if (fused) {
@@ -479,7 +480,8 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
     for (int j = 0; j < i; ++j)
       if (overlap(out[j], out[i])) return GEMM_ERR_ALIAS;
   }
-  if ((M == 0 || (K == 0 && N == 0)) && (segments == 0 || R == 0)) return GEMM_OK;
+  // No dX, and neither dA nor dB.
+  if ((M == 0 || K == 0) && (segments == 0 || R == 0 || (K == 0 && N == 0))) return GEMM_OK;
   int dev = 0, sms = 0;
   int st = gemm::current_device_info(&dev, &sms);
   if (st != gemm::kOk) return st;

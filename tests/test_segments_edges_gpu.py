@@ -123,3 +123,22 @@ def test_shrink_of_a_bank_without_adapters_is_zero(g, rows, dt):
         y64, s64 = product(x, w)
         check(y, y64, rounding(y64, s64, 64, dt))
         assert (u[1:rows + 3] == 0).all() and (u[:1] == 7).all() and (u[rows + 3:] == 7).all()
+
+
+@pytest.mark.parametrize("rows", [5, 60])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_lora_backward_of_a_projection_without_inputs(g, rows, dt):
+    # no columns of X: there is no dX, and with rank 0 or no segment nothing else
+    off, _ = offsets_of([rows])
+    dy = normal((rows, 24), 13, dt)
+    x, w = torch.empty(rows, 0, dtype=dt, device="cuda"), torch.empty(0, 24, dtype=dt, device="cuda")
+    for r, o in ((0, off), (4, off[:1])):
+        u = normal((rows, max(r, 1)), 14, dt)[:, :r]
+        s = o.numel() - 1
+        dx, da, db = g.lora_backward(dy, x, u, w, torch.empty(s, 0, r, dtype=dt, device="cuda"),
+                                     torch.empty(s, r, 24, dtype=dt, device="cuda"), o)
+        assert dx.shape == (rows, 0) and da.shape == (s, 0, r) and db.shape == (s, r, 24)
+    u, b = normal((rows, 4), 14, dt), normal((1, 4, 24), 15, dt)
+    dx, da, db = g.lora_backward(dy, x, u, w, torch.empty(1, 0, 4, dtype=dt, device="cuda"), b, off)
+    c64, s64 = product(u.t(), dy)
+    check(db[0], c64, rounding(c64, s64, rows, dt))
