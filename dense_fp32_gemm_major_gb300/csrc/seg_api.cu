@@ -97,7 +97,8 @@ class Workspace {
 
   // Room for splitting the tiles of a product of this shape.
   void splits(const SegArgs &a) {
-    if (gemm::seg_tc_splits(a) && !gemm::seg_rows_fits(a)) split_ = true;
+    if (gemm::seg_tc_splits(a) && !(gemm::seg_rows_fits(a) && gemm::seg_rows_few(a) == 0))
+      split_ = true;
   }
 
   // Allocate, place, zero the split tiles' counters, and copy.
@@ -124,7 +125,12 @@ class Workspace {
 
   // One product, with the scratch it may want.
   int launch(SegArgs &a, cudaStream_t s) {
-    if (gemm::seg_rows_fits(a)) return gemm::seg_rows_launch(a, sms_, s);
+    if (gemm::seg_rows_fits(a)) {
+      a.few = gemm::seg_rows_few(a);
+      const int st = gemm::seg_rows_launch(a, sms_, s);
+      if (st != gemm::kOk || a.few == 0) return st;
+      a.ahead = true;  // other rows of the same operands
+    }
     if (split_) {
       a.slots = slots_;
       a.arrived = arrived_ + static_cast<size_t>(products_++ % kProducts) * sms_;

@@ -35,6 +35,9 @@ constexpr int kThreads = 256, kRows = 4, kWarpN = 4;
 constexpr int kSlices = 4, kSliceK = 1024;  // CTAs of a contraction, from this k on
 // bf16 operands longer than kShortK: most of N (M + 2 CTAs' rows), seg_rows_fits.
 constexpr int64_t kShortK = 128, kMostBf16 = 36 * 1024;
+// FMAs of a product whose rows may all lie in one segment: 2 million of them take
+// a microsecond, since every four rows read the matrix again (seg_rows_few).
+constexpr double kMostSkewed = 128e6;
 constexpr int kStaged = 8192;  // values of A that stand in shared memory at a time
 
 struct P {
@@ -47,6 +50,8 @@ struct P {
   long long a_extent, b_extent, c_extent, c_lo_extent, add_extent, a_lo_extent;
   int M, N, K, groups, bank, dense, c_f32, slices;
   int alone;  // one row a CTA
+  int few;    // rows of a segment, at most (0: any number)
+  int span;   // rows that a CTA looks at, one after another
 };
 
 template <class T>
@@ -118,16 +123,17 @@ __device__ __forceinline__ void stage_a(const P &p, float *as, int t, int count,
 }
 
 // Rows [t, t + count) that this CTA computes, their matrix (-1: none), its
-// scale, and the rows that have an addend: blockIdx.y is a row; unless each is
-// alone, every fourth of a segment takes those behind it.
+// scale, and the rows that have an addend: t is a row; unless each is alone,
+// every fourth of a segment takes those behind it.
 struct Rows {
   int count, z, add0, add1;
+  int next;  // where a CTA of several rows goes on
   float scale;
 };
 
-__device__ __forceinline__ bool rows_of(const P &p, Rows *o) {
-  const int t = blockIdx.y;
+__device__ __forceinline__ bool rows_of(const P &p, int t, Rows *o) {
   int first = 0, last = p.M;
+  o->next = t + 1;
   o->z = 0;
   o->scale = 1.0f;
   o->add0 = o->add1 = 0;
@@ -155,6 +161,10 @@ __device__ __forceinline__ bool rows_of(const P &p, Rows *o) {
     if (found[0] < 0) return false;
     first = found[1];
     last = found[2];
+    if (p.few > 0 && last - first > p.few) {
+      o->next = last;
+      return false;
+    }
     o->z = found[0] < p.bank ? found[0] : -1;
     if (p.scales != nullptr && o->z >= 0) o->scale = p.scales[o->z];
   }
@@ -163,6 +173,7 @@ __device__ __forceinline__ bool rows_of(const P &p, Rows *o) {
   const int step = p.alone ? 1 : kRows;
   if ((t - first) % step != 0) return false;
   o->count = min(step, last - t);
+  o->next = t + o->count;
   return true;
 }
 
@@ -191,190 +202,222 @@ __device__ __forceinline__ void store(const P &p, int row, int n, float v, const
 // CTAs an SM that the compiler plans registers for. bf16: with two (three for B
 // stored N x K) it holds the loads of two rounds (one row of 4096 x 4096 12 -> 8
 // us, 20 -> 11). float32 is left to it (0): four CTAs of one round are faster
-// than two of two (9 against 12 us).
-template <class T, int BF16>
-constexpr int kCtas = Vec<T>::n == 4 ? 0 : BF16;
+// than two of two (9 against 12 us); in a loop over rows (SPAN) it has to be told.
+template <class T, int BF16, bool SPAN>
+constexpr int kCtas = Vec<T>::n == 4 ? (SPAN ? 4 : 0) : BF16;
+
+// This CTA's rows, one product after another: f(t, rows). SPAN: more than one.
+template <bool SPAN, class F>
+__device__ __forceinline__ void for_rows(const P &p, const F &f) {
+  Rows o;
+  if constexpr (SPAN) {
+    const int t0 = static_cast<int>(blockIdx.y) * p.span, end = min(t0 + p.span, p.M);
+    for (int t = t0; t < end; t = o.next) {
+      if (t > t0) __syncthreads();  // shared memory of the one before is read
+      if (rows_of(p, t, &o)) f(t, o);
+    }
+  } else if (rows_of(p, static_cast<int>(blockIdx.y), &o)) {
+    f(static_cast<int>(blockIdx.y), o);
+  }
+}
 
 // B stored K x N. TX threads of 16 bytes across the CTA's columns, DEEP rows of
 // B in flight a thread.
-template <class T, int TX, int kDeep>
-__global__ void __launch_bounds__(kThreads, kCtas<T, 2>) seg_rows_kn_kernel(const P p) {
+template <class T, int TX, int kDeep, bool SPAN>
+__global__ void __launch_bounds__(kThreads, kCtas<T, 2, SPAN>) seg_rows_kn_kernel(const P p) {
   constexpr int V = Vec<T>::n, TY = kThreads / TX, NT = TX * V;
   __shared__ float sums[TY * NT], as[kStaged];
   float *const total = as;  // in the end: [count][NT]
   static_assert(kRows * NT <= kStaged, "totals in A's place");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Rows o;
-  if (!rows_of(p, &o)) return;
-  const int count = o.count, z = o.z;
-  const int t = blockIdx.y, n0 = blockIdx.x * NT;
-  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, n = n0 + tx * V;
-  // This CTA's k, a multiple of 16 but for the last one's end.
-  const int slice = (p.K / 16 + p.slices - 1) / p.slices * 16;
-  const int k_lo = min(static_cast<int>(blockIdx.z) * slice, p.K);
-  const int k_hi = static_cast<int>(blockIdx.z) + 1 == p.slices ? p.K : min(k_lo + slice, p.K);
-  float acc[kRows][V] = {};
-  if (z >= 0) {
-    const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
-    const long long extent = p.b_extent - z * p.b_stride;
-    const int chunk = chunk_of(count);
-    for (int c0 = k_lo; c0 < k_hi; c0 += chunk) {
-      const int c1 = min(chunk, k_hi - c0);
-      if (c0 > k_lo) __syncthreads();
-      stage_a<T>(p, as, t, count, c0, k_hi, chunk);
-      __syncthreads();
+  for_rows<SPAN>(p, [&](int t, const Rows &o) {
+    const int count = o.count, z = o.z;
+    const int n0 = blockIdx.x * NT;
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, n = n0 + tx * V;
+    // This CTA's k, a multiple of 16 but for the last one's end.
+    const int slice = (p.K / 16 + p.slices - 1) / p.slices * 16;
+    const int k_lo = min(static_cast<int>(blockIdx.z) * slice, p.K);
+    const int k_hi = static_cast<int>(blockIdx.z) + 1 == p.slices ? p.K : min(k_lo + slice, p.K);
+    float acc[kRows][V] = {};
+    if (z >= 0) {
+      const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
+      const long long extent = p.b_extent - z * p.b_stride;
+      const int chunk = chunk_of(count);
+      for (int c0 = k_lo; c0 < k_hi; c0 += chunk) {
+        const int c1 = min(chunk, k_hi - c0);
+        if (c0 > k_lo) __syncthreads();
+        stage_a<T>(p, as, t, count, c0, k_hi, chunk);
+        __syncthreads();
 #pragma unroll 2
-      for (int k = ty * kDeep; k < c1; k += TY * kDeep) {
-        uint4 w[kDeep];
+        for (int k = ty * kDeep; k < c1; k += TY * kDeep) {
+          uint4 w[kDeep];
 #pragma unroll
-        for (int j = 0; j < kDeep; ++j)
-          w[j] = load16<T>(B, static_cast<long long>(c0 + k + j) * p.b_ld + n,
-                           k + j < c1 ? p.N - n : 0, kSiteLoadB, extent);
-        float b[kDeep][V];
+          for (int j = 0; j < kDeep; ++j)
+            w[j] = load16<T>(B, static_cast<long long>(c0 + k + j) * p.b_ld + n,
+                             k + j < c1 ? p.N - n : 0, kSiteLoadB, extent);
+          float b[kDeep][V];
 #pragma unroll
-        for (int j = 0; j < kDeep; ++j) unpack<T>(w[j], b[j]);
+          for (int j = 0; j < kDeep; ++j) unpack<T>(w[j], b[j]);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          if (r < count) {
+          for (int r = 0; r < kRows; ++r)
+            if (r < count) {
 #pragma unroll
-            for (int j = 0; j < kDeep; ++j)
+              for (int j = 0; j < kDeep; ++j)
 #pragma unroll
-              for (int v = 0; v < V; ++v)
-                acc[r][v] = fmaf(as[r * chunk + k + j], b[j][v], acc[r][v]);
-          }
+                for (int v = 0; v < V; ++v)
+                  acc[r][v] = fmaf(as[r * chunk + k + j], b[j][v], acc[r][v]);
+            }
+        }
       }
     }
-  }
-  // Two steps: groups of threads add TY / G of a column's sums, then one the
-  // groups'.
-  constexpr int G = NT < kThreads ? kThreads / NT : 1, PER = TY / G > 0 ? TY / G : 1;
+    // Two steps: groups of threads add TY / G of a column's sums, then one the
+    // groups'.
+    constexpr int G = NT < kThreads ? kThreads / NT : 1, PER = TY / G > 0 ? TY / G : 1;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    if (r >= count) break;
+    for (int r = 0; r < kRows; ++r) {
+      if (r >= count) break;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sums[ty * NT + tx * V + v] = acc[r][v];
-    __syncthreads();
-    if constexpr (G > 1 && TY % G == 0) {
-      const int c = threadIdx.x % NT, group = threadIdx.x / NT;
-      float s = 0.0f;
-#pragma unroll
-      for (int y = 0; y < PER; ++y) s += sums[(group * PER + y) * NT + c];
+      for (int v = 0; v < V; ++v) sums[ty * NT + tx * V + v] = acc[r][v];
       __syncthreads();
-      sums[group * NT + c] = s;
-      __syncthreads();
-      if (group == 0) {
-        s = 0.0f;
-#pragma unroll
-        for (int y = 0; y < G; ++y) s += sums[y * NT + c];
-        total[r * NT + c] = s;
-      }
-    } else {
-      for (int c = threadIdx.x; c < NT; c += kThreads) {
+      if constexpr (G > 1 && TY % G == 0) {
+        const int c = threadIdx.x % NT, group = threadIdx.x / NT;
         float s = 0.0f;
 #pragma unroll
-        for (int y = 0; y < TY; ++y) s += sums[y * NT + c];
-        total[r * NT + c] = s;
+        for (int y = 0; y < PER; ++y) s += sums[(group * PER + y) * NT + c];
+        __syncthreads();
+        sums[group * NT + c] = s;
+        __syncthreads();
+        if (group == 0) {
+          s = 0.0f;
+#pragma unroll
+          for (int y = 0; y < G; ++y) s += sums[y * NT + c];
+          total[r * NT + c] = s;
+        }
+      } else {
+        for (int c = threadIdx.x; c < NT; c += kThreads) {
+          float s = 0.0f;
+#pragma unroll
+          for (int y = 0; y < TY; ++y) s += sums[y * NT + c];
+          total[r * NT + c] = s;
+        }
+      }
+      __syncthreads();
+    }
+    if (p.slices > 1) cluster_sync();  // every CTA's totals are there
+    if (blockIdx.z == 0) {
+      for (int i = threadIdx.x; i < count * NT; i += kThreads) {
+        const int r = i / NT, c = i % NT;
+        float s = total[i];
+        for (int q = 1; q < p.slices; ++q) {
+          uint32_t at;
+          float v;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                       : "=r"(at)
+                       : "r"(smem_addr(total + i)), "r"(q));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+          s += v;
+        }
+        if (n0 + c < p.N) store<T>(p, t + r, n0 + c, s, o);
       }
     }
-    __syncthreads();
-  }
-  if (p.slices > 1) cluster_sync();  // every CTA's totals are there
-  if (blockIdx.z == 0) {
-    for (int i = threadIdx.x; i < count * NT; i += kThreads) {
-      const int r = i / NT, c = i % NT;
-      float s = total[i];
-      for (int q = 1; q < p.slices; ++q) {
-        uint32_t at;
-        float v;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(at)
-                     : "r"(smem_addr(total + i)), "r"(q));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-        s += v;
-      }
-      if (n0 + c < p.N) store<T>(p, t + r, n0 + c, s, o);
-    }
-  }
-  if (p.slices > 1) cluster_sync();  // and stay until they are read
+    if (p.slices > 1) cluster_sync();  // and stay until they are read
+  });
 }
 
 // B stored N x K. A warp takes kWarpN columns.
-template <class T>
-__global__ void __launch_bounds__(kThreads, kCtas<T, 3>) seg_rows_nk_kernel(const P p) {
+template <class T, bool SPAN>
+__global__ void __launch_bounds__(kThreads, kCtas<T, 3, SPAN>) seg_rows_nk_kernel(const P p) {
   constexpr int V = Vec<T>::n;
+  __shared__ __align__(16) float as[kStaged];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Rows o;
-  if (!rows_of(p, &o)) return;
-  const int count = o.count, z = o.z;
-  const int t = blockIdx.y, lane = threadIdx.x & 31;
-  const int n0 = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpN;
-  __shared__ __align__(16) float as[kStaged];
-  float acc[kRows][kWarpN] = {};
-  if (z >= 0) {
-    const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
-    const long long extent = p.b_extent - z * p.b_stride;
-    const int chunk = chunk_of(count);
-    for (int c0 = 0; c0 < p.K; c0 += chunk) {
-      const int c1 = min(chunk, p.K - c0);
-      if (c0 > 0) __syncthreads();
-      stage_a<T>(p, as, t, count, c0, p.K, chunk);
-      __syncthreads();
+  for_rows<SPAN>(p, [&](int t, const Rows &o) {
+    const int count = o.count, z = o.z;
+    const int lane = threadIdx.x & 31;
+    const int n0 = (blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kWarpN;
+    float acc[kRows][kWarpN] = {};
+    if (z >= 0) {
+      const T *B = static_cast<const T *>(p.B) + z * p.b_stride;
+      const long long extent = p.b_extent - z * p.b_stride;
+      const int chunk = chunk_of(count);
+      for (int c0 = 0; c0 < p.K; c0 += chunk) {
+        const int c1 = min(chunk, p.K - c0);
+        if (c0 > 0) __syncthreads();
+        stage_a<T>(p, as, t, count, c0, p.K, chunk);
+        __syncthreads();
 #pragma unroll 2
-      for (int k = lane * V; k < c1; k += 32 * V) {
-        uint4 w[kWarpN];
+        for (int k = lane * V; k < c1; k += 32 * V) {
+          uint4 w[kWarpN];
 #pragma unroll
-        for (int j = 0; j < kWarpN; ++j)
-          w[j] = load16<T>(B, static_cast<long long>(n0 + j) * p.b_ld + c0 + k,
-                           n0 + j < p.N ? c1 - k : 0, kSiteLoadB, extent);
-        float b[kWarpN][V];
+          for (int j = 0; j < kWarpN; ++j)
+            w[j] = load16<T>(B, static_cast<long long>(n0 + j) * p.b_ld + c0 + k,
+                             n0 + j < p.N ? c1 - k : 0, kSiteLoadB, extent);
+          float b[kWarpN][V];
 #pragma unroll
-        for (int j = 0; j < kWarpN; ++j) unpack<T>(w[j], b[j]);
+          for (int j = 0; j < kWarpN; ++j) unpack<T>(w[j], b[j]);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          if (r < count) {
+          for (int r = 0; r < kRows; ++r)
+            if (r < count) {
 #pragma unroll
-            for (int v = 0; v < V; v += 4) {
-              const float4 x = *reinterpret_cast<const float4 *>(as + r * chunk + k + v);
+              for (int v = 0; v < V; v += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(as + r * chunk + k + v);
 #pragma unroll
-              for (int j = 0; j < kWarpN; ++j) {
-                acc[r][j] = fmaf(x.x, b[j][v], acc[r][j]);
-                acc[r][j] = fmaf(x.y, b[j][v + 1], acc[r][j]);
-                acc[r][j] = fmaf(x.z, b[j][v + 2], acc[r][j]);
-                acc[r][j] = fmaf(x.w, b[j][v + 3], acc[r][j]);
+                for (int j = 0; j < kWarpN; ++j) {
+                  acc[r][j] = fmaf(x.x, b[j][v], acc[r][j]);
+                  acc[r][j] = fmaf(x.y, b[j][v + 1], acc[r][j]);
+                  acc[r][j] = fmaf(x.z, b[j][v + 2], acc[r][j]);
+                  acc[r][j] = fmaf(x.w, b[j][v + 3], acc[r][j]);
+                }
               }
             }
-          }
+        }
       }
     }
-  }
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
-    if (r < count) {
+    for (int r = 0; r < kRows; ++r)
+      if (r < count) {
 #pragma unroll
-      for (int j = 0; j < kWarpN; ++j) {
-        float s = acc[r][j];
+        for (int j = 0; j < kWarpN; ++j) {
+          float s = acc[r][j];
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        if (lane == 0 && n0 + j < p.N) store<T>(p, t + r, n0 + j, s, o);
+          for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+          if (lane == 0 && n0 + j < p.N) store<T>(p, t + r, n0 + j, s, o);
+        }
       }
-    }
+  });
 }
 
 long long extent_of(const SegMatrix &m) {
   return (m.count - 1) * m.stride + matrix_extent(m.rows, m.cols, m.ld);
 }
 
+// CTAs of a launch with a row each.
+long long ctas_of(const P &p, int columns) {
+  return static_cast<long long>((p.N + columns - 1) / columns) * p.M * p.slices;
+}
+
+// Rows a CTA looks at. Where segments may be left to the tensor cores, CTAs that
+// find nothing to do are the cost: 65536 of them (512 rows x 1024 x 1024 float32,
+// all in one segment) take 77 us of the GPU. Then 64 CTAs an SM share the rows
+// (that case 341 us evenly routed and 59 in one segment with 160 CTAs an SM, 344
+// and 45 with 64; 16 an SM no longer balance, 381 us). Up to 192 an SM a row
+// each is faster (32 rows, 16 segments, 4096 x 4096: 191 against 209 us).
+int span_of(const P &p, int columns, int sms) {
+  const long long ctas = ctas_of(p, columns);
+  if (p.few == 0 || ctas <= 192LL * sms) return 1;
+  return static_cast<int>((ctas + 64LL * sms - 1) / (64LL * sms));
+}
+
 template <class K>
 int launch(K kernel, P p, int columns, int sms, cudaStream_t stream) {
   // Rows together read their matrix once; where there are too few CTAs to fill
   // the GPU, one row each is faster (8 x 512 x 512 bf16: 7.0 -> 4.7 us).
-  const long long each = static_cast<long long>((p.N + columns - 1) / columns) * p.M * p.slices;
-  p.alone = each <= 2LL * sms;
+  p.alone = ctas_of(p, columns) <= 2LL * sms;
+  const int rows = (p.M + p.span - 1) / p.span;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.N + columns - 1) / columns),
-                     static_cast<unsigned>(p.M), static_cast<unsigned>(p.slices));
+                     static_cast<unsigned>(rows), static_cast<unsigned>(p.slices));
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -389,18 +432,29 @@ int launch(K kernel, P p, int columns, int sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? kOk : kErrLaunch;
 }
 
+template <class T, int TX>
+int launch_kn(P p, int sms, cudaStream_t stream) {
+  constexpr int kColumns = TX * Vec<T>::n;
+  p.span = span_of(p, kColumns, sms);
+  return p.span > 1 ? launch(seg_rows_kn_kernel<T, TX, 8, true>, p, kColumns, sms, stream)
+                    : launch(seg_rows_kn_kernel<T, TX, 8, false>, p, kColumns, sms, stream);
+}
+
 template <class T>
 int launch_type(P p, int transb, int sms, cudaStream_t stream) {
-  constexpr int V = Vec<T>::n;
+  constexpr int V = Vec<T>::n, kColumns = kThreads / 32 * kWarpN;
   p.slices = !transb && p.K >= kSliceK ? kSlices : 1;
-  if (transb) return launch(seg_rows_nk_kernel<T>, p, kThreads / 32 * kWarpN, sms, stream);
+  if (transb) {
+    p.span = span_of(p, kColumns, sms);
+    return p.span > 1 ? launch(seg_rows_nk_kernel<T, true>, p, kColumns, sms, stream)
+                      : launch(seg_rows_nk_kernel<T, false>, p, kColumns, sms, stream);
+  }
   // A short contraction has no work for many threads along k; a narrow result
   // none for many along n.
-  if (p.K <= 16 && p.N >= 512 * V)
-    return launch(seg_rows_kn_kernel<T, 128, 8>, p, 128 * V, sms, stream);
-  if (p.K <= 64) return launch(seg_rows_kn_kernel<T, 32, 8>, p, 32 * V, sms, stream);
-  if (p.N <= 2 * V) return launch(seg_rows_kn_kernel<T, 2, 8>, p, 2 * V, sms, stream);
-  return launch(seg_rows_kn_kernel<T, 8, 8>, p, 8 * V, sms, stream);
+  if (p.K <= 16 && p.N >= 512 * V) return launch_kn<T, 128>(p, sms, stream);
+  if (p.K <= 64) return launch_kn<T, 32>(p, sms, stream);
+  if (p.N <= 2 * V) return launch_kn<T, 2>(p, sms, stream);
+  return launch_kn<T, 8>(p, sms, stream);
 }
 
 }  // namespace
@@ -420,6 +474,19 @@ bool seg_rows_fits(const SegArgs &a) {
   // 33, of two 15 and 23; one row of 4096 x 11008 24 and 29, four 38 and 29.
   const int64_t ctas = a.dense ? fours : (a.M < a.groups - 1 + fours ? a.M : a.groups - 1 + fours);
   return a.N * (a.M + 2 * ctas) <= kMostBf16;
+}
+
+// The host knows the rows' average, not where they are: 512 rows of 256 experts
+// may all have chosen one. Its matrix of 1024 x 1024 float32 was then read 128
+// times (240 us; the tensor cores' one product 31), one of 128 x 11008 bf16 as
+// often (508 against 14). Past kMostSkewed segments of more than eight rows are
+// left to the tensor cores, in a launch of their own (45 and 34 us). Where all
+// have few rows that launch costs 6 us (32 rows, 16 segments, 4096 x 4096
+// float32: 184 -> 191); below, the worst case takes no longer than the even one
+// (64 rows, 64 segments, 1024 x 1024: 33 us in one segment, 71 in all).
+int seg_rows_few(const SegArgs &a) {
+  const double work = static_cast<double>(a.M) * static_cast<double>(a.N * a.K);
+  return a.dense || a.M <= 2 * kRows || work <= kMostSkewed ? 0 : 2 * kRows;
 }
 
 int seg_rows_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
@@ -452,6 +519,7 @@ int seg_rows_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   p.groups = static_cast<int>(a.groups);
   p.bank = static_cast<int>(a.bank);
   p.dense = a.dense;
+  p.few = a.few;
   p.c_f32 = !a.bf16 || a.c_f32;
   return a.bf16 ? launch_type<__nv_bfloat16>(p, a.transb, sm_count, stream)
                 : launch_type<float>(p, a.transb, sm_count, stream);

@@ -104,6 +104,7 @@ struct SegTc {
   float *slots;
   unsigned *arrived;  // [2 tile + rank] of the split tiles, zero
   long long slot_extent;
+  int few;            // rows: segments of up to this many are another launch's
   int ahead;          // starts before the launch before it has ended (SegArgs::ahead)
   unsigned long long timeout_ns;
 };
@@ -188,6 +189,12 @@ __device__ __forceinline__ int quotient(int a, int b) {
   return q - (q * b > a) + ((q + 1) * b <= a);
 }
 
+// Rows of an entry, none where they are another launch's.
+__device__ __forceinline__ int rows_of(const SegTc &p, const Table &tab, int g) {
+  const int rows = tab.row[g + 1] - tab.row[g];
+  return rows > p.few ? rows : 0;
+}
+
 __device__ __forceinline__ int matrix_of(const SegTc &p, int g) {
   const int z = p.index != nullptr ? p.index[g] : g;
   return z >= 0 && z < p.bank ? z : -1;
@@ -220,7 +227,7 @@ __device__ __forceinline__ bool tile_at(const SegTc &p, const Table &tab, int it
       hi = mid;
   }
   const int idx = t - tab.first[lo];
-  const int r0 = tab.row[lo], rows = max(tab.row[lo + 1] - r0, 0);
+  const int r0 = tab.row[lo], rows = rows_of(p, tab, lo);
   const int height = p.form == kWgrad ? p.K : rows;
   const int tm = (height + (1 << tab.shift) - 1) >> tab.shift;
   // Groups of kRasterM row tiles, lane tiles in the outer loop, so that the
@@ -531,6 +538,16 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
   constexpr int kFullCount = C::kSplit || QMN ? 2 : 1;
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
+  if (p.few > 0) {
+    // Nothing to do where all segments are the launch before's, behind whose
+    // end this one ends (for the launches that count on that).
+    int any = 0;
+    for (int g = threadIdx.x; g < p.groups; g += C::kThreads) any |= p.offsets[g + 1] - p.offsets[g] > p.few;
+    if (!__syncthreads_or(any)) {
+      grid_dependency_wait();
+      return;
+    }
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&sh->full[s], kFullCount);
@@ -580,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
   }
   __syncthreads();
   for (int g = threadIdx.x; g < p.entries; g += C::kThreads) {
-    const int rows = max(tab.row[g + 1] - tab.row[g], 0);
+    const int rows = rows_of(p, tab, g);
     const int height = p.form == kWgrad ? p.K : rows;
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -600,9 +617,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
       const int g = g0 + static_cast<int>(lane);
       int own = 0;
       if (g < p.entries)
-        own = cdiv(p.form == kWgrad ? p.K : max(tab.row[g + 1] - tab.row[g], 0),
-                   1 << tab.shift) *
-              p.tiles_n;
+        own = cdiv(p.form == kWgrad ? p.K : rows_of(p, tab, g), 1 << tab.shift) * p.tiles_n;
       int v = own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -1324,6 +1339,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   const int64_t c_elem = p.c_f32 ? 4 : 2;
   p.c_rows = a.C_lo.p == nullptr && reinterpret_cast<uintptr_t>(a.C.p) % 16 == 0 &&
              a.C.ld * c_elem % 16 == 0 && a.C.stride * c_elem % 16 == 0 && a.N * c_elem % 16 == 0;
+  p.few = a.few;
   p.ahead = a.ahead;
   p.c_ld = a.C.ld;
   p.c_stride = a.C.stride;

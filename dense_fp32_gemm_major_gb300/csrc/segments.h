@@ -52,6 +52,9 @@ struct SegArgs {
   // pair, zero before the launch. null: no splits.
   float *slots = nullptr;
   unsigned *arrived = nullptr;
+  // rows: > 0: two launches share the product, seg_rows the segments of up to
+  // this many rows, seg_tc the others.
+  int few = 0;
 };
 
 // Whether a product's contraction is long enough to be worth splitting, and
@@ -67,8 +70,11 @@ bool seg_tc_readable(const SegMatrix &m, bool bf16);
 int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
 
 // Products of very few rows (rows and dense forms): whether these arguments are
-// such a product, and its launch. Operands readable.
+// such a product, its launch (operands readable), and the rows a segment may
+// have in it (SegArgs::few): 0 where the launch is fast enough whichever
+// segments hold the rows.
 bool seg_rows_fits(const SegArgs &a);
+int seg_rows_few(const SegArgs &a);
 int seg_rows_launch(const SegArgs &a, int sm_count, cudaStream_t stream);
 
 int seg_rows_index_fault_take(IndexFault *out, bool clear);

@@ -142,3 +142,95 @@ def test_lora_backward_of_a_projection_without_inputs(g, rows, dt):
     dx, da, db = g.lora_backward(dy, x, u, w, torch.empty(1, 0, 4, dtype=dt, device="cuda"), b, off)
     c64, s64 = product(u.t(), dy)
     check(db[0], c64, rounding(c64, s64, rows, dt))
+
+
+# rows, segments, contraction, columns: as many rows as the segments' average of
+# two allows, and products whose matrices are many times what one CTA reads
+SKEW = [(512, 256, 1024, 1024), (64, 64, 512, 2048), (200, 100, 96, 1040), (512, 300, 128, 2050),
+        (40, 24, 333, 1531), (9, 5, 4096, 1024)]
+
+
+@pytest.mark.parametrize("m, groups, k, n", SKEW, ids=str)
+@pytest.mark.parametrize("route", ["one", "few", "even", "ends"])
+@pytest.mark.parametrize("transb", [False, True])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_skewed_routing(g, m, groups, k, n, route, transb, dt):
+    sizes = [0] * groups
+    for i in range(m):
+        sizes[{"one": groups // 2, "few": i % 3 * (groups // 3), "even": i % groups,
+               "ends": (i % 7 > 0) * (groups - 1)}[route]] += 1
+    off, o = offsets_of(sizes)
+    a = normal((m, k), 20, dt)
+    b = normal((1,) + ((n, k) if transb else (k, n)), 21, dt)
+    scale = 2.0 ** (torch.arange(groups, device="cuda") % 5 - 2)  # every segment's own, exactly
+    b = (b * scale[:, None, None]).to(dt)
+    c = g.grouped_matmul(a, b, off, transb)
+    of_row = torch.repeat_interleave(scale.double(), torch.tensor(sizes, device="cuda"))[:, None]
+    c64, s64 = product(a, b[2].t() if transb else b[2])  # scale 1
+    check(c, c64 * of_row, rounding(c64 * of_row, s64 * of_row, k, dt))
+    assert torch.equal(c, g.grouped_matmul(a, b, off, transb))
+
+
+@pytest.mark.parametrize("dt, m, groups, k, n", [(torch.float32, 512, 256, 1024, 1024),
+                                                 (torch.float32, 128, 64, 2048, 4096),
+                                                 (torch.bfloat16, 512, 256, 128, 11008)], ids=str)
+def test_skewed_routing_costs_no_more_than_one_product(g, dt, m, groups, k, n):
+    # All rows to one of many experts is the product of one matrix: read once
+    # for every few rows it took 5 to 20 times as long (here: up to 3 times,
+    # with what it takes to look for the others' rows).
+    a, b = normal((m, k), 22, dt), torch.zeros(groups, k, n, dtype=dt, device="cuda")
+    off, _ = offsets_of([0] * (groups // 2) + [m] + [0] * (groups - groups // 2 - 1))
+    alone, _ = offsets_of([m])
+
+    def time(b, off):
+        out, best = torch.empty(m, n, dtype=dt, device="cuda"), float("inf")
+        for _ in range(8):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda._sleep(200_000)  # the calls queue up behind it
+            start.record()
+            for _ in range(4):
+                g.grouped_matmul(a, b, off, out=out)
+            end.record()
+            end.synchronize()
+            best = min(best, start.elapsed_time(end))
+        return best
+
+    skewed, one = time(b, off), time(b[:1], alone)
+    assert skewed <= 3 * one, (skewed, one)
+
+
+@pytest.mark.parametrize("route", ["one", "few", "even"])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_skewed_requests_of_adapters(g, route, trans, dt):
+    # the products of U and with U each shared by two launches, between others
+    m, segments, k, n, r = 400, 200, 2048, 4400, 96
+    sizes = [0] * segments
+    for i in range(m):
+        sizes[{"one": 77, "few": i % 3 * 50, "even": i // 2}[route]] += 1
+    off, o = offsets_of(sizes)
+    which = [i % 6 - 1 for i in range(segments)]
+    index = torch.tensor(which, dtype=torch.int32, device="cuda")
+    w = normal((n, k) if trans else (k, n), 33, dt)
+    a = normal((5, r, k) if trans else (5, k, r), 34, dt)
+    b = normal((5, n, r) if trans else (5, r, n), 35, dt)
+    scales = torch.rand(5, device="cuda") + 0.5
+    jobs = [normal((m, k), 36 + i, dt) for i in range(3)]
+    x, u = torch.empty_like(jobs[0]), torch.empty(m, r, dtype=dt, device="cuda")
+
+    def step(i, wait):
+        x.copy_(jobs[i])
+        u.fill_(float("nan"))
+        wait()
+        y = g.lora_matmul(x, w, a, b, off, index, scales, trans, trans, shrink_out=u)
+        x.fill_(float("nan"))
+        return y, u.clone()
+
+    refs = [step(i, torch.cuda.synchronize) for i in range(3)]
+    at, bt = [t.t() if trans else t for t in a], [t.t() if trans else t for t in b]
+    y64, ty, u64, tu = lora_64(jobs[0], w.t() if trans else w, at, bt, o, which, scales)
+    check(refs[0][0], y64, ty, "y")
+    check(refs[0][1], u64, tu, "u")
+    outs = [(i, step(i, lambda: None)) for _ in range(4) for i in range(3)]
+    for i, out in outs:
+        assert torch.equal(out[0], refs[i][0]) and torch.equal(out[1], refs[i][1])
