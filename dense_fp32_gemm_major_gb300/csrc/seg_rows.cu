@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "ptx.cuh"
+#include "seg_terms.cuh"
 #include "segments.h"
 
 namespace gemm {
@@ -195,7 +196,7 @@ __device__ __forceinline__ void store(const P &p, int row, int n, float v, const
   if (p.C_lo != nullptr) {
     const long long lo = row * p.c_lo_ld + n;
     if (index_ok(kSitePartialWrite, lo, 1, p.c_lo_extent))
-      static_cast<__nv_bfloat16 *>(p.C_lo)[lo] = __float2bfloat16_rn(v - static_cast<float>(h));
+      static_cast<__nv_bfloat16 *>(p.C_lo)[lo] = second_term(v, h);
   }
 }
 

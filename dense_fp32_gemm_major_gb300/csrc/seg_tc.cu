@@ -54,6 +54,7 @@
 #include <type_traits>
 
 #include "ptx.cuh"
+#include "seg_terms.cuh"
 #include "segments.h"
 
 namespace gemm {
@@ -1022,8 +1023,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             for (int k = 0; k < 16; ++k) {
               const long long off = (row0 + c + k) * p.c_lo_ld + n;
               if (c + k < count && index_ok(kSitePartialWrite, off, 1, p.c_lo_extent))
-                lo[off] = __float2bfloat16_rn(
-                    f[k] - static_cast<float>(__float2bfloat16_rn(f[k])));
+                lo[off] = second_term(f[k], __float2bfloat16_rn(f[k]));
             }
           }
         }

@@ -234,3 +234,29 @@ def test_skewed_requests_of_adapters(g, route, trans, dt):
     outs = [(i, step(i, lambda: None)) for _ in range(4) for i in range(3)]
     for i, out in outs:
         assert torch.equal(out[0], refs[i][0]) and torch.equal(out[1], refs[i][1])
+
+
+@pytest.mark.parametrize("sizes, k, n", [([2, 2], 64, 264), ([30, 20], 64, 264), ([256, 300], 128, 520)],
+                         ids=lambda v: str(v))
+def test_infinite_shrink_of_bf16_stays_infinite(g, sizes, k, n):
+    # U, held as two terms, is infinite in one row: so is the row's result, not
+    # NaN (every factor of that row's sums is positive)
+    dt = torch.bfloat16
+    off, o = offsets_of(sizes)
+    x, w = normal((o[-1], k), 16, dt), normal((k, n), 17, dt).abs()
+    a, b = normal((2, k, 8), 18, dt).abs(), normal((2, 8, n), 19, dt).abs() + 0.5
+    w[0], a[:, 0] = 1, 1
+    for value in (float("inf"), 3.3e38):  # the second: sums that pass the largest value
+        x[1] = 1
+        x[1, 0] = value
+        if value != float("inf"):
+            a[:, 0] = 4
+        u = torch.empty(o[-1], 8, dtype=dt, device="cuda")
+        y = g.lora_matmul(x, w, a, b, off, shrink_out=u)
+        assert (u[1] == float("inf")).all()
+        assert (y[1] == float("inf")).all()
+        keep = [t for t in range(o[-1]) if t != 1]
+        one = torch.ones(2, device="cuda")
+        x[1] = 0
+        y64, ty, _, _ = lora_64(x, w, a, b, o, range(2), one)
+        check(y[keep], y64[keep], ty[keep])
