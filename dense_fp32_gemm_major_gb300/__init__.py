@@ -52,7 +52,7 @@ ROW_MAJOR, COL_MAJOR = 0, 1
 OP_N, OP_T = 0, 1
 # gemm_f32_type
 TYPE_F32, TYPE_BF16 = 0, 1
-MAX_SEGMENTS = 2048
+MAX_SEGMENTS, MAX_SEGMENT_SIZE = 2048, 0x7c000000
 
 
 class GemmError(RuntimeError):

@@ -13,7 +13,7 @@ namespace {
 using gemm::SegArgs;
 using gemm::SegMatrix;
 
-constexpr int64_t kMaxDim = 0x7fffffffLL;       // sizes and pitches < 2^31
+constexpr int64_t kMaxPitch = 0x7fffffffLL;     // pitches and banks < 2^31
 constexpr int64_t kMaxSpan = int64_t{1} << 44;  // elements one stack may span
 
 struct Range {
@@ -22,13 +22,13 @@ struct Range {
 
 bool overlap(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi; }
 
-bool dim_ok(int64_t x) { return x >= 0 && x <= kMaxDim; }
+bool dim_ok(int64_t x) { return x >= 0 && x <= GEMM_F32_MAX_SEGMENT_SIZE; }
 
 // A stack of matrices the call may touch: its pitch and stride, and (unless it
 // is empty) its pointer. `disjoint`: a result, whose matrices must not share
 // elements.
 bool stack_ok(const SegMatrix &m, int elem, bool disjoint, Range *range) {
-  if (m.ld < (m.cols > 1 ? m.cols : 1) || m.ld > kMaxDim || m.stride < 0) return false;
+  if (m.ld < (m.cols > 1 ? m.cols : 1) || m.ld > kMaxPitch || m.stride < 0) return false;
   const int64_t one = gemm::matrix_extent(m.rows, m.cols, m.ld);
   if (one == 0 || m.count == 0) return true;
   if (one > kMaxSpan || (m.count > 1 && m.stride > kMaxSpan / (m.count - 1))) return false;
@@ -382,7 +382,7 @@ int gemm_f32_lora(int type, int transw, int transl, int64_t segments, int64_t ba
                   int64_t ldb, int64_t strideb, const int64_t *offsets, const int32_t *index,
                   const float *scales, void *U, int64_t ldu, void *Y, int64_t ldy, void *stream) {
   if (!common_ok(type, segments) || !op_ok(transw) || !op_ok(transl) || !dim_ok(M) || !dim_ok(N) ||
-      !dim_ok(K) || !dim_ok(R) || !dim_ok(bank))
+      !dim_ok(K) || !dim_ok(R) || bank < 0 || bank > kMaxPitch)
     return GEMM_ERR_INVALID_ARG;
   const int elem = type == GEMM_F32_TYPE_BF16 ? 2 : 4;
   Lora l;

@@ -1357,7 +1357,7 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
                          p.tiles_n;
   const long long least =
       (a.wgrad ? p.entries : 1) * ((height + kCols - 1) / kCols) * p.tiles_n;
-  if (most > 0x7fffffffLL) return kErrInvalidArg;
+  if (most > 0x7fff0000LL) return kErrInvalidArg;  // an item's number and the pairs, < 2^31
   int pairs = sm_count / 2;
   if (pairs < 1) pairs = 1;
   // Lines per copy of a K-major Q: about half a tile's rows, so that small

@@ -51,6 +51,9 @@ typedef enum {
 } gemm_f32_type;
 
 #define GEMM_F32_MAX_SEGMENTS 2048
+/* M, N, K and R at most: 2^31 - 2^26, so that sums of a size, a tile and the
+ * number of tiles stay below 2^31. */
+#define GEMM_F32_MAX_SEGMENT_SIZE 0x7c000000
 
 /*
  * gemm_f32_grouped -- C_g = A_g op(B_g) for every segment (expert) g: rows of A
@@ -65,7 +68,8 @@ typedef enum {
  *   C         rows of no segment are not written; must not overlap A, B or
  *             offsets (GEMM_ERR_ALIAS)
  * Pointers are device pointers aligned to their element (offsets to 8 bytes).
- * K == 0 sets the segments' rows to zero. Size limits as for gemm_f32.
+ * K == 0 sets the segments' rows to zero. Leading dimensions and spans as for
+ * gemm_f32; sizes up to GEMM_F32_MAX_SEGMENT_SIZE.
  */
 int gemm_f32_grouped(int type, int transb, int64_t groups, int64_t M, int64_t N, int64_t K,
                      const void *A, int64_t lda,
