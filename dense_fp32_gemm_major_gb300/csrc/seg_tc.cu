@@ -105,6 +105,10 @@ struct SegTc {
   float *slots;
   unsigned *arrived;  // [2 tile + rank] of the split tiles, zero
   long long slot_extent;
+  // > 0: so many rows and segments that offsets which claim rows again and again
+  // could make more tiles than 32 bits count: the tiles there are at most
+  // otherwise.
+  int most_tiles;
   int few;            // rows: segments of up to this many are another launch's
   int ahead;          // starts before the launch before it has ended (SegArgs::ahead)
   unsigned long long timeout_ns;
@@ -597,6 +601,21 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     tab.row[g] = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
   }
   __syncthreads();
+  if (p.most_tiles > 0) {
+    // Such offsets get no tiles (their rows' results are unspecified).
+    if (threadIdx.x == 0) {
+      long long sum = 0;
+      for (int g = 0; g < p.entries; ++g)
+        sum += static_cast<long long>(cdiv(rows_of(p, tab, g), kCols / 4)) * p.tiles_n;
+      sh->longest = sum > p.most_tiles ? -1 : 0;
+    }
+    __syncthreads();
+    const bool none = sh->longest < 0;
+    __syncthreads();
+    for (int g = threadIdx.x; none && g <= p.entries; g += C::kThreads) tab.row[g] = 0;
+    if (threadIdx.x == 0) sh->longest = 0;
+    __syncthreads();
+  }
   for (int g = threadIdx.x; g < p.entries; g += C::kThreads) {
     const int rows = rows_of(p, tab, g);
     const int height = p.form == kWgrad ? p.K : rows;
@@ -1358,6 +1377,8 @@ int seg_tc_launch(const SegArgs &a, int sm_count, cudaStream_t stream) {
   const long long least =
       (a.wgrad ? p.entries : 1) * ((height + kCols - 1) / kCols) * p.tiles_n;
   if (most > 0x7fff0000LL) return kErrInvalidArg;  // an item's number and the pairs, < 2^31
+  const long long claimed = p.entries * ((height + 63) / 64) * p.tiles_n;
+  p.most_tiles = !a.wgrad && claimed > 0x7fff0000LL ? static_cast<int>(most) : 0;
   int pairs = sm_count / 2;
   if (pairs < 1) pairs = 1;
   // Lines per copy of a K-major Q: about half a tile's rows, so that small

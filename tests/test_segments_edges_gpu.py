@@ -260,3 +260,28 @@ def test_infinite_shrink_of_bf16_stays_infinite(g, sizes, k, n):
         x[1] = 0
         y64, ty, _, _ = lora_64(x, w, a, b, o, range(2), one)
         check(y[keep], y64[keep], ty[keep])
+
+
+def test_more_claimed_tiles_than_32_bits_count(g):
+    # 2048 segments that could each claim all of 2^34 results: offsets in order
+    # give each row its own; offsets that claim all rows 1024 times write
+    # nothing outside the matrix and end
+    m, n, k, segments = 1 << 18, 1 << 16, 16, g.MAX_SEGMENTS
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GB")
+    dt = torch.bfloat16
+    a, b = normal((m, k), 40, dt), normal((1, k, n), 41, dt).expand(segments, k, n)
+    buf = torch.full((m + 2, n), 7.0, dtype=dt, device="cuda")
+    c = buf[1:-1]
+    sizes = [100 + i % 57 for i in range(segments)]
+    off, o = offsets_of(sizes, first=5)
+    g.grouped_matmul(a, b, off, out=c)
+    for i in (0, 1, 1000, segments - 1):
+        r = slice(o[i], o[i + 1])
+        c64, s64 = product(a[r], b[i])
+        check(c[r], c64, rounding(c64, s64, k, dt))
+    assert (buf[:6] == 7).all() and (c[o[-1]:o[-1] + 300] == 7).all() and (buf[-1] == 7).all()
+    again = torch.tensor([0, m] * (segments // 2) + [0], dtype=torch.int64, device="cuda")
+    g.grouped_matmul(a, b, again, out=c)
+    assert g.gemm_f32_poll_device_status(torch.cuda.current_stream().cuda_stream) == g.OK
+    assert (buf[0] == 7).all() and (buf[-1] == 7).all()
