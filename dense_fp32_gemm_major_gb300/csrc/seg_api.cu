@@ -96,8 +96,8 @@ class Workspace {
   }
 
   // Room for splitting the tiles of a product of this shape.
-  void splits(const SegArgs &a) {
-    if (gemm::seg_tc_splits(a) && !(gemm::seg_rows_fits(a) && gemm::seg_rows_few(a) == 0))
+  void splits(const SegArgs &a, int terms = 1) {
+    if (gemm::seg_tc_splits(a, terms) && !(gemm::seg_rows_fits(a) && gemm::seg_rows_few(a) == 0))
       split_ = true;
   }
 
@@ -499,6 +499,13 @@ int gemm_f32_lora_backward(int type, int transw, int transl, int64_t segments, i
     shape.wgrad = true;
     shape.M = M;
     work.splits(shape);
+    // dA's V has two terms in bf16: half the rows are as long. Asked of the
+    // segments' average, since zeroing the counters takes 5 us (1531 rows in one
+    // segment, 2048 x 1000, rank 24: 55.5 -> 52 us; in seven, 48 -> 53).
+    if (l.bf16 && l.adapted) {
+      shape.M = M / segments;
+      work.splits(shape, 2);
+    }
     l.prepare(work, sms);
     if (l.adapted) {
       work.readable(x);

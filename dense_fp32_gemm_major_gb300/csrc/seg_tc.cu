@@ -1321,9 +1321,9 @@ bool seg_tc_readable(const SegMatrix &m, bool bf16) {
          (m.count <= 1 || m.stride % per16 == 0);
 }
 
-bool seg_tc_splits(const SegArgs &a) {
+bool seg_tc_splits(const SegArgs &a, int terms) {
   const int64_t blocks = ((a.wgrad ? a.M : a.K) + kBlock - 1) / kBlock *
-                         (a.A_lo.p != nullptr || a.B_lo.p != nullptr ? 2 : 1);
+                         (a.A_lo.p != nullptr || a.B_lo.p != nullptr ? 2 : terms);
   return blocks >= (a.bf16 ? kSplitBlocksBf16 : kSplitBlocksF32);
 }
 

@@ -57,9 +57,10 @@ struct SegArgs {
   int few = 0;
 };
 
-// Whether a product's contraction is long enough to be worth splitting, and
-// the floats that its slots take.
-bool seg_tc_splits(const SegArgs &a);
+// Whether a product's contraction is long enough to be worth splitting (terms:
+// of its operands, before the second one's place is known), and the floats that
+// its slots take.
+bool seg_tc_splits(const SegArgs &a, int terms = 1);
 int64_t seg_tc_slots(int sm_count);
 
 // Whether the kernels can read a matrix as it lies (by TMA: 16-byte aligned

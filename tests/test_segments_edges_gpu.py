@@ -285,3 +285,46 @@ def test_more_claimed_tiles_than_32_bits_count(g):
     g.grouped_matmul(a, b, again, out=c)
     assert g.gemm_f32_poll_device_status(torch.cuda.current_stream().cuda_stream) == g.OK
     assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+
+
+def nodes_of(call):
+    """Names of the work that a call puts on its stream, captured and not run."""
+    import ctypes
+
+    cu = ctypes.CDLL("libcuda.so.1")
+    stream, graph, count = torch.cuda.Stream(), ctypes.c_void_p(), ctypes.c_size_t(0)
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        call()  # its results' memory is there when it is captured
+        stream.synchronize()
+        assert cu.cuStreamBeginCapture_v2(handle, 2) == 0
+        try:
+            call()
+        finally:
+            assert cu.cuStreamEndCapture(handle, ctypes.byref(graph)) == 0
+    assert cu.cuGraphGetNodes(graph, None, ctypes.byref(count)) == 0
+    nodes, kind = (ctypes.c_void_p * count.value)(), ctypes.c_int()
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(count)) == 0
+    names = []
+    for n in nodes:
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(n), ctypes.byref(kind)) == 0
+        names.append({0: "kernel", 2: "memset", 10: "alloc", 11: "free"}.get(kind.value, "other"))
+    assert cu.cuGraphDestroy(graph) == 0
+    return names
+
+
+@pytest.mark.parametrize("dt, rows, segments, split", [
+    (torch.bfloat16, 900, 1, 0), (torch.bfloat16, 1100, 1, 1), (torch.bfloat16, 1500, 7, 0),
+    (torch.bfloat16, 2100, 1, 1), (torch.float32, 400, 1, 0), (torch.float32, 600, 1, 1)], ids=str)
+@pytest.mark.parametrize("trans", [False, True])
+def test_gradient_of_two_terms_may_be_split_by_its_own_length(g, dt, rows, segments, split, trans):
+    # dA reads V in two bf16 terms: 32 blocks of 64 rows, from which on tiles may
+    # be split, are 1024 rows. The counters of split tiles are zeroed first.
+    k, n, r = 264, 136, 16
+    off, _ = offsets_of([rows // segments] * (segments - 1) + [rows - rows // segments * (segments - 1)])
+    x, dy, w = normal((rows, k), 23, dt), normal((rows, n), 24, dt), normal((k, n), 25, dt)
+    a = normal((segments, r, k) if trans else (segments, k, r), 26, dt)
+    b = normal((segments, n, r) if trans else (segments, r, n), 27, dt)
+    u = normal((rows, r), 28, dt)
+    names = nodes_of(lambda: g.lora_backward(dy, x, u, w, a, b, off, transl=trans))
+    assert names.count("memset") == split, names
