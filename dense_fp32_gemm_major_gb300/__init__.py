@@ -474,10 +474,18 @@ def _matrices(t, name, dim, kind, device):
     return shape, t.data_ptr(), ld, stride
 
 
-def _result(out, name, shape, like, kind, device):
-    """out, or a new tensor of the shape, and its (pointer, ld, stride)."""
+def _result(out, name, shape, like, kind, device, stream):
+    """out, or a new tensor of the shape in memory of the call's stream (on
+    another than torch's current one the call runs ahead of work that may still
+    read what the current one's memory held), and its (pointer, ld, stride)."""
     if out is None:
-        out = like.new_empty(shape)
+        import torch
+
+        if stream is None or stream == torch._C._cuda_getCurrentRawStream(device):
+            out = like.new_empty(shape)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+                out = like.new_empty(shape)
         return out, out.data_ptr(), shape[-1] or 1, (shape[1] * shape[2] if len(shape) == 3 else 0)
     got, ptr, ld, stride = _matrices(out, name, len(shape), kind, device)
     if tuple(got) != shape:
@@ -536,7 +544,12 @@ def grouped_matmul(a, b, offsets, transb=False, out=None, stream=None):
     ``transb`` (which also is the gradient of the inputs: ``grouped_matmul(dy,
     b, offsets, transb=True)``); ``offsets`` G + 1 int64 values on the device,
     never read by the host. ``out`` (M x N) is returned; rows of no segment are
-    not written. Stream ordered on ``stream`` (default: torch's current one).
+    not written. Stream ordered on ``stream`` (default: torch's current one); a
+    new result stands in that stream's memory (``record_stream`` before it is
+    dropped while another stream may still read it).
+
+    As of all functions here, results are no part of an autograd graph: the
+    gradients are calls of their own (above, and grouped_wgrad).
     """
     kind = _segment_type(a, "a")
     dev = a.get_device()
@@ -549,7 +562,7 @@ def grouped_matmul(a, b, offsets, transb=False, out=None, stream=None):
         raise ValueError(f"{count} matrices for {groups} segments")
     if k != k2:
         raise ValueError(f"inner dimensions differ: a is {m} x {k}, op(b) {k2} x {n}")
-    out, pc, ldc, _ = _result(out, "out", (m, n), a, kind, dev)
+    out, pc, ldc, _ = _result(out, "out", (m, n), a, kind, dev, stream)
     _call("gemm_f32_grouped", dev, stream, kind, OP_T if transb else OP_N, groups, m, n, k, pa, lda,
           pb, ldb, strideb, pc, ldc, po)
     return out
@@ -566,7 +579,7 @@ def grouped_wgrad(a, d, offsets, out=None, stream=None):
     groups, po = _offsets(offsets, dev)
     if m != m2:
         raise ValueError(f"a has {m} rows, d {m2}")
-    out, pc, ldc, stridec = _result(out, "out", (groups, k, n), a, kind, dev)
+    out, pc, ldc, stridec = _result(out, "out", (groups, k, n), a, kind, dev, stream)
     _call("gemm_f32_grouped_wgrad", dev, stream, kind, groups, m, n, k, pa, lda, pd, ldd, pc, ldc,
           stridec, po)
     return out
@@ -608,10 +621,10 @@ def lora_matmul(x, w, lora_a, lora_b, offsets, adapters=None, scales=None, trans
         raise ValueError(f"{segments} segments, {bank} adapters and no choice of adapters")
     pi = None if adapters is None else _array(adapters, "adapters", torch.int32, segments, dev)
     ps = None if scales is None else _array(scales, "scales", torch.float32, bank, dev)
-    out, py, ldy, _ = _result(out, "out", (m, n), x, kind, dev)
+    out, py, ldy, _ = _result(out, "out", (m, n), x, kind, dev, stream)
     pu, ldu = None, r or 1
     if shrink_out is not None:
-        _, pu, ldu, _ = _result(shrink_out, "shrink_out", (m, r), x, kind, dev)
+        _, pu, ldu, _ = _result(shrink_out, "shrink_out", (m, r), x, kind, dev, stream)
     _call("gemm_f32_lora", dev, stream, kind, OP_T if transw else OP_N, OP_T if transl else OP_N,
           segments, bank, m, n, k, r, px, ldx, pw, ldw, pa, lda, stridea, pb, ldb, strideb, po, pi,
           ps, pu, ldu, py, ldy)
@@ -643,9 +656,9 @@ def lora_backward(dy, x, shrink, w, lora_a, lora_b, offsets, scales=None, transw
         raise ValueError(f"w {tuple(wshape)}, lora_a {tuple(ashape)} and lora_b {tuple(bshape)} are "
                          f"not those of {segments} segments, a {k} x {n} projection and rank {r}")
     ps = None if scales is None else _array(scales, "scales", torch.float32, segments, dev)
-    dx, pdx, lddx, _ = _result(None, "dx", (m, k), dy, kind, dev)
-    da, pda, ldda, strideda = _result(None, "da", tuple(ashape), dy, kind, dev)
-    db, pdb, lddb, stridedb = _result(None, "db", tuple(bshape), dy, kind, dev)
+    dx, pdx, lddx, _ = _result(None, "dx", (m, k), dy, kind, dev, stream)
+    da, pda, ldda, strideda = _result(None, "da", tuple(ashape), dy, kind, dev, stream)
+    db, pdb, lddb, stridedb = _result(None, "db", tuple(bshape), dy, kind, dev, stream)
     _call("gemm_f32_lora_backward", dev, stream, kind, OP_T if transw else OP_N,
           OP_T if transl else OP_N, segments, m, n, k, r, pdy, lddy, px, ldx, pu, ldu, pw, ldw, pa,
           lda, stridea, pb, ldb, strideb, po, ps, pdx, lddx, pda, ldda, strideda, pdb, lddb,

@@ -328,3 +328,47 @@ def test_gradient_of_two_terms_may_be_split_by_its_own_length(g, dt, rows, segme
     u = normal((rows, r), 28, dt)
     names = nodes_of(lambda: g.lora_backward(dy, x, u, w, a, b, off, transl=trans))
     assert names.count("memset") == split, names
+
+
+@pytest.mark.parametrize("call", ["grouped_matmul", "grouped_wgrad", "lora_matmul", "lora_backward"])
+def test_results_of_a_call_on_another_stream_have_memory_of_its_own(g, call):
+    # `stream` runs ahead of torch's current one: a result must not stand in
+    # memory that work still queued on the current stream reads.
+    m, n, dt = 512, 512, torch.float32
+    x, w = normal((m, n), 29, dt), normal((1, n, n), 30, dt)
+    off, _ = offsets_of([m])
+    f = {"grouped_matmul": lambda **kw: g.grouped_matmul(x, w, off, **kw),
+         "grouped_wgrad": lambda **kw: g.grouped_wgrad(x, x, off, **kw),
+         "lora_matmul": lambda **kw: g.lora_matmul(x, w[0], w, w, off, **kw),
+         "lora_backward": lambda **kw: g.lora_backward(x, x, x, w[0], w, w, off, **kw)}[call]
+    want = f()
+    want = want if isinstance(want, tuple) else (want,)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        old = [torch.ones(m, n, device="cuda") for _ in range(6)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        kept = [t + 0 for t in old]  # read only then
+        del old
+        got = f(stream=side.cuda_stream)
+        torch.cuda.synchronize()
+        assert all((t == 1).all() for t in kept)
+        got = got if isinstance(got, tuple) else (got,)
+        assert all(torch.equal(c, ref) for c, ref in zip(got, want))
+        del got, kept
+
+
+def test_streams_by_their_handle(g):
+    # the legacy default stream (0) from another one, and the current one by name
+    x, w = normal((300, 128), 42, torch.bfloat16), normal((3, 128, 264), 43, torch.bfloat16)
+    off, _ = offsets_of([100, 0, 200])
+    want = g.grouped_matmul(x, w, off)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for s in (0, side.cuda_stream, torch.cuda.default_stream().cuda_stream):
+            c = g.grouped_matmul(x, w, off, stream=s)
+            torch.cuda.synchronize()
+            assert torch.equal(c, want)
+        assert torch.cuda.current_stream() == side
