@@ -446,13 +446,25 @@ __device__ __forceinline__ uint64_t line_desc(uint32_t base) {
   return smem_desc(base, 16, BK * 16, BK == 64 ? 2 : 4);
 }
 
-// Arrive on the barrier at the shared::cluster address (the even CTA's). What
-// it announces never crosses the pair: lines that the odd CTA's threads wrote to
-// its own shared memory, fenced for its own tensor core, or its own TMEM read
-// out. A release at CTA scope is therefore enough; one at cluster scope cost
-// 280 ns of every float32 stage (4096 x 4864 x 4096: 672 against 530 us).
-__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrivals on a barrier of the even CTA (its shared::cluster address), for a
+// thread of that CTA that waits with acquire at cluster scope.
+//
+// Of lines in shared memory, which both CTAs' tensor core reads: every thread
+// that wrote some has fenced them for the asynchronous proxy and met this one.
+// A release at cluster scope of shared memory alone: a full one also waits for
+// whatever else is under way and took 280 ns of every float32 stage (4096 rows,
+// 2048 x 2048 in 8 segments: 158 us with this one, 184 with that).
+__device__ __forceinline__ void mbar_arrive_filled(uint32_t bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+      : "memory");
+}
+
+// Of TMEM that has been read out: tcgen05's own fences, before this arrival and
+// behind the wait, order the loads before the next MMAs.
+__device__ __forceinline__ void mbar_arrive_drained(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Store the box at (x, y, z) of the map from shared memory, asynchronously.
@@ -780,7 +792,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(mbar_cluster_addr(&sh->full[r.idx], 0));
+            if (lane == 0) mbar_arrive_filled(mbar_cluster_addr(&sh->full[r.idx], 0));
           }
           r.next();
         }
@@ -876,7 +888,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
       tc_fence_before_sync();
       ok = named_barrier_and(1, 32 * C::kEpiWarps, ok);
       if (ok && threadIdx.x == 32 * C::kEpiWarp0)
-        mbar_arrive_at(mbar_cluster_addr(&sh->acc_empty[a], 0));
+        mbar_arrive_drained(mbar_cluster_addr(&sh->acc_empty[a], 0));
       return ok;
     };
     // Nothing is written, nor `add` read, before the previous grid has ended.
@@ -1171,7 +1183,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
             // Each warp comes here once a stage; false if one gave up.
             fence_proxy_async_smem();
             if (!named_barrier_and(2, 32 * C::kLoadWarps, ready)) return false;
-            if (threadIdx.x == 32 * C::kLoadWarp0) mbar_arrive_at(full0 + r.idx * 8);
+            if (threadIdx.x == 32 * C::kLoadWarp0) mbar_arrive_filled(full0 + r.idx * 8);
             if (lane == 0) mbar_arrive(&sh->raw_empty[a.idx]);
             a.next();
             r.next();

@@ -40,3 +40,24 @@ def test_what_a_device_keeps_is_not_set_once_a_process():
     assert seen >= 2  # the driver's entry points
     assert list(once_bodies("std::call_once(o, [&] { if (a) { b(); } c(); }); d();")) \
         == [" if (a) { b(); } c(); }"]
+
+
+def arrivals(text):
+    """(address space, qualifiers) of every mbarrier.arrive in the text's PTX."""
+    for m in re.finditer(r"mbarrier\.arrive((?:\.[a-z_]+)*)\.(shared::\w+)\.b64", text):
+        yield m.group(2), m.group(1).split(".")[1:]
+
+
+def test_arrivals_at_another_cta_have_its_scope():
+    # Without a scope an arrival is a release at CTA scope, which a thread of
+    # another CTA cannot acquire: what it announces would be unordered.
+    remote = 0
+    for name, text in sources():
+        for space, qualifiers in arrivals(text):
+            if space == "shared::cluster":
+                remote += 1
+                assert "cluster" in qualifiers, f"{name}: {qualifiers}"
+    assert remote >= 2
+    assert list(arrivals('"mbarrier.arrive.shared::cluster.b64 _, [%0];"')) == [("shared::cluster", [])]
+    assert list(arrivals("mbarrier.arrive.release.cluster.shared::cluster.b64")) == [
+        ("shared::cluster", ["release", "cluster"])]
