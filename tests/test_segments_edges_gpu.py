@@ -372,3 +372,87 @@ def test_streams_by_their_handle(g):
             torch.cuda.synchronize()
             assert torch.equal(c, want)
         assert torch.cuda.current_stream() == side
+
+
+@pytest.fixture
+def checked(g, checked_lib, monkeypatch):
+    """The wrappers on the checked build; its record is looked at in the end."""
+    monkeypatch.setattr(g, "_lib", checked_lib)
+    yield g
+    s = torch.cuda.current_stream().cuda_stream
+    status, count, site, at, extent = g.gemm_f32_take_index_fault(s, lib=checked_lib)
+    assert (status, count) == (g.OK, 0), (g.gemm_f32_index_site_name(site), at, extent)
+    assert checked_lib.gemm_f32_poll_device_status(s or None) == g.OK
+
+
+# Single tokens, over a cluster along k and not; routing shared by two launches;
+# few tiles of long sums (slots); whole tiles; each as it lies and at an odd pitch.
+CHECKED = [([1], 1100, 40), ([2, 0, 3], 1040, 520), ([1, 1, 6], 96, 2100), ([5], 20, 4200),
+           ([0] * 30 + [60] + [0] * 9 + [1] * 20, 1024, 2100), ([1, 9] * 8 + [0] * 50, 1030, 2050),
+           ([40], 8200, 72), ([300, 20], 4200, 264), ([256, 255, 257], 200, 512)]
+
+
+@pytest.mark.parametrize("sizes, k, n", CHECKED, ids=lambda v: str(v)[:24])
+@pytest.mark.parametrize("pad, lead", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_accesses_of_grouped_products(checked, sizes, k, n, pad, lead, trans, dt):
+    off, o = offsets_of(sizes, first=1)
+    a = normal((o[-1] + 2, k), 44, dt, pad, lead)
+    b = normal((len(sizes),) + ((n, k) if trans else (k, n)), 45, dt, pad, lead)
+    c = normal((o[-1] + 2, n), 46, dt, pad, lead)
+    checked.grouped_matmul(a, b, off, trans, out=c)
+    for i, s in enumerate(sizes):
+        if s:
+            c64, s64 = product(a[o[i]:o[i + 1]], b[i].t() if trans else b[i])
+            check(c[o[i]:o[i + 1]], c64, rounding(c64, s64, k, dt))
+
+
+@pytest.mark.parametrize("sizes, k, n", [([5000], 24, 17), ([2500, 0, 2100], 300, 520), ([3], 64, 40)],
+                         ids=lambda v: str(v))
+@pytest.mark.parametrize("pad, lead", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_accesses_of_weight_gradients(checked, sizes, k, n, pad, lead, dt):
+    off, o = offsets_of(sizes, first=1)
+    a, d = normal((o[-1] + 2, k), 47, dt, pad, lead), normal((o[-1] + 2, n), 48, dt, pad, lead)
+    c = checked.grouped_wgrad(a, d, off, out=normal((len(sizes), k, n), 49, dt, pad, lead))
+    for i, s in enumerate(sizes):
+        c64, s64 = product(a[o[i]:o[i + 1]].t(), d[o[i]:o[i + 1]])
+        check(c[i], c64, rounding(c64, s64, s, dt))
+
+
+# Tokens (addend of U B among plain FMAs); few rows a segment; the fused form;
+# long sums; few rows of many segments, one of which has most.
+ADAPTERS = [([1], 1100, 520, 16), ([3, 0, 4], 640, 1100, 24), ([40, 30], 72, 137, 20),
+            ([300, 200, 157, 300], 136, 264, 24), ([1500, 700, 0, 1900], 200, 2560, 40),
+            ([90, 60], 4200, 300, 130), ([150] + [1] * 99, 1030, 2600, 70)]
+
+
+@pytest.mark.parametrize("sizes, k, n, r", ADAPTERS, ids=lambda v: str(v)[:24])
+@pytest.mark.parametrize("pad, lead", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_accesses_of_adapters(checked, sizes, k, n, r, pad, lead, trans, dt):
+    m, bank = sum(sizes) + 3, len(sizes)
+    off, o = offsets_of(sizes, first=2)
+    x, dy = normal((m, k), 50, dt, pad, lead), normal((m, n), 51, dt, pad, lead)
+    w = normal((n, k) if trans else (k, n), 52, dt, pad, lead)
+    a = normal((bank, r, k) if trans else (bank, k, r), 53, dt, pad, lead)
+    b = normal((bank, n, r) if trans else (bank, r, n), 54, dt, pad, lead)
+    scales = torch.rand(bank, device="cuda") + 0.5
+    u, y = normal((m, r), 55, dt, pad, lead), normal((m, n), 56, dt, pad, lead)
+    checked.lora_matmul(x, w, a, b, off, None, scales, trans, trans, out=y, shrink_out=u)
+    at, bt = [t.t() if trans else t for t in a], [t.t() if trans else t for t in b]
+    y64, ty, _, _ = lora_64(x, w.t() if trans else w, at, bt, o, range(bank), scales)
+    check(y, y64, ty, "y")
+    dx, da, db = checked.lora_backward(dy, x, u, w, a, b, off, scales, trans, trans)
+    x64, tx, v64, tv = lora_64(dy, w if trans else w.t(), [t.t() for t in bt], [t.t() for t in at], o,
+                               range(bank), scales)
+    check(dx, x64, tx, "dx")
+    for i in range(min(bank, 4)):
+        s = slice(o[i], o[i + 1])
+        da64, sa = product(x[s].t(), v64[s])
+        ta = rounding(da64, sa, sizes[i], dt) + x[s].double().abs().t() @ tv[s]
+        check(da[i].t() if trans else da[i], da64, ta, "da")
+        db64, sb = product(u[s].t(), dy[s])
+        check(db[i].t() if trans else db[i], db64, rounding(db64, sb, sizes[i], dt), "db")
