@@ -596,8 +596,9 @@ def lora_matmul(x, w, lora_a, lora_b, offsets, adapters=None, scales=None, trans
     ``offsets`` segments + 1 int64 values, ``adapters`` int32, one for each
     segment (a value outside the bank: no adapter; None: adapter g for segment
     g), ``scales`` float32, one for each adapter (None: 1), all on the device.
-    ``shrink_out`` (M x R), if given, receives u for lora_backward. Returns
-    ``out`` (M x N).
+    ``shrink_out`` (M x R, of x's type, u rounded to it), if given, receives u
+    for lora_backward. Returns ``out`` (M x N). Factors may be shared: an
+    expanded ``lora_a`` or ``lora_b``.
     """
     import torch
 
@@ -635,7 +636,9 @@ def lora_backward(dy, x, shrink, w, lora_a, lora_b, offsets, scales=None, transw
                   transl=False, stream=None):
     """Gradients of lora_matmul with one adapter for each segment (adapters
     None; rows sorted by adapter) on a frozen ``w``: (dx, d lora_a, d lora_b).
-    ``shrink`` is the forward's shrink_out. Factors of empty segments get zero.
+    ``shrink`` is the forward's shrink_out: for bfloat16, d lora_b is that of u
+    as it was rounded. Factors of empty segments get zero; of factors shared by
+    several segments (expanded) each segment's gradient is returned.
     """
     import torch
 
