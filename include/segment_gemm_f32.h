@@ -11,8 +11,9 @@
  * can be passed on without a synchronisation. Segments may be empty; rows
  * before offsets[0] and from offsets[segments] on belong to none. Values
  * outside [0, M] are held to it and a decreasing one makes its segment empty,
- * so that no access leaves the matrices (where two segments claim a row, the
- * results of the call are unspecified). At most GEMM_F32_MAX_SEGMENTS segments a call.
+ * so that no access leaves the matrices. Where two segments claim a row, or
+ * offsets decrease in a call with adapters, results are unspecified. At most
+ * GEMM_F32_MAX_SEGMENTS segments a call.
  *
  * Types. `type` is that of every matrix of the call (a gemm_f32_type). The
  * "f32" of the names is the type of the sums: products are exact to fp32 or

@@ -456,3 +456,26 @@ def test_accesses_of_adapters(checked, sizes, k, n, r, pad, lead, trans, dt):
         check(da[i].t() if trans else da[i], da64, ta, "da")
         db64, sb = product(u[s].t(), dy[s])
         check(db[i].t() if trans else db[i], db64, rounding(db64, sb, sizes[i], dt), "db")
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_without_rows_or_contractions(g, dt):
+    # no rows: gradients are zero; no contraction: the adapter's half is all, and U is zero
+    off = torch.zeros(4, dtype=torch.int64, device="cuda")
+    new = lambda *shape: torch.full(shape, 3.0, dtype=dt, device="cuda")
+    assert g.grouped_matmul(new(0, 64), new(3, 64, 40), off).shape == (0, 40)
+    assert (g.grouped_wgrad(new(0, 64), new(0, 40), off) == 0).all()
+    assert g.lora_matmul(new(0, 64), new(64, 40), new(3, 64, 8), new(3, 8, 40), off).shape == (0, 40)
+    dx, da, db = g.lora_backward(new(0, 40), new(0, 64), new(0, 8), new(64, 40), new(3, 64, 8),
+                                 new(3, 8, 40), off)
+    assert dx.shape == (0, 64) and (da == 0).all() and (db == 0).all()
+    assert da.shape == (3, 64, 8) and db.shape == (3, 8, 40)
+    for rows in (3, 70, 600):
+        off, _ = offsets_of([rows])
+        u = new(rows, 8)
+        y = g.lora_matmul(new(rows, 0), new(0, 40), new(1, 0, 8), new(1, 8, 40), off, shrink_out=u)
+        assert (y == 0).all() and (u == 0).all()
+        # no columns of dY: dX and dA are zero, dB is empty
+        dx, da, db = g.lora_backward(new(rows, 0), new(rows, 64), new(rows, 8), new(64, 0),
+                                     new(1, 64, 8), new(1, 8, 0), off)
+        assert (dx == 0).all() and (da == 0).all() and db.shape == (1, 8, 0)
