@@ -53,7 +53,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "seg_ptx.cuh"
 #include "seg_terms.cuh"
 #include "segments.h"
 

@@ -61,3 +61,13 @@ def test_arrivals_at_another_cta_have_its_scope():
     assert list(arrivals('"mbarrier.arrive.shared::cluster.b64 _, [%0];"')) == [("shared::cluster", [])]
     assert list(arrivals("mbarrier.arrive.release.cluster.shared::cluster.b64")) == [
         ("shared::cluster", ["release", "cluster"])]
+
+
+def test_the_dense_kernels_recorded_traffic_is_of_their_sources():
+    # DRAM bytes are on record by the hash of a kernel's sources: what only the
+    # segmented products need is no part of them
+    import bench
+
+    for kernel, mode in (("tc_pair_tma_3xtf32", "exact"), ("tc_pair_tma_tf32", "tf32"),
+                         ("simt_gemm", "exact_simt")):
+        assert bench.traffic_lookup(kernel, "c4", mode)[0] is not None, kernel
