@@ -194,6 +194,11 @@ __device__ __forceinline__ int quotient(int a, int b) {
   return q - (q * b > a) + ((q + 1) * b <= a);
 }
 
+// An offset, held to the rows there are.
+__device__ __forceinline__ int held(long long offset, int rows) {
+  return static_cast<int>(offset < 0 ? 0 : (offset > rows ? rows : offset));
+}
+
 // Rows of an entry, none where they are another launch's.
 __device__ __forceinline__ int rows_of(const SegTc &p, const Table &tab, int g) {
   const int rows = tab.row[g + 1] - tab.row[g];
@@ -559,7 +564,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     // Nothing to do where all segments are the launch before's, behind whose
     // end this one ends (for the launches that count on that).
     int any = 0;
-    for (int g = threadIdx.x; g < p.groups; g += C::kThreads) any |= p.offsets[g + 1] - p.offsets[g] > p.few;
+    for (int g = threadIdx.x; g < p.groups; g += C::kThreads)
+      any |= held(p.offsets[g + 1], p.M) - held(p.offsets[g], p.M) > p.few;
     if (!__syncthreads_or(any)) {
       grid_dependency_wait();
       return;
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
       a = g == 0 ? 0 : (g == p.entries ? p.M : p.offsets[g - 1]);
     else
       a = p.offsets[g];
-    tab.row[g] = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
+    tab.row[g] = held(a, p.M);
   }
   __syncthreads();
   if (p.most_tiles > 0) {
@@ -877,9 +883,8 @@ __global__ void __launch_bounds__(Cfg<T>::kThreads, 1)
     Ring<2> acc;
     int add0 = 0, add1 = 0;  // rows with an addend
     if (p.add != nullptr) {
-      const long long a = p.offsets[0], b = p.offsets[p.groups];
-      add0 = static_cast<int>(a < 0 ? 0 : (a > p.M ? p.M : a));
-      add1 = static_cast<int>(b < 0 ? 0 : (b > p.M ? p.M : b));
+      add0 = held(p.offsets[0], p.M);
+      add1 = held(p.offsets[p.groups], p.M);
     }
     // The accumulator can be refilled: one arrival for all the CTA's epilogue
     // warps. False if one of them gave up on its wait; every warp comes here

@@ -479,3 +479,19 @@ def test_without_rows_or_contractions(g, dt):
         dx, da, db = g.lora_backward(new(rows, 0), new(rows, 64), new(rows, 8), new(64, 0),
                                      new(1, 64, 8), new(1, 8, 0), off)
         assert (dx == 0).all() and (da == 0).all() and db.shape == (1, 8, 0)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_offsets_at_the_ends_of_their_type(g, dt):
+    # held to the rows there are, by both launches of a product that is shared
+    m, groups, k, n = 512, 256, 128, 2560
+    a, b = normal((m, k), 60, dt), normal((1, k, n), 61, dt).expand(groups, k, n)
+    off = torch.full((groups + 1,), -(1 << 63), dtype=torch.int64, device="cuda")
+    off[groups // 2:] = (1 << 63) - 1
+    c64, s64 = product(a, b[0])
+    check(g.grouped_matmul(a, b, off), c64, rounding(c64, s64, k, dt))
+    off[groups // 2:] = 300
+    c = torch.full((m, n), 7.0, dtype=dt, device="cuda")
+    g.grouped_matmul(a, b, off, out=c)
+    check(c[:300], c64[:300], rounding(c64, s64, k, dt)[:300])
+    assert (c[300:] == 7).all()
