@@ -300,7 +300,7 @@ def _own(s):
         return (*r, g.route_backward(s["dweights"], s["logits"], r.experts, r.weights, score=s["score"],
                                      renormalise=s["renormalise"], scale=s["scale"]))
     if s["op"].startswith("rows"):
-        rows = g.dispatch(s["x"], s["order"], s["k"])
+        rows = g.dispatch(s["x"], s["places"])
         back = g.combine(s["y"], s["places"], s["weights"])
         if s["op"] == "rows":
             return {"rows": rows, "back": back}
