@@ -12,7 +12,12 @@ values as integers, 0 = the legacy default stream). ``matmul`` and ``gemm``
 are convenience wrappers over ``gemm_f32_ex`` and ``gemm_f32_general`` for
 torch CUDA tensors; ``grouped_matmul``, ``grouped_wgrad``, ``lora_matmul`` and
 ``lora_backward`` those of the products over segments of rows
-(include/segment_gemm_f32.h), for float32 and bfloat16 tensors.
+(include/segment_gemm_f32.h), for float32 and bfloat16 tensors. Around those:
+the router ``route``, ``route_backward`` and ``route_plan``, the rows' way to the
+experts and back ``dispatch``, ``combine`` and ``combine_backward``
+(include/route_f32.h), products with 4-bit weights ``w4_matmul``
+(include/w4_gemm_f32.h), and the gradients' ``grad_norm`` and ``clip_grads``
+(include/reduce_f32.h).
 
 ``checked_library()`` loads libgemm_f32_checked.so, the same library built
 with device-side index checks (see include/gemm_f32.h, "The checked build");
@@ -21,6 +26,7 @@ its handle has the same functions, and the wrappers below take it as ``lib``.
 
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import re
@@ -31,7 +37,9 @@ LIB_CHECKED_PATH = os.path.join(_PKG, "libgemm_f32_checked.so")
 INCLUDE_DIR = os.path.join(os.path.dirname(_PKG), "include")
 HEADER_PATH = os.path.join(INCLUDE_DIR, "gemm_f32.h")
 HEADERS = [HEADER_PATH, os.path.join(INCLUDE_DIR, "reduce_f32.h"),
-           os.path.join(INCLUDE_DIR, "segment_gemm_f32.h")]
+           os.path.join(INCLUDE_DIR, "segment_gemm_f32.h"),
+           os.path.join(INCLUDE_DIR, "route_f32.h"),
+           os.path.join(INCLUDE_DIR, "w4_gemm_f32.h")]
 
 # gemm_f32_mode
 EXACT, TF32, EXACT_SIMT = 0, 1, 2
@@ -53,6 +61,9 @@ OP_N, OP_T = 0, 1
 # gemm_f32_type
 TYPE_F32, TYPE_BF16 = 0, 1
 MAX_SEGMENTS, MAX_SEGMENT_SIZE = 2048, 0x7c000000
+# gemm_f32_score
+SCORES = {"softmax": 0, "sigmoid": 1}
+MAX_ROUTE_SLOTS = 32
 
 
 class GemmError(RuntimeError):
@@ -100,6 +111,27 @@ def _open(path):
                                            + [p, i64, i64] * 2 + [p, p, p, i64]
                                            + [p, i64, i64] * 2 + [p])
     lib.gemm_f32_lora_backward.restype = i32
+    lib.gemm_f32_route.argtypes = ([i32, i32, i64, i64, i64, p, i64, p, p, i64, i64, i64, i32, f32]
+                                   + [p] * 6)
+    lib.gemm_f32_route.restype = i32
+    lib.gemm_f32_route_backward.argtypes = [i32, i32, i64, i64, i64, p, p, i64, p, p, i32, f32, p,
+                                            i64, p]
+    lib.gemm_f32_route_backward.restype = i32
+    lib.gemm_f32_route_plan.argtypes = [i64, i64, p, p, p, p, p]
+    lib.gemm_f32_route_plan.restype = i32
+    lib.gemm_f32_dispatch.argtypes = [i32, i64, i64, i64, i64, p, i64, p, p, i64, p]
+    lib.gemm_f32_dispatch.restype = i32
+    lib.gemm_f32_combine.argtypes = [i32, i64, i64, i64, i64, p, i64, p, p, p, i64, p]
+    lib.gemm_f32_combine.restype = i32
+    lib.gemm_f32_combine_backward.argtypes = [i32, i64, i64, i64, i64, p, i64, p, i64, p, p, p, i64,
+                                              p, p]
+    lib.gemm_f32_combine_backward.restype = i32
+    lib.gemm_f32_w4.argtypes = [i32] + [i64] * 5 + [p, i64] + [p, i64, i64] * 3 + [p, i64, p, p]
+    lib.gemm_f32_w4.restype = i32
+    lib.reduce_f32_norm.argtypes = [i64, p, p, p, p, p]
+    lib.reduce_f32_norm.restype = i32
+    lib.reduce_f32_clip.argtypes = [i64, p, p, p, p, f32, p, p]
+    lib.reduce_f32_clip.restype = i32
     lib.gemm_f32_status_string.argtypes = [i32]
     lib.gemm_f32_status_string.restype = ctypes.c_char_p
     lib.gemm_f32_measure_peaks.argtypes = [ctypes.POINTER(ctypes.c_double)] * 4
@@ -233,6 +265,66 @@ def gemm_f32_lora_backward(type, transw, transl, segments, M, N, K, R, dY, lddy,
                                           ldx, U, ldu, W, ldw, A, lda, stridea, B, ldb, strideb,
                                           offsets, scales or None, dX, lddx, dA, ldda, strideda, dB,
                                           lddb, stridedb, stream or None)
+
+
+def gemm_f32_route(type, score, T, E, k, logits, ldx, bias, mask, groups, top_groups, group_best,
+                   renormalise, scale, experts, weights, offsets, order, places, stream=0) -> int:
+    """The k best experts of every token, their weights, and the plan (see
+    include/route_f32.h)."""
+    return _load().gemm_f32_route(type, score, T, E, k, logits, ldx, bias or None, mask or None,
+                                  groups, top_groups, group_best, renormalise, scale, experts,
+                                  weights, offsets or None, order or None, places or None,
+                                  stream or None)
+
+
+def gemm_f32_route_backward(type, score, T, E, k, dweights, logits, ldx, experts, weights,
+                            renormalise, scale, dlogits, lddx, stream=0) -> int:
+    """Gradient of the logits (see include/route_f32.h)."""
+    return _load().gemm_f32_route_backward(type, score, T, E, k, dweights, logits, ldx, experts,
+                                           weights, renormalise, scale, dlogits, lddx, stream or None)
+
+
+def gemm_f32_route_plan(slots, E, experts, offsets, order, places, stream=0) -> int:
+    """The plan of given experts (see include/route_f32.h)."""
+    return _load().gemm_f32_route_plan(slots, E, experts, offsets, order, places, stream or None)
+
+
+def gemm_f32_dispatch(type, T, D, k, rows, X, ldx, places, Y, ldy, stream=0) -> int:
+    """Each token's row to all of its places (see include/route_f32.h)."""
+    return _load().gemm_f32_dispatch(type, T, D, k, rows, X, ldx, places, Y, ldy, stream or None)
+
+
+def gemm_f32_combine(type, T, D, k, rows, Y, ldy, places, weights, O, ldo, stream=0) -> int:
+    """The weighted sum of each token's rows (see include/route_f32.h)."""
+    return _load().gemm_f32_combine(type, T, D, k, rows, Y, ldy, places, weights or None, O, ldo,
+                                    stream or None)
+
+
+def gemm_f32_combine_backward(type, T, D, k, rows, dO, lddo, Y, ldy, places, weights, dY, lddy,
+                              dweights, stream=0) -> int:
+    """Gradients of gemm_f32_combine (see include/route_f32.h)."""
+    return _load().gemm_f32_combine_backward(type, T, D, k, rows, dO, lddo, Y, ldy, places,
+                                             weights or None, dY or None, lddy, dweights or None,
+                                             stream or None)
+
+
+def gemm_f32_w4(type, groups, M, N, K, group, A, lda, Q, ldq, strideq, scales, lds, strides, zeros,
+                ldz, stridez, C, ldc, offsets, stream=0) -> int:
+    """C = A W^T with weights in 4 bits (see include/w4_gemm_f32.h)."""
+    return _load().gemm_f32_w4(type, groups, M, N, K, group, A, lda, Q, ldq, strideq, scales, lds,
+                               strides, zeros or None, ldz, stridez, C, ldc, offsets or None,
+                               stream or None)
+
+
+def reduce_f32_norm(count, x, n, type, norm, stream=0) -> int:
+    """The norm of many tensors together; x, n, type: ctypes arrays (see
+    include/reduce_f32.h)."""
+    return _load().reduce_f32_norm(count, x, n, type, norm, stream or None)
+
+
+def reduce_f32_clip(count, x, y, n, type, limit, norm, stream=0) -> int:
+    """Tensors clipped by their norm (see include/reduce_f32.h)."""
+    return _load().reduce_f32_clip(count, x, y, n, type, limit, norm, stream or None)
 
 
 def gemm_f32_status_string(status: int) -> str:
@@ -667,6 +759,324 @@ def lora_backward(dy, x, shrink, w, lora_a, lora_b, offsets, scales=None, transw
           lda, stridea, pb, ldb, strideb, po, ps, pdx, lddx, pda, ldda, strideda, pdb, lddb,
           stridedb)
     return dx, da, db
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor in memory of the call's stream."""
+    import torch
+
+    if stream is None or stream == torch._C._cuda_getCurrentRawStream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _dense(t, name, dtype, shape, device):
+    """The pointer of a contiguous tensor of the type, shape and device."""
+    import torch
+
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda
+            or t.get_device() != device or tuple(t.shape) != shape or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on the "
+                        "operands' device")
+    return t.data_ptr()
+
+
+def _slots(t, name, device):
+    """(T, k, pointer) of a contiguous T x k int32 tensor."""
+    import torch
+
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2
+            or not t.is_cuda or t.get_device() != device or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous 2-D int32 tensor on the operands' device")
+    count, k = t.shape
+    if not 1 <= k <= MAX_ROUTE_SLOTS:
+        raise ValueError(f"{name} has {k} slots a token: 1 to {MAX_ROUTE_SLOTS}")
+    return count, k, t.data_ptr()
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, not {score!r}")
+    return SCORES[score]
+
+
+Routing = collections.namedtuple("Routing", "experts weights offsets order places")
+
+
+def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_best=2,
+          renormalise=True, scale=1.0, mask=None, stream=None):
+    """The router of a mixture of experts: the ``k`` experts of every token with
+    the largest score + bias, their weights, and the plan that sorts the tokens'
+    slots by expert, as a ``Routing``:
+
+      experts   T x k int32, best first, ties to the lowest index; -1: none
+      weights   T x k float32: scale * score, with ``renormalise`` over the sum of
+                the token's scores; 0 where there is no expert
+      offsets   E + 1 int64, as the products over segments take them
+      order     T k int32: the slot t k + j of each sorted row; -1 behind the last
+      places    T x k int32: the row of each slot, or -1
+
+    ``logits`` is T x E, float32 or bfloat16; ``score`` "softmax" or "sigmoid";
+    ``bias`` E float32, for the choice alone. ``groups`` > 1: the experts are that
+    many groups of neighbours, and the ``top_groups`` (None: all) groups with the
+    largest sum of their ``group_best`` (1 or 2) best are chosen from. ``mask``, T
+    bool: tokens with False take no part. Logits or biases of -infinity make an
+    expert unavailable. Scores are compared as real numbers are (see
+    include/route_f32.h). Nothing is read by the host.
+    """
+    import torch
+
+    kind = _segment_type(logits, "logits")
+    dev = logits.get_device()
+    (t, e), px, ldx, _ = _matrices(logits, "logits", 2, kind, dev)
+    if not 1 <= e <= MAX_SEGMENTS:
+        raise ValueError(f"{e} experts: 1 to {MAX_SEGMENTS}")
+    if not 1 <= k <= min(e, MAX_ROUTE_SLOTS):
+        raise ValueError(f"{k} slots a token: 1 to {MAX_ROUTE_SLOTS}, and to the {e} experts")
+    if top_groups is None:
+        top_groups = groups
+    if not 1 <= groups <= 32 or e % groups or not 1 <= top_groups <= groups or group_best not in (1, 2):
+        raise ValueError(f"{e} experts in {groups} groups, {top_groups} chosen by their best "
+                         f"{group_best}: up to 32 equal groups, by one or two")
+    pb = None if bias is None else _dense(bias, "bias", torch.float32, (e,), dev)
+    pm = None if mask is None else _dense(mask, "mask", torch.bool, (t,), dev)
+    ints = _empty((3, t, k), torch.int32, dev, stream)
+    experts, order, places = ints.unbind(0)
+    weights = _empty((t, k), torch.float32, dev, stream)
+    offsets = _empty((e + 1,), torch.int64, dev, stream)
+    at, step = ints.data_ptr(), 4 * t * k
+    _call("gemm_f32_route", dev, stream, kind, _score(score), t, e, k, px, ldx, pb, pm, groups,
+          top_groups, group_best, 1 if renormalise else 0, float(scale), at, weights.data_ptr(),
+          offsets.data_ptr(), at + step, at + 2 * step)
+    return Routing(experts, weights, offsets, order.view(t * k), places)
+
+
+def route_backward(dweights, logits, experts, weights, score="softmax", renormalise=True, scale=1.0,
+                   out=None, stream=None):
+    """Gradient of ``route``'s logits from that of its weights, ``dweights`` (T x
+    k float32), the choice held fixed. ``experts`` and ``weights`` are the
+    forward's; ``score``, ``renormalise`` and ``scale`` as there. Returns T x E of
+    the logits' type."""
+    import torch
+
+    kind = _segment_type(logits, "logits")
+    dev = logits.get_device()
+    (t, e), px, ldx, _ = _matrices(logits, "logits", 2, kind, dev)
+    t2, k, pe = _slots(experts, "experts", dev)
+    if t2 != t:
+        raise ValueError(f"logits has {t} tokens, experts {t2}")
+    if not 1 <= e <= MAX_SEGMENTS:
+        raise ValueError(f"{e} experts: 1 to {MAX_SEGMENTS}")
+    pw = _dense(weights, "weights", torch.float32, (t, k), dev)
+    pg = _dense(dweights, "dweights", torch.float32, (t, k), dev)
+    out, po, ldo, _ = _result(out, "out", (t, e), logits, kind, dev, stream)
+    _call("gemm_f32_route_backward", dev, stream, kind, _score(score), t, e, k, pg, px, ldx, pe, pw,
+          1 if renormalise else 0, float(scale), po, ldo)
+    return out
+
+
+def route_plan(experts, count, stream=None):
+    """The plan of experts that were chosen otherwise: (offsets, order, places) as
+    ``route`` returns them, for ``experts``, T x k int32 (any value outside [0,
+    count): none)."""
+    import torch
+
+    if not isinstance(experts, torch.Tensor) or not experts.is_cuda:
+        raise TypeError("experts must be a contiguous 2-D int32 CUDA tensor")
+    dev = experts.get_device()
+    t, k, pe = _slots(experts, "experts", dev)
+    if not 1 <= count <= MAX_SEGMENTS:
+        raise ValueError(f"{count} experts: 1 to {MAX_SEGMENTS}")
+    offsets = _empty((count + 1,), torch.int64, dev, stream)
+    order = _empty((t * k,), torch.int32, dev, stream)
+    places = _empty((t, k), torch.int32, dev, stream)
+    _call("gemm_f32_route_plan", dev, stream, t * k, count, pe, offsets.data_ptr(),
+          order.data_ptr(), places.data_ptr())
+    return offsets, order, places
+
+
+def dispatch(x, places, out=None, stream=None):
+    """Each token's row to all of its places: out[places[t, j]] = x[t]. ``x`` is T
+    x D, float32 or bfloat16, ``places`` T x k int32 (``route``'s; outside out's
+    rows: none). ``out`` is T k x D where it is not given; rows that no place names
+    are not written. Its gradient is ``combine`` without weights."""
+    kind = _segment_type(x, "x")
+    dev = x.get_device()
+    (t, d), px, ldx, _ = _matrices(x, "x", 2, kind, dev)
+    t2, k, pp = _slots(places, "places", dev)
+    if t2 != t:
+        raise ValueError(f"x has {t} tokens, places {t2}")
+    if out is None:
+        shape = (t * k, d)
+    elif getattr(out, "dim", lambda: 0)() == 2:
+        shape = (out.shape[0], d)
+    else:
+        raise TypeError("out must be a 2-D tensor")
+    out, po, ldo, _ = _result(out, "out", shape, x, kind, dev, stream)
+    _call("gemm_f32_dispatch", dev, stream, kind, t, d, k, shape[0], px, ldx, pp, po, ldo)
+    return out
+
+
+def combine(y, places, weights=None, out=None, stream=None):
+    """The weighted sum of each token's rows: out[t] = sum_j weights[t, j] *
+    y[places[t, j]], in fp32, rounded once; zero where a token has no place.
+    ``y`` is rows x D, float32 or bfloat16, ``places`` T x k int32, ``weights`` T x
+    k float32 (None: 1, which is the gradient of ``dispatch``)."""
+    import torch
+
+    kind = _segment_type(y, "y")
+    dev = y.get_device()
+    (rows, d), py, ldy, _ = _matrices(y, "y", 2, kind, dev)
+    t, k, pp = _slots(places, "places", dev)
+    pw = None if weights is None else _dense(weights, "weights", torch.float32, (t, k), dev)
+    out, po, ldo, _ = _result(out, "out", (t, d), y, kind, dev, stream)
+    _call("gemm_f32_combine", dev, stream, kind, t, d, k, rows, py, ldy, pp, pw, po, ldo)
+    return out
+
+
+def combine_backward(dout, y, places, weights=None, out=None, stream=None):
+    """Gradients of ``combine``: (dy, dweights), dy[places[t, j]] = weights[t, j] *
+    dout[t] (``out`` where it is given; rows that no place names are not written)
+    and dweights[t, j] = dout[t] . y[places[t, j]], float32, 0 without a place."""
+    import torch
+
+    kind = _segment_type(dout, "dout")
+    dev = dout.get_device()
+    (t, d), pd, ldd, _ = _matrices(dout, "dout", 2, kind, dev)
+    (rows, d2), py, ldy, _ = _matrices(y, "y", 2, kind, dev)
+    t2, k, pp = _slots(places, "places", dev)
+    if t2 != t or d2 != d:
+        raise ValueError(f"dout is {t} x {d}, places has {t2} tokens and y {d2} columns")
+    pw = None if weights is None else _dense(weights, "weights", torch.float32, (t, k), dev)
+    out, po, ldo, _ = _result(out, "out", (rows, d), y, kind, dev, stream)
+    dweights = _empty((t, k), torch.float32, dev, stream)
+    _call("gemm_f32_combine_backward", dev, stream, kind, t, d, k, rows, pd, ldd, py, ldy, pp, pw,
+          po, ldo, dweights.data_ptr())
+    return out, dweights
+
+
+def _w4_matrices(t, name, dtype, dim, device):
+    """As _matrices, of a type of its own."""
+    if t.dtype is not dtype or not t.is_cuda or t.get_device() != device:
+        raise TypeError(f"{name} must be a {dtype} tensor on x's device")
+    if t.dim() != dim:
+        raise TypeError(f"{name} must have {dim} dimensions, not {t.dim()}")
+    ld, stride = _addressing(t.shape, t.stride(), name)
+    return t.shape, t.data_ptr(), ld, stride
+
+
+def w4_matmul(x, q, scales, group, zeros=None, offsets=None, out=None, stream=None):
+    """Products with weights in 4 bits: out = x @ w.T, w[n, k] = scales[n, k //
+    group] * (q[n, k] - zeros[n, k // group]).
+
+    ``x`` is M x K, float32 or bfloat16. ``q`` is N x ceil(K / 2) uint8, two
+    neighbouring k a byte, the even one in the low four bits; ``scales`` N x
+    ceil(K / group) of x's type; ``zeros`` the same shape, uint8, of which the low
+    four bits count (None: 8). ``group`` is a multiple of 32. With ``offsets``
+    (segments + 1 int64 on the device) all three are stacks of a matrix for each
+    segment of rows, as for ``grouped_matmul``. Few rows (single tokens, decoding
+    steps) take the time of reading ``q``; rows of ``q`` should start on 16 bytes,
+    others are copied first. Returns ``out`` (M x N).
+    """
+    import torch
+
+    kind = _segment_type(x, "x")
+    dev = x.get_device()
+    (m, k), px, ldx, _ = _matrices(x, "x", 2, kind, dev)
+    dim, groups, po = 2, 1, None
+    if offsets is not None:
+        dim = 3
+        groups, po = _offsets(offsets, dev)
+    for t, name in ((q, "q"), (scales, "scales"), (zeros, "zeros")):
+        if not isinstance(t, torch.Tensor) and not (t is None and name == "zeros"):
+            raise TypeError(f"{name} must be a tensor")
+    qs, pq, ldq, strideq = _w4_matrices(q, "q", torch.uint8, dim, dev)
+    ss, ps, lds, strides = _matrices(scales, "scales", dim, kind, dev)
+    if group < 32 or group % 32:
+        raise ValueError(f"groups of {group}: a multiple of 32")
+    n = qs[-2]
+    stack = (groups,) if dim == 3 else ()
+    row = stack + (n, -(-k // group))
+    if tuple(qs) != stack + (n, (k + 1) // 2) or tuple(ss) != row:
+        raise ValueError(f"q {tuple(qs)} and scales {tuple(ss)} are not those of {groups} matrices of "
+                         f"{n} rows of {k} values in groups of {group}")
+    pz, ldz, stridez = None, row[-1] or 1, 0
+    if zeros is not None:
+        zs, pz, ldz, stridez = _w4_matrices(zeros, "zeros", torch.uint8, dim, dev)
+        if tuple(zs) != row:
+            raise ValueError(f"zeros {tuple(zs)} for scales {tuple(ss)}")
+    out, pc, ldc, _ = _result(out, "out", (m, n), x, kind, dev, stream)
+    _call("gemm_f32_w4", dev, stream, kind, groups, m, n, k, group, px, ldx, pq, ldq, strideq, ps,
+          lds, strides, pz, ldz, stridez, pc, ldc, po)
+    return out
+
+
+def _tensor_list(tensors, name, device):
+    """(device, pointers, sizes, types) of dense tensors on one device."""
+    import torch
+
+    types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
+    pointers, sizes, kinds = [], [], []
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in types:
+            raise TypeError(f"{name} must be float32 or bfloat16 CUDA tensors")
+        if device is None:
+            device = t.get_device()
+        elif t.get_device() != device:
+            raise ValueError(f"{name} are not all on one device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        pointers.append(t.data_ptr())
+        sizes.append(t.numel())
+        kinds.append(types[t.dtype])
+    return device, pointers, sizes, kinds
+
+
+def _arrays(pointers, sizes, kinds):
+    n = len(sizes)
+    return ((ctypes.c_void_p * n)(*pointers), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*kinds))
+
+
+def grad_norm(tensors, stream=None):
+    """The norm of all tensors together, sqrt(sum of x^2), as a one-element float32
+    CUDA tensor. ``tensors``: contiguous float32 and bfloat16 CUDA tensors (of one
+    device; none: 0, on the current one)."""
+    import torch
+
+    dev, pointers, sizes, kinds = _tensor_list(tensors, "tensors", None)
+    if dev is None:
+        dev = torch.cuda.current_device()
+    norm = _empty((1,), torch.float32, dev, stream)
+    x, n, kind = _arrays(pointers, sizes, kinds)
+    _call("reduce_f32_norm", dev, stream, len(sizes), x, n, kind, norm.data_ptr())
+    return norm
+
+
+def clip_grads(tensors, limit, out=None, stream=None):
+    """Gradients clipped by their norm: every tensor times min(1, limit / (norm +
+    1e-6)), into ``out`` (tensors of the same types and sizes; None: in place).
+    Returns the norm before, as grad_norm does; nothing is read by the host. No
+    result may overlap another tensor of the call, but its own operand."""
+    import torch
+
+    limit = float(limit)
+    if not limit >= 0.0:
+        raise ValueError(f"limit must be zero or more, not {limit}")
+    tensors = list(tensors)
+    dev, pointers, sizes, kinds = _tensor_list(tensors, "tensors", None)
+    x, n, kind = _arrays(pointers, sizes, kinds)
+    y = None
+    if out is not None:
+        dev, to, to_sizes, to_kinds = _tensor_list(out, "out", dev)
+        if to_sizes != sizes or to_kinds != kinds:
+            raise ValueError("out does not have the tensors' types and sizes")
+        y = (ctypes.c_void_p * len(to))(*to)
+    if dev is None:
+        dev = torch.cuda.current_device()
+    norm = _empty((1,), torch.float32, dev, stream)
+    _call("reduce_f32_clip", dev, stream, len(sizes), x, y, n, kind, limit, norm.data_ptr())
+    return norm
 
 
 def _check_host(x, name):

@@ -19,8 +19,11 @@
 
 #include "../../include/gemm_f32.h"
 #include "../../include/reduce_f32.h"
+#include "clip.h"
 #include "kernels.h"
+#include "route.h"
 #include "segments.h"
+#include "w4.h"
 
 namespace {
 
@@ -406,7 +409,8 @@ long long take_index_faults(bool clear, gemm::IndexFault *first) {
       gemm::tc_index_fault_take, gemm::simt_index_fault_take, gemm::pack_index_fault_take,
       gemm::transpose_index_fault_take, gemm::reduce_index_fault_take,
       gemm::seg_tc_index_fault_take, gemm::seg_pack_index_fault_take,
-      gemm::seg_rows_index_fault_take};
+      gemm::seg_rows_index_fault_take, gemm::route_index_fault_take, gemm::rows_index_fault_take,
+      gemm::w4_index_fault_take, gemm::clip_index_fault_take};
   long long total = 0;
   bool have = false;
   for (auto take : takers) {
@@ -699,6 +703,8 @@ int gemm_f32_poll_device_status(void *stream) {
   int tst = gemm::tc_poll_status(static_cast<cudaStream_t>(stream));
   const int sst = gemm::seg_tc_poll_status(static_cast<cudaStream_t>(stream));
   if (tst == gemm::kOk) tst = sst;
+  const int wst = gemm::w4_poll_status(static_cast<cudaStream_t>(stream));
+  if (tst == gemm::kOk) tst = wst;
   if (tst != gemm::kOk || !GEMM_F32_INDEX_CHECKS) return tst;
   // Checked build: a recorded index violation, left for take_index_fault.
   if (take_index_faults(false, nullptr) > 0) return GEMM_ERR_INDEX;

@@ -1,0 +1,941 @@
+// route.cu -- the router of a mixture of experts: scores, the best experts of
+// every token, their weights, the plan that sorts the tokens' slots by expert,
+// and the gradient of the logits.
+//
+// Choice. A warp takes a token; lane l holds the V = ceil(E / 32) neighbouring
+// experts from l V on. Keys are fp32 values mapped to unsigned integers of the
+// same order, so that one redux finds the warp's largest and the lowest lane
+// that holds it is that of the lowest expert. k rounds, each of which replaces
+// the key of the lane that won.
+//
+// Comparisons. Without bias and sums over groups the logits are the keys: both
+// scores ascend with them. Otherwise the keys are s + bias in fp32, which is off
+// by rounding; where two keys whose order matters are closer than the bound of
+// that (tau below), the token is chosen again in 64 bits (choose_wide): with
+// fp32 logits about one token of a thousand (256 experts), so that the slow
+// FP64 units are off the path.
+//
+// Plan. A stable counting sort: each CTA of the router counts its chunk's slots
+// by expert; a second launch (a programmatic dependent) sums the counts of the
+// chunks before its own and ranks its slots, a warp 32 at a time by matching
+// experts. Few tokens take one CTA, which does both. Counts are integers: their
+// order of addition does not show.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "route.h"
+
+namespace gemm {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+struct P {
+  const void *logits;
+  long long ldx, x_extent;
+  const float *bias;
+  const uint8_t *mask;
+  int32_t *experts;
+  float *weights;
+  int *hist;  // chunks x E counts (several CTAs)
+  int64_t *offsets;
+  int32_t *order, *places;
+  int T, E, k;
+  int sigmoid, renormalise, compare_scores, vec;
+  int groups, top_groups, group_best, per_group, group_lanes;
+  float scale;
+  int chunk, chunks;  // tokens of a CTA, CTAs
+  int plan, plan_warps;
+};
+
+// ------------------------------------------------------------------- values --
+
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <class T>
+__device__ __forceinline__ float load_logit(const P &p, long long t, int e) {
+  const long long at = t * p.ldx + e;
+  return index_ok(kSiteLoadA, at, 1, p.x_extent) ? as_float(static_cast<const T *>(p.logits)[at])
+                                                 : 0.0f;
+}
+
+// Unsigned integers in the order of the values; 0: not available, 1: NaN. The
+// zeros are one value.
+__device__ __forceinline__ unsigned key_of(float f) {
+  if (f != f) return 1u;
+  const unsigned u = __float_as_uint(__fadd_rn(f, 0.0f));
+  return u ^ (static_cast<unsigned>(static_cast<int>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(unsigned key) {
+  return __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ unsigned long long key_of(double f) {
+  if (f != f) return 1ull;
+  const unsigned long long u =
+      static_cast<unsigned long long>(__double_as_longlong(__dadd_rn(f, 0.0)));
+  return u ^ (static_cast<unsigned long long>(static_cast<long long>(u) >> 63) |
+              0x8000000000000000ull);
+}
+__device__ __forceinline__ double value_of(unsigned long long key) {
+  return __longlong_as_double(
+      static_cast<long long>(key ^ (key >> 63 ? 0x8000000000000000ull : ~0ull)));
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, m));
+  return v;
+}
+template <class F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(kFull, v, m);
+  return v;
+}
+__device__ __forceinline__ unsigned warp_best(unsigned v) { return __reduce_max_sync(kFull, v); }
+__device__ __forceinline__ unsigned long long warp_best(unsigned long long v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    const unsigned long long o = __shfl_xor_sync(kFull, v, m);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ float sigmoid(float x) {
+  const float z = expf(-fabsf(x));
+  return (x < 0.0f ? z : 1.0f) / (1.0f + z);
+}
+__device__ __forceinline__ double sigmoid(double x) {
+  const double z = exp(-fabs(x));
+  return (x < 0.0 ? z : 1.0) / (1.0 + z);
+}
+
+// The two largest of both pairs (a1 >= a2, b1 >= b2).
+template <class U>
+__device__ __forceinline__ void merge_best(U &a1, U &a2, U b1, U b2) {
+  const U low = a1 < b1 ? a1 : b1, second = a2 > b2 ? a2 : b2;
+  a1 = a1 < b1 ? b1 : a1;
+  a2 = low > second ? low : second;
+}
+
+// A group's key from those of its best experts: their sum, of one where it has
+// no second.
+template <class U>
+__device__ __forceinline__ U group_key(U b1, U b2, int best) {
+  if (b1 < 2) return b1;
+  if (best == 1 || b2 == 0) return b1;
+  if (b2 == 1) return 1;
+  return key_of(value_of(b1) + value_of(b2));
+}
+
+// The `top` largest of a key a lane (0: none), the lowest lane first, as a mask.
+template <class U>
+__device__ __forceinline__ unsigned choose_lanes(U key, int top) {
+  unsigned chosen = 0;
+  for (int i = 0; i < top; ++i) {
+    const U best = warp_best(key);
+    if (best == 0) break;
+    const int lane = __ffs(__ballot_sync(kFull, key == best)) - 1;
+    chosen |= 1u << lane;
+    if ((threadIdx.x & 31) == lane) key = 0;
+  }
+  return chosen;
+}
+
+// Lane r's choice: the r-th best of the keys, -1 where there is none; *last its
+// key.
+template <int V, class U>
+__device__ __forceinline__ int choose_experts(U (&key)[V], int k, U *won) {
+  const int lane = threadIdx.x & 31;
+  U local = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) local = key[i] > local ? key[i] : local;
+  int mine = -1;
+  *won = 0;
+  for (int r = 0; r < k; ++r) {
+    const U best = warp_best(local);
+    if (best == 0) break;
+    const int from = __ffs(__ballot_sync(kFull, local == best)) - 1;
+    int e = 0;
+    if (lane == from) {
+      // the lowest of its experts with this key goes
+      bool found = false;
+      local = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!found && key[i] == best) {
+          found = true;
+          e = lane * V + i;
+          key[i] = 0;
+        }
+        local = key[i] > local ? key[i] : local;
+      }
+    }
+    e = __shfl_sync(kFull, e, from);
+    if (lane == r) {
+      mine = e;
+      *won = best;
+    }
+  }
+  return mine;
+}
+
+// -------------------------------------------------------- choice in 64 bits --
+
+template <int V, class T>
+__device__ __noinline__ int choose_wide(const P &p, long long t) {
+  const int lane = threadIdx.x & 31;
+  double f[V];
+  unsigned long long key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane * V + i;
+    f[i] = e < p.E ? static_cast<double>(load_logit<T>(p, t, e)) : -INFINITY;
+    key[i] = f[i] == -INFINITY ? 0 : 2;
+  }
+  double m = -INFINITY, sum = 0.0;
+  if (!p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmax(m, f[i]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, s));
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (p.sigmoid) {
+      f[i] = sigmoid(f[i]);
+    } else {
+      f[i] = key[i] != 0 ? exp(f[i] - m) : 0.0;
+      sum += f[i];
+    }
+  }
+  if (!p.sigmoid) sum = warp_sum(sum);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane * V + i;
+    if (!p.sigmoid) f[i] /= sum;
+    if (key[i] != 0 && p.bias != nullptr) {
+      const float b = p.bias[e];
+      if (b == -INFINITY) key[i] = 0;
+      f[i] += static_cast<double>(b);
+    }
+    if (key[i] != 0) key[i] = key_of(f[i]);
+  }
+  if (p.groups > 1) {
+    unsigned long long mine = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      unsigned long long b1 = 0, b2 = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if ((lane * V + i) / p.per_group == g) merge_best(b1, b2, key[i], 0ull);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) {
+        const unsigned long long o1 = __shfl_xor_sync(kFull, b1, s);
+        const unsigned long long o2 = __shfl_xor_sync(kFull, b2, s);
+        merge_best(b1, b2, o1, o2);
+      }
+      if (lane == g) mine = group_key(b1, b2, p.group_best);
+    }
+    const unsigned kept = choose_lanes(mine, p.top_groups);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int g = (lane * V + i) / p.per_group;
+      if (g > 31 || !(kept >> g & 1u)) key[i] = 0;
+    }
+  }
+  unsigned long long won;
+  return choose_experts<V>(key, p.k, &won);
+}
+
+// ------------------------------------------------------------------- router --
+
+// Lane r: the expert of slot r (-1: none). *m, *sum: softmax's, where it is
+// needed; *bad: softmax of a NaN or of +infinity.
+template <int V, class T>
+__device__ __forceinline__ int choose(const P &p, long long t, unsigned *staged, float *m_out,
+                                      float *sum_out, bool *bad_out) {
+  constexpr int kVec = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  float x[V];
+  if (V % kVec == 0 && p.vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += kVec) {
+      const int e = lane * V + i;  // E is a multiple of kVec here
+      uint4 w = make_uint4(0, 0, 0, 0);
+      const long long at = t * p.ldx + e;
+      if (e < p.E && index_ok(kSiteLoadA, at, kVec, p.x_extent))
+        w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.logits) + at));
+      const unsigned u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const float v = sizeof(T) == 4 ? __uint_as_float(u[j * sizeof(T) / 4])
+                                       : __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u
+                                                               : u[j / 2] << 16);
+        x[i + j] = e < p.E ? v : -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      x[i] = e < p.E ? load_logit<T>(p, t, e) : -INFINITY;
+    }
+  }
+  float m = -INFINITY, sum = 0.0f;
+  bool bad = false;
+  const bool stats = !p.sigmoid && (p.compare_scores || !p.renormalise);
+  if (!p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bad |= !(x[i] < INFINITY);
+    bad = __any_sync(kFull, bad);
+  }
+  if (stats) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, x[i]);
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (x[i] > -INFINITY) sum += expf(x[i] - m);
+    sum = warp_sum(sum);
+  }
+  *m_out = m;
+  *sum_out = sum;
+  *bad_out = bad;
+
+  unsigned key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = 0;
+    if (x[i] == -INFINITY) continue;  // not available, or past the last expert
+    float f = x[i];
+    if (p.compare_scores) {
+      f = p.sigmoid ? sigmoid(f) : (bad ? NAN : expf(f - m) / sum);
+      if (p.bias != nullptr) {
+        const float b = __ldg(p.bias + lane * V + i);
+        if (b == -INFINITY) continue;
+        f += b;
+      }
+    }
+    key[i] = key_of(f);
+  }
+  // A key is off by at most err (score) + 2^-24 |key|. Score: expf is good to 2
+  // units, its argument to 2^-24 |x - m| (which times exp(-|x - m|) is below
+  // 0.37), the sum to as many roundings as it has steps, and each division,
+  // sum and product to half a unit of 2^-23.
+  constexpr float kUnit = 5.9604645e-8f;  // 2^-24
+  const float err = p.sigmoid ? 8.0f * kUnit : (V + 16.0f) * kUnit * (sum > 0.0f ? 1.0f / sum : 0.0f);
+  bool unsure = false;
+
+  if (p.groups > 1) {
+    // The best two of each group: 32 / (groups rounded up to a power of two)
+    // lanes look through one group's keys, in shared memory.
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane * V + i < p.E) staged[lane * V + i] = key[i];
+    __syncwarp();
+    const int g = lane / p.group_lanes, sub = lane % p.group_lanes;
+    unsigned b1 = 0, b2 = 0;
+    if (g < p.groups)
+      for (int j = sub; j < p.per_group; j += p.group_lanes)
+        merge_best(b1, b2, staged[g * p.per_group + j], 0u);
+    for (int s = p.group_lanes / 2; s > 0; s >>= 1) {
+      const unsigned o1 = __shfl_xor_sync(kFull, b1, s), o2 = __shfl_xor_sync(kFull, b2, s);
+      merge_best(b1, b2, o1, o2);
+    }
+    __syncwarp();
+    const unsigned mine = sub == 0 ? group_key(b1, b2, p.group_best) : 0u;
+    const unsigned kept = choose_lanes(mine, p.top_groups);
+    if (p.compare_scores) {
+      // the lowest chosen group against each that is not
+      const bool in = kept >> lane & 1u;
+      float off = 0.0f;  // what this group's sum may be off by
+      if (mine > 1)
+        off = 2.0f * err + kUnit * (fabsf(value_of(b1)) + (b2 > 1 ? fabsf(value_of(b2)) : 0.0f) +
+                                    fabsf(value_of(mine)));
+      const unsigned low = __reduce_min_sync(kFull, in ? mine : kFull);
+      const float off_in = __uint_as_float(
+          __reduce_max_sync(kFull, in ? __float_as_uint(off) : 0u));
+      if (!in && mine > 1 && low > 1 && low != kFull)
+        unsure = value_of(low) - value_of(mine) <= off + off_in;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int of = (lane * V + i) / p.per_group;
+      const int at = of * p.group_lanes;
+      if (of >= p.groups || !(kept >> at & 1u)) key[i] = 0;
+    }
+  }
+
+  unsigned won;
+  int mine = choose_experts<V>(key, p.k, &won);
+  if (p.compare_scores) {
+    // Two neighbours of the chosen, or the last of them and one that is left,
+    // that may stand the other way round. Equal logits and biases are equal.
+    auto same = [&](int a, int b) {
+      return load_logit<T>(p, t, a) == load_logit<T>(p, t, b) &&
+             (p.bias == nullptr || p.bias[a] == p.bias[b]);
+    };
+    const unsigned next = __shfl_down_sync(kFull, won, 1);
+    const int next_e = __shfl_down_sync(kFull, mine, 1);
+    if (lane + 1 < p.k && won > 1 && next > 1) {
+      const float a = value_of(won), b = value_of(next);
+      if (a - b <= 2.0f * err + kUnit * (fabsf(a) + fabsf(b))) unsure |= !same(mine, next_e);
+    }
+    const unsigned last = __shfl_sync(kFull, won, p.k - 1);
+    const int last_e = __shfl_sync(kFull, mine, p.k - 1);
+    if (last > 1) {
+      const float a = value_of(last);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (key[i] <= 1) continue;
+        const float b = value_of(key[i]);
+        if (a - b <= 2.0f * err + kUnit * (fabsf(a) + fabsf(b)))
+          unsure |= !same(last_e, lane * V + i);
+      }
+    }
+    if (__any_sync(kFull, unsure)) mine = choose_wide<V, T>(p, t);
+  }
+  return mine;
+}
+
+// Lane r: the weight of its expert.
+template <class T>
+__device__ __forceinline__ float weight_of(const P &p, long long t, int e, float m, float sum,
+                                           bool bad) {
+  const bool there = e >= 0;
+  const float x = there ? load_logit<T>(p, t, e) : -INFINITY;
+  float w;
+  if (!p.renormalise) {
+    w = p.sigmoid ? sigmoid(x) : expf(x - m) / sum;
+  } else {
+    // Scores relative to the largest one's, so that they may all be tiny.
+    float top = warp_max(x);
+    float part;
+    if (p.sigmoid) {
+      top = fminf(top, 0.0f);
+      part = x < 0.0f ? expf(x - top) / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
+    } else {
+      part = expf(x - top);
+    }
+    if (!there) part = 0.0f;
+    w = part / warp_sum(part);
+  }
+  if (bad) w = NAN;
+  return there ? w * p.scale : 0.0f;
+}
+
+// -------------------------------------------------------------------- plan --
+
+// start[e] = sum of count[< e], and the sum of all in start[E], by one warp.
+__device__ __forceinline__ void scan_experts(const int *count, int *start, int E) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane, v = e < E ? count[e] : 0;
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, s, d);
+      if (lane >= d) s += o;
+    }
+    if (e < E) start[e] = carry + s - v;
+    carry += __shfl_sync(kFull, s, 31);
+  }
+  if (lane == 0) start[E] = carry;
+}
+
+struct PlanShared {
+  int *count;  // E: the chunk's, or all slots', counts
+  int *start;  // E + 1: first row of each expert
+  int *base;   // E: first row of each expert's slots of this chunk
+  int *warp;   // plan_warps x E
+};
+
+__device__ __forceinline__ PlanShared plan_shared(int *smem, int E) {
+  return PlanShared{smem, smem + E, smem + 2 * E + 1, smem + 3 * E + 1};
+}
+__host__ __device__ constexpr int plan_ints(int E, int warps) { return (3 + warps) * E + 1; }
+
+// Rows of slots [s0, s1), whose experts' first rows are in sh.base. All threads.
+__device__ void rank_slots(const P &p, const PlanShared &sh, int s0, int s1, long long slots) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31, E = p.E;
+  for (int i = threadIdx.x; i < p.plan_warps * E; i += blockDim.x) sh.warp[i] = 0;
+  __syncthreads();
+  const int each = ((s1 - s0 + p.plan_warps - 1) / p.plan_warps + 31) / 32 * 32;
+  const long long from = s0 + static_cast<long long>(warp) * each;
+  const long long to = from + each < s1 ? from + each : s1;
+  const bool works = warp < p.plan_warps;
+  int *count = sh.warp + (works ? warp : 0) * E;
+  auto expert_of = [&](long long s) {
+    const int e = index_ok(kSiteLoadB, s, 1, slots) ? p.experts[s] : -1;
+    return e >= 0 && e < E ? e : -1;
+  };
+  if (works)
+    for (long long s = from + lane; s < to; s += 32) {
+      const int e = expert_of(s);
+      if (e >= 0) atomicAdd(&count[e], 1);
+    }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int at = sh.base[e];
+    for (int w = 0; w < p.plan_warps; ++w) {
+      const int n = sh.warp[w * E + e];
+      sh.warp[w * E + e] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  if (works)
+    for (long long s0w = from; s0w < to; s0w += 32) {
+      const long long s = s0w + lane;
+      const int e = s < to ? expert_of(s) : -2;
+      const unsigned same = __match_any_sync(kFull, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      if (e >= 0) {
+        const int row = count[e] + rank;
+        if (index_ok(kSiteCStore, row, 1, slots)) p.order[row] = static_cast<int>(s);
+        if (index_ok(kSiteCStore, s, 1, slots)) p.places[s] = row;
+      } else if (e == -1 && index_ok(kSiteCStore, s, 1, slots)) {
+        p.places[s] = -1;
+      }
+      __syncwarp();
+      if (e >= 0 && rank == 0) count[e] += __popc(same);
+      __syncwarp();
+    }
+}
+
+// Chunk c of the plan: counts of all chunks are in p.hist, or (one chunk) this
+// CTA's own in sh.count.
+__device__ void plan_chunk(const P &p, const PlanShared &sh, int c, long long slots) {
+  const int E = p.E, tid = threadIdx.x;
+  if (p.chunks > 1) {
+    for (int e = tid; e < E; e += blockDim.x) sh.count[e] = sh.base[e] = 0;
+    __syncthreads();
+    // several threads an expert, each over a part of the chunks
+    int parts = static_cast<int>(blockDim.x) / E;
+    parts = parts < 1 ? 1 : (parts > p.chunks ? p.chunks : parts);
+    const int each = (p.chunks + parts - 1) / parts;
+    for (int i = tid; i < E * parts; i += blockDim.x) {
+      const int e = i % E, c0 = i / E * each, c1 = min(c0 + each, p.chunks);
+      int before = 0, all = 0;
+#pragma unroll 8
+      for (int j = c0; j < c1; ++j) {
+        const long long at = static_cast<long long>(j) * E + e;
+        const int n = index_ok(kSitePartialRead, at, 1, static_cast<long long>(p.chunks) * E)
+                          ? __ldcg(p.hist + at) : 0;
+        all += n;
+        before += j < c ? n : 0;
+      }
+      if (all != 0) atomicAdd(&sh.count[e], all);
+      if (before != 0) atomicAdd(&sh.base[e], before);
+    }
+  }
+  __syncthreads();
+  if (tid < 32) scan_experts(sh.count, sh.start, E);
+  __syncthreads();
+  for (int e = tid; e <= E; e += blockDim.x) {
+    if (e < E) sh.base[e] = sh.start[e] + (p.chunks > 1 ? sh.base[e] : 0);
+    if (c == 0 && index_ok(kSiteCStore, e, 1, E + 1)) p.offsets[e] = sh.start[e];
+  }
+  // rows of no slot
+  const long long used = sh.start[E];
+  for (long long r = used + static_cast<long long>(c) * blockDim.x + tid; r < slots;
+       r += static_cast<long long>(p.chunks) * blockDim.x)
+    if (index_ok(kSiteCStore, r, 1, slots)) p.order[r] = -1;
+  const long long s0 = static_cast<long long>(c) * p.chunk * p.k;
+  const long long s1 = s0 + static_cast<long long>(p.chunk) * p.k;
+  rank_slots(p, sh, static_cast<int>(s0), static_cast<int>(s1 < slots ? s1 : slots), slots);
+}
+
+constexpr int route_threads(int V) { return V <= 8 ? 1024 : (V == 16 ? 512 : 256); }
+
+template <int V, class T>
+__global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
+  extern __shared__ int smem[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warps = static_cast<int>(blockDim.x >> 5);
+  const PlanShared sh = plan_shared(smem, p.E);
+  // groups' keys stand where the plan's counts of a warp will
+  unsigned *staged = reinterpret_cast<unsigned *>(p.plan ? sh.base : smem) + warp * p.E;
+  const long long slots = static_cast<long long>(p.T) * p.k;
+  if (p.plan) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.count[e] = 0;
+    __syncthreads();
+  }
+  const long long t1 = min(static_cast<long long>(p.T),
+                           (static_cast<long long>(blockIdx.x) + 1) * p.chunk);
+  for (long long t = static_cast<long long>(blockIdx.x) * p.chunk + warp; t < t1; t += warps) {
+    int e = -1;
+    float w = 0.0f;
+    if (p.mask == nullptr || p.mask[t] != 0) {
+      float m, sum;
+      bool bad;
+      e = choose<V, T>(p, t, staged, &m, &sum, &bad);
+      w = weight_of<T>(p, t, e, m, sum, bad);
+    }
+    if (lane < p.k) {
+      const long long s = t * p.k + lane;
+      if (index_ok(kSiteCStore, s, 1, slots)) {
+        p.experts[s] = e;
+        p.weights[s] = w;
+      }
+      if (p.plan && e >= 0) atomicAdd(&sh.count[e], 1);
+    }
+  }
+  if (!p.plan) return;
+  __syncthreads();
+  if (p.chunks > 1) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+      const long long at = static_cast<long long>(blockIdx.x) * p.E + e;
+      if (index_ok(kSitePartialWrite, at, 1, static_cast<long long>(p.chunks) * p.E))
+        p.hist[at] = sh.count[e];
+    }
+  } else {
+    plan_chunk(p, sh, 0, slots);  // reads the experts behind the barrier above
+  }
+}
+
+constexpr int kPlanThreads = 512;
+
+// Counts of a chunk of given experts.
+__global__ void __launch_bounds__(kPlanThreads) count_kernel(const P p) {
+  extern __shared__ int smem[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) smem[e] = 0;
+  __syncthreads();
+  const long long slots = static_cast<long long>(p.T) * p.k;
+  const long long s0 = static_cast<long long>(blockIdx.x) * p.chunk * p.k;
+  const long long s1 = min(slots, s0 + static_cast<long long>(p.chunk) * p.k);
+  for (long long s = s0 + threadIdx.x; s < s1; s += blockDim.x) {
+    const int e = index_ok(kSiteLoadB, s, 1, slots) ? p.experts[s] : -1;
+    if (e >= 0 && e < p.E) atomicAdd(&smem[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    const long long at = static_cast<long long>(blockIdx.x) * p.E + e;
+    if (index_ok(kSitePartialWrite, at, 1, static_cast<long long>(p.chunks) * p.E))
+      p.hist[at] = smem[e];
+  }
+}
+
+// The plan of a chunk; one chunk: its counts too.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const P p) {
+  extern __shared__ int smem[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const PlanShared sh = plan_shared(smem, p.E);
+  const long long slots = static_cast<long long>(p.T) * p.k;
+  if (p.chunks == 1) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.count[e] = 0;
+    __syncthreads();
+    for (long long s = threadIdx.x; s < slots; s += blockDim.x) {
+      const int e = index_ok(kSiteLoadB, s, 1, slots) ? p.experts[s] : -1;
+      if (e >= 0 && e < p.E) atomicAdd(&sh.count[e], 1);
+    }
+  }
+  plan_chunk(p, sh, static_cast<int>(blockIdx.x), slots);
+}
+
+// ---------------------------------------------------------------- gradient --
+
+struct B {
+  const float *dweights, *weights;
+  const void *logits;
+  const int32_t *experts;
+  void *dlogits;
+  long long ldx, x_extent, lddx, dx_extent;
+  int T, E, k, sigmoid, renormalise, vec;
+  float inv_scale;
+};
+
+constexpr int kBackThreads = 256;
+
+template <class T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// A warp takes a token: the slots' terms, spread over a row of shared memory;
+// then the row goes out in one sweep.
+template <class T>
+__global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const B p) {
+  extern __shared__ float rows[];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31, E = p.E;
+  float *row = rows + warp * ((E + 7) / 8 * 8);
+  const T *x = static_cast<const T *>(p.logits);
+  T *dx = static_cast<T *>(p.dlogits);
+  const long long slots = static_cast<long long>(p.T) * p.k;
+  const long long warps = static_cast<long long>(gridDim.x) * (kBackThreads / 32);
+  for (long long t = static_cast<long long>(blockIdx.x) * (kBackThreads / 32) + warp; t < p.T;
+       t += warps) {
+    const long long at = t * p.ldx, s = t * p.k + lane;
+    int e = -1;
+    float w = 0.0f, g = 0.0f;
+    if (lane < p.k && index_ok(kSiteLoadB, s, 1, slots)) {
+      e = p.experts[s];
+      if (e < 0 || e >= E) e = -1;
+      if (e >= 0) {
+        w = p.weights[s];
+        g = p.dweights[s];
+      }
+    }
+    const float total = warp_sum(e >= 0 ? g * w : 0.0f);
+    for (int j = lane; j < E; j += 32) row[j] = 0.0f;
+    float d = p.renormalise ? w * (g - total * p.inv_scale) : w * g;
+    if (p.sigmoid && e >= 0 && index_ok(kSiteLoadA, at + e, 1, p.x_extent))
+      d *= sigmoid(-as_float(x[at + e]));
+    __syncwarp();
+    const unsigned same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
+    if (__any_sync(kFull, __popc(same) > 1)) {
+      for (int r = 0; r < p.k; ++r) {
+        if (lane == r && e >= 0) row[e] += d;
+        __syncwarp();
+      }
+    } else if (e >= 0) {
+      row[e] = d;
+    }
+    __syncwarp();
+    float m = 0.0f, factor = 0.0f;
+    const bool dense = !p.sigmoid && !p.renormalise;
+    bool spread = false;
+    auto logit = [&](int j) {
+      return index_ok(kSiteLoadA, at + j, 1, p.x_extent) ? as_float(x[at + j]) : 0.0f;
+    };
+    if (dense) {
+      m = -INFINITY;
+      for (int j = lane; j < E; j += 32) m = fmaxf(m, logit(j));
+      m = warp_max(m);
+      float sum = 0.0f;
+      for (int j = lane; j < E; j += 32) {
+        const float v = logit(j);
+        sum += v > -INFINITY ? expf(v - m) : (v != v ? NAN : 0.0f);
+      }
+      // no expert at all: no gradient
+      const bool none = __all_sync(kFull, e < 0);
+      spread = !none;
+      factor = total / warp_sum(sum);
+    }
+    constexpr int kVec = 16 / sizeof(T);
+    const long long out = t * p.lddx;
+    auto value = [&](int j) {
+      float v = row[j];
+      if (spread) {
+        const float l = logit(j);
+        if (l > -INFINITY || l != l) v -= expf(l - m) * factor;
+      }
+      return v;
+    };
+    if (p.vec) {  // E is a multiple of kVec
+      for (int j = lane * kVec; j < E; j += 32 * kVec) {
+        unsigned u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (sizeof(T) == 4) {
+            u[i] = __float_as_uint(value(j + i));
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(value(j + 2 * i), value(j + 2 * i + 1));
+            u[i] = *reinterpret_cast<const unsigned *>(&h);
+          }
+        }
+        if (index_ok(kSiteCStore, out + j, kVec, p.dx_extent))
+          *reinterpret_cast<uint4 *>(dx + out + j) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    } else {
+      for (int j = lane; j < E; j += 32)
+        if (index_ok(kSiteCStore, out + j, 1, p.dx_extent)) dx[out + j] = from_float<T>(value(j));
+    }
+    __syncwarp();
+  }
+}
+
+// -------------------------------------------------------------------- host --
+
+template <class K, class A>
+int launch(K kernel, const A &p, unsigned grid, int threads, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // Above the 48 KiB default: set on the current device, which keeps it (every
+  // call, where it is needed; it takes no launch).
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return kErrLaunch;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? kOk : kErrLaunch;
+}
+
+// Warps of a CTA that rank slots: as many as have room for their counts.
+int plan_warps_of(int64_t E, int warps) {
+  const int64_t room = (46 * 1024 / 4 - 1) / E - 3;
+  return static_cast<int>(room < warps ? (room < 1 ? 1 : room) : warps);
+}
+
+size_t smem_of(const P &p, int threads) {
+  const size_t plan = p.plan ? static_cast<size_t>(plan_ints(p.E, p.plan_warps)) * 4 : 0;
+  const size_t keys = p.groups > 1
+                          ? static_cast<size_t>((p.plan ? 2 * p.E + 1 : 0) + threads / 32 * p.E) * 4
+                          : 0;
+  return plan > keys ? plan : keys;
+}
+
+template <int V, class T>
+int launch_v(P &p, cudaStream_t stream) {
+  int threads = route_threads(V);
+  const int64_t want = 32LL * p.chunk;
+  if (threads > want) threads = static_cast<int>((want + 127) / 128 * 128);
+  p.plan_warps = plan_warps_of(p.E, threads / 32 < 16 ? threads / 32 : 16);
+  return launch(route_kernel<V, T>, p, static_cast<unsigned>(p.chunks), threads, smem_of(p, threads),
+                stream);
+}
+
+template <class T>
+int launch_route(P &p, cudaStream_t stream) {
+  if (p.E <= 32) return launch_v<1, T>(p, stream);
+  if (p.E <= 64) return launch_v<2, T>(p, stream);
+  if (p.E <= 128) return launch_v<4, T>(p, stream);
+  if (p.E <= 256) return launch_v<8, T>(p, stream);
+  if (p.E <= 512) return launch_v<16, T>(p, stream);
+  if (p.E <= 1024) return launch_v<32, T>(p, stream);
+  return launch_v<64, T>(p, stream);
+}
+
+int launch_plan(P p, cudaStream_t stream) {
+  p.plan_warps = plan_warps_of(p.E, kPlanThreads / 32);
+  return launch(plan_kernel, p, static_cast<unsigned>(p.chunks), kPlanThreads,
+                static_cast<size_t>(plan_ints(p.E, p.plan_warps)) * 4, stream);
+}
+
+// Tokens of a CTA: at least `least`, and no more CTAs than SMs.
+void cut(P &p, int64_t tokens, int least, int sms) {
+  int64_t chunks = (tokens + least - 1) / least;
+  if (chunks > sms) chunks = sms;
+  if (chunks < 1) chunks = 1;
+  const int64_t chunk = (tokens + chunks - 1) / chunks;
+  p.chunk = static_cast<int>(chunk);
+  p.chunks = static_cast<int>((tokens + chunk - 1) / chunk);
+}
+
+}  // namespace
+
+GEMM_INDEX_FAULT_TAKE(route_index_fault_take)
+
+int route_launch(const RouteArgs &a, int sm_count, cudaStream_t stream) {
+  P p = {};
+  p.logits = a.logits;
+  p.ldx = a.ldx;
+  p.x_extent = matrix_extent(a.T, a.E, a.ldx);
+  p.bias = a.bias;
+  p.mask = a.mask;
+  p.experts = a.experts;
+  p.weights = a.weights;
+  p.offsets = a.offsets;
+  p.order = a.order;
+  p.places = a.places;
+  p.T = static_cast<int>(a.T);
+  p.E = static_cast<int>(a.E);
+  p.k = static_cast<int>(a.k);
+  p.sigmoid = a.sigmoid;
+  p.renormalise = a.renormalise;
+  p.groups = a.groups;
+  p.top_groups = a.top_groups;
+  p.group_best = a.group_best;
+  p.per_group = static_cast<int>(a.E / a.groups);
+  p.group_lanes = 32;
+  while (32 / p.group_lanes < a.groups) p.group_lanes /= 2;
+  p.compare_scores = a.bias != nullptr || (a.groups > 1 && a.group_best > 1);
+  const int elem = a.bf16 ? 2 : 4, per16 = 16 / elem;
+  p.vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ldx % per16 == 0 && a.E % per16 == 0;
+  p.scale = a.scale;
+  p.plan = a.offsets != nullptr;
+  cut(p, a.T, a.T <= 64 ? 64 : 32, sm_count);
+  void *ws = nullptr;
+  if (p.plan && p.chunks > 1) {
+    const int st = pool_alloc(&ws, static_cast<size_t>(p.chunks) * a.E * sizeof(int), stream);
+    if (st != kOk) return st;
+    p.hist = static_cast<int *>(ws);
+  }
+  int st = a.bf16 ? launch_route<__nv_bfloat16>(p, stream) : launch_route<float>(p, stream);
+  if (ws != nullptr) {
+    if (st == kOk) st = launch_plan(p, stream);
+    const int fst = pool_free(ws, stream);
+    if (st == kOk) st = fst;
+  }
+  return st;
+}
+
+int route_plan_launch(int64_t slots, int64_t E, const int32_t *experts, int64_t *offsets,
+                      int32_t *order, int32_t *places, int sm_count, cudaStream_t stream) {
+  P p = {};
+  p.experts = const_cast<int32_t *>(experts);  // read here
+  p.offsets = offsets;
+  p.order = order;
+  p.places = places;
+  p.T = static_cast<int>(slots);
+  p.E = static_cast<int>(E);
+  p.k = 1;
+  p.plan = 1;
+  cut(p, slots, 4096, sm_count);
+  if (p.chunks == 1) return launch_plan(p, stream);
+  void *ws = nullptr;
+  int st = pool_alloc(&ws, static_cast<size_t>(p.chunks) * E * sizeof(int), stream);
+  if (st != kOk) return st;
+  p.hist = static_cast<int *>(ws);
+  st = launch(count_kernel, p, static_cast<unsigned>(p.chunks), kPlanThreads,
+              static_cast<size_t>(E) * sizeof(int), stream);
+  if (st == kOk) st = launch_plan(p, stream);
+  const int fst = pool_free(ws, stream);
+  return st != kOk ? st : fst;
+}
+
+int route_backward_launch(const RouteBackwardArgs &a, int sm_count, cudaStream_t stream) {
+  B p = {};
+  p.dweights = a.dweights;
+  p.weights = a.weights;
+  p.logits = a.logits;
+  p.experts = a.experts;
+  p.dlogits = a.dlogits;
+  p.ldx = a.ldx;
+  p.x_extent = matrix_extent(a.T, a.E, a.ldx);
+  p.lddx = a.lddx;
+  p.dx_extent = matrix_extent(a.T, a.E, a.lddx);
+  p.T = static_cast<int>(a.T);
+  p.E = static_cast<int>(a.E);
+  p.k = static_cast<int>(a.k);
+  p.sigmoid = a.sigmoid;
+  p.renormalise = a.renormalise;
+  p.inv_scale = 1.0f / a.scale;
+  const int elem = a.bf16 ? 2 : 4, per16 = 16 / elem;
+  p.vec = reinterpret_cast<uintptr_t>(a.dlogits) % 16 == 0 && a.lddx % per16 == 0 &&
+          a.E % per16 == 0;
+  const int64_t blocks = (a.T + kBackThreads / 32 - 1) / (kBackThreads / 32);
+  const int64_t most = 8LL * (sm_count > 0 ? sm_count : 1);
+  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  const size_t smem = static_cast<size_t>(kBackThreads / 32) * ((a.E + 7) / 8 * 8) * sizeof(float);
+  return a.bf16 ? launch(route_backward_kernel<__nv_bfloat16>, p, grid, kBackThreads, smem, stream)
+                : launch(route_backward_kernel<float>, p, grid, kBackThreads, smem, stream);
+}
+
+}  // namespace gemm

@@ -1,0 +1,366 @@
+// route_rows.cu -- rows to the experts and back: copies of each token's row at
+// its places, the weighted sum of a token's rows, and its gradients.
+//
+//   dispatch   Y[places[t][j]] = X[t]
+//   combine    O[t] = sum_j w[t][j] Y[places[t][j]]
+//   backward   dY[places[t][j]] = w[t][j] dO[t],  dw[t][j] = dO[t] . Y[places[t][j]]
+//
+// All three are bound by memory: a token's row is read once (or written once),
+// each expert's row once, whichever order they lie in. A warp takes a piece of
+// 1 to 2 KB of a token's row through all its places, with the loads of up to four
+// places in flight. Rows are read and written 16 bytes a lane where their starts
+// and widths allow it.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "route.h"
+
+namespace gemm {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kPlaces = 4;  // places whose loads are in flight together
+
+struct P {
+  const void *token, *expert;
+  void *out;
+  const int32_t *places;
+  const float *weights;
+  float *dweights;
+  long long ld_token, ld_expert, ld_out;
+  long long token_extent, expert_extent, out_extent;
+  long long rows, T;
+  int D, k;       // D in loads (kElems elements each)
+  int pieces;     // of a row
+  int per_token;  // backward: warps of a token
+};
+
+// A lane's share of a row at a time: U loads of kElems elements, 32 loads apart.
+template <class T, bool VEC>
+struct Row {
+  using Load = T;
+  static constexpr int kElems = 1, U = 8;
+  static __device__ __forceinline__ Load zero() { return Load(0.0f); }
+  static __device__ __forceinline__ void unpack(const Load &l, float (&v)[kElems]) {
+    v[0] = static_cast<float>(l);
+  }
+  static __device__ __forceinline__ Load pack(const float (&v)[kElems]) { return static_cast<T>(v[0]); }
+};
+template <>
+struct Row<float, true> {
+  using Load = float4;
+  static constexpr int kElems = 4, U = 2;
+  static __device__ __forceinline__ Load zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+  static __device__ __forceinline__ void unpack(const Load &l, float (&v)[kElems]) {
+    v[0] = l.x;
+    v[1] = l.y;
+    v[2] = l.z;
+    v[3] = l.w;
+  }
+  static __device__ __forceinline__ Load pack(const float (&v)[kElems]) {
+    return make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <>
+struct Row<__nv_bfloat16, true> {
+  using Load = uint4;
+  static constexpr int kElems = 8, U = 2;
+  static __device__ __forceinline__ Load zero() { return make_uint4(0, 0, 0, 0); }
+  static __device__ __forceinline__ void unpack(const Load &l, float (&v)[kElems]) {
+    const unsigned u[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ Load pack(const float (&v)[kElems]) {
+    unsigned u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const unsigned *>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+// Loads [c, c + 32 U) of a row, this lane's.
+template <class R>
+__device__ __forceinline__ void load_row(const void *base, long long row_at, int c, int D, int site,
+                                         long long extent, typename R::Load (&v)[R::U]) {
+  const typename R::Load *p =
+      reinterpret_cast<const typename R::Load *>(static_cast<const char *>(base));
+#pragma unroll
+  for (int u = 0; u < R::U; ++u) {
+    const int i = c + 32 * u;
+    v[u] = i < D && index_ok(site, row_at + static_cast<long long>(i) * R::kElems, R::kElems, extent)
+               ? p[row_at / R::kElems + i]
+               : R::zero();
+  }
+}
+template <class R>
+__device__ __forceinline__ void store_row(void *base, long long row_at, int c, int D,
+                                          long long extent, const typename R::Load (&v)[R::U]) {
+  typename R::Load *p = reinterpret_cast<typename R::Load *>(static_cast<char *>(base));
+#pragma unroll
+  for (int u = 0; u < R::U; ++u) {
+    const int i = c + 32 * u;
+    if (i < D && index_ok(kSiteCStore, row_at + static_cast<long long>(i) * R::kElems, R::kElems,
+                          extent))
+      p[row_at / R::kElems + i] = v[u];
+  }
+}
+
+__device__ __forceinline__ long long place_of(const P &p, long long s) {
+  const long long at = index_ok(kSiteLoadB, s, 1, p.T * p.k) ? p.places[s] : -1;
+  return at >= 0 && at < p.rows ? at : -1;
+}
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const P p) {
+  using R = Row<T, VEC>;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long units = p.T * p.pieces, step = static_cast<long long>(gridDim.x) * kWarps;
+  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32; i < units;
+       i += step) {
+    const long long t = i / p.pieces;
+    const int c = static_cast<int>(i - t * p.pieces) * 32 * R::U + lane;
+    typename R::Load v[R::U];
+    load_row<R>(p.token, t * p.ld_token, c, p.D, kSiteCopySrc, p.token_extent, v);
+    for (int j = 0; j < p.k; ++j) {
+      const long long at = place_of(p, t * p.k + j);
+      if (at >= 0) store_row<R>(p.out, at * p.ld_out, c, p.D, p.out_extent, v);
+    }
+  }
+}
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const P p) {
+  using R = Row<T, VEC>;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long units = p.T * p.pieces, step = static_cast<long long>(gridDim.x) * kWarps;
+  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32; i < units;
+       i += step) {
+    const long long t = i / p.pieces;
+    const int c = static_cast<int>(i - t * p.pieces) * 32 * R::U + lane;
+    float sum[R::U][R::kElems] = {};
+    for (int j0 = 0; j0 < p.k; j0 += kPlaces) {
+      typename R::Load v[kPlaces][R::U];
+      long long at[kPlaces];
+      float w[kPlaces];
+#pragma unroll
+      for (int j = 0; j < kPlaces; ++j) {
+        const long long s = t * p.k + j0 + j;
+        at[j] = j0 + j < p.k ? place_of(p, s) : -1;
+        w[j] = at[j] >= 0 && p.weights != nullptr ? p.weights[s] : 1.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kPlaces; ++j)
+        if (at[j] >= 0)
+          load_row<R>(p.expert, at[j] * p.ld_expert, c, p.D, kSiteLoadA, p.expert_extent, v[j]);
+#pragma unroll
+      for (int j = 0; j < kPlaces; ++j) {
+        if (at[j] < 0) continue;
+#pragma unroll
+        for (int u = 0; u < R::U; ++u) {
+          float y[R::kElems];
+          R::unpack(v[j][u], y);
+#pragma unroll
+          for (int e = 0; e < R::kElems; ++e) sum[u][e] = fmaf(w[j], y[e], sum[u][e]);
+        }
+      }
+    }
+    typename R::Load o[R::U];
+#pragma unroll
+    for (int u = 0; u < R::U; ++u) o[u] = R::pack(sum[u]);
+    store_row<R>(p.out, t * p.ld_out, c, p.D, p.out_extent, o);
+  }
+}
+
+// `per_token` warps share a token's pieces; their sums of dw meet in shared
+// memory, in the order of the warps.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const P p) {
+  using R = Row<T, VEC>;
+  __shared__ float part[kWarps][32][33];  // warp, slot, lane
+  __shared__ float dots[kWarps][32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = static_cast<int>(threadIdx.x >> 5);
+  const int tokens = kWarps / p.per_token, mine = warp / p.per_token, sub = warp % p.per_token;
+  for (long long t0 = static_cast<long long>(blockIdx.x) * tokens; t0 < p.T;
+       t0 += static_cast<long long>(gridDim.x) * tokens) {
+    const long long t = t0 + mine;
+    if (t < p.T) {
+      for (int j = 0; j < p.k; ++j) part[warp][j][lane] = 0.0f;
+      for (int piece = sub; piece < p.pieces; piece += p.per_token) {
+        const int c = piece * 32 * R::U + lane;
+        typename R::Load d[R::U];
+        load_row<R>(p.token, t * p.ld_token, c, p.D, kSiteLoadA, p.token_extent, d);
+        for (int j0 = 0; j0 < p.k; j0 += kPlaces) {
+          typename R::Load v[kPlaces][R::U];
+          long long at[kPlaces];
+#pragma unroll
+          for (int j = 0; j < kPlaces; ++j) {
+            at[j] = j0 + j < p.k ? place_of(p, t * p.k + j0 + j) : -1;
+            if (at[j] >= 0 && p.dweights != nullptr)
+              load_row<R>(p.expert, at[j] * p.ld_expert, c, p.D, kSiteLoadB, p.expert_extent, v[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < kPlaces; ++j) {
+            if (at[j] < 0) continue;
+            const float w = p.weights != nullptr ? p.weights[t * p.k + j0 + j] : 1.0f;
+            float dot = 0.0f;
+            typename R::Load o[R::U];
+#pragma unroll
+            for (int u = 0; u < R::U; ++u) {
+              float g[R::kElems], y[R::kElems];
+              R::unpack(d[u], g);
+              if (p.dweights != nullptr) {
+                R::unpack(v[j][u], y);
+#pragma unroll
+                for (int e = 0; e < R::kElems; ++e) dot = fmaf(g[e], y[e], dot);
+              }
+#pragma unroll
+              for (int e = 0; e < R::kElems; ++e) g[e] *= w;
+              o[u] = R::pack(g);
+            }
+            if (p.out != nullptr)
+              store_row<R>(p.out, at[j] * p.ld_out, c, p.D, p.out_extent, o);
+            if (p.dweights != nullptr) part[warp][j0 + j][lane] += dot;
+          }
+        }
+      }
+      if (p.dweights != nullptr) {
+        // lane j: the sum of slot j's 32 parts
+        __syncwarp();
+        float sum = 0.0f;
+        if (lane < p.k)
+#pragma unroll 8
+          for (int l = 0; l < 32; ++l) sum += part[warp][lane][l];
+        dots[warp][lane] = sum;
+      }
+    }
+    if (p.dweights == nullptr) continue;
+    __syncthreads();
+    if (t < p.T && sub == 0 && lane < p.k) {
+      float sum = 0.0f;
+      for (int w = 0; w < p.per_token; ++w) sum += dots[warp + w][lane];
+      if (index_ok(kSiteCStore, t * p.k + lane, 1, p.T * p.k)) p.dweights[t * p.k + lane] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------------- host --
+
+template <class K>
+int launch(K kernel, const P &p, long long blocks, int sms, cudaStream_t stream) {
+  const long long most = 8LL * (sms > 0 ? sms : 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? (blocks < 1 ? 1 : blocks) : most), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? kOk : kErrLaunch;
+}
+
+bool wide(const void *base, int64_t ld, int elem) {
+  return base == nullptr || (reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld * elem % 16 == 0);
+}
+
+// Rows in 16-byte loads?
+bool fill(const RowsArgs &a, P *p) {
+  const int elem = a.bf16 ? 2 : 4;
+  const bool vec = a.D * elem % 16 == 0 && wide(a.token, a.ld_token, elem) &&
+                   wide(a.expert, a.ld_expert, elem) && wide(a.out, a.ld_out, elem);
+  *p = P{};
+  p->token = a.token;
+  p->expert = a.expert;
+  p->out = a.out;
+  p->places = a.places;
+  p->weights = a.weights;
+  p->dweights = a.dweights;
+  p->ld_token = a.ld_token;
+  p->ld_expert = a.ld_expert;
+  p->ld_out = a.ld_out;
+  p->token_extent = matrix_extent(a.T, a.D, a.ld_token);
+  p->expert_extent = matrix_extent(a.rows, a.D, a.ld_expert);
+  p->rows = a.rows;
+  p->T = a.T;
+  p->k = static_cast<int>(a.k);
+  const int elems = vec ? 16 / elem : 1, u = vec ? 2 : 8;
+  p->D = static_cast<int>(a.D / elems);
+  p->pieces = (p->D + 32 * u - 1) / (32 * u);
+  return vec;
+}
+
+template <template <class, bool> class K>
+int pick(bool bf16, bool vec, const P &p, long long blocks, int sms, cudaStream_t s) {
+  if (bf16)
+    return vec ? launch(K<__nv_bfloat16, true>::kernel(), p, blocks, sms, s)
+               : launch(K<__nv_bfloat16, false>::kernel(), p, blocks, sms, s);
+  return vec ? launch(K<float, true>::kernel(), p, blocks, sms, s)
+             : launch(K<float, false>::kernel(), p, blocks, sms, s);
+}
+
+template <class T, bool VEC>
+struct Dispatch {
+  static auto kernel() { return dispatch_kernel<T, VEC>; }
+};
+template <class T, bool VEC>
+struct Combine {
+  static auto kernel() { return combine_kernel<T, VEC>; }
+};
+template <class T, bool VEC>
+struct Backward {
+  static auto kernel() { return backward_kernel<T, VEC>; }
+};
+
+long long blocks_of(const P &p) { return (p.T * p.pieces + kWarps - 1) / kWarps; }
+
+}  // namespace
+
+GEMM_INDEX_FAULT_TAKE(rows_index_fault_take)
+
+int rows_dispatch_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
+  P p;
+  const bool vec = fill(a, &p);
+  p.out_extent = matrix_extent(a.rows, a.D, a.ld_out);
+  return pick<Dispatch>(a.bf16, vec, p, blocks_of(p), sm_count, stream);
+}
+
+int rows_combine_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
+  P p;
+  const bool vec = fill(a, &p);
+  p.out_extent = matrix_extent(a.T, a.D, a.ld_out);
+  return pick<Combine>(a.bf16, vec, p, blocks_of(p), sm_count, stream);
+}
+
+int rows_backward_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
+  P p;
+  const bool vec = fill(a, &p);
+  p.out_extent = matrix_extent(a.rows, a.D, a.ld_out);
+  // Warps of a token: as many as it has pieces while the tokens alone do not
+  // fill the GPU.
+  p.per_token = 1;
+  while (p.per_token < kWarps && p.per_token < p.pieces && a.T * p.per_token < 16LL * sm_count)
+    p.per_token *= 2;
+  const long long tokens = kWarps / p.per_token;
+  return pick<Backward>(a.bf16, vec, p, (a.T + tokens - 1) / tokens, sm_count, stream);
+}
+
+}  // namespace gemm

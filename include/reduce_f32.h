@@ -1,6 +1,7 @@
 /*
- * reduce_f32.h -- C ABI of libgemm_f32.so, part 2: the sum of a fp32 vector
- * on an NVIDIA GB300 (sm_103a).
+ * reduce_f32.h -- C ABI of libgemm_f32.so, part 2: the sum of a fp32 vector,
+ * and the norm of many tensors together and their clipping by it, on an NVIDIA
+ * GB300 (sm_103a).
  *
  * Operation. out[0] = sum_{i < n} x[i], computed as in "GPU compute shaders"
  * ("How it works", step 6, and the reduce routine under "Code"): `groups`
@@ -22,7 +23,7 @@
 
 #include <stdint.h>
 
-#include "gemm_f32.h"
+#include "segment_gemm_f32.h"  /* gemm_f32_type */
 
 #ifdef __cplusplus
 extern "C" {
@@ -44,6 +45,34 @@ extern "C" {
  * Returns a gemm_f32_status.
  */
 int reduce_f32_sum(int64_t n, const float *x, float *out, int groups, void *stream);
+
+/*
+ * reduce_f32_norm -- *norm = sqrt(sum of x^2 over all elements of all tensors).
+ * reduce_f32_clip -- y = x min(1, limit / (*norm + 1e-6)) for every tensor: the
+ * clipping of gradients by their global norm.
+ *   count   tensors, 0 .. 2^20 (none: the norm is 0)
+ *   x, y    HOST arrays of `count` device pointers, each to the n[i] elements of
+ *           a dense tensor, aligned to its element; y NULL, or y[i] = x[i]: in
+ *           place (which nothing is written to where the factor is 1). No result
+ *           may overlap another, the norm, or an operand but its own in the same
+ *           place (GEMM_ERR_ALIAS): a tensor that is listed twice cannot be
+ *           clipped in place.
+ *   n       HOST array, elements of each tensor, 0 .. 2^40
+ *   type    HOST array, a gemm_f32_type for each tensor (x[i] and y[i])
+ *   limit   >= 0 (infinity: no tensor changes unless the norm is not finite)
+ *   norm    device pointer to one fp32
+ * The arrays are read before the call returns. Squares are summed to 64 bits,
+ * over the whole range of the types, in an order that the tensors' sizes and
+ * alignment, the device and the order of the list fix: reruns are bit-identical.
+ * The factor is computed in 64 bits and rounded to fp32 (2^-24), the products
+ * once to the type. A norm of infinity makes the factor 0 (and infinite elements
+ * NaN), a NaN makes every result NaN. Workspace: 8 bytes a CTA from the library's
+ * pool. A launch takes up to 100 tensors of a shorter list, 1000 of a longer one.
+ */
+int reduce_f32_norm(int64_t count, const void *const *x, const int64_t *n, const int *type,
+                    float *norm, void *stream);
+int reduce_f32_clip(int64_t count, const void *const *x, void *const *y, const int64_t *n,
+                    const int *type, float limit, float *norm, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,63 @@
+/*
+ * w4_gemm_f32.h -- C ABI of libgemm_f32.so, part 5: matrix products with
+ * weights held in 4 bits on an NVIDIA GB300 (sm_103a), of one matrix or of one
+ * for each segment of rows (an expert; segment_gemm_f32.h).
+ *
+ * Weights. W is N x K (a row for each result column):
+ *
+ *     W[n][k] = s[n][k / group] (q[n][k] - z[n][k / group])
+ *
+ *   Q       row n holds q[n][0], q[n][1], .. in ceil(K / 2) bytes, the even k in
+ *           the low four bits; with an odd K the last byte's high bits are not
+ *           used. Pitch ldq and stride strideq in bytes.
+ *   scales  N x ceil(K / group), of `type`; the last group of a row may be short
+ *   zeros   N x ceil(K / group) bytes, of which the low four bits count; NULL: 8
+ *
+ * Types and accuracy are those of segment_gemm_f32.h: fp32 operands FP32 class
+ * against the exact W, bf16 operands with fp32 sums, rounded once. No weight is
+ * rounded, but fp32 ones to fp32 in calls of many rows. fp32 A from 2^-110 in
+ * magnitude to the largest finite value, as there; an infinite or NaN A, or an
+ * infinite or NaN scale, makes the results that it enters not finite, and no
+ * others.
+ */
+#ifndef W4_GEMM_F32_H
+#define W4_GEMM_F32_H
+
+#include <stdint.h>
+
+#include "segment_gemm_f32.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * gemm_f32_w4 -- C = A W^T, or C_g = A_g W_g^T for every segment g.
+ *   groups    matrices, and segments; without offsets at most 1
+ *   M, N, K   A is M x K, every W N x K, C is M x N
+ *   group     a multiple of 32 (K or more: a scale for each row)
+ *   strideq, strides, stridez
+ *             matrix g starts that many bytes (elements, bytes) after g - 1;
+ *             0: one for all
+ *   offsets   as for gemm_f32_grouped; NULL: all rows with matrix 0
+ *   C         rows of no segment are not written; must not overlap anything else
+ *             (GEMM_ERR_ALIAS)
+ * K == 0 sets the rows to zero. Rows of Q that start on 16 bytes (Q, ldq and
+ * strideq multiples of 16) are read as they lie; others are copied first, a
+ * call's workspace of Q's size. Calls of 128 rows a segment on average and more
+ * expand up to 128 MB of weights at a time in a workspace. Pointers are aligned
+ * to their element; sizes up to GEMM_F32_MAX_SEGMENT_SIZE.
+ */
+int gemm_f32_w4(int type, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group,
+                const void *A, int64_t lda,
+                const uint8_t *Q, int64_t ldq, int64_t strideq,
+                const void *scales, int64_t lds, int64_t strides,
+                const uint8_t *zeros, int64_t ldz, int64_t stridez,
+                void *C, int64_t ldc,
+                const int64_t *offsets, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* W4_GEMM_F32_H */
