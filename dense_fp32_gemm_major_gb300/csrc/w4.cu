@@ -38,26 +38,35 @@
 namespace gemm {
 namespace {
 
-constexpr int kTileN = 64, kBlockK = 256, kStages = 6;
+constexpr int kTileN = 64, kBlockK = 256, kStages = 4;
 constexpr int kStageBytes = kTileN * kBlockK / 2;
 constexpr int kConsumers = 128, kThreads = kConsumers + 32;
 constexpr int kMaxSplit = 8;
 
 __device__ int g_w4_status;  // first error recorded by a kernel of this unit
 
+// A as fragments: for each tile of 8 rows and each block of 256 k, `terms` bf16
+// terms and the 8 rows' factors. A segment's tiles follow each other from
+// tile r0 / 8 + g on (r0: its first row, g: its number), which no two share.
+struct Prep {
+  const void *A;
+  uint8_t *to;
+  const int64_t *offsets;
+  long long lda, a_extent, to_extent;
+  int M, K, blocks, a_vec;
+};
+
 struct P {
-  const void *A, *scales;
+  const uint8_t *A;  // Prep::to
+  const void *scales;
   const uint8_t *zeros;
   void *C;
   const int64_t *offsets;
-  long long lda, a_extent, lds, strides, s_extent, ldz, stridez, z_extent, ldc, c_extent;
-  int groups, M, N, K, group, row_groups;
-  int split;      // CTAs that share a tile's k
-  int phase;      // blocks of k whose A and scales stand in shared memory together
-  int period;     // 32-k steps between two times the scales are applied
-  int a_vec;      // A's rows in 16-byte loads
-  int step_groups;  // groups that a phase may touch
-  int z_step;       // 0: one matrix for all segments
+  long long a_extent, lds, strides, s_extent, ldz, stridez, z_extent, ldc, c_extent;
+  int M, N, K, row_groups;
+  int blocks, split;  // of k; CTAs that share them
+  int per_group;      // times that the scales are applied to a group
+  int z_step;         // 0: one matrix for all segments
   unsigned long long timeout_ns;
 };
 
@@ -65,6 +74,16 @@ struct Shared {
   uint64_t full[kStages], empty[kStages];
   int abort, drain_abort;
 };
+
+// 1-D copy into this CTA's shared memory.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar,
                                             int32_t x, int32_t y, int32_t z) {
@@ -105,8 +124,9 @@ __device__ __forceinline__ float read_cluster(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ uint32_t bits(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 
 // A's values from 2^113 on (and infinities, NaN) could leave fp32's range in a sum
-// of 128 products with up to 15, although their products with the weights do
-// not. Rows with such values are taken 2^-16 times, and their sums 2^16 times.
+// of 256 products with up to 15, although their products with the weights do
+// not. A row's block of k with such values is taken 2^-16 times, and its sums
+// 2^16 times.
 constexpr float kShrink = 0x1p-16f, kGrow = 0x1p16f;
 
 // Whether a word's two bf16 (or its fp32: the upper) have an exponent of 240 or more.
@@ -115,10 +135,10 @@ __device__ __forceinline__ uint32_t large(uint32_t u) {
   return t & t << 2;
 }
 
-// Eight neighbouring k of a row, in the fragments' order, term by term; whether
-// one is large. `shrink`: kShrink times.
+// Eight neighbouring k of a row, in the fragments' order, term by term; *shrink:
+// kShrink times, for one of the warp's 256 is large.
 template <class T>
-__device__ __forceinline__ bool load8(const P &p, long long at, int left, bool shrink,
+__device__ __forceinline__ void load8(const Prep &p, long long at, int left, bool *shrink,
                                       uint4 (&out)[sizeof(T) == 2 ? 1 : 3]) {
   const T *a = static_cast<const T *>(p.A) + at;
   if constexpr (sizeof(T) == 2) {
@@ -133,7 +153,8 @@ __device__ __forceinline__ bool load8(const P &p, long long at, int left, bool s
       v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     }
     const uint32_t big = large(v.x) | large(v.y) | large(v.z) | large(v.w);
-    if (shrink) {
+    *shrink = __any_sync(0xffffffffu, (big & 0x40004000u) != 0);
+    if (*shrink) {
       const __nv_bfloat162 f = __float2bfloat162_rn(kShrink);
       uint32_t *u = &v.x;
 #pragma unroll
@@ -144,7 +165,6 @@ __device__ __forceinline__ bool load8(const P &p, long long at, int left, bool s
     }
     out[0] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                         __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-    return (big & 0x40004000u) != 0;
   } else {
     float v[8];
     if (left >= 8 && p.a_vec) {
@@ -167,10 +187,11 @@ __device__ __forceinline__ bool load8(const P &p, long long at, int left, bool s
     }
     uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      big |= large(__float_as_uint(v[i]));
-      if (shrink) v[i] *= kShrink;
-    }
+    for (int i = 0; i < 8; ++i) big |= large(__float_as_uint(v[i]));
+    *shrink = __any_sync(0xffffffffu, (big & 0x40000000u) != 0);
+    if (*shrink)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= kShrink;
     uint32_t h[3][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -188,7 +209,6 @@ __device__ __forceinline__ bool load8(const P &p, long long at, int left, bool s
     for (int t = 0; t < 3; ++t)
       out[t] = make_uint4(h[t][0] | h[t][4] << 16, h[t][1] | h[t][5] << 16,
                           h[t][2] | h[t][6] << 16, h[t][3] | h[t][7] << 16);
-    return (big & 0x40000000u) != 0;
   }
 }
 
@@ -202,33 +222,77 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) {
 }
 
 __host__ __device__ constexpr int terms_of(int elem) { return elem == 2 ? 1 : 3; }
-// Bytes of A in a block of k, for NT tiles of 8 rows.
-__host__ __device__ constexpr int a_block_bytes(int nt, int elem) {
-  return kBlockK * 8 * 2 * nt * terms_of(elem);
-}
+// Bytes of A for a tile of 8 rows and a block of k, and from one to the next.
+__host__ __device__ constexpr int a_bytes(int elem) { return kBlockK * 8 * 2 * terms_of(elem) + 32; }
+__host__ __device__ constexpr int a_step(int elem) { return a_bytes(elem) + 96; }
 
 __device__ __forceinline__ long long held(long long a, long long m) {
   return a < 0 ? 0 : (a > m ? m : a);
 }
 
-// NT tiles of 8 rows at a time.
-template <class T, int NT>
+__device__ __forceinline__ void segment_of(const int64_t *offsets, int g, int M, long long *r0,
+                                           long long *r1) {
+  *r0 = 0;
+  *r1 = M;
+  if (offsets != nullptr) {
+    *r0 = held(offsets[g], M);
+    *r1 = held(offsets[g + 1], M);
+  }
+}
+
+constexpr int kPrepWarps = 4;
+
+// A warp takes a block of k of a row: once for all CTAs that will read it.
+template <class T>
+__global__ void __launch_bounds__(32 * kPrepWarps) w4_prep_kernel(const Prep p) {
+  constexpr int kTerms = terms_of(sizeof(T));
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, g = blockIdx.y;
+  long long r0, r1;
+  segment_of(p.offsets, g, p.M, &r0, &r1);
+  if (r0 >= r1) return;
+  const long long rows = (r1 - r0 + 7) / 8 * 8;  // the last tile's absent rows are zero
+  for (long long u = static_cast<long long>(blockIdx.x) * kPrepWarps + threadIdx.x / 32;
+       u < rows * p.blocks; u += static_cast<long long>(gridDim.x) * kPrepWarps) {
+    const long long r = u / p.blocks;
+    const int b = static_cast<int>(u - r * p.blocks), token = static_cast<int>(r & 7);
+    const long long k = static_cast<long long>(b) * kBlockK + lane * 8;
+    const long long left = r0 + r < r1 ? p.K - k : 0;
+    uint4 v[kTerms];
+    bool shrink;
+    load8<T>(p, (r0 + r) * p.lda + k, left < 8 ? static_cast<int>(left) : 8, &shrink, v);
+    const long long to = ((r0 / 8 + g + r / 8) * p.blocks + b) * a_step(sizeof(T));
+    if (!index_ok(kSitePartialWrite, to, a_bytes(sizeof(T)), p.to_extent)) continue;
+#pragma unroll
+    for (int i = 0; i < kTerms; ++i)
+      *reinterpret_cast<uint4 *>(p.to + to +
+                                 ((lane / 4 * kTerms + i) * 32 + token * 4 + lane % 4) * 16) = v[i];
+    if (lane == 0)
+      *reinterpret_cast<float *>(p.to + to + kTerms * 4096 + token * 4) = shrink ? kGrow : 1.0f;
+  }
+}
+
+// NT tiles of 8 rows at a time; the scales meet the sums every PERIOD steps of 32 k.
+template <class T, int NT, int PERIOD>
 __global__ void __launch_bounds__(kThreads)
     w4_kernel(const __grid_constant__ CUtensorMap map, const P p) {
-  constexpr int kTerms = terms_of(sizeof(T));
+  constexpr int kTerms = terms_of(sizeof(T)), kABytes = a_bytes(sizeof(T)), kAStep = a_step(sizeof(T));
+  constexpr int kTimes = 8 / PERIOD;  // of a block
   extern __shared__ uint8_t raw[];
-  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
-  uint8_t *stages = base;
-  uint8_t *as = stages + kStages * kStageBytes;
-  float *sums = reinterpret_cast<float *>(as + p.phase * a_block_bytes(NT, sizeof(T)));
-  float *scales = sums + 8 * NT * kTileN;                        // step_groups x 64
-  uint32_t *zeros = reinterpret_cast<uint32_t *>(scales + p.step_groups * kTileN);
+  uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
+  uint8_t *as = stages + kStages * kStageBytes;  // kStages x NT tiles
+  float *sums = reinterpret_cast<float *>(as + kStages * NT * kAStep);
   __shared__ Shared sh;
-  __shared__ int shrunk[8 * NT];  // rows whose A is taken kShrink times
 
   const int warp = static_cast<int>(warp_index()), lane = threadIdx.x & 31;
   const int tile = static_cast<int>(blockIdx.x) / p.split, rank = static_cast<int>(blockIdx.x) % p.split;
   const int g = blockIdx.y, n0 = tile * kTileN;
+  // What this launch reads but A was there before the one that makes A began
+  // (each launch lets the next one in behind its own wait).
+  long long r0, r1;
+  segment_of(p.offsets, g, p.M, &r0, &r1);
+  if (r0 >= r1) return;  // the whole cluster: it shares the segment
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -239,18 +303,8 @@ __global__ void __launch_bounds__(kThreads)
     tma_prefetch_map(&map);
   }
   __syncthreads();
-  grid_dependency_wait();
-  grid_launch_dependents();
-
-  long long r0 = 0, r1 = p.M;
-  if (p.offsets != nullptr) {
-    r0 = held(p.offsets[g], p.M);
-    r1 = held(p.offsets[g + 1], p.M);
-  }
-  if (r0 >= r1) return;  // the whole cluster: it shares the segment
-  const int blocks = (p.K + kBlockK - 1) / kBlockK;
-  const int b0 = static_cast<int>(static_cast<long long>(blocks) * rank / p.split);
-  const int b1 = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / p.split);
+  const int b0 = static_cast<int>(static_cast<long long>(p.blocks) * rank / p.split);
+  const int b1 = static_cast<int>(static_cast<long long>(p.blocks) * (rank + 1) / p.split);
 
   int stage = 0;
   uint32_t parity = 0;
@@ -260,20 +314,47 @@ __global__ void __launch_bounds__(kThreads)
       parity ^= 1u;
     }
   };
+  bool first = true;
 
   for (long long t0 = r0; t0 < r1; t0 += 8 * NT) {
+    const int used = static_cast<int>(r1 - t0 >= 8 * NT ? NT : (r1 - t0 + 7) / 8);  // tiles
     if (warp == kConsumers / 32) {
       if (lane == 0) {
-        int issued = 0;
-        for (int b = b0; b < b1; ++b) {
+        auto load_w = [&](int b) {
+          mbar_arrive_expect_tx(&sh.full[stage], kStageBytes + used * kABytes);
+          tma_load_3d(stages + stage * kStageBytes, &map, &sh.full[stage], b * (kBlockK / 2), n0,
+                      g * p.z_step);
+        };
+        auto load_a = [&](int b) {
+          const long long at = ((r0 / 8 + g + (t0 - r0) / 8) * p.blocks + b) * kAStep;
+          for (int i = 0; i < used; ++i) {
+            const long long from = at + static_cast<long long>(i) * p.blocks * kAStep;
+            bulk_load(as + (stage * NT + i) * kAStep, p.A + from, kABytes, &sh.full[stage]);
+          }
+        };
+        int b = b0, issued = 0;
+        if (first) {
+          // The first weights are on their way while A is being made.
+          for (; b < b1 && issued < kStages; ++b, ++issued) {
+            load_w(b);
+            next();
+          }
+          grid_dependency_wait();
+          grid_launch_dependents();
+          stage = 0;
+          parity = 0;
+          for (b = b0, issued = 0; b < b1 && issued < kStages; ++b, ++issued) {
+            load_a(b);
+            next();
+          }
+        }
+        for (; b < b1; ++b, ++issued) {
           if (!mbar_wait_bounded(&sh.empty[stage], parity ^ 1u, p.timeout_ns, &sh.abort,
                                  &g_w4_status))
             break;
-          mbar_arrive_expect_tx(&sh.full[stage], kStageBytes);
-          tma_load_3d(stages + stage * kStageBytes, &map, &sh.full[stage], b * (kBlockK / 2), n0,
-                      g * p.z_step);
+          load_w(b);
+          load_a(b);
           next();
-          ++issued;
         }
         if (sh.abort) {
           // Given up: the copies under way land before anyone leaves.
@@ -289,140 +370,102 @@ __global__ void __launch_bounds__(kThreads)
       parity = __shfl_sync(0xffffffffu, parity, 0);
     } else {
       const int row = warp * 16 + lane / 4, j = lane % 4, swz = row & 7;
-      float sum[NT][4] = {};
-      for (int ph0 = b0; ph0 < b1; ph0 += p.phase) {
-        const int ph1 = min(ph0 + p.phase, b1);
-        named_barrier_sync(1, kConsumers);  // the phase before is read
-        // A: rows t0 .. t0 + 8 NT, as fragments
-        const int units = (ph1 - ph0) * 32;
-        // (again: only the rows that are shrunk, or to see which are)
-        auto stage_a = [&](bool again, bool look) {
-          bool over = false;
-          for (int u = threadIdx.x; u < units * 8 * NT; u += kConsumers) {
-            const int token = u / units, k8 = u - token * units;  // k8: eight k
-            const long long t = t0 + token;
-            const long long k = static_cast<long long>(ph0) * kBlockK + k8 * 8;
-            if (again && !look && !shrunk[token]) continue;
-            uint4 v[kTerms];
+      // Scales and zeros of two rows, a block ahead of their use. (Rows and groups
+      // behind the last take its values: their products are not kept, or zero.)
+      const long long n_lo = min(n0 + row, p.N - 1), n_hi = min(n0 + row + 8, p.N - 1);
+      float s_next[kTimes][2];
+      uint32_t z_next[kTimes][2];
+      auto fetch = [&](int b) {
 #pragma unroll
-            for (int i = 0; i < kTerms; ++i) v[i] = make_uint4(0, 0, 0, 0);
-            if (t < r1 && k < p.K) {
-              const long long left = p.K - k;
-              const bool big = load8<T>(p, t * p.lda + k, left < 8 ? static_cast<int>(left) : 8,
-                                        again && !look, v);
-              over |= big;
-              if (look && big) shrunk[token] = 1;
-            }
-            if (look) continue;
+        for (int c = 0; c < kTimes; ++c) {
+          const unsigned at = static_cast<unsigned>(b) * kTimes + c;
+          const int gi = min(static_cast<int>(p.per_group == 1 ? at : at / p.per_group), p.row_groups - 1);
 #pragma unroll
-            for (int i = 0; i < kTerms; ++i)
-              *reinterpret_cast<uint4 *>(
-                  as + (((k8 / 4 * NT + token / 8) * kTerms + i) * 32 + token % 8 * 4 + k8 % 4) * 16) = v[i];
-          }
-          return over;
-        };
-        const bool over = stage_a(false, false);
-        // scales and zeros of the groups that the phase meets
-        const int g0 = ph0 * kBlockK / p.group;
-        const int count = min((ph1 * kBlockK - 1) / p.group + 1, p.row_groups) - g0;
-        for (int u = threadIdx.x; u < p.step_groups * kTileN; u += kConsumers) {
-          const int r = u % kTileN, at = u / kTileN;
-          float s = 0.0f;
-          uint32_t z = 8;
-          if (at < count && n0 + r < p.N) {
-            const long long i = g * p.strides + (n0 + r) * p.lds + g0 + at;
-            if (index_ok(kSiteLoadB, i, 1, p.s_extent))
-              s = static_cast<float>(static_cast<const T *>(p.scales)[i]);
+          for (int h = 0; h < 2; ++h) {
+            const long long n = h == 0 ? n_lo : n_hi;
+            const long long i = g * p.strides + n * p.lds + gi;
+            s_next[c][h] = index_ok(kSiteLoadB, i, 1, p.s_extent)
+                               ? static_cast<float>(__ldg(static_cast<const T *>(p.scales) + i)) : 0.0f;
+            z_next[c][h] = 8;
             if (p.zeros != nullptr) {
-              const long long iz = g * p.stridez + (n0 + r) * p.ldz + g0 + at;
-              if (index_ok(kSiteLoadB, iz, 1, p.z_extent)) z = p.zeros[iz] & 15u;
+              const long long iz = g * p.stridez + n * p.ldz + gi;
+              if (index_ok(kSiteLoadB, iz, 1, p.z_extent)) z_next[c][h] = __ldg(p.zeros + iz) & 15u;
             }
           }
-          scales[u] = s;
-          zeros[u] = 0x43004300u | z | z << 16;
         }
-        const bool plain = named_barrier_and(1, kConsumers, !over);
-        if (!plain) {
-          if (threadIdx.x < 8 * NT) shrunk[threadIdx.x] = 0;
-          named_barrier_sync(1, kConsumers);
-          stage_a(true, true);
-          named_barrier_sync(1, kConsumers);
-          stage_a(true, false);
-          named_barrier_sync(1, kConsumers);
-        }
-        const int per_group = p.group / 32;
-        int at_group = 0, in_group = ph0 * 8 - g0 * per_group;
-        for (int b = ph0; b < ph1; ++b) {
-          mbar_wait_bounded(&sh.full[stage], parity, p.timeout_ns, &sh.abort, &g_w4_status);
-          const uint8_t *w0 = stages + stage * kStageBytes + row * 128 + j * 4;
-          const uint8_t *ab = as + (b - ph0) * a_block_bytes(NT, sizeof(T)) + lane * 16;
-          float part[NT][4] = {};
-          int since = 0;
+      };
+      float sum[NT][4] = {};
+      if (b0 < b1) fetch(b0);
+      for (int b = b0; b < b1; ++b) {
+        float s[kTimes][2];
+        uint32_t z[kTimes][2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+        for (int c = 0; c < kTimes; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            s[c][h] = s_next[c][h];
+            z[c][h] = 0x43004300u | z_next[c][h] | z_next[c][h] << 16;
+          }
+        if (b + 1 < b1) fetch(b + 1);
+        mbar_wait_bounded(&sh.full[stage], parity, p.timeout_ns, &sh.abort, &g_w4_status);
+        const uint8_t *w0 = stages + stage * kStageBytes + row * 128 + j * 4;
+        const uint8_t *ab = as + stage * NT * kAStep;
+        float2 grow[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          grow[nt] = *reinterpret_cast<const float2 *>(ab + nt * kAStep + kTerms * 4096 + j * 8);
+#pragma unroll
+        for (int c = 0; c < kTimes; ++c) {
+          float part[NT][2][4] = {};  // two sums, so that one's MMA need not wait for the other's
+#pragma unroll
+          for (int i = c * PERIOD; i < (c + 1) * PERIOD; ++i) {
             const uint32_t lo = *reinterpret_cast<const uint32_t *>(w0 + ((i ^ swz) << 4));
             const uint32_t hi = *reinterpret_cast<const uint32_t *>(w0 + 8 * 128 + ((i ^ swz) << 4));
-            const uint32_t zlo = zeros[at_group * kTileN + row];
-            const uint32_t zhi = zeros[at_group * kTileN + row + 8];
-            const uint32_t f0[4] = {pair_of<0>(lo, zlo), pair_of<0>(hi, zhi), pair_of<1>(lo, zlo),
-                                    pair_of<1>(hi, zhi)};
-            const uint32_t f1[4] = {pair_of<2>(lo, zlo), pair_of<2>(hi, zhi), pair_of<3>(lo, zlo),
-                                    pair_of<3>(hi, zhi)};
+            const uint32_t f0[4] = {pair_of<0>(lo, z[c][0]), pair_of<0>(hi, z[c][1]),
+                                    pair_of<1>(lo, z[c][0]), pair_of<1>(hi, z[c][1])};
+            const uint32_t f1[4] = {pair_of<2>(lo, z[c][0]), pair_of<2>(hi, z[c][1]),
+                                    pair_of<3>(lo, z[c][0]), pair_of<3>(hi, z[c][1])};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+              if (nt >= used) continue;
 #pragma unroll
               for (int t = kTerms - 1; t >= 0; --t) {  // small terms first
-                const uint4 x = *reinterpret_cast<const uint4 *>(ab + ((i * NT + nt) * kTerms + t) * 512);
-                mma(part[nt], f0, x.x, x.y);
-                mma(part[nt], f1, x.z, x.w);
+                const uint4 x = *reinterpret_cast<const uint4 *>(ab + nt * kAStep +
+                                                                 (i * kTerms + t) * 512 + lane * 16);
+                mma(part[nt][0], f0, x.x, x.y);
+                mma(part[nt][1], f1, x.z, x.w);
               }
-            if (++since == p.period) {
-              const float s0 = scales[at_group * kTileN + row], s1 = scales[at_group * kTileN + row + 8];
-              if (!plain) {
-                // rows that are shrunk; the others as ever
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int c = 0; c < 2; ++c)
-                    if (shrunk[nt * 8 + 2 * j + c]) {
-                      sum[nt][c] = fmaf(s0 * part[nt][c], kGrow, sum[nt][c]);
-                      sum[nt][c + 2] = fmaf(s1 * part[nt][c + 2], kGrow, sum[nt][c + 2]);
-                      part[nt][c] = part[nt][c + 2] = 0.0f;
-                    }
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                sum[nt][0] = fmaf(s0, part[nt][0], sum[nt][0]);
-                sum[nt][1] = fmaf(s0, part[nt][1], sum[nt][1]);
-                sum[nt][2] = fmaf(s1, part[nt][2], sum[nt][2]);
-                sum[nt][3] = fmaf(s1, part[nt][3], sum[nt][3]);
-                part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.0f;
-              }
-              since = 0;
-            }
-            if (++in_group == per_group) {
-              in_group = 0;
-              ++at_group;
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.empty[stage]);
-          next();
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (nt >= used) continue;
+            const float(&a)[4] = part[nt][0], (&d)[4] = part[nt][1];
+            sum[nt][0] = fmaf(s[c][0] * grow[nt].x, a[0] + d[0], sum[nt][0]);
+            sum[nt][1] = fmaf(s[c][0] * grow[nt].y, a[1] + d[1], sum[nt][1]);
+            sum[nt][2] = fmaf(s[c][1] * grow[nt].x, a[2] + d[2], sum[nt][2]);
+            sum[nt][3] = fmaf(s[c][1] * grow[nt].y, a[3] + d[3], sum[nt][3]);
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        next();
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float *s = sums + (nt * 8 + 2 * j) * kTileN + row;
-        s[0] = sum[nt][0];
-        s[kTileN] = sum[nt][1];
-        s[8] = sum[nt][2];
-        s[kTileN + 8] = sum[nt][3];
+        float *to = sums + (nt * 8 + 2 * j) * kTileN + row;
+        to[0] = sum[nt][0];
+        to[kTileN] = sum[nt][1];
+        to[8] = sum[nt][2];
+        to[kTileN + 8] = sum[nt][3];
       }
     }
+    if (first) grid_dependency_wait();
+    first = false;
     // All parts of the tile are there (cluster); this CTA's share of them.
     if (p.split > 1) cluster_sync();
     else __syncthreads();
-    const int all = 8 * NT * kTileN;
+    const int all = 8 * used * kTileN;
     const int e0 = all * rank / p.split, e1 = all * (rank + 1) / p.split;
     for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += kThreads) {
       const long long t = t0 + e / kTileN;
@@ -579,23 +622,21 @@ int launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? kOk : kErrLaunch;
 }
 
+template <class T, int NT, int PERIOD>
+int launch_period(const CUtensorMap &map, const P &p, int groups, cudaStream_t stream) {
+  const int tiles = (p.N + kTileN - 1) / kTileN;
+  const size_t smem = 1024 + kStages * (kStageBytes + NT * a_step(sizeof(T))) + 8 * NT * kTileN * 4;
+  return launch(w4_kernel<T, NT, PERIOD>,
+                dim3(static_cast<unsigned>(tiles * p.split), static_cast<unsigned>(groups), 1), kThreads,
+                smem, p.split, stream, map, p);
+}
+
 template <class T, int NT>
-int launch_nt(const CUtensorMap &map, P &p, int sms, cudaStream_t stream) {
-  const int tiles = (p.N + kTileN - 1) / kTileN, blocks = (p.K + kBlockK - 1) / kBlockK;
-  const int used = p.groups < p.M ? p.groups : p.M;  // segments with rows, at most
-  p.split = 1;
-  while (p.split < kMaxSplit && 4 * p.split <= blocks &&
-         static_cast<int64_t>(tiles) * used * p.split < 2 * sms)
-    p.split *= 2;
-  const int own = (blocks + p.split - 1) / p.split;
-  const int room = 32 * 1024 / a_block_bytes(NT, sizeof(T));
-  p.phase = own < room ? own : (room < 1 ? 1 : room);
-  p.step_groups = (p.phase * kBlockK + p.group - 1) / p.group + 1;
-  const size_t smem = 1024 + kStages * kStageBytes +
-                      static_cast<size_t>(p.phase) * a_block_bytes(NT, sizeof(T)) +
-                      8 * NT * kTileN * 4 + static_cast<size_t>(p.step_groups) * kTileN * 8;
-  return launch(w4_kernel<T, NT>, dim3(static_cast<unsigned>(tiles * p.split), static_cast<unsigned>(p.groups), 1),
-                kThreads, smem, p.split, stream, map, p);
+int launch_nt(const CUtensorMap &map, const P &p, int groups, int64_t group, cudaStream_t stream) {
+  if (group % 256 == 0) return launch_period<T, NT, 8>(map, p, groups, stream);
+  if (group % 128 == 0) return launch_period<T, NT, 4>(map, p, groups, stream);
+  if (group % 64 == 0) return launch_period<T, NT, 2>(map, p, groups, stream);
+  return launch_period<T, NT, 1>(map, p, groups, stream);
 }
 
 }  // namespace
@@ -632,10 +673,6 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
     return kErrLaunch;
   const int elem = a.bf16 ? 2 : 4;
   P p = {};
-  p.A = a.A;
-  p.lda = a.lda;
-  p.a_extent = matrix_extent(a.M, a.K, a.lda);
-  p.a_vec = reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && a.lda * elem % 16 == 0;
   p.row_groups = static_cast<int>((a.K + a.group - 1) / a.group);
   p.scales = a.scales;
   p.lds = a.lds;
@@ -649,23 +686,56 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
   p.ldc = a.ldc;
   p.c_extent = matrix_extent(a.M, a.N, a.ldc);
   p.offsets = a.offsets;
-  p.groups = static_cast<int>(a.groups);
   p.z_step = stack ? 1 : 0;
   p.M = static_cast<int>(a.M);
   p.N = static_cast<int>(a.N);
   p.K = static_cast<int>(a.K);
-  p.group = static_cast<int>(a.group);
-  p.period = a.group % 128 == 0 ? 4 : (a.group % 64 == 0 ? 2 : 1);
+  p.blocks = static_cast<int>((a.K + kBlockK - 1) / kBlockK);
+  int period = 8;
+  while (a.group % (32 * period) != 0) period /= 2;
+  p.per_group = static_cast<int>(a.group / (32 * period));
   p.timeout_ns = 2000000000ull + 2000ull * static_cast<unsigned long long>(a.K);
-  // Rows at a time: what a segment has on average; others take several turns.
+  const int64_t tiles = (a.N + kTileN - 1) / kTileN;
+  const int64_t used = a.groups < a.M ? a.groups : a.M;  // segments with rows, at most
+  p.split = 1;
+  while (p.split < kMaxSplit && 8 * p.split <= p.blocks && tiles * used * p.split < 4 * sm_count)
+    p.split *= 2;
+
+  Prep q = {};
+  q.A = a.A;
+  q.lda = a.lda;
+  q.a_extent = matrix_extent(a.M, a.K, a.lda);
+  q.a_vec = reinterpret_cast<uintptr_t>(a.A) % 16 == 0 && a.lda * elem % 16 == 0;
+  q.offsets = a.offsets;
+  q.M = p.M;
+  q.K = p.K;
+  q.blocks = p.blocks;
+  q.to_extent = (a.M / 8 + a.groups + 1) * p.blocks * a_step(elem);
+  void *ws = nullptr;
+  int st = pool_alloc(&ws, static_cast<size_t>(q.to_extent), stream);
+  if (st != kOk) return st;
+  q.to = static_cast<uint8_t *>(ws);
+  p.A = q.to;
+  p.a_extent = q.to_extent;
   const int64_t average = (a.M + a.groups - 1) / a.groups;
-  if (a.bf16) {
-    if (average <= 8) return launch_nt<__nv_bfloat16, 1>(map, p, sm_count, stream);
-    if (average <= 16) return launch_nt<__nv_bfloat16, 2>(map, p, sm_count, stream);
-    return launch_nt<__nv_bfloat16, 4>(map, p, sm_count, stream);
+  const int64_t prep = (average + 7) / 8 * 8 * p.blocks / kPrepWarps + 1;
+  const dim3 grid(static_cast<unsigned>(prep < 4096 ? prep : 4096), static_cast<unsigned>(a.groups), 1);
+  st = a.bf16 ? launch(w4_prep_kernel<__nv_bfloat16>, grid, 32 * kPrepWarps, 0, 1, stream, q)
+              : launch(w4_prep_kernel<float>, grid, 32 * kPrepWarps, 0, 1, stream, q);
+  // Rows at a time: what a segment has on average, or (few more instructions) twice
+  // that; others take several turns.
+  const int groups = static_cast<int>(a.groups);
+  if (st == kOk) {
+    if (a.bf16)
+      st = a.M <= 8 || average <= 2 ? launch_nt<__nv_bfloat16, 1>(map, p, groups, a.group, stream)
+           : average <= 12          ? launch_nt<__nv_bfloat16, 2>(map, p, groups, a.group, stream)
+                                    : launch_nt<__nv_bfloat16, 4>(map, p, groups, a.group, stream);
+    else
+      st = a.M <= 8 || average <= 2 ? launch_nt<float, 1>(map, p, groups, a.group, stream)
+                                    : launch_nt<float, 2>(map, p, groups, a.group, stream);
   }
-  if (average <= 8) return launch_nt<float, 1>(map, p, sm_count, stream);
-  return launch_nt<float, 2>(map, p, sm_count, stream);
+  const int fst = pool_free(ws, stream);
+  return st != kOk ? st : fst;
 }
 
 int w4_pack_launch(const W4Args &a, uint8_t *dst, int64_t ldd, int64_t strided, int sm_count,
