@@ -3,26 +3,37 @@
 //   C[t, n] = sum_k A[t, k] W[n, k],   W[n, k] = s[n, k / group] (q[n, k] - z[n, k / group])
 //
 // With few rows the product is a reading of the weights: half a byte each, and
-// its time that of memory as long as nothing else takes longer. What the kernel
-// does about that:
+// its time that of memory as long as nothing else takes longer. Two things could:
+// making operands of nibbles, and multiplying them.
 //
-//   * Weights come by TMA, 64 rows of 128 bytes (256 k) a stage, swizzled so that
-//     the eight rows of a fragment lie in eight different groups of four banks.
-//   * q - z is an integer that bf16 holds exactly. It is made by two logic
-//     operations and one subtraction for two values: the nibbles q of a word, in
-//     pairs 16 bits apart, become 128 + q by setting the bits above them, and 128
-//     + z is taken away. mma.sync multiplies them with A (16 n by 8 rows by 16 k),
-//     exactly, adding in fp32; the scales meet the sums, not the weights: at the
-//     end of each group, at most 128 k, in fp32 registers. So no rounding of a
-//     weight enters, and sums in the tensor core, which truncate, stay short.
-//   * tcgen05 has nothing to give here: its smallest tile of lanes is 128 n, its
-//     operands would have to go back to shared memory as bf16, four times the
-//     bytes that came, and with eight rows an MMA of 16 x 8 x 16 a warp is enough
-//     (one for every 2.7 KB that memory delivers).
-//   * A stands in shared memory in the order of the fragments, which is that of
-//     the nibbles: k in blocks of 32, lane j of four holding 8 neighbours as the
-//     pairs (0, 4), (1, 5), (2, 6), (3, 7). fp32 values are three bf16 terms.
-//   * Few tiles: the CTAs of a cluster share k, and add their sums from each
+//   * 128 rows of W are the lanes of a tcgen05 tile, the rows of A its columns.
+//     (mma.sync multiplies 256 products a clock of an SM here, measured: at 8 rows
+//     a third less than memory delivers; the first form of this kernel spent 83 %
+//     of its time in it.)
+//   * A bf16 whose upper eight bits are zero is its lower eight times 2^-133 (the
+//     subnormals and the first normal values are one line). So the nibbles of a
+//     word, in pairs 16 bits apart, are operands as they are, q 2^-133 where they
+//     are the lowest four bits and 16 q 2^-133 above: five operations of the
+//     integer lanes for eight weights (memory at full speed brings 47 weights a
+//     clock of an SM, its integer lanes do 64 operations). A is scaled by 2^110,
+//     and by 2^106 where it meets the upper nibbles, to meet them in the middle of
+//     fp32's range; rows with values from 2^16 on by less.
+//   * sum s (q - z) a = s (sum q a - z sum a): the sums of A are made with A, a
+//     term each, and are about as exact as the tensor core's, so that where q = z
+//     nearly nothing is left.
+//   * A thread makes a row's operands out of shared memory and stores them to TMEM,
+//     where the tensor core reads them; shared memory would be written and read at
+//     4 times the bytes.
+//   * Scales and zeros meet the sums, in fp32, at the end of each group, at most
+//     128 k: no weight is rounded, and sums in the tensor core, which truncate,
+//     stay short. They are a value a thread.
+//   * Two warpgroups take 128 k in turn, each with its own operand and accumulator
+//     in TMEM: one makes operands while the other's are multiplied.
+//   * A comes as the tensor core reads it (w4_prep_kernel, once a call): its k in
+//     the order of the nibble pairs (0, 4), (1, 5), (2, 6), (3, 7); fp32 values as
+//     three bf16 terms, each a column.
+//   * Weights come by TMA, 128 rows of 256 k a stage, A by plain bulk copies.
+//     Few tiles: the CTAs of a cluster share k, and add their sums from each
 //     other's shared memory in the order of their ranks.
 
 #include <cuda.h>
@@ -31,23 +42,28 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
-#include "ptx.cuh"
+#include "seg_ptx.cuh"
 #include "w4.h"
 
 namespace gemm {
 namespace {
 
-constexpr int kTileN = 64, kBlockK = 256, kStages = 4;
-constexpr int kStageBytes = kTileN * kBlockK / 2;
-constexpr int kConsumers = 128, kThreads = kConsumers + 32;
+constexpr int kTileN = 128, kBlockK = 256;
+constexpr int kWBytes = kTileN * kBlockK / 2;  // of a stage
+constexpr int kGroups = 2, kMakers = 128 * kGroups, kMakerWarps = kMakers / 32;  // make operands
+constexpr int kProducer = kMakerWarps, kMma = kMakerWarps + 1;         // warps
+constexpr int kThreads = kMakers + 64;
 constexpr int kMaxSplit = 8;
 
 __device__ int g_w4_status;  // first error recorded by a kernel of this unit
 
-// A as fragments: for each tile of 8 rows and each block of 256 k, `terms` bf16
-// terms and the 8 rows' factors. A segment's tiles follow each other from
-// tile r0 / 8 + g on (r0: its first row, g: its number), which no two share.
+// A as operands: for each tile of rows and each block of 256 k, four panels of 64
+// k (a line of 128 bytes for each row and term, swizzled); a byte a row, load8's
+// exponent; and the sums of the row's terms between two times that scales are
+// applied. A segment's tiles follow each other from tile r0 / rows + g on (r0: its
+// first row, g: its number), which no two segments share.
 struct Prep {
   const void *A;
   uint8_t *to;
@@ -62,7 +78,7 @@ struct P {
   const uint8_t *zeros;
   void *C;
   const int64_t *offsets;
-  long long a_extent, lds, strides, s_extent, ldz, stridez, z_extent, ldc, c_extent;
+  long long lds, strides, s_extent, ldz, stridez, z_extent, ldc, c_extent;
   int M, N, K, row_groups;
   int blocks, split;  // of k; CTAs that share them
   int per_group;      // times that the scales are applied to a group
@@ -71,9 +87,42 @@ struct P {
 };
 
 struct Shared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full_w[4], full_a[4], empty[4];  // stages, at most
+  uint64_t made[kGroups], multiplied[kGroups], drain;
+  uint32_t tmem;
   int abort, drain_abort;
 };
+
+// As mbar_wait_bounded, but asleep between looks (up to kNap ns each) instead of
+// looking again at once: what waits here leaves the issue slots to the warps that
+// make operands.
+constexpr uint32_t kNap = 20000;
+__device__ __forceinline__ bool nap_wait(uint64_t *bar, uint32_t parity, uint64_t timeout_ns,
+                                         volatile int *abort, int *status) {
+  const uint32_t a = smem_addr(bar);
+  auto look = [&] {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(a), "r"(parity), "r"(kNap)
+        : "memory");
+    return done != 0;
+  };
+  if (look()) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!look()) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > timeout_ns) {
+      *abort = 1;
+      atomicCAS(status, 0, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
 
 // 1-D copy into this CTA's shared memory.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
@@ -94,23 +143,21 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
       : "memory");
 }
 
-// D += A B: A 16 x 16, B 16 x 8, bf16, fp32 sums.
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
+// D[tmem] (+)= A[tmem] B[smem]^T, kind::f16 with bf16 operands, 128 lanes.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
-// Nibbles i and i + 4 of a word, less z, as two bf16.
-template <int I>
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t zero) {
-  const uint32_t v = (w >> (4 * I) & 0x000f000fu) | 0x43004300u;  // 128 + q
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162 *>(&zero));
-  return *reinterpret_cast<const uint32_t *>(&d);
+// Instruction descriptor of kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits
+// 7-9 and 10-12 = 1), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t m, uint32_t n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 __device__ __forceinline__ float read_cluster(uint32_t addr, uint32_t rank) {
@@ -121,95 +168,79 @@ __device__ __forceinline__ float read_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t bits(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
 
-// A's values from 2^113 on (and infinities, NaN) could leave fp32's range in a sum
-// of 256 products with up to 15, although their products with the weights do
-// not. A row's block of k with such values is taken 2^-16 times, and its sums
-// 2^16 times.
-constexpr float kShrink = 0x1p-16f, kGrow = 0x1p16f;
+// Exponents of A's scaling (powers of two): kScale as long as a row's 256 values
+// are below 2^16 (biased exponent kLargest); else, that of the largest of them
+// above kLargest less. Sums are of units of 2^-133.
+constexpr int kScale = 110, kUnit = 133, kLargest = 127 + 15;
 
-// Whether a word's two bf16 (or its fp32: the upper) have an exponent of 240 or more.
-__device__ __forceinline__ uint32_t large(uint32_t u) {
-  const uint32_t t = u & u << 1;
-  return t & t << 2;
+__device__ __forceinline__ float power(int e) {  // 2^e, e in -126 .. 127
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
-// Eight neighbouring k of a row, in the fragments' order, term by term; *shrink:
-// kShrink times, for one of the warp's 256 is large.
+// Eight neighbouring k of a row as operands, term by term, and their sums, those
+// of A's scaled values times 2^-kUnit; returns the biased exponent of the warp's
+// 256 values' largest where it is above kLargest, else 0.
 template <class T>
-__device__ __forceinline__ void load8(const Prep &p, long long at, int left, bool *shrink,
-                                      uint4 (&out)[sizeof(T) == 2 ? 1 : 3]) {
+__device__ __forceinline__ int load8(const Prep &p, long long at, int left,
+                                     uint4 (&out)[sizeof(T) == 2 ? 1 : 3],
+                                     float (&sum)[sizeof(T) == 2 ? 1 : 3]) {
+  constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
   const T *a = static_cast<const T *>(p.A) + at;
-  if constexpr (sizeof(T) == 2) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (left >= 8 && p.a_vec) {
-      if (index_ok(kSiteLoadA, at, 8, p.a_extent)) v = __ldg(reinterpret_cast<const uint4 *>(a));
-    } else {
-      uint32_t h[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        h[i] = i < left && index_ok(kSiteLoadA, at + i, 1, p.a_extent) ? bits(a[i]) : 0u;
-      v = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    }
-    const uint32_t big = large(v.x) | large(v.y) | large(v.z) | large(v.w);
-    *shrink = __any_sync(0xffffffffu, (big & 0x40004000u) != 0);
-    if (*shrink) {
-      const __nv_bfloat162 f = __float2bfloat162_rn(kShrink);
-      uint32_t *u = &v.x;
+  float v[8];
+  if (left >= 8 && p.a_vec && index_ok(kSiteLoadA, at, 8, p.a_extent)) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(a));
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(u + i), f);
-        u[i] = *reinterpret_cast<const uint32_t *>(&h);
-      }
-    }
-    out[0] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                        __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-  } else {
-    float v[8];
-    if (left >= 8 && p.a_vec) {
-      float4 f[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-      if (index_ok(kSiteLoadA, at, 8, p.a_extent)) {
-        f[0] = __ldg(reinterpret_cast<const float4 *>(a));
-        f[1] = __ldg(reinterpret_cast<const float4 *>(a) + 1);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        v[4 * i] = f[i].x;
-        v[4 * i + 1] = f[i].y;
-        v[4 * i + 2] = f[i].z;
-        v[4 * i + 3] = f[i].w;
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = i < left && index_ok(kSiteLoadA, at + i, 1, p.a_extent) ? a[i] : 0.0f;
+      for (int i = 0; i < 2; ++i) {
+        const float4 f = __ldg(reinterpret_cast<const float4 *>(a) + i);
+        v[4 * i] = f.x;
+        v[4 * i + 1] = f.y;
+        v[4 * i + 2] = f.z;
+        v[4 * i + 3] = f.w;
+      }
     }
-    uint32_t big = 0;
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) big |= large(__float_as_uint(v[i]));
-    *shrink = __any_sync(0xffffffffu, (big & 0x40000000u) != 0);
-    if (*shrink)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= kShrink;
-    uint32_t h[3][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // Of an infinite value there is no second term. (What is finite is far from
-      // bf16's end: shrunk, if it was not.)
-      const __nv_bfloat16 t0 = __float2bfloat16_rn(v[i]);
-      const float r1 = isinf(v[i]) ? 0.0f : v[i] - __bfloat162float(t0);
-      const __nv_bfloat16 t1 = __float2bfloat16_rn(r1);
-      const __nv_bfloat16 t2 = __float2bfloat16_rn(r1 - __bfloat162float(t1));
-      h[0][i] = bits(t0);
-      h[1][i] = bits(t1);
-      h[2][i] = bits(t2);
-    }
-#pragma unroll
-    for (int t = 0; t < 3; ++t)
-      out[t] = make_uint4(h[t][0] | h[t][4] << 16, h[t][1] | h[t][5] << 16,
-                          h[t][2] | h[t][6] << 16, h[t][3] | h[t][7] << 16);
+    for (int i = 0; i < 8; ++i)
+      v[i] = i < left && index_ok(kSiteLoadA, at + i, 1, p.a_extent) ? static_cast<float>(a[i]) : 0.0f;
   }
+  unsigned e = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e = max(e, __float_as_uint(v[i]) >> 23 & 0xffu);
+  e = __reduce_max_sync(0xffffffffu, e);
+  const int large = static_cast<int>(e) > kLargest ? static_cast<int>(e) : 0;
+  const float scale = power(large != 0 ? kScale + kLargest - large : kScale);
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) sum[t] = 0.0f;
+  uint32_t h[kTerms][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float rest = v[i] * scale;
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      const __nv_bfloat16 term = __float2bfloat16_rn(rest);
+      const float f = __bfloat162float(term);
+      sum[t] += f * 0x1p-100f;
+      // its odd k meet the nibbles that are 16 q
+      h[t][i] = __bfloat16_as_ushort(__float2bfloat16_rn(i & 1 ? f * 0.0625f : f));
+      rest = isinf(f) ? 0.0f : rest - f;  // of infinity there is no second term
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    sum[t] *= 0x1p-33f;
+    out[t] = make_uint4(h[t][0] | h[t][4] << 16, h[t][1] | h[t][5] << 16, h[t][2] | h[t][6] << 16,
+                        h[t][3] | h[t][7] << 16);
+  }
+  return large;
 }
 
 template <class T>
@@ -222,9 +253,18 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) {
 }
 
 __host__ __device__ constexpr int terms_of(int elem) { return elem == 2 ? 1 : 3; }
-// Bytes of A for a tile of 8 rows and a block of k, and from one to the next.
-__host__ __device__ constexpr int a_bytes(int elem) { return kBlockK * 8 * 2 * terms_of(elem) + 32; }
-__host__ __device__ constexpr int a_step(int elem) { return a_bytes(elem) + 96; }
+
+// A tile of rows: COLS columns of the tensor core (a multiple of 16), a column for
+// each term of a row; the scales are applied every PERIOD steps of 32 k.
+template <class T, int COLS, int PERIOD>
+struct Tile {
+  static constexpr int kTerms = terms_of(sizeof(T)), kRows = COLS / kTerms;
+  static constexpr int kTimes = 8 / PERIOD;  // of a block of 256 k
+  static constexpr int kPanel = COLS * 128;
+  static constexpr int kFlags = 4 * kPanel, kSums = kFlags + (kRows <= 16 ? 16 : kRows);
+  static constexpr int kBytes = kSums + (kTimes * kTerms * kRows * 4 + 15) / 16 * 16;  // of a block
+  static constexpr int kStep = (kBytes + 1023) / 1024 * 1024;  // from one to the next
+};
 
 __device__ __forceinline__ long long held(long long a, long long m) {
   return a < 0 ? 0 : (a > m ? m : a);
@@ -243,46 +283,64 @@ __device__ __forceinline__ void segment_of(const int64_t *offsets, int g, int M,
 constexpr int kPrepWarps = 4;
 
 // A warp takes a block of k of a row: once for all CTAs that will read it.
-template <class T>
+template <class T, int COLS, int PERIOD>
 __global__ void __launch_bounds__(32 * kPrepWarps) w4_prep_kernel(const Prep p) {
-  constexpr int kTerms = terms_of(sizeof(T));
+  using A = Tile<T, COLS, PERIOD>;
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, g = blockIdx.y;
   long long r0, r1;
   segment_of(p.offsets, g, p.M, &r0, &r1);
   if (r0 >= r1) return;
-  const long long rows = (r1 - r0 + 7) / 8 * 8;  // the last tile's absent rows are zero
+  const long long rows = (r1 - r0 + A::kRows - 1) / A::kRows * A::kRows;  // absent rows are zero
   for (long long u = static_cast<long long>(blockIdx.x) * kPrepWarps + threadIdx.x / 32;
        u < rows * p.blocks; u += static_cast<long long>(gridDim.x) * kPrepWarps) {
     const long long r = u / p.blocks;
-    const int b = static_cast<int>(u - r * p.blocks), token = static_cast<int>(r & 7);
+    const int b = static_cast<int>(u - r * p.blocks), row = static_cast<int>(r % A::kRows);
     const long long k = static_cast<long long>(b) * kBlockK + lane * 8;
     const long long left = r0 + r < r1 ? p.K - k : 0;
-    uint4 v[kTerms];
-    bool shrink;
-    load8<T>(p, (r0 + r) * p.lda + k, left < 8 ? static_cast<int>(left) : 8, &shrink, v);
-    const long long to = ((r0 / 8 + g + r / 8) * p.blocks + b) * a_step(sizeof(T));
-    if (!index_ok(kSitePartialWrite, to, a_bytes(sizeof(T)), p.to_extent)) continue;
+    uint4 v[A::kTerms];
+    float sum[A::kTerms];
+    const int large = load8<T>(p, (r0 + r) * p.lda + k, left < 8 ? static_cast<int>(left) : 8, v, sum);
 #pragma unroll
-    for (int i = 0; i < kTerms; ++i)
-      *reinterpret_cast<uint4 *>(p.to + to +
-                                 ((lane / 4 * kTerms + i) * 32 + token * 4 + lane % 4) * 16) = v[i];
-    if (lane == 0)
-      *reinterpret_cast<float *>(p.to + to + kTerms * 4096 + token * 4) = shrink ? kGrow : 1.0f;
+    for (int i = 0; i < A::kTerms; ++i)
+#pragma unroll
+      for (int d = 1; d < 4 * PERIOD; d *= 2) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+    const long long to = ((r0 / A::kRows + g + r / A::kRows) * p.blocks + b) * A::kStep;
+    if (!index_ok(kSitePartialWrite, to, A::kBytes, p.to_extent)) continue;
+    uint8_t *panel = p.to + to + lane / 8 * A::kPanel;
+    float *sums = reinterpret_cast<float *>(p.to + to + A::kSums);
+#pragma unroll
+    for (int i = 0; i < A::kTerms; ++i) {
+      const int line = i * A::kRows + row;
+      *reinterpret_cast<uint4 *>(panel + line * 128 + ((lane % 8 ^ (line & 7)) << 4)) = v[i];
+      if (lane % (4 * PERIOD) == 0)
+        sums[(lane / (4 * PERIOD) * A::kTerms + i) * A::kRows + row] = sum[i];
+    }
+    if (lane == 0) p.to[to + A::kFlags + row] = static_cast<uint8_t>(large);
   }
 }
 
-// NT tiles of 8 rows at a time; the scales meet the sums every PERIOD steps of 32 k.
-template <class T, int NT, int PERIOD>
-__global__ void __launch_bounds__(kThreads)
+// Columns of TMEM: an operand (128 k, two a column) for each warpgroup, and its
+// accumulators, one for each time that the scales are applied.
+__host__ __device__ constexpr int tmem_columns(int cols, int times) {
+  return kGroups * (64 + cols * times) <= 256 ? 256 : 512;
+}
+
+// Stages: what shared memory has room for, twice an SM up to 32 columns.
+__host__ __device__ constexpr int stages_of(int cols) { return cols == 32 || cols == 96 ? 3 : 4; }
+
+// The scales meet the sums every PERIOD steps of 32 k.
+template <class T, int COLS, int PERIOD>
+__global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 / PERIOD) == 256 ? 2 : 1)
     w4_kernel(const __grid_constant__ CUtensorMap map, const P p) {
-  constexpr int kTerms = terms_of(sizeof(T)), kABytes = a_bytes(sizeof(T)), kAStep = a_step(sizeof(T));
-  constexpr int kTimes = 8 / PERIOD;  // of a block
+  using A = Tile<T, COLS, PERIOD>;
+  constexpr int kTimes = A::kTimes / kGroups, kColumns = tmem_columns(COLS, kTimes), kStages = stages_of(COLS);
   extern __shared__ uint8_t raw[];
-  uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
-  uint8_t *as = stages + kStages * kStageBytes;  // kStages x NT tiles
-  float *sums = reinterpret_cast<float *>(as + kStages * NT * kAStep);
+  uint8_t *ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
+  uint8_t *as = ws + kStages * kWBytes;
+  // the warpgroups' sums of a tile, when all stages have been used
+  float *sums = reinterpret_cast<float *>(ws);
   __shared__ Shared sh;
 
   const int warp = static_cast<int>(warp_index()), lane = threadIdx.x & 31;
@@ -295,42 +353,55 @@ __global__ void __launch_bounds__(kThreads)
   if (r0 >= r1) return;  // the whole cluster: it shares the segment
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], kConsumers / 32);
+      mbar_init(&sh.full_w[i], 1);
+      mbar_init(&sh.full_a[i], 1);
+      mbar_init(&sh.empty[i], kMakerWarps + 1);
     }
+    for (int i = 0; i < kGroups; ++i) {
+      mbar_init(&sh.made[i], 4);
+      mbar_init(&sh.multiplied[i], 1);
+    }
+    mbar_init(&sh.drain, 1);
     sh.abort = sh.drain_abort = 0;
     fence_barrier_init();
     tma_prefetch_map(&map);
   }
+  if (warp == kMma) {
+    tmem_alloc<1>(&sh.tmem, kColumns);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before_sync();
   __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = sh.tmem;
   const int b0 = static_cast<int>(static_cast<long long>(p.blocks) * rank / p.split);
   const int b1 = static_cast<int>(static_cast<long long>(p.blocks) * (rank + 1) / p.split);
 
   int stage = 0;
-  uint32_t parity = 0;
+  uint32_t parity = 0, phase = 0;  // of the stages, and of made and multiplied
   auto next = [&] {
     if (++stage == kStages) {
       stage = 0;
       parity ^= 1u;
     }
   };
+  auto wait = [&](uint64_t *bar, uint32_t ph) {
+    return nap_wait(bar, ph, p.timeout_ns, &sh.abort, &g_w4_status);
+  };
   bool first = true;
 
-  for (long long t0 = r0; t0 < r1; t0 += 8 * NT) {
-    const int used = static_cast<int>(r1 - t0 >= 8 * NT ? NT : (r1 - t0 + 7) / 8);  // tiles
-    if (warp == kConsumers / 32) {
+  for (long long t0 = r0; t0 < r1; t0 += A::kRows) {
+    if (warp == kProducer) {
       if (lane == 0) {
+        const long long at = (r0 / A::kRows + g + (t0 - r0) / A::kRows) * p.blocks;
         auto load_w = [&](int b) {
-          mbar_arrive_expect_tx(&sh.full[stage], kStageBytes + used * kABytes);
-          tma_load_3d(stages + stage * kStageBytes, &map, &sh.full[stage], b * (kBlockK / 2), n0,
+          mbar_arrive_expect_tx(&sh.full_w[stage], kWBytes);
+          tma_load_3d(ws + stage * kWBytes, &map, &sh.full_w[stage], b * (kBlockK / 2), n0,
                       g * p.z_step);
         };
         auto load_a = [&](int b) {
-          const long long at = ((r0 / 8 + g + (t0 - r0) / 8) * p.blocks + b) * kAStep;
-          for (int i = 0; i < used; ++i) {
-            const long long from = at + static_cast<long long>(i) * p.blocks * kAStep;
-            bulk_load(as + (stage * NT + i) * kAStep, p.A + from, kABytes, &sh.full[stage]);
-          }
+          mbar_arrive_expect_tx(&sh.full_a[stage], A::kBytes);
+          bulk_load(as + stage * A::kStep, p.A + (at + b) * A::kStep, A::kBytes, &sh.full_a[stage]);
         };
         int b = b0, issued = 0;
         if (first) {
@@ -349,9 +420,7 @@ __global__ void __launch_bounds__(kThreads)
           }
         }
         for (; b < b1; ++b, ++issued) {
-          if (!mbar_wait_bounded(&sh.empty[stage], parity ^ 1u, p.timeout_ns, &sh.abort,
-                                 &g_w4_status))
-            break;
+          if (!wait(&sh.empty[stage], parity ^ 1u)) break;
           load_w(b);
           load_a(b);
           next();
@@ -359,132 +428,227 @@ __global__ void __launch_bounds__(kThreads)
         if (sh.abort) {
           // Given up: the copies under way land before anyone leaves.
           for (int i = issued < kStages ? issued : kStages; i > 0; --i) {
-            const int at = (stage - i + kStages) % kStages;
+            const int s = (stage - i + kStages) % kStages;
             const uint32_t ph = stage - i < 0 ? parity ^ 1u : parity;
-            mbar_wait_bounded(&sh.full[at], ph, p.timeout_ns, &sh.drain_abort, &g_w4_status);
+            mbar_wait_bounded(&sh.full_w[s], ph, p.timeout_ns, &sh.drain_abort, &g_w4_status);
+            mbar_wait_bounded(&sh.full_a[s], ph, p.timeout_ns, &sh.drain_abort, &g_w4_status);
           }
         }
       }
       __syncwarp();
       stage = __shfl_sync(0xffffffffu, stage, 0);
       parity = __shfl_sync(0xffffffffu, parity, 0);
+    } else if (warp == kMma) {
+      if (lane == 0) {
+        constexpr uint32_t idesc = idesc_bf16(kTileN, COLS);
+        bool ok = true;
+        for (int b = b0; ok && b < b1; ++b) {
+          ok = wait(&sh.full_a[stage], parity);
+          const uint64_t desc = smem_desc(smem_addr(as + stage * A::kStep), 16, 1024, 2);
+#pragma unroll
+          for (int h = 0; h < kGroups; ++h) {
+            // the operand is there, and the accumulators have been read
+            ok = ok && wait(&sh.made[h], phase);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t a = tmem + h * 64, d = tmem + kGroups * 64 + h * COLS * kTimes;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // steps of 16 k
+              mma_bf16_ts(d + i / (2 * PERIOD) * COLS, a + i * 8,
+                          desc + (((h * 2 + i / 4) * A::kPanel + i % 4 * 32) >> 4), idesc,
+                          i % (2 * PERIOD) != 0);
+            mma_commit(&sh.multiplied[h]);
+          }
+          if (ok) mma_commit(&sh.empty[stage]);
+          phase ^= 1u;
+          next();
+        }
+        if (sh.abort) {
+          // Given up: the MMAs under way end before TMEM is freed.
+          mma_commit(&sh.drain);
+          mbar_wait_bounded(&sh.drain, 0, p.timeout_ns, &sh.drain_abort, &g_w4_status);
+        }
+      }
+      __syncwarp();
+      stage = __shfl_sync(0xffffffffu, stage, 0);
+      parity = __shfl_sync(0xffffffffu, parity, 0);
+      phase = __shfl_sync(0xffffffffu, phase, 0);
     } else {
-      const int row = warp * 16 + lane / 4, j = lane % 4, swz = row & 7;
-      // Scales and zeros of two rows, a block ahead of their use. (Rows and groups
-      // behind the last take its values: their products are not kept, or zero.)
-      const long long n_lo = min(n0 + row, p.N - 1), n_hi = min(n0 + row + 8, p.N - 1);
-      float s_next[kTimes][2];
-      uint32_t z_next[kTimes][2];
+      const int h = warp / 4, row = warp % 4 * 32 + lane;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+      const uint32_t a_tmem = lanes + h * 64, d_tmem = lanes + kGroups * 64 + h * COLS * kTimes;
+      // The row's scales and zeros, a block ahead of their use. (A row or a group
+      // behind the last takes its values: its products are not kept, or zero.)
+      const long long n = min(n0 + row, p.N - 1);
+      const long long s_at = g * p.strides + n * p.lds, z_at = g * p.stridez + n * p.ldz;
+      T s_next[kTimes];
+      uint32_t z_next[kTimes];
       auto fetch = [&](int b) {
 #pragma unroll
         for (int c = 0; c < kTimes; ++c) {
-          const unsigned at = static_cast<unsigned>(b) * kTimes + c;
+          const unsigned at = (static_cast<unsigned>(b) * kGroups + h) * kTimes + c;
           const int gi = min(static_cast<int>(p.per_group == 1 ? at : at / p.per_group), p.row_groups - 1);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const long long n = h == 0 ? n_lo : n_hi;
-            const long long i = g * p.strides + n * p.lds + gi;
-            s_next[c][h] = index_ok(kSiteLoadB, i, 1, p.s_extent)
-                               ? static_cast<float>(__ldg(static_cast<const T *>(p.scales) + i)) : 0.0f;
-            z_next[c][h] = 8;
-            if (p.zeros != nullptr) {
-              const long long iz = g * p.stridez + n * p.ldz + gi;
-              if (index_ok(kSiteLoadB, iz, 1, p.z_extent)) z_next[c][h] = __ldg(p.zeros + iz) & 15u;
-            }
-          }
+          s_next[c] = index_ok(kSiteLoadB, s_at + gi, 1, p.s_extent)
+                          ? __ldg(static_cast<const T *>(p.scales) + s_at + gi) : T(0.0f);
+          z_next[c] = 8;
+          if (p.zeros != nullptr && index_ok(kSiteLoadB, z_at + gi, 1, p.z_extent))
+            z_next[c] = __ldg(p.zeros + z_at + gi);
         }
       };
-      float sum[NT][4] = {};
-      if (b0 < b1) fetch(b0);
-      for (int b = b0; b < b1; ++b) {
-        float s[kTimes][2];
-        uint32_t z[kTimes][2];
-#pragma unroll
-        for (int c = 0; c < kTimes; ++c)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            s[c][h] = s_next[c][h];
-            z[c][h] = 0x43004300u | z_next[c][h] | z_next[c][h] << 16;
-          }
-        if (b + 1 < b1) fetch(b + 1);
-        mbar_wait_bounded(&sh.full[stage], parity, p.timeout_ns, &sh.abort, &g_w4_status);
-        const uint8_t *w0 = stages + stage * kStageBytes + row * 128 + j * 4;
-        const uint8_t *ab = as + stage * NT * kAStep;
-        float2 grow[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          grow[nt] = *reinterpret_cast<const float2 *>(ab + nt * kAStep + kTerms * 4096 + j * 8);
+      float sum[A::kRows] = {}, s_now[kTimes], z_now[kTimes];
+
+      // Adds the accumulators of the block before, which stands in stage `at`, to
+      // the sums: u = sum q a - z sum a for every row, in units of 2^(kScale - kUnit).
+      auto drain_as = [&](auto is_large, const uint8_t *at) {
+        constexpr bool LARGE = decltype(is_large)::value;
+        tc_fence_after_sync();
 #pragma unroll
         for (int c = 0; c < kTimes; ++c) {
-          float part[NT][2][4] = {};  // two sums, so that one's MMA need not wait for the other's
+          uint32_t v[COLS / 16][16];
 #pragma unroll
-          for (int i = c * PERIOD; i < (c + 1) * PERIOD; ++i) {
-            const uint32_t lo = *reinterpret_cast<const uint32_t *>(w0 + ((i ^ swz) << 4));
-            const uint32_t hi = *reinterpret_cast<const uint32_t *>(w0 + 8 * 128 + ((i ^ swz) << 4));
-            const uint32_t f0[4] = {pair_of<0>(lo, z[c][0]), pair_of<0>(hi, z[c][1]),
-                                    pair_of<1>(lo, z[c][0]), pair_of<1>(hi, z[c][1])};
-            const uint32_t f1[4] = {pair_of<2>(lo, z[c][0]), pair_of<2>(hi, z[c][1]),
-                                    pair_of<3>(lo, z[c][0]), pair_of<3>(hi, z[c][1])};
+          for (int i = 0; i < COLS / 16; ++i) tmem_load_16cols(d_tmem + c * COLS + i * 16, v[i]);
+          tmem_load_wait();
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (nt >= used) continue;
+          for (int i = 0; i < COLS / 16; ++i) tmem_regs_ready(v[i]);
+          const float *asums =
+              reinterpret_cast<const float *>(at + A::kSums) + (h * kTimes + c) * A::kTerms * A::kRows;
+          float as4[4];
 #pragma unroll
-              for (int t = kTerms - 1; t >= 0; --t) {  // small terms first
-                const uint4 x = *reinterpret_cast<const uint4 *>(ab + nt * kAStep +
-                                                                 (i * kTerms + t) * 512 + lane * 16);
-                mma(part[nt][0], f0, x.x, x.y);
-                mma(part[nt][1], f1, x.z, x.w);
+          for (int t = 0; t < A::kRows; ++t) {
+            float u;
+            if constexpr (A::kTerms == 1) {
+              if (t % 4 == 0) {
+                const float4 f = *reinterpret_cast<const float4 *>(asums + t);
+                as4[0] = f.x;
+                as4[1] = f.y;
+                as4[2] = f.z;
+                as4[3] = f.w;
+              }
+              u = fmaf(-z_now[c], as4[t % 4], __uint_as_float(v[t / 16][t % 16]));
+            } else {
+              u = 0.0f;
+#pragma unroll
+              for (int i = A::kTerms - 1; i >= 0; --i) {  // small terms first
+                const int col = i * A::kRows + t;
+                u += fmaf(-z_now[c], asums[col], __uint_as_float(v[col / 16][col % 16]));
               }
             }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (nt >= used) continue;
-            const float(&a)[4] = part[nt][0], (&d)[4] = part[nt][1];
-            sum[nt][0] = fmaf(s[c][0] * grow[nt].x, a[0] + d[0], sum[nt][0]);
-            sum[nt][1] = fmaf(s[c][0] * grow[nt].y, a[1] + d[1], sum[nt][1]);
-            sum[nt][2] = fmaf(s[c][1] * grow[nt].x, a[2] + d[2], sum[nt][2]);
-            sum[nt][3] = fmaf(s[c][1] * grow[nt].y, a[3] + d[3], sum[nt][3]);
+            if constexpr (LARGE) {
+              const int e = at[A::kFlags + t];
+              if (e != 0) {
+                // 2^(kLargest - e) less, which may be more than a factor holds
+                sum[t] = fmaf(s_now[c] * u, power(e - kLargest), sum[t]);
+                continue;
+              }
+            }
+            sum[t] = fmaf(s_now[c], u, sum[t]);
           }
         }
+        tc_fence_before_sync();
+      };
+      auto drain = [&](int of, uint32_t ph) {
+        wait(&sh.multiplied[h], phase ^ 1u);
+        wait(&sh.full_a[of], ph);  // (long since)
+        const uint8_t *at = as + of * A::kStep;
+        const uint32_t *flags = reinterpret_cast<const uint32_t *>(at + A::kFlags);
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < A::kRows / 4; ++i) any |= flags[i];
+        if constexpr (A::kRows % 4 != 0) any |= flags[A::kRows / 4] & ((1u << (A::kRows % 4 * 8)) - 1u);
+        if (any != 0) drain_as(std::true_type{}, at);
+        else drain_as(std::false_type{}, at);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        if (lane == 0) mbar_arrive(&sh.empty[of]);
+      };
+      if (b0 < b1) fetch(b0);
+      int before = 0;  // the stage of the block before, and its parity
+      uint32_t before_parity = 0;
+      for (int b = b0; b < b1; ++b) {
+        float s[kTimes], z[kTimes];
+#pragma unroll
+        for (int c = 0; c < kTimes; ++c) {
+          s[c] = static_cast<float>(s_next[c]) * power(kUnit - kScale);
+          z[c] = static_cast<float>(z_next[c] & 15u);
+        }
+        if (b + 1 < b1) fetch(b + 1);
+        wait(&sh.full_w[stage], parity);
+        const uint8_t *line = ws + stage * kWBytes + row * 128;
+        // 64 k of the line: 32 columns of the operand
+        auto make = [&](int q, uint32_t (&v)[32]) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int chunk = h * 4 + q * 2 + c;  // 32 k
+            const uint4 w = *reinterpret_cast<const uint4 *>(line + ((chunk ^ (row & 7)) << 4));
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[c * 16 + i * 4] = u[i] & 0x000f000fu;
+              v[c * 16 + i * 4 + 1] = u[i] & 0x00f000f0u;
+              v[c * 16 + i * 4 + 2] = u[i] >> 8 & 0x000f000fu;
+              v[c * 16 + i * 4 + 3] = u[i] >> 8 & 0x00f000f0u;
+            }
+          }
+        };
+        uint32_t v[32];
+        make(0, v);
+        if (b > b0) drain(before, before_parity);
+#pragma unroll
+        for (int c = 0; c < kTimes; ++c) {
+          s_now[c] = s[c];
+          z_now[c] = z[c];
+        }
+        tmem_store_32cols(a_tmem, v);
+        make(1, v);
+        tmem_store_32cols(a_tmem + 32, v);
+        tmem_store_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.made[h]);
+        before = stage;
+        before_parity = parity;
+        phase ^= 1u;
         next();
       }
+      if (b0 < b1) drain(before, before_parity);
+      // Every copy has landed and been used: the other warpgroup's too, once it
+      // is here.
+      named_barrier_sync(1, kMakers);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float *to = sums + (nt * 8 + 2 * j) * kTileN + row;
-        to[0] = sum[nt][0];
-        to[kTileN] = sum[nt][1];
-        to[8] = sum[nt][2];
-        to[kTileN + 8] = sum[nt][3];
-      }
+      for (int t = 0; t < A::kRows; ++t) sums[(h * A::kRows + t) * kTileN + row] = sum[t];
     }
     if (first) grid_dependency_wait();
     first = false;
     // All parts of the tile are there (cluster); this CTA's share of them.
     if (p.split > 1) cluster_sync();
     else __syncthreads();
-    const int all = 8 * used * kTileN;
+    const int used = static_cast<int>(min(static_cast<long long>(A::kRows), r1 - t0));
+    const int all = used * kTileN;
     const int e0 = all * rank / p.split, e1 = all * (rank + 1) / p.split;
     for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += kThreads) {
-      const long long t = t0 + e / kTileN;
       const int n = n0 + e % kTileN;
-      if (t >= r1 || n >= p.N) continue;
-      float v;
+      if (n >= p.N) continue;
+      float v = 0.0f;
       if (p.split == 1) {
-        v = sums[e];
+        v = sums[e] + sums[A::kRows * kTileN + e];
       } else {
-        v = 0.0f;
         const uint32_t a = smem_addr(sums + e);
-        for (int r = 0; r < p.split; ++r) v += read_cluster(a, static_cast<uint32_t>(r));
+        for (int r = 0; r < p.split; ++r)
+          v += read_cluster(a, static_cast<uint32_t>(r)) +
+               read_cluster(a + A::kRows * kTileN * 4, static_cast<uint32_t>(r));
       }
-      const long long at = t * p.ldc + n;
+      const long long at = (t0 + e / kTileN) * p.ldc + n;
       if (index_ok(kSiteCStore, at, 1, p.c_extent)) static_cast<T *>(p.C)[at] = rounded<T>(v);
     }
-    // nobody's sums are written again, or gone, before all are read
+    // Nobody's sums are gone, or overwritten by copies, before all are read.
+    fence_proxy_async_smem();
     if (p.split > 1) cluster_sync();
     else __syncthreads();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after_sync();
+    tmem_dealloc<1>(tmem, kColumns);
   }
 }
 
@@ -622,21 +786,46 @@ int launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? kOk : kErrLaunch;
 }
 
-template <class T, int NT, int PERIOD>
-int launch_period(const CUtensorMap &map, const P &p, int groups, cudaStream_t stream) {
+// A's operands, and the products.
+template <class T, int COLS, int PERIOD>
+int launch_both(const CUtensorMap &map, P p, const Prep &prep, int groups, cudaStream_t stream) {
+  using A = Tile<T, COLS, PERIOD>;
   const int tiles = (p.N + kTileN - 1) / kTileN;
-  const size_t smem = 1024 + kStages * (kStageBytes + NT * a_step(sizeof(T))) + 8 * NT * kTileN * 4;
-  return launch(w4_kernel<T, NT, PERIOD>,
+  constexpr int kStages = stages_of(COLS);
+  static_assert(kGroups * A::kRows * kTileN * 4 <= kStages * kWBytes, "sums stand where weights did");
+  size_t smem = 1024 + kStages * (kWBytes + A::kStep);
+  // Two CTAs of an SM, or one, as TMEM has room for: a third would wait for it,
+  // and its cluster with it.
+  const size_t least = tmem_columns(COLS, 4 / PERIOD) == 512 ? 116 * 1024 : 77 * 1024;
+  if (smem < least) smem = least;
+  Prep q = prep;
+  q.to_extent = (static_cast<long long>(p.M) / A::kRows + groups + 1) * p.blocks * A::kStep;
+  void *to = nullptr;
+  int st = pool_alloc(&to, static_cast<size_t>(q.to_extent), stream);
+  if (st != kOk) return st;
+  q.to = static_cast<uint8_t *>(to);
+  p.A = q.to;
+  const int64_t average = (p.M + groups - 1) / groups;
+  const int64_t units = (average + A::kRows - 1) / A::kRows * A::kRows * p.blocks;
+  const int64_t blocks = (units + kPrepWarps - 1) / kPrepWarps;
+  st = launch(w4_prep_kernel<T, COLS, PERIOD>,
+              dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), static_cast<unsigned>(groups), 1),
+              32 * kPrepWarps, 0, 1, stream, q);
+  if (st == kOk)
+    st = launch(w4_kernel<T, COLS, PERIOD>,
                 dim3(static_cast<unsigned>(tiles * p.split), static_cast<unsigned>(groups), 1), kThreads,
                 smem, p.split, stream, map, p);
+  const int fst = pool_free(to, stream);
+  return st != kOk ? st : fst;
 }
 
-template <class T, int NT>
-int launch_nt(const CUtensorMap &map, const P &p, int groups, int64_t group, cudaStream_t stream) {
-  if (group % 256 == 0) return launch_period<T, NT, 8>(map, p, groups, stream);
-  if (group % 128 == 0) return launch_period<T, NT, 4>(map, p, groups, stream);
-  if (group % 64 == 0) return launch_period<T, NT, 2>(map, p, groups, stream);
-  return launch_period<T, NT, 1>(map, p, groups, stream);
+template <class T, int COLS>
+int launch_cols(const CUtensorMap &map, const P &p, const Prep &q, int groups, int period,
+                cudaStream_t stream) {
+  if (period == 4) return launch_both<T, COLS, 4>(map, p, q, groups, stream);
+  if (period == 2) return launch_both<T, COLS, 2>(map, p, q, groups, stream);
+  // (more columns' accumulators of groups of 32 are more than TMEM holds)
+  return launch_both<T, (COLS < 48 ? COLS : (sizeof(T) == 2 ? 32 : 48)), 1>(map, p, q, groups, stream);
 }
 
 }  // namespace
@@ -691,14 +880,14 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
   p.N = static_cast<int>(a.N);
   p.K = static_cast<int>(a.K);
   p.blocks = static_cast<int>((a.K + kBlockK - 1) / kBlockK);
-  int period = 8;
+  int period = 4;
   while (a.group % (32 * period) != 0) period /= 2;
   p.per_group = static_cast<int>(a.group / (32 * period));
   p.timeout_ns = 2000000000ull + 2000ull * static_cast<unsigned long long>(a.K);
   const int64_t tiles = (a.N + kTileN - 1) / kTileN;
   const int64_t used = a.groups < a.M ? a.groups : a.M;  // segments with rows, at most
   p.split = 1;
-  while (p.split < kMaxSplit && 8 * p.split <= p.blocks && tiles * used * p.split < 4 * sm_count)
+  while (p.split < kMaxSplit && 4 * p.split <= p.blocks && tiles * used * p.split < 2 * sm_count)
     p.split *= 2;
 
   Prep q = {};
@@ -710,32 +899,18 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
   q.M = p.M;
   q.K = p.K;
   q.blocks = p.blocks;
-  q.to_extent = (a.M / 8 + a.groups + 1) * p.blocks * a_step(elem);
-  void *ws = nullptr;
-  int st = pool_alloc(&ws, static_cast<size_t>(q.to_extent), stream);
-  if (st != kOk) return st;
-  q.to = static_cast<uint8_t *>(ws);
-  p.A = q.to;
-  p.a_extent = q.to_extent;
-  const int64_t average = (a.M + a.groups - 1) / a.groups;
-  const int64_t prep = (average + 7) / 8 * 8 * p.blocks / kPrepWarps + 1;
-  const dim3 grid(static_cast<unsigned>(prep < 4096 ? prep : 4096), static_cast<unsigned>(a.groups), 1);
-  st = a.bf16 ? launch(w4_prep_kernel<__nv_bfloat16>, grid, 32 * kPrepWarps, 0, 1, stream, q)
-              : launch(w4_prep_kernel<float>, grid, 32 * kPrepWarps, 0, 1, stream, q);
-  // Rows at a time: what a segment has on average, or (few more instructions) twice
-  // that; others take several turns.
+  // Rows at a time: twice what a segment has on average, for segments differ;
+  // longer ones take several turns.
+  const int64_t rows = a.groups > 1 ? 2 * ((a.M + a.groups - 1) / a.groups) : a.M;
   const int groups = static_cast<int>(a.groups);
-  if (st == kOk) {
-    if (a.bf16)
-      st = a.M <= 8 || average <= 2 ? launch_nt<__nv_bfloat16, 1>(map, p, groups, a.group, stream)
-           : average <= 12          ? launch_nt<__nv_bfloat16, 2>(map, p, groups, a.group, stream)
-                                    : launch_nt<__nv_bfloat16, 4>(map, p, groups, a.group, stream);
-    else
-      st = a.M <= 8 || average <= 2 ? launch_nt<float, 1>(map, p, groups, a.group, stream)
-                                    : launch_nt<float, 2>(map, p, groups, a.group, stream);
+  if (a.bf16) {
+    if (rows <= 16) return launch_cols<__nv_bfloat16, 16>(map, p, q, groups, period, stream);
+    if (rows <= 32) return launch_cols<__nv_bfloat16, 32>(map, p, q, groups, period, stream);
+    return launch_cols<__nv_bfloat16, 64>(map, p, q, groups, period, stream);
   }
-  const int fst = pool_free(ws, stream);
-  return st != kOk ? st : fst;
+  if (rows <= 5) return launch_cols<float, 16>(map, p, q, groups, period, stream);
+  if (rows <= 16) return launch_cols<float, 48>(map, p, q, groups, period, stream);
+  return launch_cols<float, 96>(map, p, q, groups, period, stream);
 }
 
 int w4_pack_launch(const W4Args &a, uint8_t *dst, int64_t ldd, int64_t strided, int sm_count,
