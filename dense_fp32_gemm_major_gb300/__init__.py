@@ -574,10 +574,10 @@ def _result(out, name, shape, like, kind, device, stream):
         import torch
 
         if stream is None or stream == torch._C._cuda_getCurrentRawStream(device):
-            out = like.new_empty(shape)
+            out = torch.empty(shape, dtype=like.dtype, device=device)
         else:
             with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-                out = like.new_empty(shape)
+                out = torch.empty(shape, dtype=like.dtype, device=device)
         return out, out.data_ptr(), shape[-1] or 1, (shape[1] * shape[2] if len(shape) == 3 else 0)
     got, ptr, ld, stride = _matrices(out, name, len(shape), kind, device)
     if tuple(got) != shape:
@@ -619,7 +619,7 @@ def _call(name, device, stream, *args):
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(device)
     function = getattr(_lib or _load(), name)
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         st = function(*args, stream or None)
     else:
         with torch.cuda.device(device):
@@ -804,6 +804,16 @@ def _score(score):
 Routing = collections.namedtuple("Routing", "experts weights offsets order places")
 
 
+def _new_routing(t, e, k, device):
+    import torch
+
+    empty = torch.empty
+    experts = empty((t, k), dtype=torch.int32, device=device)
+    return Routing(experts, empty((t, k), device=device, dtype=torch.float32),
+                   empty((e + 1,), dtype=torch.int64, device=device),
+                   empty((t * k,), dtype=torch.int32, device=device), torch.empty_like(experts))
+
+
 def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_best=2,
           renormalise=True, scale=1.0, mask=None, stream=None):
     """The router of a mixture of experts: the ``k`` experts of every token with
@@ -841,15 +851,15 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, grou
                          f"{group_best}: up to 32 equal groups, by one or two")
     pb = None if bias is None else _dense(bias, "bias", torch.float32, (e,), dev)
     pm = None if mask is None else _dense(mask, "mask", torch.bool, (t,), dev)
-    ints = _empty((3, t, k), torch.int32, dev, stream)
-    experts, order, places = ints.unbind(0)
-    weights = _empty((t, k), torch.float32, dev, stream)
-    offsets = _empty((e + 1,), torch.int64, dev, stream)
-    at, step = ints.data_ptr(), 4 * t * k
+    if stream is None or stream == torch._C._cuda_getCurrentRawStream(dev):
+        r = _new_routing(t, e, k, dev)
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+            r = _new_routing(t, e, k, dev)
     _call("gemm_f32_route", dev, stream, kind, _score(score), t, e, k, px, ldx, pb, pm, groups,
-          top_groups, group_best, 1 if renormalise else 0, float(scale), at, weights.data_ptr(),
-          offsets.data_ptr(), at + step, at + 2 * step)
-    return Routing(experts, weights, offsets, order.view(t * k), places)
+          top_groups, group_best, 1 if renormalise else 0, float(scale),
+          *[x.data_ptr() for x in r])
+    return r
 
 
 def route_backward(dweights, logits, experts, weights, score="softmax", renormalise=True, scale=1.0,
@@ -1013,24 +1023,27 @@ def w4_matmul(x, q, scales, group, zeros=None, offsets=None, out=None, stream=No
 
 
 def _tensor_list(tensors, name, device):
-    """(device, pointers, sizes, types) of dense tensors on one device."""
+    """(device, pointers, sizes, types) of dense tensors on one device. An attribute
+    at a time: there may be hundreds of them before microseconds of work."""
     import torch
 
     types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
-    pointers, sizes, kinds = [], [], []
-    for t in tensors:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in types:
-            raise TypeError(f"{name} must be float32 or bfloat16 CUDA tensors")
-        if device is None:
-            device = t.get_device()
-        elif t.get_device() != device:
-            raise ValueError(f"{name} are not all on one device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        pointers.append(t.data_ptr())
-        sizes.append(t.numel())
-        kinds.append(types[t.dtype])
-    return device, pointers, sizes, kinds
+    try:
+        kinds = [types[t.dtype] for t in tensors]
+        devices = {t.get_device() for t in tensors}
+        if not devices:
+            return device, [], [], []
+        if min(devices) < 0 or not all([isinstance(t, torch.Tensor) for t in tensors]):
+            raise KeyError
+    except (AttributeError, KeyError):
+        raise TypeError(f"{name} must be float32 or bfloat16 CUDA tensors") from None
+    if device is not None:
+        devices.add(device)
+    if len(devices) > 1:
+        raise ValueError(f"{name} are not all on one device")
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name} must be contiguous")
+    return devices.pop(), [t.data_ptr() for t in tensors], [t.numel() for t in tensors], kinds
 
 
 def _arrays(pointers, sizes, kinds):
@@ -1044,7 +1057,7 @@ def grad_norm(tensors, stream=None):
     device; none: 0, on the current one)."""
     import torch
 
-    dev, pointers, sizes, kinds = _tensor_list(tensors, "tensors", None)
+    dev, pointers, sizes, kinds = _tensor_list(list(tensors), "tensors", None)
     if dev is None:
         dev = torch.cuda.current_device()
     norm = _empty((1,), torch.float32, dev, stream)
@@ -1068,7 +1081,7 @@ def clip_grads(tensors, limit, out=None, stream=None):
     x, n, kind = _arrays(pointers, sizes, kinds)
     y = None
     if out is not None:
-        dev, to, to_sizes, to_kinds = _tensor_list(out, "out", dev)
+        dev, to, to_sizes, to_kinds = _tensor_list(list(out), "out", dev)
         if to_sizes != sizes or to_kinds != kinds:
             raise ValueError("out does not have the tensors' types and sizes")
         y = (ctypes.c_void_p * len(to))(*to)

@@ -5,8 +5,11 @@
 // Choice. A warp takes a token; lane l holds the V = ceil(E / 32) neighbouring
 // experts from l V on. Keys are fp32 values mapped to unsigned integers of the
 // same order, so that one redux finds the warp's largest and the lowest lane
-// that holds it is that of the lowest expert. k rounds, each of which replaces
-// the key of the lane that won.
+// that holds it is that of the lowest expert. Up to 256 experts every lane sorts
+// its keys (a network of minima and maxima), and k rounds take the largest of the
+// lanes' heads; which of a lane's experts they were follows from their ranks
+// within the lane. (Looking for the expert in every round, and for the lane's next
+// one, was half of all instructions.)
 //
 // Comparisons. Without bias and sums over groups the logits are the keys: both
 // scores ascend with them. Otherwise the keys are s + bias in fp32, which is off
@@ -34,6 +37,7 @@ namespace gemm {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxSlots = 32;  // of a token
 
 struct P {
   const void *logits;
@@ -48,10 +52,16 @@ struct P {
   int T, E, k;
   int sigmoid, renormalise, compare_scores, vec;
   int groups, top_groups, group_best, per_group, group_lanes;
+  int lanes_hold_groups;  // every lane's experts are of one group, a group's of group_lanes lanes
   float scale;
   int chunk, chunks;  // tokens of a CTA, CTAs
   int plan, plan_warps;
 };
+
+// Integers a warp stages: E keys where groups are looked through, and its slots.
+__host__ __device__ __forceinline__ int staged_ints(const P &p) {
+  return (p.groups > 1 ? p.E : 0) + kMaxSlots;
+}
 
 // ------------------------------------------------------------------- values --
 
@@ -256,8 +266,97 @@ __device__ __noinline__ int choose_wide(const P &p, long long t) {
 
 // ------------------------------------------------------------------- router --
 
+// The bound of a score's error in a comparison, in units of 2^-24 of the largest
+// score. __expf is off by 2 + 1.173 |x| units of 2^-23, which times exp(-|x|), or
+// for a sigmoid s (1 - s), stays below 2 (0.65); __fdividef by two; the sum by as
+// many roundings as it has steps, and its terms.
+constexpr float kUnit = 5.9604645e-8f;  // 2^-24
+template <int V>
+__device__ __forceinline__ float score_error(const P &p, float sum) {
+  return p.sigmoid ? 10.0f * kUnit : (V + 24.0f) * kUnit * (sum > 0.0f ? 1.0f / sum : 0.0f);
+}
+
+// Descending, by Batcher's odd-even merge.
+template <int V>
+__device__ __forceinline__ void sort_keys(unsigned (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int j = d % p; j + d < V; j += 2 * d)
+#pragma unroll
+        for (int i = 0; i < d; ++i)
+          if (i + j + d < V && (i + j) / (2 * p) == (i + j + d) / (2 * p)) {
+            const unsigned a = k[i + j], b = k[i + j + d];
+            k[i + j] = a > b ? a : b;
+            k[i + j + d] = a > b ? b : a;
+          }
+}
+
+struct Choice {
+  int expert;     // lane r: of slot r (-1: none)
+  unsigned won;   // lane r: its key
+  unsigned next;  // the largest key left
+};
+
+// The k best of up to 8 keys a lane.
+template <int V>
+__device__ __forceinline__ Choice choose_sorted(const unsigned (&key)[V], unsigned (&head)[V], int k,
+                                                int *slots) {
+  const int lane = threadIdx.x & 31;
+  Choice c = {-1, 0u, 0u};
+  unsigned long long mine = 0;  // the slots that this lane won, five bits each
+  int count = 0, r = 0;
+  for (; r < k; ++r) {
+    const unsigned best = warp_best(head[0]);
+    if (best == 0) break;
+    const unsigned from = __ballot_sync(kFull, head[0] == best);
+    if (lane == r) c.won = best;
+    if ((from & (0u - from)) == 1u << lane) {
+      mine |= static_cast<unsigned long long>(r) << (5 * count++);
+#pragma unroll
+      for (int i = 0; i + 1 < V; ++i) head[i] = head[i + 1];
+      head[V - 1] = 0;
+    }
+  }
+  c.next = warp_best(head[0]);
+  // Each of the lane's experts by its rank within the lane, ties in order.
+  if (count != 0) {
+    int rank[V] = {};
+#pragma unroll
+    for (int j = 1; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < j; ++i) {
+        const bool first = key[i] >= key[j];
+        rank[j] += first;
+        rank[i] += !first;
+      }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (rank[i] < count) slots[mine >> (5 * rank[i]) & 31u] = lane * V + i;
+  }
+  __syncwarp();
+  if (lane < r) c.expert = slots[lane];
+  __syncwarp();
+  return c;
+}
+
+// The same of many, looked through in every round.
+template <int V>
+__device__ __forceinline__ Choice choose_any(unsigned (&key)[V], int k) {
+  Choice c;
+  c.expert = choose_experts<V>(key, k, &c.won);
+  unsigned local = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) local = key[i] > local ? key[i] : local;
+  c.next = warp_best(local);
+  return c;
+}
+
 // Lane r: the expert of slot r (-1: none). *m, *sum: softmax's, where it is
-// needed; *bad: softmax of a NaN or of +infinity.
+// needed; *bad: softmax of a NaN or of +infinity. `staged`: E integers and 32 of
+// the warp's own.
 template <int V, class T>
 __device__ __forceinline__ int choose(const P &p, long long t, unsigned *staged, float *m_out,
                                       float *sum_out, bool *bad_out) {
@@ -312,39 +411,45 @@ __device__ __forceinline__ int choose(const P &p, long long t, unsigned *staged,
   unsigned key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    key[i] = 0;
-    if (x[i] == -INFINITY) continue;  // not available, or past the last expert
     float f = x[i];
+    bool there = f != -INFINITY;  // else not available, or past the last expert
     if (p.compare_scores) {
-      f = p.sigmoid ? sigmoid(f) : (bad ? NAN : expf(f - m) / sum);
-      if (p.bias != nullptr) {
+      f = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-f)) : (bad ? NAN : __fdividef(__expf(f - m), sum));
+      // (__fdividef of 2^126 and more gives 0, as it should be)
+      if (p.bias != nullptr && there) {
         const float b = __ldg(p.bias + lane * V + i);
-        if (b == -INFINITY) continue;
+        there = b != -INFINITY;
         f += b;
       }
     }
-    key[i] = key_of(f);
+    key[i] = there ? key_of(f) : 0u;
   }
-  // A key is off by at most err (score) + 2^-24 |key|. Score: expf is good to 2
-  // units, its argument to 2^-24 |x - m| (which times exp(-|x - m|) is below
-  // 0.37), the sum to as many roundings as it has steps, and each division,
-  // sum and product to half a unit of 2^-23.
-  constexpr float kUnit = 5.9604645e-8f;  // 2^-24
-  const float err = p.sigmoid ? 8.0f * kUnit : (V + 16.0f) * kUnit * (sum > 0.0f ? 1.0f / sum : 0.0f);
+  const float err = score_error<V>(p, sum);
   bool unsure = false;
 
-  if (p.groups > 1) {
-    // The best two of each group: 32 / (groups rounded up to a power of two)
-    // lanes look through one group's keys, in shared memory.
+  constexpr bool kSort = V <= 8;
+  [[maybe_unused]] unsigned head[V] = {};
+  if constexpr (kSort) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane * V + i < p.E) staged[lane * V + i] = key[i];
-    __syncwarp();
+    for (int i = 0; i < V; ++i) head[i] = key[i];
+    sort_keys<V>(head);
+  }
+  if (p.groups > 1) {
+    // The best two of each group, by group_lanes lanes.
     const int g = lane / p.group_lanes, sub = lane % p.group_lanes;
     unsigned b1 = 0, b2 = 0;
-    if (g < p.groups)
-      for (int j = sub; j < p.per_group; j += p.group_lanes)
-        merge_best(b1, b2, staged[g * p.per_group + j], 0u);
+    if (kSort && p.lanes_hold_groups) {
+      b1 = head[0];
+      b2 = V > 1 ? head[V > 1 ? 1 : 0] : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (lane * V + i < p.E) staged[lane * V + i] = key[i];
+      __syncwarp();
+      if (g < p.groups)
+        for (int j = sub; j < p.per_group; j += p.group_lanes)
+          merge_best(b1, b2, staged[g * p.per_group + j], 0u);
+    }
     for (int s = p.group_lanes / 2; s > 0; s >>= 1) {
       const unsigned o1 = __shfl_xor_sync(kFull, b1, s), o2 = __shfl_xor_sync(kFull, b2, s);
       merge_best(b1, b2, o1, o2);
@@ -365,44 +470,60 @@ __device__ __forceinline__ int choose(const P &p, long long t, unsigned *staged,
       if (!in && mine > 1 && low > 1 && low != kFull)
         unsure = value_of(low) - value_of(mine) <= off + off_in;
     }
+    if (kSort && p.lanes_hold_groups) {
+      if (!(kept >> (g * p.group_lanes) & 1u)) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int of = (lane * V + i) / p.per_group;
-      const int at = of * p.group_lanes;
-      if (of >= p.groups || !(kept >> at & 1u)) key[i] = 0;
+        for (int i = 0; i < V; ++i) head[i] = key[i] = 0;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int of = (lane * V + i) / p.per_group;
+        if (of >= p.groups || !(kept >> (of * p.group_lanes) & 1u)) key[i] = 0;
+      }
+      if constexpr (kSort) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) head[i] = key[i];
+        sort_keys<V>(head);
+      }
     }
   }
 
-  unsigned won;
-  int mine = choose_experts<V>(key, p.k, &won);
+  Choice c;
+  if constexpr (kSort) c = choose_sorted<V>(key, head, p.k, reinterpret_cast<int *>(staged + staged_ints(p) - kMaxSlots));
+  else c = choose_any<V>(key, p.k);
   if (p.compare_scores) {
     // Two neighbours of the chosen, or the last of them and one that is left,
     // that may stand the other way round. Equal logits and biases are equal.
+    auto close = [&](unsigned a, unsigned b) {
+      const float u = value_of(a), v = value_of(b);
+      return b > 1 && u - v <= 2.0f * err + kUnit * (fabsf(u) + fabsf(v));
+    };
     auto same = [&](int a, int b) {
       return load_logit<T>(p, t, a) == load_logit<T>(p, t, b) &&
              (p.bias == nullptr || p.bias[a] == p.bias[b]);
     };
-    const unsigned next = __shfl_down_sync(kFull, won, 1);
-    const int next_e = __shfl_down_sync(kFull, mine, 1);
-    if (lane + 1 < p.k && won > 1 && next > 1) {
-      const float a = value_of(won), b = value_of(next);
-      if (a - b <= 2.0f * err + kUnit * (fabsf(a) + fabsf(b))) unsure |= !same(mine, next_e);
-    }
-    const unsigned last = __shfl_sync(kFull, won, p.k - 1);
-    const int last_e = __shfl_sync(kFull, mine, p.k - 1);
-    if (last > 1) {
-      const float a = value_of(last);
+    const unsigned next = __shfl_down_sync(kFull, c.won, 1);
+    const int next_e = __shfl_down_sync(kFull, c.expert, 1);
+    if (lane + 1 < p.k && c.won > 1 && close(c.won, next)) unsure |= !same(c.expert, next_e);
+    const unsigned last = __shfl_sync(kFull, c.won, p.k - 1);
+    if (last > 1 && close(last, c.next)) {
+      const int last_e = __shfl_sync(kFull, c.expert, p.k - 1);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (key[i] <= 1) continue;
-        const float b = value_of(key[i]);
-        if (a - b <= 2.0f * err + kUnit * (fabsf(a) + fabsf(b)))
-          unsure |= !same(last_e, lane * V + i);
+        // (a chosen one among them is the last's like, or is left for the bits)
+        if (key[i] > 1 && key[i] <= last && lane * V + i != last_e && close(last, key[i])) {
+          bool chosen = false;
+          if constexpr (kSort)
+            for (int r = 0; r < p.k; ++r)
+              chosen |= reinterpret_cast<int *>(staged + staged_ints(p) - kMaxSlots)[r] == lane * V + i;
+          if (!chosen) unsure |= !same(last_e, lane * V + i);
+        }
       }
     }
-    if (__any_sync(kFull, unsure)) mine = choose_wide<V, T>(p, t);
+    if (__any_sync(kFull, unsure)) return choose_wide<V, T>(p, t);
   }
-  return mine;
+  return c.expert;
 }
 
 // Lane r: the weight of its expert.
@@ -554,7 +675,7 @@ __device__ void plan_chunk(const P &p, const PlanShared &sh, int c, long long sl
   rank_slots(p, sh, static_cast<int>(s0), static_cast<int>(s1 < slots ? s1 : slots), slots);
 }
 
-constexpr int route_threads(int V) { return V <= 8 ? 1024 : (V == 16 ? 512 : 256); }
+constexpr int route_threads(int V) { return V <= 4 ? 1024 : (V == 8 ? 768 : (V == 16 ? 512 : 256)); }
 
 template <int V, class T>
 __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
@@ -565,7 +686,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
   const int warps = static_cast<int>(blockDim.x >> 5);
   const PlanShared sh = plan_shared(smem, p.E);
   // groups' keys stand where the plan's counts of a warp will
-  unsigned *staged = reinterpret_cast<unsigned *>(p.plan ? sh.base : smem) + warp * p.E;
+  unsigned *staged = reinterpret_cast<unsigned *>(p.plan ? sh.base : smem) + warp * staged_ints(p);
   const long long slots = static_cast<long long>(p.T) * p.k;
   if (p.plan) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.count[e] = 0;
@@ -669,98 +790,73 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// A warp takes a token: the slots' terms, spread over a row of shared memory;
-// then the row goes out in one sweep.
+// A warp takes a token: its row goes out without the slots' terms (zero, or what
+// softmax's sum gives to all experts), and behind that the slots' experts.
 template <class T>
 __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const B p) {
-  extern __shared__ float rows[];
   grid_dependency_wait();
   grid_launch_dependents();
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31, E = p.E;
-  float *row = rows + warp * ((E + 7) / 8 * 8);
   const T *x = static_cast<const T *>(p.logits);
   T *dx = static_cast<T *>(p.dlogits);
   const long long slots = static_cast<long long>(p.T) * p.k;
   const long long warps = static_cast<long long>(gridDim.x) * (kBackThreads / 32);
+  constexpr int kVec = 16 / sizeof(T);
   for (long long t = static_cast<long long>(blockIdx.x) * (kBackThreads / 32) + warp; t < p.T;
        t += warps) {
-    const long long at = t * p.ldx, s = t * p.k + lane;
+    const long long at = t * p.ldx, s = t * p.k + lane, out = t * p.lddx;
+    auto logit = [&](int j) {
+      return index_ok(kSiteLoadA, at + j, 1, p.x_extent) ? as_float(x[at + j]) : 0.0f;
+    };
     int e = -1;
     float w = 0.0f, g = 0.0f;
     if (lane < p.k && index_ok(kSiteLoadB, s, 1, slots)) {
       e = p.experts[s];
-      if (e < 0 || e >= E) e = -1;
-      if (e >= 0) {
-        w = p.weights[s];
-        g = p.dweights[s];
-      }
+      w = p.weights[s];
+      g = p.dweights[s];
     }
-    const float total = warp_sum(e >= 0 ? g * w : 0.0f);
-    for (int j = lane; j < E; j += 32) row[j] = 0.0f;
+    if (e < 0 || e >= E) e = -1;
+    const bool there = e >= 0;
+    const float l = there && (p.sigmoid || !p.renormalise) ? logit(e) : 0.0f;
+    const float total = warp_sum(there ? g * w : 0.0f);
     float d = p.renormalise ? w * (g - total * p.inv_scale) : w * g;
-    if (p.sigmoid && e >= 0 && index_ok(kSiteLoadA, at + e, 1, p.x_extent))
-      d *= sigmoid(-as_float(x[at + e]));
-    __syncwarp();
-    const unsigned same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
+    if (p.sigmoid) d *= sigmoid(-l);
+    // of an expert that stands in several slots, the sum by its first
+    const unsigned same = __match_any_sync(kFull, there ? e : -1 - lane);
+    bool writes = there;
     if (__any_sync(kFull, __popc(same) > 1)) {
+      float both = 0.0f;
       for (int r = 0; r < p.k; ++r) {
-        if (lane == r && e >= 0) row[e] += d;
-        __syncwarp();
+        const float v = __shfl_sync(kFull, d, r);
+        if (same >> r & 1u) both += v;
       }
-    } else if (e >= 0) {
-      row[e] = d;
+      d = both;
+      writes = there && __ffs(same) - 1 == lane;
     }
-    __syncwarp();
-    float m = 0.0f, factor = 0.0f;
-    const bool dense = !p.sigmoid && !p.renormalise;
-    bool spread = false;
-    auto logit = [&](int j) {
-      return index_ok(kSiteLoadA, at + j, 1, p.x_extent) ? as_float(x[at + j]) : 0.0f;
-    };
-    if (dense) {
-      m = -INFINITY;
+    if (!p.sigmoid && !p.renormalise && __any_sync(kFull, there)) {
+      float m = -INFINITY;
       for (int j = lane; j < E; j += 32) m = fmaxf(m, logit(j));
       m = warp_max(m);
       float sum = 0.0f;
       for (int j = lane; j < E; j += 32) {
         const float v = logit(j);
-        sum += v > -INFINITY ? expf(v - m) : (v != v ? NAN : 0.0f);
+        sum += v != -INFINITY ? expf(v - m) : 0.0f;
       }
-      // no expert at all: no gradient
-      const bool none = __all_sync(kFull, e < 0);
-      spread = !none;
-      factor = total / warp_sum(sum);
-    }
-    constexpr int kVec = 16 / sizeof(T);
-    const long long out = t * p.lddx;
-    auto value = [&](int j) {
-      float v = row[j];
-      if (spread) {
-        const float l = logit(j);
-        if (l > -INFINITY || l != l) v -= expf(l - m) * factor;
-      }
-      return v;
-    };
-    if (p.vec) {  // E is a multiple of kVec
-      for (int j = lane * kVec; j < E; j += 32 * kVec) {
-        unsigned u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (sizeof(T) == 4) {
-            u[i] = __float_as_uint(value(j + i));
-          } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(value(j + 2 * i), value(j + 2 * i + 1));
-            u[i] = *reinterpret_cast<const unsigned *>(&h);
-          }
-        }
+      const float factor = total / warp_sum(sum);
+      auto share = [&](float v) { return v != -INFINITY ? -expf(v - m) * factor : 0.0f; };
+      d += share(l);
+      for (int j = lane; j < E; j += 32)
+        if (index_ok(kSiteCStore, out + j, 1, p.dx_extent)) dx[out + j] = from_float<T>(share(logit(j)));
+    } else if (p.vec) {  // E is a multiple of kVec
+      for (int j = lane * kVec; j < E; j += 32 * kVec)
         if (index_ok(kSiteCStore, out + j, kVec, p.dx_extent))
-          *reinterpret_cast<uint4 *>(dx + out + j) = make_uint4(u[0], u[1], u[2], u[3]);
-      }
+          *reinterpret_cast<uint4 *>(dx + out + j) = make_uint4(0, 0, 0, 0);
     } else {
       for (int j = lane; j < E; j += 32)
-        if (index_ok(kSiteCStore, out + j, 1, p.dx_extent)) dx[out + j] = from_float<T>(value(j));
+        if (index_ok(kSiteCStore, out + j, 1, p.dx_extent)) dx[out + j] = from_float<T>(0.0f);
     }
     __syncwarp();
+    if (writes && index_ok(kSiteCStore, out + e, 1, p.dx_extent)) dx[out + e] = from_float<T>(d);
   }
 }
 
@@ -795,14 +891,14 @@ int plan_warps_of(int64_t E, int warps) {
 
 size_t smem_of(const P &p, int threads) {
   const size_t plan = p.plan ? static_cast<size_t>(plan_ints(p.E, p.plan_warps)) * 4 : 0;
-  const size_t keys = p.groups > 1
-                          ? static_cast<size_t>((p.plan ? 2 * p.E + 1 : 0) + threads / 32 * p.E) * 4
-                          : 0;
+  const size_t keys =
+      static_cast<size_t>((p.plan ? 2 * p.E + 1 : 0) + threads / 32 * staged_ints(p)) * 4;
   return plan > keys ? plan : keys;
 }
 
 template <int V, class T>
 int launch_v(P &p, cudaStream_t stream) {
+  p.lanes_hold_groups = p.per_group % V == 0 && p.per_group / V == p.group_lanes;
   int threads = route_threads(V);
   const int64_t want = 32LL * p.chunk;
   if (threads > want) threads = static_cast<int>((want + 127) / 128 * 128);
@@ -933,9 +1029,8 @@ int route_backward_launch(const RouteBackwardArgs &a, int sm_count, cudaStream_t
   const int64_t blocks = (a.T + kBackThreads / 32 - 1) / (kBackThreads / 32);
   const int64_t most = 8LL * (sm_count > 0 ? sm_count : 1);
   const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  const size_t smem = static_cast<size_t>(kBackThreads / 32) * ((a.E + 7) / 8 * 8) * sizeof(float);
-  return a.bf16 ? launch(route_backward_kernel<__nv_bfloat16>, p, grid, kBackThreads, smem, stream)
-                : launch(route_backward_kernel<float>, p, grid, kBackThreads, smem, stream);
+  return a.bf16 ? launch(route_backward_kernel<__nv_bfloat16>, p, grid, kBackThreads, 0, stream)
+                : launch(route_backward_kernel<float>, p, grid, kBackThreads, 0, stream);
 }
 
 }  // namespace gemm
