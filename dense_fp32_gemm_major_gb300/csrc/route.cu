@@ -6,10 +6,11 @@
 // experts from l V on. Keys are fp32 values mapped to unsigned integers of the
 // same order, so that one redux finds the warp's largest and the lowest lane
 // that holds it is that of the lowest expert. Up to 256 experts every lane sorts
-// its keys (a network of minima and maxima), and k rounds take the largest of the
-// lanes' heads; which of a lane's experts they were follows from their ranks
-// within the lane. (Looking for the expert in every round, and for the lane's next
-// one, was half of all instructions.)
+// its keys (a network of minima and maxima), with its experts in place of their
+// lowest bits, and k rounds take the largest of the lanes' heads. Keys that differ
+// in those bits alone are seen where they stand next to each other, and the token
+// is chosen again by whole keys. (Looking for the expert in every round, and for
+// the lane's next one, was half of all instructions.)
 //
 // Comparisons. Without bias and sums over groups the logits are the keys: both
 // scores ascend with them. Otherwise the keys are s + bias in fp32, which is off
@@ -38,6 +39,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxSlots = 32;  // of a token
+constexpr float kUnit = 5.9604645e-8f;  // 2^-24
 
 struct P {
   const void *logits;
@@ -199,44 +201,80 @@ __device__ __forceinline__ int choose_experts(U (&key)[V], int k, U *won) {
 
 // -------------------------------------------------------- choice in 64 bits --
 
+// Lane r's choice by keys of 64 bits. A sigmoid is computed again only for those
+// of a lane's experts that can matter: its best two (which a group's may be), and
+// those not below `least`; of the others fp32 tells enough.
 template <int V, class T>
-__device__ __noinline__ int choose_wide(const P &p, long long t) {
+__device__ __noinline__ int choose_wide(const P &p, long long t, float least, float err) {
   const int lane = threadIdx.x & 31;
-  double f[V];
   unsigned long long key[V];
+  if (p.sigmoid) {
+    float f[V];
+    unsigned again = 0;  // by their places, eight at a time of more than 32
+    float b1 = -INFINITY, b2 = -INFINITY;
+    auto bias_of = [&](int e) { return p.bias != nullptr ? __ldg(p.bias + e) : 0.0f; };
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    f[i] = e < p.E ? static_cast<double>(load_logit<T>(p, t, e)) : -INFINITY;
-    key[i] = f[i] == -INFINITY ? 0 : 2;
-  }
-  double m = -INFINITY, sum = 0.0;
-  if (!p.sigmoid) {
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      const float x = e < p.E ? load_logit<T>(p, t, e) : -INFINITY;
+      const float b = e < p.E ? bias_of(e) : 0.0f;
+      const bool there = x != -INFINITY && b != -INFINITY;
+      f[i] = there ? sigmoid(x) + b : -INFINITY;
+      key[i] = there ? key_of(static_cast<double>(f[i])) : 0;
+      b2 = fmaxf(b2, fminf(b1, f[i]));
+      b1 = fmaxf(b1, f[i]);
+    }
+    const float from = fminf(least, b2);
+    // (a lane of experts of several groups: all of them)
+    const float low = p.groups > 1 && p.per_group % V != 0
+                          ? -INFINITY : from - 4.0f * (err + kUnit * fabsf(from));
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = fmax(m, f[i]);
+    for (int i0 = 0; i0 < V; i0 += 32) {
+      again = 0;
+#pragma unroll
+      for (int i = i0; i < V && i < i0 + 32; ++i)
+        if (key[i] > 1 && !(f[i] < low)) again |= 1u << (i - i0);
+      while (__any_sync(kFull, again != 0)) {
+        const int at = __ffs(again) - 1;
+        unsigned long long wide = 0;
+        if (at >= 0) {
+          const int e = lane * V + i0 + at;
+          wide = key_of(sigmoid(static_cast<double>(load_logit<T>(p, t, e))) +
+                        static_cast<double>(bias_of(e)));
+          again &= again - 1;
+        }
+#pragma unroll
+        for (int i = i0; i < V && i < i0 + 32; ++i)
+          if (at == i - i0) key[i] = wide;
+      }
+    }
+  } else {
+    double f[V], m = -INFINITY, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      f[i] = e < p.E ? static_cast<double>(load_logit<T>(p, t, e)) : -INFINITY;
+      key[i] = f[i] == -INFINITY ? 0 : 2;
+      m = fmax(m, f[i]);
+    }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, s));
-  }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (p.sigmoid) {
-      f[i] = sigmoid(f[i]);
-    } else {
+    for (int i = 0; i < V; ++i) {
       f[i] = key[i] != 0 ? exp(f[i] - m) : 0.0;
       sum += f[i];
     }
-  }
-  if (!p.sigmoid) sum = warp_sum(sum);
+    sum = warp_sum(sum);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    if (!p.sigmoid) f[i] /= sum;
-    if (key[i] != 0 && p.bias != nullptr) {
-      const float b = p.bias[e];
-      if (b == -INFINITY) key[i] = 0;
-      f[i] += static_cast<double>(b);
+    for (int i = 0; i < V; ++i) {
+      f[i] /= sum;
+      if (key[i] != 0 && p.bias != nullptr) {
+        const float b = p.bias[lane * V + i];
+        if (b == -INFINITY) key[i] = 0;
+        f[i] += static_cast<double>(b);
+      }
+      if (key[i] != 0) key[i] = key_of(f[i]);
     }
-    if (key[i] != 0) key[i] = key_of(f[i]);
   }
   if (p.groups > 1) {
     unsigned long long mine = 0;
@@ -267,13 +305,23 @@ __device__ __noinline__ int choose_wide(const P &p, long long t) {
 // ------------------------------------------------------------------- router --
 
 // The bound of a score's error in a comparison, in units of 2^-24 of the largest
-// score. __expf is off by 2 + 1.173 |x| units of 2^-23, which times exp(-|x|), or
-// for a sigmoid s (1 - s), stays below 2 (0.65); __fdividef by two; the sum by as
-// many roundings as it has steps, and its terms.
-constexpr float kUnit = 5.9604645e-8f;  // 2^-24
+// score. ex2.approx is off by 2^-22, its argument by 2^-24 |x|, which times
+// exp(-|x|), or for a sigmoid s (1 - s), stays below 5 units (1.3); rcp.approx by
+// two; the sum by as many roundings as it has steps, and its terms.
 template <int V>
 __device__ __forceinline__ float score_error(const P &p, float sum) {
   return p.sigmoid ? 10.0f * kUnit : (V + 24.0f) * kUnit * (sum > 0.0f ? 1.0f / sum : 0.0f);
+}
+
+__device__ __forceinline__ float fast_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float fast_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Descending, by Batcher's odd-even merge.
@@ -300,42 +348,25 @@ struct Choice {
   unsigned next;  // the largest key left
 };
 
-// The k best of up to 8 keys a lane.
+// The k best of up to 8 keys a lane: heads sorted, the lowest bits of each V - 1
+// less the expert's place in the lane. Keys come back without those bits.
 template <int V>
-__device__ __forceinline__ Choice choose_sorted(const unsigned (&key)[V], unsigned (&head)[V], int k,
-                                                int *slots) {
+__device__ __forceinline__ Choice choose_sorted(unsigned (&head)[V], int k, int *slots) {
   const int lane = threadIdx.x & 31;
+  const unsigned before = (1u << lane) - 1u;
   Choice c = {-1, 0u, 0u};
-  unsigned long long mine = 0;  // the slots that this lane won, five bits each
-  int count = 0, r = 0;
+  int r = 0;
   for (; r < k; ++r) {
-    const unsigned best = warp_best(head[0]);
+    const unsigned mine = head[0] & ~(V - 1u), best = warp_best(mine);
     if (best == 0) break;
-    const unsigned from = __ballot_sync(kFull, head[0] == best);
-    if (lane == r) c.won = best;
-    if ((from & (0u - from)) == 1u << lane) {
-      mine |= static_cast<unsigned long long>(r) << (5 * count++);
+    const unsigned equal = __ballot_sync(kFull, mine == best);
+    const bool first = mine == best && (equal & before) == 0;
+    if (first) slots[r] = lane * V + (V - 1) - static_cast<int>(head[0] & (V - 1u));
 #pragma unroll
-      for (int i = 0; i + 1 < V; ++i) head[i] = head[i + 1];
-      head[V - 1] = 0;
-    }
+    for (int i = 0; i < V; ++i) head[i] = first ? (i + 1 < V ? head[i + 1] : 0u) : head[i];
+    c.won = lane == r ? best : c.won;
   }
-  c.next = warp_best(head[0]);
-  // Each of the lane's experts by its rank within the lane, ties in order.
-  if (count != 0) {
-    int rank[V] = {};
-#pragma unroll
-    for (int j = 1; j < V; ++j)
-#pragma unroll
-      for (int i = 0; i < j; ++i) {
-        const bool first = key[i] >= key[j];
-        rank[j] += first;
-        rank[i] += !first;
-      }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (rank[i] < count) slots[mine >> (5 * rank[i]) & 31u] = lane * V + i;
-  }
+  c.next = warp_best(head[0] & ~(V - 1u));
   __syncwarp();
   if (lane < r) c.expert = slots[lane];
   __syncwarp();
@@ -358,8 +389,8 @@ __device__ __forceinline__ Choice choose_any(unsigned (&key)[V], int k) {
 // needed; *bad: softmax of a NaN or of +infinity. `staged`: E integers and 32 of
 // the warp's own.
 template <int V, class T>
-__device__ __forceinline__ int choose(const P &p, long long t, unsigned *staged, float *m_out,
-                                      float *sum_out, bool *bad_out) {
+__device__ __forceinline__ int choose(const P &p, long long t, const float (&bias)[V], unsigned *staged,
+                                      float *m_out, float *sum_out, bool *bad_out) {
   constexpr int kVec = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   float x[V];
@@ -409,38 +440,35 @@ __device__ __forceinline__ int choose(const P &p, long long t, unsigned *staged,
   *bad_out = bad;
 
   unsigned key[V];
+  const float part = p.sigmoid ? 0.0f : (bad ? NAN : fast_inverse(sum));
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float f = x[i];
-    bool there = f != -INFINITY;  // else not available, or past the last expert
     if (p.compare_scores) {
-      f = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-f)) : (bad ? NAN : __fdividef(__expf(f - m), sum));
-      // (__fdividef of 2^126 and more gives 0, as it should be)
-      if (p.bias != nullptr && there) {
-        const float b = __ldg(p.bias + lane * V + i);
-        there = b != -INFINITY;
-        f += b;
-      }
+      f = p.sigmoid ? fast_inverse(1.0f + fast_exp(-f)) : fast_exp(f - m) * part;
+      f += bias[i];
     }
-    key[i] = there ? key_of(f) : 0u;
+    // a logit or a bias of -infinity: not available, or past the last expert
+    key[i] = x[i] != -INFINITY && bias[i] != -INFINITY ? key_of(f) : 0u;
   }
   const float err = score_error<V>(p, sum);
   bool unsure = false;
 
   constexpr bool kSort = V <= 8;
   [[maybe_unused]] unsigned head[V] = {};
-  if constexpr (kSort) {
+  auto sort = [&] {
 #pragma unroll
-    for (int i = 0; i < V; ++i) head[i] = key[i];
+    for (int i = 0; i < V; ++i) head[i] = key[i] == 0 ? 0u : (key[i] & ~(V - 1u)) | (V - 1 - i);
     sort_keys<V>(head);
-  }
+  };
+  if constexpr (kSort) sort();
   if (p.groups > 1) {
     // The best two of each group, by group_lanes lanes.
     const int g = lane / p.group_lanes, sub = lane % p.group_lanes;
     unsigned b1 = 0, b2 = 0;
     if (kSort && p.lanes_hold_groups) {
-      b1 = head[0];
-      b2 = V > 1 ? head[V > 1 ? 1 : 0] : 0u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) merge_best(b1, b2, key[i], 0u);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -481,47 +509,56 @@ __device__ __forceinline__ int choose(const P &p, long long t, unsigned *staged,
         const int of = (lane * V + i) / p.per_group;
         if (of >= p.groups || !(kept >> (of * p.group_lanes) & 1u)) key[i] = 0;
       }
-      if constexpr (kSort) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) head[i] = key[i];
-        sort_keys<V>(head);
-      }
+      if constexpr (kSort) sort();
     }
   }
 
+  int *slots = reinterpret_cast<int *>(staged + staged_ints(p) - kMaxSlots);
   Choice c;
-  if constexpr (kSort) c = choose_sorted<V>(key, head, p.k, reinterpret_cast<int *>(staged + staged_ints(p) - kMaxSlots));
+  if constexpr (kSort) c = choose_sorted<V>(head, p.k, slots);
   else c = choose_any<V>(key, p.k);
+  const unsigned next = __shfl_down_sync(kFull, c.won, 1);
+  const unsigned last = __shfl_sync(kFull, c.won, p.k - 1);
+  // Neighbours of the chosen that may stand the other way round, and the last of
+  // them and what is left: closer than the error, or equal but for the bits that
+  // the sort left out. (A NaN's key, 1, loses to those bits: whole keys again.)
+  auto close = [&](unsigned a, unsigned b) {
+    if (a == b) return true;
+    if (!p.compare_scores || b <= 8) return false;
+    const float u = value_of(a), v = value_of(b);
+    return u - v <= 2.0f * err + kUnit * (fabsf(u) + fabsf(v));
+  };
+  bool look = false;
+  if (sizeof(T) == 4 || p.compare_scores) {  // (bf16 logits have nothing in those bits)
+    look = lane + 1 < p.k && next != 0 && close(c.won, next);
+    look |= lane == p.k - 1 && last != 0 && c.next != 0 && close(last, c.next);
+  }
+  if (kSort) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) look |= key[i] == 1u;
+  }
+  if (!__any_sync(kFull, look | unsure)) return c.expert;
+
+  // By whole keys, and whether equal ones are of equal logits and biases.
+  float least = INFINITY;
+  if constexpr (kSort) c = choose_any<V>(key, p.k);
   if (p.compare_scores) {
-    // Two neighbours of the chosen, or the last of them and one that is left,
-    // that may stand the other way round. Equal logits and biases are equal.
-    auto close = [&](unsigned a, unsigned b) {
-      const float u = value_of(a), v = value_of(b);
-      return b > 1 && u - v <= 2.0f * err + kUnit * (fabsf(u) + fabsf(v));
-    };
     auto same = [&](int a, int b) {
       return load_logit<T>(p, t, a) == load_logit<T>(p, t, b) &&
              (p.bias == nullptr || p.bias[a] == p.bias[b]);
     };
-    const unsigned next = __shfl_down_sync(kFull, c.won, 1);
+    const unsigned next_key = __shfl_down_sync(kFull, c.won, 1);
     const int next_e = __shfl_down_sync(kFull, c.expert, 1);
-    if (lane + 1 < p.k && c.won > 1 && close(c.won, next)) unsure |= !same(c.expert, next_e);
-    const unsigned last = __shfl_sync(kFull, c.won, p.k - 1);
-    if (last > 1 && close(last, c.next)) {
-      const int last_e = __shfl_sync(kFull, c.expert, p.k - 1);
+    if (lane + 1 < p.k && next_key > 1 && close(c.won, next_key)) unsure |= !same(c.expert, next_e);
+    const unsigned last_key = __shfl_sync(kFull, c.won, p.k - 1);
+    const int last_e = __shfl_sync(kFull, c.expert, p.k - 1);
+    if (last_key > 1) {
+      least = value_of(last_key);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        // (a chosen one among them is the last's like, or is left for the bits)
-        if (key[i] > 1 && key[i] <= last && lane * V + i != last_e && close(last, key[i])) {
-          bool chosen = false;
-          if constexpr (kSort)
-            for (int r = 0; r < p.k; ++r)
-              chosen |= reinterpret_cast<int *>(staged + staged_ints(p) - kMaxSlots)[r] == lane * V + i;
-          if (!chosen) unsure |= !same(last_e, lane * V + i);
-        }
-      }
+      for (int i = 0; i < V; ++i)  // those that are left
+        if (key[i] > 1 && close(last_key, key[i])) unsure |= !same(last_e, lane * V + i);
     }
-    if (__any_sync(kFull, unsure)) return choose_wide<V, T>(p, t);
+    if (__any_sync(kFull, unsure)) return choose_wide<V, T>(p, t, least == INFINITY ? -INFINITY : least, err);
   }
   return c.expert;
 }
@@ -692,6 +729,10 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.count[e] = 0;
     __syncthreads();
   }
+  float bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    bias[i] = p.bias != nullptr && lane * V + i < p.E ? p.bias[lane * V + i] : 0.0f;
   const long long t1 = min(static_cast<long long>(p.T),
                            (static_cast<long long>(blockIdx.x) + 1) * p.chunk);
   for (long long t = static_cast<long long>(blockIdx.x) * p.chunk + warp; t < t1; t += warps) {
@@ -700,7 +741,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
     if (p.mask == nullptr || p.mask[t] != 0) {
       float m, sum;
       bool bad;
-      e = choose<V, T>(p, t, staged, &m, &sum, &bad);
+      e = choose<V, T>(p, t, bias, staged, &m, &sum, &bad);
       w = weight_of<T>(p, t, e, m, sum, bad);
     }
     if (lane < p.k) {
@@ -822,7 +863,10 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const B p)
     float d = p.renormalise ? w * (g - total * p.inv_scale) : w * g;
     if (p.sigmoid) d *= sigmoid(-l);
     // of an expert that stands in several slots, the sum by its first
-    const unsigned same = __match_any_sync(kFull, there ? e : -1 - lane);
+    unsigned same = 0;
+    for (int r = 0; r < p.k; ++r)
+      if (__shfl_sync(kFull, e, r) == e) same |= 1u << r;
+    if (!there) same = 0;
     bool writes = there;
     if (__any_sync(kFull, __popc(same) > 1)) {
       float both = 0.0f;
@@ -966,7 +1010,9 @@ int route_launch(const RouteArgs &a, int sm_count, cudaStream_t stream) {
   p.vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ldx % per16 == 0 && a.E % per16 == 0;
   p.scale = a.scale;
   p.plan = a.offsets != nullptr;
-  cut(p, a.T, a.T <= 64 ? 64 : 32, sm_count);
+  // Up to 24 tokens one CTA does all (a warp each); more, eight tokens a CTA: 64
+  // tokens of 256 experts took one CTA three rounds.
+  cut(p, a.T, a.T <= 24 ? 24 : 8, sm_count);
   void *ws = nullptr;
   if (p.plan && p.chunks > 1) {
     const int st = pool_alloc(&ws, static_cast<size_t>(p.chunks) * a.E * sizeof(int), stream);
