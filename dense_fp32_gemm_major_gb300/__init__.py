@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import operator
 import os
 import re
 
@@ -771,12 +772,41 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_codes = {}  # a tensor type's gemm_f32_type; filled at first use
+
+
+def _matrix(t, name, kind=None, device=None):
+    """(type code, device, rows, columns, pointer, leading dimension) of a 2-D
+    float32 or bfloat16 CUDA tensor, of the type and device where they are given."""
+    if not _codes:
+        import torch
+
+        _codes.update({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16})
+    try:
+        code, dev, (rows, cols), (ld, unit) = _codes[t.dtype], t.get_device(), t.shape, t.stride()
+        pointer = t.data_ptr()
+    except (AttributeError, KeyError, ValueError):
+        _segment_type(t, name)
+        raise TypeError(f"{name} must have 2 dimensions") from None
+    if dev < 0:
+        _segment_type(t, name)
+    if kind is not None and (code != kind or dev != device):
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, unlike the first operand")
+    if rows > 1:
+        if (unit != 1 and cols > 1) or ld < cols:
+            _check_rows((rows, cols), ld, unit, name)
+        return code, dev, rows, cols, pointer, (ld if cols else cols) or 1
+    if unit != 1 and cols > 1:
+        _check_rows((rows, cols), ld, unit, name)
+    return code, dev, rows, cols, pointer, cols or 1
+
+
 def _dense(t, name, dtype, shape, device):
     """The pointer of a contiguous tensor of the type, shape and device."""
     import torch
 
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda
-            or t.get_device() != device or tuple(t.shape) != shape or not t.is_contiguous()):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device
+            or t.shape != shape or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on the "
                         "operands' device")
     return t.data_ptr()
@@ -787,7 +817,7 @@ def _slots(t, name, device):
     import torch
 
     if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 2
-            or not t.is_cuda or t.get_device() != device or not t.is_contiguous()):
+            or t.get_device() != device or not t.is_contiguous()):
         raise TypeError(f"{name} must be a contiguous 2-D int32 tensor on the operands' device")
     count, k = t.shape
     if not 1 <= k <= MAX_ROUTE_SLOTS:
@@ -837,9 +867,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, grou
     """
     import torch
 
-    kind = _segment_type(logits, "logits")
-    dev = logits.get_device()
-    (t, e), px, ldx, _ = _matrices(logits, "logits", 2, kind, dev)
+    kind, dev, t, e, px, ldx = _matrix(logits, "logits")
     if not 1 <= e <= MAX_SEGMENTS:
         raise ValueError(f"{e} experts: 1 to {MAX_SEGMENTS}")
     if not 1 <= k <= min(e, MAX_ROUTE_SLOTS):
@@ -870,9 +898,7 @@ def route_backward(dweights, logits, experts, weights, score="softmax", renormal
     the logits' type."""
     import torch
 
-    kind = _segment_type(logits, "logits")
-    dev = logits.get_device()
-    (t, e), px, ldx, _ = _matrices(logits, "logits", 2, kind, dev)
+    kind, dev, t, e, px, ldx = _matrix(logits, "logits")
     t2, k, pe = _slots(experts, "experts", dev)
     if t2 != t:
         raise ValueError(f"logits has {t} tokens, experts {t2}")
@@ -911,9 +937,7 @@ def dispatch(x, places, out=None, stream=None):
     x D, float32 or bfloat16, ``places`` T x k int32 (``route``'s; outside out's
     rows: none). ``out`` is T k x D where it is not given; rows that no place names
     are not written. Its gradient is ``combine`` without weights."""
-    kind = _segment_type(x, "x")
-    dev = x.get_device()
-    (t, d), px, ldx, _ = _matrices(x, "x", 2, kind, dev)
+    kind, dev, t, d, px, ldx = _matrix(x, "x")
     t2, k, pp = _slots(places, "places", dev)
     if t2 != t:
         raise ValueError(f"x has {t} tokens, places {t2}")
@@ -935,9 +959,7 @@ def combine(y, places, weights=None, out=None, stream=None):
     k float32 (None: 1, which is the gradient of ``dispatch``)."""
     import torch
 
-    kind = _segment_type(y, "y")
-    dev = y.get_device()
-    (rows, d), py, ldy, _ = _matrices(y, "y", 2, kind, dev)
+    kind, dev, rows, d, py, ldy = _matrix(y, "y")
     t, k, pp = _slots(places, "places", dev)
     pw = None if weights is None else _dense(weights, "weights", torch.float32, (t, k), dev)
     out, po, ldo, _ = _result(out, "out", (t, d), y, kind, dev, stream)
@@ -951,10 +973,8 @@ def combine_backward(dout, y, places, weights=None, out=None, stream=None):
     and dweights[t, j] = dout[t] . y[places[t, j]], float32, 0 without a place."""
     import torch
 
-    kind = _segment_type(dout, "dout")
-    dev = dout.get_device()
-    (t, d), pd, ldd, _ = _matrices(dout, "dout", 2, kind, dev)
-    (rows, d2), py, ldy, _ = _matrices(y, "y", 2, kind, dev)
+    kind, dev, t, d, pd, ldd = _matrix(dout, "dout")
+    _, _, rows, d2, py, ldy = _matrix(y, "y", kind, dev)
     t2, k, pp = _slots(places, "places", dev)
     if t2 != t or d2 != d:
         raise ValueError(f"dout is {t} x {d}, places has {t2} tokens and y {d2} columns")
@@ -991,9 +1011,7 @@ def w4_matmul(x, q, scales, group, zeros=None, offsets=None, out=None, stream=No
     """
     import torch
 
-    kind = _segment_type(x, "x")
-    dev = x.get_device()
-    (m, k), px, ldx, _ = _matrices(x, "x", 2, kind, dev)
+    kind, dev, m, k, px, ldx = _matrix(x, "x")
     dim, groups, po = 2, 1, None
     if offsets is not None:
         dim = 3
@@ -1029,21 +1047,22 @@ def _tensor_list(tensors, name, device):
 
     types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16}
     try:
-        kinds = [types[t.dtype] for t in tensors]
-        devices = {t.get_device() for t in tensors}
+        kinds = list(map(types.__getitem__, map(operator.attrgetter("dtype"), tensors)))
+        devices = set(map(torch.Tensor.get_device, tensors))
         if not devices:
             return device, [], [], []
-        if min(devices) < 0 or not all([isinstance(t, torch.Tensor) for t in tensors]):
+        if min(devices) < 0:
             raise KeyError
-    except (AttributeError, KeyError):
+    except (AttributeError, KeyError, TypeError):
         raise TypeError(f"{name} must be float32 or bfloat16 CUDA tensors") from None
     if device is not None:
         devices.add(device)
     if len(devices) > 1:
         raise ValueError(f"{name} are not all on one device")
-    if not all([t.is_contiguous() for t in tensors]):
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
-    return devices.pop(), [t.data_ptr() for t in tensors], [t.numel() for t in tensors], kinds
+    return (devices.pop(), list(map(torch.Tensor.data_ptr, tensors)),
+            list(map(torch.Tensor.numel, tensors)), kinds)
 
 
 def _arrays(pointers, sizes, kinds):
