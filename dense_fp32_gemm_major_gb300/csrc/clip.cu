@@ -3,15 +3,15 @@
 //   norm = sqrt(sum over all tensors of x^2),  y = x min(1, limit / (norm + 1e-6))
 //
 // Two passes over memory that nothing can join: every factor waits for the last
-// element. The first sums squares, 16 KB of a tensor a CTA at a time; the second
+// element. The first sums squares, 32 KB of a tensor a CTA at a time; the second
 // scales, from the end backwards, so that what the first pass read last is still
 // in L2. The sums of the first pass's CTAs (a double each) are added by every CTA
 // of the second by itself, in one order, in place of a launch between them.
 //
 // Squares of fp32 leave fp32's range from 1.8e19 on and lose bits below 1e-19.
-// A thread adds the squares of its 16 to 32 values of a chunk in fp32, and where
+// A thread adds the squares of its 32 to 64 values of a chunk in fp32, and where
 // their sum is not between 2^-100 and 2^100 (and not of zeros alone), again in 64
-// bits; chunks are added in 64 bits. The FP64 units take one addition of 32
+// bits; chunks are added in 64 bits. The FP64 units take one addition of 64
 // elements, which hides behind the loads.
 //
 // The list of tensors travels as the kernels' argument (100 of them, or 1000 a
@@ -29,7 +29,7 @@
 namespace gemm {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kLoads = 4;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kLoads = 8;
 constexpr int kChunkBytes = kThreads * 16 * kLoads;
 constexpr int kFew = 100, kMany = 1000;  // tensors of a launch
 
@@ -221,7 +221,7 @@ __device__ __forceinline__ void scale_chunk(const Entry &e, int c, float f) {
           u[j] = *reinterpret_cast<const unsigned *>(&h);
         }
       }
-      yv[at] = make_uint4(u[0], u[1], u[2], u[3]);
+      __stcs(yv + at, make_uint4(u[0], u[1], u[2], u[3]));  // beside what is still to be read
     }
   }
   if (c == 0) {

@@ -6,10 +6,10 @@
 //   backward   dY[places[t][j]] = w[t][j] dO[t],  dw[t][j] = dO[t] . Y[places[t][j]]
 //
 // All three are bound by memory: a token's row is read once (or written once),
-// each expert's row once, whichever order they lie in. A warp takes a piece of
-// 1 to 2 KB of a token's row through all its places, with the loads of up to four
-// places in flight. Rows are read and written 16 bytes a lane where their starts
-// and widths allow it.
+// each expert's row once, whichever order they lie in. Up to eight warps share a
+// token's row, each a piece of 1 KB of it at a time through all its places, with the
+// loads of up to four places in flight. Rows are read and written 16 bytes a lane
+// where their starts and widths allow it.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -23,7 +23,6 @@ namespace gemm {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPlaces = 4;  // places whose loads are in flight together
 
 struct P {
   const void *token, *expert;
@@ -33,10 +32,10 @@ struct P {
   float *dweights;
   long long ld_token, ld_expert, ld_out;
   long long token_extent, expert_extent, out_extent;
-  long long rows, T;
-  int D, k;       // D in loads (kElems elements each)
+  long long rows;
+  int T, D, k;    // D in loads (kElems elements each)
   int pieces;     // of a row
-  int per_token;  // backward: warps of a token
+  int per_token;  // warps of a token: 1, 2, 4 or 8
 };
 
 // A lane's share of a row at a time: U loads of kElems elements, 32 loads apart.
@@ -99,7 +98,7 @@ __device__ __forceinline__ void load_row(const void *base, long long row_at, int
   for (int u = 0; u < R::U; ++u) {
     const int i = c + 32 * u;
     v[u] = i < D && index_ok(site, row_at + static_cast<long long>(i) * R::kElems, R::kElems, extent)
-               ? p[row_at / R::kElems + i]
+               ? __ldcs(p + row_at / R::kElems + i)  // read once
                : R::zero();
   }
 }
@@ -117,58 +116,66 @@ __device__ __forceinline__ void store_row(void *base, long long row_at, int c, i
 }
 
 __device__ __forceinline__ long long place_of(const P &p, long long s) {
-  const long long at = index_ok(kSiteLoadB, s, 1, p.T * p.k) ? p.places[s] : -1;
+  const long long at = index_ok(kSiteLoadB, s, 1, static_cast<long long>(p.T) * p.k) ? p.places[s] : -1;
   return at >= 0 && at < p.rows ? at : -1;
 }
 
-template <class T, bool VEC>
+// Calls of f(token, piece) for this warp's pieces.
+template <class F>
+__device__ __forceinline__ void for_pieces(const P &p, F f) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), per = p.per_token;
+  const int tokens = kWarps / per, sub = warp % per;
+  const long long step = static_cast<long long>(gridDim.x) * tokens;
+  for (long long t = static_cast<long long>(blockIdx.x) * tokens + warp / per; t < p.T; t += step)
+    for (int piece = sub; piece < p.pieces; piece += per) f(t, piece);
+}
+
+template <class T, bool VEC, int PLACES>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const P p) {
   using R = Row<T, VEC>;
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long units = p.T * p.pieces, step = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32; i < units;
-       i += step) {
-    const long long t = i / p.pieces;
-    const int c = static_cast<int>(i - t * p.pieces) * 32 * R::U + lane;
+  for_pieces(p, [&](long long t, int piece) {
+    const int c = piece * 32 * R::U + lane;
     typename R::Load v[R::U];
     load_row<R>(p.token, t * p.ld_token, c, p.D, kSiteCopySrc, p.token_extent, v);
-    for (int j = 0; j < p.k; ++j) {
-      const long long at = place_of(p, t * p.k + j);
-      if (at >= 0) store_row<R>(p.out, at * p.ld_out, c, p.D, p.out_extent, v);
+    for (int j0 = 0; j0 < p.k; j0 += PLACES) {
+      long long at[PLACES];
+#pragma unroll
+      for (int j = 0; j < PLACES; ++j) at[j] = j0 + j < p.k ? place_of(p, t * p.k + j0 + j) : -1;
+#pragma unroll
+      for (int j = 0; j < PLACES; ++j)
+        if (at[j] >= 0) store_row<R>(p.out, at[j] * p.ld_out, c, p.D, p.out_extent, v);
     }
-  }
+  });
 }
 
-template <class T, bool VEC>
+template <class T, bool VEC, int PLACES>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const P p) {
   using R = Row<T, VEC>;
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long units = p.T * p.pieces, step = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long i = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32; i < units;
-       i += step) {
-    const long long t = i / p.pieces;
-    const int c = static_cast<int>(i - t * p.pieces) * 32 * R::U + lane;
+  for_pieces(p, [&](long long t, int piece) {
+    const int c = piece * 32 * R::U + lane;
     float sum[R::U][R::kElems] = {};
-    for (int j0 = 0; j0 < p.k; j0 += kPlaces) {
-      typename R::Load v[kPlaces][R::U];
-      long long at[kPlaces];
-      float w[kPlaces];
+    for (int j0 = 0; j0 < p.k; j0 += PLACES) {
+      typename R::Load v[PLACES][R::U];
+      long long at[PLACES];
+      float w[PLACES];
 #pragma unroll
-      for (int j = 0; j < kPlaces; ++j) {
+      for (int j = 0; j < PLACES; ++j) {
         const long long s = t * p.k + j0 + j;
         at[j] = j0 + j < p.k ? place_of(p, s) : -1;
-        w[j] = at[j] >= 0 && p.weights != nullptr ? p.weights[s] : 1.0f;
+        w[j] = j0 + j < p.k && p.weights != nullptr ? p.weights[s] : 1.0f;
       }
 #pragma unroll
-      for (int j = 0; j < kPlaces; ++j)
+      for (int j = 0; j < PLACES; ++j)
         if (at[j] >= 0)
           load_row<R>(p.expert, at[j] * p.ld_expert, c, p.D, kSiteLoadA, p.expert_extent, v[j]);
 #pragma unroll
-      for (int j = 0; j < kPlaces; ++j) {
+      for (int j = 0; j < PLACES; ++j) {
         if (at[j] < 0) continue;
 #pragma unroll
         for (int u = 0; u < R::U; ++u) {
@@ -183,12 +190,12 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const P p) {
 #pragma unroll
     for (int u = 0; u < R::U; ++u) o[u] = R::pack(sum[u]);
     store_row<R>(p.out, t * p.ld_out, c, p.D, p.out_extent, o);
-  }
+  });
 }
 
 // `per_token` warps share a token's pieces; their sums of dw meet in shared
 // memory, in the order of the warps.
-template <class T, bool VEC>
+template <class T, bool VEC, int PLACES>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const P p) {
   using R = Row<T, VEC>;
   __shared__ float part[kWarps][32][33];  // warp, slot, lane
@@ -206,19 +213,25 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const P p) {
         const int c = piece * 32 * R::U + lane;
         typename R::Load d[R::U];
         load_row<R>(p.token, t * p.ld_token, c, p.D, kSiteLoadA, p.token_extent, d);
-        for (int j0 = 0; j0 < p.k; j0 += kPlaces) {
-          typename R::Load v[kPlaces][R::U];
-          long long at[kPlaces];
+        for (int j0 = 0; j0 < p.k; j0 += PLACES) {
+          typename R::Load v[PLACES][R::U];
+          long long at[PLACES];
+          float wj[PLACES];
 #pragma unroll
-          for (int j = 0; j < kPlaces; ++j) {
-            at[j] = j0 + j < p.k ? place_of(p, t * p.k + j0 + j) : -1;
+          for (int j = 0; j < PLACES; ++j) {
+            const long long s = t * p.k + j0 + j;
+            at[j] = j0 + j < p.k ? place_of(p, s) : -1;
+            wj[j] = j0 + j < p.k && p.weights != nullptr ? p.weights[s] : 1.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < PLACES; ++j) {
             if (at[j] >= 0 && p.dweights != nullptr)
               load_row<R>(p.expert, at[j] * p.ld_expert, c, p.D, kSiteLoadB, p.expert_extent, v[j]);
           }
 #pragma unroll
-          for (int j = 0; j < kPlaces; ++j) {
+          for (int j = 0; j < PLACES; ++j) {
             if (at[j] < 0) continue;
-            const float w = p.weights != nullptr ? p.weights[t * p.k + j0 + j] : 1.0f;
+            const float w = wj[j];
             float dot = 0.0f;
             typename R::Load o[R::U];
 #pragma unroll
@@ -255,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const P p) {
     if (t < p.T && sub == 0 && lane < p.k) {
       float sum = 0.0f;
       for (int w = 0; w < p.per_token; ++w) sum += dots[warp + w][lane];
-      if (index_ok(kSiteCStore, t * p.k + lane, 1, p.T * p.k)) p.dweights[t * p.k + lane] = sum;
+      if (index_ok(kSiteCStore, t * p.k + lane, 1, static_cast<long long>(p.T) * p.k)) p.dweights[t * p.k + lane] = sum;
     }
     __syncthreads();
   }
@@ -300,37 +313,45 @@ bool fill(const RowsArgs &a, P *p) {
   p->token_extent = matrix_extent(a.T, a.D, a.ld_token);
   p->expert_extent = matrix_extent(a.rows, a.D, a.ld_expert);
   p->rows = a.rows;
-  p->T = a.T;
+  p->T = static_cast<int>(a.T);
   p->k = static_cast<int>(a.k);
   const int elems = vec ? 16 / elem : 1, u = vec ? 2 : 8;
   p->D = static_cast<int>(a.D / elems);
   p->pieces = (p->D + 32 * u - 1) / (32 * u);
+  // As many warps a token as it has pieces.
+  p->per_token = 1;
+  while (p->per_token < kWarps && p->per_token < p->pieces) p->per_token *= 2;
   return vec;
 }
 
-template <template <class, bool> class K>
-int pick(bool bf16, bool vec, const P &p, long long blocks, int sms, cudaStream_t s) {
-  if (bf16)
-    return vec ? launch(K<__nv_bfloat16, true>::kernel(), p, blocks, sms, s)
-               : launch(K<__nv_bfloat16, false>::kernel(), p, blocks, sms, s);
-  return vec ? launch(K<float, true>::kernel(), p, blocks, sms, s)
-             : launch(K<float, false>::kernel(), p, blocks, sms, s);
+template <template <class, bool, int> class K, bool VEC, int PLACES>
+int pick_type(bool bf16, const P &p, int sms, cudaStream_t s) {
+  const int tokens = kWarps / p.per_token;
+  const long long blocks = (static_cast<long long>(p.T) + tokens - 1) / tokens;
+  return bf16 ? launch(K<__nv_bfloat16, VEC, PLACES>::kernel(), p, blocks, sms, s)
+              : launch(K<float, VEC, PLACES>::kernel(), p, blocks, sms, s);
 }
 
-template <class T, bool VEC>
-struct Dispatch {
-  static auto kernel() { return dispatch_kernel<T, VEC>; }
-};
-template <class T, bool VEC>
-struct Combine {
-  static auto kernel() { return combine_kernel<T, VEC>; }
-};
-template <class T, bool VEC>
-struct Backward {
-  static auto kernel() { return backward_kernel<T, VEC>; }
-};
+// Places in flight: what a token has, up to four (few registers, and so more
+// warps, where it has one or two).
+template <template <class, bool, int> class K>
+int pick(bool bf16, bool vec, const P &p, int sms, cudaStream_t s) {
+  if (vec) return p.k <= 2 ? pick_type<K, true, 2>(bf16, p, sms, s) : pick_type<K, true, 4>(bf16, p, sms, s);
+  return p.k <= 2 ? pick_type<K, false, 2>(bf16, p, sms, s) : pick_type<K, false, 4>(bf16, p, sms, s);
+}
 
-long long blocks_of(const P &p) { return (p.T * p.pieces + kWarps - 1) / kWarps; }
+template <class T, bool VEC, int PLACES>
+struct Dispatch {
+  static auto kernel() { return dispatch_kernel<T, VEC, PLACES>; }
+};
+template <class T, bool VEC, int PLACES>
+struct Combine {
+  static auto kernel() { return combine_kernel<T, VEC, PLACES>; }
+};
+template <class T, bool VEC, int PLACES>
+struct Backward {
+  static auto kernel() { return backward_kernel<T, VEC, PLACES>; }
+};
 
 }  // namespace
 
@@ -340,27 +361,21 @@ int rows_dispatch_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
   P p;
   const bool vec = fill(a, &p);
   p.out_extent = matrix_extent(a.rows, a.D, a.ld_out);
-  return pick<Dispatch>(a.bf16, vec, p, blocks_of(p), sm_count, stream);
+  return pick<Dispatch>(a.bf16, vec, p, sm_count, stream);
 }
 
 int rows_combine_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
   P p;
   const bool vec = fill(a, &p);
   p.out_extent = matrix_extent(a.T, a.D, a.ld_out);
-  return pick<Combine>(a.bf16, vec, p, blocks_of(p), sm_count, stream);
+  return pick<Combine>(a.bf16, vec, p, sm_count, stream);
 }
 
 int rows_backward_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
   P p;
   const bool vec = fill(a, &p);
   p.out_extent = matrix_extent(a.rows, a.D, a.ld_out);
-  // Warps of a token: as many as it has pieces while the tokens alone do not
-  // fill the GPU.
-  p.per_token = 1;
-  while (p.per_token < kWarps && p.per_token < p.pieces && a.T * p.per_token < 16LL * sm_count)
-    p.per_token *= 2;
-  const long long tokens = kWarps / p.per_token;
-  return pick<Backward>(a.bf16, vec, p, (a.T + tokens - 1) / tokens, sm_count, stream);
+  return pick<Backward>(a.bf16, vec, p, sm_count, stream);
 }
 
 }  // namespace gemm

@@ -1,9 +1,9 @@
 """The norm of many tensors and their clipping by it, on the GPU against the
 definition in 64 bits.
 
-The squares of at most 32 values are added in fp32 (33 roundings of 2^-24, half of
-which show in the root), everything else in 64 bits, and the norm is rounded once:
-18 2^-24 of it. The factor is as good, and rounded once; a product is rounded once
+The squares of at most 64 values are added in fp32 (each through 16 roundings of
+2^-24, half of which show in the root), everything else in 64 bits, and the norm is
+rounded once: below 18 2^-24 of it. The factor is as good, and rounded once; a product is rounded once
 to its type (finfo.eps / 2), below the type's normal numbers to half of its
 smallest one.
 """
