@@ -3,15 +3,18 @@
 //   norm = sqrt(sum over all tensors of x^2),  y = x min(1, limit / (norm + 1e-6))
 //
 // Two passes over memory that nothing can join: every factor waits for the last
-// element. The first sums squares, 32 KB of a tensor a CTA at a time; the second
+// element. The first sums squares, 16 KB of a tensor a CTA at a time, the next
+// ones under way meanwhile; the second
 // scales, from the end backwards, so that what the first pass read last is still
-// in L2. The sums of the first pass's CTAs (a double each) are added by every CTA
-// of the second by itself, in one order, in place of a launch between them.
+// in L2. The sums of the first pass's CTAs (a double each, three CTAs an SM) are
+// added by a warp of every CTA of the second by itself, in one order, in place of a
+// launch between them. (By all threads, root and quotient too, the FP64 units took a
+// fifth of the pass.)
 //
 // Squares of fp32 leave fp32's range from 1.8e19 on and lose bits below 1e-19.
-// A thread adds the squares of its 32 to 64 values of a chunk in fp32, and where
+// A thread adds the squares of its 16 to 32 values of a chunk in fp32, and where
 // their sum is not between 2^-100 and 2^100 (and not of zeros alone), again in 64
-// bits; chunks are added in 64 bits. The FP64 units take one addition of 64
+// bits; chunks are added in 64 bits. The FP64 units take one addition of 32
 // elements, which hides behind the loads.
 //
 // The list of tensors travels as the kernels' argument (100 of them, or 1000 a
@@ -29,7 +32,7 @@
 namespace gemm {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kLoads = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kLoads = 4;
 constexpr int kChunkBytes = kThreads * 16 * kLoads;
 constexpr int kFew = 100, kMany = 1000;  // tensors of a launch
 
@@ -92,27 +95,51 @@ __device__ __forceinline__ double squares(const float *v, int n) {
   return s;
 }
 
-// Squares of a chunk, this thread's.
+// A chunk's vectors, this thread's: 16-byte loads, kThreads apart.
+struct Chunk {
+  const Entry *e;  // null: none
+  int c;           // of the tensor's chunks
+  uint4 w[kLoads];
+};
+
 template <class T>
-__device__ __forceinline__ double chunk_squares(const Entry &e, int c) {
+__device__ __forceinline__ void load_vectors(const Entry &e, int c, uint4 (&w)[kLoads]) {
   constexpr int kVec = 16 / sizeof(T);
   const T *x = static_cast<const T *>(e.src);
   const int head = head_of(e, sizeof(T));
-  const long long vecs = (e.n - head) / kVec, tail = head + vecs * kVec;
+  const long long vecs = (e.n - head) / kVec;
   const long long v0 = static_cast<long long>(c) * (kThreads * kLoads) + threadIdx.x;
   const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
-  uint4 w[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const long long at = v0 + i * kThreads;
     w[i] = at < vecs && index_ok(kSiteReduceIn, head + at * kVec, kVec, e.n)
-               ? __ldg(xv + at) : make_uint4(0, 0, 0, 0);
+               ? xv[at] : make_uint4(0, 0, 0, 0);
   }
+}
+
+template <int CAP>
+__device__ __forceinline__ Chunk load_chunk(const List<CAP> &p, int c, bool there) {
+  Chunk k;
+  k.e = nullptr;
+  if (!there) return k;
+  k.e = &p.e[entry_of(p, c)];
+  k.c = c - k.e->chunk;
+  if (k.e->flags & kBf16) load_vectors<__nv_bfloat16>(*k.e, k.c, k.w);
+  else load_vectors<float>(*k.e, k.c, k.w);
+  return k;
+}
+
+// Squares of a chunk, this thread's.
+template <class T>
+__device__ __forceinline__ double chunk_squares(const Chunk &k) {
+  constexpr int kVec = 16 / sizeof(T);
+  const Entry &e = *k.e;
   float local = 0.0f;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     float v[kVec], s = 0.0f;
-    unpack<T>(w[i], v);
+    unpack<T>(k.w[i], v);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) s = fmaf(v[j], v[j], s);
     local += s;
@@ -121,19 +148,22 @@ __device__ __forceinline__ double chunk_squares(const Entry &e, int c) {
   if (!(local >= 0x1p-100f && local <= 0x1p100f)) {
     unsigned any = 0;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) any |= w[i].x | w[i].y | w[i].z | w[i].w;
+    for (int i = 0; i < kLoads; ++i) any |= k.w[i].x | k.w[i].y | k.w[i].z | k.w[i].w;
     sum = 0.0;
     if (any != 0) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         float v[kVec];
-        unpack<T>(w[i], v);
+        unpack<T>(k.w[i], v);
         sum += squares(v, kVec);
       }
     }
   }
   // the first chunk takes the elements around the vectors too
-  if (c == 0) {
+  if (k.c == 0) {
+    const T *x = static_cast<const T *>(e.src);
+    const int head = head_of(e, sizeof(T));
+    const long long tail = head + (e.n - head) / kVec * kVec;
     const int ends = head + static_cast<int>(e.n - tail);
     if (static_cast<int>(threadIdx.x) < ends) {
       const int t = threadIdx.x;
@@ -147,7 +177,7 @@ __device__ __forceinline__ double chunk_squares(const Entry &e, int c) {
   return sum;
 }
 
-// Sum over the CTA, in every thread.
+// Sum over the CTA, in thread 0.
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double part[kWarps];
 #pragma unroll
@@ -155,8 +185,9 @@ __device__ __forceinline__ double block_sum(double v) {
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.0;
+  if (threadIdx.x == 0)
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += part[w];
+    for (int w = 0; w < kWarps; ++w) v += part[w];
   return v;
 }
 
@@ -165,10 +196,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   grid_dependency_wait();
   grid_launch_dependents();
   double sum = 0.0;
-  for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-    const Entry &e = p.e[entry_of(p, c)];
-    sum += e.flags & kBf16 ? chunk_squares<__nv_bfloat16>(e, c - e.chunk)
-                           : chunk_squares<float>(e, c - e.chunk);
+  const int step = static_cast<int>(gridDim.x);
+  Chunk now = load_chunk(p, blockIdx.x, static_cast<int>(blockIdx.x) < p.chunks);
+  for (int c = blockIdx.x; c < p.chunks; c += step) {
+    const Chunk next = load_chunk(p, c + step, p.chunks - c > step);
+    sum += now.e->flags & kBf16 ? chunk_squares<__nv_bfloat16>(now) : chunk_squares<float>(now);
+    now = next;
   }
   sum = block_sum(sum);
   const long long at = p.first + blockIdx.x;
@@ -185,32 +218,26 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) {
 }
 
 template <class T>
-__device__ __forceinline__ void scale_chunk(const Entry &e, int c, float f) {
+__device__ __forceinline__ void scale_chunk(const Chunk &k, float f) {
   constexpr int kVec = 16 / sizeof(T);
+  const Entry &e = *k.e;
   const T *x = static_cast<const T *>(e.src);
   T *y = static_cast<T *>(e.dst);
   const int head = head_of(e, sizeof(T));
   const long long vecs = (e.n - head) / kVec, tail = head + vecs * kVec;
-  const long long first = static_cast<long long>(c) * (kThreads * kLoads);
+  const long long first = static_cast<long long>(k.c) * (kThreads * kLoads);
   if (e.flags & kScalar) {  // the two lie on boundaries of their own
     const long long last = min(first + kThreads * kLoads, vecs);
     for (long long i = head + first * kVec + threadIdx.x; i < head + last * kVec; i += kThreads)
       if (index_ok(kSiteReduceIn, i, 1, e.n)) y[i] = rounded<T>(static_cast<float>(x[i]) * f);
   } else {
-    const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
     uint4 *yv = reinterpret_cast<uint4 *>(y + head);
-    uint4 w[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const long long at = first + threadIdx.x + i * kThreads;
-      if (at < vecs && index_ok(kSiteReduceIn, head + at * kVec, kVec, e.n)) w[i] = xv[at];
-    }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const long long at = first + threadIdx.x + i * kThreads;
       if (!(at < vecs && index_ok(kSiteReduceOut, head + at * kVec, kVec, e.n))) continue;
       float v[kVec];
-      unpack<T>(w[i], v);
+      unpack<T>(k.w[i], v);
       unsigned u[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -224,7 +251,7 @@ __device__ __forceinline__ void scale_chunk(const Entry &e, int c, float f) {
       __stcs(yv + at, make_uint4(u[0], u[1], u[2], u[3]));  // beside what is still to be read
     }
   }
-  if (c == 0) {
+  if (k.c == 0) {
     const int ends = head + static_cast<int>(e.n - tail), t = threadIdx.x;
     if (t < ends) {
       const long long at = t < head ? t : tail + (t - head);
@@ -235,21 +262,36 @@ __device__ __forceinline__ void scale_chunk(const Entry &e, int c, float f) {
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ List<CAP> p) {
+  __shared__ float factor;
   grid_dependency_wait();
   grid_launch_dependents();
-  double sum = 0.0;
-  for (long long i = threadIdx.x; i < p.slots; i += kThreads)
-    if (index_ok(kSiteReducePartial, i, 1, p.slots)) sum += p.partials[i];
-  const double norm = sqrt(block_sum(sum));
-  if (blockIdx.x == 0 && threadIdx.x == 0 && p.norm != nullptr) *p.norm = static_cast<float>(norm);
-  const double ratio = static_cast<double>(p.limit) / (norm + 1e-6);
-  const float f = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);  // a NaN stays one
-  for (int i = blockIdx.x; i < p.chunks; i += gridDim.x) {
-    const int c = p.chunks - 1 - i;
-    const Entry &e = p.e[entry_of(p, c)];
-    if (f == 1.0f && (e.flags & kInPlace)) continue;
-    if (e.flags & kBf16) scale_chunk<__nv_bfloat16>(e, c - e.chunk, f);
-    else scale_chunk<float>(e, c - e.chunk, f);
+  // A thread reads no element that another one writes (a tensor in place is its own
+  // operand, element by element), so the first ones may be on their way.
+  const int step = static_cast<int>(gridDim.x);
+  Chunk now = load_chunk(p, p.chunks - 1 - static_cast<int>(blockIdx.x),
+                         static_cast<int>(blockIdx.x) < p.chunks);
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (long long i = threadIdx.x; i < p.slots; i += 32)
+      if (index_ok(kSiteReducePartial, i, 1, p.slots)) sum += p.partials[i];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(sum), ratio = static_cast<double>(p.limit) / (norm + 1e-6);
+      if (blockIdx.x == 0 && p.norm != nullptr) *p.norm = static_cast<float>(norm);
+      factor = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);  // a NaN stays one
+    }
+  }
+  __syncthreads();
+  const float f = factor;
+  for (int i = blockIdx.x; i < p.chunks; i += step) {
+    const Chunk next = load_chunk(p, p.chunks - 1 - i - step, p.chunks - i > step);
+    if (!(f == 1.0f && (now.e->flags & kInPlace))) {
+      if (now.e->flags & kBf16) scale_chunk<__nv_bfloat16>(now, f);
+      else scale_chunk<float>(now, f);
+    }
+    now = next;
   }
 }
 
@@ -292,7 +334,7 @@ void fill(const ClipArgs &a, int64_t i0, int64_t *next, List<CAP> *p) {
 }
 
 int grid_of(int chunks, int sms) {
-  const int most = 8 * (sms > 0 ? sms : 1);
+  const int most = 3 * (sms > 0 ? sms : 1);
   return chunks < most ? (chunks > 0 ? chunks : 1) : most;
 }
 
