@@ -3,18 +3,18 @@
 //   norm = sqrt(sum over all tensors of x^2),  y = x min(1, limit / (norm + 1e-6))
 //
 // Two passes over memory that nothing can join: every factor waits for the last
-// element. The first sums squares, 16 KB of a tensor a CTA at a time, the next
+// element. The first sums squares, 32 KB of a tensor a CTA at a time, the next
 // ones under way meanwhile; the second
 // scales, from the end backwards, so that what the first pass read last is still
-// in L2. The sums of the first pass's CTAs (a double each, three CTAs an SM) are
+// in L2. The sums of the first pass's CTAs (a double each, two CTAs an SM) are
 // added by a warp of every CTA of the second by itself, in one order, in place of a
 // launch between them. (By all threads, root and quotient too, the FP64 units took a
 // fifth of the pass.)
 //
 // Squares of fp32 leave fp32's range from 1.8e19 on and lose bits below 1e-19.
-// A thread adds the squares of its 16 to 32 values of a chunk in fp32, and where
+// A thread adds the squares of its 32 to 64 values of a chunk in fp32, and where
 // their sum is not between 2^-100 and 2^100 (and not of zeros alone), again in 64
-// bits; chunks are added in 64 bits. The FP64 units take one addition of 32
+// bits; chunks are added in 64 bits. The FP64 units take one addition of 64
 // elements, which hides behind the loads.
 //
 // The list of tensors travels as the kernels' argument (100 of them, or 1000 a
@@ -32,7 +32,7 @@
 namespace gemm {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kLoads = 4;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kLoads = 8;
 constexpr int kChunkBytes = kThreads * 16 * kLoads;
 constexpr int kFew = 100, kMany = 1000;  // tensors of a launch
 
@@ -334,7 +334,7 @@ void fill(const ClipArgs &a, int64_t i0, int64_t *next, List<CAP> *p) {
 }
 
 int grid_of(int chunks, int sms) {
-  const int most = 3 * (sms > 0 ? sms : 1);
+  const int most = 2 * (sms > 0 ? sms : 1);
   return chunks < most ? (chunks > 0 ? chunks : 1) : most;
 }
 

@@ -143,6 +143,24 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
       : "memory");
 }
 
+// Loads that stay where they are written: ahead of their use, which the compiler
+// would move them back to.
+__device__ __forceinline__ float load_ahead(const float *p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ __nv_bfloat16 load_ahead(const __nv_bfloat16 *p) {
+  unsigned short v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return __ushort_as_bfloat16(v);
+}
+__device__ __forceinline__ uint32_t load_ahead(const uint8_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // D[tmem] (+)= A[tmem] B[smem]^T, kind::f16 with bf16 operands, 128 lanes.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {
@@ -337,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
   using A = Tile<T, COLS, PERIOD>;
   constexpr int kTimes = A::kTimes / kGroups, kColumns = tmem_columns(COLS, kTimes), kStages = stages_of(COLS);
   extern __shared__ uint8_t raw[];
-  uint8_t *ws = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
+  uint8_t *ws = raw + (-smem_addr(raw) & 1023u);  // (an offset: the compiler still sees shared memory)
   uint8_t *as = ws + kStages * kWBytes;
   // the warpgroups' sums of a tile, when all stages have been used
   float *sums = reinterpret_cast<float *>(ws);
@@ -489,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
           const unsigned at = (static_cast<unsigned>(b) * kGroups + h) * kTimes + c;
           const int gi = min(static_cast<int>(p.per_group == 1 ? at : at / p.per_group), p.row_groups - 1);
           s_next[c] = index_ok(kSiteLoadB, s_at + gi, 1, p.s_extent)
-                          ? __ldg(static_cast<const T *>(p.scales) + s_at + gi) : T(0.0f);
+                          ? load_ahead(static_cast<const T *>(p.scales) + s_at + gi) : T(0.0f);
           z_next[c] = 8;
           if (p.zeros != nullptr && index_ok(kSiteLoadB, z_at + gi, 1, p.z_extent))
-            z_next[c] = __ldg(p.zeros + z_at + gi);
+            z_next[c] = load_ahead(p.zeros + z_at + gi);
         }
       };
       float sum[A::kRows] = {}, s_now[kTimes], z_now[kTimes];
@@ -512,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
           for (int i = 0; i < COLS / 16; ++i) tmem_regs_ready(v[i]);
           const float *asums =
               reinterpret_cast<const float *>(at + A::kSums) + (h * kTimes + c) * A::kTerms * A::kRows;
-          float as4[4];
+          [[maybe_unused]] float as4[4];
 #pragma unroll
           for (int t = 0; t < A::kRows; ++t) {
             float u;
