@@ -835,11 +835,12 @@ Routing = collections.namedtuple("Routing", "experts weights offsets order place
 
 
 def _new_routing(t, e, k, device):
+    # (five pieces of memory: 7 us of the host; views into one, 13)
     import torch
 
     empty = torch.empty
     experts = empty((t, k), dtype=torch.int32, device=device)
-    return Routing(experts, empty((t, k), device=device, dtype=torch.float32),
+    return Routing(experts, empty((t, k), dtype=torch.float32, device=device),
                    empty((e + 1,), dtype=torch.int64, device=device),
                    empty((t * k,), dtype=torch.int32, device=device), torch.empty_like(experts))
 

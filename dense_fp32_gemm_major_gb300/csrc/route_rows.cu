@@ -375,6 +375,8 @@ int rows_backward_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
   P p;
   const bool vec = fill(a, &p);
   p.out_extent = matrix_extent(a.rows, a.D, a.ld_out);
+  // Warps of one token meet at its end: no more of them than fill the GPU.
+  while (p.per_token > 1 && a.T * p.per_token >= 32LL * sm_count) p.per_token /= 2;
   return pick<Backward>(a.bf16, vec, p, sm_count, stream);
 }
 

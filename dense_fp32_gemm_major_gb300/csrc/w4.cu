@@ -904,9 +904,12 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
   p.timeout_ns = 2000000000ull + 2000ull * static_cast<unsigned long long>(a.K);
   const int64_t tiles = (a.N + kTileN - 1) / kTileN;
   const int64_t used = a.groups < a.M ? a.groups : a.M;  // segments with rows, at most
-  p.split = 1;
-  while (p.split < kMaxSplit && 4 * p.split <= p.blocks && tiles * used * p.split < 2 * sm_count)
-    p.split *= 2;
+  // CTAs of a tile: as many as an SM has two of at a time (a third would wait for a
+  // round of its own: 4096 x 11008, 86 tiles), and two blocks each.
+  int64_t split = 2 * static_cast<int64_t>(sm_count) / (tiles * used);
+  if (split > p.blocks / 2) split = p.blocks / 2;
+  if (split > kMaxSplit) split = kMaxSplit;
+  p.split = split < 1 ? 1 : static_cast<int>(split);
 
   Prep q = {};
   q.A = a.A;
