@@ -20,10 +20,11 @@
 // FP64 units are off the path.
 //
 // Plan. A stable counting sort: each CTA of the router counts its chunk's slots
-// by expert; a second launch (a programmatic dependent) sums the counts of the
-// chunks before its own and ranks its slots, a warp 32 at a time by matching
-// experts. Few tokens take one CTA, which does both. Counts are integers: their
-// order of addition does not show.
+// by expert, sums the counts of the chunks before its own and ranks its slots, a
+// warp 32 at a time by matching experts. Up to 24 tokens one CTA does it all, up to
+// 192 the CTAs of a cluster, which read each other's counts in shared memory; of
+// more, a second launch (a programmatic dependent) takes the counts from global
+// memory. Counts are integers: their order of addition does not show.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -621,6 +622,14 @@ __device__ __forceinline__ PlanShared plan_shared(int *smem, int E) {
 }
 __host__ __device__ constexpr int plan_ints(int E, int warps) { return (3 + warps) * E + 1; }
 
+__device__ __forceinline__ int read_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
 // Rows of slots [s0, s1), whose experts' first rows are in sh.base. All threads.
 __device__ void rank_slots(const P &p, const PlanShared &sh, int s0, int s1, long long slots) {
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31, E = p.E;
@@ -673,7 +682,21 @@ __device__ void rank_slots(const P &p, const PlanShared &sh, int s0, int s1, lon
 // CTA's own in sh.count.
 __device__ void plan_chunk(const P &p, const PlanShared &sh, int c, long long slots) {
   const int E = p.E, tid = threadIdx.x;
-  if (p.chunks > 1) {
+  if (p.chunks > 1 && p.hist == nullptr) {  // the cluster's
+    cluster_sync();
+    for (int e = tid; e < E; e += blockDim.x) {
+      int before = 0, all = 0;
+      for (int j = 0; j < p.chunks; ++j) {
+        const int n = read_cluster(smem_addr(sh.count + e), static_cast<unsigned>(j));
+        all += n;
+        before += j < c ? n : 0;
+      }
+      sh.base[e] = before;
+      sh.warp[e] = all;
+    }
+    cluster_sync();  // all counts are read
+    for (int e = tid; e < E; e += blockDim.x) sh.count[e] = sh.warp[e];
+  } else if (p.chunks > 1) {
     for (int e = tid; e < E; e += blockDim.x) sh.count[e] = sh.base[e] = 0;
     __syncthreads();
     // several threads an expert, each over a part of the chunks
@@ -755,14 +778,14 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
   }
   if (!p.plan) return;
   __syncthreads();
-  if (p.chunks > 1) {
+  if (p.hist != nullptr) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
       const long long at = static_cast<long long>(blockIdx.x) * p.E + e;
       if (index_ok(kSitePartialWrite, at, 1, static_cast<long long>(p.chunks) * p.E))
         p.hist[at] = sh.count[e];
     }
   } else {
-    plan_chunk(p, sh, 0, slots);  // reads the experts behind the barrier above
+    plan_chunk(p, sh, blockIdx.x, slots);  // reads the experts behind the barrier above
   }
 }
 
@@ -907,17 +930,22 @@ __global__ void __launch_bounds__(kBackThreads) route_backward_kernel(const B p)
 // -------------------------------------------------------------------- host --
 
 template <class K, class A>
-int launch(K kernel, const A &p, unsigned grid, int threads, size_t smem, cudaStream_t stream) {
+int launch(K kernel, const A &p, unsigned grid, int threads, size_t smem, cudaStream_t stream,
+           unsigned cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   // Above the 48 KiB default: set on the current device, which keeps it (every
   // call, where it is needed; it takes no launch).
   if (smem > 48 * 1024 &&
@@ -948,7 +976,7 @@ int launch_v(P &p, cudaStream_t stream) {
   if (threads > want) threads = static_cast<int>((want + 127) / 128 * 128);
   p.plan_warps = plan_warps_of(p.E, threads / 32 < 16 ? threads / 32 : 16);
   return launch(route_kernel<V, T>, p, static_cast<unsigned>(p.chunks), threads, smem_of(p, threads),
-                stream);
+                stream, p.plan && p.hist == nullptr ? static_cast<unsigned>(p.chunks) : 1u);
 }
 
 template <class T>
@@ -1012,9 +1040,11 @@ int route_launch(const RouteArgs &a, int sm_count, cudaStream_t stream) {
   p.plan = a.offsets != nullptr;
   // Up to 24 tokens one CTA does all (a warp each); more, eight tokens a CTA: 64
   // tokens of 256 experts took one CTA three rounds.
-  cut(p, a.T, a.T <= 24 ? 24 : 8, sm_count);
+  constexpr int kCluster = 8;
+  const bool together = a.T <= 24 * kCluster;
+  cut(p, a.T, a.T <= 24 ? 24 : 8, together ? kCluster : sm_count);
   void *ws = nullptr;
-  if (p.plan && p.chunks > 1) {
+  if (p.plan && !together) {
     const int st = pool_alloc(&ws, static_cast<size_t>(p.chunks) * a.E * sizeof(int), stream);
     if (st != kOk) return st;
     p.hist = static_cast<int *>(ws);
