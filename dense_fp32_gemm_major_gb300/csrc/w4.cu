@@ -812,9 +812,11 @@ int launch_both(const CUtensorMap &map, P p, const Prep &prep, int groups, cudaS
   constexpr int kStages = stages_of(COLS);
   static_assert(kGroups * A::kRows * kTileN * 4 <= kStages * kWBytes, "sums stand where weights did");
   size_t smem = 1024 + kStages * (kWBytes + A::kStep);
-  // Two CTAs of an SM, or one, as TMEM has room for: a third would wait for it,
-  // and its cluster with it.
-  const size_t least = tmem_columns(COLS, 4 / PERIOD) == 512 ? 116 * 1024 : 77 * 1024;
+  // Shared memory keeps an SM to the CTAs that its TMEM has room for: two of 256
+  // columns or one of 512, and none beside a dense or a segmented product's (512
+  // columns). One more would wait in its allocation for another to leave, and, on
+  // two streams, clusters could wait for each other.
+  const size_t least = tmem_columns(COLS, 4 / PERIOD) == 512 ? 128 * 1024 : 100 * 1024;
   if (smem < least) smem = least;
   Prep q = prep;
   q.to_extent = (static_cast<long long>(p.M) / A::kRows + groups + 1) * p.blocks * A::kStep;
