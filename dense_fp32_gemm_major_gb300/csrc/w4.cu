@@ -62,15 +62,21 @@ __device__ int g_w4_status;  // first error recorded by a kernel of this unit
 // A as operands: for each tile of rows and each block of 256 k, four panels of 64
 // k (a line of 128 bytes for each row and term, swizzled); a byte a row, load8's
 // exponent; and the sums of the row's terms between two times that scales are
-// applied. A segment's tiles follow each other from tile r0 / rows + g on (r0: its
-// first row, g: its number), which no two segments share.
+// applied.
 struct Prep {
   const void *A;
   uint8_t *to;
   const int64_t *offsets;
   long long lda, a_extent, to_extent;
   int M, K, blocks, a_vec;
+  int by_rows;  // see first_tile
 };
+
+// A segment's tiles follow each other from here on, which no two segments share (r0:
+// its first row, g: its number): M / rows + groups of them, or M where that is less.
+__host__ __device__ __forceinline__ long long first_tile(bool by_rows, long long r0, int rows, int g) {
+  return by_rows ? r0 : r0 / rows + g;
+}
 
 struct P {
   const uint8_t *A;  // Prep::to
@@ -83,6 +89,7 @@ struct P {
   int blocks, split;  // of k; CTAs that share them
   int per_group;      // times that the scales are applied to a group
   int z_step;         // 0: one matrix for all segments
+  int by_rows;
   unsigned long long timeout_ns;
 };
 
@@ -186,19 +193,19 @@ __device__ __forceinline__ float read_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-
 // Exponents of A's scaling (powers of two): kScale as long as a row's 256 values
 // are below 2^16 (biased exponent kLargest); else, that of the largest of them
 // above kLargest less. Sums are of units of 2^-133.
 constexpr int kScale = 110, kUnit = 133, kLargest = 127 + 15;
+constexpr float kLargeScale = 0x1p104f;
 
 __device__ __forceinline__ float power(int e) {  // 2^e, e in -126 .. 127
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
 // Eight neighbouring k of a row as operands, term by term, and their sums, those
-// of A's scaled values times 2^-kUnit; returns the biased exponent of the warp's
-// 256 values' largest where it is above kLargest, else 0.
+// of A's scaled values times 2^-kUnit; returns how far the exponent of the warp's
+// 256 values' largest is above kLargest.
 template <class T>
 __device__ __forceinline__ int load8(const Prep &p, long long at, int left,
                                      uint4 (&out)[sizeof(T) == 2 ? 1 : 3],
@@ -234,8 +241,8 @@ __device__ __forceinline__ int load8(const Prep &p, long long at, int left,
 #pragma unroll
   for (int i = 0; i < 8; ++i) e = max(e, __float_as_uint(v[i]) >> 23 & 0xffu);
   e = __reduce_max_sync(0xffffffffu, e);
-  const int large = static_cast<int>(e) > kLargest ? static_cast<int>(e) : 0;
-  const float scale = power(large != 0 ? kScale + kLargest - large : kScale);
+  const int large = static_cast<int>(e) > kLargest ? static_cast<int>(e) - kLargest : 0;
+  const float scale = power(kScale - large);
 #pragma unroll
   for (int t = 0; t < kTerms; ++t) sum[t] = 0.0f;
   uint32_t h[kTerms][8];
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps) w4_prep_kernel(const Prep p) 
     for (int i = 0; i < A::kTerms; ++i)
 #pragma unroll
       for (int d = 1; d < 4 * PERIOD; d *= 2) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
-    const long long to = ((r0 / A::kRows + g + r / A::kRows) * p.blocks + b) * A::kStep;
+    const long long to = ((first_tile(p.by_rows, r0, A::kRows, g) + r / A::kRows) * p.blocks + b) * A::kStep;
     if (!index_ok(kSitePartialWrite, to, A::kBytes, p.to_extent)) continue;
     uint8_t *panel = p.to + to + lane / 8 * A::kPanel;
     float *sums = reinterpret_cast<float *>(p.to + to + A::kSums);
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
   for (long long t0 = r0; t0 < r1; t0 += A::kRows) {
     if (warp == kProducer) {
       if (lane == 0) {
-        const long long at = (r0 / A::kRows + g + (t0 - r0) / A::kRows) * p.blocks;
+        const long long at = (first_tile(p.by_rows, r0, A::kRows, g) + (t0 - r0) / A::kRows) * p.blocks;
         auto load_w = [&](int b) {
           mbar_arrive_expect_tx(&sh.full_w[stage], kWBytes);
           tma_load_3d(ws + stage * kWBytes, &map, &sh.full_w[stage], b * (kBlockK / 2), n0,
@@ -530,6 +537,10 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
           for (int i = 0; i < COLS / 16; ++i) tmem_regs_ready(v[i]);
           const float *asums =
               reinterpret_cast<const float *>(at + A::kSums) + (h * kTimes + c) * A::kTerms * A::kRows;
+          // From 2^104 on a scale and the unit of the sums are two factors.
+          const bool apart = LARGE && !(fabsf(s_now[c]) < kLargeScale);
+          const float s = apart ? s_now[c] : s_now[c] * power(kUnit - kScale);
+          [[maybe_unused]] const float unit = apart ? power(kUnit - kScale) : 1.0f;
           [[maybe_unused]] float as4[4];
 #pragma unroll
           for (int t = 0; t < A::kRows; ++t) {
@@ -551,15 +562,9 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
                 u += fmaf(-z_now[c], asums[col], __uint_as_float(v[col / 16][col % 16]));
               }
             }
-            if constexpr (LARGE) {
-              const int e = at[A::kFlags + t];
-              if (e != 0) {
-                // 2^(kLargest - e) less, which may be more than a factor holds
-                sum[t] = fmaf(s_now[c] * u, power(e - kLargest), sum[t]);
-                continue;
-              }
-            }
-            sum[t] = fmaf(s_now[c], u, sum[t]);
+            // (exact: A is scaled by that much less)
+            if constexpr (LARGE) u = u * power(at[A::kFlags + t]) * unit;
+            sum[t] = fmaf(s, u, sum[t]);
           }
         }
         tc_fence_before_sync();
@@ -573,7 +578,11 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
 #pragma unroll
         for (int i = 0; i < A::kRows / 4; ++i) any |= flags[i];
         if constexpr (A::kRows % 4 != 0) any |= flags[A::kRows / 4] & ((1u << (A::kRows % 4 * 8)) - 1u);
-        if (any != 0) drain_as(std::true_type{}, at);
+        bool large = any != 0;
+#pragma unroll
+        for (int c = 0; c < kTimes; ++c) large |= !(fabsf(s_now[c]) < kLargeScale);
+        // (the warp's choice: all its lanes read TMEM together)
+        if (__any_sync(0xffffffffu, large)) drain_as(std::true_type{}, at);
         else drain_as(std::false_type{}, at);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[of]);
@@ -585,11 +594,12 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
         float s[kTimes], z[kTimes];
 #pragma unroll
         for (int c = 0; c < kTimes; ++c) {
-          s[c] = static_cast<float>(s_next[c]) * power(kUnit - kScale);
+          s[c] = static_cast<float>(s_next[c]);
           z[c] = static_cast<float>(z_next[c] & 15u);
         }
         if (b + 1 < b1) fetch(b + 1);
         wait(&sh.full_w[stage], parity);
+        __syncwarp();  // together again, for TMEM
         const uint8_t *line = ws + stage * kWBytes + row * 128;
         // 64 k of the line: 32 columns of the operand
         auto make = [&](int q, uint32_t (&v)[32]) {
@@ -710,45 +720,72 @@ struct Expand {
   void *hi, *lo;
   long long ldq, strideq, q_extent, lds, strides, s_extent, ldz, stridez, z_extent, ldd, d_extent;
   long long n0, rows, count;
-  int K, group;
+  int K, group, words;  // q in words of four bytes?
   const int64_t *offsets;
   long long M;
 };
 
-// A thread takes a byte: two neighbours of a row.
+// A warp takes 2048 k of a row, a lane eight neighbours at a time: four bytes of q,
+// and 16 of each result (whose rows have room for whole eights).
+constexpr int kExpandK = 2048;
 template <class T>
 __global__ void __launch_bounds__(256) w4_expand_kernel(const Expand p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int half = (p.K + 1) / 2;
-  for (long long i = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32; i < p.rows * p.count;
+  const int half = (p.K + 1) / 2, pieces = (p.K + kExpandK - 1) / kExpandK;
+  for (long long i = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32; i < p.rows * p.count * pieces;
        i += static_cast<long long>(gridDim.x) * 8) {
-    const long long z = i / p.rows, row = i - z * p.rows, n = p.n0 + row;
+    const long long line = i / pieces, z = line / p.rows, n = p.n0 + line - z * p.rows;
     if (p.offsets != nullptr && held(p.offsets[z], p.M) >= held(p.offsets[z + 1], p.M)) continue;
-    const long long from = z * p.strideq + n * p.ldq, to = i * p.ldd;
-    for (int b = lane; b < half; b += 32) {
-      if (!index_ok(kSiteCopySrc, from + b, 1, p.q_extent)) continue;
-      const int q = p.q[from + b], k = 2 * b, at = k / p.group;  // group is even
-      const long long is = z * p.strides + n * p.lds + at, iz = z * p.stridez + n * p.ldz + at;
-      if (!index_ok(kSiteLoadB, is, 1, p.s_extent)) continue;
-      const float s = static_cast<float>(static_cast<const T *>(p.scales)[is]);
-      int zero = 8;
-      if (p.zeros != nullptr && index_ok(kSiteLoadB, iz, 1, p.z_extent)) zero = p.zeros[iz] & 15;
+    const long long from = z * p.strideq + n * p.ldq, to = line * p.ldd;
+    const long long s_at = z * p.strides + n * p.lds, z_at = z * p.stridez + n * p.ldz;
+    const int k0 = static_cast<int>(i - line * pieces) * kExpandK;
+#pragma unroll 4
+    for (int c = 0; c < kExpandK / 256; ++c) {
+      const int k = k0 + c * 256 + lane * 8, b = k / 2;
+      if (k >= p.K) break;
+      uint32_t q = 0;
+      if (p.words && b + 4 <= half && index_ok(kSiteCopySrc, from + b, 4, p.q_extent)) {
+        q = __ldcs(reinterpret_cast<const uint32_t *>(p.q + from + b));
+      } else {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (k + e >= p.K || !index_ok(kSiteCopyDst, to + k + e, 1, p.d_extent)) continue;
-        // exact but for fp32 scales of more than 20 bits
-        const float w = s * static_cast<float>((q >> (4 * e) & 15) - zero);
-        if constexpr (sizeof(T) == 4) {
-          static_cast<float *>(p.hi)[to + k + e] = w;
-        } else {
-          const __nv_bfloat16 h = __float2bfloat16_rn(w);
-          const float first = __bfloat162float(h);
-          static_cast<__nv_bfloat16 *>(p.hi)[to + k + e] = h;
-          static_cast<__nv_bfloat16 *>(p.lo)[to + k + e] =
-              __float2bfloat16_rn(isinf(first) ? 0.0f : w - first);
+        for (int j = 0; j < 4; ++j)
+          if (b + j < half && index_ok(kSiteCopySrc, from + b + j, 1, p.q_extent))
+            q |= static_cast<uint32_t>(p.q[from + b + j]) << (8 * j);
+      }
+      const int at = k / p.group;  // of a multiple of 32
+      if (!index_ok(kSiteLoadB, s_at + at, 1, p.s_extent)) continue;
+      const float s = static_cast<float>(static_cast<const T *>(p.scales)[s_at + at]);
+      float zero = 8.0f;
+      if (p.zeros != nullptr && index_ok(kSiteLoadB, z_at + at, 1, p.z_extent))
+        zero = static_cast<float>(p.zeros[z_at + at] & 15);
+      float w[8];
+      // 2^23 + q less 2^23 + z; the product is exact but for fp32 scales of more
+      // than 20 bits
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j] = s * (__uint_as_float(0x4b000000u | (q >> (4 * j) & 15u)) - (0x1p23f + zero));
+      if (!index_ok(kSiteCopyDst, to + k, 8, p.d_extent)) continue;
+      if constexpr (sizeof(T) == 4) {
+        float4 *out = reinterpret_cast<float4 *>(static_cast<float *>(p.hi) + to + k);
+        out[0] = make_float4(w[0], w[1], w[2], w[3]);
+        out[1] = make_float4(w[4], w[5], w[6], w[7]);
+      } else {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(w[2 * j], w[2 * j + 1]);
+          const float2 f = __bfloat1622float2(h);
+          const __nv_bfloat162 l = __floats2bfloat162_rn(isinf(f.x) ? 0.0f : w[2 * j] - f.x,
+                                                         isinf(f.y) ? 0.0f : w[2 * j + 1] - f.y);
+          hi[j] = *reinterpret_cast<const uint32_t *>(&h);
+          lo[j] = *reinterpret_cast<const uint32_t *>(&l);
         }
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.hi) + to + k) =
+            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.lo) + to + k) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
   }
@@ -819,7 +856,9 @@ int launch_both(const CUtensorMap &map, P p, const Prep &prep, int groups, cudaS
   const size_t least = tmem_columns(COLS, 4 / PERIOD) == 512 ? 128 * 1024 : 100 * 1024;
   if (smem < least) smem = least;
   Prep q = prep;
-  q.to_extent = (static_cast<long long>(p.M) / A::kRows + groups + 1) * p.blocks * A::kStep;
+  const long long most = static_cast<long long>(p.M) / A::kRows + groups;
+  p.by_rows = q.by_rows = p.M < most;
+  q.to_extent = (p.by_rows ? p.M : most) * p.blocks * A::kStep;
   void *to = nullptr;
   int st = pool_alloc(&to, static_cast<size_t>(q.to_extent), stream);
   if (st != kOk) return st;
@@ -982,9 +1021,11 @@ int w4_expand_launch(const W4Args &a, int64_t n0, int64_t rows, void *hi, void *
   p.count = a.groups;
   p.K = static_cast<int>(a.K);
   p.group = static_cast<int>(a.group);
+  p.words = reinterpret_cast<uintptr_t>(a.Q) % 4 == 0 && a.ldq % 4 == 0 && a.strideq % 4 == 0;
   p.offsets = a.offsets;
   p.M = a.M;
-  const int64_t blocks = (rows * a.groups + 7) / 8, most = 8LL * sm_count;
+  const int64_t pieces = (a.K + kExpandK - 1) / kExpandK;
+  const int64_t blocks = (rows * a.groups * pieces + 7) / 8, most = 8LL * sm_count;
   const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1);
   return a.bf16 ? launch(w4_expand_kernel<__nv_bfloat16>, grid, 256, 0, 1, stream, p)
                 : launch(w4_expand_kernel<float>, grid, 256, 0, 1, stream, p);

@@ -21,10 +21,18 @@ using gemm::stack_ok;
 using gemm::W4Args;
 
 // Rows a segment from which on the weights are expanded once for the tensor-core
-// kernels of the segmented products.
-constexpr int64_t kManyRows = 128;
-// Bytes of expanded weights at a time.
-constexpr int64_t kExpanded = int64_t{128} << 20;
+// kernels of the segmented products: measured, few_rows | many_rows in us at group
+// 128,
+//   rows                     128        256        512        2048
+//   bf16  4096 x 11008     78 | 148  146 | 149  283 | 150  1114 | 254
+//   bf16  32 x 1408 x 2048 97 | 180  185 | 187  360 | 235  1398 | 530
+//   fp32  4096 x 11008    138 | 325  266 | 326  526 | 347  2127 | 749
+//   fp32  32 x 1408 x 2048 172 | 275 334 | 315  654 | 525  2577 | 1570
+constexpr int64_t kManyRows = 256;
+// Bytes of expanded weights at a time: more than 4096 x 11008 have, for a part of
+// them has fewer tiles than the GPU SMs (at 128 MB that one took 247 us in place of
+// 149; 256 MB and 1 GB are within 6 % of each other).
+constexpr int64_t kExpanded = int64_t{512} << 20;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 

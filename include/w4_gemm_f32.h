@@ -13,11 +13,15 @@
  *   scales  N x ceil(K / group), of `type`; the last group of a row may be short
  *   zeros   N x ceil(K / group) bytes, of which the low four bits count; NULL: 8
  *
- * Types and accuracy are those of segment_gemm_f32.h: fp32 operands FP32 class
- * against the exact W, bf16 operands with fp32 sums, rounded once. No weight is
- * rounded, but fp32 ones to fp32 in calls of many rows. fp32 A from 2^-110 in
- * magnitude to the largest finite value, as there; an infinite or NaN A, or an
- * infinite or NaN scale, makes the results that it enters not finite, and no
+ * Types are those of segment_gemm_f32.h, and so is the accuracy (fp32 FP32 class;
+ * bf16 with fp32 sums, rounded once), but relative to the products that are
+ * summed: calls of few rows compute s (sum q a - z sum a), whose error is relative
+ * to the sum of |s| (q + z) |a|. That is more than the sum of |W| |a| only where
+ * most weights stand at their zeros. No weight is rounded, but to fp32 those of
+ * fp32 calls of many rows (scales of more than 20 bits).
+ *   A from 2^-110 in magnitude (smaller values may count as zero) to the largest
+ * finite one; scales to 2^124, so that 15 of them are finite. An infinite or NaN A,
+ * or an infinite or NaN scale, makes the results that it enters not finite, and no
  * others.
  */
 #ifndef W4_GEMM_F32_H
@@ -42,11 +46,15 @@ extern "C" {
  *   offsets   as for gemm_f32_grouped; NULL: all rows with matrix 0
  *   C         rows of no segment are not written; must not overlap anything else
  *             (GEMM_ERR_ALIAS)
- * K == 0 sets the rows to zero. Rows of Q that start on 16 bytes (Q, ldq and
- * strideq multiples of 16) are read as they lie; others are copied first, a
- * call's workspace of Q's size. Calls of 128 rows a segment on average and more
- * expand up to 128 MB of weights at a time in a workspace. Pointers are aligned
- * to their element; sizes up to GEMM_F32_MAX_SEGMENT_SIZE.
+ * K == 0 sets the rows to zero. Pointers are aligned to their element; sizes up
+ * to GEMM_F32_MAX_SEGMENT_SIZE. Workspaces come from the library's pool, for the
+ * call:
+ *   fewer than 256 rows a segment on average: A as operands, tiles of 5 to 64 rows
+ * (2.3 bytes a value of 16 bf16 rows, 6.3 of 16 fp32 ones), for every segment a last
+ * one that may be part empty (but no more of them than rows); and where rows of Q
+ * do not start on 16 bytes (Q, ldq and strideq multiples of 16), a copy of it.
+ *   256 and more: up to 512 MB of weights at a time in 4 bytes each, and a copy of
+ * A where its rows do not start on 16 bytes.
  */
 int gemm_f32_w4(int type, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group,
                 const void *A, int64_t lda,
