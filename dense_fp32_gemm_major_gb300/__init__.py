@@ -26,6 +26,7 @@ its handle has the same functions, and the wrappers below take it as ``lib``.
 
 from __future__ import annotations
 
+import array
 import collections
 import ctypes
 import operator
@@ -1067,8 +1068,12 @@ def _tensor_list(tensors, name, device):
 
 
 def _arrays(pointers, sizes, kinds):
-    n = len(sizes)
-    return ((ctypes.c_void_p * n)(*pointers), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*kinds))
+    # (ctypes arrays of 48 tensors take 12 us of the host, these 2)
+    return array.array("Q", pointers), array.array("q", sizes), array.array("i", kinds)
+
+
+def _address(values):
+    return values.buffer_info()[0] or None
 
 
 def grad_norm(tensors, stream=None):
@@ -1082,7 +1087,8 @@ def grad_norm(tensors, stream=None):
         dev = torch.cuda.current_device()
     norm = _empty((1,), torch.float32, dev, stream)
     x, n, kind = _arrays(pointers, sizes, kinds)
-    _call("reduce_f32_norm", dev, stream, len(sizes), x, n, kind, norm.data_ptr())
+    _call("reduce_f32_norm", dev, stream, len(sizes), _address(x), _address(n), _address(kind),
+          norm.data_ptr())
     return norm
 
 
@@ -1104,11 +1110,12 @@ def clip_grads(tensors, limit, out=None, stream=None):
         dev, to, to_sizes, to_kinds = _tensor_list(list(out), "out", dev)
         if to_sizes != sizes or to_kinds != kinds:
             raise ValueError("out does not have the tensors' types and sizes")
-        y = (ctypes.c_void_p * len(to))(*to)
+        y = array.array("Q", to)
     if dev is None:
         dev = torch.cuda.current_device()
     norm = _empty((1,), torch.float32, dev, stream)
-    _call("reduce_f32_clip", dev, stream, len(sizes), x, y, n, kind, limit, norm.data_ptr())
+    _call("reduce_f32_clip", dev, stream, len(sizes), _address(x), None if y is None else _address(y),
+          _address(n), _address(kind), limit, norm.data_ptr())
     return norm
 
 

@@ -841,10 +841,56 @@ int launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? kOk : kErrLaunch;
 }
 
+long long up16(long long x) { return (x + 15) / 16 * 16; }
+
+// Whether TMA can read Q as it lies.
+bool readable(const W4Args &a) {
+  return reinterpret_cast<uintptr_t>(a.Q) % 16 == 0 && a.ldq % 16 == 0 &&
+         (a.groups <= 1 || a.strideq % 16 == 0);
+}
+
+// Q's rows to rows that it can: dst has pitch ldd and stride strided.
+int pack(const W4Args &a, uint8_t *dst, int64_t ldd, int64_t strided, int sm_count,
+         cudaStream_t stream) {
+  Copy p = {};
+  p.src = a.Q;
+  p.dst = dst;
+  p.lds = a.ldq;
+  p.strides = a.strideq;
+  p.rows = a.N;
+  p.count = a.strideq == 0 ? 1 : a.groups;
+  p.bytes = (a.K + 1) / 2;
+  p.extent = extent_of(p.count, a.strideq, a.N, p.bytes, a.ldq);
+  p.ldd = ldd;
+  p.strided = strided;
+  p.dst_extent = extent_of(p.count, strided, a.N, ldd, ldd);
+  p.offsets = p.count > 1 ? a.offsets : nullptr;
+  p.M = a.M;
+  const int64_t blocks = (p.rows * p.count + 7) / 8, most = 8LL * sm_count;
+  return launch(w4_pack_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1),
+                256, 0, 1, stream, p);
+}
+
+int encode(const W4Args &a, CUtensorMap *map) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return kErrLaunch;
+  const bool stack = a.groups > 1 && a.strideq > 0;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>((a.K + 1) / 2), static_cast<cuuint64_t>(a.N),
+                              static_cast<cuuint64_t>(stack ? a.groups : 1)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ldq),
+                                 static_cast<cuuint64_t>(stack ? a.strideq : a.ldq)};
+  const cuuint32_t box[3] = {kBlockK / 2, kTileN, 1}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(a.Q), dims, strides, box,
+            step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? kOk : kErrLaunch;
+}
+
 // A's operands, and the products.
 template <class T, int COLS, int PERIOD>
-int launch_both(const CUtensorMap &map, P p, const Prep &prep, int groups, cudaStream_t stream) {
+int launch_both(const W4Args &a, P p, const Prep &prep, int sm_count, cudaStream_t stream) {
   using A = Tile<T, COLS, PERIOD>;
+  const int groups = static_cast<int>(a.groups);
   const int tiles = (p.N + kTileN - 1) / kTileN;
   constexpr int kStages = stages_of(COLS);
   static_assert(kGroups * A::kRows * kTileN * 4 <= kStages * kWBytes, "sums stand where weights did");
@@ -859,17 +905,33 @@ int launch_both(const CUtensorMap &map, P p, const Prep &prep, int groups, cudaS
   const long long most = static_cast<long long>(p.M) / A::kRows + groups;
   p.by_rows = q.by_rows = p.M < most;
   q.to_extent = (p.by_rows ? p.M : most) * p.blocks * A::kStep;
+  // One workspace: the operands, and behind them Q where it has to be copied.
+  W4Args from = a;
+  const bool copied = !readable(a);
+  if (copied) {
+    from.ldq = up16((a.K + 1) / 2);
+    from.strideq = a.strideq == 0 ? 0 : a.N * from.ldq;
+  }
+  const int64_t copy = copied ? (a.strideq == 0 ? 1 : a.groups) * a.N * from.ldq : 0;
   void *to = nullptr;
-  int st = pool_alloc(&to, static_cast<size_t>(q.to_extent), stream);
+  int st = pool_alloc(&to, static_cast<size_t>(q.to_extent + copy), stream);
   if (st != kOk) return st;
   q.to = static_cast<uint8_t *>(to);
   p.A = q.to;
+  CUtensorMap map;
+  if (copied) {
+    uint8_t *dst = q.to + q.to_extent;
+    from.Q = dst;
+    st = pack(a, dst, from.ldq, from.strideq, sm_count, stream);
+  }
+  if (st == kOk) st = encode(from, &map);
   const int64_t average = (p.M + groups - 1) / groups;
   const int64_t units = (average + A::kRows - 1) / A::kRows * A::kRows * p.blocks;
   const int64_t blocks = (units + kPrepWarps - 1) / kPrepWarps;
-  st = launch(w4_prep_kernel<T, COLS, PERIOD>,
-              dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), static_cast<unsigned>(groups), 1),
-              32 * kPrepWarps, 0, 1, stream, q);
+  if (st == kOk)
+    st = launch(w4_prep_kernel<T, COLS, PERIOD>,
+                dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), static_cast<unsigned>(groups), 1),
+                32 * kPrepWarps, 0, 1, stream, q);
   if (st == kOk)
     st = launch(w4_kernel<T, COLS, PERIOD>,
                 dim3(static_cast<unsigned>(tiles * p.split), static_cast<unsigned>(groups), 1), kThreads,
@@ -879,12 +941,11 @@ int launch_both(const CUtensorMap &map, P p, const Prep &prep, int groups, cudaS
 }
 
 template <class T, int COLS>
-int launch_cols(const CUtensorMap &map, const P &p, const Prep &q, int groups, int period,
-                cudaStream_t stream) {
-  if (period == 4) return launch_both<T, COLS, 4>(map, p, q, groups, stream);
-  if (period == 2) return launch_both<T, COLS, 2>(map, p, q, groups, stream);
+int launch_cols(const W4Args &a, const P &p, const Prep &q, int period, int sms, cudaStream_t stream) {
+  if (period == 4) return launch_both<T, COLS, 4>(a, p, q, sms, stream);
+  if (period == 2) return launch_both<T, COLS, 2>(a, p, q, sms, stream);
   // (more columns' accumulators of groups of 32 are more than TMEM holds)
-  return launch_both<T, (COLS < 48 ? COLS : (sizeof(T) == 2 ? 32 : 48)), 1>(map, p, q, groups, stream);
+  return launch_both<T, (COLS < 48 ? COLS : (sizeof(T) == 2 ? 32 : 48)), 1>(a, p, q, sms, stream);
 }
 
 }  // namespace
@@ -900,25 +961,7 @@ int w4_poll_status(cudaStream_t stream) {
   return h;
 }
 
-bool w4_readable(const W4Args &a) {
-  return reinterpret_cast<uintptr_t>(a.Q) % 16 == 0 && a.ldq % 16 == 0 &&
-         (a.groups <= 1 || a.strideq % 16 == 0);
-}
-
 int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return kErrLaunch;
-  CUtensorMap map;
-  const bool stack = a.groups > 1 && a.strideq > 0;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>((a.K + 1) / 2), static_cast<cuuint64_t>(a.N),
-                              static_cast<cuuint64_t>(stack ? a.groups : 1)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ldq),
-                                 static_cast<cuuint64_t>(stack ? a.strideq : a.ldq)};
-  const cuuint32_t box[3] = {kBlockK / 2, kTileN, 1}, step[3] = {1, 1, 1};
-  if (fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(a.Q), dims, strides, box,
-         step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return kErrLaunch;
   const int elem = a.bf16 ? 2 : 4;
   P p = {};
   p.row_groups = static_cast<int>((a.K + a.group - 1) / a.group);
@@ -934,7 +977,7 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
   p.ldc = a.ldc;
   p.c_extent = matrix_extent(a.M, a.N, a.ldc);
   p.offsets = a.offsets;
-  p.z_step = stack ? 1 : 0;
+  p.z_step = a.groups > 1 && a.strideq > 0 ? 1 : 0;
   p.M = static_cast<int>(a.M);
   p.N = static_cast<int>(a.N);
   p.K = static_cast<int>(a.K);
@@ -964,36 +1007,14 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
   // Rows at a time: twice what a segment has on average, for segments differ;
   // longer ones take several turns.
   const int64_t rows = a.groups > 1 ? 2 * ((a.M + a.groups - 1) / a.groups) : a.M;
-  const int groups = static_cast<int>(a.groups);
   if (a.bf16) {
-    if (rows <= 16) return launch_cols<__nv_bfloat16, 16>(map, p, q, groups, period, stream);
-    if (rows <= 32) return launch_cols<__nv_bfloat16, 32>(map, p, q, groups, period, stream);
-    return launch_cols<__nv_bfloat16, 64>(map, p, q, groups, period, stream);
+    if (rows <= 16) return launch_cols<__nv_bfloat16, 16>(a, p, q, period, sm_count, stream);
+    if (rows <= 32) return launch_cols<__nv_bfloat16, 32>(a, p, q, period, sm_count, stream);
+    return launch_cols<__nv_bfloat16, 64>(a, p, q, period, sm_count, stream);
   }
-  if (rows <= 5) return launch_cols<float, 16>(map, p, q, groups, period, stream);
-  if (rows <= 16) return launch_cols<float, 48>(map, p, q, groups, period, stream);
-  return launch_cols<float, 96>(map, p, q, groups, period, stream);
-}
-
-int w4_pack_launch(const W4Args &a, uint8_t *dst, int64_t ldd, int64_t strided, int sm_count,
-                   cudaStream_t stream) {
-  Copy p = {};
-  p.src = a.Q;
-  p.dst = dst;
-  p.lds = a.ldq;
-  p.strides = a.strideq;
-  p.rows = a.N;
-  p.count = a.strideq == 0 ? 1 : a.groups;
-  p.bytes = (a.K + 1) / 2;
-  p.extent = extent_of(p.count, a.strideq, a.N, p.bytes, a.ldq);
-  p.ldd = ldd;
-  p.strided = strided;
-  p.dst_extent = extent_of(p.count, strided, a.N, ldd, ldd);
-  p.offsets = p.count > 1 ? a.offsets : nullptr;
-  p.M = a.M;
-  const int64_t blocks = (p.rows * p.count + 7) / 8, most = 8LL * sm_count;
-  return launch(w4_pack_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most), 1, 1),
-                256, 0, 1, stream, p);
+  if (rows <= 5) return launch_cols<float, 16>(a, p, q, period, sm_count, stream);
+  if (rows <= 16) return launch_cols<float, 48>(a, p, q, period, sm_count, stream);
+  return launch_cols<float, 96>(a, p, q, period, sm_count, stream);
 }
 
 int w4_expand_launch(const W4Args &a, int64_t n0, int64_t rows, void *hi, void *lo, int64_t ldd,

@@ -27,14 +27,9 @@ struct W4Args {
   const int64_t *offsets = nullptr;
 };
 
-// Whether the kernel can read Q as it lies (by TMA).
-bool w4_readable(const W4Args &a);
-// M, N, K >= 1, Q readable.
+// Few rows: the kernel that reads the weights as they are (rows that do not start on
+// 16 bytes, for TMA, are copied first). M, N, K >= 1.
 int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream);
-
-// Q's rows to rows that are readable: dst has pitch ldd and stride strided.
-int w4_pack_launch(const W4Args &a, uint8_t *dst, int64_t ldd, int64_t strided, int sm_count,
-                   cudaStream_t stream);
 
 // Rows [n0, n0 + rows) of each W in fp32, or as the sum of two bf16 terms; pitch
 // ldd, stride rows * ldd.

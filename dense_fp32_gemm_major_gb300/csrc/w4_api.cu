@@ -21,7 +21,7 @@ using gemm::stack_ok;
 using gemm::W4Args;
 
 // Rows a segment from which on the weights are expanded once for the tensor-core
-// kernels of the segmented products: measured, few_rows | many_rows in us at group
+// kernels of the segmented products: measured, w4_launch | many_rows in us at group
 // 128,
 //   rows                     128        256        512        2048
 //   bf16  4096 x 11008     78 | 148  146 | 149  283 | 150  1114 | 254
@@ -35,30 +35,6 @@ constexpr int64_t kManyRows = 256;
 constexpr int64_t kExpanded = int64_t{512} << 20;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
-
-// Few rows: the kernel that reads the weights as they are.
-int few_rows(W4Args a, int sms, cudaStream_t s) {
-  void *ws = nullptr;
-  int st = gemm::kOk;
-  if (!gemm::w4_readable(a)) {
-    // Rows that start on 16 bytes, for TMA: one copy of the matrices that are used.
-    const int64_t ld = up((a.K + 1) / 2, 16), stride = a.strideq == 0 ? 0 : a.N * ld;
-    const int64_t count = stride == 0 ? 1 : a.groups;
-    st = gemm::pool_alloc(&ws, static_cast<size_t>(count * a.N * ld), s);
-    if (st != gemm::kOk) return st;
-    uint8_t *q = static_cast<uint8_t *>(ws);
-    st = gemm::w4_pack_launch(a, q, ld, stride, sms, s);
-    a.Q = q;
-    a.ldq = ld;
-    a.strideq = stride;
-  }
-  if (st == gemm::kOk) st = gemm::w4_launch(a, sms, s);
-  if (ws != nullptr) {
-    const int fst = gemm::pool_free(ws, s);
-    if (st == gemm::kOk) st = fst;
-  }
-  return st;
-}
 
 // Many rows: the weights as matrices of the type (bf16: as the sum of two, which
 // holds s (q - z) exactly), so many at a time as kExpanded holds, through the
@@ -182,5 +158,5 @@ extern "C" int gemm_f32_w4(int type, int64_t groups, int64_t M, int64_t N, int64
   a.C = C;
   a.ldc = ldc;
   a.offsets = offsets;
-  return M >= kManyRows * groups ? many_rows(a, sms, s) : few_rows(a, sms, s);
+  return M >= kManyRows * groups ? many_rows(a, sms, s) : gemm::w4_launch(a, sms, s);
 }
