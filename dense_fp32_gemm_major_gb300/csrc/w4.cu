@@ -29,12 +29,24 @@
 //     stay short. They are a value a thread.
 //   * Two warpgroups take 128 k in turn, each with its own operand and accumulator
 //     in TMEM: one makes operands while the other's are multiplied.
-//   * A comes as the tensor core reads it (w4_prep_kernel, once a call): its k in
+//   * A comes as the tensor core reads it (w4_prep_kernel, once a call; of one or two
+//     rows the producer's warp makes it, a launch less): its k in
 //     the order of the nibble pairs (0, 4), (1, 5), (2, 6), (3, 7); fp32 values as
 //     three bf16 terms, each a column.
 //   * Weights come by TMA, 128 rows of 256 k a stage, A by plain bulk copies.
 //     Few tiles: the CTAs of a cluster share k, and add their sums from each
 //     other's shared memory in the order of their ranks.
+//
+// Measured (launches by themselves, group 128): one bf16 row of 4096 x 11008 15 us (23
+// MB: 1.5 TB/s), 64 rows of 8 experts, 6 of them used, 51 us (142 MB: 2.8 TB/s of
+// 6.8). Neither memory nor a pipe is what bounds it (integer lanes 37 %, tensor core
+// 8 %), but the chain of a block: 128 k of operands are made and stored (about 700
+// clocks), multiplied by eight dependent MMAs (118 clocks each), and read out (600),
+// with four such chains an SM; and the MMAs of one thread start no closer than about
+// 100 clocks, so that two CTAs an SM give 1600 clocks a block each at best, of 2500
+// measured. Not kept: mma.sync 76 us; operands of 64 k, double buffered, 58; with two
+// chains of accumulators 56; a warpgroup that reads sums for one that makes operands
+// 64 to 66; two issuing threads 53; bigger hand-overs 87 (spills).
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -91,6 +103,7 @@ struct P {
   int z_step;         // 0: one matrix for all segments
   int by_rows;
   unsigned long long timeout_ns;
+  Prep prep;  // A itself
 };
 
 struct Shared {
@@ -203,16 +216,12 @@ __device__ __forceinline__ float power(int e) {  // 2^e, e in -126 .. 127
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
-// Eight neighbouring k of a row as operands, term by term, and their sums, those
-// of A's scaled values times 2^-kUnit; returns how far the exponent of the warp's
-// 256 values' largest is above kLargest.
+__host__ __device__ constexpr int terms_of(int elem) { return elem == 2 ? 1 : 3; }
+
+// Eight neighbouring k of a row, `left` of which there are.
 template <class T>
-__device__ __forceinline__ int load8(const Prep &p, long long at, int left,
-                                     uint4 (&out)[sizeof(T) == 2 ? 1 : 3],
-                                     float (&sum)[sizeof(T) == 2 ? 1 : 3]) {
-  constexpr int kTerms = sizeof(T) == 2 ? 1 : 3;
+__device__ __forceinline__ void load8(const Prep &p, long long at, long long left, float (&v)[8]) {
   const T *a = static_cast<const T *>(p.A) + at;
-  float v[8];
   if (left >= 8 && p.a_vec && index_ok(kSiteLoadA, at, 8, p.a_extent)) {
     if constexpr (sizeof(T) == 2) {
       const uint4 w = __ldg(reinterpret_cast<const uint4 *>(a));
@@ -237,6 +246,15 @@ __device__ __forceinline__ int load8(const Prep &p, long long at, int left,
     for (int i = 0; i < 8; ++i)
       v[i] = i < left && index_ok(kSiteLoadA, at + i, 1, p.a_extent) ? static_cast<float>(a[i]) : 0.0f;
   }
+}
+
+// They as operands, term by term, and their sums, those of A's scaled values times
+// 2^-kUnit; returns how far the exponent of the warp's 256 values' largest is above
+// kLargest.
+template <class T>
+__device__ __forceinline__ int terms8(const float (&v)[8], uint4 (&out)[terms_of(sizeof(T))],
+                                      float (&sum)[terms_of(sizeof(T))]) {
+  constexpr int kTerms = terms_of(sizeof(T));
   unsigned e = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) e = max(e, __float_as_uint(v[i]) >> 23 & 0xffu);
@@ -277,8 +295,6 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-__host__ __device__ constexpr int terms_of(int elem) { return elem == 2 ? 1 : 3; }
-
 // A tile of rows: COLS columns of the tensor core (a multiple of 16), a column for
 // each term of a row; the scales are applied every PERIOD steps of 32 k.
 template <class T, int COLS, int PERIOD>
@@ -305,9 +321,32 @@ __device__ __forceinline__ void segment_of(const int64_t *offsets, int g, int M,
   }
 }
 
+// A row of a tile's block, by a warp with 8 values a lane.
+template <class T, class A, int PERIOD>
+__device__ __forceinline__ void put_row(const float (&v)[8], uint8_t *to, int row) {
+  const int lane = threadIdx.x & 31;
+  uint4 w[A::kTerms];
+  float sum[A::kTerms];
+  const int large = terms8<T>(v, w, sum);
+#pragma unroll
+  for (int i = 0; i < A::kTerms; ++i)
+#pragma unroll
+    for (int d = 1; d < 4 * PERIOD; d *= 2) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+  uint8_t *panel = to + lane / 8 * A::kPanel;
+  float *sums = reinterpret_cast<float *>(to + A::kSums);
+#pragma unroll
+  for (int i = 0; i < A::kTerms; ++i) {
+    const int line = i * A::kRows + row;
+    *reinterpret_cast<uint4 *>(panel + line * 128 + ((lane % 8 ^ (line & 7)) << 4)) = w[i];
+    if (lane % (4 * PERIOD) == 0) sums[(lane / (4 * PERIOD) * A::kTerms + i) * A::kRows + row] = sum[i];
+  }
+  if (lane == 0) to[A::kFlags + row] = static_cast<uint8_t>(large);
+}
+
 constexpr int kPrepWarps = 4;
 
-// A warp takes a block of k of a row: once for all CTAs that will read it.
+// A warp takes a block of k of a row: once for all CTAs that will read it. (3 to 4 us, a
+// launch; without it every CTA made its own: 64 rows of 8 experts took 268 us, not 66.)
 template <class T, int COLS, int PERIOD>
 __global__ void __launch_bounds__(32 * kPrepWarps) w4_prep_kernel(const Prep p) {
   using A = Tile<T, COLS, PERIOD>;
@@ -324,25 +363,10 @@ __global__ void __launch_bounds__(32 * kPrepWarps) w4_prep_kernel(const Prep p) 
     const int b = static_cast<int>(u - r * p.blocks), row = static_cast<int>(r % A::kRows);
     const long long k = static_cast<long long>(b) * kBlockK + lane * 8;
     const long long left = r0 + r < r1 ? p.K - k : 0;
-    uint4 v[A::kTerms];
-    float sum[A::kTerms];
-    const int large = load8<T>(p, (r0 + r) * p.lda + k, left < 8 ? static_cast<int>(left) : 8, v, sum);
-#pragma unroll
-    for (int i = 0; i < A::kTerms; ++i)
-#pragma unroll
-      for (int d = 1; d < 4 * PERIOD; d *= 2) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+    float v[8];
+    load8<T>(p, (r0 + r) * p.lda + k, left, v);
     const long long to = ((first_tile(p.by_rows, r0, A::kRows, g) + r / A::kRows) * p.blocks + b) * A::kStep;
-    if (!index_ok(kSitePartialWrite, to, A::kBytes, p.to_extent)) continue;
-    uint8_t *panel = p.to + to + lane / 8 * A::kPanel;
-    float *sums = reinterpret_cast<float *>(p.to + to + A::kSums);
-#pragma unroll
-    for (int i = 0; i < A::kTerms; ++i) {
-      const int line = i * A::kRows + row;
-      *reinterpret_cast<uint4 *>(panel + line * 128 + ((lane % 8 ^ (line & 7)) << 4)) = v[i];
-      if (lane % (4 * PERIOD) == 0)
-        sums[(lane / (4 * PERIOD) * A::kTerms + i) * A::kRows + row] = sum[i];
-    }
-    if (lane == 0) p.to[to + A::kFlags + row] = static_cast<uint8_t>(large);
+    if (index_ok(kSitePartialWrite, to, A::kBytes, p.to_extent)) put_row<T, A, PERIOD>(v, p.to + to, row);
   }
 }
 
@@ -355,8 +379,16 @@ __host__ __device__ constexpr int tmem_columns(int cols, int times) {
 // Stages: what shared memory has room for, twice an SM up to 32 columns.
 __host__ __device__ constexpr int stages_of(int cols) { return cols == 32 || cols == 96 ? 3 : 4; }
 
-// The scales meet the sums every PERIOD steps of 32 k.
-template <class T, int COLS, int PERIOD>
+// Rows of a call up to which the kernel makes A's operands itself, in the producer's
+// warp of every CTA (fp32: one, three terms). Of 4096 x 11008, one launch | two, GPU
+// time of bf16: 1 row 16.5 | 16.6 us, 2 rows 16.8 | 16.8, 4 rows 22.6 | 17.1; of fp32:
+// 1 row 16.6 | 16.7, 2 rows 19.5 | 16.7. The launch and its workspace that this saves
+// are 4 us of the host, of 19 from Python.
+constexpr int kMakeRows = 2;
+constexpr int make_rows(int elem) { return elem == 2 ? kMakeRows : 1; }
+
+// The scales meet the sums every PERIOD steps of 32 k. MAKE: of up to make_rows rows.
+template <class T, int COLS, int PERIOD, bool MAKE>
 __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 / PERIOD) == 256 ? 2 : 1)
     w4_kernel(const __grid_constant__ CUtensorMap map, const P p) {
   using A = Tile<T, COLS, PERIOD>;
@@ -371,8 +403,12 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
   const int warp = static_cast<int>(warp_index()), lane = threadIdx.x & 31;
   const int tile = static_cast<int>(blockIdx.x) / p.split, rank = static_cast<int>(blockIdx.x) % p.split;
   const int g = blockIdx.y, n0 = tile * kTileN;
-  // What this launch reads but A was there before the one that makes A began
-  // (each launch lets the next one in behind its own wait).
+  if constexpr (MAKE) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
+  // (Else: what this launch reads but A was there before the one that makes A began;
+  // each launch lets the next one in behind its own wait.)
   long long r0, r1;
   segment_of(p.offsets, g, p.M, &r0, &r1);
   if (r0 >= r1) return;  // the whole cluster: it shares the segment
@@ -416,7 +452,59 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
   bool first = true;
 
   for (long long t0 = r0; t0 < r1; t0 += A::kRows) {
-    if (warp == kProducer) {
+    if (warp == kProducer && MAKE) {
+      const int used = static_cast<int>(min(static_cast<long long>(A::kRows), r1 - t0));
+      int ahead = stage, b_w = b0;  // lane 0's weights, up to kStages blocks ahead
+      uint32_t ahead_parity = parity;
+      auto load_w = [&] {
+        if (!wait(&sh.empty[ahead], ahead_parity ^ 1u)) return false;
+        mbar_arrive_expect_tx(&sh.full_w[ahead], kWBytes);
+        tma_load_3d(ws + ahead * kWBytes, &map, &sh.full_w[ahead], b_w * (kBlockK / 2), n0, g * p.z_step);
+        ++b_w;
+        if (++ahead == kStages) {
+          ahead = 0;
+          ahead_parity ^= 1u;
+        }
+        return true;
+      };
+      if (lane == 0)
+        while (b_w < b1 && b_w - b0 < kStages && load_w()) {}
+      __syncwarp();
+      // rows that are not there are zero, in all stages
+      for (int i = lane; i < kStages * A::kStep / 16; i += 32)
+        reinterpret_cast<uint4 *>(as)[i] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+      for (int b = b0; b < b1; ++b) {
+        bool ok = true;
+        if (b - b0 >= kStages) {
+          if (lane == 0) ok = load_w();  // (and the stage is empty)
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!ok) break;
+        __syncwarp();
+        uint8_t *to = as + stage * A::kStep;
+        const long long k = static_cast<long long>(b) * kBlockK + lane * 8;
+        float v[kMakeRows][8];
+#pragma unroll
+        for (int i = 0; i < kMakeRows; ++i)
+          if (i < used) load8<T>(p.prep, (t0 + i) * p.prep.lda + k, p.K - k, v[i]);
+#pragma unroll
+        for (int i = 0; i < kMakeRows; ++i)
+          if (i < used) put_row<T, A, PERIOD>(v[i], to, i);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full_a[stage]);
+        next();
+      }
+      if (lane == 0 && sh.abort) {
+        // Given up: the copies under way land before anyone leaves.
+        for (int i = min(b_w - b0, kStages); i > 0; --i)
+          mbar_wait_bounded(&sh.full_w[(ahead - i + kStages) % kStages],
+                            ahead - i < 0 ? ahead_parity ^ 1u : ahead_parity, p.timeout_ns,
+                            &sh.drain_abort, &g_w4_status);
+      }
+      __syncwarp();
+    } else if (warp == kProducer) {
       if (lane == 0) {
         const long long at = (first_tile(p.by_rows, r0, A::kRows, g) + (t0 - r0) / A::kRows) * p.blocks;
         auto load_w = [&](int b) {
@@ -691,7 +779,8 @@ struct Copy {
   long long M;
 };
 
-// A warp takes a row, a lane four bytes of it.
+// A warp takes a row, a lane four bytes of it. (1531 x 389 bytes: 4.7 us, of which a
+// launch is most.)
 __global__ void __launch_bounds__(256) w4_pack_kernel(const Copy p) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -726,7 +815,8 @@ struct Expand {
 };
 
 // A warp takes 2048 k of a row, a lane eight neighbours at a time: four bytes of q,
-// and 16 of each result (whose rows have room for whole eights).
+// and 16 of each result (whose rows have room for whole eights). 4096 x 11008 to two
+// bf16 terms: 47 us, 203 MB at 4.3 TB/s (54 % of the integer lanes); fp32 43 us.
 constexpr int kExpandK = 2048;
 template <class T>
 __global__ void __launch_bounds__(256) w4_expand_kernel(const Expand p) {
@@ -887,7 +977,7 @@ int encode(const W4Args &a, CUtensorMap *map) {
 }
 
 // A's operands, and the products.
-template <class T, int COLS, int PERIOD>
+template <class T, int COLS, int PERIOD, bool MAKE>
 int launch_both(const W4Args &a, P p, const Prep &prep, int sm_count, cudaStream_t stream) {
   using A = Tile<T, COLS, PERIOD>;
   const int groups = static_cast<int>(a.groups);
@@ -904,7 +994,7 @@ int launch_both(const W4Args &a, P p, const Prep &prep, int sm_count, cudaStream
   Prep q = prep;
   const long long most = static_cast<long long>(p.M) / A::kRows + groups;
   p.by_rows = q.by_rows = p.M < most;
-  q.to_extent = (p.by_rows ? p.M : most) * p.blocks * A::kStep;
+  q.to_extent = MAKE ? 0 : (p.by_rows ? p.M : most) * p.blocks * A::kStep;
   // One workspace: the operands, and behind them Q where it has to be copied.
   W4Args from = a;
   const bool copied = !readable(a);
@@ -914,10 +1004,12 @@ int launch_both(const W4Args &a, P p, const Prep &prep, int sm_count, cudaStream
   }
   const int64_t copy = copied ? (a.strideq == 0 ? 1 : a.groups) * a.N * from.ldq : 0;
   void *to = nullptr;
-  int st = pool_alloc(&to, static_cast<size_t>(q.to_extent + copy), stream);
+  int st = kOk;
+  if (q.to_extent + copy > 0) st = pool_alloc(&to, static_cast<size_t>(q.to_extent + copy), stream);
   if (st != kOk) return st;
   q.to = static_cast<uint8_t *>(to);
   p.A = q.to;
+  p.prep = q;
   CUtensorMap map;
   if (copied) {
     uint8_t *dst = q.to + q.to_extent;
@@ -928,24 +1020,25 @@ int launch_both(const W4Args &a, P p, const Prep &prep, int sm_count, cudaStream
   const int64_t average = (p.M + groups - 1) / groups;
   const int64_t units = (average + A::kRows - 1) / A::kRows * A::kRows * p.blocks;
   const int64_t blocks = (units + kPrepWarps - 1) / kPrepWarps;
+  if constexpr (!MAKE)
+    if (st == kOk)
+      st = launch(w4_prep_kernel<T, COLS, PERIOD>,
+                  dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), static_cast<unsigned>(groups), 1),
+                  32 * kPrepWarps, 0, 1, stream, q);
   if (st == kOk)
-    st = launch(w4_prep_kernel<T, COLS, PERIOD>,
-                dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), static_cast<unsigned>(groups), 1),
-                32 * kPrepWarps, 0, 1, stream, q);
-  if (st == kOk)
-    st = launch(w4_kernel<T, COLS, PERIOD>,
+    st = launch(w4_kernel<T, COLS, PERIOD, MAKE>,
                 dim3(static_cast<unsigned>(tiles * p.split), static_cast<unsigned>(groups), 1), kThreads,
                 smem, p.split, stream, map, p);
-  const int fst = pool_free(to, stream);
+  const int fst = to != nullptr ? pool_free(to, stream) : kOk;
   return st != kOk ? st : fst;
 }
 
-template <class T, int COLS>
+template <class T, int COLS, bool MAKE = false>
 int launch_cols(const W4Args &a, const P &p, const Prep &q, int period, int sms, cudaStream_t stream) {
-  if (period == 4) return launch_both<T, COLS, 4>(a, p, q, sms, stream);
-  if (period == 2) return launch_both<T, COLS, 2>(a, p, q, sms, stream);
+  if (period == 4) return launch_both<T, COLS, 4, MAKE>(a, p, q, sms, stream);
+  if (period == 2) return launch_both<T, COLS, 2, MAKE>(a, p, q, sms, stream);
   // (more columns' accumulators of groups of 32 are more than TMEM holds)
-  return launch_both<T, (COLS < 48 ? COLS : (sizeof(T) == 2 ? 32 : 48)), 1>(a, p, q, sms, stream);
+  return launch_both<T, (COLS < 48 ? COLS : (sizeof(T) == 2 ? 32 : 48)), 1, MAKE>(a, p, q, sms, stream);
 }
 
 }  // namespace
@@ -1005,13 +1098,16 @@ int w4_launch(const W4Args &a, int sm_count, cudaStream_t stream) {
   q.K = p.K;
   q.blocks = p.blocks;
   // Rows at a time: twice what a segment has on average, for segments differ;
-  // longer ones take several turns.
+  // longer ones take several turns. (11008 x 4096 in bf16, 16 | 32 | 64 rows in one
+  // turn: 19 | 21 | 33 us; 96 in two of 64: 56.)
   const int64_t rows = a.groups > 1 ? 2 * ((a.M + a.groups - 1) / a.groups) : a.M;
   if (a.bf16) {
+    if (a.M <= make_rows(2)) return launch_cols<__nv_bfloat16, 16, true>(a, p, q, period, sm_count, stream);
     if (rows <= 16) return launch_cols<__nv_bfloat16, 16>(a, p, q, period, sm_count, stream);
     if (rows <= 32) return launch_cols<__nv_bfloat16, 32>(a, p, q, period, sm_count, stream);
     return launch_cols<__nv_bfloat16, 64>(a, p, q, period, sm_count, stream);
   }
+  if (a.M <= make_rows(4)) return launch_cols<float, 16, true>(a, p, q, period, sm_count, stream);
   if (rows <= 5) return launch_cols<float, 16>(a, p, q, period, sm_count, stream);
   if (rows <= 16) return launch_cols<float, 48>(a, p, q, period, sm_count, stream);
   return launch_cols<float, 96>(a, p, q, period, sm_count, stream);

@@ -49,12 +49,14 @@ extern "C" {
  * K == 0 sets the rows to zero. Pointers are aligned to their element; sizes up
  * to GEMM_F32_MAX_SEGMENT_SIZE. Workspaces come from the library's pool, for the
  * call:
+ *   one or two rows (fp32: one): none.
  *   fewer than 256 rows a segment on average: A as operands, tiles of 5 to 64 rows
  * (2.3 bytes a value of 16 bf16 rows, 6.3 of 16 fp32 ones), for every segment a last
- * one that may be part empty (but no more of them than rows); and where rows of Q
- * do not start on 16 bytes (Q, ldq and strideq multiples of 16), a copy of it.
- *   256 and more: up to 512 MB of weights at a time in 4 bytes each, and a copy of
- * A where its rows do not start on 16 bytes.
+ * one that may be part empty (but no more of them than rows).
+ *   In both, where rows of Q do not start on 16 bytes (Q, ldq and strideq multiples
+ * of 16), a copy of it.
+ *   256 and more: up to 512 MB of weights at a time (256 rows of W at least) in 4
+ * bytes each, and a copy of A where its rows do not start on 16 bytes.
  */
 int gemm_f32_w4(int type, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group,
                 const void *A, int64_t lda,

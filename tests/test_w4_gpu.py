@@ -230,6 +230,25 @@ def test_many_segments_of_few_rows(g, dt, sizes):
         check(got[a:b], x[a:b], weights_64(q[i], s[i], z[i], k, group), dt, f"segment {i}")
 
 
+@pytest.mark.parametrize("m", [1, 2])
+@pytest.mark.parametrize("n, k, group", [(130, 30000, 64), (1, 33, 32), (300, 2304, 96), (11008, 4096, 128)])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_single_tokens(g, dt, n, k, group, m):
+    x, q, s, z = case(m, n, k, group, dt, True)
+    got = g.w4_matmul(x, q, s, group, zeros=z)
+    check(got, x, weights_64(q, s, z, k, group), dt)
+    for first in (0, 1, m):  # one row a segment, or both, or none
+        off = torch.tensor([0, first, first, m]).cuda()
+        mine = g.w4_matmul(x, q.expand(3, -1, -1), s.expand(3, -1, -1), group, zeros=z.expand(3, -1, -1), offsets=off)
+        check(mine, x, weights_64(q, s, z, k, group), dt)
+    x[0, k - 1] = math.inf
+    if m == 2:
+        x[1] *= 2.0 ** 30
+        mine = g.w4_matmul(x, q, s, group, zeros=z)
+        check(mine[1:], x[1:], weights_64(q, s, z, k, group), dt)
+        assert not mine[0].isfinite().any()
+
+
 @pytest.mark.parametrize("m", [1, 150])
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
 def test_without_a_contraction(g, dt, m):
