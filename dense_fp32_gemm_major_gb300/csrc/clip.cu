@@ -17,6 +17,11 @@
 // bits; chunks are added in 64 bits. The FP64 units take one addition of 64
 // elements, which hides behind the loads.
 //
+// Measured (24 bf16 tensors of 332 MB in all, launches by themselves): norm 52 us (6.4
+// TB/s), scale 99 us (6.7 TB/s). Two CTAs an SM: four tensors of 90 MB 178 us, with one
+// 215, three 191, four 182. 48 tensors of 8192 fp32: 4.7 + 5.7 us, launches and their
+// chains of loads.
+//
 // The list of tensors travels as the kernels' argument (100 of them, or 1000 a
 // launch), so a captured graph holds it and nothing is copied to the device.
 

@@ -25,6 +25,17 @@
 // 192 the CTAs of a cluster, which read each other's counts in shared memory; of
 // more, a second launch (a programmatic dependent) takes the counts from global
 // memory. Counts are integers: their order of addition does not show.
+//
+// Measured (one GB300, launches by themselves). 1 token of 8 experts 6.7 us, 64 of 256
+// in groups 11: chains of dependent steps of a few warps. 4095 of 64 in bf16 5.8 + 8.4
+// (choice + plan). 32768 of 256 in groups, fp32, 8 slots, a fifth of them masked: 53 + 18, against 5 us of
+// memory for the logits: the choice is bound by instructions, 1070 warp instructions a
+// token (45 % of the integer lanes' rate, 2.4 instructions a clock). Softmax without
+// bias and groups, one slot, takes 24 us; each further slot 1.5, bias 3 to 10, groups
+// 7 to 10 (a 64-bit choice at a CTA's end shows as 8). The plan's time is the counts of
+// all chunks, which every CTA sums, and two passes over its slots; the gradient's 14 us
+// there (64 experts: 5.4) are 33 MB written at 2.5 TB/s, a row's zeros and then its
+// slots.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,7 +65,7 @@ struct P {
   int32_t *order, *places;
   int T, E, k;
   int sigmoid, renormalise, compare_scores, vec;
-  int groups, top_groups, group_best, per_group, group_lanes;
+  int groups, top_groups, group_best, per_group, group_lanes, group_shift;  // lanes: 1 << shift
   int lanes_hold_groups;  // every lane's experts are of one group, a group's of group_lanes lanes
   float scale;
   int chunk, chunks;  // tokens of a CTA, CTAs
@@ -113,12 +124,9 @@ __device__ __forceinline__ F warp_sum(F v) {
 }
 __device__ __forceinline__ unsigned warp_best(unsigned v) { return __reduce_max_sync(kFull, v); }
 __device__ __forceinline__ unsigned long long warp_best(unsigned long long v) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) {
-    const unsigned long long o = __shfl_xor_sync(kFull, v, m);
-    v = o > v ? o : v;
-  }
-  return v;
+  const unsigned high = static_cast<unsigned>(v >> 32), best = __reduce_max_sync(kFull, high);
+  const unsigned low = __reduce_max_sync(kFull, high == best ? static_cast<unsigned>(v) : 0u);
+  return static_cast<unsigned long long>(best) << 32 | low;
 }
 
 __device__ __forceinline__ float sigmoid(float x) {
@@ -203,8 +211,9 @@ __device__ __forceinline__ int choose_experts(U (&key)[V], int k, U *won) {
 // -------------------------------------------------------- choice in 64 bits --
 
 // Lane r's choice by keys of 64 bits. A sigmoid is computed again only for those
-// of a lane's experts that can matter: its best two (which a group's may be), and
-// those not below `least`; of the others fp32 tells enough.
+// of a lane's experts that can matter: those not below `least` and, with groups, its
+// best two (which a group's may be); of the others fp32 tells enough. One token of
+// this is some 8 us, beside the CTA's other warps.
 template <int V, class T>
 __device__ __noinline__ int choose_wide(const P &p, long long t, float least, float err) {
   const int lane = threadIdx.x & 31;
@@ -225,7 +234,7 @@ __device__ __noinline__ int choose_wide(const P &p, long long t, float least, fl
       b2 = fmaxf(b2, fminf(b1, f[i]));
       b1 = fmaxf(b1, f[i]);
     }
-    const float from = fminf(least, b2);
+    const float from = p.groups > 1 ? fminf(least, b2) : least;
     // (a lane of experts of several groups: all of them)
     const float low = p.groups > 1 && p.per_group % V != 0
                           ? -INFINITY : from - 4.0f * (err + kUnit * fabsf(from));
@@ -265,10 +274,10 @@ __device__ __noinline__ int choose_wide(const P &p, long long t, float least, fl
       f[i] = key[i] != 0 ? exp(f[i] - m) : 0.0;
       sum += f[i];
     }
-    sum = warp_sum(sum);
+    const double part = 1.0 / warp_sum(sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      f[i] /= sum;
+      f[i] *= part;
       if (key[i] != 0 && p.bias != nullptr) {
         const float b = p.bias[lane * V + i];
         if (b == -INFINITY) key[i] = 0;
@@ -278,25 +287,42 @@ __device__ __noinline__ int choose_wide(const P &p, long long t, float least, fl
     }
   }
   if (p.groups > 1) {
-    unsigned long long mine = 0;
-    for (int g = 0; g < p.groups; ++g) {
+    if (p.lanes_hold_groups) {  // as choose()
       unsigned long long b1 = 0, b2 = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if ((lane * V + i) / p.per_group == g) merge_best(b1, b2, key[i], 0ull);
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) {
-        const unsigned long long o1 = __shfl_xor_sync(kFull, b1, s);
-        const unsigned long long o2 = __shfl_xor_sync(kFull, b2, s);
+      for (int i = 0; i < V; ++i) merge_best(b1, b2, key[i], 0ull);
+      for (int d = p.group_lanes / 2; d > 0; d >>= 1) {
+        const unsigned long long o1 = __shfl_xor_sync(kFull, b1, d);
+        const unsigned long long o2 = __shfl_xor_sync(kFull, b2, d);
         merge_best(b1, b2, o1, o2);
       }
-      if (lane == g) mine = group_key(b1, b2, p.group_best);
-    }
-    const unsigned kept = choose_lanes(mine, p.top_groups);
+      const int first = lane & ~(p.group_lanes - 1);
+      const unsigned kept =
+          choose_lanes(lane == first ? group_key(b1, b2, p.group_best) : 0ull, p.top_groups);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int g = (lane * V + i) / p.per_group;
-      if (g > 31 || !(kept >> g & 1u)) key[i] = 0;
+      for (int i = 0; i < V; ++i)
+        if (!(kept >> first & 1u)) key[i] = 0;
+    } else {
+      unsigned long long mine = 0;
+      for (int g = 0; g < p.groups; ++g) {
+        unsigned long long b1 = 0, b2 = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if ((lane * V + i) / p.per_group == g) merge_best(b1, b2, key[i], 0ull);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          const unsigned long long o1 = __shfl_xor_sync(kFull, b1, d);
+          const unsigned long long o2 = __shfl_xor_sync(kFull, b2, d);
+          merge_best(b1, b2, o1, o2);
+        }
+        if (lane == g) mine = group_key(b1, b2, p.group_best);
+      }
+      const unsigned kept = choose_lanes(mine, p.top_groups);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int g = (lane * V + i) / p.per_group;
+        if (g > 31 || !(kept >> g & 1u)) key[i] = 0;
+      }
     }
   }
   unsigned long long won;
@@ -465,7 +491,7 @@ __device__ __forceinline__ int choose(const P &p, long long t, const float (&bia
   if constexpr (kSort) sort();
   if (p.groups > 1) {
     // The best two of each group, by group_lanes lanes.
-    const int g = lane / p.group_lanes, sub = lane % p.group_lanes;
+    const int g = lane >> p.group_shift, sub = lane & (p.group_lanes - 1);
     unsigned b1 = 0, b2 = 0;
     if (kSort && p.lanes_hold_groups) {
 #pragma unroll
@@ -579,7 +605,7 @@ __device__ __forceinline__ float weight_of(const P &p, long long t, int e, float
     float part;
     if (p.sigmoid) {
       top = fminf(top, 0.0f);
-      part = x < 0.0f ? expf(x - top) / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
+      part = (x < 0.0f ? expf(x - top) : 1.0f) / (1.0f + expf(-fabsf(x)));
     } else {
       part = expf(x - top);
     }
@@ -735,6 +761,9 @@ __device__ void plan_chunk(const P &p, const PlanShared &sh, int c, long long sl
   rank_slots(p, sh, static_cast<int>(s0), static_cast<int>(s1 < slots ? s1 : slots), slots);
 }
 
+// As many warps as registers leave room for without spills that count: 32768 tokens,
+// 256 experts (V = 8): 768 threads 74 us with the plan, 512 90, 384 96; 64 experts: 1024
+// 62, 768 66, 512 78; 512 experts: 512 205, 384 221.
 constexpr int route_threads(int V) { return V <= 4 ? 1024 : (V == 8 ? 768 : (V == 16 ? 512 : 256)); }
 
 template <int V, class T>
@@ -748,17 +777,22 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
   // groups' keys stand where the plan's counts of a warp will
   unsigned *staged = reinterpret_cast<unsigned *>(p.plan ? sh.base : smem) + warp * staged_ints(p);
   const long long slots = static_cast<long long>(p.T) * p.k;
-  if (p.plan) {
+  __shared__ int taken;  // tokens of the chunk, behind the warps' first
+  if (threadIdx.x == 0) taken = warps;
+  if (p.plan)
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh.count[e] = 0;
-    __syncthreads();
-  }
+  __syncthreads();
   float bias[V];
 #pragma unroll
   for (int i = 0; i < V; ++i)
     bias[i] = p.bias != nullptr && lane * V + i < p.E ? p.bias[lane * V + i] : 0.0f;
-  const long long t1 = min(static_cast<long long>(p.T),
-                           (static_cast<long long>(blockIdx.x) + 1) * p.chunk);
-  for (long long t = static_cast<long long>(blockIdx.x) * p.chunk + warp; t < t1; t += warps) {
+  // A warp takes the next token when it is done with one: masked ones take no time, and
+  // those of choose_wide much.
+  const long long t0 = static_cast<long long>(blockIdx.x) * p.chunk;
+  const int count = static_cast<int>(min(static_cast<long long>(p.T) - t0, static_cast<long long>(p.chunk)));
+  for (int i = warp; i < count;) {
+    const long long t = t0 + i;
+    if (lane == 0) i = atomicAdd(&taken, 1);
     int e = -1;
     float w = 0.0f;
     if (p.mask == nullptr || p.mask[t] != 0) {
@@ -775,6 +809,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
       }
       if (p.plan && e >= 0) atomicAdd(&sh.count[e], 1);
     }
+    i = __shfl_sync(kFull, i, 0);
   }
   if (!p.plan) return;
   __syncthreads();
@@ -1031,15 +1066,18 @@ int route_launch(const RouteArgs &a, int sm_count, cudaStream_t stream) {
   p.top_groups = a.top_groups;
   p.group_best = a.group_best;
   p.per_group = static_cast<int>(a.E / a.groups);
-  p.group_lanes = 32;
-  while (32 / p.group_lanes < a.groups) p.group_lanes /= 2;
+  p.group_shift = 5;
+  while (32 >> p.group_shift < a.groups) --p.group_shift;
+  p.group_lanes = 1 << p.group_shift;
   p.compare_scores = a.bias != nullptr || (a.groups > 1 && a.group_best > 1);
   const int elem = a.bf16 ? 2 : 4, per16 = 16 / elem;
   p.vec = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.ldx % per16 == 0 && a.E % per16 == 0;
   p.scale = a.scale;
   p.plan = a.offsets != nullptr;
   // Up to 24 tokens one CTA does all (a warp each); more, eight tokens a CTA: 64
-  // tokens of 256 experts took one CTA three rounds.
+  // tokens of 256 experts, with the plan, 13.4 us, in one CTA 25.7. Up to 192 the CTAs
+  // of a cluster, one launch: 64 tokens 13.4 against 16.5 to 18.6 in two launches, 192
+  // tokens 17.5 against 18.6, and 256 21.6 against 16.5.
   constexpr int kCluster = 8;
   const bool together = a.T <= 24 * kCluster;
   cut(p, a.T, a.T <= 24 ? 24 : 8, together ? kCluster : sm_count);

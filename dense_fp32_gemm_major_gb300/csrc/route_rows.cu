@@ -10,6 +10,12 @@
 // token's row, each a piece of 1 KB of it at a time through all its places, with the
 // loads of up to four places in flight. Rows are read and written 16 bytes a lane
 // where their starts and widths allow it.
+//
+// Measured (8192 tokens of 4096 bf16, two places each, launches by themselves):
+// dispatch 29 us (201 MB: 6.9 TB/s), combine 28 us (7.3 TB/s), backward 60 us (336 MB:
+// 5.6 TB/s at a third of the warps, for its registers and 35 KB of shared memory); a
+// plain copy has 6.8. 1531 tokens of 777 fp32 (rows on no 16 bytes), three places: 5.6,
+// 6.9 and 13.7 us.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -318,7 +324,9 @@ bool fill(const RowsArgs &a, P *p) {
   const int elems = vec ? 16 / elem : 1, u = vec ? 2 : 8;
   p->D = static_cast<int>(a.D / elems);
   p->pieces = (p->D + 32 * u - 1) / (32 * u);
-  // As many warps a token as it has pieces.
+  // As many warps a token as it has pieces: 64 tokens of 4096 bf16, six places,
+  // dispatch, combine, backward with up to eight warps 9, 9, 11 us, with one 16, 24, 34;
+  // of 8192 tokens the same but for dispatch (38 against 42; cold).
   p->per_token = 1;
   while (p->per_token < kWarps && p->per_token < p->pieces) p->per_token *= 2;
   return vec;
@@ -333,7 +341,8 @@ int pick_type(bool bf16, const P &p, int sms, cudaStream_t s) {
 }
 
 // Places in flight: what a token has, up to four (few registers, and so more
-// warps, where it has one or two).
+// warps, where it has one or two: combine of 8192 tokens of 4096 bf16 40 us, by the
+// kernel of four 44, backward 71 and 82; cold).
 template <template <class, bool, int> class K>
 int pick(bool bf16, bool vec, const P &p, int sms, cudaStream_t s) {
   if (vec) return p.k <= 2 ? pick_type<K, true, 2>(bf16, p, sms, s) : pick_type<K, true, 4>(bf16, p, sms, s);
@@ -375,7 +384,8 @@ int rows_backward_launch(const RowsArgs &a, int sm_count, cudaStream_t stream) {
   P p;
   const bool vec = fill(a, &p);
   p.out_extent = matrix_extent(a.rows, a.D, a.ld_out);
-  // Warps of one token meet at its end: no more of them than fill the GPU.
+  // Warps of one token meet at its end: no more of them than fill the GPU (8192
+  // tokens of 4096 bf16: 71 us, with eight warps a token 75; 1024: 18.6 and 17.5).
   while (p.per_token > 1 && a.T * p.per_token >= 32LL * sm_count) p.per_token /= 2;
   return pick<Backward>(a.bf16, vec, p, sm_count, stream);
 }

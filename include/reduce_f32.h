@@ -61,9 +61,11 @@ int reduce_f32_sum(int64_t n, const float *x, float *out, int groups, void *stre
  *   type    HOST array, a gemm_f32_type for each tensor (x[i] and y[i])
  *   limit   >= 0 (infinity: no tensor changes unless the norm is not finite)
  *   norm    device pointer to one fp32
- * The arrays are read before the call returns. Squares are summed to 64 bits,
- * over the whole range of the types, in an order that the tensors' sizes and
- * alignment, the device and the order of the list fix: reruns are bit-identical.
+ * The arrays are read before the call returns. Squares are added by 32 to 64 in
+ * fp32 (in 64 bits where their sum is below 2^-100 or above 2^100), those sums in 64
+ * bits: the norm is within 2^-20 of its value over the whole range of the types. The
+ * order is fixed by the tensors' sizes and alignment, the device and the order of
+ * the list: reruns are bit-identical.
  * The factor is computed in 64 bits and rounded to fp32 (2^-24), the products
  * once to the type. A norm of infinity makes the factor 0 (and infinite elements
  * NaN), a NaN makes every result NaN. Workspace: 8 bytes a CTA from the library's

@@ -15,9 +15,9 @@
  *
  * Matrices are row-major device memory with a pitch in elements, of `type` (a
  * gemm_f32_type); the other arrays are dense. Streams, ownership, errors and
- * thread safety are those of gemm_f32.h; no result depends on timing, and none
- * may overlap an operand or another result (GEMM_ERR_ALIAS). Sizes are at most
- * GEMM_F32_MAX_SEGMENT_SIZE, and T k too.
+ * thread safety are those of gemm_f32.h; no result depends on timing (but that of
+ * places that name a row twice), and none may overlap an operand or another result
+ * (GEMM_ERR_ALIAS). Sizes are at most GEMM_F32_MAX_SEGMENT_SIZE, and T k too.
  */
 #ifndef ROUTE_F32_H
 #define ROUTE_F32_H
@@ -109,7 +109,8 @@ int gemm_f32_route_plan(int64_t slots, int64_t E, const int32_t *experts,
 /*
  * gemm_f32_dispatch -- each token's row to all of its places: Y[places[t][j]] =
  * X[t]. X is T x D, Y `rows` x D. Rows that no place names are not written; a
- * place outside [0, rows) is none. A row named twice gets one of the two.
+ * place outside [0, rows) is none. Each element of a row that is named twice gets
+ * the value of one of the two, not always of the same one (a plan names none twice).
  */
 int gemm_f32_dispatch(int type, int64_t T, int64_t D, int64_t k, int64_t rows,
                       const void *X, int64_t ldx, const int32_t *places,
@@ -133,8 +134,8 @@ int gemm_f32_combine(int type, int64_t T, int64_t D, int64_t k, int64_t rows,
  *
  *     dY[places[t][j]] = w[t][j] dO[t],   dw[t][j] = sum_d dO[t][d] Y[places[t][j]][d]
  *
- *   dY        rows that no place names are not written; a row named twice gets
- *             one of the two
+ *   dY        rows that no place names are not written; a row named twice as for
+ *             gemm_f32_dispatch
  *   dweights  T x k float, 0 for slots without a place
  * One of dY and dweights may be NULL (with weights NULL: 1 there too).
  */
