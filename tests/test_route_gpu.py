@@ -286,6 +286,32 @@ def test_long_batches(g, t, e, k):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("t", [23, 24, 25, 191, 192, 193, 5000])
+def test_padded_batches_route_as_their_tokens_do(g, t):
+    # whole stretches of the batch masked, as padding is
+    e, k = 256, 8
+    gen = torch.Generator().manual_seed(t)
+    x, b = torch.randn(t, e, generator=gen).cuda(), torch.randn(e, generator=gen).cuda()
+    mask = torch.ones(t, dtype=torch.bool)
+    mask[t // 3:t // 2] = False
+    mask[t - t // 5:] = False
+    kw = dict(score="sigmoid", bias=b, groups=8, top_groups=4)
+    r, every = g.route(x, k, mask=mask.cuda(), **kw), g.route(x, k, **kw)
+    there = mask.cuda()[:, None]
+    assert torch.equal(r.experts, torch.where(there, every.experts, -1))
+    assert torch.equal(r.weights, torch.where(there, every.weights, 0.0))
+    flat = r.experts.flatten().long()
+    used = int((flat >= 0).sum())
+    order = torch.sort(torch.where(flat < 0, e, flat), stable=True).indices
+    assert torch.equal(r.order[:used].long(), order[:used]) and (r.order[used:] == -1).all()
+    counts = torch.bincount(flat[flat >= 0], minlength=e)
+    assert torch.equal(r.offsets, torch.cat([counts.new_zeros(1), counts.cumsum(0)]))
+    assert torch.equal(r.places.flatten()[order[:used]].long(), torch.arange(used, device="cuda"))
+    assert torch.equal(r.places < 0, r.experts < 0)
+    again = g.route(x, k, mask=mask.cuda(), **kw)
+    assert all(torch.equal(u, v) for u, v in zip(r, again))
+
+
 @pytest.mark.parametrize("slots, e", [(1, 1), (31, 5), (4096, 3), (4097, 7), (70000, 200), (10000, 2048)])
 def test_plan_of_given_experts(g, slots, e):
     gen = torch.Generator().manual_seed(15)

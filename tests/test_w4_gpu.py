@@ -110,7 +110,7 @@ def test_offsets_outside_the_rows_are_held_to_them(g, dt, m):
     check(out[2:], x[2:], weights_64(q[2], s[2], None, 128, 32), dt)
 
 
-@pytest.mark.parametrize("m", [5, 600])
+@pytest.mark.parametrize("m", [1, 2, 5, 600])
 @pytest.mark.parametrize("pad, lead", [(16, 0), (16, 16), (3, 0), (0, 1), (8, 8)])
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
 def test_pitches_and_alignment(g, dt, m, pad, lead):
@@ -247,6 +247,30 @@ def test_single_tokens(g, dt, n, k, group, m):
         mine = g.w4_matmul(x, q, s, group, zeros=z)
         check(mine[1:], x[1:], weights_64(q, s, z, k, group), dt)
         assert not mine[0].isfinite().any()
+
+
+# Weights of more than 512 MB in 4 bytes each are expanded in parts: of the matrices, and
+# of a matrix.
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_weights_expanded_in_parts(g, dt):
+    n, k, group, groups = 1024, 1024, 128, 140
+    sizes = [260] * groups
+    sizes[3], sizes[131], sizes[139] = 0, 700, 1
+    starts = [0]
+    for size in sizes:
+        starts.append(starts[-1] + size)
+    assert starts[-1] >= 256 * groups
+    x, q, s, z = case(starts[-1], n, k, group, dt, True, groups)
+    got = g.w4_matmul(x, q, s, group, zeros=z, offsets=torch.tensor(starts).cuda())
+    for i in (0, 2, 3, 127, 128, 131, 138, 139):
+        rows = slice(starts[i], starts[i + 1])
+        check(got[rows], x[rows], weights_64(q[i], s[i], z[i], k, group), dt, f"segment {i}")
+    n, k = 8200, 16384
+    x, q, s, z = case(256, n, k, group, dt, True)
+    got = g.w4_matmul(x, q, s, group, zeros=z)
+    for i in (0, 4096, 8104):
+        rows = slice(i, i + 96)
+        check(got[:, rows], x, weights_64(q[rows], s[rows], z[rows], k, group), dt, f"rows from {i}")
 
 
 @pytest.mark.parametrize("m", [1, 150])
