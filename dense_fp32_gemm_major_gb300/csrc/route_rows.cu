@@ -12,10 +12,9 @@
 // where their starts and widths allow it.
 //
 // Measured (8192 tokens of 4096 bf16, two places each, launches by themselves):
-// dispatch 29 us (201 MB: 6.9 TB/s), combine 28 us (7.3 TB/s), backward 60 us (336 MB:
-// 5.6 TB/s at a third of the warps, for its registers and 35 KB of shared memory); a
-// plain copy has 6.8. 1531 tokens of 777 fp32 (rows on no 16 bytes), three places: 5.6,
-// 6.9 and 13.7 us.
+// dispatch 29 us (201 MB: 6.9 TB/s), combine 28 us (7.3 TB/s), backward 57 us (336 MB:
+// 5.9 TB/s); a plain copy has 6.8. 1531 tokens of 777 fp32 (rows on no 16 bytes), three
+// places: 5.6, 6.9 and 7.8 us.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -157,8 +156,13 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const P p) {
   });
 }
 
+// CTAs an SM, and so registers. 8192 tokens of 4096 bf16, two places: 29 us with four,
+// 33 with three or five; 4096 tokens, six places: 38 with three, 43 with two, 65 with
+// four (spills).
+constexpr int combine_ctas(int places) { return places == 2 ? 4 : 3; }
+
 template <class T, bool VEC, int PLACES>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const P p) {
+__global__ void __launch_bounds__(kThreads, combine_ctas(PLACES)) combine_kernel(const P p) {
   using R = Row<T, VEC>;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -199,10 +203,16 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const P p) {
   });
 }
 
+// CTAs an SM, and so registers. 8192 tokens of 4096 bf16, two places: 57 us with four,
+// 65 with three, 81 with five (spills); 4096 tokens, six places: 82 with two, 95 with
+// three; element by element (1531 tokens of 777, fp32, three places): 7.8 with three,
+// 11.4 with two.
+constexpr int backward_ctas(bool vec, int places) { return !vec ? 3 : (places == 2 ? 4 : 2); }
+
 // `per_token` warps share a token's pieces; their sums of dw meet in shared
 // memory, in the order of the warps.
 template <class T, bool VEC, int PLACES>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const P p) {
+__global__ void __launch_bounds__(kThreads, backward_ctas(VEC, PLACES)) backward_kernel(const P p) {
   using R = Row<T, VEC>;
   __shared__ float part[kWarps][32][33];  // warp, slot, lane
   __shared__ float dots[kWarps][32];
