@@ -27,15 +27,15 @@
 // memory. Counts are integers: their order of addition does not show.
 //
 // Measured (one GB300, launches by themselves). 1 token of 8 experts 6.7 us, 64 of 256
-// in groups 11: chains of dependent steps of a few warps. 4095 of 64 in bf16 5.8 + 8.4
-// (choice + plan). 32768 of 256 in groups, fp32, 8 slots, a fifth of them masked: 53 + 18, against 5 us of
-// memory for the logits: the choice is bound by instructions, 1070 warp instructions a
-// token (45 % of the integer lanes' rate, 2.4 instructions a clock). Softmax without
-// bias and groups, one slot, takes 24 us; each further slot 1.5, bias 3 to 10, groups
-// 7 to 10 (a 64-bit choice at a CTA's end shows as 8). The plan's time is the counts of
-// all chunks, which every CTA sums, and two passes over its slots; the gradient's 14 us
-// there (64 experts: 5.4) are 33 MB written at 2.5 TB/s, a row's zeros and then its
-// slots.
+// in groups 11: chains of dependent steps of a few warps. 4095 of 64 in bf16 5.8 us and
+// 7.5 for the plan. 32768 of 256 in groups, fp32, 8 slots, a fifth of them masked: 53
+// and 15, against 5 us of memory for the logits: the choice is bound by instructions,
+// 1070 warp instructions a token (45 % of the integer lanes' rate, 2.4 instructions a
+// clock). Softmax without bias and groups, one slot, takes 24 us; each further slot
+// 1.5, bias 3 to 10, groups 7 to 10 (a 64-bit choice at a CTA's end shows as 8). The
+// plan's time is the counts of all chunks, which every CTA sums, and two passes over
+// its slots; the gradient's 14 us there (64 experts: 5.4) are 33 MB written at 2.5
+// TB/s, a row's zeros and then its slots.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -824,7 +824,9 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
   }
 }
 
-constexpr int kPlanThreads = 512;
+// 32768 tokens of 256 experts, 8 slots, choice and plan: 50 us, with 512 threads 56, 256
+// 68; 8192 of 1024: 75, 97, 111; 500 of 256 12, 12, 14.
+constexpr int kPlanThreads = 1024;
 
 // Counts of a chunk of given experts.
 __global__ void __launch_bounds__(kPlanThreads) count_kernel(const P p) {
