@@ -15,7 +15,7 @@
 // Comparisons. Without bias and sums over groups the logits are the keys: both
 // scores ascend with them. Otherwise the keys are s + bias in fp32, which is off
 // by rounding; where two keys whose order matters are closer than the bound of
-// that (tau below), the token is chosen again in 64 bits (choose_wide): with
+// that (close() below), the token is chosen again in 64 bits (choose_wide): with
 // fp32 logits about one token of a thousand (256 experts), so that the slow
 // FP64 units are off the path.
 //
@@ -548,17 +548,19 @@ __device__ __forceinline__ int choose(const P &p, long long t, const float (&bia
   const unsigned last = __shfl_sync(kFull, c.won, p.k - 1);
   // Neighbours of the chosen that may stand the other way round, and the last of
   // them and what is left: closer than the error, or equal but for the bits that
-  // the sort left out. (A NaN's key, 1, loses to those bits: whole keys again.)
-  auto close = [&](unsigned a, unsigned b) {
+  // the sort left out (`cut`), which bring the smaller key up to as many steps of
+  // fp32 closer. (A NaN's key, 1, loses to those bits: whole keys again.)
+  auto close = [&](unsigned a, unsigned b, unsigned cut) {
     if (a == b) return true;
     if (!p.compare_scores || b <= 8) return false;
-    const float u = value_of(a), v = value_of(b);
+    const float u = value_of(a), v = value_of(b | cut);
     return u - v <= 2.0f * err + kUnit * (fabsf(u) + fabsf(v));
   };
   bool look = false;
   if (sizeof(T) == 4 || p.compare_scores) {  // (bf16 logits have nothing in those bits)
-    look = lane + 1 < p.k && next != 0 && close(c.won, next);
-    look |= lane == p.k - 1 && last != 0 && c.next != 0 && close(last, c.next);
+    constexpr unsigned kCut = kSort ? V - 1u : 0u;
+    look = lane + 1 < p.k && next != 0 && close(c.won, next, kCut);
+    look |= lane == p.k - 1 && last != 0 && c.next != 0 && close(last, c.next, kCut);
   }
   if (kSort) {
 #pragma unroll
@@ -576,14 +578,14 @@ __device__ __forceinline__ int choose(const P &p, long long t, const float (&bia
     };
     const unsigned next_key = __shfl_down_sync(kFull, c.won, 1);
     const int next_e = __shfl_down_sync(kFull, c.expert, 1);
-    if (lane + 1 < p.k && next_key > 1 && close(c.won, next_key)) unsure |= !same(c.expert, next_e);
+    if (lane + 1 < p.k && next_key > 1 && close(c.won, next_key, 0u)) unsure |= !same(c.expert, next_e);
     const unsigned last_key = __shfl_sync(kFull, c.won, p.k - 1);
     const int last_e = __shfl_sync(kFull, c.expert, p.k - 1);
     if (last_key > 1) {
       least = value_of(last_key);
 #pragma unroll
       for (int i = 0; i < V; ++i)  // those that are left
-        if (key[i] > 1 && close(last_key, key[i])) unsure |= !same(last_e, lane * V + i);
+        if (key[i] > 1 && close(last_key, key[i], 0u)) unsure |= !same(last_e, lane * V + i);
     }
     if (__any_sync(kFull, unsure)) return choose_wide<V, T>(p, t, least == INFINITY ? -INFINITY : least, err);
   }

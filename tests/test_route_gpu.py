@@ -207,6 +207,59 @@ def test_scores_closer_than_fp32_tells(g, score, groups, best):
     call(g, x.cuda(), 9, score=score, groups=groups, top_groups=max(1, groups // 2), group_best=best)
 
 
+def pairs_around(e, near, score, t, seed):
+    """Logits of two available experts a token, and biases, such that both sums s +
+    b lie within 1e-7 or so of a border between two fp32 numbers: the one below a
+    multiple of eight steps of fp32, `near` in size, and that multiple."""
+    gen = torch.Generator().manual_seed(seed)
+    rand = lambda *n: torch.rand(*n, generator=gen, dtype=torch.float64)
+    step = 2.0 ** (math.floor(math.log2(near)) - 23)
+    logit = lambda s: torch.log(s / (1 - s))
+    x, rows = torch.full((t, e), -math.inf), torch.arange(t)
+    if score == "sigmoid":
+        bias = (near - 0.3 - 0.4 * rand(e)).float()
+        border = (torch.round((near - 0.2 + 0.4 * rand(t)) / (8 * step)) * 8 - 0.5) * step
+        first = torch.randint(e, (t,), generator=gen)
+        second = (first + torch.randint(1, e, (t,), generator=gen)) % e
+        for at in (first, second):
+            s = border - bias.double()[at] + (rand(t) - 0.5) * 2e-7
+            x[rows, at] = logit(s).float()
+    else:  # two scores are 1 in sum, and so each pair of experts has a border of its own
+        perm, n = torch.randperm(e, generator=gen), e // 2
+        high = torch.round((near - 0.2 + 0.4 * rand(n)) / (8 * step)) * 8 * step
+        part = torch.round((0.2 + 0.6 * rand(n)) / step) * step
+        bias = torch.zeros(e, dtype=torch.float64)
+        bias[perm[:n]], bias[perm[n:2 * n]] = high - part, high - step - 1 + part
+        pair = torch.randint(n, (t,), generator=gen)
+        s = part[pair] - step / 2 + (rand(t) - 0.5) * 2e-7
+        low = (rand(t) - 0.5).float()
+        x[rows, perm[:n][pair]] = (low.double() + logit(s)).float()
+        x[rows, perm[n:2 * n][pair]] = low
+        assert torch.equal(bias, bias.float().double())
+    return x, bias.float()
+
+
+@pytest.mark.parametrize("e, near", [(48, 17.0), (64, 20.0), (80, 5.0), (80, 9.0), (128, 9.0), (200, 3.5), (200, 9.0),
+                                     (256, 3.5), (256, 5.0), (256, 100.0), (300, 3.5), (256, -3.5), (256, -9.0)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 2])
+def test_sums_on_both_sides_of_a_rounding(g, e, near, score, k):
+    # fp32 sums may stand the wrong way round, one step apart, and where keys lose
+    # their lowest bits eight steps
+    t = 30000
+    x, bias = pairs_around(e, abs(near), score, t, 50)
+    if near < 0:
+        bias = bias - 2 * abs(near) - (1 if score == "sigmoid" else 0)
+    d = x.double().cuda()
+    s = torch.sigmoid(d) if score == "sigmoid" else torch.softmax(d, 1)
+    key = torch.where(x.cuda() == -math.inf, -math.inf, s + bias.double().cuda())
+    top = key.sort(dim=1, descending=True, stable=True)
+    r = g.route(x.cuda(), k, score=score, bias=bias.cuda())
+    clear = top.values[:, 0] - top.values[:, 1] > 1e-13 * abs(near)  # (64 bits have their own)
+    wrong = (r.experts != top.indices[:, :k].int()).any(1) & clear
+    assert clear.sum() > t // 2 and not wrong.any(), f"{int(wrong.sum())} of {t}"
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalise", [False, True])
 @pytest.mark.parametrize("biased", [False, True])
