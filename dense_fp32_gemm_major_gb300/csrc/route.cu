@@ -211,9 +211,10 @@ __device__ __forceinline__ int choose_experts(U (&key)[V], int k, U *won) {
 // -------------------------------------------------------- choice in 64 bits --
 
 // Lane r's choice by keys of 64 bits. A sigmoid is computed again only for those
-// of a lane's experts that can matter: those not below `least` and, with groups, its
-// best two (which a group's may be); of the others fp32 tells enough. One token of
-// this is some 8 us, beside the CTA's other warps.
+// of a lane's experts that can matter: those not below `least` (the last of the chosen;
+// -infinity, all of them, where the groups themselves may be others) and, with
+// groups, its best two (which a group's may be); of the others fp32 tells enough. One
+// token of this is some 8 us, beside the CTA's other warps.
 template <int V, class T>
 __device__ __noinline__ int choose_wide(const P &p, long long t, float least, float err) {
   const int lane = threadIdx.x & 31;
@@ -569,6 +570,7 @@ __device__ __forceinline__ int choose(const P &p, long long t, const float (&bia
   if (!__any_sync(kFull, look | unsure)) return c.expert;
 
   // By whole keys, and whether equal ones are of equal logits and biases.
+  const bool regroup = __any_sync(kFull, unsure);
   float least = INFINITY;
   if constexpr (kSort) c = choose_any<V>(key, p.k);
   if (p.compare_scores) {
@@ -587,7 +589,9 @@ __device__ __forceinline__ int choose(const P &p, long long t, const float (&bia
       for (int i = 0; i < V; ++i)  // those that are left
         if (key[i] > 1 && close(last_key, key[i], 0u)) unsure |= !same(last_e, lane * V + i);
     }
-    if (__any_sync(kFull, unsure)) return choose_wide<V, T>(p, t, least == INFINITY ? -INFINITY : least, err);
+    // (Other groups may have the k-th best far below what these ones have.)
+    if (__any_sync(kFull, unsure))
+      return choose_wide<V, T>(p, t, regroup || least == INFINITY ? -INFINITY : least, err);
   }
   return c.expert;
 }

@@ -260,6 +260,24 @@ def test_sums_on_both_sides_of_a_rounding(g, e, near, score, k):
     assert clear.sum() > t // 2 and not wrong.any(), f"{int(wrong.sum())} of {t}"
 
 
+@pytest.mark.parametrize("e, groups", [(256, 8), (256, 4), (64, 4), (512, 8), (1024, 8)])
+def test_experts_of_a_group_that_only_64_bits_choose(g, e, groups):
+    # Two groups whose sums are one in fp32: the later one's is larger. Its experts
+    # behind the best two are below those that the first group would give, and so close
+    # that fp32 has one score for several of them; the highest index is the best.
+    t, per = 48, e // groups
+    gen = torch.Generator().manual_seed(51)
+    x = torch.full((t, e), -5.0)
+    for r in range(t):
+        a, b = sorted(torch.randperm(groups, generator=gen)[:2].tolist())
+        x[r, a * per:(a + 1) * per] = 4.0
+        x[r, b * per:(b + 1) * per] = 3.0 + torch.arange(per).float() * 2.0 ** -22
+        for of, best in ((a, 5.0), (b, 5.0 + (r % 3 + 1) * 2.0 ** -21)):
+            x[r, of * per + torch.randperm(per, generator=gen)[:2]] = torch.tensor([5.0, best])
+    for k in (4, 8):
+        call(g, x.cuda(), k, score="sigmoid", groups=groups, top_groups=1, group_best=2)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalise", [False, True])
 @pytest.mark.parametrize("biased", [False, True])
