@@ -411,7 +411,11 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
   // each launch lets the next one in behind its own wait.)
   long long r0, r1;
   segment_of(p.offsets, g, p.M, &r0, &r1);
-  if (r0 >= r1) return;  // the whole cluster: it shares the segment
+  if (r0 >= r1) {  // the whole cluster: it shares the segment
+    // A launch behind this one counts on this one's end being that of the one before.
+    if constexpr (!MAKE) grid_dependency_wait();
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh.full_w[i], 1);

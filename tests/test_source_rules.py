@@ -97,3 +97,79 @@ def test_rule_catches_an_unfenced_use():
       tmem_regs_ready(r0);
     """
     assert fence_violations(good) == []
+
+
+# A kernel that starts before the launch ahead of it has ended (griddepcontrol.wait)
+# waits for that end on every way out: the launch behind it waits for this one's end
+# alone, and builds on both.
+
+_WAIT = r"(?:grid_dependency_wait\(\)|asm volatile\(\"griddepcontrol\.wait;\"[^;]*)\s*;"
+
+
+def _kernels(text):
+    """(name, body) of each __global__ function."""
+    for m in re.finditer(r"__global__\s+void\s", text):
+        bounds = re.compile(r"(?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s*)?").match(text, m.end())
+        head = re.compile(r"(\w+)\s*\(").search(text, bounds.end())
+        at = end = text.index("{", head.end())
+        depth = 0
+        while True:
+            depth += {"{": 1, "}": -1}.get(text[end], 0)
+            end += 1
+            if depth == 0:
+                break
+        yield head.group(1), text[at:end]
+
+
+def _block_before(body, at):
+    """(depth, text before `at` in the block around it, blocks in it left out)"""
+    depth = [""]
+    for c in body[:at]:
+        if c == "{":
+            depth.append("")
+        elif c == "}":
+            depth.pop()
+            depth[-1] += "}"
+        else:
+            depth[-1] += c
+    return len(depth) - 1, depth[-1]
+
+
+def early_returns(text):
+    """Kernels of the source with a wait, and what returns without one."""
+    bad, kernels = [], []
+    for name, body in _kernels(_strip_comments(text)):
+        if not re.search(_WAIT, body):
+            continue
+        kernels.append(name)
+        top = [w.end() for w in re.finditer(r"(?<=[;{}])\s*" + _WAIT, body)
+               if _block_before(body, w.end())[0] == 1]  # (behind no condition)
+        for m in re.finditer(r"\breturn\s*;", body):
+            depth, before = _block_before(body, m.start())
+            if not any(w < m.start() for w in top) and not (depth > 1 and re.search(_WAIT, before)):
+                bad.append(name)
+    return kernels, bad
+
+
+def test_dependent_launches_wait_before_they_return():
+    kernels = []
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith(".cu"):
+            with open(os.path.join(CSRC, name)) as f:
+                found, bad = early_returns(f.read())
+            assert not bad, f"{name}: {bad}"
+            kernels += found
+    assert {"w4_kernel", "seg_tc_kernel", "route_kernel", "scale_kernel"} <= set(kernels)
+
+
+def test_rule_catches_a_return_without_a_wait():
+    kernel = """
+template <int V> __global__ void __launch_bounds__(f(V), 2) a_kernel(const P p) {
+  if (p.n == 0) { %s return; }
+  if (p.ahead) { grid_dependency_wait(); }
+  if (!p.ahead) grid_dependency_wait();
+  if (p.m == 0) %s
+}"""
+    assert early_returns(kernel % ("", "")) == (["a_kernel"], ["a_kernel"])
+    assert early_returns(kernel % ("grid_dependency_wait();", ";")) == (["a_kernel"], [])
+    assert early_returns(kernel % ("grid_dependency_wait();", "return;")) == (["a_kernel"], ["a_kernel"])

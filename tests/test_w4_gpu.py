@@ -230,6 +230,29 @@ def test_many_segments_of_few_rows(g, dt, sizes):
         check(got[a:b], x[a:b], weights_64(q[i], s[i], z[i], k, group), dt, f"segment {i}")
 
 
+@pytest.mark.parametrize("m", [3, 40])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_offsets_that_change_behind_a_call_without_rows(g, dt, m):
+    # nothing of a call without rows reads the offsets that the next launch writes
+    n, k, group = 200, 512, 128
+    x, q, s, z = case(m, n, k, group, dt, True, 3)
+    experts = (torch.arange(m, device="cuda").view(m, 1) % 3).int()
+    off, want = torch.zeros(4, dtype=torch.int64, device="cuda"), g.route_plan(experts, 3)[0]
+    order, places = (torch.empty(m, dtype=torch.int32, device="cuda") for _ in range(2))
+    stream = torch.cuda.current_stream().cuda_stream
+    out = torch.full((m, n), 7.0, dtype=dt, device="cuda")
+    for _ in range(20):
+        off.zero_()
+        g.w4_matmul(x, q, s, group, zeros=z, offsets=off, out=out)
+        st = g.gemm_f32_route_plan(m, 3, experts.data_ptr(), off.data_ptr(), order.data_ptr(), places.data_ptr(), stream)
+        assert st == g.OK
+        got = g.w4_matmul(x, q, s, group, zeros=z, offsets=off)
+    assert torch.equal(off, want) and (out == 7).all()
+    starts = want.tolist()
+    for i, (a, b) in enumerate(zip(starts, starts[1:])):
+        check(got[a:b], x[a:b], weights_64(q[i], s[i], z[i], k, group), dt, f"segment {i}")
+
+
 @pytest.mark.parametrize("m", [1, 2])
 @pytest.mark.parametrize("n, k, group", [(130, 30000, 64), (1, 33, 32), (300, 2304, 96), (11008, 4096, 128)])
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
