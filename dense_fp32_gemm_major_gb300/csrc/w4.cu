@@ -72,7 +72,7 @@ constexpr int kMaxSplit = 8;
 __device__ int g_w4_status;  // first error recorded by a kernel of this unit
 
 // A as operands: for each tile of rows and each block of 256 k, four panels of 64
-// k (a line of 128 bytes for each row and term, swizzled); a byte a row, load8's
+// k (a line of 128 bytes for each row and term, swizzled); a byte a row, terms8's
 // exponent; and the sums of the row's terms between two times that scales are
 // applied.
 struct Prep {
@@ -208,8 +208,10 @@ __device__ __forceinline__ float read_cluster(uint32_t addr, uint32_t rank) {
 
 // Exponents of A's scaling (powers of two): kScale as long as a row's 256 values
 // are below 2^16 (biased exponent kLargest); else, that of the largest of them
-// above kLargest less. Sums are of units of 2^-133.
-constexpr int kScale = 110, kUnit = 133, kLargest = 127 + 15;
+// above kLargest less. fp32 values that are all below 2^-60 (kSmallest) kMore more:
+// their products' last bits, of the third term, would be below 2^-149 from 2^-102 on.
+// Sums are of units of 2^-133.
+constexpr int kScale = 110, kUnit = 133, kLargest = 127 + 15, kSmallest = 127 - 60, kMore = 16;
 constexpr float kLargeScale = 0x1p104f;
 
 __device__ __forceinline__ float power(int e) {  // 2^e, e in -126 .. 127
@@ -249,8 +251,7 @@ __device__ __forceinline__ void load8(const Prep &p, long long at, long long lef
 }
 
 // They as operands, term by term, and their sums, those of A's scaled values times
-// 2^-kUnit; returns how far the exponent of the warp's 256 values' largest is above
-// kLargest.
+// 2^-kUnit; returns how much less than by kScale the warp's 256 values are scaled.
 template <class T>
 __device__ __forceinline__ int terms8(const float (&v)[8], uint4 (&out)[terms_of(sizeof(T))],
                                       float (&sum)[terms_of(sizeof(T))]) {
@@ -259,8 +260,10 @@ __device__ __forceinline__ int terms8(const float (&v)[8], uint4 (&out)[terms_of
 #pragma unroll
   for (int i = 0; i < 8; ++i) e = max(e, __float_as_uint(v[i]) >> 23 & 0xffu);
   e = __reduce_max_sync(0xffffffffu, e);
-  const int large = static_cast<int>(e) > kLargest ? static_cast<int>(e) - kLargest : 0;
-  const float scale = power(kScale - large);
+  int less = static_cast<int>(e) > kLargest ? static_cast<int>(e) - kLargest : 0;
+  if constexpr (kTerms > 1)
+    if (e != 0 && e < kSmallest) less = -kMore;
+  const float scale = power(kScale - less);
 #pragma unroll
   for (int t = 0; t < kTerms; ++t) sum[t] = 0.0f;
   uint32_t h[kTerms][8];
@@ -283,7 +286,7 @@ __device__ __forceinline__ int terms8(const float (&v)[8], uint4 (&out)[terms_of
     out[t] = make_uint4(h[t][0] | h[t][4] << 16, h[t][1] | h[t][5] << 16, h[t][2] | h[t][6] << 16,
                         h[t][3] | h[t][7] << 16);
   }
-  return large;
+  return less;
 }
 
 template <class T>
@@ -327,7 +330,7 @@ __device__ __forceinline__ void put_row(const float (&v)[8], uint8_t *to, int ro
   const int lane = threadIdx.x & 31;
   uint4 w[A::kTerms];
   float sum[A::kTerms];
-  const int large = terms8<T>(v, w, sum);
+  const int less = terms8<T>(v, w, sum);
 #pragma unroll
   for (int i = 0; i < A::kTerms; ++i)
 #pragma unroll
@@ -340,7 +343,7 @@ __device__ __forceinline__ void put_row(const float (&v)[8], uint8_t *to, int ro
     *reinterpret_cast<uint4 *>(panel + line * 128 + ((lane % 8 ^ (line & 7)) << 4)) = w[i];
     if (lane % (4 * PERIOD) == 0) sums[(lane / (4 * PERIOD) * A::kTerms + i) * A::kRows + row] = sum[i];
   }
-  if (lane == 0) to[A::kFlags + row] = static_cast<uint8_t>(large);
+  if (lane == 0) to[A::kFlags + row] = static_cast<uint8_t>(less);
 }
 
 constexpr int kPrepWarps = 4;
@@ -654,7 +657,14 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
                 u += fmaf(-z_now[c], asums[col], __uint_as_float(v[col / 16][col % 16]));
               }
             }
-            // (exact: A is scaled by that much less)
+            // (exact: A is scaled by that much less; by more, the scale is, lest u leaves
+            // the normal numbers)
+            if constexpr (LARGE && A::kTerms > 1) {
+              const int less = static_cast<int8_t>(at[A::kFlags + t]);
+              const float f = power(less);
+              sum[t] = fmaf(less < 0 ? s * f : s, (less < 0 ? u : u * f) * unit, sum[t]);
+              continue;
+            }
             if constexpr (LARGE) u = u * power(at[A::kFlags + t]) * unit;
             sum[t] = fmaf(s, u, sum[t]);
           }

@@ -20,9 +20,11 @@
  * most weights stand at their zeros. No weight is rounded, but to fp32 those of
  * fp32 calls of many rows (scales of more than 20 bits).
  *   A from 2^-110 in magnitude (smaller values may count as zero) to the largest
- * finite one; scales to 2^124, so that 15 of them are finite. An infinite or NaN A,
- * or an infinite or NaN scale, makes the results that it enters not finite, and no
- * others.
+ * finite one; fp32 calls of few rows: beside values from 2^-60 on in the same 256 of
+ * k, each is held to 2^-121 (of its product with q or z, so that this shows only
+ * where the larger ones' are zero). Scales to 2^124, so that 15 of them are finite. An
+ * infinite or NaN A, or an infinite or NaN scale, makes the results that it enters not
+ * finite, and no others.
  */
 #ifndef W4_GEMM_F32_H
 #define W4_GEMM_F32_H

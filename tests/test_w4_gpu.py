@@ -175,6 +175,40 @@ def test_fp32_from_the_smallest_to_the_largest(g):
     check(got, x, w * 2.0 ** -8, torch.float32)
 
 
+@pytest.mark.parametrize("m", [1, 2, 4, 14, 300])
+@pytest.mark.parametrize("k", [1, 3, 40, 600])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_small_values_have_all_their_bits(g, dt, m, k):
+    # from 2^-110 on; in other rows and blocks of k larger ones
+    n, group = 70, 32
+    x, q, s, _ = case(m, n, k, group, dt, False)
+    z = torch.zeros(n, -(-k // group), dtype=torch.uint8, device="cuda")
+    gen = torch.Generator().manual_seed(7)
+    size = torch.randint(-110, -95, (m, k), generator=gen).double().exp2()
+    size[:, 256:] = torch.randint(-70, -40, size[:, 256:].shape, generator=gen).double().exp2()
+    x = ((1 + torch.rand(m, k, generator=gen).double()) * size).to(dt).cuda()
+    x[1::4] *= 2.0 ** 90
+    x[2::4, k // 2:] = 0.0
+    got = g.w4_matmul(x, q, s, group, zeros=z)
+    check(got, x, weights_64(q, s, z, k, group), dt)
+
+
+@pytest.mark.parametrize("m", [1, 4, 14, 300])
+@pytest.mark.parametrize("large", [1.0, 2.0 ** 40])
+def test_small_values_beside_large_ones_of_no_weight(g, m, large):
+    # what is lost of a small value then: 2^-121 of q - z, below 2^16 so much more of it
+    n, k, group = 70, 300, 32
+    x, q, s, _ = case(m, n, k, group, torch.float32, False)
+    z = torch.zeros(n, -(-k // group), dtype=torch.uint8, device="cuda")
+    x *= torch.randint(-108, -80, (m, k), generator=torch.Generator().manual_seed(8)).double().exp2().float().cuda()
+    x[:, 1::64] = large
+    q[:, ::32] &= 15  # (q of the odd k)
+    got = g.w4_matmul(x, q, s, group, zeros=z)
+    w = weights_64(q, s, z, k, group)
+    lost = k * 2.0 ** -121 * max(1.0, large * 2.0 ** -16) * s.double().abs().max()
+    check(got, x, w, torch.float32, least=float(lost))
+
+
 @pytest.mark.parametrize("m", [3, 300])
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
 def test_large_scales(g, dt, m):
