@@ -89,6 +89,10 @@ __device__ __forceinline__ float load_logit(const P &p, long long t, int e) {
                                                  : 0.0f;
 }
 
+__device__ __forceinline__ float load_bias(const P &p, int e) {
+  return p.bias != nullptr && index_ok(kSiteLoadB, e, 1, p.E) ? __ldg(p.bias + e) : 0.0f;
+}
+
 // Unsigned integers in the order of the values; 0: not available, 1: NaN. The
 // zeros are one value.
 __device__ __forceinline__ unsigned key_of(float f) {
@@ -223,12 +227,11 @@ __device__ __noinline__ int choose_wide(const P &p, long long t, float least, fl
     float f[V];
     unsigned again = 0;  // by their places, eight at a time of more than 32
     float b1 = -INFINITY, b2 = -INFINITY;
-    auto bias_of = [&](int e) { return p.bias != nullptr ? __ldg(p.bias + e) : 0.0f; };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = lane * V + i;
       const float x = e < p.E ? load_logit<T>(p, t, e) : -INFINITY;
-      const float b = e < p.E ? bias_of(e) : 0.0f;
+      const float b = e < p.E ? load_bias(p, e) : 0.0f;
       const bool there = x != -INFINITY && b != -INFINITY;
       f[i] = there ? sigmoid(x) + b : -INFINITY;
       key[i] = there ? key_of(static_cast<double>(f[i])) : 0;
@@ -251,7 +254,7 @@ __device__ __noinline__ int choose_wide(const P &p, long long t, float least, fl
         if (at >= 0) {
           const int e = lane * V + i0 + at;
           wide = key_of(sigmoid(static_cast<double>(load_logit<T>(p, t, e))) +
-                        static_cast<double>(bias_of(e)));
+                        static_cast<double>(load_bias(p, e)));
           again &= again - 1;
         }
 #pragma unroll
@@ -280,7 +283,7 @@ __device__ __noinline__ int choose_wide(const P &p, long long t, float least, fl
     for (int i = 0; i < V; ++i) {
       f[i] *= part;
       if (key[i] != 0 && p.bias != nullptr) {
-        const float b = p.bias[lane * V + i];
+        const float b = load_bias(p, lane * V + i);
         if (b == -INFINITY) key[i] = 0;
         f[i] += static_cast<double>(b);
       }
@@ -576,7 +579,7 @@ __device__ __forceinline__ int choose(const P &p, long long t, const float (&bia
   if (p.compare_scores) {
     auto same = [&](int a, int b) {
       return load_logit<T>(p, t, a) == load_logit<T>(p, t, b) &&
-             (p.bias == nullptr || p.bias[a] == p.bias[b]);
+             load_bias(p, a) == load_bias(p, b);
     };
     const unsigned next_key = __shfl_down_sync(kFull, c.won, 1);
     const int next_e = __shfl_down_sync(kFull, c.expert, 1);
@@ -791,7 +794,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
   float bias[V];
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    bias[i] = p.bias != nullptr && lane * V + i < p.E ? p.bias[lane * V + i] : 0.0f;
+    bias[i] = lane * V + i < p.E ? load_bias(p, lane * V + i) : 0.0f;
   // A warp takes the next token when it is done with one: masked ones take no time, and
   // those of choose_wide much.
   const long long t0 = static_cast<long long>(blockIdx.x) * p.chunk;
@@ -801,7 +804,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
     if (lane == 0) i = atomicAdd(&taken, 1);
     int e = -1;
     float w = 0.0f;
-    if (p.mask == nullptr || p.mask[t] != 0) {
+    if (p.mask == nullptr || (index_ok(kSiteLoadB, t, 1, p.T) && p.mask[t] != 0)) {
       float m, sum;
       bool bad;
       e = choose<V, T>(p, t, bias, staged, &m, &sum, &bad);

@@ -125,6 +125,11 @@ __device__ __forceinline__ long long place_of(const P &p, long long s) {
   return at >= 0 && at < p.rows ? at : -1;
 }
 
+__device__ __forceinline__ float weight_of(const P &p, long long s) {
+  return p.weights != nullptr && index_ok(kSiteLoadB, s, 1, static_cast<long long>(p.T) * p.k)
+             ? p.weights[s] : 1.0f;
+}
+
 // Calls of f(token, piece) for this warp's pieces.
 template <class F>
 __device__ __forceinline__ void for_pieces(const P &p, F f) {
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, combine_ctas(PLACES)) combine_kernel
       for (int j = 0; j < PLACES; ++j) {
         const long long s = t * p.k + j0 + j;
         at[j] = j0 + j < p.k ? place_of(p, s) : -1;
-        w[j] = j0 + j < p.k && p.weights != nullptr ? p.weights[s] : 1.0f;
+        w[j] = j0 + j < p.k ? weight_of(p, s) : 1.0f;
       }
 #pragma unroll
       for (int j = 0; j < PLACES; ++j)
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, backward_ctas(VEC, PLACES)) backward
           for (int j = 0; j < PLACES; ++j) {
             const long long s = t * p.k + j0 + j;
             at[j] = j0 + j < p.k ? place_of(p, s) : -1;
-            wj[j] = j0 + j < p.k && p.weights != nullptr ? p.weights[s] : 1.0f;
+            wj[j] = j0 + j < p.k ? weight_of(p, s) : 1.0f;
           }
 #pragma unroll
           for (int j = 0; j < PLACES; ++j) {

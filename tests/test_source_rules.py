@@ -173,3 +173,27 @@ template <int V> __global__ void __launch_bounds__(f(V), 2) a_kernel(const P p) 
     assert early_returns(kernel % ("", "")) == (["a_kernel"], ["a_kernel"])
     assert early_returns(kernel % ("grid_dependency_wait();", ";")) == (["a_kernel"], [])
     assert early_returns(kernel % ("grid_dependency_wait();", "return;")) == (["a_kernel"], ["a_kernel"])
+
+
+# The checked build looks at every index that a kernel computes: what the router's and
+# the rows' kernels read and write beside their matrices stands behind index_ok, in the
+# same statement or in the condition around it.
+
+def unchecked_accesses(text):
+    bad = []
+    for m in re.finditer(r"p\.(?:mask|bias|weights|dweights|experts|order|places|hist|partials)\s*(?:\[|\+ )",
+                         _strip_comments(text)):
+        before = _strip_comments(text)[max(0, m.start() - 240):m.start()]
+        block = before[before.rfind("}") + 1:]
+        if "index_ok(" not in block:
+            bad.append(m.group())
+    return bad
+
+
+def test_accesses_beside_the_matrices_are_checked():
+    for name in ("route.cu", "route_rows.cu", "clip.cu"):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        assert unchecked_accesses(text) == [], name
+    assert unchecked_accesses("if (a) { f(); }\n const float w = p.weights[s];") == ["p.weights["]
+    assert unchecked_accesses("if (index_ok(1, s, 1, n)) { p.experts[s] = e; p.weights[s] = w; }") == []
