@@ -165,3 +165,24 @@ def test_shapes_and_refusals(g):
     out = [torch.empty_like(a), torch.empty_like(a)]
     g.clip_grads([a, a], 0.5, out=out)
     assert torch.equal(out[0], out[1])
+
+
+def test_results_in_the_place_of_operands(g):
+    # refused but for a tensor's own place, whatever the shape that it is seen in there
+    a, b = torch.randn(8, 16, device="cuda"), torch.randn(8, 16, device="cuda")
+    before, both = a.clone(), torch.cat([a.view(-1), b.view(-1)])
+    want = before.double() * (0.5 / (norm_64([a]) + 1e-6))
+    for ts, out in (([a, b], [b, a]), ([a, a], None), ([a, a.view(-1)[5:]], None), ([a, a], [a, b]),
+                    ([both[:128], both[128:]], [both[1:129], b.view(-1)]),
+                    ([both[:128], a.view(-1)], [both[64:192], both[:128]])):
+        kept = [t.clone() for t in ts]
+        with pytest.raises(g.GemmError) as e:
+            g.clip_grads(ts, 0.5, out=out)
+        assert e.value.status == g.ERR_ALIAS
+        assert all(torch.equal(t, k) for t, k in zip(ts, kept))
+    g.clip_grads([a], 0.5, out=[a.view(-1)])
+    assert ((a.double() - want).abs() <= 21 * U * want.abs()).all()
+    x = torch.randn(100, device="cuda")
+    y = x.clone()
+    g.clip_grads([x, b], 0.5, out=[x, both[:128].view(8, 16)])  # one in place, one elsewhere
+    assert ((x.double() - y.double() * (0.5 / (norm_64([y, b]) + 1e-6))).abs() <= 21 * U * y.double().abs()).all()
