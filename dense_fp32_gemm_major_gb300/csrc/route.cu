@@ -26,16 +26,20 @@
 // more, a second launch (a programmatic dependent) takes the counts from global
 // memory. Counts are integers: their order of addition does not show.
 //
-// Measured (one GB300, launches by themselves). 1 token of 8 experts 6.7 us, 64 of 256
-// in groups 11: chains of dependent steps of a few warps. 4095 of 64 in bf16 5.8 us and
-// 7.5 for the plan. 32768 of 256 in groups, fp32, 8 slots, a fifth of them masked: 53
-// and 15, against 5 us of memory for the logits: the choice is bound by instructions,
-// 1070 warp instructions a token (45 % of the integer lanes' rate, 2.4 instructions a
-// clock). Softmax without bias and groups, one slot, takes 24 us; each further slot
-// 1.5, bias 3 to 10, groups 7 to 10 (a 64-bit choice at a CTA's end shows as 8). The
-// plan's time is the counts of all chunks, which every CTA sums, and two passes over
-// its slots; the gradient's 14 us there (64 experts: 5.4) are 33 MB written at 2.5
-// TB/s, a row's zeros and then its slots.
+// Measured (one GB300, all figures of this file: calls back to back in a graph, so that
+// logits below some 100 MB are in L2; in brackets by themselves with cold caches, as
+// ncu times them). 1 token of 8 experts 3.6 us, 64 of 256 in groups 8.9 (12.7): chains
+// of dependent steps of a few warps. 4095 of 64, bf16, softmax, 6 slots: choice 4.0,
+// plan 7.5. 32768 of 256, fp32, 8 slots: softmax 34, with a bias 54; sigmoid with a
+// bias 47, in 8 groups 56, of these a fifth masked 49 (62); and 16 (17) for the plan;
+// against 5 us of memory for the logits: the choice is bound by instructions, 1075 warp
+// instructions a token (49 % of the integer lanes' rate). Softmax of one slot takes 23
+// us, each further slot 1.5, a bias 6 (one slot) to 20 (eight: of more pairs some are
+// too close, and a 64-bit choice at a CTA's end shows as 8). The plan's time is the
+// counts of all chunks, which every CTA sums, and two passes over its slots; the
+// gradient's 11 us there (15; 64 experts, 4095 tokens: 4.6) are 33 MB written, a row's
+// zeros and then its slots; softmax that is not renormalised, three reads of the row
+// more, 23.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -770,9 +774,10 @@ __device__ void plan_chunk(const P &p, const PlanShared &sh, int c, long long sl
   rank_slots(p, sh, static_cast<int>(s0), static_cast<int>(s1 < slots ? s1 : slots), slots);
 }
 
-// As many warps as registers leave room for without spills that count: 32768 tokens,
-// 256 experts (V = 8): 768 threads 74 us with the plan, 512 90, 384 96; 64 experts: 1024
-// 62, 768 66, 512 78; 512 experts: 512 205, 384 221.
+// As many warps as registers leave room for without spills that count: the choice of
+// 32768 tokens, 8 slots, by a sigmoid with a bias in groups (softmax), 256 experts (V =
+// 8): 768 threads 56 us (34), 512 70 (46), 384 82 (53); 64 experts: 1024 37 (23), 768 37
+// (22), 512 55 (36); 512 experts: 512 (72), 384 (84).
 constexpr int route_threads(int V) { return V <= 4 ? 1024 : (V == 8 ? 768 : (V == 16 ? 512 : 256)); }
 
 template <int V, class T>
@@ -833,8 +838,8 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const P p) {
   }
 }
 
-// 32768 tokens of 256 experts, 8 slots, choice and plan: 50 us, with 512 threads 56, 256
-// 68; 8192 of 1024: 75, 97, 111; 500 of 256 12, 12, 14.
+// The plan of 32768 tokens of 256 experts, 8 slots: 16 us, with 512 threads 21, 256 34;
+// 8192 of 1024: 29, 51, 65; 500 of 256: 7.5, 7.4, 8.7.
 constexpr int kPlanThreads = 1024;
 
 // Counts of a chunk of given experts.
@@ -1086,7 +1091,7 @@ int route_launch(const RouteArgs &a, int sm_count, cudaStream_t stream) {
   p.scale = a.scale;
   p.plan = a.offsets != nullptr;
   // Up to 24 tokens one CTA does all (a warp each); more, eight tokens a CTA: 64
-  // tokens of 256 experts, with the plan, 13.4 us, in one CTA 25.7. Up to 192 the CTAs
+  // tokens of 256 experts, with the plan, 13.4 us (cold), in one CTA 25.7. Up to 192 the CTAs
   // of a cluster, one launch: 64 tokens 13.4 against 16.5 to 18.6 in two launches, 192
   // tokens 17.5 against 18.6, and 256 21.6 against 16.5.
   constexpr int kCluster = 8;

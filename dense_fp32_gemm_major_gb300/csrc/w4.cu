@@ -37,9 +37,9 @@
 //     Few tiles: the CTAs of a cluster share k, and add their sums from each
 //     other's shared memory in the order of their ranks.
 //
-// Measured (launches by themselves, group 128): one bf16 row of 4096 x 11008 15 us (23
-// MB: 1.5 TB/s), 64 rows of 8 experts, 6 of them used, 51 us (142 MB: 2.8 TB/s of
-// 6.8). Neither memory nor a pipe is what bounds it (integer lanes 37 %, tensor core
+// Measured (launches by themselves with cold caches, group 128): one bf16 row of 4096 x
+// 11008 16.5 to 17.3 us (23 MB: 1.4 TB/s; back to back, the weights in L2, 12.8), 64 rows
+// of 8 experts, 6 of them used, 52 us (142 MB: 2.7 TB/s of 6.8; back to back 51). Neither memory nor a pipe is what bounds it (integer lanes 37 %, tensor core
 // 8 %), but the chain of a block: 128 k of operands are made and stored (about 700
 // clocks), multiplied by eight dependent MMAs (118 clocks each), and read out (600),
 // with four such chains an SM; and the MMAs of one thread start no closer than about

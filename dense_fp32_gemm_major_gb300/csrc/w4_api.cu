@@ -22,12 +22,21 @@ using gemm::W4Args;
 
 // Rows a segment from which on the weights are expanded once for the tensor-core
 // kernels of the segmented products: measured, w4_launch | many_rows in us at group
-// 128,
-//   rows                     128        256        512        2048
-//   bf16  4096 x 11008     78 | 148  146 | 149  283 | 150  1114 | 254
-//   bf16  32 x 1408 x 2048 97 | 180  185 | 187  360 | 235  1398 | 530
-//   fp32  4096 x 11008    138 | 325  266 | 326  526 | 347  2127 | 749
-//   fp32  32 x 1408 x 2048 172 | 275 334 | 315  654 | 525  2577 | 1570
+// 128, cold caches, a call in a graph,
+//   rows                       128        256        512        2048
+//   bf16  4096 x 11008       66 | 103  115 | 105  217 | 140   819 | 256
+//   bf16  32 x 1408 x 2048  113 | 186  205 | 191  391 | 221  1514 | 514
+//   fp32  4096 x 11008      107 | 170  197 | 191  377 | 326  1478 | 731
+//   fp32  32 x 1408 x 2048  189 | 271  356 | 311  696 | 464  2719 | 1460
+// The host knows their average alone. Where one segment has most of the rows, that one's
+// turns follow each other; with 8 of 10 rows in the last segment, the others equal,
+//   rows, average              128        256
+//   bf16  8 x 4096 x 11008  426 | 787   752 | 897  (equal: 240 | 758, 457 | 766)
+//   bf16  32 x 1408 x 2048  707 | 199  1337 | 227
+//   fp32  8 x 4096 x 11008  754 | 1389 1383 | 1768 (equal: 455 | 1354, 891 | 1460)
+//   fp32  32 x 1408 x 2048 1235 | 318  2383 | 416
+// so that many small matrices with most rows in one take up to six times as long as
+// expanded ones would.
 constexpr int64_t kManyRows = 256;
 // Bytes of expanded weights at a time: more than 4096 x 11008 have, for a part of
 // them has fewer tiles than the GPU SMs (at 128 MB that one took 247 us in place of

@@ -66,10 +66,14 @@ int reduce_f32_sum(int64_t n, const float *x, float *out, int groups, void *stre
  * bits: the norm is within 2^-20 of its value over the whole range of the types. The
  * order is fixed by the tensors' sizes and alignment, the device and the order of
  * the list: reruns are bit-identical.
- * The factor is computed in 64 bits and rounded to fp32 (2^-24), the products
- * once to the type. A norm of infinity makes the factor 0 (and infinite elements
- * NaN), a NaN makes every result NaN. Workspace: 8 bytes a CTA from the library's
- * pool. A launch takes up to 100 tensors of a shorter list, 1000 of a longer one.
+ * The factor is computed in 64 bits and rounded to fp32 (2^-24; below 2^-126 to
+ * 2^-150), the products once to the type. An infinite element makes the norm infinite,
+ * the factor 0 (NaN with an infinite limit) and infinite elements NaN; a NaN makes every
+ * result NaN. A finite norm above fp32's range is given as infinity, with the factor
+ * of its value. Workspace: 8 bytes a CTA from the library's pool.
+ *   A launch takes up to 100 tensors of a shorter list, 1000 of a longer one. Each of
+ * the clipping's launches adds the partial sums of all of the norm's: 10000 tensors of
+ * 100 elements take 0.35 ms, 100000 9 ms (the norm alone 1.5), 2^20 0.76 s (16 ms).
  */
 int reduce_f32_norm(int64_t count, const void *const *x, const int64_t *n, const int *type,
                     float *norm, void *stream);

@@ -45,7 +45,9 @@ extern "C" {
  *   strideq, strides, stridez
  *             matrix g starts that many bytes (elements, bytes) after g - 1;
  *             0: one for all
- *   offsets   as for gemm_f32_grouped; NULL: all rows with matrix 0
+ *   offsets   as for gemm_f32_grouped, but where they decrease, results are
+ *             unspecified, as with adapters (a segment's place in the workspace
+ *             follows from its first row); NULL: all rows with matrix 0
  *   C         rows of no segment are not written; must not overlap anything else
  *             (GEMM_ERR_ALIAS)
  * K == 0 sets the rows to zero. Pointers are aligned to their element; sizes up
@@ -56,7 +58,8 @@ extern "C" {
  * (2.3 bytes a value of 16 bf16 rows, 6.3 of 16 fp32 ones), for every segment a last
  * one that may be part empty (but no more of them than rows).
  *   In both, where rows of Q do not start on 16 bytes (Q, ldq and strideq multiples
- * of 16), a copy of it.
+ * of 16), a copy of it. A segment of many rows is gone through tile by tile, its
+ * weights read anew for each.
  *   256 and more: up to 512 MB of weights at a time (256 rows of W at least) in 4
  * bytes each, and a copy of A where its rows do not start on 16 bytes.
  */

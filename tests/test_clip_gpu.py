@@ -186,3 +186,16 @@ def test_results_in_the_place_of_operands(g):
     y = x.clone()
     g.clip_grads([x, b], 0.5, out=[x, both[:128].view(8, 16)])  # one in place, one elsewhere
     assert ((x.double() - y.double() * (0.5 / (norm_64([y, b]) + 1e-6))).abs() <= 21 * U * y.double().abs()).all()
+
+
+def test_norms_beyond_fp32_and_infinite_limits(g):
+    x = torch.full((1000,), 1e38, device="cuda")
+    out = [torch.empty_like(x)]
+    assert float(g.clip_grads([x], 1.0, out=out)) == math.inf  # 3.2e39
+    want = x.double() / norm_64([x])
+    # a factor of 3e-40 is rounded to 2^-149: 2^-150 / 3.1e-40 of it
+    assert ((out[0].double() - want).abs() <= (2.0 ** -150 / 3.1e-40 + U) * want).all()
+    x[7] = math.inf
+    assert float(g.clip_grads([x], math.inf, out=out)) == math.inf and out[0].isnan().all()
+    assert float(g.clip_grads([x], 1.0, out=out)) == math.inf
+    assert out[0][7].isnan() and not out[0][:7].any()
