@@ -12,12 +12,16 @@
 //     of its time in it.)
 //   * A bf16 whose upper eight bits are zero is its lower eight times 2^-133 (the
 //     subnormals and the first normal values are one line). So the nibbles of a
-//     word, in pairs 16 bits apart, are operands as they are, q 2^-133 where they
-//     are the lowest four bits and 16 q 2^-133 above: five operations of the
-//     integer lanes for eight weights (memory at full speed brings 47 weights a
-//     clock of an SM, its integer lanes do 64 operations). A is scaled by 2^110,
-//     and by 2^106 where it meets the upper nibbles, to meet them in the middle of
-//     fp32's range; rows with values from 2^16 on by less.
+//     word, in pairs 16 bits apart and moved to bits 4 to 7 of each half, are operands
+//     16 q 2^-133: seven operations of the integer lanes for eight weights (memory at
+//     full speed brings 47 weights a clock of an SM, its integer lanes do 64
+//     operations). Not to bits 0 to 3, where four of them need no move: the tensor core
+//     aligns the products of 16 k by their operands' exponents, which for subnormals is
+//     that of 2^-126, and drops what lies 25 bits below the largest. So it keeps
+//     products to 2^-22 of the largest |a| (to 2^-18 with q 2^-133, where sums of few or
+//     very different values were off by up to nine times their bound). A is scaled by
+//     2^106, to meet them in the middle of fp32's range; rows with values from 2^16 on by
+//     less.
 //   * sum s (q - z) a = s (sum q a - z sum a): the sums of A are made with A, a
 //     term each, and are about as exact as the tensor core's, so that where q = z
 //     nearly nothing is left.
@@ -39,7 +43,7 @@
 //
 // Measured (launches by themselves with cold caches, group 128): one bf16 row of 4096 x
 // 11008 16.5 to 17.3 us (23 MB: 1.4 TB/s; back to back, the weights in L2, 12.8), 64 rows
-// of 8 experts, 6 of them used, 52 us (142 MB: 2.7 TB/s of 6.8; back to back 51). Neither memory nor a pipe is what bounds it (integer lanes 37 %, tensor core
+// of 8 experts, 6 of them used, 52 us (142 MB: 2.7 TB/s of 6.8; back to back 53). Neither memory nor a pipe is what bounds it (integer lanes 37 %, tensor core
 // 8 %), but the chain of a block: 128 k of operands are made and stored (about 700
 // clocks), multiplied by eight dependent MMAs (118 clocks each), and read out (600),
 // with four such chains an SM; and the MMAs of one thread start no closer than about
@@ -210,8 +214,8 @@ __device__ __forceinline__ float read_cluster(uint32_t addr, uint32_t rank) {
 // are below 2^16 (biased exponent kLargest); else, that of the largest of them
 // above kLargest less. fp32 values that are all below 2^-60 (kSmallest) kMore more:
 // their products' last bits, of the third term, would be below 2^-149 from 2^-102 on.
-// Sums are of units of 2^-133.
-constexpr int kScale = 110, kUnit = 133, kLargest = 127 + 15, kSmallest = 127 - 60, kMore = 16;
+// Sums are of units of 2^-129, a weight's (16 2^-133).
+constexpr int kScale = 106, kUnit = 129, kLargest = 127 + 15, kSmallest = 127 - 60, kMore = 16;
 constexpr float kLargeScale = 0x1p104f;
 
 __device__ __forceinline__ float power(int e) {  // 2^e, e in -126 .. 127
@@ -275,14 +279,13 @@ __device__ __forceinline__ int terms8(const float (&v)[8], uint4 (&out)[terms_of
       const __nv_bfloat16 term = __float2bfloat16_rn(rest);
       const float f = __bfloat162float(term);
       sum[t] += f * 0x1p-100f;
-      // its odd k meet the nibbles that are 16 q
-      h[t][i] = __bfloat16_as_ushort(__float2bfloat16_rn(i & 1 ? f * 0.0625f : f));
+      h[t][i] = __bfloat16_as_ushort(term);
       rest = isinf(f) ? 0.0f : rest - f;  // of infinity there is no second term
     }
   }
 #pragma unroll
   for (int t = 0; t < kTerms; ++t) {
-    sum[t] *= 0x1p-33f;
+    sum[t] *= 0x1p-29f;
     out[t] = make_uint4(h[t][0] | h[t][4] << 16, h[t][1] | h[t][5] << 16, h[t][2] | h[t][6] << 16,
                         h[t][3] | h[t][7] << 16);
   }
@@ -712,9 +715,9 @@ __global__ void __launch_bounds__(kThreads, COLS <= 32 && tmem_columns(COLS, 4 /
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              v[c * 16 + i * 4] = u[i] & 0x000f000fu;
+              v[c * 16 + i * 4] = u[i] << 4 & 0x00f000f0u;
               v[c * 16 + i * 4 + 1] = u[i] & 0x00f000f0u;
-              v[c * 16 + i * 4 + 2] = u[i] >> 8 & 0x000f000fu;
+              v[c * 16 + i * 4 + 2] = u[i] >> 4 & 0x00f000f0u;
               v[c * 16 + i * 4 + 3] = u[i] >> 8 & 0x00f000f0u;
             }
           }

@@ -209,6 +209,35 @@ def test_small_values_beside_large_ones_of_no_weight(g, m, large):
     check(got, x, w, torch.float32, least=float(lost))
 
 
+@pytest.mark.parametrize("m", [1, 2, 14, 60, 300])
+@pytest.mark.parametrize("k", [2, 3, 5, 16, 33, 200])
+@pytest.mark.parametrize("zeros", [0, 1, 8])
+@pytest.mark.parametrize("dt", TYPES, ids=ids)
+def test_small_values_beside_large_ones(g, dt, m, k, zeros):
+    # products of few and very different values, relative to the sum of |s| (q + z) |a|
+    n, group = 200, 32
+    gen = torch.Generator().manual_seed(k)
+    low = 2 - min(zeros, 2)  # q + z of 2 at least
+    q4 = torch.randint(low, 16, (n, k + k % 2), generator=gen)
+    q4[:, k:] = 0
+    q = (q4[:, ::2] | q4[:, 1::2] << 4).to(torch.uint8).cuda()
+    s = ((torch.rand(n, -(-k // group), generator=gen) + 0.5) / 16).to(dt).cuda()
+    z = torch.full((n, -(-k // group)), zeros, dtype=torch.uint8, device="cuda")
+    size = torch.randint(-26, -6, (m, k), generator=gen)
+    size[torch.arange(m), torch.randint(k, (m,), generator=gen)] = 0
+    sign = torch.randint(0, 2, (m, k), generator=gen) * 2 - 1
+    x = (sign * (1 + torch.rand(m, k, generator=gen).double()) * size.double().exp2()).to(dt).cuda()
+    got = g.w4_matmul(x, q, s, group, zeros=z).double()
+    w = weights_64(q, s, z, k, group)
+    all_s = s.double().abs().repeat_interleave(group, 1)[:, :k]
+    c64 = x.double() @ w.t()
+    size = x.double().abs() @ (all_s * (q4[:, :k].cuda() + zeros)).t()
+    step = 2 * k * 2.0 ** -24 if dt == torch.float32 else (k + 2) * 2.0 ** -23
+    tol = step * size + (2.0 ** -24 if dt == torch.float32 else 2.0 ** -8) * c64.abs()
+    bad = ~((got - c64).abs() <= tol)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, worst {float(((got - c64).abs() / tol).max()):.3g} of the bound"
+
+
 @pytest.mark.parametrize("m", [3, 300])
 @pytest.mark.parametrize("dt", TYPES, ids=ids)
 def test_large_scales(g, dt, m):
