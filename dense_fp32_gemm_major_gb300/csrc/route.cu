@@ -219,82 +219,20 @@ __device__ __forceinline__ int choose_experts(U (&key)[V], int k, U *won) {
 // -------------------------------------------------------- choice in 64 bits --
 
 // Lane r's choice by keys of 64 bits. A sigmoid is computed again only for those
-// of a lane's experts that can matter: those not below `least` (the last of the chosen;
-// -infinity, all of them, where the groups themselves may be others) and, with
-// groups, its best two (which a group's may be); of the others fp32 tells enough. One
-// token of this is some 8 us, beside the CTA's other warps.
+// of a lane's experts that can matter: those not below `least` (the last of the chosen)
+// and, with groups, its best two (which a group's may be); of the others fp32 tells
+// enough. Where the groups themselves may be others (`regroup`) their experts can be
+// far below `least`: the groups are chosen by the lanes' best two, and behind that
+// the experts not below the last that those have. One token of this is some 8 us, beside
+// the CTA's other warps. (All scores of a token at once: 32768 tokens of 256 experts in
+// groups, with the gradient, 79 -> 83 us, for CTAs end with one.)
 template <int V, class T>
-__device__ __noinline__ int choose_wide(const P &p, long long t, float least, float err) {
+__device__ __noinline__ int choose_wide(const P &p, long long t, float least, float err, bool regroup) {
   const int lane = threadIdx.x & 31;
   unsigned long long key[V];
-  if (p.sigmoid) {
-    float f[V];
-    unsigned again = 0;  // by their places, eight at a time of more than 32
-    float b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      const float x = e < p.E ? load_logit<T>(p, t, e) : -INFINITY;
-      const float b = e < p.E ? load_bias(p, e) : 0.0f;
-      const bool there = x != -INFINITY && b != -INFINITY;
-      f[i] = there ? sigmoid(x) + b : -INFINITY;
-      key[i] = there ? key_of(static_cast<double>(f[i])) : 0;
-      b2 = fmaxf(b2, fminf(b1, f[i]));
-      b1 = fmaxf(b1, f[i]);
-    }
-    const float from = p.groups > 1 ? fminf(least, b2) : least;
-    // (a lane of experts of several groups: all of them)
-    const float low = p.groups > 1 && p.per_group % V != 0
-                          ? -INFINITY : from - 4.0f * (err + kUnit * fabsf(from));
-#pragma unroll
-    for (int i0 = 0; i0 < V; i0 += 32) {
-      again = 0;
-#pragma unroll
-      for (int i = i0; i < V && i < i0 + 32; ++i)
-        if (key[i] > 1 && !(f[i] < low)) again |= 1u << (i - i0);
-      while (__any_sync(kFull, again != 0)) {
-        const int at = __ffs(again) - 1;
-        unsigned long long wide = 0;
-        if (at >= 0) {
-          const int e = lane * V + i0 + at;
-          wide = key_of(sigmoid(static_cast<double>(load_logit<T>(p, t, e))) +
-                        static_cast<double>(load_bias(p, e)));
-          again &= again - 1;
-        }
-#pragma unroll
-        for (int i = i0; i < V && i < i0 + 32; ++i)
-          if (at == i - i0) key[i] = wide;
-      }
-    }
-  } else {
-    double f[V], m = -INFINITY, sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      f[i] = e < p.E ? static_cast<double>(load_logit<T>(p, t, e)) : -INFINITY;
-      key[i] = f[i] == -INFINITY ? 0 : 2;
-      m = fmax(m, f[i]);
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, s));
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      f[i] = key[i] != 0 ? exp(f[i] - m) : 0.0;
-      sum += f[i];
-    }
-    const double part = 1.0 / warp_sum(sum);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      f[i] *= part;
-      if (key[i] != 0 && p.bias != nullptr) {
-        const float b = load_bias(p, lane * V + i);
-        if (b == -INFINITY) key[i] = 0;
-        f[i] += static_cast<double>(b);
-      }
-      if (key[i] != 0) key[i] = key_of(f[i]);
-    }
-  }
-  if (p.groups > 1) {
+  // Keys of groups that are not chosen are 0 behind this.
+  auto keep_groups = [&] {
+    if (p.groups <= 1) return;
     if (p.lanes_hold_groups) {  // as choose()
       unsigned long long b1 = 0, b2 = 0;
 #pragma unroll
@@ -332,6 +270,90 @@ __device__ __noinline__ int choose_wide(const P &p, long long t, float least, fl
         if (g > 31 || !(kept >> g & 1u)) key[i] = 0;
       }
     }
+  };
+  if (p.sigmoid) {
+    float f[V];
+    unsigned done[(V + 31) / 32] = {};  // of a lane's experts, by their places
+    float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      const float x = e < p.E ? load_logit<T>(p, t, e) : -INFINITY;
+      const float b = e < p.E ? load_bias(p, e) : 0.0f;
+      const bool there = x != -INFINITY && b != -INFINITY;
+      f[i] = there ? sigmoid(x) + b : -INFINITY;
+      key[i] = there ? key_of(static_cast<double>(f[i])) : 0;
+      const float v = f[i] != f[i] ? -INFINITY : f[i];  // (a NaN is behind all others)
+      b2 = fmaxf(b2, fminf(b1, v));
+      b1 = fmaxf(b1, v);
+    }
+    auto refine = [&](float from) {
+      const float low = from - 4.0f * (err + kUnit * fabsf(from));
+#pragma unroll
+      for (int i0 = 0; i0 < V; i0 += 32) {
+        unsigned again = 0;
+#pragma unroll
+        for (int i = i0; i < V && i < i0 + 32; ++i)
+          if (key[i] > 1 && !(f[i] < low)) again |= 1u << (i - i0);
+        again &= ~done[i0 / 32];
+        done[i0 / 32] |= again;
+        while (__any_sync(kFull, again != 0)) {
+          const int at = __ffs(again) - 1;
+          unsigned long long wide = 0;
+          if (at >= 0) {
+            const int e = lane * V + i0 + at;
+            wide = key_of(sigmoid(static_cast<double>(load_logit<T>(p, t, e))) +
+                          static_cast<double>(load_bias(p, e)));
+            again &= again - 1;
+          }
+#pragma unroll
+          for (int i = i0; i < V && i < i0 + 32; ++i)
+            if (at == i - i0) key[i] = wide;
+        }
+      }
+    };
+    // (A lane of experts of several groups: all of them. Many experts a lane, too,
+    // for want of registers.)
+    constexpr bool kTwice = V <= 8;
+    if (p.groups > 1 && (p.per_group % V != 0 || (regroup && !kTwice))) refine(-INFINITY);
+    else refine(p.groups == 1 ? least : (regroup ? b2 : fminf(least, b2)));
+    keep_groups();
+    if (kTwice && regroup) {
+      unsigned narrow[V], won32;
+#pragma unroll
+      for (int i = 0; i < V; ++i) narrow[i] = key[i] > 1 ? key_of(f[i]) : static_cast<unsigned>(key[i]);
+      choose_experts<V>(narrow, p.k, &won32);
+      won32 = __shfl_sync(kFull, won32, p.k - 1);
+      refine(won32 > 1 ? value_of(won32) : -INFINITY);
+    }
+  } else {
+    double f[V], m = -INFINITY, sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      f[i] = e < p.E ? static_cast<double>(load_logit<T>(p, t, e)) : -INFINITY;
+      key[i] = f[i] == -INFINITY ? 0 : 2;
+      m = fmax(m, f[i]);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, s));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      f[i] = key[i] != 0 ? exp(f[i] - m) : 0.0;
+      sum += f[i];
+    }
+    const double part = 1.0 / warp_sum(sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      f[i] *= part;
+      if (key[i] != 0 && p.bias != nullptr) {
+        const float b = load_bias(p, lane * V + i);
+        if (b == -INFINITY) key[i] = 0;
+        f[i] += static_cast<double>(b);
+      }
+      if (key[i] != 0) key[i] = key_of(f[i]);
+    }
+    keep_groups();
   }
   unsigned long long won;
   return choose_experts<V>(key, p.k, &won);
@@ -596,9 +618,8 @@ __device__ __forceinline__ int choose(const P &p, long long t, const float (&bia
       for (int i = 0; i < V; ++i)  // those that are left
         if (key[i] > 1 && close(last_key, key[i], 0u)) unsure |= !same(last_e, lane * V + i);
     }
-    // (Other groups may have the k-th best far below what these ones have.)
     if (__any_sync(kFull, unsure))
-      return choose_wide<V, T>(p, t, regroup || least == INFINITY ? -INFINITY : least, err);
+      return choose_wide<V, T>(p, t, least == INFINITY ? -INFINITY : least, err, regroup);
   }
   return c.expert;
 }
