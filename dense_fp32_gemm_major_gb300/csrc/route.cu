@@ -31,9 +31,9 @@
 // ncu times them). 1 token of 8 experts 3.6 us, 64 of 256 in groups 8.9 (12.7): chains
 // of dependent steps of a few warps. 4095 of 64, bf16, softmax, 6 slots: choice 4.0,
 // plan 7.5. 32768 of 256, fp32, 8 slots: softmax 34, with a bias 54; sigmoid with a
-// bias 47, in 8 groups 56, of these a fifth masked 49 (62); and 16 (17) for the plan;
-// against 5 us of memory for the logits: the choice is bound by instructions, 1075 warp
-// instructions a token (49 % of the integer lanes' rate). Softmax of one slot takes 23
+// bias 47, in 8 groups 56, of these a fifth masked 49 (58); and 16 (17) for the plan;
+// against 5 us of memory for the logits: the choice is bound by instructions, 1080 warp
+// instructions a token (47 % of the integer lanes' rate). Softmax of one slot takes 23
 // us, each further slot 1.5, a bias 6 (one slot) to 20 (eight: of more pairs some are
 // too close, and a 64-bit choice at a CTA's end shows as 8). The plan's time is the
 // counts of all chunks, which every CTA sums, and two passes over its slots; the

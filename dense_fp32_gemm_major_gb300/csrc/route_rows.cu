@@ -12,8 +12,8 @@
 // where their starts and widths allow it.
 //
 // Measured (8192 tokens of 4096 bf16, two places each, launches by themselves):
-// dispatch 29 us (201 MB: 6.9 TB/s), combine 28 us (7.3 TB/s), backward 57 us (336 MB:
-// 5.9 TB/s); a plain copy has 6.8. 1531 tokens of 777 fp32 (rows on no 16 bytes), three
+// dispatch 29 to 31 us (201 MB: 6.4 to 6.9 TB/s), combine 28 us (7.1 TB/s), backward 54
+// us (336 MB: 6.2 TB/s); a plain copy has 6.8. 1531 tokens of 777 fp32 (rows on no 16 bytes), three
 // places: 5.6, 6.9 and 7.8 us.
 
 #include <cuda_bf16.h>

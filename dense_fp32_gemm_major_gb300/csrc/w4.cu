@@ -42,9 +42,9 @@
 //     other's shared memory in the order of their ranks.
 //
 // Measured (launches by themselves with cold caches, group 128): one bf16 row of 4096 x
-// 11008 16.5 to 17.3 us (23 MB: 1.4 TB/s; back to back, the weights in L2, 12.8), 64 rows
-// of 8 experts, 6 of them used, 52 us (142 MB: 2.7 TB/s of 6.8; back to back 53). Neither memory nor a pipe is what bounds it (integer lanes 37 %, tensor core
-// 8 %), but the chain of a block: 128 k of operands are made and stored (about 700
+// 11008 17.5 us (23 MB: 1.3 TB/s; back to back, the weights in L2, 13.1), 64 rows of 8
+// experts, 6 of them used, 54 us (142 MB: 2.7 TB/s of 6.8; back to back 53). Neither
+// memory nor a pipe is what bounds it (integer lanes 39 %, tensor core 8 %), but the chain of a block: 128 k of operands are made and stored (about 700
 // clocks), multiplied by eight dependent MMAs (118 clocks each), and read out (600),
 // with four such chains an SM; and the MMAs of one thread start no closer than about
 // 100 clocks, so that two CTAs an SM give 1600 clocks a block each at best, of 2500
